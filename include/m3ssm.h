@@ -289,6 +289,171 @@ m3_status m3_decode_tokens(const m3_dims* dims, float* h, const void* x,
                            const float* A, const void* lam, const void* theta,
                            void* y, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The other layers of a hybrid stack: a gated linear recurrence, the norms
+ * and rotary positions of queries and keys, and causal attention.  They take
+ * the packed layout of m3_scan_prefill_varlen (token rows of S sequences back
+ * to back, cu_seqlens a DEVICE array of S + 1 rising int32 offsets, 4-byte
+ * aligned), so one batch runs through all of them.  The conventions above
+ * hold, with these differences: there is one dtype for inputs and outputs;
+ * gradients have the type of what they belong to (weights, decays and states
+ * fp32); and the token rows of an input may be cut out of wider rows (one
+ * projection's output): ld_* is the distance of consecutive rows in elements,
+ * 0 meaning dense.  Outputs are dense unless they have an ld of their own. */
+
+/* The gated linear recurrence, one state per channel:
+ *     L_t = -c softplus(decay) sigmoid(r_t),   a_t = exp(L_t),
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,   y_t = h_t
+ * with r and i before their sigmoid.  Sums and states are fp32; 1 - a^2 is
+ * formed from L without cancellation. */
+typedef struct {
+  int32_t batch;  /* Bsz, or S sequences of a packed call, >= 1            */
+  int32_t seqlen; /* T, or all rows of a packed call (ignored by the step) */
+  int32_t width;  /* D >= 1, any                                           */
+  int32_t dtype;  /* m3_dtype of x, r, i, y and their gradients            */
+  float c;        /* finite, > 0                                           */
+  int64_t ld_x, ld_r, ld_i; /* >= D or 0; a dense call's sequences follow
+                               each other T rows apart                     */
+  int64_t ld_g;   /* of dx, dr, di                                         */
+} m3_gated_dims;
+
+/* rows between the states that m3_gated_scan saves for the backward pass */
+#define M3_GATED_CHUNK 128
+
+/* Bytes of device workspace m3_gated_scan (packed: nonzero for calls with
+ * cu_seqlens) and m3_gated_scan_backward need; 0 if dims is invalid. */
+size_t m3_gated_scan_workspace_size(const m3_gated_dims* dims, int packed);
+size_t m3_gated_scan_backward_workspace_size(const m3_gated_dims* dims, int packed);
+
+/* The scan over x, r, i [Bsz, T, D] (cu_seqlens NULL) or, packed, [T, D]:
+ *   y       [Bsz, T, D] or [T, D]
+ *   hT      [Bsz, D] fp32, the state after the last token (NULL: not written)
+ *   states  [Bsz, ceil(T / M3_GATED_CHUNK), D] fp32 (packed: without Bsz), the
+ *           state before every 128th row, for the backward pass (NULL: not
+ *           written)
+ * decay [D] fp32; h0 [Bsz, D] fp32 or NULL (zero), may alias hT.  An empty
+ * sequence's hT row is its h0 row.  Packed offsets are clamped into [0, T] and
+ * raised to the largest before them, as in m3_scan_prefill_varlen; rows that
+ * no sequence covers are left as they are.  A NaN or Inf reaches the later
+ * tokens of its own sequence and channel and nothing else.  Time tiles of one
+ * channel hand their state on inside one launch; results do not depend on the
+ * order in which they run. */
+m3_status m3_gated_scan(const m3_gated_dims* dims, const int32_t* cu_seqlens, const void* x,
+                        const void* r, const void* i, const float* decay, const float* h0,
+                        void* y, float* hT, float* states, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* Gradients for L = <y, dy> + <hT, dhT> (dhT NULL = 0), with `states` as
+ * m3_gated_scan wrote them for the same inputs: dx, dr, di in dtype; ddecay
+ * [D] and dh0 [Bsz, D] (NULL: not written) fp32.  Sums run in a fixed order
+ * (no atomics): equal calls return equal bits.  At a = 1 (a gate that is
+ * exactly closed) the gradient through sqrt(1 - a^2) is its limit, 0. */
+m3_status m3_gated_scan_backward(const m3_gated_dims* dims, const int32_t* cu_seqlens,
+                                 const void* x, const void* r, const void* i,
+                                 const float* decay, const float* h0, const float* states,
+                                 const void* dy, const float* dhT, void* dx, void* dr, void* di,
+                                 float* ddecay, float* dh0, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/* One step: h [Bsz, D] fp32 advances in place by x, r, i [Bsz, D]; y [Bsz, D].
+ * dims->seqlen is ignored. */
+m3_status m3_gated_step(const m3_gated_dims* dims, float* h, const void* x, const void* r,
+                        const void* i, const float* decay, void* y, void* stream);
+
+/* Norms of queries and keys per head, with the position rotation:
+ *     u = v / sqrt(mean(v^2) + eps) * weight,
+ *     pairs (u_2j, u_2j+1), j < rotary_dim / 2, turned by
+ *     position * base^(-2j / rotary_dim); the other channels stay as they are.
+ * flags: M3_ROPE_HALF pairs (u_j, u_j+rotary_dim/2) instead.  Angles are
+ * reduced in fp64, so any int32 position keeps its phase. */
+#define M3_ROPE_HALF (1u << 0)
+typedef struct {
+  int32_t tokens;     /* T >= 1 rows, of any number of sequences           */
+  int32_t nheads_q;   /* Hq >= 1                                           */
+  int32_t nheads_k;   /* Hk >= 1                                           */
+  int32_t headdim;    /* D: 32, 64, 128 or 256                             */
+  int32_t rotary_dim; /* even, 0 .. D                                      */
+  int32_t dtype;      /* m3_dtype of q, k, their outputs and gradients     */
+  uint32_t flags;     /* M3_ROPE_HALF                                      */
+  float eps;          /* finite, >= 0 (a row of zeros with eps = 0: NaN)   */
+  double base;        /* finite, > 0                                       */
+  int64_t ld_q, ld_k; /* >= H D, multiples of 8, or 0                      */
+  int64_t ld_dq, ld_dk;
+} m3_qk_dims;
+
+/* q [T, Hq, D] and k [T, Hk, D] to q_out and k_out (dense).  q_weight and
+ * k_weight [D] fp32 or NULL (1); positions [T] int32 (DEVICE, 4-byte
+ * aligned).  With dense rows q_out may be q and k_out may be k. */
+m3_status m3_qk_norm_rope(const m3_qk_dims* dims, const void* q, const void* k,
+                          const float* q_weight, const float* k_weight,
+                          const int32_t* positions, void* q_out, void* k_out, void* stream);
+
+size_t m3_qk_norm_rope_backward_workspace_size(const m3_qk_dims* dims);
+
+/* Gradients from dq_out, dk_out (dense): dq, dk in dtype, dq_weight and
+ * dk_weight [D] fp32 (NULL: not written), summed in a fixed order. */
+m3_status m3_qk_norm_rope_backward(const m3_qk_dims* dims, const void* q, const void* k,
+                                   const float* q_weight, const float* k_weight,
+                                   const int32_t* positions, const void* dq_out,
+                                   const void* dk_out, void* dq, void* dk, float* dq_weight,
+                                   float* dk_weight, void* ws, size_t ws_bytes, void* stream);
+
+/* Causal attention with grouped heads: head h of q reads head
+ * h / (Hq / Hk) of k and v.  Query i of a sequence with Lq queries and Lk keys
+ * sees keys 0 .. i + Lk - Lq (the last query sees all: Lk > Lq continues a
+ * prompt whose first keys are there already).  A query that sees no key has
+ * o = 0 and lse = -inf, and gradients 0.  Scores and softmax sums are fp32
+ * (bf16: weights are rounded to bf16 before the product with v). */
+typedef struct {
+  int32_t nseq;     /* S >= 1                                              */
+  int32_t tokens_q; /* Tq >= 1 rows of q (ignored by the decode call)      */
+  int32_t tokens_k; /* Tk >= 1 rows of k, v (decode: rows of one cache)    */
+  int32_t nheads_q; /* Hq, a multiple of Hk                                */
+  int32_t nheads_k; /* Hk >= 1                                             */
+  int32_t headdim;  /* D: 64 or 128                                        */
+  int32_t dtype;    /* m3_dtype of q, k, v, o and gradients                */
+  float scale;      /* of the scores; finite                               */
+  int64_t ld_q, ld_k, ld_v, ld_o, ld_do; /* >= H D, multiples of 8, or 0   */
+  int64_t stride_k, stride_v; /* decode: elements from one sequence's cache
+                                 to the next, multiples of 8; 0: Tk rows   */
+} m3_attn_dims;
+
+/* q [Tq, Hq, D], k and v [Tk, Hk, D] packed by cu_seqlens_q and cu_seqlens_k
+ * to o [Tq, Hq, D] and lse [Tq, Hq] fp32 (natural logarithm; NULL: not
+ * written).  Offsets are clamped into their rows, so no access leaves the
+ * buffers whatever they hold; they are meant to rise, and the rows of a batch
+ * whose offsets do not are unspecified.  Rows behind the last sequence are
+ * left as they are.  Infinities and NaN of a key or value reach the queries
+ * that see it and no others. */
+m3_status m3_attn_prefill_varlen(const m3_attn_dims* dims, const int32_t* cu_seqlens_q,
+                                 const int32_t* cu_seqlens_k, const void* q, const void* k,
+                                 const void* v, void* o, float* lse, void* stream);
+
+size_t m3_attn_prefill_varlen_backward_workspace_size(const m3_attn_dims* dims);
+
+/* Gradients for L = <o, d_o>, with o and lse of the forward call; dq, dk, dv
+ * dense, in dtype.  The heads of a group are summed in a fixed order (no
+ * atomics).  Infinities and NaN may reach all gradients of their sequence
+ * (masked products multiply them by zero), and those of no other. */
+m3_status m3_attn_prefill_varlen_backward(const m3_attn_dims* dims,
+                                          const int32_t* cu_seqlens_q,
+                                          const int32_t* cu_seqlens_k, const void* q,
+                                          const void* k, const void* v, const void* o,
+                                          const float* lse, const void* d_o, void* dq, void* dk,
+                                          void* dv, void* ws, size_t ws_bytes, void* stream);
+
+/* (0 if dims is invalid; a call whose cache is not split needs no more than
+ * the 16 bytes returned for it) */
+size_t m3_attn_decode_workspace_size(const m3_attn_dims* dims);
+
+/* One token per sequence against its cache: q, o [S, Hq, D], caches k and v
+ * [S, Tk, Hk, D], of which the first lengths[s] rows (DEVICE int32, 4-byte
+ * aligned, clamped into [0, Tk]) are there; the others are not read.  lse
+ * [S, Hq] fp32 or NULL.  Length 0: o = 0, lse = -inf. */
+m3_status m3_attn_decode(const m3_attn_dims* dims, const int32_t* lengths, const void* q,
+                         const void* k, const void* v, void* o, float* lse, void* ws,
+                         size_t ws_bytes, void* stream);
+
 /* Static, human-readable name of a status. */
 const char* m3_status_str(m3_status status);
 

@@ -20,6 +20,8 @@ LIB_PATH = os.path.join(_PKG, "libm3ssm.so")
 M3_F32, M3_BF16 = 0, 1
 M3_THETA_IS_ANGLE = 1 << 0
 M3_A_PER_TOKEN = 1 << 1
+M3_ROPE_HALF = 1 << 0
+M3_GATED_CHUNK = 128
 
 STATUS = {0: "M3_OK", 1: "M3_ERR_NULL", 2: "M3_ERR_SHAPE", 3: "M3_ERR_DTYPE",
           4: "M3_ERR_UNSUPPORTED", 5: "M3_ERR_ALIGN", 6: "M3_ERR_WORKSPACE", 7: "M3_ERR_HIP",
@@ -45,6 +47,32 @@ class m3_dims(ctypes.Structure):
                 ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
                 ("ngroups", ctypes.c_int32), ("bc", ctypes.POINTER(m3_bc_prep)),
                 ("tp", ctypes.POINTER(m3_theta_proj))]
+
+
+class m3_gated_dims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("dtype", ctypes.c_int32), ("c", ctypes.c_float),
+                ("ld_x", ctypes.c_int64), ("ld_r", ctypes.c_int64), ("ld_i", ctypes.c_int64),
+                ("ld_g", ctypes.c_int64)]
+
+
+class m3_qk_dims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("nheads_q", ctypes.c_int32),
+                ("nheads_k", ctypes.c_int32), ("headdim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("eps", ctypes.c_float), ("base", ctypes.c_double),
+                ("ld_q", ctypes.c_int64), ("ld_k", ctypes.c_int64), ("ld_dq", ctypes.c_int64),
+                ("ld_dk", ctypes.c_int64)]
+
+
+class m3_attn_dims(ctypes.Structure):
+    _fields_ = [("nseq", ctypes.c_int32), ("tokens_q", ctypes.c_int32),
+                ("tokens_k", ctypes.c_int32), ("nheads_q", ctypes.c_int32),
+                ("nheads_k", ctypes.c_int32), ("headdim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("ld_q", ctypes.c_int64),
+                ("ld_k", ctypes.c_int64), ("ld_v", ctypes.c_int64), ("ld_o", ctypes.c_int64),
+                ("ld_do", ctypes.c_int64), ("stride_k", ctypes.c_int64),
+                ("stride_v", ctypes.c_int64)]
 
 
 class BCPrep:
@@ -124,6 +152,27 @@ def _lib():
         lib.m3_decode_step.argtypes = [dp] + [vp] * 11 + [vp]
         lib.m3_decode_tokens.restype = ctypes.c_int
         lib.m3_decode_tokens.argtypes = [dp] + [vp] * 11 + [vp]
+        gp, qp, ap, i32 = (ctypes.POINTER(m3_gated_dims), ctypes.POINTER(m3_qk_dims),
+                           ctypes.POINTER(m3_attn_dims), ctypes.c_int)
+        for name, args in (
+                ("m3_gated_scan_workspace_size", [gp, i32]),
+                ("m3_gated_scan_backward_workspace_size", [gp, i32]),
+                ("m3_qk_norm_rope_backward_workspace_size", [qp]),
+                ("m3_attn_prefill_varlen_backward_workspace_size", [ap]),
+                ("m3_attn_decode_workspace_size", [ap])):
+            getattr(lib, name).restype = sz
+            getattr(lib, name).argtypes = args
+        for name, args in (
+                ("m3_gated_scan", [gp] + [vp] * 10 + [sz, vp]),
+                ("m3_gated_scan_backward", [gp] + [vp] * 15 + [sz, vp]),
+                ("m3_gated_step", [gp] + [vp] * 7),
+                ("m3_qk_norm_rope", [qp] + [vp] * 8),
+                ("m3_qk_norm_rope_backward", [qp] + [vp] * 12 + [sz, vp]),
+                ("m3_attn_prefill_varlen", [ap] + [vp] * 8),
+                ("m3_attn_prefill_varlen_backward", [ap] + [vp] * 12 + [sz, vp]),
+                ("m3_attn_decode", [ap] + [vp] * 7 + [sz, vp])):
+            getattr(lib, name).restype = ctypes.c_int
+            getattr(lib, name).argtypes = args
         lib.m3_status_str.restype = ctypes.c_char_p
         lib.m3_status_str.argtypes = [ctypes.c_int]
         lib.m3_last_hip_error.restype = ctypes.c_int
@@ -527,3 +576,322 @@ def decode_tokens(h, x, B, C, dt, A, lam, theta, x_prev=None, B_prev=None,
         y = torch.empty((Bsz, K, H, P, R), dtype=out_dtype, device=h.device)
     m3_decode_tokens(d, h, x, x_prev, B, B_prev, C, dt, A, lam, theta, y, stream)
     return y
+
+
+# ---------------------------------------------------------------------------
+# the other layers of a hybrid stack: gated recurrence, q/k norms with rotary
+# positions, causal attention
+class _on:
+    """The device of a call's tensors as the current one and, if given, the
+    stream as the current one, so that what a helper allocates belongs to the
+    stream that uses it."""
+
+    def __init__(self, device, stream):
+        self.device = torch.cuda.device(device)
+        self.stream = torch.cuda.stream(stream)   # None: no change
+
+    def __enter__(self):
+        self.device.__enter__()
+        self.stream.__enter__()
+        return self
+
+    def __exit__(self, *e):
+        self.stream.__exit__(*e)
+        self.device.__exit__(*e)
+
+
+def _same_device(**tensors):
+    """All given tensors on one GPU; returns it."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, others on {dev}")
+    return dev
+
+
+def _rows(name, t, shape, dtype) -> int:
+    """Checks a tensor of token rows that may be cut out of wider rows: the
+    trailing (per-token) axes dense, consecutive tokens one stride apart
+    across all leading axes.  Returns that stride."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype} != expected {dtype}")
+    lead = 2 if len(shape) == 3 and name in _BATCHED else 1
+    width = 1
+    for n, st in zip(reversed(shape[lead:]), reversed(t.stride()[lead:])):
+        if n != 1 and st != width:
+            raise ValueError(f"{name}: a token's values must be contiguous")
+        width *= n
+    ld = t.stride(lead - 1) if shape[lead - 1] > 1 else max(t.stride(lead - 1), width)
+    if shape[lead - 1] == 1 and lead == 2 and shape[0] > 1:
+        ld = t.stride(0)
+    if lead == 2 and shape[0] > 1 and shape[1] > 1 and t.stride(0) != shape[1] * ld:
+        raise ValueError(f"{name}: sequences must follow each other without a gap")
+    if ld < width:
+        raise ValueError(f"{name}: token rows overlap")
+    return ld
+
+
+_BATCHED = ("x", "r", "i")
+
+
+def _gated_setup(x, r, i, decay, c, cu_seqlens, extra):
+    dev = _same_device(x=x, r=r, i=i, decay=decay, cu_seqlens=cu_seqlens, **extra)
+    packed = cu_seqlens is not None
+    if x.dim() != (2 if packed else 3):
+        raise ValueError("x must be [T, D] with cu_seqlens and [Bsz, T, D] without")
+    D, dt = x.shape[-1], x.dtype
+    code = dtype_code(dt)
+    if packed:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must hold S + 1 offsets")
+        B, T = cu_seqlens.numel() - 1, x.shape[0]
+        _check("cu_seqlens", cu_seqlens, (B + 1,), torch.int32)
+    else:
+        B, T = x.shape[:2]
+    lds = [_rows(n, t, x.shape, dt) for n, t in (("x", x), ("r", r), ("i", i))]
+    _check("decay", decay, (D,), torch.float32)
+    return dev, m3_gated_dims(B, T, D, code, c, *lds, 0), packed
+
+
+def _nst(T):
+    return (T + M3_GATED_CHUNK - 1) // M3_GATED_CHUNK
+
+
+def _ws(n, what, device):
+    if n == 0:
+        raise M3Error(2, what)
+    return torch.empty((n + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def gated_scan(x, r, i, decay, h0=None, c=8.0, cu_seqlens=None, want_hT=True, want_states=False,
+               stream=None):
+    """The gated linear recurrence over x, r, i [Bsz, T, D], or packed [T, D]
+    with cu_seqlens (m3_gated_scan).  Returns (y, hT, states); states are for
+    gated_scan_backward."""
+    dev, d, packed = _gated_setup(x, r, i, decay, c, cu_seqlens, dict(h0=h0))
+    B, T, D = d.batch, d.seqlen, d.width
+    _check("h0", h0, (B, D), torch.float32, optional=True)
+    lib = _lib()
+    with _on(dev, stream):
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        hT = torch.empty((B, D), dtype=torch.float32, device=dev) if want_hT else None
+        st = None
+        if want_states:
+            st = torch.empty(((_nst(T),) if packed else (B, _nst(T))) + (D,), dtype=torch.float32,
+                             device=dev)
+        ws = _ws(lib.m3_gated_scan_workspace_size(ctypes.byref(d), packed), "m3_gated_scan", dev)
+        e = lib.m3_gated_scan(ctypes.byref(d), _ptr(cu_seqlens), _ptr(x), _ptr(r), _ptr(i),
+                              _ptr(decay), _ptr(h0), _ptr(y), _ptr(hT), _ptr(st), _ptr(ws),
+                              ws.numel(), _stream(None))
+    if e != 0:
+        raise M3Error(e, "m3_gated_scan")
+    return y, hT, st
+
+
+def gated_scan_backward(x, r, i, decay, dy, states, h0=None, dhT=None, c=8.0, cu_seqlens=None,
+                        stream=None) -> dict:
+    """Gradients of gated_scan (m3_gated_scan_backward): a dict with x, r, i
+    in their dtype, decay and (if h0 is given) h0 in fp32.  Rows that no
+    sequence covers are not written."""
+    dev, d, packed = _gated_setup(x, r, i, decay, c, cu_seqlens,
+                                  dict(h0=h0, dy=dy, states=states, dhT=dhT))
+    B, T, D = d.batch, d.seqlen, d.width
+    _check("h0", h0, (B, D), torch.float32, optional=True)
+    _check("dhT", dhT, (B, D), torch.float32, optional=True)
+    _check("dy", dy, x.shape, x.dtype)
+    _check("states", states, ((_nst(T),) if packed else (B, _nst(T))) + (D,), torch.float32)
+    lib = _lib()
+    with _on(dev, stream):
+        g = {k: torch.empty(x.shape, dtype=x.dtype, device=dev) for k in ("x", "r", "i")}
+        g["decay"] = torch.empty(D, dtype=torch.float32, device=dev)
+        g["h0"] = torch.empty((B, D), dtype=torch.float32, device=dev) if h0 is not None else None
+        ws = _ws(lib.m3_gated_scan_backward_workspace_size(ctypes.byref(d), packed),
+                 "m3_gated_scan_backward", dev)
+        e = lib.m3_gated_scan_backward(
+            ctypes.byref(d), _ptr(cu_seqlens), _ptr(x), _ptr(r), _ptr(i), _ptr(decay), _ptr(h0),
+            _ptr(states), _ptr(dy), _ptr(dhT), _ptr(g["x"]), _ptr(g["r"]), _ptr(g["i"]),
+            _ptr(g["decay"]), _ptr(g["h0"]), _ptr(ws), ws.numel(), _stream(None))
+    if e != 0:
+        raise M3Error(e, "m3_gated_scan_backward")
+    return g
+
+
+def gated_step(h, x, r, i, decay, c=8.0, y=None, stream=None):
+    """Advances h [Bsz, D] (fp32, in place) by one token of x, r, i [Bsz, D];
+    returns y (allocated unless given)."""
+    dev = _same_device(h=h, x=x, r=r, i=i, decay=decay, y=y)
+    if h.dim() != 2:
+        raise ValueError("h must be [Bsz, D]")
+    B, D = h.shape
+    _check("h", h, (B, D), torch.float32)
+    _check("decay", decay, (D,), torch.float32)
+    code = dtype_code(x.dtype)
+    lds = [_rows(n, t, (B, D), x.dtype) for n, t in (("x", x), ("r", r), ("i", i))]
+    d = m3_gated_dims(B, 1, D, code, c, *lds, 0)
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty((B, D), dtype=x.dtype, device=dev)
+        _check("y", y, (B, D), x.dtype)
+        e = _lib().m3_gated_step(ctypes.byref(d), _ptr(h), _ptr(x), _ptr(r), _ptr(i),
+                                 _ptr(decay), _ptr(y), _stream(None))
+    if e != 0:
+        raise M3Error(e, "m3_gated_step")
+    return y
+
+
+def _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags, extra):
+    dev = _same_device(q=q, k=k, positions=positions, q_weight=q_weight, k_weight=k_weight, **extra)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [T, heads, headdim]")
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    code = dtype_code(q.dtype)
+    ldq = _rows("q", q, (T, Hq, D), q.dtype)
+    ldk = _rows("k", k, (T, Hk, D), q.dtype)
+    _check("positions", positions, (T,), torch.int32)
+    _check("q_weight", q_weight, (D,), torch.float32, optional=True)
+    _check("k_weight", k_weight, (D,), torch.float32, optional=True)
+    return dev, m3_qk_dims(T, Hq, Hk, D, D if rotary_dim is None else rotary_dim, code, flags, eps,
+                           base, ldq, ldk, 0, 0)
+
+
+def qk_norm_rope(q, k, positions, q_weight=None, k_weight=None, eps=1e-6, base=10000.0,
+                 rotary_dim=None, flags=0, stream=None):
+    """RMS norms of q [T, Hq, D] and k [T, Hk, D] per head and their rotation
+    by position (m3_qk_norm_rope).  Returns (q_out, k_out)."""
+    dev, d = _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags, {})
+    with _on(dev, stream):
+        qo = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        ko = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        e = _lib().m3_qk_norm_rope(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(q_weight),
+                                   _ptr(k_weight), _ptr(positions), _ptr(qo), _ptr(ko),
+                                   _stream(None))
+    if e != 0:
+        raise M3Error(e, "m3_qk_norm_rope")
+    return qo, ko
+
+
+def qk_norm_rope_backward(q, k, positions, dq_out, dk_out, q_weight=None, k_weight=None, eps=1e-6,
+                          base=10000.0, rotary_dim=None, flags=0, stream=None) -> dict:
+    """Gradients of qk_norm_rope: a dict with q, k in their dtype and, for the
+    weights that are given, q_weight, k_weight in fp32."""
+    dev, d = _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags,
+                       dict(dq_out=dq_out, dk_out=dk_out))
+    _check("dq_out", dq_out, q.shape, q.dtype)
+    _check("dk_out", dk_out, k.shape, q.dtype)
+    lib, f32 = _lib(), torch.float32
+    with _on(dev, stream):
+        g = dict(q=torch.empty(q.shape, dtype=q.dtype, device=dev),
+                 k=torch.empty(k.shape, dtype=q.dtype, device=dev))
+        for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            g[n] = None if w is None else torch.empty(w.shape, dtype=f32, device=dev)
+        ws = _ws(lib.m3_qk_norm_rope_backward_workspace_size(ctypes.byref(d)),
+                 "m3_qk_norm_rope_backward", dev)
+        e = lib.m3_qk_norm_rope_backward(
+            ctypes.byref(d), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+            _ptr(dq_out), _ptr(dk_out), _ptr(g["q"]), _ptr(g["k"]), _ptr(g["q_weight"]),
+            _ptr(g["k_weight"]), _ptr(ws), ws.numel(), _stream(None))
+    if e != 0:
+        raise M3Error(e, "m3_qk_norm_rope_backward")
+    return g
+
+
+def _attn_setup(q, k, v, cu_q, cu_k, scale, extra):
+    dev = _same_device(q=q, k=k, v=v, cu_seqlens_q=cu_q, cu_seqlens_k=cu_k, **extra)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [T, heads, headdim]")
+    Tq, Hq, D = q.shape
+    Tk, Hk = k.shape[:2]
+    code = dtype_code(q.dtype)
+    ld = [_rows("q", q, (Tq, Hq, D), q.dtype), _rows("k", k, (Tk, Hk, D), q.dtype),
+          _rows("v", v, (Tk, Hk, D), q.dtype)]
+    if cu_q.dim() != 1 or cu_q.numel() < 2:
+        raise ValueError("cu_seqlens_q must hold S + 1 offsets")
+    S = cu_q.numel() - 1
+    _check("cu_seqlens_q", cu_q, (S + 1,), torch.int32)
+    _check("cu_seqlens_k", cu_k, (S + 1,), torch.int32)
+    return dev, m3_attn_dims(S, Tq, Tk, Hq, Hk, D, code, D ** -0.5 if scale is None else scale,
+                             *ld, 0, 0, 0, 0)
+
+
+def attn_prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, scale=None, stream=None):
+    """Causal attention of packed sequences: q [Tq, Hq, D], k and v
+    [Tk, Hk, D] (m3_attn_prefill_varlen; scale D^-1/2 by default).  Returns
+    (o, lse).  Rows behind the last sequence are not written."""
+    dev, d = _attn_setup(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, {})
+    with _on(dev, stream):
+        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+        e = _lib().m3_attn_prefill_varlen(ctypes.byref(d), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
+                                          _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
+                                          _stream(None))
+    if e != 0:
+        raise M3Error(e, "m3_attn_prefill_varlen")
+    return o, lse
+
+
+def attn_prefill_varlen_backward(q, k, v, o, lse, d_o, cu_seqlens_q, cu_seqlens_k, scale=None,
+                                 stream=None):
+    """Gradients of attn_prefill_varlen for d_o: (dq, dk, dv)."""
+    dev, d = _attn_setup(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, dict(o=o, lse=lse, d_o=d_o))
+    d.ld_o = _rows("o", o, q.shape, q.dtype)
+    d.ld_do = _rows("d_o", d_o, q.shape, q.dtype)
+    _check("lse", lse, q.shape[:2], torch.float32)
+    lib = _lib()
+    with _on(dev, stream):
+        dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=dev) for t in (q, k, v))
+        ws = _ws(lib.m3_attn_prefill_varlen_backward_workspace_size(ctypes.byref(d)),
+                 "m3_attn_prefill_varlen_backward", dev)
+        e = lib.m3_attn_prefill_varlen_backward(
+            ctypes.byref(d), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(q), _ptr(k), _ptr(v),
+            _ptr(o), _ptr(lse), _ptr(d_o), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
+            _stream(None))
+    if e != 0:
+        raise M3Error(e, "m3_attn_prefill_varlen_backward")
+    return dq, dk, dv
+
+
+def attn_decode(q, k_cache, v_cache, lengths, scale=None, o=None, ws=None, stream=None):
+    """One token per sequence, q [S, Hq, D], against caches [S, cap, Hk, D]
+    holding lengths[s] rows (m3_attn_decode).  Returns (o, lse)."""
+    dev = _same_device(q=q, k_cache=k_cache, v_cache=v_cache, lengths=lengths, o=o, ws=ws)
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [S, Hq, D], the caches [S, cap, Hk, D]")
+    S, Hq, D = q.shape
+    cap, Hk = k_cache.shape[1:3]
+    code = dtype_code(q.dtype)
+    strides = []
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if tuple(t.shape) != (S, cap, Hk, D):
+            raise ValueError(f"{n}: shape {tuple(t.shape)} != expected {(S, cap, Hk, D)}")
+        if S > 1 and (t.stride(0) <= 0):
+            raise ValueError(f"{n}: sequences must not share rows")
+        strides.append((_rows(n, t[0], (cap, Hk, D), q.dtype), t.stride(0) if S > 1 else 0))
+    _check("lengths", lengths, (S,), torch.int32)
+    d = m3_attn_dims(S, 0, cap, Hq, Hk, D, code, D ** -0.5 if scale is None else scale,
+                     _rows("q", q, (S, Hq, D), q.dtype), strides[0][0], strides[1][0], 0, 0,
+                     strides[0][1], strides[1][1])
+    lib = _lib()
+    with _on(dev, stream):
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        d.ld_o = _rows("o", o, q.shape, q.dtype)
+        lse = torch.empty((S, Hq), dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = _ws(lib.m3_attn_decode_workspace_size(ctypes.byref(d)), "m3_attn_decode", dev)
+        e = lib.m3_attn_decode(ctypes.byref(d), _ptr(lengths), _ptr(q), _ptr(k_cache),
+                               _ptr(v_cache), _ptr(o), _ptr(lse), _ptr(ws),
+                               ws.numel() * ws.element_size(), _stream(None))
+    if e != 0:
+        raise M3Error(e, "m3_attn_decode")
+    return o, lse

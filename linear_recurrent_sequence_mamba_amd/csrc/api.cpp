@@ -9,7 +9,10 @@
 #include <mutex>
 
 #include "../../include/m3ssm.h"
+#include "attn.h"
+#include "gated.h"
 #include "m3_launch.h"
+#include "qk_norm.h"
 
 namespace {
 
@@ -186,6 +189,141 @@ m3_status scan_prefill(const m3_dims* d, const void* x, const void* dt, const fl
   return hip_status(err);
 }
 
+
+// ---------------------------------------------------------------------------
+// the other layers of a hybrid stack
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+bool bad_dtype(int t) { return t != M3_F32 && t != M3_BF16; }
+// a kernel's threads are counted in 32 bits
+bool grid_fits(int64_t blocks, int threads) { return blocks <= int64_t{0xffffffff} / threads; }
+
+template <size_t N>
+bool any_misaligned(const void* const (&p)[N]) {
+  for (const void* x : p)
+    if (x && misaligned(x)) return true;
+  return false;
+}
+
+m3_status check_gated(const m3_gated_dims* d, bool scan, bool packed) {
+  if (!d) return M3_ERR_NULL;
+  if (d->batch <= 0 || d->width <= 0 || (scan && d->seqlen <= 0)) return M3_ERR_SHAPE;
+  if (!isfinite(d->c) || d->c <= 0.0f) return M3_ERR_SHAPE;
+  const int64_t lds[] = {d->ld_x, d->ld_r, d->ld_i, d->ld_g};
+  for (int64_t ld : lds)
+    if (ld != 0 && ld < d->width) return M3_ERR_SHAPE;
+  if (bad_dtype(d->dtype)) return M3_ERR_DTYPE;
+  if (scan) {
+    const m3::GatedPlan p = m3::gated_plan(d->batch, d->seqlen, d->width, packed);
+    if (p.nchain > 0x7fffffff || !grid_fits(p.nchain * p.ntile, 1024)) return M3_ERR_SHAPE;
+  } else if (!grid_fits((static_cast<int64_t>(d->batch) * d->width + 255) / 256, 256)) {
+    return M3_ERR_SHAPE;
+  }
+  return M3_OK;
+}
+
+m3::GatedArgs gated_args(const m3_gated_dims* d) {
+  m3::GatedArgs g{};
+  g.B = d->batch;
+  g.T = d->seqlen;
+  g.D = d->width;
+  g.c = d->c;
+  g.ldx = d->ld_x ? d->ld_x : d->width;
+  g.ldr = d->ld_r ? d->ld_r : d->width;
+  g.ldi = d->ld_i ? d->ld_i : d->width;
+  g.ldg = d->ld_g ? d->ld_g : d->width;
+  return g;
+}
+
+m3_status check_qk(const m3_qk_dims* d) {
+  if (!d) return M3_ERR_NULL;
+  if (d->tokens <= 0 || d->nheads_q <= 0 || d->nheads_k <= 0 || d->headdim <= 0) return M3_ERR_SHAPE;
+  if (d->rotary_dim < 0 || d->rotary_dim > d->headdim || d->rotary_dim % 2) return M3_ERR_SHAPE;
+  if (d->flags & ~M3_ROPE_HALF) return M3_ERR_SHAPE;
+  if (!isfinite(d->eps) || d->eps < 0.0f) return M3_ERR_SHAPE;
+  if (!isfinite(d->base) || d->base <= 0.0) return M3_ERR_SHAPE;
+  if (bad_dtype(d->dtype)) return M3_ERR_DTYPE;
+  const int64_t wq = static_cast<int64_t>(d->nheads_q) * d->headdim;
+  const int64_t wk = static_cast<int64_t>(d->nheads_k) * d->headdim;
+  if (wq > 0x3fffffff || wk > 0x3fffffff) return M3_ERR_SHAPE;
+  if ((d->ld_q && d->ld_q < wq) || (d->ld_dq && d->ld_dq < wq) || (d->ld_k && d->ld_k < wk) ||
+      (d->ld_dk && d->ld_dk < wk))
+    return M3_ERR_SHAPE;
+  if (!m3::qk_norm_supported(d->headdim)) return M3_ERR_UNSUPPORTED;
+  if ((d->ld_q | d->ld_k | d->ld_dq | d->ld_dk) % 8) return M3_ERR_ALIGN;
+  return M3_OK;
+}
+
+m3::QkNormArgs qk_args(const m3_qk_dims* d) {
+  m3::QkNormArgs a{};
+  a.T = d->tokens;
+  a.Hq = d->nheads_q;
+  a.Hk = d->nheads_k;
+  a.D = d->headdim;
+  a.rot = d->rotary_dim;
+  a.half = (d->flags & M3_ROPE_HALF) != 0;
+  a.eps = d->eps;
+  const int64_t wq = static_cast<int64_t>(a.Hq) * a.D, wk = static_cast<int64_t>(a.Hk) * a.D;
+  a.ldq = d->ld_q ? d->ld_q : wq;
+  a.ldk = d->ld_k ? d->ld_k : wk;
+  a.ld_dq = d->ld_dq ? d->ld_dq : wq;
+  a.ld_dk = d->ld_dk ? d->ld_dk : wk;
+  const double turn = 0.15915494309189533577;   // 1 / (2 pi)
+  for (int j = 0; j < a.rot / 2; ++j) a.freq[j] = turn * pow(d->base, -2.0 * j / a.rot);
+  return a;
+}
+
+m3_status check_attn(const m3_attn_dims* d, bool decode) {
+  if (!d) return M3_ERR_NULL;
+  if (d->nseq <= 0 || d->tokens_k <= 0 || (!decode && d->tokens_q <= 0)) return M3_ERR_SHAPE;
+  if (d->nheads_q <= 0 || d->nheads_k <= 0 || d->headdim <= 0) return M3_ERR_SHAPE;
+  if (d->nheads_q % d->nheads_k) return M3_ERR_SHAPE;
+  if (!isfinite(d->scale)) return M3_ERR_SHAPE;
+  if (bad_dtype(d->dtype)) return M3_ERR_DTYPE;
+  if (!m3::attn_supported(d->headdim)) return M3_ERR_UNSUPPORTED;
+  const int64_t wq = static_cast<int64_t>(d->nheads_q) * d->headdim;
+  const int64_t wk = static_cast<int64_t>(d->nheads_k) * d->headdim;
+  if (wq > 0x3fffffff) return M3_ERR_SHAPE;
+  const int64_t lq[] = {d->ld_q, d->ld_o, d->ld_do}, lk[] = {d->ld_k, d->ld_v};
+  for (int64_t ld : lq)
+    if (ld != 0 && ld < wq) return M3_ERR_SHAPE;
+  for (int64_t ld : lk)
+    if (ld != 0 && ld < wk) return M3_ERR_SHAPE;
+  if (d->stride_k < 0 || d->stride_v < 0) return M3_ERR_SHAPE;
+  if ((d->ld_q | d->ld_o | d->ld_do | d->ld_k | d->ld_v | d->stride_k | d->stride_v) % 8)
+    return M3_ERR_ALIGN;
+  if (!decode) {
+    const int64_t tiles = (static_cast<int64_t>(d->tokens_q > d->tokens_k ? d->tokens_q
+                                                                          : d->tokens_k) >> 7) + d->nseq;
+    if (tiles > 0x7fffffff || !grid_fits(tiles * d->nheads_q, 256) ||
+        !grid_fits((static_cast<int64_t>(d->tokens_q) * d->nheads_q + 1) / 2, 32) ||
+        !grid_fits(static_cast<int64_t>(d->tokens_k) * wk / 1024 + 1, 256))
+      return M3_ERR_SHAPE;
+  } else if (!grid_fits(static_cast<int64_t>(d->nseq) * d->nheads_q * 512, 256)) {
+    return M3_ERR_SHAPE;
+  }
+  return M3_OK;
+}
+
+m3::AttnArgs attn_args(const m3_attn_dims* d) {
+  m3::AttnArgs a{};
+  a.S = d->nseq;
+  a.Tq = d->tokens_q;
+  a.Tk = d->tokens_k;
+  a.cap = d->tokens_k;
+  a.Hq = d->nheads_q;
+  a.Hk = d->nheads_k;
+  a.D = d->headdim;
+  a.scale = d->scale;
+  const int64_t wq = static_cast<int64_t>(a.Hq) * a.D, wk = static_cast<int64_t>(a.Hk) * a.D;
+  a.ldq = d->ld_q ? d->ld_q : wq;
+  a.ldo = d->ld_o ? d->ld_o : wq;
+  a.lddo = d->ld_do ? d->ld_do : wq;
+  a.ldk = d->ld_k ? d->ld_k : wk;
+  a.ldv = d->ld_v ? d->ld_v : wk;
+  a.bk = d->stride_k ? d->stride_k : a.cap * a.ldk;
+  a.bv = d->stride_v ? d->stride_v : a.cap * a.ldv;
+  return a;
+}
 
 }  // namespace
 
@@ -473,6 +611,229 @@ m3_status m3_decode_tokens(const m3_dims* d, float* h, const void* x, const void
                                static_cast<int>(units), static_cast<hipStream_t>(stream), &err) != 0)
     return M3_ERR_UNSUPPORTED;
   return hip_status(err);
+}
+
+size_t m3_gated_scan_workspace_size(const m3_gated_dims* d, int packed) {
+  if (check_gated(d, true, packed != 0) != M3_OK) return 0;
+  return m3::gated_workspace_bytes(d->batch, d->seqlen, d->width, packed != 0, false);
+}
+
+size_t m3_gated_scan_backward_workspace_size(const m3_gated_dims* d, int packed) {
+  if (check_gated(d, true, packed != 0) != M3_OK) return 0;
+  return m3::gated_workspace_bytes(d->batch, d->seqlen, d->width, packed != 0, true);
+}
+
+m3_status m3_gated_scan(const m3_gated_dims* d, const int32_t* cu_seqlens, const void* x,
+                        const void* r, const void* i, const float* decay, const float* h0, void* y,
+                        float* hT, float* states, void* ws, size_t ws_bytes, void* stream) {
+  const bool packed = cu_seqlens != nullptr;
+  m3_status st = check_gated(d, true, packed);
+  if (st != M3_OK) return st;
+  if (!x || !r || !i || !decay || !y) return M3_ERR_NULL;
+  const void* const ptrs[] = {x, r, i, decay, h0, y, hT, states, ws};
+  if (any_misaligned(ptrs) || misaligned4(cu_seqlens)) return M3_ERR_ALIGN;
+  if (!ws || ws_bytes < m3::gated_workspace_bytes(d->batch, d->seqlen, d->width, packed, false))
+    return M3_ERR_WORKSPACE;
+  m3::GatedArgs g = gated_args(d);
+  g.cu = cu_seqlens;
+  g.x = x;
+  g.r = r;
+  g.i = i;
+  g.decay = decay;
+  g.h0 = h0;
+  g.y = y;
+  g.hT = hT;
+  g.states = states;
+  m3::gated_carve(g, ws);
+  return hip_status(m3::launch_gated_scan(g, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
+}
+
+m3_status m3_gated_scan_backward(const m3_gated_dims* d, const int32_t* cu_seqlens, const void* x,
+                                 const void* r, const void* i, const float* decay, const float* h0,
+                                 const float* states, const void* dy, const float* dhT, void* dx,
+                                 void* dr, void* di, float* ddecay, float* dh0, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  const bool packed = cu_seqlens != nullptr;
+  m3_status st = check_gated(d, true, packed);
+  if (st != M3_OK) return st;
+  if (!x || !r || !i || !decay || !states || !dy || !dx || !dr || !di || !ddecay)
+    return M3_ERR_NULL;
+  const void* const ptrs[] = {x, r, i, decay, h0, states, dy, dhT, dx, dr, di, ddecay, dh0, ws};
+  if (any_misaligned(ptrs) || misaligned4(cu_seqlens)) return M3_ERR_ALIGN;
+  if (!ws || ws_bytes < m3::gated_workspace_bytes(d->batch, d->seqlen, d->width, packed, true))
+    return M3_ERR_WORKSPACE;
+  m3::GatedArgs g = gated_args(d);
+  g.cu = cu_seqlens;
+  g.x = x;
+  g.r = r;
+  g.i = i;
+  g.decay = decay;
+  g.h0 = h0;
+  g.cstates = states;
+  g.dy = dy;
+  g.dhT = dhT;
+  g.dx = dx;
+  g.dr = dr;
+  g.di = di;
+  g.ddecay = ddecay;
+  g.dh0 = dh0;
+  m3::gated_carve(g, ws);
+  return hip_status(
+      m3::launch_gated_backward(g, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
+}
+
+m3_status m3_gated_step(const m3_gated_dims* d, float* h, const void* x, const void* r,
+                        const void* i, const float* decay, void* y, void* stream) {
+  m3_status st = check_gated(d, false, false);
+  if (st != M3_OK) return st;
+  if (!h || !x || !r || !i || !decay || !y) return M3_ERR_NULL;
+  const void* const ptrs[] = {h, x, r, i, decay, y};
+  if (any_misaligned(ptrs)) return M3_ERR_ALIGN;
+  m3::GatedArgs g = gated_args(d);
+  g.x = x;
+  g.r = r;
+  g.i = i;
+  g.decay = decay;
+  g.y = y;
+  return hip_status(m3::launch_gated_step(g, h, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
+}
+
+m3_status m3_qk_norm_rope(const m3_qk_dims* d, const void* q, const void* k, const float* q_weight,
+                          const float* k_weight, const int32_t* positions, void* q_out, void* k_out,
+                          void* stream) {
+  m3_status st = check_qk(d);
+  if (st != M3_OK) return st;
+  if (!q || !k || !positions || !q_out || !k_out) return M3_ERR_NULL;
+  const void* const ptrs[] = {q, k, q_weight, k_weight, q_out, k_out};
+  if (any_misaligned(ptrs) || misaligned4(positions)) return M3_ERR_ALIGN;
+  m3::QkNormArgs a = qk_args(d);
+  a.q = q;
+  a.k = k;
+  a.wq = q_weight;
+  a.wk = k_weight;
+  a.pos = positions;
+  a.qo = q_out;
+  a.ko = k_out;
+  return hip_status(m3::launch_qk_norm(a, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
+}
+
+size_t m3_qk_norm_rope_backward_workspace_size(const m3_qk_dims* d) {
+  if (check_qk(d) != M3_OK) return 0;
+  return m3::qk_norm_workspace_bytes(d->tokens, d->nheads_q, d->nheads_k, d->headdim);
+}
+
+m3_status m3_qk_norm_rope_backward(const m3_qk_dims* d, const void* q, const void* k,
+                                   const float* q_weight, const float* k_weight,
+                                   const int32_t* positions, const void* dq_out, const void* dk_out,
+                                   void* dq, void* dk, float* dq_weight, float* dk_weight, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  m3_status st = check_qk(d);
+  if (st != M3_OK) return st;
+  if (!q || !k || !positions || !dq_out || !dk_out || !dq || !dk) return M3_ERR_NULL;
+  const void* const ptrs[] = {q, k, q_weight, k_weight, dq_out, dk_out, dq, dk, dq_weight, dk_weight, ws};
+  if (any_misaligned(ptrs) || misaligned4(positions)) return M3_ERR_ALIGN;
+  if (!ws || ws_bytes < m3::qk_norm_workspace_bytes(d->tokens, d->nheads_q, d->nheads_k, d->headdim))
+    return M3_ERR_WORKSPACE;
+  m3::QkNormArgs a = qk_args(d);
+  a.q = q;
+  a.k = k;
+  a.wq = q_weight;
+  a.wk = k_weight;
+  a.pos = positions;
+  a.gq = dq_out;
+  a.gk = dk_out;
+  a.dq = dq;
+  a.dk = dk;
+  a.dwq = dq_weight;
+  a.dwk = dk_weight;
+  a.part = static_cast<float*>(ws);
+  return hip_status(
+      m3::launch_qk_norm_backward(a, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
+}
+
+m3_status m3_attn_prefill_varlen(const m3_attn_dims* d, const int32_t* cu_seqlens_q,
+                                 const int32_t* cu_seqlens_k, const void* q, const void* k,
+                                 const void* v, void* o, float* lse, void* stream) {
+  m3_status st = check_attn(d, false);
+  if (st != M3_OK) return st;
+  if (!cu_seqlens_q || !cu_seqlens_k || !q || !k || !v || !o) return M3_ERR_NULL;
+  const void* const ptrs[] = {q, k, v, o, lse};
+  if (any_misaligned(ptrs) || misaligned4(cu_seqlens_q) || misaligned4(cu_seqlens_k))
+    return M3_ERR_ALIGN;
+  m3::AttnArgs a = attn_args(d);
+  a.cuq = cu_seqlens_q;
+  a.cuk = cu_seqlens_k;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.lse = lse;
+  return hip_status(m3::launch_attn(a, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
+}
+
+size_t m3_attn_prefill_varlen_backward_workspace_size(const m3_attn_dims* d) {
+  if (check_attn(d, false) != M3_OK) return 0;
+  return m3::attn_backward_workspace_bytes(d->tokens_q, d->tokens_k, d->nseq, d->nheads_q,
+                                           d->nheads_k, d->headdim);
+}
+
+m3_status m3_attn_prefill_varlen_backward(const m3_attn_dims* d, const int32_t* cu_seqlens_q,
+                                          const int32_t* cu_seqlens_k, const void* q, const void* k,
+                                          const void* v, const void* o, const float* lse,
+                                          const void* d_o, void* dq, void* dk, void* dv, void* ws,
+                                          size_t ws_bytes, void* stream) {
+  m3_status st = check_attn(d, false);
+  if (st != M3_OK) return st;
+  if (!cu_seqlens_q || !cu_seqlens_k || !q || !k || !v || !o || !lse || !d_o || !dq || !dk || !dv)
+    return M3_ERR_NULL;
+  const void* const ptrs[] = {q, k, v, o, lse, d_o, dq, dk, dv, ws};
+  if (any_misaligned(ptrs) || misaligned4(cu_seqlens_q) || misaligned4(cu_seqlens_k))
+    return M3_ERR_ALIGN;
+  if (!ws || ws_bytes < m3::attn_backward_workspace_bytes(d->tokens_q, d->tokens_k, d->nseq,
+                                                          d->nheads_q, d->nheads_k, d->headdim))
+    return M3_ERR_WORKSPACE;
+  m3::AttnArgs a = attn_args(d);
+  a.cuq = cu_seqlens_q;
+  a.cuk = cu_seqlens_k;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.co = o;
+  a.clse = lse;
+  a.dout = d_o;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  return hip_status(
+      m3::launch_attn_backward(a, d->dtype == M3_BF16, ws, static_cast<hipStream_t>(stream)));
+}
+
+size_t m3_attn_decode_workspace_size(const m3_attn_dims* d) {
+  if (check_attn(d, true) != M3_OK) return 0;
+  const size_t n = m3::attn_decode_workspace_bytes(d->nseq, d->tokens_k, d->nheads_q, d->nheads_k,
+                                                   d->headdim);
+  return n ? n : 16;
+}
+
+m3_status m3_attn_decode(const m3_attn_dims* d, const int32_t* lengths, const void* q,
+                         const void* k, const void* v, void* o, float* lse, void* ws,
+                         size_t ws_bytes, void* stream) {
+  m3_status st = check_attn(d, true);
+  if (st != M3_OK) return st;
+  if (!lengths || !q || !k || !v || !o) return M3_ERR_NULL;
+  const void* const ptrs[] = {q, k, v, o, lse, ws};
+  if (any_misaligned(ptrs) || misaligned4(lengths)) return M3_ERR_ALIGN;
+  const size_t need = m3::attn_decode_workspace_bytes(d->nseq, d->tokens_k, d->nheads_q,
+                                                      d->nheads_k, d->headdim);
+  if (need && (!ws || ws_bytes < need)) return M3_ERR_WORKSPACE;
+  m3::AttnArgs a = attn_args(d);
+  a.len = lengths;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.lse = lse;
+  return hip_status(m3::launch_attn_decode(a, d->dtype == M3_BF16, ws, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

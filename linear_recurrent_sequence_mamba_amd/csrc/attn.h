@@ -1,0 +1,41 @@
+// attn.h -- host-side launch interface of the causal attention kernels.  Not
+// part of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace m3 {
+
+struct AttnArgs {
+  const void *q, *k, *v;        // rows of H heads of D, ld* elements apart
+  const int32_t *cuq, *cuk;     // [S + 1] row offsets of the sequences
+  void* o;                      // rows ldo apart
+  float* lse;                   // [Tq, Hq] (decode: [S, Hq])
+  // backward
+  const void *co, *dout;        // o and its gradient, rows ldo / lddo apart
+  const float* clse;
+  void *dq, *dk, *dv;           // dense rows
+  float2* stat;                 // workspace [Hq, Tq]: lse log2(e) and <o, do>
+  float *pk, *pv;               // workspace [gsplit, Tk, Hk, D]: parts of dk, dv
+  // decode
+  const int32_t* len;           // [S] rows of each sequence's cache
+  float *po, *pm;               // workspace: parts of o and their (max, sum)
+  int64_t ldq, ldk, ldv, ldo, lddo;
+  int64_t bk, bv;               // decode: elements from one sequence's cache to the next
+  int Tq, Tk, S, Hq, Hk, D;
+  int cap;                      // decode: rows a cache has room for
+  int gsplit;                   // parts of a group of heads (backward of k, v)
+  int nsplit;                   // parts of a cache (decode)
+  float scale;
+};
+
+bool attn_supported(int D);
+size_t attn_backward_workspace_bytes(int Tq, int Tk, int S, int Hq, int Hk, int D);
+size_t attn_decode_workspace_bytes(int S, int cap, int Hq, int Hk, int D);
+hipError_t launch_attn(AttnArgs& a, int bf16, hipStream_t s);
+hipError_t launch_attn_backward(AttnArgs& a, int bf16, void* ws, hipStream_t s);
+hipError_t launch_attn_decode(AttnArgs& a, int bf16, void* ws, hipStream_t s);
+
+}  // namespace m3

@@ -1,0 +1,414 @@
+// attn.hip -- causal attention over packed sequences, and one token against a
+// cache (gfx950).
+//
+//   s = scale <q_i, k_j> for keys j <= i + (Lk - Lq),  p = softmax(s),
+//   o_i = sum_j p_ij v_j,  lse_i = log sum_j exp(s_ij)
+//
+// Head h of q reads head h / (Hq / Hk) of k and v.  A row that sees no key
+// has o = 0 and lse = -inf.
+//
+// The tiles are transposed (keys by queries), so that a query is a lane: the
+// running maximum and sum of the softmax are one number per lane, a row of
+// scores is reduced inside the lane and one exchange, and the weights are the
+// B operand of the second product as they stand.
+#include "attn_common.h"
+
+namespace m3 {
+namespace {
+
+// ---------------------------------------------------------------------------
+// The state of 32 queries: o transposed, maximum and sum (this lane's keys)
+template <int D>
+struct Rows {
+  f16v o[D / 32];
+  float m, l;
+  __device__ __forceinline__ void init() {
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) o[d] = f16v{};
+    m = -INFINITY;
+    l = 0.0f;
+  }
+};
+
+// Infinities and NaN of a tile of V in LDS become 0; returns whether this
+// thread found any.  (The zero weights of keys that a query does not see would
+// make NaN of them; they are added afterwards where they are seen.)
+__device__ __forceinline__ bool special(bf16_t v) { return (v.bits & 0x7f80u) == 0x7f80u; }
+__device__ __forceinline__ bool special(float v) {
+  return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u;
+}
+template <typename T, int D, int ROWS, int THREADS>
+__device__ __forceinline__ bool drop_special(T* V) {
+  bool found = false;
+#pragma unroll
+  for (int n = 0; n < ROWS * D * static_cast<int>(sizeof(T)) / 16 / THREADS; ++n) {
+    uint4* p = reinterpret_cast<uint4*>(V) + n * THREADS + threadIdx.x;
+    uint4 u = *p;
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 2) {
+        const bool lo = (w[j] & 0x7f80u) == 0x7f80u, hi = (w[j] & 0x7f800000u) == 0x7f800000u;
+        w[j] &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
+        bad |= lo | hi;
+      } else {
+        const bool b = (w[j] & 0x7f800000u) == 0x7f800000u;
+        if (b) w[j] = 0u;
+        bad |= b;
+      }
+    }
+    if (bad) *p = uint4{w[0], w[1], w[2], w[3]};
+    found |= bad;
+  }
+  return found;
+}
+
+// One tile of NB x 32 keys against 32 queries.  seen: how many of the tile's
+// keys this lane's query sees (may be <= 0 or more than the tile has).
+// MASK: some lane sees fewer than all.
+template <typename T, int D, int NB, bool MASK>
+__device__ __forceinline__ void attend(Rows<D>& st, const Frag<T>* q, const T* K, const T* V,
+                                       float c, int seen, int lane) {
+  using L = Tile<T, D>;
+  const int half = lane >> 5;
+  f16v s[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    s[b] = f16v{};
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) s[b] = mma(L::frag(K, 32 * b, kk, lane), q[kk], s[b]);
+  }
+  if (MASK) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        s[b][i] = 32 * b + row_of(i, half) < seen ? s[b][i] : -INFINITY;
+  }
+  float mx = s[0][0];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
+  mx = fmaxf(mx, other_half(mx)) * c;
+  // The maximum moves only when it has to: weights up to 2^8 lose nothing in
+  // fp32 sums or bf16 products, and most tiles then leave o as it is.
+  if (__ballot(mx > st.m + 8.0f)) {
+    const float m = fmaxf(st.m, mx);
+    const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
+    st.m = m;
+    st.l *= f;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) st.o[d][i] *= f;
+  }
+  const float m0 = st.m == -INFINITY ? 0.0f : st.m;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], c, -m0));
+      st.l += s[b][i];
+    }
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      Frag<T> p;
+      float e8[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e8[j] = s[b][8 * w + j];
+      frag_from(p, e8);
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+        st.o[d] = mma(L::frag_t(V, 32 * b + 16 * w, 32 * d, lane), p, st.o[d]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The prompt: a workgroup takes 32 WAVES queries of one head; K and V tiles
+// of BN keys are double-buffered in LDS.
+template <typename T, int D, int BN, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn(AttnArgs a) {
+  using L = Tile<T, D>;
+  constexpr int BM = 32 * WAVES, NB = BN / 32;
+  __shared__ __align__(16) T sK[2][BN * D], sV[2][BN * D];
+  __shared__ int sSpecial;
+  if (threadIdx.x == 0) sSpecial = 0;   // read after the tiles' barriers
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nslot = gridDim.x / a.Hq;
+  const int h = blockIdx.x % a.Hq;
+  // late tiles of a sequence see most keys: they start first
+  const Slot sl = slot_of<BM>(a.cuq, a.S, a.Tq, nslot - 1 - static_cast<int>(blockIdx.x / a.Hq), lane);
+  if (sl.s < 0) return;
+  const int q0 = clamp_row(a.cuq[sl.s], a.Tq), q1 = clamp_row(a.cuq[sl.s + 1], a.Tq);
+  const int k0 = clamp_row(a.cuk[sl.s], a.Tk), k1 = clamp_row(a.cuk[sl.s + 1], a.Tk);
+  const int Lq = q1 - q0, Lk = max(0, k1 - k0);
+  const int i0 = sl.tile * BM;
+  if (i0 >= Lq) return;
+  const int off = Lk - Lq;
+  const int hk = h / (a.Hq / a.Hk);
+
+  const int half = lane >> 5;
+  const int iw = i0 + 32 * wave;               // the wave's first query
+  const int i = iw + (lane & 31);              // the lane's
+  const int64_t row = q0 + min(i, Lq - 1);
+  Frag<T> q[D / 16];
+  {
+    const T* p = static_cast<const T*>(a.q) + row * a.ldq + h * D + 8 * half;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) frag_load(q[kk], p + 16 * kk);
+  }
+  Rows<D> st;
+  st.init();
+  const float c = a.scale * kLog2eA;
+  const int sees = min(i, Lq - 1) + off + 1;   // keys that the lane's query sees
+  const int most = min(min(i0 + BM, Lq) + off, Lk);   // that any query of the block sees
+  const int ntile = most <= 0 ? 0 : (most + BN - 1) / BN;
+  // from here on some query of the block does not see the whole tile
+  const int tmask = max(0, min(i0, Lq - 1) + off + 1) / BN;
+  const int wmost = min(min(iw + 32, Lq) + off, Lk);
+  const int wleast = min(iw, Lq - 1) + off + 1;
+  const T* kp = static_cast<const T*>(a.k) + static_cast<int64_t>(k0) * a.ldk + hk * D;
+  const T* vp = static_cast<const T*>(a.v) + static_cast<int64_t>(k0) * a.ldv + hk * D;
+  if (ntile > 0) {
+    L::template load<BN, WAVES>(sK[0], kp, a.ldk, 0, Lk - 1, wave, lane);
+    L::template load<BN, WAVES>(sV[0], vp, a.ldv, 0, Lk - 1, wave, lane);
+  }
+  for (int t = 0; t < ntile; ++t) {
+    lds_loads_done();
+    __syncthreads();   // tile t is there, and every wave is done with t - 1
+    if (t + 1 < ntile) {
+      L::template load<BN, WAVES>(sK[(t + 1) & 1], kp, a.ldk, (t + 1) * BN, Lk - 1, wave, lane);
+      L::template load<BN, WAVES>(sV[(t + 1) & 1], vp, a.ldv, (t + 1) * BN, Lk - 1, wave, lane);
+    }
+    const int j0 = t * BN;
+    const T *K = sK[t & 1], *V = sV[t & 1];
+    if (t >= tmask) {
+      if (drop_special<T, D, BN, 64 * WAVES>(sV[t & 1])) sSpecial = 1;
+      __syncthreads();
+    }
+    if (j0 >= wmost) continue;
+    if (j0 + BN <= wleast)
+      attend<T, D, NB, false>(st, q, K, V, c, BN, lane);
+    else
+      attend<T, D, NB, true>(st, q, K, V, c, sees - j0, lane);
+  }
+  if (ntile > 0 && sSpecial) {
+    for (int key = tmask * BN; key < most; ++key) {
+      const T* r = vp + key * a.ldv + 4 * half;
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const T v = r[32 * d + row_of(e, 0)];
+          if (key < sees && special(v)) st.o[d][e] += to_f32(v);
+        }
+    }
+  }
+  const float l = st.l + other_half(st.l);
+  if (i >= Lq) return;
+  const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);   // a NaN stays
+  T* o = static_cast<T*>(a.o) + row * a.ldo + h * D + 4 * half;
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      put4(o + 32 * d + 8 * e, st.o[d][4 * e] * inv, st.o[d][4 * e + 1] * inv,
+           st.o[d][4 * e + 2] * inv, st.o[d][4 * e + 3] * inv);
+  if (half == 0 && a.lse)
+    a.lse[row * a.Hq + h] = l == 0.0f ? -INFINITY : (st.m + __builtin_amdgcn_logf(l)) * kLn2A;
+}
+
+// ---------------------------------------------------------------------------
+// One token: the queries of a group of heads (at most 32 at a time) are the
+// tile's columns.  A workgroup takes a part of one sequence's cache, its
+// waves every WAVES-th tile of 32 keys each, without barriers; the waves'
+// sums are joined in LDS and the parts by k_attn_join.
+template <typename T, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
+  using L = Tile<T, D>;
+  constexpr int BN = 32;
+  // a wave's two K and two V tiles; afterwards its o [32][D] in fp32
+  __shared__ __align__(16) T sKV[WAVES][2][2][BN * D];
+  __shared__ float sM[WAVES][32], sL[WAVES][32];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, g = a.Hq / a.Hk, ng = (g + 31) / 32;
+  int n = blockIdx.x;
+  const int part = n % a.nsplit;
+  n /= a.nsplit;
+  const int gb = n % ng;
+  n /= ng;
+  const int hk = n % a.Hk, s = n / a.Hk;
+  const int len = max(0, min(a.len[s], a.cap));
+  // the part's keys, in whole tiles
+  const int tiles = (len + BN - 1) / BN;
+  const int per = (tiles + a.nsplit - 1) / a.nsplit;
+  const int t0 = part * per, t1 = min(t0 + per, tiles);
+  const int hl = min(gb * 32 + (lane & 31), g - 1);   // the lane's head in the group
+  const int h = hk * g + hl;
+  Frag<T> q[D / 16];
+  {
+    const T* p = static_cast<const T*>(a.q) + s * a.ldq + h * D + 8 * half;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) frag_load(q[kk], p + 16 * kk);
+  }
+  Rows<D> st;
+  st.init();
+  const float c = a.scale * kLog2eA;
+  const T* kp = static_cast<const T*>(a.k) + s * a.bk + hk * D;
+  const T* vp = static_cast<const T*>(a.v) + s * a.bv + hk * D;
+  int t = t0 + wave;
+  if (t < t1) {
+    L::template load<BN, 1>(sKV[wave][0][0], kp, a.ldk, t * BN, len - 1, 0, lane);
+    L::template load<BN, 1>(sKV[wave][0][1], vp, a.ldv, t * BN, len - 1, 0, lane);
+  }
+  for (int u = 0; t < t1; t += WAVES, ++u) {
+    lds_loads_done();
+    if (t + WAVES < t1) {
+      L::template load<BN, 1>(sKV[wave][(u + 1) & 1][0], kp, a.ldk, (t + WAVES) * BN, len - 1, 0, lane);
+      L::template load<BN, 1>(sKV[wave][(u + 1) & 1][1], vp, a.ldv, (t + WAVES) * BN, len - 1, 0, lane);
+    }
+    const T *K = sKV[wave][u & 1][0], *V = sKV[wave][u & 1][1];
+    // rows past the end repeat the last one, which every query sees
+    if ((t + 1) * BN <= len)
+      attend<T, D, 1, false>(st, q, K, V, c, BN, lane);
+    else
+      attend<T, D, 1, true>(st, q, K, V, c, len - t * BN, lane);
+  }
+  const float l = st.l + other_half(st.l);
+  if (half == 0) {
+    sM[wave][lane] = st.m;
+    sL[wave][lane] = l;
+  }
+  // o of this wave, over its own tiles (of which it is done reading)
+  static_assert(sizeof(T) * 4 * BN * D >= sizeof(float) * 32 * D, "room for o");
+  float* so = reinterpret_cast<float*>(&sKV[wave][0][0][0]);
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) so[(lane & 31) * D + 32 * d + row_of(e, half)] = st.o[d][e];
+  __syncthreads();
+  const int rows = min(32, g - gb * 32);
+  for (int x = threadIdx.x; x < rows * (D / 4); x += 64 * WAVES) {
+    const int r = x / (D / 4), d = 4 * (x % (D / 4));
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) m = fmaxf(m, sM[w][r]);
+    float ls = 0.0f;
+    f4 v = f4{0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const float f = sM[w][r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(sM[w][r] - m);
+      const float lw = sL[w][r];
+      // a wave that saw no key has l = 0 and o = 0
+      if (lw != 0.0f) {
+        ls = fmaf(f, lw, ls);
+        const f4 ow = *reinterpret_cast<const f4*>(reinterpret_cast<const float*>(&sKV[w][0][0][0]) + r * D + d);
+        v.x = fmaf(f, ow.x, v.x);
+        v.y = fmaf(f, ow.y, v.y);
+        v.z = fmaf(f, ow.z, v.z);
+        v.w = fmaf(f, ow.w, v.w);
+      }
+    }
+    const int hh = hk * g + gb * 32 + r;
+    if (a.nsplit == 1) {
+      const float inv = ls > 0.0f ? 1.0f / ls : (ls == ls ? 0.0f : ls);
+      put4(static_cast<T*>(a.o) + static_cast<int64_t>(s) * a.ldo + hh * D + d, v.x * inv, v.y * inv,
+           v.z * inv, v.w * inv);
+      if (d == 0 && a.lse)
+        a.lse[static_cast<int64_t>(s) * a.Hq + hh] =
+            ls == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(ls)) * kLn2A;
+    } else {
+      const int64_t at = (static_cast<int64_t>(s) * a.Hq + hh) * a.nsplit + part;
+      *reinterpret_cast<f4*>(a.po + at * D + d) = v;
+      if (d == 0) *reinterpret_cast<f2*>(a.pm + 2 * at) = f2{m, ls};
+    }
+  }
+}
+
+// joins the parts of one (sequence, head): D / 4 threads of four channels,
+// 256 / (D / 4) heads per workgroup
+template <typename T, int D>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * (1024 / D) + threadIdx.x / (D / 4);
+  if (n >= static_cast<int64_t>(a.S) * a.Hq) return;
+  const int d = 4 * (threadIdx.x % (D / 4));
+  const f2* pm = reinterpret_cast<const f2*>(a.pm) + n * a.nsplit;
+  float m = -INFINITY;
+  for (int p = 0; p < a.nsplit; ++p) m = fmaxf(m, pm[p].x);
+  float l = 0.0f;
+  f4 v = f4{0, 0, 0, 0};
+  for (int p = 0; p < a.nsplit; ++p) {
+    const f2 ml = pm[p];
+    if (ml.y == 0.0f) continue;
+    const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - m);
+    const f4 o = *reinterpret_cast<const f4*>(a.po + (n * a.nsplit + p) * D + d);
+    l = fmaf(f, ml.y, l);
+    v.x = fmaf(f, o.x, v.x);
+    v.y = fmaf(f, o.y, v.y);
+    v.z = fmaf(f, o.z, v.z);
+    v.w = fmaf(f, o.w, v.w);
+  }
+  const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+  const int64_t s = n / a.Hq;
+  const int h = static_cast<int>(n % a.Hq);
+  put4(static_cast<T*>(a.o) + s * a.ldo + h * D + d, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  if (d == 0 && a.lse) a.lse[n] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2A;
+}
+
+template <typename T, int D, int BN>
+hipError_t run_attn(const AttnArgs& a, hipStream_t s) {
+  constexpr int BM = 128;
+  const int64_t slots = a.Tq / BM + a.S;
+  k_attn<T, D, BN, BM / 32><<<static_cast<unsigned>(slots * a.Hq), 2 * BM, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, int D, int WAVES>
+hipError_t run_decode(const AttnArgs& a, hipStream_t s) {
+  const int g = a.Hq / a.Hk, ng = (g + 31) / 32;
+  const int64_t grid = static_cast<int64_t>(a.S) * a.Hk * ng * a.nsplit;
+  k_attn_decode<T, D, WAVES><<<static_cast<unsigned>(grid), 64 * WAVES, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.nsplit == 1) return e;
+  const int64_t heads = static_cast<int64_t>(a.S) * a.Hq, per = 1024 / D;
+  k_attn_join<T, D><<<static_cast<unsigned>((heads + per - 1) / per), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// Parts of a cache: enough workgroups for the chip (two a CU), each with at
+// least four tiles of 32 keys for each of its four waves.
+int decode_parts(int S, int cap, int Hq, int Hk) {
+  const int64_t blocks = static_cast<int64_t>(S) * Hk * ((Hq / Hk + 31) / 32);
+  int64_t n = (512 + blocks - 1) / blocks;
+  const int64_t most = (cap + 511) / 512;
+  if (n > most) n = most;
+  return n < 1 ? 1 : static_cast<int>(n);
+}
+
+}  // namespace
+
+bool attn_supported(int D) { return D == 64 || D == 128; }
+
+hipError_t launch_attn(AttnArgs& a, int bf16, hipStream_t s) {
+  if (bf16) return a.D == 64 ? run_attn<bf16_t, 64, 64>(a, s) : run_attn<bf16_t, 128, 64>(a, s);
+  return a.D == 64 ? run_attn<float, 64, 32>(a, s) : run_attn<float, 128, 32>(a, s);
+}
+
+size_t attn_decode_workspace_bytes(int S, int cap, int Hq, int Hk, int D) {
+  const int n = decode_parts(S, cap, Hq, Hk);
+  return n == 1 ? 0 : sizeof(float) * (static_cast<size_t>(D) + 2) * S * Hq * n;
+}
+
+hipError_t launch_attn_decode(AttnArgs& a, int bf16, void* ws, hipStream_t s) {
+  a.nsplit = decode_parts(a.S, a.cap, a.Hq, a.Hk);
+  a.po = static_cast<float*>(ws);
+  a.pm = a.po + static_cast<size_t>(a.D) * a.S * a.Hq * a.nsplit;
+  if (bf16) return a.D == 64 ? run_decode<bf16_t, 64, 4>(a, s) : run_decode<bf16_t, 128, 4>(a, s);
+  return a.D == 64 ? run_decode<float, 64, 4>(a, s) : run_decode<float, 128, 2>(a, s);
+}
+
+}  // namespace m3

@@ -1,0 +1,711 @@
+// gated.hip -- the gated linear recurrence (gfx950): the scan over a prompt
+// (dense or packed), one decode step, and the gradients of the scan.
+//
+//   L_t = -c softplus(decay) sigmoid(r_t),   a_t = exp(L_t),
+//   m_t = sqrt(1 - a_t^2),                   u_t = sigmoid(i_t) x_t,
+//   h_t = a_t h_{t-1} + m_t u_t
+//
+// per channel, in fp32.  1 - a_t^2 is -expm1(2 L_t): a polynomial near zero,
+// where 1 - a^2 would cancel.  The gradients follow the adjoint
+// g_t = dy_t + a_{t+1} g_{t+1} (plus dhT at a sequence's end), carried here
+// as q_t = a_t g_t; with d m / d L = -a^2 / m the gradient of L appears only
+// as dL_t L_t, in which L / m has the limit 0 at a = 1.
+#include "m3_device.h"
+#include "gated.h"
+
+namespace m3 {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+typedef unsigned long long u64;
+
+// V consecutive channels as loaded (V = 2 needs an even channel)
+template <typename T, int V>
+using Raw = RawVec<T, V>;
+
+template <typename T, int V>
+__device__ __forceinline__ void store_v(T* p, const float* v) {
+  if constexpr (V == 1) {
+    p[0] = from_f32<T>(v[0]);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) reinterpret_cast<f2*>(p)[k] = f2{v[2 * k], v[2 * k + 1]};
+  } else {
+    uint32_t w[V / 2];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      const bh2 b = __builtin_convertvector(f2{v[2 * k], v[2 * k + 1]}, bh2);
+      w[k] = __builtin_bit_cast(uint32_t, b);
+    }
+    if constexpr (V == 8) {
+      *reinterpret_cast<uint4*>(p) = uint4{w[0], w[1], w[2], w[3]};
+    } else {
+      *reinterpret_cast<uint32_t*>(p) = w[0];
+    }
+  }
+}
+
+// -c softplus(decay) log2(e), the factor of sigmoid(r) in log2(a)
+__device__ __forceinline__ float decay_factor(float d, float c) {
+  return -c * kLog2e * (fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d))));
+}
+
+__device__ __forceinline__ float sigmoid(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * v));
+}
+
+// a and 1 - a^2 from log2(a) <= 0.  The polynomial interpolates
+// (e^z - 1) / z on [-0.35, 0] at Chebyshev points (relative error 1.5e-8);
+// below that 1 - a^2 >= 0.3 loses nothing that fp32 keeps.
+__device__ __forceinline__ void decay_of(float l2, float& a, float& m2) {
+  a = __builtin_amdgcn_exp2f(l2);
+  const float z = (2.0f * kLn2) * l2;
+  float p = fmaf(z, 7.2112456e-03f, 4.1331873e-02f);
+  p = fmaf(z, p, 1.6662531e-01f);
+  p = fmaf(z, p, 4.9999820e-01f);
+  p = fmaf(z, p, 0.99999999f);
+  m2 = z > -0.35f ? -z * p : fmaf(-a, a, 1.0f);
+}
+
+// ---------------------------------------------------------------------------
+// Carries between the time tiles of one channel.  A tile's workgroup takes a
+// ticket when it starts; tickets run over the tiles in the order in which the
+// carry moves, so whoever waits for a carry waits for a workgroup that has
+// started already and that waits, in turn, only for earlier tickets: every
+// wait ends.  Value and flag travel in one 8-byte word, which needs no fence.
+__device__ __forceinline__ void publish(u64* slot, float v) {
+  __hip_atomic_store(slot, (u64{1} << 32) | __float_as_uint(v), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float await_carry(const u64* slot) {
+  u64 w;
+  while (((w = __hip_atomic_load(slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) >> 32) == 0)
+    __builtin_amdgcn_s_sleep(1);
+  return __uint_as_float(static_cast<uint32_t>(w));
+}
+
+// Joining affine maps of a carry: after `h + p * c`.  In packed calls a row
+// that starts (ends) a sequence cuts the carry off: its p is kReset, and what
+// was carried up to there is dropped by a select, so that a NaN or an
+// infinity of one sequence, or of rows that belong to none, stays there.  A
+// decay is never negative, so -0 marks nothing else.
+constexpr float kReset = -0.0f;
+template <bool PACKED>
+__device__ __forceinline__ bool is_reset(float p) {
+  return PACKED && __float_as_uint(p) == 0x80000000u;
+}
+template <bool PACKED>
+__device__ __forceinline__ float join(float p, float c, float h) {
+  return is_reset<PACKED>(p) ? h : fmaf(p, c, h);
+}
+template <bool PACKED>
+__device__ __forceinline__ float join_p(float p, float cp) {
+  return is_reset<PACKED>(p) ? p : cp * p;
+}
+
+// Clears the ticket counter and the carry slots; for packed calls also writes
+// the clean offsets (clamped into [0, T] and raised to the largest one before)
+// and gives the state rows of empty sequences their value (src row or 0).
+__global__ void k_gated_init(GatedArgs a, const float* src, float* dst, int64_t nslot) {
+  const int tid = threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + tid; i < nslot; i += step)
+    a.slots[i] = 0;
+  if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;
+  if (!a.cu) return;
+  __shared__ int part[256];
+  for (int k = blockIdx.x; k <= a.S; k += gridDim.x) {
+    int v = 0;
+    for (int j = tid; j <= k; j += blockDim.x) v = max(v, min(a.cu[j], a.T));
+    part[tid] = v;
+    __syncthreads();
+    for (int o = blockDim.x / 2; o > 0; o >>= 1) {
+      if (tid < o) part[tid] = max(part[tid], part[tid + o]);
+      __syncthreads();
+    }
+    const int start = part[0];
+    __syncthreads();
+    if (tid == 0) a.cuc[k] = start;
+    if (k < a.S && dst && min(a.cu[k + 1], a.T) <= start)
+      for (int j = tid; j < a.D; j += blockDim.x)
+        dst[static_cast<int64_t>(k) * a.D + j] = src ? src[static_cast<int64_t>(k) * a.D + j] : 0.0f;
+  }
+}
+
+// The last sequence that starts at or before row t (-1: none), by a search
+// over the clean offsets that every lane of the wave does alike.
+__device__ __forceinline__ int seq_of(const int32_t* cu, int S, int t) {
+  int lo = 0, hi = S + 1;   // first index with cu > t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t) lo = mid + 1; else hi = mid;
+  }
+  return lo - 1;
+}
+
+// The rows t0 .. t0 + n of a packed batch as bit masks, with the sequences of
+// the window in order: bit j of `start` / `end`: row t0 + j is the first /
+// last of its sequence; `live`: it belongs to one.
+struct Window {
+  uint32_t start, end, live;
+  int s0;   // the sequence of the first live row (or the first that starts)
+};
+__device__ __forceinline__ Window window_of(const int32_t* cu, int S, int t0, int n) {
+  Window w{0u, 0u, 0u, 0};
+  int s = seq_of(cu, S, t0);
+  if (s < 0) s = 0;
+  w.s0 = s;
+  while (s < S) {
+    const int b = cu[s] - t0, e = cu[s + 1] - t0;
+    if (b >= n) break;
+    if (e > b && e > 0) {
+      if (b >= 0) w.start |= 1u << b;
+      if (e <= n) w.end |= 1u << (e - 1);
+      const uint32_t upto = e >= 32 ? 0xffffffffu : (1u << e) - 1u;
+      w.live |= upto & ~(b > 0 ? (1u << b) - 1u : 0u);
+    }
+    ++s;
+  }
+  const uint32_t all = n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+  w.live &= all;
+  return w;
+}
+// the next sequence after s that has rows
+__device__ __forceinline__ int next_seq(const int32_t* cu, int S, int s) {
+  do ++s; while (s < S && cu[s + 1] <= cu[s]);
+  return s;
+}
+__device__ __forceinline__ int prev_seq(const int32_t* cu, int s) {
+  do --s; while (s > 0 && cu[s + 1] <= cu[s]);
+  return s;
+}
+
+__device__ __forceinline__ unsigned take_ticket(const GatedArgs& a) {
+  if (a.ntile == 1) return blockIdx.x;
+  __shared__ unsigned n;
+  if (threadIdx.x == 0)
+    n = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return n;
+}
+
+// ---------------------------------------------------------------------------
+// One workgroup: TOK * WAVES rows of 64 V channels.  A wave scans its TOK
+// rows from a zero state, keeping h and the running product of a; the waves'
+// ends are joined through LDS, the tiles' through the carry slots, and
+// y = h_local + product * carry.
+template <typename T, int V, int TOK, int WAVES, bool PACKED>
+__global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_scan(GatedArgs g) {
+  constexpr int TILE = TOK * WAVES;
+  __shared__ float sH[WAVES][64 * V], sP[WAVES][64 * V], sC[64 * V];
+  const unsigned n = take_ticket(g);
+  const int tile = static_cast<int>(n / g.nchain), chain = static_cast<int>(n % g.nchain);
+  const int b = chain / g.ncb, cb = chain % g.ncb;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ch = (cb * 64 + lane) * V;
+  const bool on = ch < g.D;
+  const int chc = on ? ch : g.D - V;   // lanes past the end read the last channels
+  const int t0 = tile * TILE + wave * TOK;
+  const int64_t row0 = static_cast<int64_t>(b) * g.T;
+  const T* x = static_cast<const T*>(g.x) + row0 * g.ldx + chc;
+  const T* r = static_cast<const T*>(g.r) + row0 * g.ldr + chc;
+  const T* gi = static_cast<const T*>(g.i) + row0 * g.ldi + chc;
+  T* y = static_cast<T*>(g.y) + row0 * g.D + chc;
+
+  Raw<T, V> rx[TOK], rr[TOK], ri[TOK];
+#pragma unroll
+  for (int j = 0; j < TOK; ++j) {
+    const int64_t t = min(t0 + j, g.T - 1);
+    rr[j].load(r + t * g.ldr);
+    rx[j].load(x + t * g.ldx);
+    ri[j].load(gi + t * g.ldi);
+  }
+  Window w{};
+  if constexpr (PACKED) w = window_of(g.cuc, g.S, t0, TOK);
+  float k[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) k[v] = decay_factor(g.decay[chc + v], g.c);
+
+  float h[V], P[V], hl[TOK][V], pl[TOK][V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) { h[v] = 0.0f; P[v] = 1.0f; }
+  int s = w.s0;
+#pragma unroll
+  for (int j = 0; j < TOK; ++j) {
+    float vx[V], vr[V], vi[V];
+    rr[j].get(vr);
+    rx[j].get(vx);
+    ri[j].get(vi);
+    if constexpr (PACKED) {
+      if (w.start >> j & 1) {
+        while (g.cuc[s] < t0 + j || g.cuc[s + 1] <= t0 + j) ++s;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          h[v] = g.h0 ? g.h0[static_cast<int64_t>(s) * g.D + chc + v] : 0.0f;
+          P[v] = kReset;
+        }
+      }
+    }
+    const bool in = t0 + j < g.T;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float a, m2;
+      decay_of(k[v] * sigmoid(vr[v]), a, m2);
+      float bt = __builtin_amdgcn_sqrtf(m2) * (sigmoid(vi[v]) * vx[v]);
+      if (!in) { a = 1.0f; bt = 0.0f; }
+      h[v] = fmaf(a, h[v], bt);
+      P[v] *= a;
+      hl[j][v] = h[v];
+      pl[j][v] = P[v];
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    sH[wave][lane * V + v] = h[v];
+    sP[wave][lane * V + v] = P[v];
+  }
+  __syncthreads();
+  // the wave's entry state from the tile's: cH + cP * carry
+  float cH[V], cP[V], carry[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) { cH[v] = 0.0f; cP[v] = 1.0f; }
+  for (int u = 0; u < wave; ++u)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float p = sP[u][lane * V + v];
+      cH[v] = join<PACKED>(p, cH[v], sH[u][lane * V + v]);
+      cP[v] = join_p<PACKED>(p, cP[v]);
+    }
+  if (wave == WAVES - 1) {
+    u64* slot = g.slots + (static_cast<int64_t>(tile) * g.nchain + chain) * (64 * V) + lane * V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (tile == 0)
+        carry[v] = !PACKED && g.h0 ? g.h0[static_cast<int64_t>(b) * g.D + chc + v] : 0.0f;
+      else
+        carry[v] = await_carry(slot - static_cast<int64_t>(g.nchain) * (64 * V) + v);
+      if (tile + 1 < g.ntile) publish(slot + v, join<PACKED>(P[v], join<PACKED>(cP[v], carry[v], cH[v]), h[v]));
+      sC[lane * V + v] = carry[v];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) carry[v] = join<PACKED>(cP[v], sC[lane * V + v], cH[v]);
+  if (!on) return;
+  if (g.states && t0 % kGatedChunk == 0 && t0 < g.T) {
+    const int64_t nst = (g.T + kGatedChunk - 1) / kGatedChunk;
+    float* st = g.states + (b * nst + t0 / kGatedChunk) * g.D + ch;
+#pragma unroll
+    for (int v = 0; v < V; ++v) st[v] = carry[v];
+  }
+  s = w.s0;
+#pragma unroll
+  for (int j = 0; j < TOK; ++j) {
+    const int t = t0 + j;
+    if (t >= g.T) break;
+    if (PACKED && !(w.live >> j & 1)) continue;
+    float o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = join<PACKED>(pl[j][v], carry[v], hl[j][v]);
+    store_v<T, V>(y + static_cast<int64_t>(t) * g.D, o);
+    if (PACKED) {
+      if (w.end >> j & 1) {
+        while (g.cuc[s + 1] <= t) ++s;   // the sequence whose last row this is
+        if (g.hT)
+#pragma unroll
+          for (int v = 0; v < V; ++v) g.hT[static_cast<int64_t>(s) * g.D + ch + v] = o[v];
+      }
+    } else if (t == g.T - 1 && g.hT) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) g.hT[static_cast<int64_t>(b) * g.D + ch + v] = o[v];
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradients.  Tiles run from the last to the first.  Each recomputes its h
+// from the chunk state that the scan saved, scans q_t = a_t (dy_t + q_{t+1})
+// backwards from zero with the running product of a, takes q of the next
+// tile as its carry, and writes dx, dr, di and a partial sum of ddecay.
+template <typename T, int V, int TOK, int WAVES, bool PACKED>
+__global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_backward(GatedArgs g) {
+  constexpr int TILE = TOK * WAVES;
+  static_assert(TILE == kGatedChunk, "one saved state per tile");
+  __shared__ float sH[WAVES][64 * V], sP[WAVES][64 * V], sC[64 * V];
+  const unsigned n = take_ticket(g);
+  const int tile = g.ntile - 1 - static_cast<int>(n / g.nchain);
+  const int chain = static_cast<int>(n % g.nchain);
+  const int b = chain / g.ncb, cb = chain % g.ncb;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ch = (cb * 64 + lane) * V;
+  const bool on = ch < g.D;
+  const int chc = on ? ch : g.D - V;
+  const int t0 = tile * TILE + wave * TOK;
+  const int64_t row0 = static_cast<int64_t>(b) * g.T;
+  const T* x = static_cast<const T*>(g.x) + row0 * g.ldx + chc;
+  const T* r = static_cast<const T*>(g.r) + row0 * g.ldr + chc;
+  const T* gi = static_cast<const T*>(g.i) + row0 * g.ldi + chc;
+  const T* dy = static_cast<const T*>(g.dy) + row0 * g.D + chc;
+
+  Raw<T, V> rx[TOK], rr[TOK], ri[TOK], rd[TOK];
+#pragma unroll
+  for (int j = 0; j < TOK; ++j) {
+    const int64_t t = min(t0 + j, g.T - 1);
+    rr[j].load(r + t * g.ldr);
+    rx[j].load(x + t * g.ldx);
+    ri[j].load(gi + t * g.ldi);
+    rd[j].load(dy + t * g.D);
+  }
+  float entry[V], k[V];
+  {
+    const float* st = g.cstates + (b * static_cast<int64_t>(g.ntile) + tile) * g.D + chc;
+#pragma unroll
+    for (int v = 0; v < V; ++v) entry[v] = st[v];
+  }
+  Window w{};
+  if constexpr (PACKED) w = window_of(g.cuc, g.S, t0, TOK);
+#pragma unroll
+  for (int v = 0; v < V; ++v) k[v] = decay_factor(g.decay[chc + v], g.c);
+
+  // forward: a, the gates and the wave's local scan
+  float h[V], P[V], av[TOK][V], m2v[TOK][V], srv[TOK][V], siv[TOK][V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) { h[v] = 0.0f; P[v] = 1.0f; }
+  int s = w.s0;
+#pragma unroll
+  for (int j = 0; j < TOK; ++j) {
+    float vx[V], vr[V], vi[V];
+    rr[j].get(vr);
+    rx[j].get(vx);
+    ri[j].get(vi);
+    if constexpr (PACKED) {
+      if (w.start >> j & 1) {
+        while (g.cuc[s] < t0 + j || g.cuc[s + 1] <= t0 + j) ++s;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          h[v] = g.h0 ? g.h0[static_cast<int64_t>(s) * g.D + chc + v] : 0.0f;
+          P[v] = kReset;
+        }
+      }
+    }
+    const bool in = t0 + j < g.T;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float a, m2;
+      const float sr = sigmoid(vr[v]), si = sigmoid(vi[v]);
+      decay_of(k[v] * sr, a, m2);
+      float bt = __builtin_amdgcn_sqrtf(m2) * (si * vx[v]);
+      if (!in) { a = 1.0f; bt = 0.0f; }
+      av[j][v] = a;
+      m2v[j][v] = m2;
+      srv[j][v] = sr;
+      siv[j][v] = si;
+      h[v] = fmaf(a, h[v], bt);
+      P[v] *= a;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    sH[wave][lane * V + v] = h[v];
+    sP[wave][lane * V + v] = P[v];
+  }
+  __syncthreads();
+  for (int u = 0; u < wave; ++u)
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      entry[v] = join<PACKED>(sP[u][lane * V + v], entry[v], sH[u][lane * V + v]);
+  __syncthreads();   // sH and sP are written again below
+
+  // backward: q from zero and the product of a, from the last row on
+  float q[V], ql[TOK][V], pl[TOK][V];   // what follows a row: q_{t+1} = ql + pl * carry
+#pragma unroll
+  for (int v = 0; v < V; ++v) { q[v] = 0.0f; P[v] = 1.0f; }
+  int se = s;   // the sequence of the window's last row that starts or goes on here
+  if constexpr (PACKED) {
+    se = seq_of(g.cuc, g.S, min(t0 + TOK, g.T) - 1);
+    if (se < 0) se = 0;
+    if (se >= g.S) se = prev_seq(g.cuc, g.S);
+  }
+  int sb = se;
+#pragma unroll
+  for (int j = TOK - 1; j >= 0; --j) {
+    if constexpr (PACKED) {
+      if (w.end >> j & 1) {
+        while (g.cuc[sb] > t0 + j || g.cuc[sb + 1] <= g.cuc[sb]) --sb;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          q[v] = g.dhT ? g.dhT[static_cast<int64_t>(sb) * g.D + chc + v] : 0.0f;
+          P[v] = kReset;
+        }
+      }
+    }
+    float vd[V];
+    rd[j].get(vd);
+    const bool in = t0 + j < g.T;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      ql[j][v] = q[v];
+      pl[j][v] = P[v];
+      q[v] = av[j][v] * (in ? q[v] + vd[v] : q[v]);
+      P[v] *= av[j][v];
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    sH[wave][lane * V + v] = q[v];
+    sP[wave][lane * V + v] = P[v];
+  }
+  __syncthreads();
+  float cH[V], cP[V], carry[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) { cH[v] = 0.0f; cP[v] = 1.0f; }
+  for (int u = WAVES - 1; u > wave; --u)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float p = sP[u][lane * V + v];
+      cH[v] = join<PACKED>(p, cH[v], sH[u][lane * V + v]);
+      cP[v] = join_p<PACKED>(p, cP[v]);
+    }
+  if (wave == 0) {
+    u64* slot = g.slots + (static_cast<int64_t>(tile) * g.nchain + chain) * (64 * V) + lane * V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if (tile == g.ntile - 1)
+        carry[v] = !PACKED && g.dhT ? g.dhT[static_cast<int64_t>(b) * g.D + chc + v] : 0.0f;
+      else
+        carry[v] = await_carry(slot + static_cast<int64_t>(g.nchain) * (64 * V) + v);
+      const float q0 = join<PACKED>(P[v], join<PACKED>(cP[v], carry[v], cH[v]), q[v]);
+      if (tile > 0) publish(slot + v, q0);
+      else if (!PACKED && on && g.dh0) g.dh0[static_cast<int64_t>(b) * g.D + ch + v] = q0;
+      sC[lane * V + v] = carry[v];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < V; ++v) carry[v] = join<PACKED>(cP[v], sC[lane * V + v], cH[v]);
+
+  // the gradients, in order of time (h runs along)
+  float dk[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) dk[v] = 0.0f;
+  T* dx = static_cast<T*>(g.dx) + row0 * g.ldg + chc;
+  T* dr = static_cast<T*>(g.dr) + row0 * g.ldg + chc;
+  T* di = static_cast<T*>(g.di) + row0 * g.ldg + chc;
+  s = w.s0;
+#pragma unroll
+  for (int j = 0; j < TOK; ++j) {
+    const int t = t0 + j;
+    const bool live = t < g.T && (!PACKED || (w.live >> j & 1));
+    bool first = false;
+    if constexpr (PACKED) {
+      if (w.start >> j & 1) {
+        first = true;
+        while (g.cuc[s] < t || g.cuc[s + 1] <= t) ++s;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          entry[v] = g.h0 ? g.h0[static_cast<int64_t>(s) * g.D + chc + v] : 0.0f;
+      }
+    }
+    float vx[V], vd[V], ox[V], orr[V], oi[V];
+    rx[j].get(vx);
+    rd[j].get(vd);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float a = av[j][v], sr = srv[j][v], si = siv[j][v];
+      const float gt = vd[v] + join<PACKED>(pl[j][v], carry[v], ql[j][v]);
+      const float m2 = m2v[j][v];
+      // the hardware root takes a denormal 1 - a^2 for 0
+      const float im = m2 >= 1.17549435e-38f ? __builtin_amdgcn_rsqf(m2) : 0.0f;
+      const float m = m2 * im, L = kLn2 * (k[v] * sr), u = si * vx[v];
+      const float ah = a * entry[v];
+      const float gl = gt * (ah * L - (a * a) * (L * im) * u);
+      ox[v] = gt * m * si;
+      oi[v] = gt * m * u * (1.0f - si);
+      orr[v] = gl * (1.0f - sr);
+      if (live) dk[v] += gl;
+      if (PACKED && first && on && g.dh0)
+        g.dh0[static_cast<int64_t>(s) * g.D + ch + v] = a * gt;
+      entry[v] = fmaf(m, u, ah);
+    }
+    if (live && on) {
+      store_v<T, V>(dx + static_cast<int64_t>(t) * g.ldg, ox);
+      store_v<T, V>(dr + static_cast<int64_t>(t) * g.ldg, orr);
+      store_v<T, V>(di + static_cast<int64_t>(t) * g.ldg, oi);
+    }
+  }
+  // the tile's part of the sum for ddecay, over its waves in order
+#pragma unroll
+  for (int v = 0; v < V; ++v) sH[wave][lane * V + v] = dk[v];
+  __syncthreads();
+  if (wave == 0 && on) {
+    float* part = g.part + (b * static_cast<int64_t>(g.ntile) + tile) * g.D + ch;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float acc = 0.0f;
+#pragma unroll
+      for (int u = 0; u < WAVES; ++u) acc += sH[u][lane * V + v];
+      part[v] = acc;
+    }
+  }
+}
+
+// ddecay = (sum of the tiles' parts) * sigmoid(decay) / softplus(decay), in a
+// fixed order: 16 threads of a channel take every 16th part each.
+__global__ __launch_bounds__(256) void k_gated_ddecay(GatedArgs g, int64_t nparts) {
+  __shared__ float sum[16][17];
+  const int cl = threadIdx.x & 15, k = threadIdx.x >> 4;
+  const int ch = blockIdx.x * 16 + cl;
+  float acc = 0.0f;
+  if (ch < g.D)
+    for (int64_t p = k; p < nparts; p += 16) acc += g.part[p * g.D + ch];
+  sum[k][cl] = acc;
+  __syncthreads();
+  if (k == 0 && ch < g.D) {
+    float v = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v += sum[j][cl];
+    const float d = g.decay[ch];
+    float ratio;
+    if (d < -15.0f) {   // softplus(d) -> e^d: the ratio tends to 1
+      ratio = 1.0f - 0.5f * expf(d);
+    } else {
+      const float e = expf(-fabsf(d));
+      ratio = (d >= 0.0f ? 1.0f : e) / (1.0f + e) / (fmaxf(d, 0.0f) + log1pf(e));
+    }
+    g.ddecay[ch] = v * ratio;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One decode step: h is read and written once.
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_gated_step(GatedArgs g, float* hs) {
+  const int ncb = (g.D + V - 1) / V;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int b = static_cast<int>(n / ncb), ch = static_cast<int>(n % ncb) * V;
+  if (b >= g.B) return;
+  Raw<T, V> rx, rr, ri;
+  rr.load(static_cast<const T*>(g.r) + b * g.ldr + ch);
+  rx.load(static_cast<const T*>(g.x) + b * g.ldx + ch);
+  ri.load(static_cast<const T*>(g.i) + b * g.ldi + ch);
+  RawVec<float, V> rh, rk;
+  float* hp = hs + static_cast<int64_t>(b) * g.D + ch;
+  rh.load(hp);
+  rk.load(g.decay + ch);
+  float x[V], r[V], i[V], h[V], d[V];
+  rr.get(r);
+  rx.get(x);
+  ri.get(i);
+  rh.get(h);
+  rk.get(d);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float a, m2;
+    decay_of(decay_factor(d[v], g.c) * sigmoid(r[v]), a, m2);
+    h[v] = fmaf(a, h[v], __builtin_amdgcn_sqrtf(m2) * (sigmoid(i[v]) * x[v]));
+  }
+  store_v<float, V>(hp, h);
+  store_v<T, V>(static_cast<T*>(g.y) + static_cast<int64_t>(b) * g.D + ch, h);
+}
+
+template <typename T, int V, int TOK, int WAVES>
+hipError_t run_scan(GatedArgs& g, hipStream_t s) {
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(g.ntile) * g.nchain);
+  if (g.cu)
+    k_gated_scan<T, V, TOK, WAVES, true><<<grid, 64 * WAVES, 0, s>>>(g);
+  else
+    k_gated_scan<T, V, TOK, WAVES, false><<<grid, 64 * WAVES, 0, s>>>(g);
+  return hipGetLastError();
+}
+template <typename T, int V>
+hipError_t run_backward(GatedArgs& g, hipStream_t s) {
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(g.ntile) * g.nchain);
+  if (g.cu)
+    k_gated_backward<T, V, kGatedChunk / 16, 16, true><<<grid, 1024, 0, s>>>(g);
+  else
+    k_gated_backward<T, V, kGatedChunk / 16, 16, false><<<grid, 1024, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+hipError_t run_init(const GatedArgs& g, const float* src, float* dst, int64_t nslot, hipStream_t s) {
+  if (g.ntile == 1 && !g.cu) return hipSuccess;
+  int64_t blocks = (nslot + 2047) / 2048;
+  if (g.cu && blocks < g.S + 1) blocks = g.S + 1;
+  if (blocks > 4096) blocks = 4096;
+  if (blocks < 1) blocks = 1;
+  k_gated_init<<<static_cast<unsigned>(blocks), 256, 0, s>>>(g, src, dst, nslot);
+  return hipGetLastError();
+}
+
+constexpr size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+GatedPlan gated_plan(int B, int T, int D, bool packed) {
+  GatedPlan p;
+  p.V = 1;
+  p.tile = kGatedChunk;
+  p.ncb = (D + 64 * p.V - 1) / (64 * p.V);
+  p.nchain = static_cast<int64_t>(p.ncb) * (packed ? 1 : B);
+  p.ntile = (T + p.tile - 1) / p.tile;
+  return p;
+}
+
+size_t gated_workspace_bytes(int B, int T, int D, bool packed, bool backward) {
+  const GatedPlan p = gated_plan(B, T, D, packed);
+  size_t n = 256 + up256(sizeof(int32_t) * (static_cast<size_t>(B) + 1));
+  n += up256(sizeof(u64) * 64 * p.V * p.nchain * p.ntile);
+  if (backward) n += up256(sizeof(float) * D * (packed ? 1 : B) * p.ntile);
+  return n;
+}
+
+void gated_carve(GatedArgs& g, void* ws) {
+  const GatedPlan p = gated_plan(g.B, g.T, g.D, g.cu != nullptr);
+  g.ncb = p.ncb;
+  g.nchain = static_cast<int>(p.nchain);
+  g.ntile = p.ntile;
+  char* c = static_cast<char*>(ws);
+  g.ticket = reinterpret_cast<unsigned*>(c);
+  c += 256;
+  g.cuc = reinterpret_cast<int32_t*>(c);
+  c += up256(sizeof(int32_t) * (static_cast<size_t>(g.B) + 1));
+  g.slots = reinterpret_cast<u64*>(c);
+  c += up256(sizeof(u64) * 64 * p.V * p.nchain * p.ntile);
+  g.part = reinterpret_cast<float*>(c);
+  g.S = g.B;
+}
+
+hipError_t launch_gated_scan(GatedArgs& g, int bf16, hipStream_t s) {
+  const GatedPlan p = gated_plan(g.B, g.T, g.D, g.cu != nullptr);
+  hipError_t e = run_init(g, g.h0, g.hT, p.nchain * p.ntile * 64 * p.V, s);
+  if (e != hipSuccess) return e;
+  return bf16 ? run_scan<bf16_t, 1, 8, 16>(g, s) : run_scan<float, 1, 8, 16>(g, s);
+}
+
+hipError_t launch_gated_backward(GatedArgs& g, int bf16, hipStream_t s) {
+  const GatedPlan p = gated_plan(g.B, g.T, g.D, g.cu != nullptr);
+  hipError_t e = run_init(g, g.dhT, g.dh0, p.nchain * p.ntile * 64 * p.V, s);
+  if (e != hipSuccess) return e;
+  e = bf16 ? run_backward<bf16_t, 1>(g, s) : run_backward<float, 1>(g, s);
+  if (e != hipSuccess) return e;
+  const int64_t nparts = static_cast<int64_t>(g.cu ? 1 : g.B) * g.ntile;
+  k_gated_ddecay<<<(g.D + 15) / 16, 256, 0, s>>>(g, nparts);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_step(const GatedArgs& g, float* h, int bf16, hipStream_t s) {
+  const bool wide = g.D % 8 == 0 && g.ldx % 8 == 0 && g.ldr % 8 == 0 && g.ldi % 8 == 0;
+  const int64_t n = static_cast<int64_t>(g.B) * (wide ? g.D / 8 : g.D);
+  const unsigned grid = static_cast<unsigned>((n + 255) / 256);
+  if (bf16) {
+    if (wide) k_gated_step<bf16_t, 8><<<grid, 256, 0, s>>>(g, h);
+    else k_gated_step<bf16_t, 1><<<grid, 256, 0, s>>>(g, h);
+  } else {
+    if (wide) k_gated_step<float, 8><<<grid, 256, 0, s>>>(g, h);
+    else k_gated_step<float, 1><<<grid, 256, 0, s>>>(g, h);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace m3

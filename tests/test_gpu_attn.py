@@ -1,0 +1,291 @@
+"""Causal attention over packed sequences, its gradients and the one-token
+form over a cache, against the definition in 64 bits."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from linear_recurrent_sequence_mamba_amd import binding as m3
+from tests import layers_ref as ref
+from tests.util import say
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def _check(name, got, want, bound):
+    w = ref.worst(got, want, bound)
+    say(f"  {name}: {w:.3f} of its bound")
+    assert w <= 1.0, (name, w)
+
+
+def _offsets(n):
+    cu = [0]
+    for v in n:
+        cu.append(cu[-1] + v)
+    return cu
+
+
+def _dev(cu):
+    return torch.tensor(cu, dtype=torch.int32).cuda()
+
+
+def _inputs(Tq, Tk, Hq, Hk, D, dtype, seed, strided=False):
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g)
+    if strided:
+        pq = n(Tq, (Hq + 1) * D).to(dtype).cuda()
+        pk = n(Tk, 2 * Hk * D + 8).to(dtype).cuda()
+        return (pq[:, D:].view(Tq, Hq, D), pk[:, :Hk * D].view(Tk, Hk, D),
+                pk[:, Hk * D + 8:].view(Tk, Hk, D), n(Tq, Hq, D).to(dtype).cuda())
+    return (n(Tq, Hq, D).to(dtype).cuda(), n(Tk, Hk, D).to(dtype).cuda(),
+            n(Tk, Hk, D).to(dtype).cuda(), n(Tq, Hq, D).to(dtype).cuda())
+
+
+def _all(q, k, v, do, nq, nk, scale, dtype):
+    """Outputs, gradients and bounds over all sequences, in 64 bits."""
+    cq, ck = _offsets(nq), _offsets(nk)
+    parts = []
+    for s in range(len(nq)):
+        a, b = (ref.f64(t[cq[s]:cq[s + 1]]) for t in (q, do))
+        c, d = (ref.f64(t[ck[s]:ck[s + 1]]) for t in (k, v))
+        o, lse, p = ref.attn(a, c, d, scale)
+        g, gb = ref.attn_grads(a, c, d, b, scale, dtype)
+        parts.append((o, ref.attn_bound(a, c, d, o, p, scale, dtype), lse, *g, *gb))
+    return [torch.cat(t) for t in zip(*parts)]
+
+
+CASES = [  # queries and keys of each sequence, Hq, Hk, D
+    ([1], [1], 1, 1, 64), ([5, 0, 1, 70], [5, 3, 1, 70], 4, 2, 64),
+    ([128, 129], [128, 129], 2, 1, 128), ([63, 200], [300, 200], 8, 1, 128),
+    ([40, 33], [10, 0], 3, 3, 64), ([1, 1, 1], [33, 64, 65], 10, 2, 128),
+    ([257], [321], 5, 1, 64), ([0, 0, 2], [0, 4, 2], 2, 2, 128)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("case", CASES)
+def test_prompt_and_gradients(case, dtype):
+    nq, nk, Hq, Hk, D = case
+    for strided in (False, True):
+        say(f"attn {case} {dtype} strided={strided}")
+        tail = 3   # rows behind the last sequence
+        Tq, Tk = sum(nq) + tail, sum(nk) + tail
+        q, k, v, do = _inputs(Tq, Tk, Hq, Hk, D, dtype, Tq, strided)
+        for t in (q, k, v, do):
+            t[t.shape[0] - tail:] = float("nan")
+        scale = D ** -0.5
+        cq, ck = _dev(_offsets(nq)), _dev(_offsets(nk))
+        o, lse = m3.attn_prefill_varlen(q, k, v, cq, ck)
+        dq, dk, dv = m3.attn_prefill_varlen_backward(q, k, v, o, lse, do, cq, ck)
+        torch.cuda.synchronize()
+        wo, bo, wl, wq, wk, wv, bq, bk, bv = _all(q, k, v, do, nq, nk, scale, dtype)
+        n, m = Tq - tail, Tk - tail
+        _check("o", o[:n], wo, bo)
+        # a score: D fp32 sums of products; the logarithm of their sum 2^-20
+        amax = float(scale * D * 16)
+        _check("lse", lse[:n], wl, torch.tensor(2.0 ** -24 * (D + 8) * amax + 2.0 ** -19 * 8))
+        _check("dq", dq[:n], wq, bq)
+        _check("dk", dk[:m], wk, bk)
+        _check("dv", dv[:m], wv, bv)
+
+
+def test_rows_behind_the_last_sequence_stay():
+    q, k, v, do = _inputs(200, 200, 2, 1, 64, BF16, 3)
+    cu = _dev([0, 100, 150])
+    o = torch.full_like(q, 7.0)
+    lse = torch.full((200, 2), 7.0, device="cuda")
+    d = m3.m3_attn_dims(2, 200, 200, 2, 1, 64, m3.M3_BF16, 0.125, 0, 0, 0, 0, 0, 0, 0)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    lib = m3.library()
+    assert lib.m3_attn_prefill_varlen(ctypes.byref(d), p(cu), p(cu), p(q), p(k), p(v), p(o), p(lse), s) == 0
+    g = [torch.full_like(t, 7.0) for t in (q, k, v)]
+    ws = torch.empty(lib.m3_attn_prefill_varlen_backward_workspace_size(ctypes.byref(d)), dtype=torch.uint8,
+                     device="cuda")
+    assert lib.m3_attn_prefill_varlen_backward(
+        ctypes.byref(d), p(cu), p(cu), p(q), p(k), p(v), p(o), p(lse), p(do), *(p(t) for t in g), p(ws),
+        ws.numel(), s) == 0
+    torch.cuda.synchronize()
+    for t in (o, lse, *g):
+        assert (t[150:] == 7).all() and not (t[:150] == 7).all(-1).any()
+
+
+def test_offsets_outside_the_rows_touch_nothing_else():
+    """Offsets that do not rise or leave the rows: no row outside the buffers
+    is touched (guard rows around them stay), and the call returns."""
+    T, H, D = 100, 2, 64
+    guard = lambda: torch.full((T + 20, H, D), 5.0, dtype=BF16, device="cuda")
+    q, k, v, do = _inputs(T, T, H, H, D, BF16, 4)
+    bufs = [guard() for _ in range(4)]
+    o, dq, dk, dv = (b[10:10 + T] for b in bufs)
+    lse = torch.zeros(T, H, device="cuda")
+    lib = m3.library()
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    for cu in ([-7, 50, 400], [90, 10, 100], [100, 100, 0], [0, 500, 20]):
+        c = _dev(cu)
+        d = m3.m3_attn_dims(2, T, T, H, H, D, m3.M3_BF16, 0.125, 0, 0, 0, 0, 0, 0, 0)
+        ws = torch.empty(lib.m3_attn_prefill_varlen_backward_workspace_size(ctypes.byref(d)),
+                         dtype=torch.uint8, device="cuda")
+        assert lib.m3_attn_prefill_varlen(ctypes.byref(d), p(c), p(c), p(q), p(k), p(v), p(o), p(lse), s) == 0
+        assert lib.m3_attn_prefill_varlen_backward(
+            ctypes.byref(d), p(c), p(c), p(q), p(k), p(v), p(o), p(lse), p(do), p(dq), p(dk), p(dv), p(ws),
+            ws.numel(), s) == 0
+        torch.cuda.synchronize()
+    for b in bufs:
+        assert (b[:10] == 5).all() and (b[10 + T:] == 5).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_infinities_and_nan_reach_only_who_sees_them(D, dtype):
+    n, Hq, Hk = [150, 90], 2, 1
+    q, k, v, _ = _inputs(240, 240, Hq, Hk, D, dtype, 6)
+    v[70, 0, 3] = float("nan")
+    v[100, 0, 9] = float("inf")
+    v[149, 0, D - 1] = -float("inf")
+    k[120, 0, 1] = float("nan")
+    k[239] = float("inf")
+    cu = _dev(_offsets(n))
+    o, lse = m3.attn_prefill_varlen(q, k, v, cu, cu)
+    k2, v2 = k.clone(), v.clone()
+    for t in (k2, v2):
+        t[~torch.isfinite(t)] = 0.5
+    o2, lse2 = m3.attn_prefill_varlen(q, k2, v2, cu, cu)
+    torch.cuda.synchronize()
+    # before a special value nothing changes; the second sequence has only
+    # its last query's own key
+    assert torch.equal(o[:70], o2[:70]) and torch.equal(lse[:120], lse2[:120])
+    assert torch.equal(o[150:239], o2[150:239]) and torch.equal(lse[150:239], lse2[150:239])
+    keep = [d for d in range(D) if d not in (3, 9)]
+    assert torch.equal(o[70:120][..., keep], o2[70:120][..., keep])
+    assert torch.isnan(o[70:120, :, 3]).all()
+    assert torch.equal(o[70:100, :, 9], o2[70:100, :, 9])
+    assert (o[100:120, :, 9] == float("inf")).all()
+    assert torch.isnan(o[120:150]).all()
+
+
+def test_a_masked_score_of_any_size():
+    """Scores far below and above what fp32's exponential holds."""
+    q, k, v, _ = _inputs(100, 100, 1, 1, 64, F32, 7)
+    k = k * torch.logspace(-3, 3, 100, device="cuda")[:, None, None]
+    cu = _dev([0, 100])
+    o, lse = m3.attn_prefill_varlen(q, k, v, cu, cu)
+    wo, wl, p = ref.attn(ref.f64(q), ref.f64(k), ref.f64(v), 0.125)
+    _check("o", o, wo, ref.attn_bound(ref.f64(q), ref.f64(k), ref.f64(v), wo, p, 0.125, F32))
+    assert torch.isfinite(lse).all()
+
+
+def _decode_ref(q, k, v, lengths, scale, dtype):
+    outs = []
+    for s, n in enumerate(lengths):
+        a, c, d = ref.f64(q[s:s + 1]), ref.f64(k[s, :n]), ref.f64(v[s, :n])
+        o, lse, p = ref.attn(a, c, d, scale)
+        outs.append((o, ref.attn_bound(a, c, d, o, p, scale, dtype), lse))
+    return [torch.cat(t) for t in zip(*outs)]
+
+
+DECODE = [  # lengths, cap, Hq, Hk, D
+    ([0, 1, 31, 32, 33], 40, 4, 2, 64), ([700, 5, 1500], 1500, 8, 1, 128),
+    ([2000], 2100, 3, 3, 64), ([513], 513, 40, 1, 64), ([64, 1000, 0, 3], 1030, 33, 1, 128)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("case", DECODE)
+def test_decode(case, dtype):
+    lengths, cap, Hq, Hk, D = case
+    S = len(lengths)
+    say(f"decode {case} {dtype}")
+    g = torch.Generator().manual_seed(cap)
+    q = torch.randn(S, Hq, D, generator=g).to(dtype).cuda()
+    kv = torch.randn(S, cap + 2, 2, Hk, D, generator=g).to(dtype).cuda()
+    for s, n in enumerate(lengths):   # the rest of a cache is not read
+        kv[s, n:] = float("nan")
+    k, v = kv[:, :cap, 0], kv[:, :cap, 1]
+    o, lse = m3.attn_decode(q, k, v, torch.tensor(lengths, dtype=torch.int32).cuda())
+    o2, lse2 = m3.attn_decode(q, k.contiguous(), v.contiguous(), torch.tensor(lengths, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    scale = D ** -0.5
+    wo, bo, wl = _decode_ref(q, k, v, lengths, scale, dtype)
+    _check("o", o, wo, bo)
+    _check("lse", lse, wl, torch.tensor(2.0 ** -24 * (D + 8) * scale * D * 16 + 2.0 ** -19 * 8))
+
+
+def test_decode_lengths_are_clamped():
+    q = torch.randn(2, 2, 64, device="cuda")
+    k, v = torch.randn(2, 50, 1, 64, device="cuda"), torch.randn(2, 50, 1, 64, device="cuda")
+    t = lambda *n: torch.tensor(n, dtype=torch.int32).cuda()
+    a, b = m3.attn_decode(q, k, v, t(-4, 900)), m3.attn_decode(q, k, v, t(0, 50))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert (a[0][0] == 0).all() and torch.isinf(a[1][0]).all()
+
+
+def test_decode_offsets_beyond_32_bits():
+    """A cache of 2^31 and more elements: nearly all weight on its last row."""
+    Hk, D = 8, 128
+    n = (1 << 21) + 77
+    k = torch.zeros(1, n, Hk, D, dtype=BF16, device="cuda")
+    v = torch.zeros(1, n, Hk, D, dtype=BF16, device="cuda")
+    q = torch.ones(1, Hk, D, dtype=BF16, device="cuda")
+    k[0, -1] = 20.0 / D
+    val = torch.randn(Hk, D, device="cuda").to(BF16)
+    v[0, -1] = val
+    o, lse = m3.attn_decode(q, k, v, torch.tensor([n], dtype=torch.int32).cuda(), scale=1.0)
+    torch.cuda.synchronize()
+    e = math.exp(float(ref.f64(k[0, -1, 0]).sum()))
+    w = e / (e + n - 1)
+    _check("o", o[0], ref.f64(val) * w, 2 * 2.0 ** -8 * ref.f64(val).abs() + 1e-30)
+    assert abs(float(lse[0, 0]) - math.log(e + n - 1)) <= 1e-4
+
+
+def test_one_token_prompt_equals_decode():
+    """A single query at the end of a cache through both calls."""
+    q, k, v, _ = _inputs(1, 900, 4, 2, 128, F32, 12)
+    o, lse = m3.attn_prefill_varlen(q, k, v, _dev([0, 1]), _dev([0, 900]))
+    o2, lse2 = m3.attn_decode(q, k[None], v[None], torch.tensor([900], dtype=torch.int32).cuda())
+    wo, wl, p = ref.attn(ref.f64(q), ref.f64(k), ref.f64(v), 128 ** -0.5)
+    b = ref.attn_bound(ref.f64(q), ref.f64(k), ref.f64(v), wo, p, 128 ** -0.5, F32)
+    _check("prompt", o, wo, b)
+    _check("decode", o2, wo, b)
+
+
+def test_equal_bits_graphs_and_streams():
+    q, k, v, do = _inputs(500, 500, 8, 2, 64, BF16, 8)
+    cu = _dev([0, 300, 301, 500])
+    cache = torch.randn(2, 2000, 2, 64, device="cuda").to(BF16)
+    ln = torch.tensor([1999, 7], dtype=torch.int32).cuda()
+
+    def once():
+        o, lse = m3.attn_prefill_varlen(q, k, v, cu, cu)
+        g = m3.attn_prefill_varlen_backward(q, k, v, o, lse, do, cu, cu)
+        return [o, lse, *g, *m3.attn_decode(q[:2], cache, cache, ln)]
+
+    want = [t.clone() for t in once()]
+    for _ in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(once(), want))
+    graphs = []
+    for _ in range(2):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            once()
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = once()
+        graphs.append((g, out))
+    for _ in range(3):
+        for g, out in graphs:
+            for t in out:
+                t.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+        once()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    o, lse = m3.attn_prefill_varlen(q, k, v, cu, cu, stream=s)
+    s.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])

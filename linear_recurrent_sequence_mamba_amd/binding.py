@@ -584,20 +584,27 @@ def decode_tokens(h, x, B, C, dt, A, lam, theta, x_prev=None, B_prev=None,
 class _on:
     """The device of a call's tensors as the current one and, if given, the
     stream as the current one, so that what a helper allocates belongs to the
-    stream that uses it."""
+    stream that uses it.  Entering gives the raw stream to launch on.  Nothing
+    is switched where nothing has to be: a small call is bound by the host."""
+
+    __slots__ = ("index", "guards")
 
     def __init__(self, device, stream):
-        self.device = torch.cuda.device(device)
-        self.stream = torch.cuda.stream(stream)   # None: no change
+        self.index = device.index
+        self.guards = []
+        if self.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            self.guards.append(torch.cuda.stream(stream))
 
     def __enter__(self):
-        self.device.__enter__()
-        self.stream.__enter__()
-        return self
+        for g in self.guards:
+            g.__enter__()
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *e):
-        self.stream.__exit__(*e)
-        self.device.__exit__(*e)
+        for g in reversed(self.guards):
+            g.__exit__(*e)
 
 
 def _same_device(**tensors):
@@ -615,16 +622,37 @@ def _same_device(**tensors):
     return dev
 
 
-def _rows(name, t, shape, dtype) -> int:
-    """Checks a tensor of token rows that may be cut out of wider rows: the
-    trailing (per-token) axes dense, consecutive tokens one stride apart
-    across all leading axes.  Returns that stride."""
+def _addr(t):
+    """A tensor's address as ctypes takes it for a void pointer."""
+    return None if t is None else t.data_ptr()
+
+
+def _dense(name, t, shape, dtype, optional=False):
+    """_check for a tensor whose device is known."""
     if t is None:
+        if optional:
+            return
         raise ValueError(f"{name} is required")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != expected {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype} != expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(name, t, shape, dtype) -> int:
+    """Checks a tensor of token rows that may be cut out of wider rows: the
+    trailing (per-token) axes dense, consecutive tokens one stride apart
+    across all leading axes.  Returns that stride, 0 for a dense tensor."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype} != expected {dtype}")
+    if t.is_contiguous():
+        return 0
     lead = 2 if len(shape) == 3 and name in _BATCHED else 1
     width = 1
     for n, st in zip(reversed(shape[lead:]), reversed(t.stride()[lead:])):
@@ -655,11 +683,11 @@ def _gated_setup(x, r, i, decay, c, cu_seqlens, extra):
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must hold S + 1 offsets")
         B, T = cu_seqlens.numel() - 1, x.shape[0]
-        _check("cu_seqlens", cu_seqlens, (B + 1,), torch.int32)
+        _dense("cu_seqlens", cu_seqlens, (B + 1,), torch.int32)
     else:
         B, T = x.shape[:2]
     lds = [_rows(n, t, x.shape, dt) for n, t in (("x", x), ("r", r), ("i", i))]
-    _check("decay", decay, (D,), torch.float32)
+    _dense("decay", decay, (D,), torch.float32)
     return dev, m3_gated_dims(B, T, D, code, c, *lds, 0), packed
 
 
@@ -680,9 +708,9 @@ def gated_scan(x, r, i, decay, h0=None, c=8.0, cu_seqlens=None, want_hT=True, wa
     gated_scan_backward."""
     dev, d, packed = _gated_setup(x, r, i, decay, c, cu_seqlens, dict(h0=h0))
     B, T, D = d.batch, d.seqlen, d.width
-    _check("h0", h0, (B, D), torch.float32, optional=True)
+    _dense("h0", h0, (B, D), torch.float32, optional=True)
     lib = _lib()
-    with _on(dev, stream):
+    with _on(dev, stream) as raw:
         y = torch.empty(x.shape, dtype=x.dtype, device=dev)
         hT = torch.empty((B, D), dtype=torch.float32, device=dev) if want_hT else None
         st = None
@@ -690,9 +718,9 @@ def gated_scan(x, r, i, decay, h0=None, c=8.0, cu_seqlens=None, want_hT=True, wa
             st = torch.empty(((_nst(T),) if packed else (B, _nst(T))) + (D,), dtype=torch.float32,
                              device=dev)
         ws = _ws(lib.m3_gated_scan_workspace_size(ctypes.byref(d), packed), "m3_gated_scan", dev)
-        e = lib.m3_gated_scan(ctypes.byref(d), _ptr(cu_seqlens), _ptr(x), _ptr(r), _ptr(i),
-                              _ptr(decay), _ptr(h0), _ptr(y), _ptr(hT), _ptr(st), _ptr(ws),
-                              ws.numel(), _stream(None))
+        e = lib.m3_gated_scan(ctypes.byref(d), _addr(cu_seqlens), _addr(x), _addr(r), _addr(i),
+                              _addr(decay), _addr(h0), _addr(y), _addr(hT), _addr(st), _addr(ws),
+                              ws.numel(), raw)
     if e != 0:
         raise M3Error(e, "m3_gated_scan")
     return y, hT, st
@@ -706,21 +734,21 @@ def gated_scan_backward(x, r, i, decay, dy, states, h0=None, dhT=None, c=8.0, cu
     dev, d, packed = _gated_setup(x, r, i, decay, c, cu_seqlens,
                                   dict(h0=h0, dy=dy, states=states, dhT=dhT))
     B, T, D = d.batch, d.seqlen, d.width
-    _check("h0", h0, (B, D), torch.float32, optional=True)
-    _check("dhT", dhT, (B, D), torch.float32, optional=True)
-    _check("dy", dy, x.shape, x.dtype)
-    _check("states", states, ((_nst(T),) if packed else (B, _nst(T))) + (D,), torch.float32)
+    _dense("h0", h0, (B, D), torch.float32, optional=True)
+    _dense("dhT", dhT, (B, D), torch.float32, optional=True)
+    _dense("dy", dy, x.shape, x.dtype)
+    _dense("states", states, ((_nst(T),) if packed else (B, _nst(T))) + (D,), torch.float32)
     lib = _lib()
-    with _on(dev, stream):
+    with _on(dev, stream) as raw:
         g = {k: torch.empty(x.shape, dtype=x.dtype, device=dev) for k in ("x", "r", "i")}
         g["decay"] = torch.empty(D, dtype=torch.float32, device=dev)
         g["h0"] = torch.empty((B, D), dtype=torch.float32, device=dev) if h0 is not None else None
         ws = _ws(lib.m3_gated_scan_backward_workspace_size(ctypes.byref(d), packed),
                  "m3_gated_scan_backward", dev)
         e = lib.m3_gated_scan_backward(
-            ctypes.byref(d), _ptr(cu_seqlens), _ptr(x), _ptr(r), _ptr(i), _ptr(decay), _ptr(h0),
-            _ptr(states), _ptr(dy), _ptr(dhT), _ptr(g["x"]), _ptr(g["r"]), _ptr(g["i"]),
-            _ptr(g["decay"]), _ptr(g["h0"]), _ptr(ws), ws.numel(), _stream(None))
+            ctypes.byref(d), _addr(cu_seqlens), _addr(x), _addr(r), _addr(i), _addr(decay), _addr(h0),
+            _addr(states), _addr(dy), _addr(dhT), _addr(g["x"]), _addr(g["r"]), _addr(g["i"]),
+            _addr(g["decay"]), _addr(g["h0"]), _addr(ws), ws.numel(), raw)
     if e != 0:
         raise M3Error(e, "m3_gated_scan_backward")
     return g
@@ -733,17 +761,17 @@ def gated_step(h, x, r, i, decay, c=8.0, y=None, stream=None):
     if h.dim() != 2:
         raise ValueError("h must be [Bsz, D]")
     B, D = h.shape
-    _check("h", h, (B, D), torch.float32)
-    _check("decay", decay, (D,), torch.float32)
+    _dense("h", h, (B, D), torch.float32)
+    _dense("decay", decay, (D,), torch.float32)
     code = dtype_code(x.dtype)
     lds = [_rows(n, t, (B, D), x.dtype) for n, t in (("x", x), ("r", r), ("i", i))]
     d = m3_gated_dims(B, 1, D, code, c, *lds, 0)
-    with _on(dev, stream):
+    with _on(dev, stream) as raw:
         if y is None:
             y = torch.empty((B, D), dtype=x.dtype, device=dev)
-        _check("y", y, (B, D), x.dtype)
-        e = _lib().m3_gated_step(ctypes.byref(d), _ptr(h), _ptr(x), _ptr(r), _ptr(i),
-                                 _ptr(decay), _ptr(y), _stream(None))
+        _dense("y", y, (B, D), x.dtype)
+        e = _lib().m3_gated_step(ctypes.byref(d), _addr(h), _addr(x), _addr(r), _addr(i),
+                                 _addr(decay), _addr(y), raw)
     if e != 0:
         raise M3Error(e, "m3_gated_step")
     return y
@@ -758,9 +786,9 @@ def _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags,
     code = dtype_code(q.dtype)
     ldq = _rows("q", q, (T, Hq, D), q.dtype)
     ldk = _rows("k", k, (T, Hk, D), q.dtype)
-    _check("positions", positions, (T,), torch.int32)
-    _check("q_weight", q_weight, (D,), torch.float32, optional=True)
-    _check("k_weight", k_weight, (D,), torch.float32, optional=True)
+    _dense("positions", positions, (T,), torch.int32)
+    _dense("q_weight", q_weight, (D,), torch.float32, optional=True)
+    _dense("k_weight", k_weight, (D,), torch.float32, optional=True)
     return dev, m3_qk_dims(T, Hq, Hk, D, D if rotary_dim is None else rotary_dim, code, flags, eps,
                            base, ldq, ldk, 0, 0)
 
@@ -770,12 +798,12 @@ def qk_norm_rope(q, k, positions, q_weight=None, k_weight=None, eps=1e-6, base=1
     """RMS norms of q [T, Hq, D] and k [T, Hk, D] per head and their rotation
     by position (m3_qk_norm_rope).  Returns (q_out, k_out)."""
     dev, d = _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags, {})
-    with _on(dev, stream):
+    with _on(dev, stream) as raw:
         qo = torch.empty(q.shape, dtype=q.dtype, device=dev)
         ko = torch.empty(k.shape, dtype=q.dtype, device=dev)
-        e = _lib().m3_qk_norm_rope(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(q_weight),
-                                   _ptr(k_weight), _ptr(positions), _ptr(qo), _ptr(ko),
-                                   _stream(None))
+        e = _lib().m3_qk_norm_rope(ctypes.byref(d), _addr(q), _addr(k), _addr(q_weight),
+                                   _addr(k_weight), _addr(positions), _addr(qo), _addr(ko),
+                                   raw)
     if e != 0:
         raise M3Error(e, "m3_qk_norm_rope")
     return qo, ko
@@ -787,10 +815,10 @@ def qk_norm_rope_backward(q, k, positions, dq_out, dk_out, q_weight=None, k_weig
     weights that are given, q_weight, k_weight in fp32."""
     dev, d = _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags,
                        dict(dq_out=dq_out, dk_out=dk_out))
-    _check("dq_out", dq_out, q.shape, q.dtype)
-    _check("dk_out", dk_out, k.shape, q.dtype)
+    _dense("dq_out", dq_out, q.shape, q.dtype)
+    _dense("dk_out", dk_out, k.shape, q.dtype)
     lib, f32 = _lib(), torch.float32
-    with _on(dev, stream):
+    with _on(dev, stream) as raw:
         g = dict(q=torch.empty(q.shape, dtype=q.dtype, device=dev),
                  k=torch.empty(k.shape, dtype=q.dtype, device=dev))
         for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
@@ -798,9 +826,9 @@ def qk_norm_rope_backward(q, k, positions, dq_out, dk_out, q_weight=None, k_weig
         ws = _ws(lib.m3_qk_norm_rope_backward_workspace_size(ctypes.byref(d)),
                  "m3_qk_norm_rope_backward", dev)
         e = lib.m3_qk_norm_rope_backward(
-            ctypes.byref(d), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
-            _ptr(dq_out), _ptr(dk_out), _ptr(g["q"]), _ptr(g["k"]), _ptr(g["q_weight"]),
-            _ptr(g["k_weight"]), _ptr(ws), ws.numel(), _stream(None))
+            ctypes.byref(d), _addr(q), _addr(k), _addr(q_weight), _addr(k_weight), _addr(positions),
+            _addr(dq_out), _addr(dk_out), _addr(g["q"]), _addr(g["k"]), _addr(g["q_weight"]),
+            _addr(g["k_weight"]), _addr(ws), ws.numel(), raw)
     if e != 0:
         raise M3Error(e, "m3_qk_norm_rope_backward")
     return g
@@ -818,8 +846,8 @@ def _attn_setup(q, k, v, cu_q, cu_k, scale, extra):
     if cu_q.dim() != 1 or cu_q.numel() < 2:
         raise ValueError("cu_seqlens_q must hold S + 1 offsets")
     S = cu_q.numel() - 1
-    _check("cu_seqlens_q", cu_q, (S + 1,), torch.int32)
-    _check("cu_seqlens_k", cu_k, (S + 1,), torch.int32)
+    _dense("cu_seqlens_q", cu_q, (S + 1,), torch.int32)
+    _dense("cu_seqlens_k", cu_k, (S + 1,), torch.int32)
     return dev, m3_attn_dims(S, Tq, Tk, Hq, Hk, D, code, D ** -0.5 if scale is None else scale,
                              *ld, 0, 0, 0, 0)
 
@@ -829,12 +857,12 @@ def attn_prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, scale=None, stream=
     [Tk, Hk, D] (m3_attn_prefill_varlen; scale D^-1/2 by default).  Returns
     (o, lse).  Rows behind the last sequence are not written."""
     dev, d = _attn_setup(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, {})
-    with _on(dev, stream):
+    with _on(dev, stream) as raw:
         o = torch.empty(q.shape, dtype=q.dtype, device=dev)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-        e = _lib().m3_attn_prefill_varlen(ctypes.byref(d), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
-                                          _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
-                                          _stream(None))
+        e = _lib().m3_attn_prefill_varlen(ctypes.byref(d), _addr(cu_seqlens_q), _addr(cu_seqlens_k),
+                                          _addr(q), _addr(k), _addr(v), _addr(o), _addr(lse),
+                                          raw)
     if e != 0:
         raise M3Error(e, "m3_attn_prefill_varlen")
     return o, lse
@@ -846,16 +874,16 @@ def attn_prefill_varlen_backward(q, k, v, o, lse, d_o, cu_seqlens_q, cu_seqlens_
     dev, d = _attn_setup(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, dict(o=o, lse=lse, d_o=d_o))
     d.ld_o = _rows("o", o, q.shape, q.dtype)
     d.ld_do = _rows("d_o", d_o, q.shape, q.dtype)
-    _check("lse", lse, q.shape[:2], torch.float32)
+    _dense("lse", lse, q.shape[:2], torch.float32)
     lib = _lib()
-    with _on(dev, stream):
+    with _on(dev, stream) as raw:
         dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=dev) for t in (q, k, v))
         ws = _ws(lib.m3_attn_prefill_varlen_backward_workspace_size(ctypes.byref(d)),
                  "m3_attn_prefill_varlen_backward", dev)
         e = lib.m3_attn_prefill_varlen_backward(
-            ctypes.byref(d), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(q), _ptr(k), _ptr(v),
-            _ptr(o), _ptr(lse), _ptr(d_o), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
-            _stream(None))
+            ctypes.byref(d), _addr(cu_seqlens_q), _addr(cu_seqlens_k), _addr(q), _addr(k), _addr(v),
+            _addr(o), _addr(lse), _addr(d_o), _addr(dq), _addr(dk), _addr(dv), _addr(ws), ws.numel(),
+            raw)
     if e != 0:
         raise M3Error(e, "m3_attn_prefill_varlen_backward")
     return dq, dk, dv
@@ -877,21 +905,21 @@ def attn_decode(q, k_cache, v_cache, lengths, scale=None, o=None, ws=None, strea
         if S > 1 and (t.stride(0) <= 0):
             raise ValueError(f"{n}: sequences must not share rows")
         strides.append((_rows(n, t[0], (cap, Hk, D), q.dtype), t.stride(0) if S > 1 else 0))
-    _check("lengths", lengths, (S,), torch.int32)
+    _dense("lengths", lengths, (S,), torch.int32)
     d = m3_attn_dims(S, 0, cap, Hq, Hk, D, code, D ** -0.5 if scale is None else scale,
                      _rows("q", q, (S, Hq, D), q.dtype), strides[0][0], strides[1][0], 0, 0,
                      strides[0][1], strides[1][1])
     lib = _lib()
-    with _on(dev, stream):
+    with _on(dev, stream) as raw:
         if o is None:
             o = torch.empty(q.shape, dtype=q.dtype, device=dev)
         d.ld_o = _rows("o", o, q.shape, q.dtype)
         lse = torch.empty((S, Hq), dtype=torch.float32, device=dev)
         if ws is None:
             ws = _ws(lib.m3_attn_decode_workspace_size(ctypes.byref(d)), "m3_attn_decode", dev)
-        e = lib.m3_attn_decode(ctypes.byref(d), _ptr(lengths), _ptr(q), _ptr(k_cache),
-                               _ptr(v_cache), _ptr(o), _ptr(lse), _ptr(ws),
-                               ws.numel() * ws.element_size(), _stream(None))
+        e = lib.m3_attn_decode(ctypes.byref(d), _addr(lengths), _addr(q), _addr(k_cache),
+                               _addr(v_cache), _addr(o), _addr(lse), _addr(ws),
+                               ws.numel() * ws.element_size(), raw)
     if e != 0:
         raise M3Error(e, "m3_attn_decode")
     return o, lse

@@ -213,7 +213,7 @@ m3_status check_gated(const m3_gated_dims* d, bool scan, bool packed) {
     if (ld != 0 && ld < d->width) return M3_ERR_SHAPE;
   if (bad_dtype(d->dtype)) return M3_ERR_DTYPE;
   if (scan) {
-    const m3::GatedPlan p = m3::gated_plan(d->batch, d->seqlen, d->width, packed);
+    const m3::GatedPlan p = m3::gated_plan(d->batch, d->seqlen, d->width, packed, true);
     if (p.nchain > 0x7fffffff || !grid_fits(p.nchain * p.ntile, 1024)) return M3_ERR_SHAPE;
   } else if (!grid_fits((static_cast<int64_t>(d->batch) * d->width + 255) / 256, 256)) {
     return M3_ERR_SHAPE;
@@ -644,7 +644,7 @@ m3_status m3_gated_scan(const m3_gated_dims* d, const int32_t* cu_seqlens, const
   g.y = y;
   g.hT = hT;
   g.states = states;
-  m3::gated_carve(g, ws);
+  m3::gated_carve(g, false, ws);
   return hip_status(m3::launch_gated_scan(g, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
 }
 
@@ -677,7 +677,7 @@ m3_status m3_gated_scan_backward(const m3_gated_dims* d, const int32_t* cu_seqle
   g.di = di;
   g.ddecay = ddecay;
   g.dh0 = dh0;
-  m3::gated_carve(g, ws);
+  m3::gated_carve(g, true, ws);
   return hip_status(
       m3::launch_gated_backward(g, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
 }

@@ -329,34 +329,50 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
   }
 }
 
-// joins the parts of one (sequence, head): D / 4 threads of four channels,
-// 256 / (D / 4) heads per workgroup
+// Joins the parts of one (sequence, head) per workgroup: 256 / (D / 4) groups
+// of threads take every so manieth part each, four channels a thread.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * (1024 / D) + threadIdx.x / (D / 4);
-  if (n >= static_cast<int64_t>(a.S) * a.Hq) return;
-  const int d = 4 * (threadIdx.x % (D / 4));
+  constexpr int NG = 1024 / D;
+  __shared__ f4 sv[NG][D / 4];
+  __shared__ float sl[NG];
+  const int64_t n = blockIdx.x;
+  const int dl = threadIdx.x % (D / 4), g = threadIdx.x / (D / 4), lane = threadIdx.x & 63;
   const f2* pm = reinterpret_cast<const f2*>(a.pm) + n * a.nsplit;
   float m = -INFINITY;
-  for (int p = 0; p < a.nsplit; ++p) m = fmaxf(m, pm[p].x);
+  for (int p = lane; p < a.nsplit; p += 64) m = fmaxf(m, pm[p].x);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
   float l = 0.0f;
   f4 v = f4{0, 0, 0, 0};
-  for (int p = 0; p < a.nsplit; ++p) {
+#pragma unroll 2
+  for (int p = g; p < a.nsplit; p += NG) {
     const f2 ml = pm[p];
+    const f4 o = *reinterpret_cast<const f4*>(a.po + (n * a.nsplit + p) * D + 4 * dl);
     if (ml.y == 0.0f) continue;
     const float f = ml.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ml.x - m);
-    const f4 o = *reinterpret_cast<const f4*>(a.po + (n * a.nsplit + p) * D + d);
     l = fmaf(f, ml.y, l);
     v.x = fmaf(f, o.x, v.x);
     v.y = fmaf(f, o.y, v.y);
     v.z = fmaf(f, o.z, v.z);
     v.w = fmaf(f, o.w, v.w);
   }
+  sv[g][dl] = v;
+  if (dl == 0) sl[g] = l;
+  __syncthreads();
+  if (g != 0) return;
+  l = 0.0f;
+  v = f4{0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < NG; ++k) {
+    l += sl[k];
+    v += sv[k][dl];
+  }
   const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
   const int64_t s = n / a.Hq;
   const int h = static_cast<int>(n % a.Hq);
-  put4(static_cast<T*>(a.o) + s * a.ldo + h * D + d, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-  if (d == 0 && a.lse) a.lse[n] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2A;
+  put4(static_cast<T*>(a.o) + s * a.ldo + h * D + 4 * dl, v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  if (dl == 0 && a.lse) a.lse[n] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2A;
 }
 
 template <typename T, int D, int BN>
@@ -374,8 +390,7 @@ hipError_t run_decode(const AttnArgs& a, hipStream_t s) {
   k_attn_decode<T, D, WAVES><<<static_cast<unsigned>(grid), 64 * WAVES, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.nsplit == 1) return e;
-  const int64_t heads = static_cast<int64_t>(a.S) * a.Hq, per = 1024 / D;
-  k_attn_join<T, D><<<static_cast<unsigned>((heads + per - 1) / per), 256, 0, s>>>(a);
+  k_attn_join<T, D><<<static_cast<unsigned>(a.S * a.Hq), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

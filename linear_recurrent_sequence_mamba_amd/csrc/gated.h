@@ -36,12 +36,12 @@ struct GatedArgs {
 };
 
 struct GatedPlan {
-  int V, tile, ncb, ntile;    // channels per lane, rows per tile, channel blocks, tiles
+  int tile, ncb, ntile;       // rows per tile, blocks of 64 channels, tiles
   int64_t nchain;             // independent chains of tiles
 };
-GatedPlan gated_plan(int B, int T, int D, bool packed);
+GatedPlan gated_plan(int B, int T, int D, bool packed, bool backward);
 size_t gated_workspace_bytes(int B, int T, int D, bool packed, bool backward);
-void gated_carve(GatedArgs& g, void* ws);
+void gated_carve(GatedArgs& g, bool backward, void* ws);
 hipError_t launch_gated_scan(GatedArgs& g, int bf16, hipStream_t s);
 hipError_t launch_gated_backward(GatedArgs& g, int bf16, hipStream_t s);
 hipError_t launch_gated_step(const GatedArgs& g, float* h, int bf16, hipStream_t s);

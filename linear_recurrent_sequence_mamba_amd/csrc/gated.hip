@@ -26,8 +26,11 @@ using Raw = RawVec<T, V>;
 
 template <typename T, int V>
 __device__ __forceinline__ void store_v(T* p, const float* v) {
-  if constexpr (V == 1) {
-    p[0] = from_f32<T>(v[0]);
+  if constexpr (V == 1 && sizeof(T) == 4) {
+    p[0] = v[0];
+  } else if constexpr (V == 1) {
+    const bh2 b = __builtin_convertvector(f2{v[0], v[0]}, bh2);
+    p[0] = __builtin_bit_cast(T, b[0]);
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int k = 0; k < V / 2; ++k) reinterpret_cast<f2*>(p)[k] = f2{v[2 * k], v[2 * k + 1]};
@@ -46,6 +49,22 @@ __device__ __forceinline__ void store_v(T* p, const float* v) {
   }
 }
 
+// TOK rows from t0 on of the channels at ch.  Rows past the end repeat the
+// last one.  The row's address is uniform: the lane adds a 32-bit offset.
+template <typename T, int V, int TOK>
+__device__ __forceinline__ void load_rows(Raw<T, V>* raw, const T* p, int64_t ld, int ch, int t0,
+                                          int T_) {
+  const uint32_t off = static_cast<uint32_t>(ch) * static_cast<uint32_t>(sizeof(T));
+  const char* row = reinterpret_cast<const char*>(p + min(t0, T_ - 1) * ld);
+  const int64_t step = ld * static_cast<int64_t>(sizeof(T));
+#pragma unroll
+  for (int j = 0; j < TOK; ++j) {
+    raw[j].load(reinterpret_cast<const T*>(row + off));
+    row += t0 + j + 1 < T_ ? step : 0;
+    __builtin_amdgcn_sched_barrier(0);   // one row address at a time
+  }
+}
+
 // -c softplus(decay) log2(e), the factor of sigmoid(r) in log2(a)
 __device__ __forceinline__ float decay_factor(float d, float c) {
   return -c * kLog2e * (fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d))));
@@ -55,17 +74,18 @@ __device__ __forceinline__ float sigmoid(float v) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * v));
 }
 
-// a and 1 - a^2 from log2(a) <= 0.  The polynomial interpolates
-// (e^z - 1) / z on [-0.35, 0] at Chebyshev points (relative error 1.5e-8);
-// below that 1 - a^2 >= 0.3 loses nothing that fp32 keeps.
-__device__ __forceinline__ void decay_of(float l2, float& a, float& m2) {
-  a = __builtin_amdgcn_exp2f(l2);
-  const float z = (2.0f * kLn2) * l2;
-  float p = fmaf(z, 7.2112456e-03f, 4.1331873e-02f);
-  p = fmaf(z, p, 1.6662531e-01f);
-  p = fmaf(z, p, 4.9999820e-01f);
-  p = fmaf(z, p, 0.99999999f);
-  m2 = z > -0.35f ? -z * p : fmaf(-a, a, 1.0f);
+// a and 1 - a^2 from l = log2(a) <= 0.  With z = 2 L = 2 ln(2) l, the
+// polynomial interpolates (1 - e^z) / l at Chebyshev points of z in
+// [-0.35, 0] (relative error 1.5e-8); below that 1 - a^2 >= 0.3 loses nothing
+// that fp32 keeps.
+constexpr float kZ = 2.0f * kLn2;
+__device__ __forceinline__ void decay_of(float l, float& a, float& m2) {
+  a = __builtin_amdgcn_exp2f(l);
+  float p = fmaf(l, -7.2112456e-03f * kZ * kZ * kZ * kZ * kZ, -4.1331873e-02f * kZ * kZ * kZ * kZ);
+  p = fmaf(l, p, -1.6662531e-01f * kZ * kZ * kZ);
+  p = fmaf(l, p, -4.9999820e-01f * kZ * kZ);
+  p = fmaf(l, p, -0.99999999f * kZ);
+  m2 = l > -0.35f / kZ ? l * p : fmaf(-a, a, 1.0f);
 }
 
 // ---------------------------------------------------------------------------
@@ -110,8 +130,8 @@ __device__ __forceinline__ float join_p(float p, float cp) {
 __global__ void k_gated_init(GatedArgs a, const float* src, float* dst, int64_t nslot) {
   const int tid = threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + tid; i < nslot; i += step)
-    a.slots[i] = 0;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + tid; i < nslot / 2; i += step)
+    reinterpret_cast<ulonglong2*>(a.slots)[i] = ulonglong2{0, 0};   // 64 slots to a chain
   if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;
   if (!a.cu) return;
   __shared__ int part[256];
@@ -196,8 +216,9 @@ __device__ __forceinline__ unsigned take_ticket(const GatedArgs& a) {
 // ends are joined through LDS, the tiles' through the carry slots, and
 // y = h_local + product * carry.
 template <typename T, int V, int TOK, int WAVES, bool PACKED>
-__global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_scan(GatedArgs g) {
+__global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
   constexpr int TILE = TOK * WAVES;
+  static_assert(TOK <= 32 && kGatedChunk % TOK == 0, "rows of a window in 32 bits");
   __shared__ float sH[WAVES][64 * V], sP[WAVES][64 * V], sC[64 * V];
   const unsigned n = take_ticket(g);
   const int tile = static_cast<int>(n / g.nchain), chain = static_cast<int>(n % g.nchain);
@@ -208,24 +229,27 @@ __global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_scan(
   const int chc = on ? ch : g.D - V;   // lanes past the end read the last channels
   const int t0 = tile * TILE + wave * TOK;
   const int64_t row0 = static_cast<int64_t>(b) * g.T;
-  const T* x = static_cast<const T*>(g.x) + row0 * g.ldx + chc;
-  const T* r = static_cast<const T*>(g.r) + row0 * g.ldr + chc;
-  const T* gi = static_cast<const T*>(g.i) + row0 * g.ldi + chc;
-  T* y = static_cast<T*>(g.y) + row0 * g.D + chc;
+  const T* x = static_cast<const T*>(g.x) + row0 * g.ldx;
+  const T* r = static_cast<const T*>(g.r) + row0 * g.ldr;
+  const T* gi = static_cast<const T*>(g.i) + row0 * g.ldi;
+  T* y = static_cast<T*>(g.y) + row0 * g.D;
 
-  Raw<T, V> rx[TOK], rr[TOK], ri[TOK];
+  float dec[V];
 #pragma unroll
-  for (int j = 0; j < TOK; ++j) {
-    const int64_t t = min(t0 + j, g.T - 1);
-    rr[j].load(r + t * g.ldr);
-    rx[j].load(x + t * g.ldx);
-    ri[j].load(gi + t * g.ldi);
-  }
+  for (int v = 0; v < V; ++v) dec[v] = g.decay[chc + v];
+  Raw<T, V> rx[TOK], rr[TOK], ri[TOK];
+  load_rows<T, V, TOK>(rr, r, g.ldr, chc, t0, g.T);
+  load_rows<T, V, TOK>(rx, x, g.ldx, chc, t0, g.T);
+  load_rows<T, V, TOK>(ri, gi, g.ldi, chc, t0, g.T);
+  if (wave == 0)
+#pragma unroll
+    for (int v = 0; v < V; ++v) sC[lane * V + v] = decay_factor(dec[v], g.c);
   Window w{};
   if constexpr (PACKED) w = window_of(g.cuc, g.S, t0, TOK);
+  __syncthreads();
   float k[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) k[v] = decay_factor(g.decay[chc + v], g.c);
+  for (int v = 0; v < V; ++v) k[v] = sC[lane * V + v];
 
   float h[V], P[V], hl[TOK][V], pl[TOK][V];
 #pragma unroll
@@ -247,13 +271,11 @@ __global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_scan(
         }
       }
     }
-    const bool in = t0 + j < g.T;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float a, m2;
       decay_of(k[v] * sigmoid(vr[v]), a, m2);
-      float bt = __builtin_amdgcn_sqrtf(m2) * (sigmoid(vi[v]) * vx[v]);
-      if (!in) { a = 1.0f; bt = 0.0f; }
+      const float bt = __builtin_amdgcn_sqrtf(m2) * (sigmoid(vi[v]) * vx[v]);
       h[v] = fmaf(a, h[v], bt);
       P[v] *= a;
       hl[j][v] = h[v];
@@ -308,7 +330,9 @@ __global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_scan(
     float o[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = join<PACKED>(pl[j][v], carry[v], hl[j][v]);
-    store_v<T, V>(y + static_cast<int64_t>(t) * g.D, o);
+    store_v<T, V>(reinterpret_cast<T*>(reinterpret_cast<char*>(y + static_cast<int64_t>(t) * g.D) +
+                                       static_cast<uint32_t>(ch) * static_cast<uint32_t>(sizeof(T))),
+                  o);
     if (PACKED) {
       if (w.end >> j & 1) {
         while (g.cuc[s + 1] <= t) ++s;   // the sequence whose last row this is
@@ -328,10 +352,14 @@ __global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_scan(
 // from the chunk state that the scan saved, scans q_t = a_t (dy_t + q_{t+1})
 // backwards from zero with the running product of a, takes q of the next
 // tile as its carry, and writes dx, dr, di and a partial sum of ddecay.
+//
+// A row keeps six numbers from pass to pass: a, dy and, first, m, sigmoid(r),
+// sigmoid(i), x; these become the factors of g in dx, di, dL L and dr as soon
+// as h is known, in place, so 16 rows fit 128 registers (four waves a SIMD).
 template <typename T, int V, int TOK, int WAVES, bool PACKED>
-__global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_backward(GatedArgs g) {
+__global__ __launch_bounds__(64 * WAVES, 4) void k_gated_backward(GatedArgs g) {
   constexpr int TILE = TOK * WAVES;
-  static_assert(TILE == kGatedChunk, "one saved state per tile");
+  static_assert(TILE == kGatedChunk && TOK <= 32, "one saved state per tile; rows of a window in 32 bits");
   __shared__ float sH[WAVES][64 * V], sP[WAVES][64 * V], sC[64 * V];
   const unsigned n = take_ticket(g);
   const int tile = g.ntile - 1 - static_cast<int>(n / g.nchain);
@@ -342,34 +370,35 @@ __global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_backw
   const bool on = ch < g.D;
   const int chc = on ? ch : g.D - V;
   const int t0 = tile * TILE + wave * TOK;
+  const int nrow = min(TOK, g.T - t0);   // rows of this wave (may be <= 0)
   const int64_t row0 = static_cast<int64_t>(b) * g.T;
-  const T* x = static_cast<const T*>(g.x) + row0 * g.ldx + chc;
-  const T* r = static_cast<const T*>(g.r) + row0 * g.ldr + chc;
-  const T* gi = static_cast<const T*>(g.i) + row0 * g.ldi + chc;
-  const T* dy = static_cast<const T*>(g.dy) + row0 * g.D + chc;
 
-  Raw<T, V> rx[TOK], rr[TOK], ri[TOK], rd[TOK];
-#pragma unroll
-  for (int j = 0; j < TOK; ++j) {
-    const int64_t t = min(t0 + j, g.T - 1);
-    rr[j].load(r + t * g.ldr);
-    rx[j].load(x + t * g.ldx);
-    ri[j].load(gi + t * g.ldi);
-    rd[j].load(dy + t * g.D);
-  }
-  float entry[V], k[V];
+  float entry[V], k[V], dec[V];
   {
-    const float* st = g.cstates + (b * static_cast<int64_t>(g.ntile) + tile) * g.D + chc;
+    const float* st = g.cstates + (b * static_cast<int64_t>(g.ntile) + tile) * g.D;
 #pragma unroll
-    for (int v = 0; v < V; ++v) entry[v] = st[v];
+    for (int v = 0; v < V; ++v) {
+      dec[v] = g.decay[chc + v];
+      entry[v] = st[chc + v];
+    }
   }
+  Raw<T, V> rx[TOK], rr[TOK], ri[TOK], rd[TOK];
+  load_rows<T, V, TOK>(rr, static_cast<const T*>(g.r) + row0 * g.ldr, g.ldr, chc, t0, g.T);
+  load_rows<T, V, TOK>(rx, static_cast<const T*>(g.x) + row0 * g.ldx, g.ldx, chc, t0, g.T);
+  load_rows<T, V, TOK>(ri, static_cast<const T*>(g.i) + row0 * g.ldi, g.ldi, chc, t0, g.T);
+  load_rows<T, V, TOK>(rd, static_cast<const T*>(g.dy) + row0 * g.D, g.D, chc, t0, g.T);
+  if (wave == 0)
+#pragma unroll
+    for (int v = 0; v < V; ++v) sC[lane * V + v] = decay_factor(dec[v], g.c);
   Window w{};
   if constexpr (PACKED) w = window_of(g.cuc, g.S, t0, TOK);
+  __syncthreads();
 #pragma unroll
-  for (int v = 0; v < V; ++v) k[v] = decay_factor(g.decay[chc + v], g.c);
+  for (int v = 0; v < V; ++v) k[v] = sC[lane * V + v];
 
-  // forward: a, the gates and the wave's local scan
-  float h[V], P[V], av[TOK][V], m2v[TOK][V], srv[TOK][V], siv[TOK][V];
+  // forward: the gates and the wave's scan from zero (rows past the end come
+  // after those that count)
+  float h[V], P[V], av[TOK][V], f1[TOK][V], f2_[TOK][V], f3[TOK][V], f4_[TOK][V];
 #pragma unroll
   for (int v = 0; v < V; ++v) { h[v] = 0.0f; P[v] = 1.0f; }
   int s = w.s0;
@@ -389,19 +418,18 @@ __global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_backw
         }
       }
     }
-    const bool in = t0 + j < g.T;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float a, m2;
       const float sr = sigmoid(vr[v]), si = sigmoid(vi[v]);
       decay_of(k[v] * sr, a, m2);
-      float bt = __builtin_amdgcn_sqrtf(m2) * (si * vx[v]);
-      if (!in) { a = 1.0f; bt = 0.0f; }
+      const float m = __builtin_amdgcn_sqrtf(m2);
       av[j][v] = a;
-      m2v[j][v] = m2;
-      srv[j][v] = sr;
-      siv[j][v] = si;
-      h[v] = fmaf(a, h[v], bt);
+      f1[j][v] = m;
+      f2_[j][v] = sr;
+      f3[j][v] = si;
+      f4_[j][v] = vx[v];
+      h[v] = fmaf(a, h[v], m * (si * vx[v]));
       P[v] *= a;
     }
   }
@@ -417,11 +445,40 @@ __global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_backw
       entry[v] = join<PACKED>(sP[u][lane * V + v], entry[v], sH[u][lane * V + v]);
   __syncthreads();   // sH and sP are written again below
 
-  // backward: q from zero and the product of a, from the last row on
-  float q[V], ql[TOK][V], pl[TOK][V];   // what follows a row: q_{t+1} = ql + pl * carry
+  // forward again, now with h: the factors of g
+  s = w.s0;
+#pragma unroll
+  for (int j = 0; j < TOK; ++j) {
+    if constexpr (PACKED) {
+      if (w.start >> j & 1) {
+        while (g.cuc[s] < t0 + j || g.cuc[s + 1] <= t0 + j) ++s;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          entry[v] = g.h0 ? g.h0[static_cast<int64_t>(s) * g.D + chc + v] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      // products of the first pass are formed anew, not kept in registers
+      asm volatile("" : "+v"(f1[j][v]), "+v"(f2_[j][v]), "+v"(f3[j][v]), "+v"(f4_[j][v]));
+      const float a = av[j][v], m = f1[j][v], sr = f2_[j][v], si = f3[j][v];
+      const float u = si * f4_[j][v], L = kLn2 * (k[v] * sr), ah = a * entry[v];
+      // L / m where m is 0 (a = 1): the limit 0
+      const float lm = m > 0.0f ? L * __builtin_amdgcn_rcpf(m) : 0.0f;
+      const float mu = m * u;
+      f1[j][v] = m * si;                                 // dx / g
+      f3[j][v] = fmaf(-mu, si, mu);                      // di / g
+      f4_[j][v] = fmaf(ah, L, -(a * a) * (lm * u));      // dL L / g
+      f2_[j][v] = 1.0f - sr;
+      entry[v] = ah + mu;
+    }
+  }
+
+  // backward: q from zero and the product of a
+  float q[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) { q[v] = 0.0f; P[v] = 1.0f; }
-  int se = s;   // the sequence of the window's last row that starts or goes on here
+  int se = 0;   // the sequence of the last row
   if constexpr (PACKED) {
     se = seq_of(g.cuc, g.S, min(t0 + TOK, g.T) - 1);
     if (se < 0) se = 0;
@@ -430,6 +487,7 @@ __global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_backw
   int sb = se;
 #pragma unroll
   for (int j = TOK - 1; j >= 0; --j) {
+    if (j >= nrow) continue;
     if constexpr (PACKED) {
       if (w.end >> j & 1) {
         while (g.cuc[sb] > t0 + j || g.cuc[sb + 1] <= g.cuc[sb]) --sb;
@@ -442,12 +500,9 @@ __global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_backw
     }
     float vd[V];
     rd[j].get(vd);
-    const bool in = t0 + j < g.T;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      ql[j][v] = q[v];
-      pl[j][v] = P[v];
-      q[v] = av[j][v] * (in ? q[v] + vd[v] : q[v]);
+      q[v] = av[j][v] * (q[v] + vd[v]);
       P[v] *= av[j][v];
     }
   }
@@ -457,7 +512,7 @@ __global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_backw
     sP[wave][lane * V + v] = P[v];
   }
   __syncthreads();
-  float cH[V], cP[V], carry[V];
+  float cH[V], cP[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) { cH[v] = 0.0f; cP[v] = 1.0f; }
   for (int u = WAVES - 1; u > wave; --u)
@@ -471,67 +526,64 @@ __global__ __launch_bounds__(64 * WAVES, 2048 / (64 * WAVES)) void k_gated_backw
     u64* slot = g.slots + (static_cast<int64_t>(tile) * g.nchain + chain) * (64 * V) + lane * V;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+      float c;
       if (tile == g.ntile - 1)
-        carry[v] = !PACKED && g.dhT ? g.dhT[static_cast<int64_t>(b) * g.D + chc + v] : 0.0f;
+        c = !PACKED && g.dhT ? g.dhT[static_cast<int64_t>(b) * g.D + chc + v] : 0.0f;
       else
-        carry[v] = await_carry(slot + static_cast<int64_t>(g.nchain) * (64 * V) + v);
-      const float q0 = join<PACKED>(P[v], join<PACKED>(cP[v], carry[v], cH[v]), q[v]);
+        c = await_carry(slot + static_cast<int64_t>(g.nchain) * (64 * V) + v);
+      const float q0 = join<PACKED>(P[v], join<PACKED>(cP[v], c, cH[v]), q[v]);
       if (tile > 0) publish(slot + v, q0);
       else if (!PACKED && on && g.dh0) g.dh0[static_cast<int64_t>(b) * g.D + ch + v] = q0;
-      sC[lane * V + v] = carry[v];
+      sC[lane * V + v] = c;
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = join<PACKED>(cP[v], sC[lane * V + v], cH[v]);
+  for (int v = 0; v < V; ++v) q[v] = join<PACKED>(cP[v], sC[lane * V + v], cH[v]);
 
-  // the gradients, in order of time (h runs along)
+  // backward again, now with q: the gradients
   float dk[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) dk[v] = 0.0f;
-  T* dx = static_cast<T*>(g.dx) + row0 * g.ldg + chc;
-  T* dr = static_cast<T*>(g.dr) + row0 * g.ldg + chc;
-  T* di = static_cast<T*>(g.di) + row0 * g.ldg + chc;
-  s = w.s0;
+  const uint32_t off = static_cast<uint32_t>(ch) * static_cast<uint32_t>(sizeof(T));
+  const int64_t step = g.ldg * static_cast<int64_t>(sizeof(T));
+  const int64_t at = (row0 + t0 + TOK) * step;
+  char* dx = static_cast<char*>(g.dx) + at;
+  char* dr = static_cast<char*>(g.dr) + at;
+  char* di = static_cast<char*>(g.di) + at;
+  sb = se;
 #pragma unroll
-  for (int j = 0; j < TOK; ++j) {
-    const int t = t0 + j;
-    const bool live = t < g.T && (!PACKED || (w.live >> j & 1));
-    bool first = false;
+  for (int j = TOK - 1; j >= 0; --j) {
+    dx -= step;
+    dr -= step;
+    di -= step;
+    if (j >= nrow) continue;
     if constexpr (PACKED) {
-      if (w.start >> j & 1) {
-        first = true;
-        while (g.cuc[s] < t || g.cuc[s + 1] <= t) ++s;
+      if (!(w.live >> j & 1)) continue;
+      if (w.end >> j & 1) {
+        while (g.cuc[sb] > t0 + j || g.cuc[sb + 1] <= g.cuc[sb]) --sb;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-          entry[v] = g.h0 ? g.h0[static_cast<int64_t>(s) * g.D + chc + v] : 0.0f;
+          q[v] = g.dhT ? g.dhT[static_cast<int64_t>(sb) * g.D + chc + v] : 0.0f;
       }
     }
-    float vx[V], vd[V], ox[V], orr[V], oi[V];
-    rx[j].get(vx);
+    float vd[V], ox[V], orr[V], oi[V];
     rd[j].get(vd);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float a = av[j][v], sr = srv[j][v], si = siv[j][v];
-      const float gt = vd[v] + join<PACKED>(pl[j][v], carry[v], ql[j][v]);
-      const float m2 = m2v[j][v];
-      // the hardware root takes a denormal 1 - a^2 for 0
-      const float im = m2 >= 1.17549435e-38f ? __builtin_amdgcn_rsqf(m2) : 0.0f;
-      const float m = m2 * im, L = kLn2 * (k[v] * sr), u = si * vx[v];
-      const float ah = a * entry[v];
-      const float gl = gt * (ah * L - (a * a) * (L * im) * u);
-      ox[v] = gt * m * si;
-      oi[v] = gt * m * u * (1.0f - si);
-      orr[v] = gl * (1.0f - sr);
-      if (live) dk[v] += gl;
-      if (PACKED && first && on && g.dh0)
-        g.dh0[static_cast<int64_t>(s) * g.D + ch + v] = a * gt;
-      entry[v] = fmaf(m, u, ah);
+      const float gt = vd[v] + q[v], gl = gt * f4_[j][v];
+      ox[v] = gt * f1[j][v];
+      oi[v] = gt * f3[j][v];
+      orr[v] = gl * f2_[j][v];
+      dk[v] += gl;
+      q[v] = av[j][v] * gt;
+      if (PACKED && (w.start >> j & 1) && on && g.dh0)
+        g.dh0[static_cast<int64_t>(sb) * g.D + ch + v] = q[v];
     }
-    if (live && on) {
-      store_v<T, V>(dx + static_cast<int64_t>(t) * g.ldg, ox);
-      store_v<T, V>(dr + static_cast<int64_t>(t) * g.ldg, orr);
-      store_v<T, V>(di + static_cast<int64_t>(t) * g.ldg, oi);
+    if (on) {
+      store_v<T, V>(reinterpret_cast<T*>(dx + off), ox);
+      store_v<T, V>(reinterpret_cast<T*>(dr + off), orr);
+      store_v<T, V>(reinterpret_cast<T*>(di + off), oi);
     }
   }
   // the tile's part of the sum for ddecay, over its waves in order
@@ -618,19 +670,22 @@ hipError_t run_scan(GatedArgs& g, hipStream_t s) {
     k_gated_scan<T, V, TOK, WAVES, false><<<grid, 64 * WAVES, 0, s>>>(g);
   return hipGetLastError();
 }
-template <typename T, int V>
+// The dense kernel's 16 rows a wave just fit 128 registers; the packed one's
+// windows do not (19 spilled: 155 us against 111 us for 8192 rows of 2048
+// channels), so its waves take 8 rows, twice as many waves to a tile.
+template <typename T>
 hipError_t run_backward(GatedArgs& g, hipStream_t s) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(g.ntile) * g.nchain);
   if (g.cu)
-    k_gated_backward<T, V, kGatedChunk / 16, 16, true><<<grid, 1024, 0, s>>>(g);
+    k_gated_backward<T, 1, 8, kGatedChunk / 8, true><<<grid, 8 * kGatedChunk, 0, s>>>(g);
   else
-    k_gated_backward<T, V, kGatedChunk / 16, 16, false><<<grid, 1024, 0, s>>>(g);
+    k_gated_backward<T, 1, 16, kGatedChunk / 16, false><<<grid, 4 * kGatedChunk, 0, s>>>(g);
   return hipGetLastError();
 }
 
 hipError_t run_init(const GatedArgs& g, const float* src, float* dst, int64_t nslot, hipStream_t s) {
   if (g.ntile == 1 && !g.cu) return hipSuccess;
-  int64_t blocks = (nslot + 2047) / 2048;
+  int64_t blocks = (nslot + 1023) / 1024;
   if (g.cu && blocks < g.S + 1) blocks = g.S + 1;
   if (blocks > 4096) blocks = 4096;
   if (blocks < 1) blocks = 1;
@@ -642,26 +697,31 @@ constexpr size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-GatedPlan gated_plan(int B, int T, int D, bool packed) {
+// Tiles of the scan: 256 rows, or 512 where all workgroups of 256 would be
+// resident at once (two a CU).  Then the time is that of handing the carry
+// from tile to tile, about 0.8 us each, and half as many tiles take less:
+// 16384 rows of 512 channels 37 against 52 us, of 4096 channels 161 against
+// 126 us.
+GatedPlan gated_plan(int B, int T, int D, bool packed, bool backward) {
   GatedPlan p;
-  p.V = 1;
-  p.tile = kGatedChunk;
-  p.ncb = (D + 64 * p.V - 1) / (64 * p.V);
+  p.ncb = (D + 63) / 64;
   p.nchain = static_cast<int64_t>(p.ncb) * (packed ? 1 : B);
-  p.ntile = (T + p.tile - 1) / p.tile;
+  p.tile = backward ? kGatedChunk : 256;
+  if (!backward && T > 256 && (static_cast<int64_t>(T) + 255) / 256 * p.nchain <= 512) p.tile = 512;
+  p.ntile = (T - 1) / p.tile + 1;
   return p;
 }
 
 size_t gated_workspace_bytes(int B, int T, int D, bool packed, bool backward) {
-  const GatedPlan p = gated_plan(B, T, D, packed);
+  const GatedPlan p = gated_plan(B, T, D, packed, backward);
   size_t n = 256 + up256(sizeof(int32_t) * (static_cast<size_t>(B) + 1));
-  n += up256(sizeof(u64) * 64 * p.V * p.nchain * p.ntile);
+  n += up256(sizeof(u64) * 64 * p.nchain * p.ntile);
   if (backward) n += up256(sizeof(float) * D * (packed ? 1 : B) * p.ntile);
   return n;
 }
 
-void gated_carve(GatedArgs& g, void* ws) {
-  const GatedPlan p = gated_plan(g.B, g.T, g.D, g.cu != nullptr);
+void gated_carve(GatedArgs& g, bool backward, void* ws) {
+  const GatedPlan p = gated_plan(g.B, g.T, g.D, g.cu != nullptr, backward);
   g.ncb = p.ncb;
   g.nchain = static_cast<int>(p.nchain);
   g.ntile = p.ntile;
@@ -671,23 +731,24 @@ void gated_carve(GatedArgs& g, void* ws) {
   g.cuc = reinterpret_cast<int32_t*>(c);
   c += up256(sizeof(int32_t) * (static_cast<size_t>(g.B) + 1));
   g.slots = reinterpret_cast<u64*>(c);
-  c += up256(sizeof(u64) * 64 * p.V * p.nchain * p.ntile);
+  c += up256(sizeof(u64) * 64 * p.nchain * p.ntile);
   g.part = reinterpret_cast<float*>(c);
   g.S = g.B;
 }
 
 hipError_t launch_gated_scan(GatedArgs& g, int bf16, hipStream_t s) {
-  const GatedPlan p = gated_plan(g.B, g.T, g.D, g.cu != nullptr);
-  hipError_t e = run_init(g, g.h0, g.hT, p.nchain * p.ntile * 64 * p.V, s);
+  const GatedPlan p = gated_plan(g.B, g.T, g.D, g.cu != nullptr, false);
+  hipError_t e = run_init(g, g.h0, g.hT, p.nchain * p.ntile* 64, s);
   if (e != hipSuccess) return e;
-  return bf16 ? run_scan<bf16_t, 1, 8, 16>(g, s) : run_scan<float, 1, 8, 16>(g, s);
+  if (p.tile == 512) return bf16 ? run_scan<bf16_t, 1, 32, 16>(g, s) : run_scan<float, 1, 32, 16>(g, s);
+  return bf16 ? run_scan<bf16_t, 1, 32, 8>(g, s) : run_scan<float, 1, 32, 8>(g, s);
 }
 
 hipError_t launch_gated_backward(GatedArgs& g, int bf16, hipStream_t s) {
-  const GatedPlan p = gated_plan(g.B, g.T, g.D, g.cu != nullptr);
-  hipError_t e = run_init(g, g.dhT, g.dh0, p.nchain * p.ntile * 64 * p.V, s);
+  const GatedPlan p = gated_plan(g.B, g.T, g.D, g.cu != nullptr, true);
+  hipError_t e = run_init(g, g.dhT, g.dh0, p.nchain * p.ntile* 64, s);
   if (e != hipSuccess) return e;
-  e = bf16 ? run_backward<bf16_t, 1>(g, s) : run_backward<float, 1>(g, s);
+  e = bf16 ? run_backward<bf16_t>(g, s) : run_backward<float>(g, s);
   if (e != hipSuccess) return e;
   const int64_t nparts = static_cast<int64_t>(g.cu ? 1 : g.B) * g.ntile;
   k_gated_ddecay<<<(g.D + 15) / 16, 256, 0, s>>>(g, nparts);

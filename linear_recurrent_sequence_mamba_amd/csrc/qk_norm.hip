@@ -95,8 +95,8 @@ __device__ __forceinline__ void turns(const double* f, int p, float* c, float* s
   }
 }
 
-// A wave takes unit u = (token, part of the heads); its lane groups take rows
-// h = group, group + 64 / G, ... of the part.
+// A wave takes a token and the part blockIdx.y of its heads; its lane groups
+// take rows h = group, group + 64 / G, ... of the part.
 template <typename T, int D, int MODE, bool BWD>
 __global__ __launch_bounds__(256) void k_qk_norm(QkNormArgs a) {
   constexpr int G = D / 8, ROWS = 64 / G;
@@ -121,12 +121,10 @@ __global__ __launch_bounds__(256) void k_qk_norm(QkNormArgs a) {
 
   const int H = a.Hq + a.Hk;
   const int per = (H + a.split - 1) / a.split;
-  const int64_t units = static_cast<int64_t>(a.T) * a.split;
-  const int64_t nw = static_cast<int64_t>(gridDim.x) * 4;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); u < units; u += nw) {
-    const int64_t t = u / a.split;
-    const int h0 = static_cast<int>(u % a.split) * per;
-    const int h1 = min(h0 + per, H);
+  const int h0 = static_cast<int>(blockIdx.y) * per, h1 = min(h0 + per, H);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int tt = blockIdx.x * 4 + wave; tt < a.T; tt += gridDim.x * 4) {
+    const int64_t t = tt;
     float c[4], sn[4];
     turns(f, a.pos[t], c, sn);
     for (int hb = h0; hb < h1; hb += ROWS) {
@@ -142,7 +140,7 @@ __global__ __launch_bounds__(256) void k_qk_norm(QkNormArgs a) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) ss = fmaf(x[s], x[s], fmaf(y[s], y[s], ss));
       ss = group_sum<G>(ss);
-      const float inv = 1.0f / __builtin_sqrtf(fmaf(ss, 1.0f / D, a.eps));
+      const float inv = __builtin_amdgcn_rsqf(fmaf(ss, 1.0f / D, a.eps));   // 1 ulp
       const int64_t ro = (t * (isq ? a.Hq : a.Hk) + hh) * D;
       if constexpr (!BWD) {
         float ox[4], oy[4];
@@ -205,25 +203,26 @@ __global__ __launch_bounds__(256) void k_qk_norm(QkNormArgs a) {
       for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) v += red[q][e / D][r][e % D];
-      a.part[static_cast<int64_t>(blockIdx.x) * 2 * D + e] = v;
+      a.part[(static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 2 * D + e] = v;
     }
   }
 }
 
-// dw = the sum of the blocks' parts: 16 threads of a channel take every 16th
-// part each, joined in order
-__global__ __launch_bounds__(256) void k_qk_norm_dw(QkNormArgs a, int nblocks) {
-  __shared__ float sum[16][17];
+// dw = the sum of the blocks' parts, in a fixed order: 64 threads of a channel
+// take every 64th part each (four in flight) and are joined in LDS.
+__global__ __launch_bounds__(1024) void k_qk_norm_dw(QkNormArgs a, int nblocks) {
+  __shared__ float sum[64][17];
   const int cl = threadIdx.x & 15, k = threadIdx.x >> 4;
   const int e = blockIdx.x * 16 + cl;   // of 2 D
   float acc = 0.0f;
-  for (int p = k; p < nblocks; p += 16) acc += a.part[static_cast<int64_t>(p) * 2 * a.D + e];
+#pragma unroll 4
+  for (int p = k; p < nblocks; p += 64) acc += a.part[static_cast<int64_t>(p) * 2 * a.D + e];
   sum[k][cl] = acc;
   __syncthreads();
   if (k == 0) {
     float v = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v += sum[j][cl];
+    for (int j = 0; j < 64; ++j) v += sum[j][cl];
     float* o = e < a.D ? a.dwq : a.dwk;
     if (o) o[e < a.D ? e : e - a.D] = v;
   }
@@ -237,15 +236,16 @@ int split_of(int T, int H, int D) {
   const int rows = 64 / (D / 8);
   const int most = (H + rows - 1) / rows;
   int s = (4096 + T - 1) / T;
-  return s < 1 ? 1 : s > most ? most : s;
+  if (s > most) s = most;
+  return s > 512 ? 512 : s;
 }
-int blocks_of(int T, int split, int most) {
-  const int64_t n = (static_cast<int64_t>(T) * split + 3) / 4;
-  return static_cast<int>(n < most ? n : most);
+dim3 grid_of(int T, int split, int most) {
+  const int n = (T + 3) / 4, m = most / split;
+  return dim3(static_cast<unsigned>(n < m ? n : m), static_cast<unsigned>(split));
 }
 
 template <typename T, int D, bool BWD>
-void run_dim(const QkNormArgs& a, int grid, hipStream_t s) {
+void run_dim(const QkNormArgs& a, dim3 grid, hipStream_t s) {
   const int n = a.rot / 2;
   if (!a.half)
     k_qk_norm<T, D, kAdj, BWD><<<grid, 256, 0, s>>>(a);
@@ -255,7 +255,7 @@ void run_dim(const QkNormArgs& a, int grid, hipStream_t s) {
     k_qk_norm<T, D, kAny, BWD><<<grid, 256, 0, s>>>(a);
 }
 template <typename T, bool BWD>
-void run_type(const QkNormArgs& a, int grid, hipStream_t s) {
+void run_type(const QkNormArgs& a, dim3 grid, hipStream_t s) {
   switch (a.D) {
     case 32: run_dim<T, 32, BWD>(a, grid, s); break;
     case 64: run_dim<T, 64, BWD>(a, grid, s); break;
@@ -269,12 +269,13 @@ void run_type(const QkNormArgs& a, int grid, hipStream_t s) {
 bool qk_norm_supported(int D) { return D == 32 || D == 64 || D == 128 || D == 256; }
 
 size_t qk_norm_workspace_bytes(int T, int Hq, int Hk, int D) {
-  return sizeof(float) * 2 * D * blocks_of(T, split_of(T, Hq + Hk, D), kBwdBlocks);
+  const dim3 g = grid_of(T, split_of(T, Hq + Hk, D), kBwdBlocks);
+  return sizeof(float) * 2 * D * g.x * g.y;
 }
 
 hipError_t launch_qk_norm(QkNormArgs& a, int bf16, hipStream_t s) {
   a.split = split_of(a.T, a.Hq + a.Hk, a.D);
-  const int grid = blocks_of(a.T, a.split, kFwdBlocks);
+  const dim3 grid = grid_of(a.T, a.split, kFwdBlocks);
   if (bf16) run_type<bf16_t, false>(a, grid, s);
   else run_type<float, false>(a, grid, s);
   return hipGetLastError();
@@ -282,13 +283,13 @@ hipError_t launch_qk_norm(QkNormArgs& a, int bf16, hipStream_t s) {
 
 hipError_t launch_qk_norm_backward(QkNormArgs& a, int bf16, hipStream_t s) {
   a.split = split_of(a.T, a.Hq + a.Hk, a.D);
-  const int grid = blocks_of(a.T, a.split, kBwdBlocks);
+  const dim3 grid = grid_of(a.T, a.split, kBwdBlocks);
   if (bf16) run_type<bf16_t, true>(a, grid, s);
   else run_type<float, true>(a, grid, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (a.dwq || a.dwk) {
-    k_qk_norm_dw<<<2 * a.D / 16, 256, 0, s>>>(a, grid);
+    k_qk_norm_dw<<<2 * a.D / 16, 1024, 0, s>>>(a, static_cast<int>(grid.x * grid.y));
     e = hipGetLastError();
   }
   return e;

@@ -40,9 +40,10 @@ __device__ __forceinline__ bool special(float v) {
 template <typename T, int D, int ROWS, int THREADS>
 __device__ __forceinline__ bool drop_special(T* V) {
   bool found = false;
-#pragma unroll
+  const int tid = opaque(threadIdx.x);
+#pragma unroll 1
   for (int n = 0; n < ROWS * D * static_cast<int>(sizeof(T)) / 16 / THREADS; ++n) {
-    uint4* p = reinterpret_cast<uint4*>(V) + n * THREADS + threadIdx.x;
+    uint4* p = reinterpret_cast<uint4*>(V) + n * THREADS + tid;
     uint4 u = *p;
     uint32_t w[4] = {u.x, u.y, u.z, u.w};
     bool bad = false;
@@ -64,36 +65,39 @@ __device__ __forceinline__ bool drop_special(T* V) {
   return found;
 }
 
-// One tile of NB x 32 keys against 32 queries.  seen: how many of the tile's
-// keys this lane's query sees (may be <= 0 or more than the tile has).
-// MASK: some lane sees fewer than all.
-template <typename T, int D, int NB, bool MASK>
-__device__ __forceinline__ void attend(Rows<D>& st, const Frag<T>* q, const T* K, const T* V,
-                                       float c, int seen, int lane) {
-  using L = Tile<T, D>;
-  const int half = lane >> 5;
-  f16v s[NB];
+// Scores of 32 queries against NB x 32 keys
+template <typename T, int D, int NB>
+__device__ __forceinline__ void score(f16v* s, const Frag<T>* q, const T* K, int lane) {
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     s[b] = f16v{};
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) s[b] = mma(L::frag(K, 32 * b, kk, lane), q[kk], s[b]);
+    for (int kk = 0; kk < D / 16; ++kk) s[b] = mma(Tile<T, D>::frag(K, 32 * b, kk, lane), q[kk], s[b]);
   }
-  if (MASK) {
+}
+
+// Only the first `seen` keys of a tile count (may be <= 0)
+template <int NB>
+__device__ __forceinline__ void hide(f16v* s, int seen, int lane) {
+  seen -= 4 * (opaque(lane) >> 5);
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        s[b][i] = 32 * b + row_of(i, half) < seen ? s[b][i] : -INFINITY;
-  }
+    for (int i = 0; i < 16; ++i)
+      s[b][i] = 32 * b + row_of(i, 0) < seen ? s[b][i] : -INFINITY;
+}
+
+// The maximum that the weights are taken against.  It moves only when it has
+// to: weights up to 2^8 lose nothing in fp32 sums or bf16 products, and most
+// tiles then leave o as it is.
+template <int D, int NB>
+__device__ __forceinline__ void raise_max(Rows<D>& st, const f16v* s, float c) {
   float mx = s[0][0];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
-  mx = fmaxf(mx, other_half(mx)) * c;
-  // The maximum moves only when it has to: weights up to 2^8 lose nothing in
-  // fp32 sums or bf16 products, and most tiles then leave o as it is.
+  mx = half_max(mx) * c;
   if (__ballot(mx > st.m + 8.0f)) {
     const float m = fmaxf(st.m, mx);
     const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
@@ -104,16 +108,19 @@ __device__ __forceinline__ void attend(Rows<D>& st, const Frag<T>* q, const T* K
 #pragma unroll
       for (int i = 0; i < 16; ++i) st.o[d][i] *= f;
   }
+}
+
+// Weights of a tile's scores, added to the sums
+template <typename T, int D, int NB>
+__device__ __forceinline__ void weigh(Rows<D>& st, f16v* s, const T* V, float c, int lane) {
   const float m0 = st.m == -INFINITY ? 0.0f : st.m;
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int b = 0; b < NB; ++b) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], c, -m0));
       st.l += s[b][i];
     }
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       Frag<T> p;
@@ -123,8 +130,70 @@ __device__ __forceinline__ void attend(Rows<D>& st, const Frag<T>* q, const T* K
       frag_from(p, e8);
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
-        st.o[d] = mma(L::frag_t(V, 32 * b + 16 * w, 32 * d, lane), p, st.o[d]);
+        st.o[d] = mma(Tile<T, D>::frag_t(V, 32 * b + 16 * w, 32 * d, lane), p, st.o[d]);
     }
+  }
+}
+
+// The same with the scores of the next tile formed meanwhile: they depend on
+// nothing here, so the matrix cores work while the exponentials run.  The
+// instructions are laid out step by step, each with one product (first those
+// of the next scores, then those with V), its share of the exponentials, and
+// the operand of the product two steps on, read from LDS.
+template <typename T, int D, int NB>
+__device__ __forceinline__ void weigh_ahead(Rows<D>& st, f16v* s, f16v* next, const Frag<T>* q,
+                                            const T* Knext, const T* V, float c, int lane) {
+  using L = Tile<T, D>;
+  constexpr int NM = NB * D / 16;          // products of each kind
+  constexpr int F = 2 * NB, E = 16 * NB;   // fragments of weights, elements
+  constexpr int S = NM + NM * (F - 1) / F; // steps until the last weight is needed
+  const float m0 = st.m == -INFINITY ? 0.0f : st.m;
+  auto operand = [&](int n) __attribute__((always_inline)) -> Frag<T> {
+    if (n < NM) return L::frag(Knext, 32 * (n / (D / 16)), n % (D / 16), lane);
+    const int m = n - NM;
+    return L::frag_t(V, 16 * (m / (D / 32)), 32 * (m % (D / 32)), lane);
+  };
+#pragma unroll
+  for (int b = 0; b < NB; ++b) next[b] = f16v{};
+  Frag<T> op[3], p[F];
+  op[0] = operand(0);
+  op[1] = operand(1);
+#pragma unroll
+  for (int n = 0; n < 2 * NM; ++n) {
+    if (n + 2 < 2 * NM) op[(n + 2) % 3] = operand(n + 2);
+    if (n < NM) {
+      const int b = n / (D / 16);
+      next[b] = mma(op[n % 3], q[n % (D / 16)], next[b]);
+    } else {
+      const int m = n - NM, d = m % (D / 32);
+      st.o[d] = mma(op[n % 3], p[m / (D / 32)], st.o[d]);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      if (e * S / E != n) continue;
+      const float v = __builtin_amdgcn_exp2f(fmaf(s[e / 16][e % 16], c, -m0));
+      s[e / 16][e % 16] = v;
+      st.l += v;
+      if (e % 8 == 7) {
+        float e8[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e8[j] = s[e / 16][e % 16 - 7 + j];
+        frag_from(p[e / 8], e8);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// One tile by itself
+template <typename T, int D, int NB, bool MASK>
+__device__ __forceinline__ void attend(Rows<D>& st, const Frag<T>* q, const T* K, const T* V,
+                                       float c, int seen, int lane) {
+  f16v s[NB];
+  score<T, D, NB>(s, q, K, lane);
+  if (MASK) hide<NB>(s, seen, lane);
+  raise_max<D, NB>(st, s, c);
+  weigh<T, D, NB>(st, s, V, c, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -170,31 +239,48 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   // from here on some query of the block does not see the whole tile
   const int tmask = max(0, min(i0, Lq - 1) + off + 1) / BN;
   const int wmost = min(min(iw + 32, Lq) + off, Lk);
-  const int wleast = min(iw, Lq - 1) + off + 1;
   const T* kp = static_cast<const T*>(a.k) + static_cast<int64_t>(k0) * a.ldk + hk * D;
   const T* vp = static_cast<const T*>(a.v) + static_cast<int64_t>(k0) * a.ldv + hk * D;
+  // K runs one tile ahead of V.  Tiles that every query of the block sees
+  // whole come first, in pairs (the two sets of scores change places): while
+  // a tile's weights are formed the next tile's scores are.
+  f16v s[NB], next[NB];
+  const int nw = (max(wmost, 0) + BN - 1) / BN;   // tiles that the wave sees
+  const int npipe = max(0, min(tmask, ntile - 1)) & ~1;   // (no tile: none)
+  auto arrive = [&](int t) __attribute__((always_inline)) {
+    lds_loads_done();
+    __syncthreads();   // V of t and K of t + 1 are there; every wave is done with t - 1
+    if (t + 2 < ntile) L::template load<BN, WAVES>(sK[t & 1], kp, a.ldk, (t + 2) * BN, Lk - 1, wave, lane);
+    if (t + 1 < ntile) L::template load<BN, WAVES>(sV[(t + 1) & 1], vp, a.ldv, (t + 1) * BN, Lk - 1, wave, lane);
+  };
   if (ntile > 0) {
     L::template load<BN, WAVES>(sK[0], kp, a.ldk, 0, Lk - 1, wave, lane);
-    L::template load<BN, WAVES>(sV[0], vp, a.ldv, 0, Lk - 1, wave, lane);
-  }
-  for (int t = 0; t < ntile; ++t) {
     lds_loads_done();
-    __syncthreads();   // tile t is there, and every wave is done with t - 1
-    if (t + 1 < ntile) {
-      L::template load<BN, WAVES>(sK[(t + 1) & 1], kp, a.ldk, (t + 1) * BN, Lk - 1, wave, lane);
-      L::template load<BN, WAVES>(sV[(t + 1) & 1], vp, a.ldv, (t + 1) * BN, Lk - 1, wave, lane);
-    }
-    const int j0 = t * BN;
-    const T *K = sK[t & 1], *V = sV[t & 1];
+    __syncthreads();
+    L::template load<BN, WAVES>(sV[0], vp, a.ldv, 0, Lk - 1, wave, lane);
+    if (ntile > 1) L::template load<BN, WAVES>(sK[1], kp, a.ldk, BN, Lk - 1, wave, lane);
+    score<T, D, NB>(s, q, sK[0], lane);
+  }
+  for (int t = 0; t < npipe; t += 2) {
+    arrive(t);
+    raise_max<D, NB>(st, s, c);
+    weigh_ahead<T, D, NB>(st, s, next, q, sK[1], sV[0], c, lane);
+    arrive(t + 1);
+    raise_max<D, NB>(st, next, c);
+    weigh_ahead<T, D, NB>(st, next, s, q, sK[0], sV[1], c, lane);
+  }
+#pragma unroll 1
+  for (int t = npipe; t < ntile; ++t) {
+    arrive(t);
     if (t >= tmask) {
       if (drop_special<T, D, BN, 64 * WAVES>(sV[t & 1])) sSpecial = 1;
       __syncthreads();
     }
-    if (j0 >= wmost) continue;
-    if (j0 + BN <= wleast)
-      attend<T, D, NB, false>(st, q, K, V, c, BN, lane);
-    else
-      attend<T, D, NB, true>(st, q, K, V, c, sees - j0, lane);
+    if (t >= nw) continue;
+    hide<NB>(s, sees - t * BN, lane);
+    raise_max<D, NB>(st, s, c);
+    weigh<T, D, NB>(st, s, sV[t & 1], c, lane);
+    if (t + 1 < nw) score<T, D, NB>(s, q, sK[(t + 1) & 1], lane);
   }
   if (ntile > 0 && sSpecial) {
     for (int key = tmask * BN; key < most; ++key) {
@@ -208,7 +294,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
         }
     }
   }
-  const float l = st.l + other_half(st.l);
+  const float l = half_sum(st.l);
   if (i >= Lq) return;
   const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);   // a NaN stays
   T* o = static_cast<T*>(a.o) + row * a.ldo + h * D + 4 * half;
@@ -278,7 +364,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
     else
       attend<T, D, 1, true>(st, q, K, V, c, len - t * BN, lane);
   }
-  const float l = st.l + other_half(st.l);
+  const float l = half_sum(st.l);
   if (half == 0) {
     sM[wave][lane] = st.m;
     sL[wave][lane] = l;

@@ -71,6 +71,13 @@ __device__ __forceinline__ void frag_from(Frag<float>& f, const float* v) {
 // row of element i of a result tile
 __device__ __forceinline__ int row_of(int i, int half) { return 8 * (i >> 2) + 4 * half + (i & 3); }
 
+// The same number, but what is derived from it in a rarely taken branch is not
+// computed ahead of a loop and kept in registers there.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // A tile of rows of D elements in LDS.  A row is CPR 16-byte chunks; chunk c
 // of row r lies at position c ^ swz(r), so that neither sixteen rows' reads
 // of one chunk (frag) nor four rows' reads of four chunks (frag_t) meet in a
@@ -86,19 +93,35 @@ struct Tile {
     if constexpr (CPR == 8) return ((r >> 1) & 1) << 2 | ((r >> 2) & 3);
     return (r & 3) << 2 | ((r >> 2) & 3);
   }
-  // rows row0 .. row0 + ROWS of p (rows ld elements apart), row indices
-  // clamped to last; by NW waves, of which this is wave w
+  // Rows row0 .. row0 + ROWS of p (rows ld elements apart), row indices
+  // clamped to last; by NW waves, of which this is wave w.  The rows of one
+  // instruction are a multiple of 16 from those of the next, so their swizzle
+  // is the same: a whole tile takes one 32-bit lane offset (64 rows of less
+  // than 2^24 elements) and uniform bases.
   template <int ROWS, int NW>
   static __device__ __forceinline__ void load(T* lds, const T* p, int64_t ld, int row0, int last,
                                               int w, int lane) {
     static_assert(ROWS * CPR % (64 * NW) == 0, "whole waves");
+    constexpr int N = ROWS * CPR / (64 * NW), STEP = 64 * NW / CPR;
+    const int r0 = (w * 64 + lane) / CPR, c0 = ((w * 64 + lane) % CPR) ^ swz(r0);
+    if (STEP % 16 == 0 && row0 + ROWS - 1 <= last) {
+      const uint32_t off = (static_cast<uint32_t>(r0) * static_cast<uint32_t>(ld) + c0 * EPC) * sizeof(T);
+      const char* base = reinterpret_cast<const char*>(p + row0 * ld);
 #pragma unroll
-    for (int n = 0; n < ROWS * CPR / (64 * NW); ++n) {
-      const int base = (n * NW + w) * 64, pos = base + lane;
-      const int r = pos / CPR, c = (pos % CPR) ^ swz(r);
-      const T* src = p + static_cast<int64_t>(min(row0 + r, last)) * ld + c * EPC;
-      __builtin_amdgcn_global_load_lds((const M3_GLB void*)src, (M3_LDS void*)(lds + base * EPC), 16,
-                                       0, 0);
+      for (int n = 0; n < N; ++n) {
+        __builtin_amdgcn_global_load_lds((const M3_GLB void*)(base + off),
+                                         (M3_LDS void*)(lds + (n * NW + w) * 64 * EPC), 16, 0, 0);
+        base += STEP * ld * static_cast<int64_t>(sizeof(T));
+      }
+    } else {
+      lane = opaque(lane);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int pos = (n * NW + w) * 64 + lane, r = pos / CPR, c = (pos % CPR) ^ swz(r);
+        const T* src = p + static_cast<int64_t>(min(row0 + r, last)) * ld + c * EPC;
+        __builtin_amdgcn_global_load_lds((const M3_GLB void*)src,
+                                         (M3_LDS void*)(lds + (n * NW + w) * 64 * EPC), 16, 0, 0);
+      }
     }
   }
   // fragment kk (elements 16 kk ..) of rows row0 + lane % 32
@@ -182,7 +205,16 @@ __device__ __forceinline__ Slot slot_of(const int32_t* cu, int S, int T, int slo
   return tile < 0 ? Slot{-1, 0} : Slot{lo, tile};
 }
 
-__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32, 64); }
+// maximum and sum of lanes l and l ^ 32, in both.  The swap exchanges the
+// upper half of its first operand with the lower half of its second.
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
 
 // four consecutive elements of an output row
 __device__ __forceinline__ void put4(float* p, float a, float b, float c, float d) {

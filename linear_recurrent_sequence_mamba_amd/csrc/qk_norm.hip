@@ -37,20 +37,47 @@ struct RowIO {
     const int j = j0 + s;
     return MODE != kAdj && j < n ? j + n : 2 * j + 1;
   }
-  // a[s], b[s]: the members of pair s
-  __device__ __forceinline__ void load(const T* p, float* a, float* b) const {
-    if (MODE == kAdj || (MODE == kHalf4 && j0 >= n)) {
-      float v[8];
-      ld8(p, 2 * j0, v);
+  // A lane's pairs as loaded: eight consecutive elements, or twice four (kAny:
+  // the members one by one), turned into floats only where they are used.
+  struct Raw {
+    RawVec<T, MODE == kAdj ? 8 : 4> lo, hi;   // kAdj: lo alone
+    float a[MODE == kAny ? 4 : 1], b[MODE == kAny ? 4 : 1];
+  };
+  __device__ __forceinline__ void load(Raw& r, const T* p) const {
+    if constexpr (MODE == kAny) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) { a[s] = v[2 * s]; b[s] = v[2 * s + 1]; }
-    } else if (MODE == kHalf4) {
-      const f4 x = ld4(p, j0), y = ld4(p, j0 + n);
-#pragma unroll
-      for (int s = 0; s < 4; ++s) { a[s] = x[s]; b[s] = y[s]; }
+      for (int s = 0; s < 4; ++s) { r.a[s] = to_f32(p[first(s)]); r.b[s] = to_f32(p[second(s)]); }
+    } else if constexpr (MODE == kAdj) {
+      r.lo.load(p + 2 * j0);
     } else {
+      const bool split = j0 < n;
+      r.lo.load(p + (split ? j0 : 2 * j0));
+      r.hi.load(p + (split ? j0 + n : 2 * j0 + 4));
+    }
+  }
+  // a[s], b[s]: the members of pair s
+  __device__ __forceinline__ void get(const Raw& r, float* a, float* b) const {
+    if constexpr (MODE == kAny) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) { a[s] = to_f32(p[first(s)]); b[s] = to_f32(p[second(s)]); }
+      for (int s = 0; s < 4; ++s) { a[s] = r.a[s]; b[s] = r.b[s]; }
+    } else if constexpr (MODE == kAdj) {
+      float x[8];
+      r.lo.get(x);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) { a[s] = x[2 * s]; b[s] = x[2 * s + 1]; }
+    } else {
+      float x[4], y[4];
+      r.lo.get(x);
+      r.hi.get(y);
+      const bool split = j0 < n;
+      a[0] = x[0];
+      a[1] = split ? x[1] : x[2];
+      a[2] = split ? x[2] : y[0];
+      a[3] = split ? x[3] : y[2];
+      b[0] = split ? y[0] : x[1];
+      b[1] = split ? y[1] : x[3];
+      b[2] = split ? y[2] : y[1];
+      b[3] = y[3];
     }
   }
   static __device__ __forceinline__ uint32_t pack(float x, float y) {
@@ -95,14 +122,88 @@ __device__ __forceinline__ void turns(const double* f, int p, float* c, float* s
   }
 }
 
-// A wave takes a token and the part blockIdx.y of its heads; its lane groups
-// take rows h = group, group + 64 / G, ... of the part.
+// One tensor's rows g * ROWS + (lane group), g0 <= g < g1, of one token.
+// U groups' rows are on their way together; groups past the last head repeat
+// it without storing.
+template <typename T, int D, int MODE, bool BWD>
+struct Heads {
+  static constexpr int G = D / 8, ROWS = 64 / G, U = BWD ? 2 : 4;
+  using IO = RowIO<T, MODE>;
+  static __device__ __forceinline__ void run(const IO& io, int grp, int g0, int g1, int H,
+                                             const T* in, const T* gin, T* out, const float* w,
+                                             const float* c, const float* sn, float eps,
+                                             float* acc) {
+    for (int gb = g0; gb < g1; gb += U) {
+      typename IO::Raw rv[U], rg[BWD ? U : 1];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (gb + u >= g1) continue;
+        const int h = min((gb + u) * ROWS + grp, H - 1);
+        io.load(rv[u], in + h * D);
+        if constexpr (BWD) io.load(rg[u], gin + h * D);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (gb + u >= g1) continue;
+        const int h = (gb + u) * ROWS + grp;
+        const bool on = h < H;
+        float x[4], y[4];
+        io.get(rv[u], x, y);
+        float ss = 0.0f;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) ss = fmaf(x[s], x[s], fmaf(y[s], y[s], ss));
+        ss = group_sum<G>(ss);
+        const float inv = __builtin_amdgcn_rsqf(fmaf(ss, 1.0f / D, eps));   // 1 ulp
+        if constexpr (!BWD) {
+          float ox[4], oy[4];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const float zx = x[s] * inv * w[s], zy = y[s] * inv * w[4 + s];
+            ox[s] = fmaf(zx, c[s], -zy * sn[s]);
+            oy[s] = fmaf(zx, sn[s], zy * c[s]);
+          }
+          if (on) io.store(out + h * D, ox, oy);
+        } else {
+          float gx[4], gy[4];
+          io.get(rg[u], gx, gy);
+          float dot = 0.0f, px[4], py[4];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            const float ux = x[s] * inv, uy = y[s] * inv;
+            const float rx = fmaf(gx[s], c[s], gy[s] * sn[s]);
+            const float ry = fmaf(gy[s], c[s], -gx[s] * sn[s]);
+            if (on) {
+              acc[s] = fmaf(rx, ux, acc[s]);
+              acc[4 + s] = fmaf(ry, uy, acc[4 + s]);
+            }
+            px[s] = rx * w[s];
+            py[s] = ry * w[4 + s];
+            dot = fmaf(px[s], ux, fmaf(py[s], uy, dot));
+            x[s] = ux;
+            y[s] = uy;
+          }
+          dot = group_sum<G>(dot) * (1.0f / D);
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            px[s] = inv * fmaf(-x[s], dot, px[s]);
+            py[s] = inv * fmaf(-y[s], dot, py[s]);
+          }
+          if (on) io.store(out + h * D, px, py);
+        }
+      }
+    }
+  }
+};
+
+// A wave takes tokens, and of each the part blockIdx.y of the groups of heads
+// (q's first, then k's).
 template <typename T, int D, int MODE, bool BWD>
 __global__ __launch_bounds__(256) void k_qk_norm(QkNormArgs a) {
-  constexpr int G = D / 8, ROWS = 64 / G;
+  using K = Heads<T, D, MODE, BWD>;
+  constexpr int G = K::G, ROWS = K::ROWS;
   const int lane = threadIdx.x & 63, l = lane % G, grp = lane / G;
   const int n = a.rot / 2;
-  const RowIO<T, MODE> io(l, n);
+  const typename K::IO io(l, n);
   float wq[8], wk[8];
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
@@ -119,72 +220,21 @@ __global__ __launch_bounds__(256) void k_qk_norm(QkNormArgs a) {
 #pragma unroll
     for (int s = 0; s < 8; ++s) accq[s] = acck[s] = 0.0f;
 
-  const int H = a.Hq + a.Hk;
-  const int per = (H + a.split - 1) / a.split;
-  const int h0 = static_cast<int>(blockIdx.y) * per, h1 = min(h0 + per, H);
+  const int nq = (a.Hq + ROWS - 1) / ROWS, nk = (a.Hk + ROWS - 1) / ROWS;
+  const int per = (nq + nk + a.split - 1) / a.split;
+  const int g0 = static_cast<int>(blockIdx.y) * per, g1 = min(g0 + per, nq + nk);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int tt = blockIdx.x * 4 + wave; tt < a.T; tt += gridDim.x * 4) {
     const int64_t t = tt;
     float c[4], sn[4];
     turns(f, a.pos[t], c, sn);
-    for (int hb = h0; hb < h1; hb += ROWS) {
-      const int hr = hb + grp;
-      const bool on = hr < h1;
-      const int h = on ? hr : h1 - 1;   // idle groups repeat the last row
-      const bool isq = h < a.Hq;
-      const int hh = isq ? h : h - a.Hq;
-      const T* p = isq ? static_cast<const T*>(a.q) + t * a.ldq : static_cast<const T*>(a.k) + t * a.ldk;
-      float x[4], y[4];
-      io.load(p + hh * D, x, y);
-      float ss = 0.0f;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) ss = fmaf(x[s], x[s], fmaf(y[s], y[s], ss));
-      ss = group_sum<G>(ss);
-      const float inv = __builtin_amdgcn_rsqf(fmaf(ss, 1.0f / D, a.eps));   // 1 ulp
-      const int64_t ro = (t * (isq ? a.Hq : a.Hk) + hh) * D;
-      if constexpr (!BWD) {
-        float ox[4], oy[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const float zx = x[s] * inv * (isq ? wq[s] : wk[s]);
-          const float zy = y[s] * inv * (isq ? wq[4 + s] : wk[4 + s]);
-          ox[s] = fmaf(zx, c[s], -zy * sn[s]);
-          oy[s] = fmaf(zx, sn[s], zy * c[s]);
-        }
-        if (on) io.store((isq ? static_cast<T*>(a.qo) : static_cast<T*>(a.ko)) + ro, ox, oy);
-      } else {
-        float gx[4], gy[4];
-        io.load((isq ? static_cast<const T*>(a.gq) : static_cast<const T*>(a.gk)) + ro, gx, gy);
-        float dot = 0.0f, px[4], py[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const float ux = x[s] * inv, uy = y[s] * inv;
-          const float rx = fmaf(gx[s], c[s], gy[s] * sn[s]);
-          const float ry = fmaf(gy[s], c[s], -gx[s] * sn[s]);
-          if (on && isq) {
-            accq[s] = fmaf(rx, ux, accq[s]);
-            accq[4 + s] = fmaf(ry, uy, accq[4 + s]);
-          }
-          if (on && !isq) {
-            acck[s] = fmaf(rx, ux, acck[s]);
-            acck[4 + s] = fmaf(ry, uy, acck[4 + s]);
-          }
-          px[s] = rx * (isq ? wq[s] : wk[s]);
-          py[s] = ry * (isq ? wq[4 + s] : wk[4 + s]);
-          dot = fmaf(px[s], ux, fmaf(py[s], uy, dot));
-          x[s] = ux;
-          y[s] = uy;
-        }
-        dot = group_sum<G>(dot) * (1.0f / D);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          px[s] = inv * fmaf(-x[s], dot, px[s]);
-          py[s] = inv * fmaf(-y[s], dot, py[s]);
-        }
-        T* o = isq ? static_cast<T*>(a.dq) + t * a.ld_dq : static_cast<T*>(a.dk) + t * a.ld_dk;
-        if (on) io.store(o + hh * D, px, py);
-      }
-    }
+    const int64_t oq = t * a.Hq * D, ok = t * a.Hk * D;
+    K::run(io, grp, g0, min(g1, nq), a.Hq, static_cast<const T*>(a.q) + t * a.ldq,
+           static_cast<const T*>(a.gq) + oq,
+           BWD ? static_cast<T*>(a.dq) + t * a.ld_dq : static_cast<T*>(a.qo) + oq, wq, c, sn, a.eps, accq);
+    K::run(io, grp, max(g0 - nq, 0), g1 - nq, a.Hk, static_cast<const T*>(a.k) + t * a.ldk,
+           static_cast<const T*>(a.gk) + ok,
+           BWD ? static_cast<T*>(a.dk) + t * a.ld_dk : static_cast<T*>(a.ko) + ok, wk, c, sn, a.eps, acck);
   }
   if constexpr (BWD) {
     // sums over the lane groups and the four waves, in a fixed order
@@ -228,13 +278,18 @@ __global__ __launch_bounds__(1024) void k_qk_norm_dw(QkNormArgs a, int nblocks) 
   }
 }
 
-constexpr int kFwdBlocks = 4096, kBwdBlocks = 1024;
+// Workgroups of four waves: as many as are resident together, so that a wave
+// reads the weights once for several tokens (16384 tokens of 18 heads of 128:
+// 31 us; with one token a wave, 4096 workgroups, 42 us).  The gradients' grid
+// also sets how many parts the weights' sums have.
+constexpr int kFwdBlocks = 2048, kBwdBlocks = 1024;
 
-// waves per token: enough units for every SIMD of the chip where tokens are
-// few, one wave for all heads of a token (one set of cosines) where not
-int split_of(int T, int H, int D) {
+// Waves that share a token's heads: enough of them for every SIMD of the chip
+// where tokens are few, one wave for all heads of a token (one set of cosines)
+// where not.
+int split_of(int T, int Hq, int Hk, int D) {
   const int rows = 64 / (D / 8);
-  const int most = (H + rows - 1) / rows;
+  const int most = (Hq + rows - 1) / rows + (Hk + rows - 1) / rows;
   int s = (4096 + T - 1) / T;
   if (s > most) s = most;
   return s > 512 ? 512 : s;
@@ -269,12 +324,12 @@ void run_type(const QkNormArgs& a, dim3 grid, hipStream_t s) {
 bool qk_norm_supported(int D) { return D == 32 || D == 64 || D == 128 || D == 256; }
 
 size_t qk_norm_workspace_bytes(int T, int Hq, int Hk, int D) {
-  const dim3 g = grid_of(T, split_of(T, Hq + Hk, D), kBwdBlocks);
+  const dim3 g = grid_of(T, split_of(T, Hq, Hk, D), kBwdBlocks);
   return sizeof(float) * 2 * D * g.x * g.y;
 }
 
 hipError_t launch_qk_norm(QkNormArgs& a, int bf16, hipStream_t s) {
-  a.split = split_of(a.T, a.Hq + a.Hk, a.D);
+  a.split = split_of(a.T, a.Hq, a.Hk, a.D);
   const dim3 grid = grid_of(a.T, a.split, kFwdBlocks);
   if (bf16) run_type<bf16_t, false>(a, grid, s);
   else run_type<float, false>(a, grid, s);
@@ -282,7 +337,7 @@ hipError_t launch_qk_norm(QkNormArgs& a, int bf16, hipStream_t s) {
 }
 
 hipError_t launch_qk_norm_backward(QkNormArgs& a, int bf16, hipStream_t s) {
-  a.split = split_of(a.T, a.Hq + a.Hk, a.D);
+  a.split = split_of(a.T, a.Hq, a.Hk, a.D);
   const dim3 grid = grid_of(a.T, a.split, kBwdBlocks);
   if (bf16) run_type<bf16_t, true>(a, grid, s);
   else run_type<float, true>(a, grid, s);

@@ -282,12 +282,13 @@ m3_status check_attn(const m3_attn_dims* d, bool decode) {
   if (!m3::attn_supported(d->headdim)) return M3_ERR_UNSUPPORTED;
   const int64_t wq = static_cast<int64_t>(d->nheads_q) * d->headdim;
   const int64_t wk = static_cast<int64_t>(d->nheads_k) * d->headdim;
-  if (wq > 0x3fffffff) return M3_ERR_SHAPE;
   const int64_t lq[] = {d->ld_q, d->ld_o, d->ld_do}, lk[] = {d->ld_k, d->ld_v};
+  const int64_t most = int64_t{1} << 24;   // a tile's rows are 32-bit offsets apart
+  if (wq >= most) return M3_ERR_SHAPE;
   for (int64_t ld : lq)
-    if (ld != 0 && ld < wq) return M3_ERR_SHAPE;
+    if (ld != 0 && (ld < wq || ld >= most)) return M3_ERR_SHAPE;
   for (int64_t ld : lk)
-    if (ld != 0 && ld < wk) return M3_ERR_SHAPE;
+    if (ld != 0 && (ld < wk || ld >= most)) return M3_ERR_SHAPE;
   if (d->stride_k < 0 || d->stride_v < 0) return M3_ERR_SHAPE;
   if ((d->ld_q | d->ld_o | d->ld_do | d->ld_k | d->ld_v | d->stride_k | d->stride_v) % 8)
     return M3_ERR_ALIGN;

@@ -37,13 +37,15 @@ __device__ __forceinline__ bool special(bf16_t v) { return (v.bits & 0x7f80u) ==
 __device__ __forceinline__ bool special(float v) {
   return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u;
 }
-template <typename T, int D, int ROWS, int THREADS>
-__device__ __forceinline__ bool drop_special(T* V) {
+template <typename T, int D, int THREADS>
+__device__ __forceinline__ bool drop_special(char* V) {
+  using L = Tile<T, D>;
   bool found = false;
   const int tid = opaque(threadIdx.x);
 #pragma unroll 1
-  for (int n = 0; n < ROWS * D * static_cast<int>(sizeof(T)) / 16 / THREADS; ++n) {
-    uint4* p = reinterpret_cast<uint4*>(V) + n * THREADS + tid;
+  for (int n = 0; n < 64 * L::NG / THREADS; ++n) {
+    const int at = n * THREADS + tid;
+    uint4* p = reinterpret_cast<uint4*>(V + L::place(at / 64) + 16 * (at % 64));
     uint4 u = *p;
     uint32_t w[4] = {u.x, u.y, u.z, u.w};
     bool bad = false;
@@ -67,7 +69,7 @@ __device__ __forceinline__ bool drop_special(T* V) {
 
 // Scores of 32 queries against NB x 32 keys
 template <typename T, int D, int NB>
-__device__ __forceinline__ void score(f16v* s, const Frag<T>* q, const T* K, int lane) {
+__device__ __forceinline__ void score(f16v* s, const Frag<T>* q, const char* K, int lane) {
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     s[b] = f16v{};
@@ -87,16 +89,21 @@ __device__ __forceinline__ void hide(f16v* s, int seen, int lane) {
       s[b][i] = 32 * b + row_of(i, 0) < seen ? s[b][i] : -INFINITY;
 }
 
-// The maximum that the weights are taken against.  It moves only when it has
-// to: weights up to 2^8 lose nothing in fp32 sums or bf16 products, and most
-// tiles then leave o as it is.
-template <int D, int NB>
-__device__ __forceinline__ void raise_max(Rows<D>& st, const f16v* s, float c) {
+template <int NB>
+__device__ __forceinline__ float max_of(const f16v* s) {
   float mx = s[0][0];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[b][i]);
+  return mx;
+}
+
+// The maximum that the weights are taken against, from the tile's (this
+// lane's keys).  It moves only when it has to: weights up to 2^8 lose nothing
+// in fp32 sums or bf16 products, and most tiles then leave o as it is.
+template <int D>
+__device__ __forceinline__ void raise_max(Rows<D>& st, float mx, float c) {
   mx = half_max(mx) * c;
   if (__ballot(mx > st.m + 8.0f)) {
     const float m = fmaxf(st.m, mx);
@@ -111,8 +118,8 @@ __device__ __forceinline__ void raise_max(Rows<D>& st, const f16v* s, float c) {
 }
 
 // Weights of a tile's scores, added to the sums
-template <typename T, int D, int NB>
-__device__ __forceinline__ void weigh(Rows<D>& st, f16v* s, const T* V, float c, int lane) {
+template <typename T, int D, int NB, int ROW0 = 0>
+__device__ __forceinline__ void weigh(Rows<D>& st, f16v* s, const char* V, float c, int lane) {
   const float m0 = st.m == -INFINITY ? 0.0f : st.m;
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
@@ -130,7 +137,7 @@ __device__ __forceinline__ void weigh(Rows<D>& st, f16v* s, const T* V, float c,
       frag_from(p, e8);
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
-        st.o[d] = mma(Tile<T, D>::frag_t(V, 32 * b + 16 * w, 32 * d, lane), p, st.o[d]);
+        st.o[d] = mma(Tile<T, D>::frag_t(V, ROW0 + 32 * b + 16 * w, 32 * d, lane), p, st.o[d]);
     }
   }
 }
@@ -139,10 +146,11 @@ __device__ __forceinline__ void weigh(Rows<D>& st, f16v* s, const T* V, float c,
 // nothing here, so the matrix cores work while the exponentials run.  The
 // instructions are laid out step by step, each with one product (first those
 // of the next scores, then those with V), its share of the exponentials, and
-// the operand of the product two steps on, read from LDS.
+// the operand of the product two steps on, read from LDS.  Returns the maximum
+// of the next scores, taken while the products with V run.
 template <typename T, int D, int NB>
-__device__ __forceinline__ void weigh_ahead(Rows<D>& st, f16v* s, f16v* next, const Frag<T>* q,
-                                            const T* Knext, const T* V, float c, int lane) {
+__device__ __forceinline__ float weigh_ahead(Rows<D>& st, f16v* s, f16v* next, const Frag<T>* q,
+                                            const char* Knext, const char* V, float c, int lane) {
   using L = Tile<T, D>;
   constexpr int NM = NB * D / 16;          // products of each kind
   constexpr int F = 2 * NB, E = 16 * NB;   // fragments of weights, elements
@@ -155,6 +163,7 @@ __device__ __forceinline__ void weigh_ahead(Rows<D>& st, f16v* s, f16v* next, co
   };
 #pragma unroll
   for (int b = 0; b < NB; ++b) next[b] = f16v{};
+  float mx = -INFINITY;
   Frag<T> op[3], p[F];
   op[0] = operand(0);
   op[1] = operand(1);
@@ -174,6 +183,7 @@ __device__ __forceinline__ void weigh_ahead(Rows<D>& st, f16v* s, f16v* next, co
       const float v = __builtin_amdgcn_exp2f(fmaf(s[e / 16][e % 16], c, -m0));
       s[e / 16][e % 16] = v;
       st.l += v;
+      asm volatile("" : "+v"(st.l));   // added here, not after the loop
       if (e % 8 == 7) {
         float e8[8];
 #pragma unroll
@@ -181,29 +191,37 @@ __device__ __forceinline__ void weigh_ahead(Rows<D>& st, f16v* s, f16v* next, co
         frag_from(p[e / 8], e8);
       }
     }
+    // the last quarter of the next scores is still on its way at step NM
+    constexpr int M0 = NM + 3, MS = 2 * NM - M0;
+    if (n == M0) mx = next[0][0];
+#pragma unroll
+    for (int e = 1; e < E; ++e)
+      if (M0 + e * MS / E == n) mx = fmaxf(mx, next[e / 16][e % 16]);
+    if (n >= M0) asm volatile("" : "+v"(mx));
     __builtin_amdgcn_sched_barrier(0);
   }
+  return mx;
 }
 
-// One tile by itself
-template <typename T, int D, int NB, bool MASK>
-__device__ __forceinline__ void attend(Rows<D>& st, const Frag<T>* q, const T* K, const T* V,
-                                       float c, int seen, int lane) {
-  f16v s[NB];
-  score<T, D, NB>(s, q, K, lane);
-  if (MASK) hide<NB>(s, seen, lane);
-  raise_max<D, NB>(st, s, c);
-  weigh<T, D, NB>(st, s, V, c, lane);
+// 32 keys (rows 0 .. 31 of a tile) and their values (rows 32 .. 63)
+template <typename T, int D, bool MASK>
+__device__ __forceinline__ void attend(Rows<D>& st, const Frag<T>* q, const char* KV, float c,
+                                       int seen, int lane) {
+  f16v s[1];
+  score<T, D, 1>(s, q, KV, lane);
+  if (MASK) hide<1>(s, seen, lane);
+  raise_max<D>(st, max_of<1>(s), c);
+  weigh<T, D, 1, 32>(st, s, KV, c, lane);
 }
 
 // ---------------------------------------------------------------------------
 // The prompt: a workgroup takes 32 WAVES queries of one head; K and V tiles
 // of BN keys are double-buffered in LDS.
-template <typename T, int D, int BN, int WAVES>
+template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn(AttnArgs a) {
   using L = Tile<T, D>;
-  constexpr int BM = 32 * WAVES, NB = BN / 32;
-  __shared__ __align__(16) T sK[2][BN * D], sV[2][BN * D];
+  constexpr int BM = 32 * WAVES, BN = 64, NB = 2;
+  __shared__ __align__(16) char sK[2][L::BYTES], sV[2][L::BYTES];
   __shared__ int sSpecial;
   if (threadIdx.x == 0) sSpecial = 0;   // read after the tiles' barriers
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -250,35 +268,36 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   auto arrive = [&](int t) __attribute__((always_inline)) {
     lds_loads_done();
     __syncthreads();   // V of t and K of t + 1 are there; every wave is done with t - 1
-    if (t + 2 < ntile) L::template load<BN, WAVES>(sK[t & 1], kp, a.ldk, (t + 2) * BN, Lk - 1, wave, lane);
-    if (t + 1 < ntile) L::template load<BN, WAVES>(sV[(t + 1) & 1], vp, a.ldv, (t + 1) * BN, Lk - 1, wave, lane);
+    if (t + 2 < ntile) L::template load<WAVES>(sK[t & 1], kp, a.ldk, (t + 2) * BN, Lk - 1, wave, lane);
+    if (t + 1 < ntile) L::template load<WAVES>(sV[(t + 1) & 1], vp, a.ldv, (t + 1) * BN, Lk - 1, wave, lane);
   };
   if (ntile > 0) {
-    L::template load<BN, WAVES>(sK[0], kp, a.ldk, 0, Lk - 1, wave, lane);
+    L::template load<WAVES>(sK[0], kp, a.ldk, 0, Lk - 1, wave, lane);
     lds_loads_done();
     __syncthreads();
-    L::template load<BN, WAVES>(sV[0], vp, a.ldv, 0, Lk - 1, wave, lane);
-    if (ntile > 1) L::template load<BN, WAVES>(sK[1], kp, a.ldk, BN, Lk - 1, wave, lane);
+    L::template load<WAVES>(sV[0], vp, a.ldv, 0, Lk - 1, wave, lane);
+    if (ntile > 1) L::template load<WAVES>(sK[1], kp, a.ldk, BN, Lk - 1, wave, lane);
     score<T, D, NB>(s, q, sK[0], lane);
   }
+  float mx = npipe > 0 ? max_of<NB>(s) : 0.0f;
   for (int t = 0; t < npipe; t += 2) {
     arrive(t);
-    raise_max<D, NB>(st, s, c);
-    weigh_ahead<T, D, NB>(st, s, next, q, sK[1], sV[0], c, lane);
+    raise_max<D>(st, mx, c);
+    mx = weigh_ahead<T, D, NB>(st, s, next, q, sK[1], sV[0], c, lane);
     arrive(t + 1);
-    raise_max<D, NB>(st, next, c);
-    weigh_ahead<T, D, NB>(st, next, s, q, sK[0], sV[1], c, lane);
+    raise_max<D>(st, mx, c);
+    mx = weigh_ahead<T, D, NB>(st, next, s, q, sK[0], sV[1], c, lane);
   }
 #pragma unroll 1
   for (int t = npipe; t < ntile; ++t) {
     arrive(t);
     if (t >= tmask) {
-      if (drop_special<T, D, BN, 64 * WAVES>(sV[t & 1])) sSpecial = 1;
+      if (drop_special<T, D, 64 * WAVES>(sV[t & 1])) sSpecial = 1;
       __syncthreads();
     }
     if (t >= nw) continue;
     hide<NB>(s, sees - t * BN, lane);
-    raise_max<D, NB>(st, s, c);
+    raise_max<D>(st, max_of<NB>(s), c);
     weigh<T, D, NB>(st, s, sV[t & 1], c, lane);
     if (t + 1 < nw) score<T, D, NB>(s, q, sK[(t + 1) & 1], lane);
   }
@@ -317,8 +336,8 @@ template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
   using L = Tile<T, D>;
   constexpr int BN = 32;
-  // a wave's two K and two V tiles; afterwards its o [32][D] in fp32
-  __shared__ __align__(16) T sKV[WAVES][2][2][BN * D];
+  // a wave's two tiles (32 rows of K, 32 of V); afterwards its o [32][D] in fp32
+  __shared__ __align__(16) char sKV[WAVES][2][L::BYTES];
   __shared__ float sM[WAVES][32], sL[WAVES][32];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, g = a.Hq / a.Hk, ng = (g + 31) / 32;
@@ -348,21 +367,19 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
   const T* vp = static_cast<const T*>(a.v) + s * a.bv + hk * D;
   int t = t0 + wave;
   if (t < t1) {
-    L::template load<BN, 1>(sKV[wave][0][0], kp, a.ldk, t * BN, len - 1, 0, lane);
-    L::template load<BN, 1>(sKV[wave][0][1], vp, a.ldv, t * BN, len - 1, 0, lane);
+    L::template load2<1>(sKV[wave][0], kp, a.ldk, vp, a.ldv, t * BN, len - 1, 0, lane);
   }
   for (int u = 0; t < t1; t += WAVES, ++u) {
     lds_loads_done();
     if (t + WAVES < t1) {
-      L::template load<BN, 1>(sKV[wave][(u + 1) & 1][0], kp, a.ldk, (t + WAVES) * BN, len - 1, 0, lane);
-      L::template load<BN, 1>(sKV[wave][(u + 1) & 1][1], vp, a.ldv, (t + WAVES) * BN, len - 1, 0, lane);
+      L::template load2<1>(sKV[wave][(u + 1) & 1], kp, a.ldk, vp, a.ldv, (t + WAVES) * BN, len - 1, 0, lane);
     }
-    const T *K = sKV[wave][u & 1][0], *V = sKV[wave][u & 1][1];
+    const char* KV = sKV[wave][u & 1];
     // rows past the end repeat the last one, which every query sees
     if ((t + 1) * BN <= len)
-      attend<T, D, 1, false>(st, q, K, V, c, BN, lane);
+      attend<T, D, false>(st, q, KV, c, BN, lane);
     else
-      attend<T, D, 1, true>(st, q, K, V, c, len - t * BN, lane);
+      attend<T, D, true>(st, q, KV, c, len - t * BN, lane);
   }
   const float l = half_sum(st.l);
   if (half == 0) {
@@ -370,8 +387,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
     sL[wave][lane] = l;
   }
   // o of this wave, over its own tiles (of which it is done reading)
-  static_assert(sizeof(T) * 4 * BN * D >= sizeof(float) * 32 * D, "room for o");
-  float* so = reinterpret_cast<float*>(&sKV[wave][0][0][0]);
+  static_assert(2 * L::BYTES >= static_cast<int>(sizeof(float)) * 32 * D, "room for o");
+  float* so = reinterpret_cast<float*>(&sKV[wave][0][0]);
 #pragma unroll
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -392,7 +409,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
       // a wave that saw no key has l = 0 and o = 0
       if (lw != 0.0f) {
         ls = fmaf(f, lw, ls);
-        const f4 ow = *reinterpret_cast<const f4*>(reinterpret_cast<const float*>(&sKV[w][0][0][0]) + r * D + d);
+        const f4 ow = *reinterpret_cast<const f4*>(reinterpret_cast<const float*>(&sKV[w][0][0]) + r * D + d);
         v.x = fmaf(f, ow.x, v.x);
         v.y = fmaf(f, ow.y, v.y);
         v.z = fmaf(f, ow.z, v.z);
@@ -461,11 +478,11 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   if (dl == 0 && a.lse) a.lse[n] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2A;
 }
 
-template <typename T, int D, int BN>
+template <typename T, int D>
 hipError_t run_attn(const AttnArgs& a, hipStream_t s) {
   constexpr int BM = 128;
   const int64_t slots = a.Tq / BM + a.S;
-  k_attn<T, D, BN, BM / 32><<<static_cast<unsigned>(slots * a.Hq), 2 * BM, 0, s>>>(a);
+  k_attn<T, D, BM / 32><<<static_cast<unsigned>(slots * a.Hq), 2 * BM, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -495,8 +512,8 @@ int decode_parts(int S, int cap, int Hq, int Hk) {
 bool attn_supported(int D) { return D == 64 || D == 128; }
 
 hipError_t launch_attn(AttnArgs& a, int bf16, hipStream_t s) {
-  if (bf16) return a.D == 64 ? run_attn<bf16_t, 64, 64>(a, s) : run_attn<bf16_t, 128, 64>(a, s);
-  return a.D == 64 ? run_attn<float, 64, 32>(a, s) : run_attn<float, 128, 32>(a, s);
+  if (bf16) return a.D == 64 ? run_attn<bf16_t, 64>(a, s) : run_attn<bf16_t, 128>(a, s);
+  return a.D == 64 ? run_attn<float, 64>(a, s) : run_attn<float, 128>(a, s);
 }
 
 size_t attn_decode_workspace_bytes(int S, int cap, int Hq, int Hk, int D) {

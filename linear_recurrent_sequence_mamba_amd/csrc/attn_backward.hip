@@ -42,7 +42,7 @@ template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn_dq(AttnArgs a) {
   using L = Tile<T, D>;
   constexpr int BM = 32 * WAVES, BN = 32;
-  __shared__ __align__(16) T sK[2][BN * D], sV[2][BN * D];
+  __shared__ __align__(16) char sKV[2][L::BYTES];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nslot = gridDim.x / a.Hq;
   const int h = blockIdx.x % a.Hq;
@@ -79,24 +79,22 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   const T* kp = static_cast<const T*>(a.k) + static_cast<int64_t>(k0) * a.ldk + hk * D;
   const T* vp = static_cast<const T*>(a.v) + static_cast<int64_t>(k0) * a.ldv + hk * D;
   if (ntile > 0) {
-    L::template load<BN, WAVES>(sK[0], kp, a.ldk, 0, Lk - 1, wave, lane);
-    L::template load<BN, WAVES>(sV[0], vp, a.ldv, 0, Lk - 1, wave, lane);
+    L::template load2<WAVES>(sKV[0], kp, a.ldk, vp, a.ldv, 0, Lk - 1, wave, lane);
   }
   for (int t = 0; t < ntile; ++t) {
     lds_loads_done();
     __syncthreads();
     if (t + 1 < ntile) {
-      L::template load<BN, WAVES>(sK[(t + 1) & 1], kp, a.ldk, (t + 1) * BN, Lk - 1, wave, lane);
-      L::template load<BN, WAVES>(sV[(t + 1) & 1], vp, a.ldv, (t + 1) * BN, Lk - 1, wave, lane);
+      L::template load2<WAVES>(sKV[(t + 1) & 1], kp, a.ldk, vp, a.ldv, (t + 1) * BN, Lk - 1, wave, lane);
     }
     const int j0 = t * BN;
     if (j0 >= wmost) continue;
-    const T *K = sK[t & 1], *V = sV[t & 1];
+    const char* KV = sKV[t & 1];
     f16v s = f16v{}, dp = f16v{};
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      s = mma(L::frag(K, 0, kk, lane), q[kk], s);
-      dp = mma(L::frag(V, 0, kk, lane), g[kk], dp);
+      s = mma(L::frag(KV, 0, kk, lane), q[kk], s);
+      dp = mma(L::frag(KV, 32, kk, lane), g[kk], dp);
     }
     float ds[16];
 #pragma unroll
@@ -109,7 +107,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
       Frag<T> f;
       frag_from(f, ds + 8 * w);
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) dq[d] = mma(L::frag_t(K, 16 * w, 32 * d, lane), f, dq[d]);
+      for (int d = 0; d < D / 32; ++d) dq[d] = mma(L::frag_t(KV, 16 * w, 32 * d, lane), f, dq[d]);
     }
   }
   if (i >= Lq) return;
@@ -128,7 +126,7 @@ template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 1) void k_attn_dkv(AttnArgs a) {
   using L = Tile<T, D>;
   constexpr int BK = 32 * WAVES, BQ = 32;
-  __shared__ __align__(16) T sQ[2][BQ * D], sG[2][BQ * D];
+  __shared__ __align__(16) char sQG[2][L::BYTES];
   __shared__ __align__(16) float sL[2][BQ], sD[2][BQ];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int per = a.Hk * a.gsplit;
@@ -166,8 +164,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_attn_dkv(AttnArgs a) {
     const int h = hk * grp + part * gper + n / nt, i0 = (first + n % nt) * BQ;
     const T* qp = static_cast<const T*>(a.q) + static_cast<int64_t>(q0) * a.ldq + h * D;
     const T* gp = static_cast<const T*>(a.dout) + static_cast<int64_t>(q0) * a.lddo + h * D;
-    L::template load<BQ, WAVES>(sQ[buf], qp, a.ldq, i0, Lq - 1, wave, lane);
-    L::template load<BQ, WAVES>(sG[buf], gp, a.lddo, i0, Lq - 1, wave, lane);
+    L::template load2<WAVES>(sQG[buf], qp, a.ldq, gp, a.lddo, i0, Lq - 1, wave, lane);
     if (threadIdx.x < BQ) {
       const int i = i0 + threadIdx.x;
       const float2 st = a.stat[static_cast<int64_t>(h) * a.Tq + q0 + min(i, Lq - 1)];
@@ -184,12 +181,12 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_attn_dkv(AttnArgs a) {
     if (n + 1 < all) fetch(n + 1, buf ^ 1);
     const int i0 = (first + n % nt) * BQ;
     if (i0 + BQ <= wfirst) continue;
-    const T *Q = sQ[buf], *G = sG[buf];
+    const char* QG = sQG[buf];
     f16v s = f16v{}, dp = f16v{};
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      s = mma(L::frag(Q, 0, kk, lane), k[kk], s);
-      dp = mma(L::frag(G, 0, kk, lane), v[kk], dp);
+      s = mma(L::frag(QG, 0, kk, lane), k[kk], s);
+      dp = mma(L::frag(QG, 32, kk, lane), v[kk], dp);
     }
     float p[16], ds[16];
 #pragma unroll
@@ -212,8 +209,8 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_attn_dkv(AttnArgs a) {
       frag_from(fd, ds + 8 * w);
 #pragma unroll
       for (int d = 0; d < D / 32; ++d) {
-        dv[d] = mma(L::frag_t(G, 16 * w, 32 * d, lane), fp, dv[d]);
-        dk[d] = mma(L::frag_t(Q, 16 * w, 32 * d, lane), fd, dk[d]);
+        dv[d] = mma(L::frag_t(QG, 32 + 16 * w, 32 * d, lane), fp, dv[d]);
+        dk[d] = mma(L::frag_t(QG, 16 * w, 32 * d, lane), fd, dk[d]);
       }
     }
   }

@@ -78,97 +78,125 @@ __device__ __forceinline__ int opaque(int v) {
   return v;
 }
 
-// A tile of rows of D elements in LDS.  A row is CPR 16-byte chunks; chunk c
-// of row r lies at position c ^ swz(r), so that neither sixteen rows' reads
-// of one chunk (frag) nor four rows' reads of four chunks (frag_t) meet in a
-// bank.  Rows arrive by loads that go straight to LDS: a wave's 64 lanes fill
-// 64 consecutive positions, and the permutation is in the address each lane
-// reads from.
+// 64 rows of D elements in LDS (or twice 32 from two arrays).  Rows arrive by
+// loads that go straight to LDS, where a wave's 64 lanes fill 1024 consecutive
+// bytes; which rows those are, and where the 1024 bytes lie, is free.  Both
+// are chosen so that neither sixteen rows' reads of one 16-byte chunk (frag)
+// nor four rows' reads of 64 bytes (frag_t) meet in a bank: row r lies at
+// 64 (r % 4) + 16 (r / 4 % 4) modulo the 256 bytes of all banks.  And since a
+// row's place is a sum of terms of its index, every fragment is one lane
+// address plus a constant (a permutation by exclusive or, as bank-free, costs
+// an instruction for each fragment).
 template <typename T, int D>
 struct Tile {
+  static constexpr int RB = D * sizeof(T);     // bytes of a row: 128, 256 or 512
+  static constexpr int RPI = 1024 / RB;        // rows of one load instruction
+  static constexpr int CPR = RB / 16;          // chunks of a row
+  static constexpr int NG = 64 / RPI;          // load instructions of a tile
   static constexpr int EPC = 16 / sizeof(T);
-  static constexpr int CPR = D / EPC;
-  static constexpr int ROW = D;   // elements
-  static __device__ __forceinline__ int swz(int r) {
-    if constexpr (CPR == 8) return ((r >> 1) & 1) << 2 | ((r >> 2) & 3);
-    return (r & 3) << 2 | ((r >> 2) & 3);
+  static constexpr int G1 = 1088;              // 64 bytes on
+  static constexpr int G4 = RB == 128 ? 2320 : 4368;   // 16 bytes on
+  static constexpr int HALF = 4 * 4368;        // 512-byte rows: from row 32 on
+  static constexpr int BYTES = RB == 128 ? 4 * 2320 : RB == 256 ? 4 * 4368 : 2 * HALF;
+
+  // load instruction g: where its bytes go, and its row beyond the lane's
+  static __device__ __forceinline__ constexpr int place(int g) {
+    return RB == 128 ? (g >> 1) * G4 + (g & 1) * G1
+                     : (g >> 4) * HALF + ((g >> 2) & 3) * G4 + (g & 3) * G1;
   }
-  // Rows row0 .. row0 + ROWS of p (rows ld elements apart), row indices
-  // clamped to last; by NW waves, of which this is wave w.  The rows of one
-  // instruction are a multiple of 16 from those of the next, so their swizzle
-  // is the same: a whole tile takes one 32-bit lane offset (64 rows of less
-  // than 2^24 elements) and uniform bases.
-  template <int ROWS, int NW>
-  static __device__ __forceinline__ void load(T* lds, const T* p, int64_t ld, int row0, int last,
+  static __device__ __forceinline__ constexpr int group_row(int g) {
+    return RB == 128 ? 4 * (g >> 1) + 2 * (g & 1) : (g & 15) + 32 * (g >> 4);
+  }
+  static __device__ __forceinline__ int lane_row(int lane) {
+    const int j = lane / CPR;
+    return RB == 128 ? (j & 1) + 16 * (j >> 1) : 16 * j;
+  }
+
+  // Rows row0 .. row0 + 63 of p (rows ld elements apart), row indices clamped
+  // to last; by NW waves, of which this is wave w.  A whole tile takes one
+  // 32-bit lane offset (64 rows of less than 2^24 elements) and uniform bases.
+  template <int NW>
+  static __device__ __forceinline__ void load(char* lds, const T* p, int64_t ld, int row0, int last,
                                               int w, int lane) {
-    static_assert(ROWS * CPR % (64 * NW) == 0, "whole waves");
-    constexpr int N = ROWS * CPR / (64 * NW), STEP = 64 * NW / CPR;
-    const int r0 = (w * 64 + lane) / CPR, c0 = ((w * 64 + lane) % CPR) ^ swz(r0);
-    if (STEP % 16 == 0 && row0 + ROWS - 1 <= last) {
-      const uint32_t off = (static_cast<uint32_t>(r0) * static_cast<uint32_t>(ld) + c0 * EPC) * sizeof(T);
+    if (row0 + 63 <= last) {
+      const uint32_t off = static_cast<uint32_t>(lane_row(lane)) * static_cast<uint32_t>(ld) *
+                               static_cast<uint32_t>(sizeof(T)) + 16 * (lane % CPR);
       const char* base = reinterpret_cast<const char*>(p + row0 * ld);
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        __builtin_amdgcn_global_load_lds((const M3_GLB void*)(base + off),
-                                         (M3_LDS void*)(lds + (n * NW + w) * 64 * EPC), 16, 0, 0);
-        base += STEP * ld * static_cast<int64_t>(sizeof(T));
+      for (int n = 0; n < NG / NW; ++n) {
+        const int g = n * NW + w;
+        __builtin_amdgcn_global_load_lds(
+            (const M3_GLB void*)(base + group_row(g) * ld * static_cast<int64_t>(sizeof(T)) + off),
+            (M3_LDS void*)(lds + place(g)), 16, 0, 0);
       }
     } else {
       lane = opaque(lane);
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        const int pos = (n * NW + w) * 64 + lane, r = pos / CPR, c = (pos % CPR) ^ swz(r);
-        const T* src = p + static_cast<int64_t>(min(row0 + r, last)) * ld + c * EPC;
-        __builtin_amdgcn_global_load_lds((const M3_GLB void*)src,
-                                         (M3_LDS void*)(lds + (n * NW + w) * 64 * EPC), 16, 0, 0);
+      for (int n = 0; n < NG / NW; ++n) {
+        const int g = n * NW + w;
+        const T* src = p + static_cast<int64_t>(min(row0 + group_row(g) + lane_row(lane), last)) * ld +
+                       EPC * (lane % CPR);
+        __builtin_amdgcn_global_load_lds((const M3_GLB void*)src, (M3_LDS void*)(lds + place(g)), 16, 0, 0);
       }
     }
   }
-  // fragment kk (elements 16 kk ..) of rows row0 + lane % 32
-  static __device__ __forceinline__ Frag<T> frag(const T* lds, int row0, int kk, int lane) {
-    const int r = row0 + (lane & 31), h = lane >> 5;
+  // Rows row0 .. row0 + 31 of a as rows 0 .. 31 and of b as rows 32 .. 63
+  template <int NW>
+  static __device__ __forceinline__ void load2(char* lds, const T* a, int64_t lda, const T* b,
+                                               int64_t ldb, int row0, int last, int w, int lane) {
+    const int lr = lane_row(lane);
+#pragma unroll
+    for (int n = 0; n < NG / NW; ++n) {
+      const int g = n * NW + w, r = group_row(g) + lr;
+      const bool second = r >= 32;
+      const int64_t row = min(row0 + (second ? r - 32 : r), last);
+      const T* src = (second ? b + row * ldb : a + row * lda) + EPC * (lane % CPR);
+      __builtin_amdgcn_global_load_lds((const M3_GLB void*)src, (M3_LDS void*)(lds + place(g)), 16, 0, 0);
+    }
+  }
+
+  // fragment kk (elements 16 kk ..) of rows row0 + lane % 32 (row0 0 or 32)
+  static __device__ __forceinline__ Frag<T> frag(const char* lds, int row0, int kk, int lane) {
+    const int r = lane & 31, h = lane >> 5;
+    const char* a;
+    if constexpr (RB == 128)
+      a = lds + ((r >> 2) & 3) * G4 + ((r >> 1) & 1) * G1 + ((r & 1) + 2 * (r >> 4)) * RB + 4 * RB * (row0 / 32);
+    else
+      a = lds + ((r >> 2) & 3) * G4 + (r & 3) * G1 + (r >> 4) * RB + (RB == 256 ? 2 * RB : HALF) * (row0 / 32);
+    a += 8 * sizeof(T) * h + 16 * sizeof(T) * kk;
     Frag<T> f;
     if constexpr (sizeof(T) == 2) {
-      f.v = *reinterpret_cast<const bh8*>(lds + r * ROW + (((2 * kk + h) ^ swz(r)) * EPC));
+      f.v = *reinterpret_cast<const bh8*>(a);
     } else {
-      f.a = *reinterpret_cast<const f4*>(lds + r * ROW + (((4 * kk + 2 * h) ^ swz(r)) * EPC));
-      f.b = *reinterpret_cast<const f4*>(lds + r * ROW + (((4 * kk + 2 * h + 1) ^ swz(r)) * EPC));
+      f.a = *reinterpret_cast<const f4*>(a);
+      f.b = *reinterpret_cast<const f4*>(a + 16);
     }
     return f;
   }
   // the transposed fragment: column d0 + lane % 32, k slots = rows
-  // row0 + 4 h + {0..3}, row0 + 8 + 4 h + {0..3}
-  static __device__ __forceinline__ Frag<T> frag_t(const T* lds, int row0, int d0, int lane) {
-    const int h = lane >> 5;
+  // row0 + 4 h + {0..3}, row0 + 8 + 4 h + {0..3} (row0 a multiple of 16)
+  static __device__ __forceinline__ Frag<T> frag_t(const char* lds, int row0, int d0, int lane) {
+    const int h = lane >> 5, q = row0 / 16;
+    const int far = RB == 128 ? q * 2 * RB : RB == 256 ? q * RB : (q & 1) * RB + (q >> 1) * HALF;
     Frag<T> f;
     if constexpr (sizeof(T) == 2) {
       // a transposing read: sixteen lanes point at four rows of sixteen
       // elements, each lane at four; lane i receives column i of the four
-      const int i = lane & 15;
-      const int c = (d0 >> 3) + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
-      s4v x[2];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int r = row0 + 8 * n + 4 * h + (i >> 2);
-        const T* a = lds + r * ROW + ((c ^ swz(r)) * EPC) + (i & 1) * 4;
-        x[n] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((M3_LDS s4v*)a);
-      }
-      const s8v y = __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7);
-      f.v = __builtin_bit_cast(bh8, y);
+      const int i = lane & 15, c = i >> 2;
+      const char* a = lds + h * G4 + (RB == 128 ? (c >> 1) * G1 + (c & 1) * RB : c * G1) +
+                      32 * ((lane >> 4) & 1) + 8 * (i & 3) + far + 2 * d0;
+      const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((M3_LDS s4v*)a);
+      const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((M3_LDS s4v*)(a + 2 * G4));
+      f.v = __builtin_bit_cast(bh8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      const int d = d0 + (lane & 31), c = d / EPC, e = d % EPC;
+      const char* a = lds + h * G4 + far + 4 * (d0 + (lane & 31));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = row0 + 4 * h + j, r2 = r + 8;
-        f.a[j] = lds[r * ROW + ((c ^ swz(r)) * EPC) + e];
-        f.b[j] = lds[r2 * ROW + ((c ^ swz(r2)) * EPC) + e];
+        f.a[j] = *reinterpret_cast<const float*>(a + j * G1);
+        f.b[j] = *reinterpret_cast<const float*>(a + 2 * G4 + j * G1);
       }
     }
     return f;
-  }
-  // one element
-  static __device__ __forceinline__ float at(const T* lds, int r, int d) {
-    return to_f32(lds[r * ROW + (((d / EPC) ^ swz(r)) * EPC) + d % EPC]);
   }
 };
 

@@ -174,7 +174,7 @@ def test_attn_refusals():
         for bad in (dict(nseq=0), dict(tokens_k=0), dict(nheads_q=0), dict(nheads_k=0), dict(nheads_q=5),
                     dict(nheads_q=2, nheads_k=4), dict(scale=float("nan")), dict(scale=float("inf")),
                     dict(ld_q=248), dict(ld_k=120), dict(ld_v=-8), dict(ld_o=8), dict(ld_do=8),
-                    dict(stride_k=-8)):
+                    dict(stride_k=-8), dict(ld_q=1 << 24), dict(ld_v=1 << 24)):
             assert call(_adims(**bad)) == SHAPE, bad
         assert call(_adims(dtype=-1)) == DTYPE
         for D in (32, 96, 256):

@@ -17,7 +17,7 @@
 namespace m3 {
 namespace {
 
-// D / 4 lanes to a row and head
+// D / 8 lanes to a row and head; behind all rows' numbers infinity and 0
 template <typename T, int D>
 __global__ __launch_bounds__(256) void k_attn_stat(AttnArgs a) {
   constexpr int G = D / 8;
@@ -32,8 +32,15 @@ __global__ __launch_bounds__(256) void k_attn_stat(AttnArgs a) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) s = fmaf(o[j], g[j], s);
   s = group_sum<G>(s);
-  if (n < all && e == 0)
-    a.stat[static_cast<int64_t>(h) * a.Tq + t] = float2{a.clse[m] * kLog2eA, s};
+  if (n == 0 && e == 0) {
+    a.stat[2 * all] = INFINITY;
+    a.stat[2 * all + 1] = 0.0f;
+  }
+  if (n < all && e == 0) {
+    float* st = a.stat + static_cast<int64_t>(h) * a.Tq + t;
+    st[0] = a.clse[m] * kLog2eA;
+    st[static_cast<int64_t>(a.Hq) * a.Tq] = s;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -66,8 +73,9 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
       frag_load(g[kk], d + 16 * kk);
     }
   }
-  const float2 st = a.stat[static_cast<int64_t>(h) * a.Tq + row];
-  const float lse = st.x == -INFINITY ? INFINITY : st.x;   // no key: every weight 0
+  const float* st = a.stat + static_cast<int64_t>(h) * a.Tq + row;
+  const float lse = st[0] == -INFINITY ? INFINITY : st[0];   // no key: every weight 0
+  const float dd = st[static_cast<int64_t>(a.Hq) * a.Tq];
   f16v dq[D / 32];
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) dq[d] = f16v{};
@@ -100,7 +108,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const float p = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse));
-      ds[e] = j0 + row_of(e, half) < sees ? p * (dp[e] - st.y) : 0.0f;
+      ds[e] = j0 + row_of(e, half) < sees ? p * (dp[e] - dd) : 0.0f;
     }
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
@@ -121,13 +129,89 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
 }
 
 // ---------------------------------------------------------------------------
-// dk, dv: 32 keys a wave, tiles of 32 queries of the group's heads in LDS
-template <typename T, int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 1) void k_attn_dkv(AttnArgs a) {
+// dv and dk: 32 keys a wave, tiles of 32 queries of the group's heads in LDS.
+// They are two kernels: together they need 25% fewer products, but keys,
+// values, both sums and two tiles' scores are more than 256 registers, which
+// leaves one wave a SIMD and, of those, copies between the two halves of the
+// register file (measured 600 us for the two sums of 8192 rows, 16 heads of
+// 128 on 2, against 305 us for both kernels).  Each overlaps by itself as
+// well: while a tile's weights are formed, the matrix cores form the next
+// tile's s and dp.
+
+// One step: weights (dk: and ds) of the tile `cur` from its s, its products
+// into the sum, and s of the tile `nxt`.  row0: the first row of the tile that
+// counts for this lane's key (the lane's own offset 4 (lane / 32) taken off);
+// rows past the last have lse = infinity, so their weights are 0.  dk's products with V stand first:
+// the exponentials run beside them, the rest of ds beside those of the next s.
+template <typename T, int D, bool DK>
+__device__ __forceinline__ void key_step(f16v* sum, f16v& s, f16v& s2, const Frag<T>* k,
+                                         const Frag<T>* v, const char* cur, const char* nxt,
+                                         const float* stat, float c, int row0, int lane) {
+  using L = Tile<T, D>;
+  constexpr int N1 = D / 16;                  // products of each kind
+  constexpr int A = DK ? N1 : 0, B = A + N1;  // first product of s2, of the sum
+  const int half = lane >> 5;
+  auto operand = [&](int n) __attribute__((always_inline)) -> Frag<T> {
+    if (n < A) return L::frag(cur, 32, n, lane);
+    if (n < B) return L::frag(nxt, 0, n - A, lane);
+    const int m = n - B;
+    return L::frag_t(cur, (DK ? 0 : 32) + 16 * (m / (N1 / 2)), 32 * (m % (N1 / 2)), lane);
+  };
+  // lse (which = 0) or D (1) of the rows 8 b + 4 half + 0 .. 3
+  auto stats = [&](int which, int b) __attribute__((always_inline)) -> f4 {
+    return *reinterpret_cast<const f4*>(stat + 32 * which + 8 * b + 4 * half);
+  };
+  f16v dp;
+  if (DK) dp = f16v{};
+  s2 = f16v{};
+  Frag<T> op[3], f[2];
+  f4 l4[2], d4[2];
+  l4[0] = stats(0, 0);
+  op[0] = operand(0);
+  op[1] = operand(1);
+  float w8[8];
+#pragma unroll
+  for (int n = 0; n < B + N1; ++n) {
+    if (n + 2 < B + N1) op[(n + 2) % 3] = operand(n + 2);
+    if (n < A) {
+      dp = mma(op[n % 3], v[n], dp);
+    } else if (n < B) {
+      s2 = mma(op[n % 3], k[n - A], s2);
+    } else {
+      const int m = n - B, w = m / (N1 / 2), d = m % (N1 / 2);
+      sum[d] = mma(op[n % 3], f[w], sum[d]);
+    }
+    if (DK && n == A - 1) d4[0] = stats(1, 0);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      // the weights: beside the first products; dv's until its sum needs them
+      if ((DK ? e * N1 / 16 : e * (N1 + N1 / 2) / 16) == n) {
+        if (e % 4 == 0 && e < 12) l4[(e / 4 + 1) & 1] = stats(0, e / 4 + 1);
+        float w = __builtin_amdgcn_exp2f(fmaf(s[e], c, -l4[(e / 4) & 1][e % 4]));
+        w = row_of(e, 0) >= row0 ? w : 0.0f;
+        s[e] = w;
+        if (!DK) {
+          w8[e % 8] = w;
+          if (e % 8 == 7) frag_from(f[e / 8], w8);
+        }
+      }
+      if (DK && A + 1 + e * (N1 + N1 / 2 - 1) / 16 == n) {
+        if (e % 4 == 0 && e < 12) d4[(e / 4 + 1) & 1] = stats(1, e / 4 + 1);
+        w8[e % 8] = s[e] * (dp[e] - d4[(e / 4) & 1][e % 4]);
+        if (e % 8 == 7) frag_from(f[e / 8], w8);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+template <typename T, int D, int WAVES, bool DK>
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn_dkv(AttnArgs a) {
   using L = Tile<T, D>;
   constexpr int BK = 32 * WAVES, BQ = 32;
-  __shared__ __align__(16) char sQG[2][L::BYTES];
-  __shared__ __align__(16) float sL[2][BQ], sD[2][BQ];
+  // tiles t, t + 1 (its s), t + 2 (arriving)
+  __shared__ __align__(16) char sQG[3][L::BYTES];
+  __shared__ __align__(16) float sS[3][2 * BQ];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int per = a.Hk * a.gsplit;
   const int part = blockIdx.x % a.gsplit, hk = blockIdx.x % per / a.gsplit;
@@ -149,94 +233,73 @@ __global__ __launch_bounds__(64 * WAVES, 1) void k_attn_dkv(AttnArgs a) {
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       frag_load(k[kk], p + 16 * kk);
-      frag_load(v[kk], r + 16 * kk);
+      if (DK) frag_load(v[kk], r + 16 * kk);
     }
   }
-  f16v dk[D / 32], dv[D / 32];
+  f16v sum[D / 32];
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d) dk[d] = dv[d] = f16v{};
+  for (int d = 0; d < D / 32; ++d) sum[d] = f16v{};
   const float c = a.scale * kLog2eA;
   // the first query that sees the block's first key, in whole tiles
   const int first = max(0, j0 - off) / BQ;
   const int nt = max(0, (Lq + BQ - 1) / BQ - first), all = nt * gper;
-  const int wfirst = jw - off;   // the first query that sees the wave's first key
-  auto fetch = [&](int n, int buf) {
-    const int h = hk * grp + part * gper + n / nt, i0 = (first + n % nt) * BQ;
-    const T* qp = static_cast<const T*>(a.q) + static_cast<int64_t>(q0) * a.ldq + h * D;
-    const T* gp = static_cast<const T*>(a.dout) + static_cast<int64_t>(q0) * a.lddo + h * D;
-    L::template load2<WAVES>(sQG[buf], qp, a.ldq, gp, a.lddo, i0, Lq - 1, wave, lane);
-    if (threadIdx.x < BQ) {
-      const int i = i0 + threadIdx.x;
-      const float2 st = a.stat[static_cast<int64_t>(h) * a.Tq + q0 + min(i, Lq - 1)];
-      // rows without keys and rows past the end: every weight 0
-      sL[buf][threadIdx.x] = i < Lq && st.x != -INFINITY ? st.x : INFINITY;
-      sD[buf][threadIdx.x] = st.y;
+  // the tiles run over the queries of one head after the other
+  int fh = hk * grp + part * gper, fi = first;   // of the next fetch
+  auto fetch = [&](int buf) __attribute__((always_inline)) {
+    const T* qp = static_cast<const T*>(a.q) + static_cast<int64_t>(q0) * a.ldq + fh * D;
+    const T* gp = static_cast<const T*>(a.dout) + static_cast<int64_t>(q0) * a.lddo + fh * D;
+    L::template load2<WAVES>(sQG[buf], qp, a.ldq, gp, a.lddo, fi * BQ, Lq - 1, wave, lane);
+    if (wave == 0) {   // lse of 32 rows, then D of them; past the last row infinity and 0
+      const int i = fi * BQ + (lane & 31);
+      const float* src = a.stat + (i < Lq ? (static_cast<int64_t>(half) * a.Hq + fh) * a.Tq + q0 + i
+                                          : 2 * static_cast<int64_t>(a.Hq) * a.Tq + half);
+      __builtin_amdgcn_global_load_lds((const M3_GLB void*)src, (M3_LDS void*)sS[buf], 4, 0, 0);
+    }
+    if (++fi == first + nt) {
+      fi = first;
+      ++fh;
     }
   };
-  if (all > 0) fetch(0, 0);
-  for (int n = 0; n < all; ++n) {
+  f16v s, s2;
+  if (all > 0) {
+    fetch(0);
     lds_loads_done();
     __syncthreads();
-    const int buf = n & 1;
-    if (n + 1 < all) fetch(n + 1, buf ^ 1);
-    const int i0 = (first + n % nt) * BQ;
-    if (i0 + BQ <= wfirst) continue;
-    const char* QG = sQG[buf];
-    f16v s = f16v{}, dp = f16v{};
+    if (all > 1) fetch(1);
+    s = f16v{};
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      s = mma(L::frag(QG, 0, kk, lane), k[kk], s);
-      dp = mma(L::frag(QG, 32, kk, lane), v[kk], dp);
-    }
-    float p[16], ds[16];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const f4 l4 = *reinterpret_cast<const f4*>(&sL[buf][8 * b + 4 * half]);
-      const f4 d4 = *reinterpret_cast<const f4*>(&sD[buf][8 * b + 4 * half]);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int e = 4 * b + x;
-        const float w = __builtin_amdgcn_exp2f(fmaf(s[e], c, -l4[x]));
-        const bool on = i0 + 8 * b + 4 * half + x + off >= j && l4[x] != INFINITY;
-        p[e] = on ? w : 0.0f;
-        ds[e] = on ? w * (dp[e] - d4[x]) : 0.0f;
-      }
-    }
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      Frag<T> fp, fd;
-      frag_from(fp, p + 8 * w);
-      frag_from(fd, ds + 8 * w);
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d) {
-        dv[d] = mma(L::frag_t(QG, 32 + 16 * w, 32 * d, lane), fp, dv[d]);
-        dk[d] = mma(L::frag_t(QG, 16 * w, 32 * d, lane), fd, dk[d]);
-      }
-    }
+    for (int kk = 0; kk < D / 16; ++kk) s = mma(L::frag(sQG[0], 0, kk, lane), k[kk], s);
+  }
+  int ci = first, cur = 0;   // the tile at hand and its buffer
+  auto step = [&](int n, f16v& s, f16v& s2) __attribute__((always_inline)) {
+    lds_loads_done();
+    __syncthreads();   // tile n + 1 is there; every wave is done with n - 1
+    const int nxt = cur == 2 ? 0 : cur + 1, aft = nxt == 2 ? 0 : nxt + 1;
+    if (n + 2 < all) fetch(aft);
+    const int i0 = ci * BQ;
+    // rows i >= j - off count
+    key_step<T, D, DK>(sum, s, s2, k, v, sQG[cur], sQG[nxt], sS[cur], c, j - off - i0 - 4 * half, lane);
+    cur = nxt;
+    if (++ci == first + nt) ci = first;
+  };
+  for (int n = 0; n < all; n += 2) {   // by two: the scores change places
+    step(n, s, s2);
+    if (n + 1 < all) step(n + 1, s2, s);
   }
   if (j >= Lk) return;
+  const float f = DK && a.gsplit == 1 ? a.scale : 1.0f;   // parts are scaled where they are added
   const int64_t at = (row * a.Hk + hk) * D + 4 * half;
-  if (a.gsplit == 1) {
-    T *ok = static_cast<T*>(a.dk) + at, *ov = static_cast<T*>(a.dv) + at;
+  T* o = static_cast<T*>(DK ? a.dk : a.dv) + at;
+  float* op = (DK ? a.pk : a.pv) + static_cast<int64_t>(part) * a.Tk * a.Hk * D + at;
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
+  for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        put4(ok + 32 * d + 8 * e, dk[d][4 * e] * a.scale, dk[d][4 * e + 1] * a.scale,
-             dk[d][4 * e + 2] * a.scale, dk[d][4 * e + 3] * a.scale);
-        put4(ov + 32 * d + 8 * e, dv[d][4 * e], dv[d][4 * e + 1], dv[d][4 * e + 2], dv[d][4 * e + 3]);
-      }
-  } else {
-    const int64_t to = static_cast<int64_t>(part) * a.Tk * a.Hk * D + at;
-    float *ok = a.pk + to, *ov = a.pv + to;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        put4(ok + 32 * d + 8 * e, dk[d][4 * e], dk[d][4 * e + 1], dk[d][4 * e + 2], dk[d][4 * e + 3]);
-        put4(ov + 32 * d + 8 * e, dv[d][4 * e], dv[d][4 * e + 1], dv[d][4 * e + 2], dv[d][4 * e + 3]);
-      }
-  }
+    for (int e = 0; e < 4; ++e) {
+      const float x0 = sum[d][4 * e] * f, x1 = sum[d][4 * e + 1] * f, x2 = sum[d][4 * e + 2] * f,
+                  x3 = sum[d][4 * e + 3] * f;
+      if (a.gsplit == 1) put4(o + 32 * d + 8 * e, x0, x1, x2, x3);
+      else put4(op + 32 * d + 8 * e, x0, x1, x2, x3);
+    }
 }
 
 // adds the parts of a group in order, for the rows that belong to a sequence
@@ -261,7 +324,7 @@ int group_parts(int Tk, int S, int Hq, int Hk) {
   const int g = Hq / Hk;
   const int64_t blocks = (static_cast<int64_t>(Tk) / 128 + 1) * Hk;
   for (int n = 1; n < g; ++n)
-    if (g % n == 0 && blocks * n >= 512) return n;
+    if (g % n == 0 && blocks * n >= 1024) return n;
   return g;
 }
 
@@ -273,7 +336,9 @@ hipError_t run(const AttnArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t nk = (static_cast<int64_t>(a.Tk) / B + a.S) * a.Hk * a.gsplit;
-  k_attn_dkv<T, D, W><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
+  k_attn_dkv<T, D, W, false><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  k_attn_dkv<T, D, W, true><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (a.gsplit > 1) {
     const int64_t n = static_cast<int64_t>(a.Tk) * a.Hk * D / 4;
@@ -291,7 +356,7 @@ constexpr size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t attn_backward_workspace_bytes(int Tq, int Tk, int S, int Hq, int Hk, int D) {
   const int g = group_parts(Tk, S, Hq, Hk);
-  size_t n = up256(sizeof(float2) * Tq * static_cast<size_t>(Hq));
+  size_t n = up256(2 * sizeof(float) * (Tq * static_cast<size_t>(Hq) + 1));
   if (g > 1) n += 2 * up256(sizeof(float) * g * static_cast<size_t>(Tk) * Hk * D);
   return n;
 }
@@ -299,8 +364,8 @@ size_t attn_backward_workspace_bytes(int Tq, int Tk, int S, int Hq, int Hk, int 
 hipError_t launch_attn_backward(AttnArgs& a, int bf16, void* ws, hipStream_t s) {
   a.gsplit = group_parts(a.Tk, a.S, a.Hq, a.Hk);
   char* c = static_cast<char*>(ws);
-  a.stat = reinterpret_cast<float2*>(c);
-  c += up256(sizeof(float2) * a.Tq * static_cast<size_t>(a.Hq));
+  a.stat = reinterpret_cast<float*>(c);
+  c += up256(2 * sizeof(float) * (a.Tq * static_cast<size_t>(a.Hq) + 1));
   a.pk = reinterpret_cast<float*>(c);
   c += up256(sizeof(float) * a.gsplit * static_cast<size_t>(a.Tk) * a.Hk * a.D);
   a.pv = reinterpret_cast<float*>(c);

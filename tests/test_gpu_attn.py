@@ -166,6 +166,23 @@ def test_infinities_and_nan_reach_only_who_sees_them(D, dtype):
     assert torch.isnan(o[120:150]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradients_of_a_sequence_with_nan_stay_there(dtype):
+    n, Hq, Hk, D = [70, 45, 130], 4, 2, 64
+    q, k, v, do = _inputs(245, 245, Hq, Hk, D, dtype, 16)
+    cu = _dev(_offsets(n))
+    o, lse = m3.attn_prefill_varlen(q, k, v, cu, cu)
+    g = m3.attn_prefill_varlen_backward(q, k, v, o, lse, do, cu, cu)
+    for t in (q, k, v, do):
+        t[70:115] = float("nan")
+    o2, lse2 = m3.attn_prefill_varlen(q, k, v, cu, cu)
+    g2 = m3.attn_prefill_varlen_backward(q, k, v, o2, lse2, do, cu, cu)
+    torch.cuda.synchronize()
+    for a, b in zip((o, lse, *g), (o2, lse2, *g2)):
+        assert torch.equal(a[:70], b[:70]) and torch.equal(a[115:], b[115:])
+        assert torch.isnan(b[70:115]).all()
+
+
 def test_a_masked_score_of_any_size():
     """Scores far below and above what fp32's exponential holds."""
     q, k, v, _ = _inputs(100, 100, 1, 1, 64, F32, 7)

@@ -44,12 +44,92 @@ __global__ __launch_bounds__(256) void k_attn_stat(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// One step of a sum over tiles of 32 rows, the same for the three gradients:
+//   kDv  lanes are keys, rows queries: sum += p^T do
+//   kDk  lanes are keys, rows queries: sum += ds^T q
+//   kDq  lanes are queries, rows keys: sum += ds k
+// A tile holds the rows that s is formed of (q, q, k) and, from row 32 on, the
+// others (do, do, v); x and y are the lanes' own (k v, k v, q do).  From s of
+// the tile `cur` the step forms the weights, then (kDk, kDq) ds, then the
+// products into the sum, and s of the tile `nxt`.  It is laid out product by
+// product, each with its share of the softmax and the operand of the product
+// two steps on: dp's products beside the exponentials, those of the next s
+// beside the rest of ds.  Rows count from `edge` on (kDq: up to it), the lane's
+// own offset 4 (lane / 32) taken off.
+enum { kDv = 0, kDk = 1, kDq = 2 };
+template <typename T, int D, int KIND>
+__device__ __forceinline__ void grad_step(f16v* sum, f16v& s, f16v& s2, const Frag<T>* x,
+                                          const Frag<T>* y, const char* cur, const char* nxt,
+                                          const float* stat, float lse, float dd, float c, int edge,
+                                          int lane) {
+  using L = Tile<T, D>;
+  constexpr bool DS = KIND != kDv;
+  constexpr int N1 = D / 16;                  // products of each kind
+  constexpr int A = DS ? N1 : 0, B = A + N1;  // first product of s2, of the sum
+  const int half = lane >> 5;
+  auto operand = [&](int n) __attribute__((always_inline)) -> Frag<T> {
+    if (n < A) return L::frag(cur, 32, n, lane);
+    if (n < B) return L::frag(nxt, 0, n - A, lane);
+    const int m = n - B;
+    return L::frag_t(cur, (DS ? 0 : 32) + 16 * (m / (N1 / 2)), 32 * (m % (N1 / 2)), lane);
+  };
+  // lse (which = 0) or D (1) of the rows 8 b + 4 half + 0 .. 3; of queries as
+  // lanes they are the lane's own
+  auto stats = [&](int which, int b) __attribute__((always_inline)) -> f4 {
+    if (KIND == kDq) return which ? f4{dd, dd, dd, dd} : f4{lse, lse, lse, lse};
+    return *reinterpret_cast<const f4*>(stat + 32 * which + 8 * b + 4 * half);
+  };
+  f16v dp;
+  if (DS) dp = f16v{};
+  s2 = f16v{};
+  Frag<T> op[3], f[2];
+  f4 l4[2], d4[2];
+  l4[0] = stats(0, 0);
+  op[0] = operand(0);
+  op[1] = operand(1);
+  float w8[8];
+#pragma unroll
+  for (int n = 0; n < B + N1; ++n) {
+    if (n + 2 < B + N1) op[(n + 2) % 3] = operand(n + 2);
+    if (n < A) {
+      dp = mma(op[n % 3], y[n], dp);
+    } else if (n < B) {
+      s2 = mma(op[n % 3], x[n - A], s2);
+    } else {
+      const int m = n - B, w = m / (N1 / 2), d = m % (N1 / 2);
+      sum[d] = mma(op[n % 3], f[w], sum[d]);
+    }
+    if (DS && n == A - 1) d4[0] = stats(1, 0);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      // the weights: beside dp's products; dv's until its sum needs them
+      if ((DS ? e * N1 / 16 : e * (N1 + N1 / 2) / 16) == n) {
+        if (e % 4 == 0 && e < 12) l4[(e / 4 + 1) & 1] = stats(0, e / 4 + 1);
+        float w = __builtin_amdgcn_exp2f(fmaf(s[e], c, -l4[(e / 4) & 1][e % 4]));
+        w = (KIND == kDq ? row_of(e, 0) < edge : row_of(e, 0) >= edge) ? w : 0.0f;
+        s[e] = w;
+        if (!DS) {
+          w8[e % 8] = w;
+          if (e % 8 == 7) frag_from(f[e / 8], w8);
+        }
+      }
+      if (DS && A + 1 + e * (N1 + N1 / 2 - 1) / 16 == n) {
+        if (e % 4 == 0 && e < 12) d4[(e / 4 + 1) & 1] = stats(1, e / 4 + 1);
+        w8[e % 8] = s[e] * (dp[e] - d4[(e / 4) & 1][e % 4]);
+        if (e % 8 == 7) frag_from(f[e / 8], w8);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // dq: 32 queries a wave, tiles of 32 keys in LDS
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn_dq(AttnArgs a) {
   using L = Tile<T, D>;
   constexpr int BM = 32 * WAVES, BN = 32;
-  __shared__ __align__(16) char sKV[2][L::BYTES];
+  __shared__ __align__(16) char sKV[3][L::BYTES];   // tiles t, t + 1 (its s), t + 2 (arriving)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nslot = gridDim.x / a.Hq;
   const int h = blockIdx.x % a.Hq;
@@ -83,40 +163,30 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   const int sees = min(i, Lq - 1) + off + 1;
   const int most = min(min(i0 + BM, Lq) + off, Lk);
   const int ntile = most <= 0 ? 0 : (most + BN - 1) / BN;
-  const int wmost = min(min(iw + 32, Lq) + off, Lk);
   const T* kp = static_cast<const T*>(a.k) + static_cast<int64_t>(k0) * a.ldk + hk * D;
   const T* vp = static_cast<const T*>(a.v) + static_cast<int64_t>(k0) * a.ldv + hk * D;
+  f16v s, s2;
   if (ntile > 0) {
     L::template load2<WAVES>(sKV[0], kp, a.ldk, vp, a.ldv, 0, Lk - 1, wave, lane);
-  }
-  for (int t = 0; t < ntile; ++t) {
     lds_loads_done();
     __syncthreads();
-    if (t + 1 < ntile) {
-      L::template load2<WAVES>(sKV[(t + 1) & 1], kp, a.ldk, vp, a.ldv, (t + 1) * BN, Lk - 1, wave, lane);
-    }
-    const int j0 = t * BN;
-    if (j0 >= wmost) continue;
-    const char* KV = sKV[t & 1];
-    f16v s = f16v{}, dp = f16v{};
+    if (ntile > 1) L::template load2<WAVES>(sKV[1], kp, a.ldk, vp, a.ldv, BN, Lk - 1, wave, lane);
+    s = f16v{};
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      s = mma(L::frag(KV, 0, kk, lane), q[kk], s);
-      dp = mma(L::frag(KV, 32, kk, lane), g[kk], dp);
-    }
-    float ds[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float p = __builtin_amdgcn_exp2f(fmaf(s[e], c, -lse));
-      ds[e] = j0 + row_of(e, half) < sees ? p * (dp[e] - dd) : 0.0f;
-    }
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      Frag<T> f;
-      frag_from(f, ds + 8 * w);
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d) dq[d] = mma(L::frag_t(KV, 16 * w, 32 * d, lane), f, dq[d]);
-    }
+    for (int kk = 0; kk < D / 16; ++kk) s = mma(L::frag(sKV[0], 0, kk, lane), q[kk], s);
+  }
+  int cur = 0;
+  auto step = [&](int t, f16v& s, f16v& s2) __attribute__((always_inline)) {
+    lds_loads_done();
+    __syncthreads();   // tile t + 1 is there; every wave is done with t - 1
+    const int nxt = cur == 2 ? 0 : cur + 1, aft = nxt == 2 ? 0 : nxt + 1;
+    if (t + 2 < ntile) L::template load2<WAVES>(sKV[aft], kp, a.ldk, vp, a.ldv, (t + 2) * BN, Lk - 1, wave, lane);
+    grad_step<T, D, kDq>(dq, s, s2, q, g, sKV[cur], sKV[nxt], nullptr, lse, dd, c, sees - t * BN - 4 * half, lane);
+    cur = nxt;
+  };
+  for (int t = 0; t < ntile; t += 2) {   // by two: the scores change places
+    step(t, s, s2);
+    if (t + 1 < ntile) step(t + 1, s2, s);
   }
   if (i >= Lq) return;
   T* o = static_cast<T*>(a.dq) + (row * a.Hq + h) * D + 4 * half;
@@ -130,80 +200,10 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
 
 // ---------------------------------------------------------------------------
 // dv and dk: 32 keys a wave, tiles of 32 queries of the group's heads in LDS.
-// They are two kernels: together they need 25% fewer products, but keys,
-// values, both sums and two tiles' scores are more than 256 registers, which
-// leaves one wave a SIMD and, of those, copies between the two halves of the
-// register file (measured 600 us for the two sums of 8192 rows, 16 heads of
-// 128 on 2, against 305 us for both kernels).  Each overlaps by itself as
-// well: while a tile's weights are formed, the matrix cores form the next
-// tile's s and dp.
-
-// One step: weights (dk: and ds) of the tile `cur` from its s, its products
-// into the sum, and s of the tile `nxt`.  row0: the first row of the tile that
-// counts for this lane's key (the lane's own offset 4 (lane / 32) taken off);
-// rows past the last have lse = infinity, so their weights are 0.  dk's products with V stand first:
-// the exponentials run beside them, the rest of ds beside those of the next s.
-template <typename T, int D, bool DK>
-__device__ __forceinline__ void key_step(f16v* sum, f16v& s, f16v& s2, const Frag<T>* k,
-                                         const Frag<T>* v, const char* cur, const char* nxt,
-                                         const float* stat, float c, int row0, int lane) {
-  using L = Tile<T, D>;
-  constexpr int N1 = D / 16;                  // products of each kind
-  constexpr int A = DK ? N1 : 0, B = A + N1;  // first product of s2, of the sum
-  const int half = lane >> 5;
-  auto operand = [&](int n) __attribute__((always_inline)) -> Frag<T> {
-    if (n < A) return L::frag(cur, 32, n, lane);
-    if (n < B) return L::frag(nxt, 0, n - A, lane);
-    const int m = n - B;
-    return L::frag_t(cur, (DK ? 0 : 32) + 16 * (m / (N1 / 2)), 32 * (m % (N1 / 2)), lane);
-  };
-  // lse (which = 0) or D (1) of the rows 8 b + 4 half + 0 .. 3
-  auto stats = [&](int which, int b) __attribute__((always_inline)) -> f4 {
-    return *reinterpret_cast<const f4*>(stat + 32 * which + 8 * b + 4 * half);
-  };
-  f16v dp;
-  if (DK) dp = f16v{};
-  s2 = f16v{};
-  Frag<T> op[3], f[2];
-  f4 l4[2], d4[2];
-  l4[0] = stats(0, 0);
-  op[0] = operand(0);
-  op[1] = operand(1);
-  float w8[8];
-#pragma unroll
-  for (int n = 0; n < B + N1; ++n) {
-    if (n + 2 < B + N1) op[(n + 2) % 3] = operand(n + 2);
-    if (n < A) {
-      dp = mma(op[n % 3], v[n], dp);
-    } else if (n < B) {
-      s2 = mma(op[n % 3], k[n - A], s2);
-    } else {
-      const int m = n - B, w = m / (N1 / 2), d = m % (N1 / 2);
-      sum[d] = mma(op[n % 3], f[w], sum[d]);
-    }
-    if (DK && n == A - 1) d4[0] = stats(1, 0);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      // the weights: beside the first products; dv's until its sum needs them
-      if ((DK ? e * N1 / 16 : e * (N1 + N1 / 2) / 16) == n) {
-        if (e % 4 == 0 && e < 12) l4[(e / 4 + 1) & 1] = stats(0, e / 4 + 1);
-        float w = __builtin_amdgcn_exp2f(fmaf(s[e], c, -l4[(e / 4) & 1][e % 4]));
-        w = row_of(e, 0) >= row0 ? w : 0.0f;
-        s[e] = w;
-        if (!DK) {
-          w8[e % 8] = w;
-          if (e % 8 == 7) frag_from(f[e / 8], w8);
-        }
-      }
-      if (DK && A + 1 + e * (N1 + N1 / 2 - 1) / 16 == n) {
-        if (e % 4 == 0 && e < 12) d4[(e / 4 + 1) & 1] = stats(1, e / 4 + 1);
-        w8[e % 8] = s[e] * (dp[e] - d4[(e / 4) & 1][e % 4]);
-        if (e % 8 == 7) frag_from(f[e / 8], w8);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  }
-}
+// They are two kernels: one for both needs a fifth fewer products, but keys,
+// values, both sums and a tile's scores are more than 256 registers, which
+// leaves one wave a SIMD and copies between the halves of its register file
+// (8192 packed rows, 16 heads of 128 on 2: 600 us, against 162 + 202 us).
 
 template <typename T, int D, int WAVES, bool DK>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn_dkv(AttnArgs a) {
@@ -278,7 +278,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
     if (n + 2 < all) fetch(aft);
     const int i0 = ci * BQ;
     // rows i >= j - off count
-    key_step<T, D, DK>(sum, s, s2, k, v, sQG[cur], sQG[nxt], sS[cur], c, j - off - i0 - 4 * half, lane);
+    grad_step<T, D, DK ? kDk : kDv>(sum, s, s2, k, v, sQG[cur], sQG[nxt], sS[cur], 0.0f, 0.0f, c,
+                                    j - off - i0 - 4 * half, lane);
     cur = nxt;
     if (++ci == first + nt) ci = first;
   };

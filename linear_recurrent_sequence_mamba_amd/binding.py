@@ -9,7 +9,9 @@ library is missing the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -581,45 +583,67 @@ def decode_tokens(h, x, B, C, dt, A, lam, theta, x_prev=None, B_prev=None,
 # ---------------------------------------------------------------------------
 # the other layers of a hybrid stack: gated recurrence, q/k norms with rotary
 # positions, causal attention
-class _on:
+class _Switch:
     """The device of a call's tensors as the current one and, if given, the
     stream as the current one, so that what a helper allocates belongs to the
-    stream that uses it.  Entering gives the raw stream to launch on.  Nothing
-    is switched where nothing has to be: a small call is bound by the host."""
+    stream that uses it."""
 
-    __slots__ = ("index", "guards")
-
-    def __init__(self, device, stream):
-        self.index = device.index
-        self.guards = []
-        if self.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(stream))
+    def __init__(self, index, stream):
+        self.device = torch.cuda.device(index)
+        self.stream = torch.cuda.stream(stream)   # None: no change
 
     def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.index)
+        self.device.__enter__()
+        self.stream.__enter__()
 
     def __exit__(self, *e):
-        for g in reversed(self.guards):
-            g.__exit__(*e)
+        self.stream.__exit__(*e)
+        self.device.__exit__(*e)
 
 
-def _same_device(**tensors):
-    """All given tensors on one GPU; returns it."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{name} must be a device tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, others on {dev}")
-    return dev
+_HERE = contextlib.nullcontext()
+
+
+def _on(index, stream):
+    """A context for the launch.  Nothing is switched where nothing has to be:
+    a small call is bound by the host."""
+    if stream is None and index == torch.cuda.current_device():
+        return _HERE
+    return _Switch(index, stream)
+
+
+def _raw(index):
+    """The current stream of a device as the library takes it."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _same_device(names, *tensors):
+    """All given tensors on one GPU; returns its index."""
+    index = None
+    for t in tensors:
+        if t is not None:
+            k = t.get_device() if isinstance(t, torch.Tensor) else -1
+            if k != index:
+                if index is not None or k < 0:
+                    _device_error(names, tensors)
+                index = k
+    return index
+
+
+def _device_error(names, tensors):
+    for n, t in zip(names.split(), tensors):
+        if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda):
+            raise ValueError(f"{n} must be a device tensor")
+    on = {n: str(t.device) for n, t in zip(names.split(), tensors) if t is not None}
+    raise ValueError(f"tensors on several devices: {on}")
+
+
+@functools.lru_cache(maxsize=256)
+def _dims(kind, *fields):
+    """The dims of a call, read only, with the reference that ctypes passes:
+    equal calls share them."""
+    d = kind(*fields)
+    return d, ctypes.byref(d)
 
 
 def _addr(t):
@@ -672,8 +696,7 @@ def _rows(name, t, shape, dtype) -> int:
 _BATCHED = ("x", "r", "i")
 
 
-def _gated_setup(x, r, i, decay, c, cu_seqlens, extra):
-    dev = _same_device(x=x, r=r, i=i, decay=decay, cu_seqlens=cu_seqlens, **extra)
+def _gated_setup(x, r, i, decay, c, cu_seqlens):
     packed = cu_seqlens is not None
     if x.dim() != (2 if packed else 3):
         raise ValueError("x must be [T, D] with cu_seqlens and [Bsz, T, D] without")
@@ -686,9 +709,11 @@ def _gated_setup(x, r, i, decay, c, cu_seqlens, extra):
         _dense("cu_seqlens", cu_seqlens, (B + 1,), torch.int32)
     else:
         B, T = x.shape[:2]
-    lds = [_rows(n, t, x.shape, dt) for n, t in (("x", x), ("r", r), ("i", i))]
+    sh = x.shape
     _dense("decay", decay, (D,), torch.float32)
-    return dev, m3_gated_dims(B, T, D, code, c, *lds, 0), packed
+    d, ref = _dims(m3_gated_dims, B, T, D, code, c, _rows("x", x, sh, dt), _rows("r", r, sh, dt),
+                   _rows("i", i, sh, dt), 0)
+    return d, ref, packed
 
 
 def _nst(T):
@@ -706,21 +731,22 @@ def gated_scan(x, r, i, decay, h0=None, c=8.0, cu_seqlens=None, want_hT=True, wa
     """The gated linear recurrence over x, r, i [Bsz, T, D], or packed [T, D]
     with cu_seqlens (m3_gated_scan).  Returns (y, hT, states); states are for
     gated_scan_backward."""
-    dev, d, packed = _gated_setup(x, r, i, decay, c, cu_seqlens, dict(h0=h0))
+    dev = _same_device("x r i decay h0 cu_seqlens", x, r, i, decay, h0, cu_seqlens)
+    d, ref, packed = _gated_setup(x, r, i, decay, c, cu_seqlens)
     B, T, D = d.batch, d.seqlen, d.width
     _dense("h0", h0, (B, D), torch.float32, optional=True)
     lib = _lib()
-    with _on(dev, stream) as raw:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        hT = torch.empty((B, D), dtype=torch.float32, device=dev) if want_hT else None
+    with _on(dev, stream):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        hT = torch.empty((B, D), dtype=torch.float32, device=x.device) if want_hT else None
         st = None
         if want_states:
             st = torch.empty(((_nst(T),) if packed else (B, _nst(T))) + (D,), dtype=torch.float32,
-                             device=dev)
-        ws = _ws(lib.m3_gated_scan_workspace_size(ctypes.byref(d), packed), "m3_gated_scan", dev)
-        e = lib.m3_gated_scan(ctypes.byref(d), _addr(cu_seqlens), _addr(x), _addr(r), _addr(i),
+                             device=x.device)
+        ws = _ws(lib.m3_gated_scan_workspace_size(ref, packed), "m3_gated_scan", x.device)
+        e = lib.m3_gated_scan(ref, _addr(cu_seqlens), _addr(x), _addr(r), _addr(i),
                               _addr(decay), _addr(h0), _addr(y), _addr(hT), _addr(st), _addr(ws),
-                              ws.numel(), raw)
+                              ws.numel(), _raw(dev))
     if e != 0:
         raise M3Error(e, "m3_gated_scan")
     return y, hT, st
@@ -731,24 +757,25 @@ def gated_scan_backward(x, r, i, decay, dy, states, h0=None, dhT=None, c=8.0, cu
     """Gradients of gated_scan (m3_gated_scan_backward): a dict with x, r, i
     in their dtype, decay and (if h0 is given) h0 in fp32.  Rows that no
     sequence covers are not written."""
-    dev, d, packed = _gated_setup(x, r, i, decay, c, cu_seqlens,
-                                  dict(h0=h0, dy=dy, states=states, dhT=dhT))
+    dev = _same_device("x r i decay dy states h0 dhT cu_seqlens", x, r, i, decay, dy, states, h0,
+                       dhT, cu_seqlens)
+    d, ref, packed = _gated_setup(x, r, i, decay, c, cu_seqlens)
     B, T, D = d.batch, d.seqlen, d.width
     _dense("h0", h0, (B, D), torch.float32, optional=True)
     _dense("dhT", dhT, (B, D), torch.float32, optional=True)
     _dense("dy", dy, x.shape, x.dtype)
     _dense("states", states, ((_nst(T),) if packed else (B, _nst(T))) + (D,), torch.float32)
     lib = _lib()
-    with _on(dev, stream) as raw:
-        g = {k: torch.empty(x.shape, dtype=x.dtype, device=dev) for k in ("x", "r", "i")}
-        g["decay"] = torch.empty(D, dtype=torch.float32, device=dev)
-        g["h0"] = torch.empty((B, D), dtype=torch.float32, device=dev) if h0 is not None else None
-        ws = _ws(lib.m3_gated_scan_backward_workspace_size(ctypes.byref(d), packed),
-                 "m3_gated_scan_backward", dev)
+    with _on(dev, stream):
+        g = {k: torch.empty(x.shape, dtype=x.dtype, device=x.device) for k in ("x", "r", "i")}
+        g["decay"] = torch.empty(D, dtype=torch.float32, device=x.device)
+        g["h0"] = torch.empty((B, D), dtype=torch.float32, device=x.device) if h0 is not None else None
+        ws = _ws(lib.m3_gated_scan_backward_workspace_size(ref, packed),
+                 "m3_gated_scan_backward", x.device)
         e = lib.m3_gated_scan_backward(
-            ctypes.byref(d), _addr(cu_seqlens), _addr(x), _addr(r), _addr(i), _addr(decay), _addr(h0),
+            ref, _addr(cu_seqlens), _addr(x), _addr(r), _addr(i), _addr(decay), _addr(h0),
             _addr(states), _addr(dy), _addr(dhT), _addr(g["x"]), _addr(g["r"]), _addr(g["i"]),
-            _addr(g["decay"]), _addr(g["h0"]), _addr(ws), ws.numel(), raw)
+            _addr(g["decay"]), _addr(g["h0"]), _addr(ws), ws.numel(), _raw(dev))
     if e != 0:
         raise M3Error(e, "m3_gated_scan_backward")
     return g
@@ -757,28 +784,28 @@ def gated_scan_backward(x, r, i, decay, dy, states, h0=None, dhT=None, c=8.0, cu
 def gated_step(h, x, r, i, decay, c=8.0, y=None, stream=None):
     """Advances h [Bsz, D] (fp32, in place) by one token of x, r, i [Bsz, D];
     returns y (allocated unless given)."""
-    dev = _same_device(h=h, x=x, r=r, i=i, decay=decay, y=y)
+    dev = _same_device("h x r i decay y", h, x, r, i, decay, y)
     if h.dim() != 2:
         raise ValueError("h must be [Bsz, D]")
     B, D = h.shape
     _dense("h", h, (B, D), torch.float32)
     _dense("decay", decay, (D,), torch.float32)
-    code = dtype_code(x.dtype)
-    lds = [_rows(n, t, (B, D), x.dtype) for n, t in (("x", x), ("r", r), ("i", i))]
-    d = m3_gated_dims(B, 1, D, code, c, *lds, 0)
-    with _on(dev, stream) as raw:
+    dt, sh = x.dtype, h.shape
+    _, ref = _dims(m3_gated_dims, B, 1, D, dtype_code(dt), c, _rows("x", x, sh, dt),
+                   _rows("r", r, sh, dt), _rows("i", i, sh, dt), 0)
+    with _on(dev, stream):
         if y is None:
-            y = torch.empty((B, D), dtype=x.dtype, device=dev)
-        _dense("y", y, (B, D), x.dtype)
-        e = _lib().m3_gated_step(ctypes.byref(d), _addr(h), _addr(x), _addr(r), _addr(i),
-                                 _addr(decay), _addr(y), raw)
+            y = x.new_empty((B, D))
+        else:
+            _dense("y", y, sh, dt)
+        e = _lib().m3_gated_step(ref, _addr(h), _addr(x), _addr(r), _addr(i),
+                                 _addr(decay), _addr(y), _raw(dev))
     if e != 0:
         raise M3Error(e, "m3_gated_step")
     return y
 
 
-def _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags, extra):
-    dev = _same_device(q=q, k=k, positions=positions, q_weight=q_weight, k_weight=k_weight, **extra)
+def _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags):
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [T, heads, headdim]")
     T, Hq, D = q.shape
@@ -789,21 +816,21 @@ def _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags,
     _dense("positions", positions, (T,), torch.int32)
     _dense("q_weight", q_weight, (D,), torch.float32, optional=True)
     _dense("k_weight", k_weight, (D,), torch.float32, optional=True)
-    return dev, m3_qk_dims(T, Hq, Hk, D, D if rotary_dim is None else rotary_dim, code, flags, eps,
-                           base, ldq, ldk, 0, 0)
+    return _dims(m3_qk_dims, T, Hq, Hk, D, D if rotary_dim is None else rotary_dim, code, flags,
+                 eps, base, ldq, ldk, 0, 0)[1]
 
 
 def qk_norm_rope(q, k, positions, q_weight=None, k_weight=None, eps=1e-6, base=10000.0,
                  rotary_dim=None, flags=0, stream=None):
     """RMS norms of q [T, Hq, D] and k [T, Hk, D] per head and their rotation
     by position (m3_qk_norm_rope).  Returns (q_out, k_out)."""
-    dev, d = _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags, {})
-    with _on(dev, stream) as raw:
-        qo = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        ko = torch.empty(k.shape, dtype=q.dtype, device=dev)
-        e = _lib().m3_qk_norm_rope(ctypes.byref(d), _addr(q), _addr(k), _addr(q_weight),
+    dev = _same_device("q k positions q_weight k_weight", q, k, positions, q_weight, k_weight)
+    ref = _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags)
+    with _on(dev, stream):
+        qo, ko = q.new_empty(q.shape), k.new_empty(k.shape)
+        e = _lib().m3_qk_norm_rope(ref, _addr(q), _addr(k), _addr(q_weight),
                                    _addr(k_weight), _addr(positions), _addr(qo), _addr(ko),
-                                   raw)
+                                   _raw(dev))
     if e != 0:
         raise M3Error(e, "m3_qk_norm_rope")
     return qo, ko
@@ -813,29 +840,29 @@ def qk_norm_rope_backward(q, k, positions, dq_out, dk_out, q_weight=None, k_weig
                           base=10000.0, rotary_dim=None, flags=0, stream=None) -> dict:
     """Gradients of qk_norm_rope: a dict with q, k in their dtype and, for the
     weights that are given, q_weight, k_weight in fp32."""
-    dev, d = _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags,
-                       dict(dq_out=dq_out, dk_out=dk_out))
+    dev = _same_device("q k positions q_weight k_weight dq_out dk_out", q, k, positions, q_weight,
+                       k_weight, dq_out, dk_out)
+    ref = _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags)
     _dense("dq_out", dq_out, q.shape, q.dtype)
     _dense("dk_out", dk_out, k.shape, q.dtype)
     lib, f32 = _lib(), torch.float32
-    with _on(dev, stream) as raw:
-        g = dict(q=torch.empty(q.shape, dtype=q.dtype, device=dev),
-                 k=torch.empty(k.shape, dtype=q.dtype, device=dev))
+    with _on(dev, stream):
+        g = dict(q=torch.empty(q.shape, dtype=q.dtype, device=q.device),
+                 k=torch.empty(k.shape, dtype=q.dtype, device=q.device))
         for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            g[n] = None if w is None else torch.empty(w.shape, dtype=f32, device=dev)
-        ws = _ws(lib.m3_qk_norm_rope_backward_workspace_size(ctypes.byref(d)),
-                 "m3_qk_norm_rope_backward", dev)
+            g[n] = None if w is None else torch.empty(w.shape, dtype=f32, device=q.device)
+        ws = _ws(lib.m3_qk_norm_rope_backward_workspace_size(ref),
+                 "m3_qk_norm_rope_backward", q.device)
         e = lib.m3_qk_norm_rope_backward(
-            ctypes.byref(d), _addr(q), _addr(k), _addr(q_weight), _addr(k_weight), _addr(positions),
+            ref, _addr(q), _addr(k), _addr(q_weight), _addr(k_weight), _addr(positions),
             _addr(dq_out), _addr(dk_out), _addr(g["q"]), _addr(g["k"]), _addr(g["q_weight"]),
-            _addr(g["k_weight"]), _addr(ws), ws.numel(), raw)
+            _addr(g["k_weight"]), _addr(ws), ws.numel(), _raw(dev))
     if e != 0:
         raise M3Error(e, "m3_qk_norm_rope_backward")
     return g
 
 
-def _attn_setup(q, k, v, cu_q, cu_k, scale, extra):
-    dev = _same_device(q=q, k=k, v=v, cu_seqlens_q=cu_q, cu_seqlens_k=cu_k, **extra)
+def _attn_setup(q, k, v, cu_q, cu_k, scale, ld_o=0, ld_do=0):
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v must be [T, heads, headdim]")
     Tq, Hq, D = q.shape
@@ -848,21 +875,22 @@ def _attn_setup(q, k, v, cu_q, cu_k, scale, extra):
     S = cu_q.numel() - 1
     _dense("cu_seqlens_q", cu_q, (S + 1,), torch.int32)
     _dense("cu_seqlens_k", cu_k, (S + 1,), torch.int32)
-    return dev, m3_attn_dims(S, Tq, Tk, Hq, Hk, D, code, D ** -0.5 if scale is None else scale,
-                             *ld, 0, 0, 0, 0)
+    return _dims(m3_attn_dims, S, Tq, Tk, Hq, Hk, D, code, D ** -0.5 if scale is None else scale,
+                 *ld, ld_o, ld_do, 0, 0)[1]
 
 
 def attn_prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, scale=None, stream=None):
     """Causal attention of packed sequences: q [Tq, Hq, D], k and v
     [Tk, Hk, D] (m3_attn_prefill_varlen; scale D^-1/2 by default).  Returns
     (o, lse).  Rows behind the last sequence are not written."""
-    dev, d = _attn_setup(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, {})
-    with _on(dev, stream) as raw:
-        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-        e = _lib().m3_attn_prefill_varlen(ctypes.byref(d), _addr(cu_seqlens_q), _addr(cu_seqlens_k),
+    dev = _same_device("q k v cu_seqlens_q cu_seqlens_k", q, k, v, cu_seqlens_q, cu_seqlens_k)
+    ref = _attn_setup(q, k, v, cu_seqlens_q, cu_seqlens_k, scale)
+    with _on(dev, stream):
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        e = _lib().m3_attn_prefill_varlen(ref, _addr(cu_seqlens_q), _addr(cu_seqlens_k),
                                           _addr(q), _addr(k), _addr(v), _addr(o), _addr(lse),
-                                          raw)
+                                          _raw(dev))
     if e != 0:
         raise M3Error(e, "m3_attn_prefill_varlen")
     return o, lse
@@ -871,19 +899,20 @@ def attn_prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, scale=None, stream=
 def attn_prefill_varlen_backward(q, k, v, o, lse, d_o, cu_seqlens_q, cu_seqlens_k, scale=None,
                                  stream=None):
     """Gradients of attn_prefill_varlen for d_o: (dq, dk, dv)."""
-    dev, d = _attn_setup(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, dict(o=o, lse=lse, d_o=d_o))
-    d.ld_o = _rows("o", o, q.shape, q.dtype)
-    d.ld_do = _rows("d_o", d_o, q.shape, q.dtype)
+    dev = _same_device("q k v o lse d_o cu_seqlens_q cu_seqlens_k", q, k, v, o, lse, d_o,
+                       cu_seqlens_q, cu_seqlens_k)
+    ref = _attn_setup(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, _rows("o", o, q.shape, q.dtype),
+                      _rows("d_o", d_o, q.shape, q.dtype))
     _dense("lse", lse, q.shape[:2], torch.float32)
     lib = _lib()
-    with _on(dev, stream) as raw:
-        dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=dev) for t in (q, k, v))
-        ws = _ws(lib.m3_attn_prefill_varlen_backward_workspace_size(ctypes.byref(d)),
-                 "m3_attn_prefill_varlen_backward", dev)
+    with _on(dev, stream):
+        dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
+        ws = _ws(lib.m3_attn_prefill_varlen_backward_workspace_size(ref),
+                 "m3_attn_prefill_varlen_backward", q.device)
         e = lib.m3_attn_prefill_varlen_backward(
-            ctypes.byref(d), _addr(cu_seqlens_q), _addr(cu_seqlens_k), _addr(q), _addr(k), _addr(v),
+            ref, _addr(cu_seqlens_q), _addr(cu_seqlens_k), _addr(q), _addr(k), _addr(v),
             _addr(o), _addr(lse), _addr(d_o), _addr(dq), _addr(dk), _addr(dv), _addr(ws), ws.numel(),
-            raw)
+            _raw(dev))
     if e != 0:
         raise M3Error(e, "m3_attn_prefill_varlen_backward")
     return dq, dk, dv
@@ -892,7 +921,7 @@ def attn_prefill_varlen_backward(q, k, v, o, lse, d_o, cu_seqlens_q, cu_seqlens_
 def attn_decode(q, k_cache, v_cache, lengths, scale=None, o=None, ws=None, stream=None):
     """One token per sequence, q [S, Hq, D], against caches [S, cap, Hk, D]
     holding lengths[s] rows (m3_attn_decode).  Returns (o, lse)."""
-    dev = _same_device(q=q, k_cache=k_cache, v_cache=v_cache, lengths=lengths, o=o, ws=ws)
+    dev = _same_device("q k_cache v_cache lengths o ws", q, k_cache, v_cache, lengths, o, ws)
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [S, Hq, D], the caches [S, cap, Hk, D]")
     S, Hq, D = q.shape
@@ -906,20 +935,20 @@ def attn_decode(q, k_cache, v_cache, lengths, scale=None, o=None, ws=None, strea
             raise ValueError(f"{n}: sequences must not share rows")
         strides.append((_rows(n, t[0], (cap, Hk, D), q.dtype), t.stride(0) if S > 1 else 0))
     _dense("lengths", lengths, (S,), torch.int32)
-    d = m3_attn_dims(S, 0, cap, Hq, Hk, D, code, D ** -0.5 if scale is None else scale,
-                     _rows("q", q, (S, Hq, D), q.dtype), strides[0][0], strides[1][0], 0, 0,
-                     strides[0][1], strides[1][1])
+    _, ref = _dims(m3_attn_dims, S, 0, cap, Hq, Hk, D, code, D ** -0.5 if scale is None else scale,
+                   _rows("q", q, (S, Hq, D), q.dtype), strides[0][0], strides[1][0],
+                   0 if o is None else _rows("o", o, q.shape, q.dtype), 0, strides[0][1],
+                   strides[1][1])
     lib = _lib()
-    with _on(dev, stream) as raw:
+    with _on(dev, stream):
         if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        d.ld_o = _rows("o", o, q.shape, q.dtype)
-        lse = torch.empty((S, Hq), dtype=torch.float32, device=dev)
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty((S, Hq), dtype=torch.float32, device=q.device)
         if ws is None:
-            ws = _ws(lib.m3_attn_decode_workspace_size(ctypes.byref(d)), "m3_attn_decode", dev)
-        e = lib.m3_attn_decode(ctypes.byref(d), _addr(lengths), _addr(q), _addr(k_cache),
+            ws = _ws(lib.m3_attn_decode_workspace_size(ref), "m3_attn_decode", q.device)
+        e = lib.m3_attn_decode(ref, _addr(lengths), _addr(q), _addr(k_cache),
                                _addr(v_cache), _addr(o), _addr(lse), _addr(ws),
-                               ws.numel() * ws.element_size(), raw)
+                               ws.numel() * ws.element_size(), _raw(dev))
     if e != 0:
         raise M3Error(e, "m3_attn_decode")
     return o, lse

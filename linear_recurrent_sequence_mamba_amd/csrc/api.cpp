@@ -267,8 +267,10 @@ m3::QkNormArgs qk_args(const m3_qk_dims* d) {
   a.ldk = d->ld_k ? d->ld_k : wk;
   a.ld_dq = d->ld_dq ? d->ld_dq : wq;
   a.ld_dk = d->ld_dk ? d->ld_dk : wk;
-  const double turn = 0.15915494309189533577;   // 1 / (2 pi)
-  for (int j = 0; j < a.rot / 2; ++j) a.freq[j] = turn * pow(d->base, -2.0 * j / a.rot);
+  // by products: 128 of them are off by 2^-46, far below the phase's fp32
+  const double next = a.rot ? pow(d->base, -2.0 / a.rot) : 0.0;
+  double f = 0.15915494309189533577;   // 1 / (2 pi)
+  for (int j = 0; j < a.rot / 2; ++j, f *= next) a.freq[j] = f;
   return a;
 }
 

@@ -123,6 +123,14 @@ __device__ __forceinline__ void grad_step(f16v* sum, f16v& s, f16v& s2, const Fr
   }
 }
 
+// D_i = <o_i, do_i> takes o as it was rounded, from weights that were.  Over n
+// keys of like weight that moves dq and dk by sqrt(2 / n) of their own
+// rounding, which only counts where n is small: blocks that see at most this
+// many keys sum p dp instead, before anything else, and leave it to dk.  (All
+// blocks would cost a sixth of the gradients' time; a long row whose weight is
+// on a few keys keeps the larger error, up to 1.9 roundings.)
+constexpr int kExactD = 512;
+
 // ---------------------------------------------------------------------------
 // dq: 32 queries a wave, tiles of 32 keys in LDS
 template <typename T, int D, int WAVES>
@@ -155,7 +163,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   }
   const float* st = a.stat + static_cast<int64_t>(h) * a.Tq + row;
   const float lse = st[0] == -INFINITY ? INFINITY : st[0];   // no key: every weight 0
-  const float dd = st[static_cast<int64_t>(a.Hq) * a.Tq];
+  float dd = st[static_cast<int64_t>(a.Hq) * a.Tq];
   f16v dq[D / 32];
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) dq[d] = f16v{};
@@ -166,6 +174,30 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   const T* kp = static_cast<const T*>(a.k) + static_cast<int64_t>(k0) * a.ldk + hk * D;
   const T* vp = static_cast<const T*>(a.v) + static_cast<int64_t>(k0) * a.ldv + hk * D;
   f16v s, s2;
+  if (most > 0 && most <= kExactD) {
+    // D = sum_j p_ij dp_ij instead of <o, do>, for dk as well
+    float r = 0.0f;
+#pragma unroll 1
+    for (int t = 0; t < ntile; ++t) {
+      L::template load2<WAVES>(sKV[0], kp, a.ldk, vp, a.ldv, t * BN, Lk - 1, wave, lane);
+      lds_loads_done();
+      __syncthreads();
+      s = f16v{};
+      s2 = f16v{};
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        s = mma(L::frag(sKV[0], 0, kk, lane), q[kk], s);
+        s2 = mma(L::frag(sKV[0], 32, kk, lane), g[kk], s2);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (t * BN + row_of(e, half) < sees)
+          r = fmaf(__builtin_amdgcn_exp2f(fmaf(s[e], c, -lse)), s2[e], r);
+      __syncthreads();
+    }
+    dd = half_sum(r);
+    if (half == 0 && i < Lq) a.stat[(static_cast<int64_t>(a.Hq) + h) * a.Tq + row] = dd;
+  }
   if (ntile > 0) {
     L::template load2<WAVES>(sKV[0], kp, a.ldk, vp, a.ldv, 0, Lk - 1, wave, lane);
     lds_loads_done();
@@ -339,16 +371,17 @@ hipError_t run(const AttnArgs& a, hipStream_t s) {
   const int64_t nk = (static_cast<int64_t>(a.Tk) / B + a.S) * a.Hk * a.gsplit;
   k_attn_dkv<T, D, W, false><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
+  const int64_t nq = (static_cast<int64_t>(a.Tq) / B + a.S) * a.Hq;
+  k_attn_dq<T, D, W><<<static_cast<unsigned>(nq), 64 * W, 0, s>>>(a);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
   k_attn_dkv<T, D, W, true><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (a.gsplit > 1) {
     const int64_t n = static_cast<int64_t>(a.Tk) * a.Hk * D / 4;
     k_attn_sum<T><<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    e = hipGetLastError();
   }
-  const int64_t nq = (static_cast<int64_t>(a.Tq) / B + a.S) * a.Hq;
-  k_attn_dq<T, D, W><<<static_cast<unsigned>(nq), 64 * W, 0, s>>>(a);
-  return hipGetLastError();
+  return e;
 }
 
 constexpr size_t up256(size_t n) { return (n + 255) / 256 * 256; }

@@ -47,6 +47,7 @@ __global__ __launch_bounds__(256) void k_attn_stat(AttnArgs a) {
 // One step of a sum over tiles of 32 rows, the same for the three gradients:
 //   kDv  lanes are keys, rows queries: sum += p^T do
 //   kDk  lanes are keys, rows queries: sum += ds^T q
+//   kDkv both, sum for dk and sum2 for dv
 //   kDq  lanes are queries, rows keys: sum += ds k
 // A tile holds the rows that s is formed of (q, q, k) and, from row 32 on, the
 // others (do, do, v); x and y are the lanes' own (k v, k v, q do).  From s of
@@ -56,22 +57,26 @@ __global__ __launch_bounds__(256) void k_attn_stat(AttnArgs a) {
 // two steps on: dp's products beside the exponentials, those of the next s
 // beside the rest of ds.  Rows count from `edge` on (kDq: up to it), the lane's
 // own offset 4 (lane / 32) taken off.
-enum { kDv = 0, kDk = 1, kDq = 2 };
+enum { kDv = 0, kDk = 1, kDq = 2, kDkv = 3 };
 template <typename T, int D, int KIND>
-__device__ __forceinline__ void grad_step(f16v* sum, f16v& s, f16v& s2, const Frag<T>* x,
+__device__ __forceinline__ void grad_step(f16v* sum, f16v* sum2, f16v& s, f16v& s2, const Frag<T>* x,
                                           const Frag<T>* y, const char* cur, const char* nxt,
                                           const float* stat, float lse, float dd, float c, int edge,
                                           int lane) {
   using L = Tile<T, D>;
   constexpr bool DS = KIND != kDv;
   constexpr int N1 = D / 16;                  // products of each kind
-  constexpr int A = DS ? N1 : 0, B = A + N1;  // first product of s2, of the sum
+  constexpr int A = DS ? N1 : 0, B = A + N1;  // first product of s2, of the first sum
+  constexpr int C = KIND == kDkv ? B + N1 : B;        // ... of dk's
+  // steps over which the weights are spread: beside dp's products, or until
+  // dv's sum needs them; and those of ds, which follows dp
+  constexpr int SW = KIND == kDv || KIND == kDkv ? B + N1 / 2 : A, SD = C + N1 / 2 - A - 1;
   const int half = lane >> 5;
   auto operand = [&](int n) __attribute__((always_inline)) -> Frag<T> {
     if (n < A) return L::frag(cur, 32, n, lane);
     if (n < B) return L::frag(nxt, 0, n - A, lane);
-    const int m = n - B;
-    return L::frag_t(cur, (DS ? 0 : 32) + 16 * (m / (N1 / 2)), 32 * (m % (N1 / 2)), lane);
+    const int m = (n - B) % N1;
+    return L::frag_t(cur, (DS && n >= C ? 0 : 32) + 16 * (m / (N1 / 2)), 32 * (m % (N1 / 2)), lane);
   };
   // lse (which = 0) or D (1) of the rows 8 b + 4 half + 0 .. 3; of queries as
   // lanes they are the lane's own
@@ -82,38 +87,38 @@ __device__ __forceinline__ void grad_step(f16v* sum, f16v& s, f16v& s2, const Fr
   f16v dp;
   if (DS) dp = f16v{};
   s2 = f16v{};
-  Frag<T> op[3], f[2];
+  Frag<T> op[3], f[2], f2_[2];
   f4 l4[2], d4[2];
   l4[0] = stats(0, 0);
   op[0] = operand(0);
   op[1] = operand(1);
-  float w8[8];
+  float w8[8], v8[8];
 #pragma unroll
-  for (int n = 0; n < B + N1; ++n) {
-    if (n + 2 < B + N1) op[(n + 2) % 3] = operand(n + 2);
+  for (int n = 0; n < C + N1; ++n) {
+    if (n + 2 < C + N1) op[(n + 2) % 3] = operand(n + 2);
     if (n < A) {
       dp = mma(op[n % 3], y[n], dp);
     } else if (n < B) {
       s2 = mma(op[n % 3], x[n - A], s2);
     } else {
-      const int m = n - B, w = m / (N1 / 2), d = m % (N1 / 2);
-      sum[d] = mma(op[n % 3], f[w], sum[d]);
+      const int m = (n - B) % N1, w = m / (N1 / 2), d = m % (N1 / 2);
+      if (n < C) sum2[d] = mma(op[n % 3], f2_[w], sum2[d]);
+      else sum[d] = mma(op[n % 3], f[w], sum[d]);
     }
     if (DS && n == A - 1) d4[0] = stats(1, 0);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      // the weights: beside dp's products; dv's until its sum needs them
-      if ((DS ? e * N1 / 16 : e * (N1 + N1 / 2) / 16) == n) {
+      if (e * SW / 16 == n) {
         if (e % 4 == 0 && e < 12) l4[(e / 4 + 1) & 1] = stats(0, e / 4 + 1);
         float w = __builtin_amdgcn_exp2f(fmaf(s[e], c, -l4[(e / 4) & 1][e % 4]));
         w = (KIND == kDq ? row_of(e, 0) < edge : row_of(e, 0) >= edge) ? w : 0.0f;
         s[e] = w;
-        if (!DS) {
-          w8[e % 8] = w;
-          if (e % 8 == 7) frag_from(f[e / 8], w8);
+        if (KIND == kDv || KIND == kDkv) {
+          v8[e % 8] = w;
+          if (e % 8 == 7) frag_from(KIND == kDv ? f[e / 8] : f2_[e / 8], v8);
         }
       }
-      if (DS && A + 1 + e * (N1 + N1 / 2 - 1) / 16 == n) {
+      if (DS && A + 1 + e * SD / 16 == n) {
         if (e % 4 == 0 && e < 12) d4[(e / 4 + 1) & 1] = stats(1, e / 4 + 1);
         w8[e % 8] = s[e] * (dp[e] - d4[(e / 4) & 1][e % 4]);
         if (e % 8 == 7) frag_from(f[e / 8], w8);
@@ -213,7 +218,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
     __syncthreads();   // tile t + 1 is there; every wave is done with t - 1
     const int nxt = cur == 2 ? 0 : cur + 1, aft = nxt == 2 ? 0 : nxt + 1;
     if (t + 2 < ntile) L::template load2<WAVES>(sKV[aft], kp, a.ldk, vp, a.ldv, (t + 2) * BN, Lk - 1, wave, lane);
-    grad_step<T, D, kDq>(dq, s, s2, q, g, sKV[cur], sKV[nxt], nullptr, lse, dd, c, sees - t * BN - 4 * half, lane);
+    grad_step<T, D, kDq>(dq, nullptr, s, s2, q, g, sKV[cur], sKV[nxt], nullptr, lse, dd, c, sees - t * BN - 4 * half, lane);
     cur = nxt;
   };
   for (int t = 0; t < ntile; t += 2) {   // by two: the scores change places
@@ -237,7 +242,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
 // leaves one wave a SIMD and copies between the halves of its register file
 // (8192 packed rows, 16 heads of 128 on 2: 600 us, against 162 + 202 us).
 
-template <typename T, int D, int WAVES, bool DK>
+template <typename T, int D, int WAVES, int KIND>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn_dkv(AttnArgs a) {
   using L = Tile<T, D>;
   constexpr int BK = 32 * WAVES, BQ = 32;
@@ -265,12 +270,12 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       frag_load(k[kk], p + 16 * kk);
-      if (DK) frag_load(v[kk], r + 16 * kk);
+      if (KIND != kDv) frag_load(v[kk], r + 16 * kk);
     }
   }
-  f16v sum[D / 32];
+  f16v sum[D / 32], sum2[D / 32];
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d) sum[d] = f16v{};
+  for (int d = 0; d < D / 32; ++d) sum[d] = sum2[d] = f16v{};
   const float c = a.scale * kLog2eA;
   // the first query that sees the block's first key, in whole tiles
   const int first = max(0, j0 - off) / BQ;
@@ -310,8 +315,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
     if (n + 2 < all) fetch(aft);
     const int i0 = ci * BQ;
     // rows i >= j - off count
-    grad_step<T, D, DK ? kDk : kDv>(sum, s, s2, k, v, sQG[cur], sQG[nxt], sS[cur], 0.0f, 0.0f, c,
-                                    j - off - i0 - 4 * half, lane);
+    grad_step<T, D, KIND>(sum, sum2, s, s2, k, v, sQG[cur], sQG[nxt], sS[cur], 0.0f, 0.0f, c,
+                          j - off - i0 - 4 * half, lane);
     cur = nxt;
     if (++ci == first + nt) ci = first;
   };
@@ -320,19 +325,23 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
     if (n + 1 < all) step(n + 1, s2, s);
   }
   if (j >= Lk) return;
-  const float f = DK && a.gsplit == 1 ? a.scale : 1.0f;   // parts are scaled where they are added
   const int64_t at = (row * a.Hk + hk) * D + 4 * half;
-  T* o = static_cast<T*>(DK ? a.dk : a.dv) + at;
-  float* op = (DK ? a.pk : a.pv) + static_cast<int64_t>(part) * a.Tk * a.Hk * D + at;
+  const int64_t to = static_cast<int64_t>(part) * a.Tk * a.Hk * D + at;
+  // parts are scaled where they are added
+  auto store = [&](const f16v* x, void* o, float* parts, float f) __attribute__((always_inline)) {
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d)
+    for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x0 = sum[d][4 * e] * f, x1 = sum[d][4 * e + 1] * f, x2 = sum[d][4 * e + 2] * f,
-                  x3 = sum[d][4 * e + 3] * f;
-      if (a.gsplit == 1) put4(o + 32 * d + 8 * e, x0, x1, x2, x3);
-      else put4(op + 32 * d + 8 * e, x0, x1, x2, x3);
-    }
+      for (int e = 0; e < 4; ++e) {
+        const float x0 = x[d][4 * e], x1 = x[d][4 * e + 1], x2 = x[d][4 * e + 2], x3 = x[d][4 * e + 3];
+        if (a.gsplit == 1)
+          put4(static_cast<T*>(o) + at + 32 * d + 8 * e, x0 * f, x1 * f, x2 * f, x3 * f);
+        else
+          put4(parts + to + 32 * d + 8 * e, x0, x1, x2, x3);
+      }
+  };
+  if (KIND != kDv) store(sum, a.dk, a.pk, a.scale);
+  if (KIND != kDk) store(KIND == kDv ? sum : sum2, a.dv, a.pv, 1.0f);
 }
 
 // adds the parts of a group in order, for the rows that belong to a sequence
@@ -369,12 +378,17 @@ hipError_t run(const AttnArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t nk = (static_cast<int64_t>(a.Tk) / B + a.S) * a.Hk * a.gsplit;
-  k_attn_dkv<T, D, W, false><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
   const int64_t nq = (static_cast<int64_t>(a.Tq) / B + a.S) * a.Hq;
   k_attn_dq<T, D, W><<<static_cast<unsigned>(nq), 64 * W, 0, s>>>(a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  k_attn_dkv<T, D, W, true><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
+  // dk after dq, which may have left it a better D
+  if constexpr (D == 64) {
+    k_attn_dkv<T, D, W, kDkv><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
+  } else {
+    k_attn_dkv<T, D, W, kDv><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    k_attn_dkv<T, D, W, kDk><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
+  }
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (a.gsplit > 1) {
     const int64_t n = static_cast<int64_t>(a.Tk) * a.Hk * D / 4;

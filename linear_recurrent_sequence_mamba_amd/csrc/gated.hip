@@ -89,22 +89,6 @@ __device__ __forceinline__ void decay_of(float l, float& a, float& m2) {
 }
 
 // ---------------------------------------------------------------------------
-// Carries between the time tiles of one channel.  A tile's workgroup takes a
-// ticket when it starts; tickets run over the tiles in the order in which the
-// carry moves, so whoever waits for a carry waits for a workgroup that has
-// started already and that waits, in turn, only for earlier tickets: every
-// wait ends.  Value and flag travel in one 8-byte word, which needs no fence.
-__device__ __forceinline__ void publish(u64* slot, float v) {
-  __hip_atomic_store(slot, (u64{1} << 32) | __float_as_uint(v), __ATOMIC_RELAXED,
-                     __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float await_carry(const u64* slot) {
-  u64 w;
-  while (((w = __hip_atomic_load(slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) >> 32) == 0)
-    __builtin_amdgcn_s_sleep(1);
-  return __uint_as_float(static_cast<uint32_t>(w));
-}
-
 // Joining affine maps of a carry: after `h + p * c`.  In packed calls a row
 // that starts (ends) a sequence cuts the carry off: its p is kReset, and what
 // was carried up to there is dropped by a select, so that a NaN or an
@@ -124,6 +108,75 @@ __device__ __forceinline__ float join_p(float p, float cp) {
   return is_reset<PACKED>(p) ? p : cp * p;
 }
 
+// The carry from time tile to time tile of one channel.  A tile is a map
+// h -> H + P h.  Each publishes its map as soon as it has it; tiles come in
+// groups of kGroup, and only the last tile of a group publishes the state
+// after it.  A tile starts from the state before its group and applies the
+// maps of the tiles before it in the group, always in that order, so results
+// do not depend on timing, and the wait for a state passes from group to group
+// instead of from tile to tile (about 0.8 us each).
+//
+// A workgroup takes a ticket when it starts; tickets run over the tiles in the
+// order in which the carry moves, so whoever waits, waits for a workgroup that
+// has started already and that waits, in turn, only for earlier tickets: every
+// wait ends.  A slot is one 8-byte word, which needs no fence: a map's P and H
+// (or 0 and a state), all ones until it is there (a NaN is published as the
+// usual one, which has fewer).
+constexpr int kGroup = 8;
+constexpr u64 kNotYet = ~u64{0};
+__device__ __forceinline__ void publish(u64* slot, float p, float h) {
+  const uint32_t hi = p == p ? __float_as_uint(p) : 0x7fc00000u;
+  __hip_atomic_store(slot, u64{hi} << 32 | __float_as_uint(h), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ u64 peek(const u64* slot) {
+  return __hip_atomic_load(slot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ bool ready(u64 w) { return static_cast<uint32_t>(w >> 32) != 0xffffffffu; }
+
+// Slots of tile n (in the order of the carry) of a chain, for one lane.
+struct Carry {
+  u64 *maps, *states;   // of the first tile of its group; before its group
+  int64_t stride;
+  int r, n0;
+  bool more;            // tiles follow
+  __device__ __forceinline__ Carry(const GatedArgs& g, int n, int chain, int lane)
+      : stride(static_cast<int64_t>(g.nchain) * 64), r(n % kGroup), n0(n - n % kGroup),
+        more(n + 1 < g.ntile) {
+    maps = g.slots + n0 * stride + chain * 64 + lane;
+    states = g.slots + (g.ntile + n0 / kGroup - 1) * stride + chain * 64 + lane;
+  }
+  // the tile's own map
+  __device__ __forceinline__ void give(float P, float H) const {
+    if (r + 1 < kGroup && more) publish(maps + r * stride, P, H);
+  }
+  // wave w fetches the w-th map before the tile, the last one the state before the group
+  __device__ __forceinline__ void fetch(u64 (*s)[64], int w, int lane) const {
+    static_assert(kGroup <= 8, "a wave for each");
+    const u64* slot = w < r ? maps + w * stride : states;
+    if (w < r || (w == kGroup - 1 && n0 > 0)) {
+      u64 m;
+      while (!ready(m = peek(slot))) __builtin_amdgcn_s_sleep(1);
+      s[w][lane] = m;
+    }
+  }
+  // the state before the tile from what was fetched
+  template <bool PACKED>
+  __device__ __forceinline__ float take(const u64 (*s)[64], int lane, float first) const {
+    float h = n0 > 0 ? __uint_as_float(static_cast<uint32_t>(s[kGroup - 1][lane])) : first;
+    for (int k = 0; k < r; ++k) {
+      const u64 m = s[k][lane];
+      h = join<PACKED>(__uint_as_float(static_cast<uint32_t>(m >> 32)), h,
+                       __uint_as_float(static_cast<uint32_t>(m)));
+    }
+    return h;
+  }
+  // the state after the tile, from the last of a group
+  __device__ __forceinline__ void pass_on(float h) const {
+    if (r + 1 == kGroup && more) publish(states + stride, 0.0f, h);
+  }
+};
+
 // Clears the ticket counter and the carry slots; for packed calls also writes
 // the clean offsets (clamped into [0, T] and raised to the largest one before)
 // and gives the state rows of empty sequences their value (src row or 0).
@@ -131,7 +184,7 @@ __global__ void k_gated_init(GatedArgs a, const float* src, float* dst, int64_t 
   const int tid = threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + tid; i < nslot / 2; i += step)
-    reinterpret_cast<ulonglong2*>(a.slots)[i] = ulonglong2{0, 0};   // 64 slots to a chain
+    reinterpret_cast<ulonglong2*>(a.slots)[i] = ulonglong2{kNotYet, kNotYet};   // 64 slots to a chain
   if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;
   if (!a.cu) return;
   __shared__ int part[256];
@@ -219,7 +272,9 @@ template <typename T, int V, int TOK, int WAVES, bool PACKED>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
   constexpr int TILE = TOK * WAVES;
   static_assert(TOK <= 32 && kGatedChunk % TOK == 0, "rows of a window in 32 bits");
+  static_assert(V == 1 && WAVES >= kGroup, "a wave for each slot before a tile");
   __shared__ float sH[WAVES][64 * V], sP[WAVES][64 * V], sC[64 * V];
+  __shared__ u64 sM[kGroup][64];
   const unsigned n = take_ticket(g);
   const int tile = static_cast<int>(n / g.nchain), chain = static_cast<int>(n % g.nchain);
   const int b = chain / g.ncb, cb = chain % g.ncb;
@@ -299,21 +354,17 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
       cH[v] = join<PACKED>(p, cH[v], sH[u][lane * V + v]);
       cP[v] = join_p<PACKED>(p, cP[v]);
     }
-  if (wave == WAVES - 1) {
-    u64* slot = g.slots + (static_cast<int64_t>(tile) * g.nchain + chain) * (64 * V) + lane * V;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (tile == 0)
-        carry[v] = !PACKED && g.h0 ? g.h0[static_cast<int64_t>(b) * g.D + chc + v] : 0.0f;
-      else
-        carry[v] = await_carry(slot - static_cast<int64_t>(g.nchain) * (64 * V) + v);
-      if (tile + 1 < g.ntile) publish(slot + v, join<PACKED>(P[v], join<PACKED>(cP[v], carry[v], cH[v]), h[v]));
-      sC[lane * V + v] = carry[v];
-    }
-  }
+  const Carry cr(g, tile, chain, lane);
+  const float tP = join_p<PACKED>(P[0], cP[0]), tH = join<PACKED>(P[0], cH[0], h[0]);
+  if (wave == WAVES - 1) cr.give(tP, tH);   // the last wave's is the tile's
+  cr.fetch(sM, wave, lane);
+  float first = 0.0f;
+  if (!PACKED && cr.n0 == 0 && g.h0) first = g.h0[static_cast<int64_t>(b) * g.D + chc];
   __syncthreads();
+  const float before = cr.take<PACKED>(sM, lane, first);
+  if (wave == WAVES - 1) cr.pass_on(join<PACKED>(tP, before, tH));
 #pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = join<PACKED>(cP[v], sC[lane * V + v], cH[v]);
+  for (int v = 0; v < V; ++v) carry[v] = join<PACKED>(cP[v], before, cH[v]);
   if (!on) return;
   if (g.states && t0 % kGatedChunk == 0 && t0 < g.T) {
     const int64_t nst = (g.T + kGatedChunk - 1) / kGatedChunk;
@@ -360,7 +411,9 @@ template <typename T, int V, int TOK, int WAVES, bool PACKED>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_backward(GatedArgs g) {
   constexpr int TILE = TOK * WAVES;
   static_assert(TILE == kGatedChunk && TOK <= 32, "one saved state per tile; rows of a window in 32 bits");
+  static_assert(V == 1 && WAVES >= kGroup, "a wave for each slot before a tile");
   __shared__ float sH[WAVES][64 * V], sP[WAVES][64 * V], sC[64 * V];
+  __shared__ u64 sM[kGroup][64];
   const unsigned n = take_ticket(g);
   const int tile = g.ntile - 1 - static_cast<int>(n / g.nchain);
   const int chain = static_cast<int>(n % g.nchain);
@@ -522,24 +575,21 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_backward(GatedArgs g) {
       cH[v] = join<PACKED>(p, cH[v], sH[u][lane * V + v]);
       cP[v] = join_p<PACKED>(p, cP[v]);
     }
-  if (wave == 0) {
-    u64* slot = g.slots + (static_cast<int64_t>(tile) * g.nchain + chain) * (64 * V) + lane * V;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float c;
-      if (tile == g.ntile - 1)
-        c = !PACKED && g.dhT ? g.dhT[static_cast<int64_t>(b) * g.D + chc + v] : 0.0f;
-      else
-        c = await_carry(slot + static_cast<int64_t>(g.nchain) * (64 * V) + v);
-      const float q0 = join<PACKED>(P[v], join<PACKED>(cP[v], c, cH[v]), q[v]);
-      if (tile > 0) publish(slot + v, q0);
-      else if (!PACKED && on && g.dh0) g.dh0[static_cast<int64_t>(b) * g.D + ch + v] = q0;
-      sC[lane * V + v] = c;
-    }
-  }
+  const Carry cr(g, g.ntile - 1 - tile, chain, lane);
+  const float tP = join_p<PACKED>(P[0], cP[0]), tH = join<PACKED>(P[0], cH[0], q[0]);
+  if (wave == 0) cr.give(tP, tH);   // the first wave's is the tile's
+  cr.fetch(sM, wave, lane);
+  float last = 0.0f;
+  if (!PACKED && cr.n0 == 0 && g.dhT) last = g.dhT[static_cast<int64_t>(b) * g.D + chc];
   __syncthreads();
+  const float after = cr.take<PACKED>(sM, lane, last);
+  if (wave == 0) {
+    const float q0 = join<PACKED>(tP, after, tH);
+    cr.pass_on(q0);
+    if (!PACKED && tile == 0 && on && g.dh0) g.dh0[static_cast<int64_t>(b) * g.D + ch] = q0;
+  }
 #pragma unroll
-  for (int v = 0; v < V; ++v) q[v] = join<PACKED>(cP[v], sC[lane * V + v], cH[v]);
+  for (int v = 0; v < V; ++v) q[v] = join<PACKED>(cP[v], after, cH[v]);
 
   // backward again, now with q: the gradients
   float dk[V];
@@ -670,14 +720,17 @@ hipError_t run_scan(GatedArgs& g, hipStream_t s) {
     k_gated_scan<T, V, TOK, WAVES, false><<<grid, 64 * WAVES, 0, s>>>(g);
   return hipGetLastError();
 }
-// The dense kernel's 16 rows a wave just fit 128 registers; the packed one's
-// windows do not (19 spilled: 155 us against 111 us for 8192 rows of 2048
-// channels), so its waves take 8 rows, twice as many waves to a tile.
+// 16 rows a wave just fit 128 registers in the dense bf16 kernel (4 x 2048 x
+// 4096: 127 us, with 8 rows and twice the waves 166 us).  Windows of packed
+// rows and fp32 inputs do not fit (fp32: 327 us, with 8 rows 199 us; packed
+// 8192 x 2048 in bf16 155 and 110 us).
 template <typename T>
 hipError_t run_backward(GatedArgs& g, hipStream_t s) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(g.ntile) * g.nchain);
   if (g.cu)
     k_gated_backward<T, 1, 8, kGatedChunk / 8, true><<<grid, 8 * kGatedChunk, 0, s>>>(g);
+  else if constexpr (sizeof(T) == 4)
+    k_gated_backward<T, 1, 8, kGatedChunk / 8, false><<<grid, 8 * kGatedChunk, 0, s>>>(g);
   else
     k_gated_backward<T, 1, 16, kGatedChunk / 16, false><<<grid, 4 * kGatedChunk, 0, s>>>(g);
   return hipGetLastError();
@@ -698,10 +751,10 @@ constexpr size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 // Tiles of the scan: 256 rows, or 512 where all workgroups of 256 would be
-// resident at once (two a CU).  Then the time is that of handing the carry
-// from tile to tile, about 0.8 us each, and half as many tiles take less:
-// 16384 rows of 512 channels 37 against 52 us, of 4096 channels 161 against
-// 126 us.
+// resident at once (two a CU).  Then the time is that of a tile and of the
+// carry passing on, and fewer, larger tiles take less: 16384 rows of 512
+// channels 27 against 31 us, of 4096 channels 162 against 128 us.  (128 rows:
+// 35 and 132 us.)
 GatedPlan gated_plan(int B, int T, int D, bool packed, bool backward) {
   GatedPlan p;
   p.ncb = (D + 63) / 64;
@@ -712,10 +765,15 @@ GatedPlan gated_plan(int B, int T, int D, bool packed, bool backward) {
   return p;
 }
 
+// a word for every tile's map and for the state after every whole group
+static int64_t gated_slots(const GatedPlan& p) {
+  return 64 * p.nchain * (p.ntile + p.ntile / kGroup);
+}
+
 size_t gated_workspace_bytes(int B, int T, int D, bool packed, bool backward) {
   const GatedPlan p = gated_plan(B, T, D, packed, backward);
   size_t n = 256 + up256(sizeof(int32_t) * (static_cast<size_t>(B) + 1));
-  n += up256(sizeof(u64) * 64 * p.nchain * p.ntile);
+  n += up256(sizeof(u64) * gated_slots(p));
   if (backward) n += up256(sizeof(float) * D * (packed ? 1 : B) * p.ntile);
   return n;
 }
@@ -731,14 +789,14 @@ void gated_carve(GatedArgs& g, bool backward, void* ws) {
   g.cuc = reinterpret_cast<int32_t*>(c);
   c += up256(sizeof(int32_t) * (static_cast<size_t>(g.B) + 1));
   g.slots = reinterpret_cast<u64*>(c);
-  c += up256(sizeof(u64) * 64 * p.nchain * p.ntile);
+  c += up256(sizeof(u64) * gated_slots(p));
   g.part = reinterpret_cast<float*>(c);
   g.S = g.B;
 }
 
 hipError_t launch_gated_scan(GatedArgs& g, int bf16, hipStream_t s) {
   const GatedPlan p = gated_plan(g.B, g.T, g.D, g.cu != nullptr, false);
-  hipError_t e = run_init(g, g.h0, g.hT, p.nchain * p.ntile* 64, s);
+  hipError_t e = run_init(g, g.h0, g.hT, gated_slots(p), s);
   if (e != hipSuccess) return e;
   if (p.tile == 512) return bf16 ? run_scan<bf16_t, 1, 32, 16>(g, s) : run_scan<float, 1, 32, 16>(g, s);
   return bf16 ? run_scan<bf16_t, 1, 32, 8>(g, s) : run_scan<float, 1, 32, 8>(g, s);
@@ -746,7 +804,7 @@ hipError_t launch_gated_scan(GatedArgs& g, int bf16, hipStream_t s) {
 
 hipError_t launch_gated_backward(GatedArgs& g, int bf16, hipStream_t s) {
   const GatedPlan p = gated_plan(g.B, g.T, g.D, g.cu != nullptr, true);
-  hipError_t e = run_init(g, g.dhT, g.dh0, p.nchain * p.ntile* 64, s);
+  hipError_t e = run_init(g, g.dhT, g.dh0, gated_slots(p), s);
   if (e != hipSuccess) return e;
   e = bf16 ? run_backward<bf16_t>(g, s) : run_backward<float>(g, s);
   if (e != hipSuccess) return e;

@@ -20,46 +20,44 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 typedef unsigned long long u64;
 
-// V consecutive channels as loaded (V = 2 needs an even channel)
-template <typename T, int V>
-using Raw = RawVec<T, V>;
-
+// V consecutive elements (1 or 8) of a row
 template <typename T, int V>
 __device__ __forceinline__ void store_v(T* p, const float* v) {
-  if constexpr (V == 1 && sizeof(T) == 4) {
-    p[0] = v[0];
-  } else if constexpr (V == 1) {
-    const bh2 b = __builtin_convertvector(f2{v[0], v[0]}, bh2);
-    p[0] = __builtin_bit_cast(T, b[0]);
+  if constexpr (V == 1) {
+    p[0] = from_f32<T>(v[0]);
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int k = 0; k < V / 2; ++k) reinterpret_cast<f2*>(p)[k] = f2{v[2 * k], v[2 * k + 1]};
+    for (int k = 0; k < V / 4; ++k)
+      reinterpret_cast<f4*>(p)[k] = f4{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
   } else {
     uint32_t w[V / 2];
 #pragma unroll
-    for (int k = 0; k < V / 2; ++k) {
-      const bh2 b = __builtin_convertvector(f2{v[2 * k], v[2 * k + 1]}, bh2);
-      w[k] = __builtin_bit_cast(uint32_t, b);
-    }
-    if constexpr (V == 8) {
-      *reinterpret_cast<uint4*>(p) = uint4{w[0], w[1], w[2], w[3]};
-    } else {
-      *reinterpret_cast<uint32_t*>(p) = w[0];
-    }
+    for (int k = 0; k < V / 2; ++k)
+      w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[2 * k], v[2 * k + 1]}, bh2));
+    *reinterpret_cast<uint4*>(p) = uint4{w[0], w[1], w[2], w[3]};
   }
 }
 
-// TOK rows from t0 on of the channels at ch.  Rows past the end repeat the
+// one element of a row whose address is uniform, off bytes on (the hardware's
+// conversion to bf16 rounds to nearest, as from_f32 does in six instructions)
+__device__ __forceinline__ void put(float* row, uint32_t off, float v) {
+  *reinterpret_cast<float*>(reinterpret_cast<char*>(row) + off) = v;
+}
+__device__ __forceinline__ void put(bf16_t* row, uint32_t off, float v) {
+  *reinterpret_cast<__bf16*>(reinterpret_cast<char*>(row) + off) = static_cast<__bf16>(v);
+}
+
+// TOK rows from t0 on of the channel at ch.  Rows past the end repeat the
 // last one.  The row's address is uniform: the lane adds a 32-bit offset.
-template <typename T, int V, int TOK>
-__device__ __forceinline__ void load_rows(Raw<T, V>* raw, const T* p, int64_t ld, int ch, int t0,
+template <typename T, int TOK>
+__device__ __forceinline__ void load_rows(Raw1<T>* raw, const T* p, int64_t ld, int ch, int t0,
                                           int T_) {
   const uint32_t off = static_cast<uint32_t>(ch) * static_cast<uint32_t>(sizeof(T));
   const char* row = reinterpret_cast<const char*>(p + min(t0, T_ - 1) * ld);
   const int64_t step = ld * static_cast<int64_t>(sizeof(T));
 #pragma unroll
   for (int j = 0; j < TOK; ++j) {
-    raw[j].load(reinterpret_cast<const T*>(row + off));
+    raw[j].load(reinterpret_cast<const T*>(row + off), 0);
     row += t0 + j + 1 < T_ ? step : 0;
     __builtin_amdgcn_sched_barrier(0);   // one row address at a time
   }
@@ -244,11 +242,7 @@ __device__ __forceinline__ Window window_of(const int32_t* cu, int S, int t0, in
   w.live &= all;
   return w;
 }
-// the next sequence after s that has rows
-__device__ __forceinline__ int next_seq(const int32_t* cu, int S, int s) {
-  do ++s; while (s < S && cu[s + 1] <= cu[s]);
-  return s;
-}
+// the sequence before s that has rows
 __device__ __forceinline__ int prev_seq(const int32_t* cu, int s) {
   do --s; while (s > 0 && cu[s + 1] <= cu[s]);
   return s;
@@ -264,24 +258,24 @@ __device__ __forceinline__ unsigned take_ticket(const GatedArgs& a) {
 }
 
 // ---------------------------------------------------------------------------
-// One workgroup: TOK * WAVES rows of 64 V channels.  A wave scans its TOK
+// One workgroup: TOK * WAVES rows of 64 channels.  A wave scans its TOK
 // rows from a zero state, keeping h and the running product of a; the waves'
 // ends are joined through LDS, the tiles' through the carry slots, and
 // y = h_local + product * carry.
-template <typename T, int V, int TOK, int WAVES, bool PACKED>
+template <typename T, int TOK, int WAVES, bool PACKED>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
   constexpr int TILE = TOK * WAVES;
   static_assert(TOK <= 32 && kGatedChunk % TOK == 0, "rows of a window in 32 bits");
-  static_assert(V == 1 && WAVES >= kGroup, "a wave for each slot before a tile");
-  __shared__ float sH[WAVES][64 * V], sP[WAVES][64 * V], sC[64 * V];
+  static_assert(WAVES >= kGroup, "a wave for each slot before a tile");
+  __shared__ float sH[WAVES][64], sP[WAVES][64], sC[64];
   __shared__ u64 sM[kGroup][64];
   const unsigned n = take_ticket(g);
   const int tile = static_cast<int>(n / g.nchain), chain = static_cast<int>(n % g.nchain);
   const int b = chain / g.ncb, cb = chain % g.ncb;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int ch = (cb * 64 + lane) * V;
+  const int ch = cb * 64 + lane;
   const bool on = ch < g.D;
-  const int chc = on ? ch : g.D - V;   // lanes past the end read the last channels
+  const int chc = on ? ch : g.D - 1;   // lanes past the end read the last channel
   const int t0 = tile * TILE + wave * TOK;
   const int64_t row0 = static_cast<int64_t>(b) * g.T;
   const T* x = static_cast<const T*>(g.x) + row0 * g.ldx;
@@ -289,73 +283,49 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
   const T* gi = static_cast<const T*>(g.i) + row0 * g.ldi;
   T* y = static_cast<T*>(g.y) + row0 * g.D;
 
-  float dec[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) dec[v] = g.decay[chc + v];
-  Raw<T, V> rx[TOK], rr[TOK], ri[TOK];
-  load_rows<T, V, TOK>(rr, r, g.ldr, chc, t0, g.T);
-  load_rows<T, V, TOK>(rx, x, g.ldx, chc, t0, g.T);
-  load_rows<T, V, TOK>(ri, gi, g.ldi, chc, t0, g.T);
-  if (wave == 0)
-#pragma unroll
-    for (int v = 0; v < V; ++v) sC[lane * V + v] = decay_factor(dec[v], g.c);
+  const float dec = g.decay[chc];
+  Raw1<T> rx[TOK], rr[TOK], ri[TOK];
+  load_rows<T, TOK>(rr, r, g.ldr, chc, t0, g.T);
+  load_rows<T, TOK>(rx, x, g.ldx, chc, t0, g.T);
+  load_rows<T, TOK>(ri, gi, g.ldi, chc, t0, g.T);
+  if (wave == 0) sC[lane] = decay_factor(dec, g.c);
   Window w{};
   if constexpr (PACKED) w = window_of(g.cuc, g.S, t0, TOK);
   __syncthreads();
-  float k[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) k[v] = sC[lane * V + v];
+  const float k = sC[lane];
 
-  float h[V], P[V], hl[TOK][V], pl[TOK][V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) { h[v] = 0.0f; P[v] = 1.0f; }
+  float h = 0.0f, P = 1.0f, hl[TOK], pl[TOK];
   int s = w.s0;
 #pragma unroll
   for (int j = 0; j < TOK; ++j) {
-    float vx[V], vr[V], vi[V];
-    rr[j].get(vr);
-    rx[j].get(vx);
-    ri[j].get(vi);
+    const float vx = rx[j].f(), vr = rr[j].f(), vi = ri[j].f();
     if constexpr (PACKED) {
       if (w.start >> j & 1) {
         while (g.cuc[s] < t0 + j || g.cuc[s + 1] <= t0 + j) ++s;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          h[v] = g.h0 ? g.h0[static_cast<int64_t>(s) * g.D + chc + v] : 0.0f;
-          P[v] = kReset;
-        }
+        h = g.h0 ? g.h0[static_cast<int64_t>(s) * g.D + chc] : 0.0f;
+        P = kReset;
       }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float a, m2;
-      decay_of(k[v] * sigmoid(vr[v]), a, m2);
-      const float bt = __builtin_amdgcn_sqrtf(m2) * (sigmoid(vi[v]) * vx[v]);
-      h[v] = fmaf(a, h[v], bt);
-      P[v] *= a;
-      hl[j][v] = h[v];
-      pl[j][v] = P[v];
-    }
+    float a, m2;
+    decay_of(k * sigmoid(vr), a, m2);
+    const float bt = __builtin_amdgcn_sqrtf(m2) * (sigmoid(vi) * vx);
+    h = fmaf(a, h, bt);
+    P *= a;
+    hl[j] = h;
+    pl[j] = P;
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    sH[wave][lane * V + v] = h[v];
-    sP[wave][lane * V + v] = P[v];
-  }
+  sH[wave][lane] = h;
+  sP[wave][lane] = P;
   __syncthreads();
   // the wave's entry state from the tile's: cH + cP * carry
-  float cH[V], cP[V], carry[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) { cH[v] = 0.0f; cP[v] = 1.0f; }
-  for (int u = 0; u < wave; ++u)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float p = sP[u][lane * V + v];
-      cH[v] = join<PACKED>(p, cH[v], sH[u][lane * V + v]);
-      cP[v] = join_p<PACKED>(p, cP[v]);
-    }
+  float cH = 0.0f, cP = 1.0f;
+  for (int u = 0; u < wave; ++u) {
+    const float p = sP[u][lane];
+    cH = join<PACKED>(p, cH, sH[u][lane]);
+    cP = join_p<PACKED>(p, cP);
+  }
   const Carry cr(g, tile, chain, lane);
-  const float tP = join_p<PACKED>(P[0], cP[0]), tH = join<PACKED>(P[0], cH[0], h[0]);
+  const float tP = join_p<PACKED>(P, cP), tH = join<PACKED>(P, cH, h);
   if (wave == WAVES - 1) cr.give(tP, tH);   // the last wave's is the tile's
   cr.fetch(sM, wave, lane);
   float first = 0.0f;
@@ -363,37 +333,28 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
   __syncthreads();
   const float before = cr.take<PACKED>(sM, lane, first);
   if (wave == WAVES - 1) cr.pass_on(join<PACKED>(tP, before, tH));
-#pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = join<PACKED>(cP[v], before, cH[v]);
+  const float carry = join<PACKED>(cP, before, cH);
   if (!on) return;
   if (g.states && t0 % kGatedChunk == 0 && t0 < g.T) {
     const int64_t nst = (g.T + kGatedChunk - 1) / kGatedChunk;
-    float* st = g.states + (b * nst + t0 / kGatedChunk) * g.D + ch;
-#pragma unroll
-    for (int v = 0; v < V; ++v) st[v] = carry[v];
+    g.states[(b * nst + t0 / kGatedChunk) * g.D + ch] = carry;
   }
+  const uint32_t off = static_cast<uint32_t>(ch) * static_cast<uint32_t>(sizeof(T));
   s = w.s0;
 #pragma unroll
   for (int j = 0; j < TOK; ++j) {
     const int t = t0 + j;
     if (t >= g.T) break;
     if (PACKED && !(w.live >> j & 1)) continue;
-    float o[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = join<PACKED>(pl[j][v], carry[v], hl[j][v]);
-    store_v<T, V>(reinterpret_cast<T*>(reinterpret_cast<char*>(y + static_cast<int64_t>(t) * g.D) +
-                                       static_cast<uint32_t>(ch) * static_cast<uint32_t>(sizeof(T))),
-                  o);
+    const float o = join<PACKED>(pl[j], carry, hl[j]);
+    put(y + static_cast<int64_t>(t) * g.D, off, o);
     if (PACKED) {
       if (w.end >> j & 1) {
         while (g.cuc[s + 1] <= t) ++s;   // the sequence whose last row this is
-        if (g.hT)
-#pragma unroll
-          for (int v = 0; v < V; ++v) g.hT[static_cast<int64_t>(s) * g.D + ch + v] = o[v];
+        if (g.hT) g.hT[static_cast<int64_t>(s) * g.D + ch] = o;
       }
     } else if (t == g.T - 1 && g.hT) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) g.hT[static_cast<int64_t>(b) * g.D + ch + v] = o[v];
+      g.hT[static_cast<int64_t>(b) * g.D + ch] = o;
     }
   }
 }
@@ -407,95 +368,68 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
 // A row keeps six numbers from pass to pass: a, dy and, first, m, sigmoid(r),
 // sigmoid(i), x; these become the factors of g in dx, di, dL L and dr as soon
 // as h is known, in place, so 16 rows fit 128 registers (four waves a SIMD).
-template <typename T, int V, int TOK, int WAVES, bool PACKED>
+template <typename T, int TOK, int WAVES, bool PACKED>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_backward(GatedArgs g) {
   constexpr int TILE = TOK * WAVES;
   static_assert(TILE == kGatedChunk && TOK <= 32, "one saved state per tile; rows of a window in 32 bits");
-  static_assert(V == 1 && WAVES >= kGroup, "a wave for each slot before a tile");
-  __shared__ float sH[WAVES][64 * V], sP[WAVES][64 * V], sC[64 * V];
+  static_assert(WAVES >= kGroup, "a wave for each slot before a tile");
+  __shared__ float sH[WAVES][64], sP[WAVES][64], sC[64];
   __shared__ u64 sM[kGroup][64];
   const unsigned n = take_ticket(g);
   const int tile = g.ntile - 1 - static_cast<int>(n / g.nchain);
   const int chain = static_cast<int>(n % g.nchain);
   const int b = chain / g.ncb, cb = chain % g.ncb;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int ch = (cb * 64 + lane) * V;
+  const int ch = cb * 64 + lane;
   const bool on = ch < g.D;
-  const int chc = on ? ch : g.D - V;
+  const int chc = on ? ch : g.D - 1;
   const int t0 = tile * TILE + wave * TOK;
   const int nrow = min(TOK, g.T - t0);   // rows of this wave (may be <= 0)
   const int64_t row0 = static_cast<int64_t>(b) * g.T;
 
-  float entry[V], k[V], dec[V];
-  {
-    const float* st = g.cstates + (b * static_cast<int64_t>(g.ntile) + tile) * g.D;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      dec[v] = g.decay[chc + v];
-      entry[v] = st[chc + v];
-    }
-  }
-  Raw<T, V> rx[TOK], rr[TOK], ri[TOK], rd[TOK];
-  load_rows<T, V, TOK>(rr, static_cast<const T*>(g.r) + row0 * g.ldr, g.ldr, chc, t0, g.T);
-  load_rows<T, V, TOK>(rx, static_cast<const T*>(g.x) + row0 * g.ldx, g.ldx, chc, t0, g.T);
-  load_rows<T, V, TOK>(ri, static_cast<const T*>(g.i) + row0 * g.ldi, g.ldi, chc, t0, g.T);
-  load_rows<T, V, TOK>(rd, static_cast<const T*>(g.dy) + row0 * g.D, g.D, chc, t0, g.T);
-  if (wave == 0)
-#pragma unroll
-    for (int v = 0; v < V; ++v) sC[lane * V + v] = decay_factor(dec[v], g.c);
+  const float dec = g.decay[chc];
+  float entry = g.cstates[(b * static_cast<int64_t>(g.ntile) + tile) * g.D + chc];
+  Raw1<T> rx[TOK], rr[TOK], ri[TOK], rd[TOK];
+  load_rows<T, TOK>(rr, static_cast<const T*>(g.r) + row0 * g.ldr, g.ldr, chc, t0, g.T);
+  load_rows<T, TOK>(rx, static_cast<const T*>(g.x) + row0 * g.ldx, g.ldx, chc, t0, g.T);
+  load_rows<T, TOK>(ri, static_cast<const T*>(g.i) + row0 * g.ldi, g.ldi, chc, t0, g.T);
+  load_rows<T, TOK>(rd, static_cast<const T*>(g.dy) + row0 * g.D, g.D, chc, t0, g.T);
+  if (wave == 0) sC[lane] = decay_factor(dec, g.c);
   Window w{};
   if constexpr (PACKED) w = window_of(g.cuc, g.S, t0, TOK);
   __syncthreads();
-#pragma unroll
-  for (int v = 0; v < V; ++v) k[v] = sC[lane * V + v];
+  const float k = sC[lane];
 
   // forward: the gates and the wave's scan from zero (rows past the end come
   // after those that count)
-  float h[V], P[V], av[TOK][V], f1[TOK][V], f2_[TOK][V], f3[TOK][V], f4_[TOK][V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) { h[v] = 0.0f; P[v] = 1.0f; }
+  float h = 0.0f, P = 1.0f, av[TOK], g1[TOK], g2[TOK], g3[TOK], g4[TOK];
   int s = w.s0;
 #pragma unroll
   for (int j = 0; j < TOK; ++j) {
-    float vx[V], vr[V], vi[V];
-    rr[j].get(vr);
-    rx[j].get(vx);
-    ri[j].get(vi);
+    const float vx = rx[j].f(), vr = rr[j].f(), vi = ri[j].f();
     if constexpr (PACKED) {
       if (w.start >> j & 1) {
         while (g.cuc[s] < t0 + j || g.cuc[s + 1] <= t0 + j) ++s;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          h[v] = g.h0 ? g.h0[static_cast<int64_t>(s) * g.D + chc + v] : 0.0f;
-          P[v] = kReset;
-        }
+        h = g.h0 ? g.h0[static_cast<int64_t>(s) * g.D + chc] : 0.0f;
+        P = kReset;
       }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float a, m2;
-      const float sr = sigmoid(vr[v]), si = sigmoid(vi[v]);
-      decay_of(k[v] * sr, a, m2);
-      const float m = __builtin_amdgcn_sqrtf(m2);
-      av[j][v] = a;
-      f1[j][v] = m;
-      f2_[j][v] = sr;
-      f3[j][v] = si;
-      f4_[j][v] = vx[v];
-      h[v] = fmaf(a, h[v], m * (si * vx[v]));
-      P[v] *= a;
-    }
+    float a, m2;
+    const float sr = sigmoid(vr), si = sigmoid(vi);
+    decay_of(k * sr, a, m2);
+    const float m = __builtin_amdgcn_sqrtf(m2);
+    av[j] = a;
+    g1[j] = m;
+    g2[j] = sr;
+    g3[j] = si;
+    g4[j] = vx;
+    h = fmaf(a, h, m * (si * vx));
+    P *= a;
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    sH[wave][lane * V + v] = h[v];
-    sP[wave][lane * V + v] = P[v];
-  }
+  sH[wave][lane] = h;
+  sP[wave][lane] = P;
   __syncthreads();
-  for (int u = 0; u < wave; ++u)
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      entry[v] = join<PACKED>(sP[u][lane * V + v], entry[v], sH[u][lane * V + v]);
+  for (int u = 0; u < wave; ++u) entry = join<PACKED>(sP[u][lane], entry, sH[u][lane]);
   __syncthreads();   // sH and sP are written again below
 
   // forward again, now with h: the factors of g
@@ -505,32 +439,26 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_backward(GatedArgs g) {
     if constexpr (PACKED) {
       if (w.start >> j & 1) {
         while (g.cuc[s] < t0 + j || g.cuc[s + 1] <= t0 + j) ++s;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          entry[v] = g.h0 ? g.h0[static_cast<int64_t>(s) * g.D + chc + v] : 0.0f;
+        entry = g.h0 ? g.h0[static_cast<int64_t>(s) * g.D + chc] : 0.0f;
       }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      // products of the first pass are formed anew, not kept in registers
-      asm volatile("" : "+v"(f1[j][v]), "+v"(f2_[j][v]), "+v"(f3[j][v]), "+v"(f4_[j][v]));
-      const float a = av[j][v], m = f1[j][v], sr = f2_[j][v], si = f3[j][v];
-      const float u = si * f4_[j][v], L = kLn2 * (k[v] * sr), ah = a * entry[v];
-      // L / m where m is 0 (a = 1): the limit 0
-      const float lm = m > 0.0f ? L * __builtin_amdgcn_rcpf(m) : 0.0f;
-      const float mu = m * u;
-      f1[j][v] = m * si;                                 // dx / g
-      f3[j][v] = fmaf(-mu, si, mu);                      // di / g
-      f4_[j][v] = fmaf(ah, L, -(a * a) * (lm * u));      // dL L / g
-      f2_[j][v] = 1.0f - sr;
-      entry[v] = ah + mu;
-    }
+    // products of the first pass are formed anew, not kept in registers
+    asm volatile("" : "+v"(g1[j]), "+v"(g2[j]), "+v"(g3[j]), "+v"(g4[j]));
+    const float a = av[j], m = g1[j], sr = g2[j], si = g3[j];
+    const float u = si * g4[j], L = kLn2 * (k * sr), ah = a * entry;
+    // L / m where m is 0 (a = 1): the limit 0
+    const float lm = m > 0.0f ? L * __builtin_amdgcn_rcpf(m) : 0.0f;
+    const float mu = m * u;
+    g1[j] = m * si;                                 // dx / g
+    g3[j] = fmaf(-mu, si, mu);                      // di / g
+    g4[j] = fmaf(ah, L, -(a * a) * (lm * u));      // dL L / g
+    g2[j] = 1.0f - sr;
+    entry = ah + mu;
   }
 
   // backward: q from zero and the product of a
-  float q[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) { q[v] = 0.0f; P[v] = 1.0f; }
+  float q = 0.0f;
+  P = 1.0f;
   int se = 0;   // the sequence of the last row
   if constexpr (PACKED) {
     se = seq_of(g.cuc, g.S, min(t0 + TOK, g.T) - 1);
@@ -544,39 +472,24 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_backward(GatedArgs g) {
     if constexpr (PACKED) {
       if (w.end >> j & 1) {
         while (g.cuc[sb] > t0 + j || g.cuc[sb + 1] <= g.cuc[sb]) --sb;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          q[v] = g.dhT ? g.dhT[static_cast<int64_t>(sb) * g.D + chc + v] : 0.0f;
-          P[v] = kReset;
-        }
+        q = g.dhT ? g.dhT[static_cast<int64_t>(sb) * g.D + chc] : 0.0f;
+        P = kReset;
       }
     }
-    float vd[V];
-    rd[j].get(vd);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      q[v] = av[j][v] * (q[v] + vd[v]);
-      P[v] *= av[j][v];
-    }
+    q = av[j] * (q + rd[j].f());
+    P *= av[j];
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    sH[wave][lane * V + v] = q[v];
-    sP[wave][lane * V + v] = P[v];
-  }
+  sH[wave][lane] = q;
+  sP[wave][lane] = P;
   __syncthreads();
-  float cH[V], cP[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) { cH[v] = 0.0f; cP[v] = 1.0f; }
-  for (int u = WAVES - 1; u > wave; --u)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float p = sP[u][lane * V + v];
-      cH[v] = join<PACKED>(p, cH[v], sH[u][lane * V + v]);
-      cP[v] = join_p<PACKED>(p, cP[v]);
-    }
+  float cH = 0.0f, cP = 1.0f;
+  for (int u = WAVES - 1; u > wave; --u) {
+    const float p = sP[u][lane];
+    cH = join<PACKED>(p, cH, sH[u][lane]);
+    cP = join_p<PACKED>(p, cP);
+  }
   const Carry cr(g, g.ntile - 1 - tile, chain, lane);
-  const float tP = join_p<PACKED>(P[0], cP[0]), tH = join<PACKED>(P[0], cH[0], q[0]);
+  const float tP = join_p<PACKED>(P, cP), tH = join<PACKED>(P, cH, q);
   if (wave == 0) cr.give(tP, tH);   // the first wave's is the tile's
   cr.fetch(sM, wave, lane);
   float last = 0.0f;
@@ -588,13 +501,10 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_backward(GatedArgs g) {
     cr.pass_on(q0);
     if (!PACKED && tile == 0 && on && g.dh0) g.dh0[static_cast<int64_t>(b) * g.D + ch] = q0;
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) q[v] = join<PACKED>(cP[v], after, cH[v]);
+  q = join<PACKED>(cP, after, cH);
 
   // backward again, now with q: the gradients
-  float dk[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) dk[v] = 0.0f;
+  float dk = 0.0f;
   const uint32_t off = static_cast<uint32_t>(ch) * static_cast<uint32_t>(sizeof(T));
   const int64_t step = g.ldg * static_cast<int64_t>(sizeof(T));
   const int64_t at = (row0 + t0 + TOK) * step;
@@ -612,43 +522,27 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_backward(GatedArgs g) {
       if (!(w.live >> j & 1)) continue;
       if (w.end >> j & 1) {
         while (g.cuc[sb] > t0 + j || g.cuc[sb + 1] <= g.cuc[sb]) --sb;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          q[v] = g.dhT ? g.dhT[static_cast<int64_t>(sb) * g.D + chc + v] : 0.0f;
+        q = g.dhT ? g.dhT[static_cast<int64_t>(sb) * g.D + chc] : 0.0f;
       }
     }
-    float vd[V], ox[V], orr[V], oi[V];
-    rd[j].get(vd);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float gt = vd[v] + q[v], gl = gt * f4_[j][v];
-      ox[v] = gt * f1[j][v];
-      oi[v] = gt * f3[j][v];
-      orr[v] = gl * f2_[j][v];
-      dk[v] += gl;
-      q[v] = av[j][v] * gt;
-      if (PACKED && (w.start >> j & 1) && on && g.dh0)
-        g.dh0[static_cast<int64_t>(sb) * g.D + ch + v] = q[v];
-    }
+    const float gt = rd[j].f() + q, gl = gt * g4[j];
+    dk += gl;
+    q = av[j] * gt;
     if (on) {
-      store_v<T, V>(reinterpret_cast<T*>(dx + off), ox);
-      store_v<T, V>(reinterpret_cast<T*>(dr + off), orr);
-      store_v<T, V>(reinterpret_cast<T*>(di + off), oi);
+      put(reinterpret_cast<T*>(dx), off, gt * g1[j]);
+      put(reinterpret_cast<T*>(dr), off, gl * g2[j]);
+      put(reinterpret_cast<T*>(di), off, gt * g3[j]);
+      if (PACKED && (w.start >> j & 1) && g.dh0) g.dh0[static_cast<int64_t>(sb) * g.D + ch] = q;
     }
   }
   // the tile's part of the sum for ddecay, over its waves in order
-#pragma unroll
-  for (int v = 0; v < V; ++v) sH[wave][lane * V + v] = dk[v];
+  sH[wave][lane] = dk;
   __syncthreads();
   if (wave == 0 && on) {
-    float* part = g.part + (b * static_cast<int64_t>(g.ntile) + tile) * g.D + ch;
+    float acc = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float acc = 0.0f;
-#pragma unroll
-      for (int u = 0; u < WAVES; ++u) acc += sH[u][lane * V + v];
-      part[v] = acc;
-    }
+    for (int u = 0; u < WAVES; ++u) acc += sH[u][lane];
+    g.part[(b * static_cast<int64_t>(g.ntile) + tile) * g.D + ch] = acc;
   }
 }
 
@@ -687,7 +581,7 @@ __global__ __launch_bounds__(256) void k_gated_step(GatedArgs g, float* hs) {
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int b = static_cast<int>(n / ncb), ch = static_cast<int>(n % ncb) * V;
   if (b >= g.B) return;
-  Raw<T, V> rx, rr, ri;
+  RawVec<T, V> rx, rr, ri;
   rr.load(static_cast<const T*>(g.r) + b * g.ldr + ch);
   rx.load(static_cast<const T*>(g.x) + b * g.ldx + ch);
   ri.load(static_cast<const T*>(g.i) + b * g.ldi + ch);
@@ -711,13 +605,13 @@ __global__ __launch_bounds__(256) void k_gated_step(GatedArgs g, float* hs) {
   store_v<T, V>(static_cast<T*>(g.y) + static_cast<int64_t>(b) * g.D + ch, h);
 }
 
-template <typename T, int V, int TOK, int WAVES>
+template <typename T, int TOK, int WAVES>
 hipError_t run_scan(GatedArgs& g, hipStream_t s) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(g.ntile) * g.nchain);
   if (g.cu)
-    k_gated_scan<T, V, TOK, WAVES, true><<<grid, 64 * WAVES, 0, s>>>(g);
+    k_gated_scan<T, TOK, WAVES, true><<<grid, 64 * WAVES, 0, s>>>(g);
   else
-    k_gated_scan<T, V, TOK, WAVES, false><<<grid, 64 * WAVES, 0, s>>>(g);
+    k_gated_scan<T, TOK, WAVES, false><<<grid, 64 * WAVES, 0, s>>>(g);
   return hipGetLastError();
 }
 // 16 rows a wave just fit 128 registers in the dense bf16 kernel (4 x 2048 x
@@ -728,11 +622,11 @@ template <typename T>
 hipError_t run_backward(GatedArgs& g, hipStream_t s) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(g.ntile) * g.nchain);
   if (g.cu)
-    k_gated_backward<T, 1, 8, kGatedChunk / 8, true><<<grid, 8 * kGatedChunk, 0, s>>>(g);
+    k_gated_backward<T, 8, kGatedChunk / 8, true><<<grid, 8 * kGatedChunk, 0, s>>>(g);
   else if constexpr (sizeof(T) == 4)
-    k_gated_backward<T, 1, 8, kGatedChunk / 8, false><<<grid, 8 * kGatedChunk, 0, s>>>(g);
+    k_gated_backward<T, 8, kGatedChunk / 8, false><<<grid, 8 * kGatedChunk, 0, s>>>(g);
   else
-    k_gated_backward<T, 1, 16, kGatedChunk / 16, false><<<grid, 4 * kGatedChunk, 0, s>>>(g);
+    k_gated_backward<T, 16, kGatedChunk / 16, false><<<grid, 4 * kGatedChunk, 0, s>>>(g);
   return hipGetLastError();
 }
 
@@ -798,8 +692,8 @@ hipError_t launch_gated_scan(GatedArgs& g, int bf16, hipStream_t s) {
   const GatedPlan p = gated_plan(g.B, g.T, g.D, g.cu != nullptr, false);
   hipError_t e = run_init(g, g.h0, g.hT, gated_slots(p), s);
   if (e != hipSuccess) return e;
-  if (p.tile == 512) return bf16 ? run_scan<bf16_t, 1, 32, 16>(g, s) : run_scan<float, 1, 32, 16>(g, s);
-  return bf16 ? run_scan<bf16_t, 1, 32, 8>(g, s) : run_scan<float, 1, 32, 8>(g, s);
+  if (p.tile == 512) return bf16 ? run_scan<bf16_t, 32, 16>(g, s) : run_scan<float, 32, 16>(g, s);
+  return bf16 ? run_scan<bf16_t, 32, 8>(g, s) : run_scan<float, 32, 8>(g, s);
 }
 
 hipError_t launch_gated_backward(GatedArgs& g, int bf16, hipStream_t s) {

@@ -48,7 +48,8 @@ def _grad_bound(want, amax, T, dtype):
     return 3 * ref.gated_bound(want, amax, T, dtype) + (ref.U[dtype] * want.abs())
 
 
-DENSE = [(1, 1, 64), (2, 2, 1), (1, 127, 65), (3, 128, 64), (1, 129, 130), (2, 300, 63), (1, 1000, 96)]
+DENSE = [(1, 1, 64), (2, 2, 1), (1, 127, 65), (3, 128, 64), (1, 129, 130), (2, 300, 63), (1, 1000, 96),
+         (1, 2700, 20)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -88,7 +89,8 @@ def test_scan_and_gradients(B, T, D, dtype):
                    2.0 ** -20 * (min(T, 100) + 2) * want["h0"].abs().mean())
 
 
-LENGTHS = [[1], [0, 5, 0, 0, 1, 127, 0], [128, 1, 128, 255], [700, 3, 1, 1, 40], [0, 0, 300]]
+LENGTHS = [[1], [0, 5, 0, 0, 1, 127, 0], [128, 1, 128, 255], [700, 3, 1, 1, 40], [0, 0, 300],
+           [2500, 3, 700], [1] * 150 + [0] * 40 + [2] * 33]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])

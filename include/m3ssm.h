@@ -1,5 +1,6 @@
 /*
- * m3ssm.h -- C ABI of libm3ssm: the Mamba-3 SSM core recurrence on gfx950.
+ * m3ssm.h -- C ABI of libm3ssm: the Mamba-3 SSM core recurrence on gfx950,
+ * and, further down, the other layers of a hybrid stack.
  *
  * The library computes, for every (batch, head) pair independently, the
  * exponential-trapezoidal three-term update

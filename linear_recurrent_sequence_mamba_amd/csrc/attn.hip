@@ -218,8 +218,9 @@ __device__ __forceinline__ void attend(Rows<D>& st, const Frag<T>* q, const char
 // The prompt: a workgroup takes 32 WAVES queries of one head; K and V tiles
 // of BN keys are double-buffered in LDS.  Two waves a SIMD (D = 64: three), so
 // that one's softmax runs beside another's products as well.  16384 tokens, 16
-// heads of 128: 1.06 ms, 1.04 PFLOP/s, matrix cores busy 57% and vector units
-// 51% of the cycles; packed rows of 32 heads of 64: 265 us, 0.74 PFLOP/s.
+// heads of 128: 1.06 ms, 1.04 PFLOP/s, matrix cores busy 55% and vector units
+// 50% of the cycles; packed rows of 32 heads of 64: 265 us, 0.74 PFLOP/s, 37%
+// and 66%.
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn(AttnArgs a) {
   using L = Tile<T, D>;
@@ -335,8 +336,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
 // tile's columns.  A workgroup takes a part of one sequence's cache, its
 // waves every WAVES-th tile of 32 keys each, without barriers; the waves'
 // sums are joined in LDS and the parts by k_attn_join.  Bound by reading the
-// cache: 65536 keys of 16 heads of 64 in 46 us (5.8 TB/s where the last-level
-// cache holds part of it, 4.7 where not), the join 4 us.
+// cache: 65536 keys of 16 heads of 64 in 50 us when called again and again (5.4
+// TB/s: the last-level cache holds part of it), the join 4.5 us.
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
   using L = Tile<T, D>;
@@ -502,8 +503,8 @@ hipError_t run_decode(const AttnArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Parts of a cache: enough workgroups for the chip (two a CU), each with at
-// least four tiles of 32 keys for each of its four waves.
+// Parts of a cache: enough workgroups for the chip (two a CU), each with 512
+// keys at the least, four tiles of 32 for each of four waves.
 int decode_parts(int S, int cap, int Hq, int Hk) {
   const int64_t blocks = static_cast<int64_t>(S) * Hk * ((Hq / Hk + 31) / 32);
   int64_t n = (512 + blocks - 1) / blocks;

@@ -138,7 +138,7 @@ constexpr int kExactD = 512;
 
 // ---------------------------------------------------------------------------
 // dq: 32 queries a wave, tiles of 32 keys in LDS (8192 packed rows, 16 heads of
-// 128 on 2: 186 us, 0.84 PFLOP/s)
+// 128 on 2: 188 us, 0.83 PFLOP/s, matrix cores and vector units each busy 44%)
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn_dq(AttnArgs a) {
   using L = Tile<T, D>;
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
 // They are two kernels: one for both needs a fifth fewer products, but keys,
 // values, both sums and a tile's scores are more than 256 registers, which
 // leaves one wave a SIMD and copies between the halves of its register file
-// (8192 packed rows, 16 heads of 128 on 2: 600 us, against 157 + 199 us).  At
+// (8192 packed rows, 16 heads of 128 on 2: 600 us, against 162 + 204 us).  At
 // head dimension 64 both fit (16384 packed rows, 32 heads on 8, all gradients:
 // 0.97 ms, in two kernels 1.45 ms).
 
@@ -363,8 +363,10 @@ __global__ __launch_bounds__(256) void k_attn_sum(AttnArgs a) {
   put4(static_cast<T*>(a.dv) + n, v.x, v.y, v.z, v.w);
 }
 
-// Parts of a group of heads: enough workgroups of 128 keys to fill the chip
-// twice, in equal parts.
+// Parts of a group of heads: at least 1024 workgroups of 128 keys where the
+// group has the heads for it, in equal parts: their work is uneven, and a third
+// and fourth round of them evens it out (8192 packed rows, 16 heads of 128 on 2:
+// aiming at 512, dv 245 and dk 330 us; at 1024, 168 and 226).
 int group_parts(int Tk, int S, int Hq, int Hk) {
   const int g = Hq / Hk;
   const int64_t blocks = (static_cast<int64_t>(Tk) / 128 + 1) * Hk;

@@ -263,9 +263,10 @@ __device__ __forceinline__ unsigned take_ticket(const GatedArgs& a) {
 // ends are joined through LDS, the tiles' through the carry slots, and
 // y = h_local + product * carry.  x, r, i are read once and y written once, 8
 // bytes an element in bf16: bound by HBM, closely followed by the six
-// transcendental instructions an element (16384 x 4096: 123 us, 4.4 TB/s; 16 x
-// 2048 x 4096: 4.8 TB/s).  One channel a lane and 32 rows a wave: with 8 rows
-// 205 us, with two channels 135 us.
+// transcendental instructions an element (16384 x 4096: 123 to 127 us, 4.2 to
+// 4.4 TB/s; 16 x 2048 x 4096: 226 us, 4.7 TB/s).  One channel a lane and 32
+// rows a wave, timed before the carry went by groups: 127 us; 16 rows 136,
+// 16 waves of 8 rows 205, two channels and 16 rows 135.
 template <typename T, int TOK, int WAVES, bool PACKED>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
   constexpr int TILE = TOK * WAVES;
@@ -579,8 +580,8 @@ __global__ __launch_bounds__(256) void k_gated_ddecay(GatedArgs g, int64_t npart
 }
 
 // ---------------------------------------------------------------------------
-// One decode step: h is read and written once (128 x 4096 in 6 us, 1 x 4096 in
-// 4 us: a launch and a round trip to memory).
+// One decode step: h is read and written once (1 x 4096 and 128 x 4096 in 4
+// to 7 us: a launch and a round trip to memory).
 template <typename T, int V>
 __global__ __launch_bounds__(256) void k_gated_step(GatedArgs g, float* hs) {
   const int ncb = (g.D + V - 1) / V;

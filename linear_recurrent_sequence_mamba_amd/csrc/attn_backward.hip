@@ -365,7 +365,7 @@ __global__ __launch_bounds__(256) void k_attn_sum(AttnArgs a) {
 
 // Parts of a group of heads: at least 1024 workgroups of 128 keys where the
 // group has the heads for it, in equal parts: their work is uneven, and a third
-// and fourth round of them evens it out (8192 packed rows, 16 heads of 128 on 2:
+// and fourth of them a CU even it out (8192 packed rows, 16 heads of 128 on 2:
 // aiming at 512, dv 245 and dk 330 us; at 1024, 168 and 226).
 int group_parts(int Tk, int S, int Hq, int Hk) {
   const int g = Hq / Hk;

@@ -272,7 +272,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
   constexpr int TILE = TOK * WAVES;
   static_assert(TOK <= 32 && kGatedChunk % TOK == 0, "rows of a window in 32 bits");
   static_assert(WAVES >= kGroup, "a wave for each slot before a tile");
-  __shared__ float sH[WAVES][64], sP[WAVES][64], sC[64];
+  __shared__ float sH[WAVES][64], sP[WAVES][64], sC[64], sF[64];
   __shared__ u64 sM[kGroup][64];
   const unsigned n = take_ticket(g);
   const int tile = static_cast<int>(n / g.nchain), chain = static_cast<int>(n % g.nchain);
@@ -293,6 +293,11 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
   load_rows<T, TOK>(rr, r, g.ldr, chc, t0, g.T);
   load_rows<T, TOK>(rx, x, g.ldx, chc, t0, g.T);
   load_rows<T, TOK>(ri, gi, g.ldi, chc, t0, g.T);
+  const Carry cr(g, tile, chain, lane);
+  // h0 is read before the tile gives its map: hT may be the same memory, and
+  // the last tile writes it as soon as it has the maps before it
+  if (!PACKED && wave == 0)
+    sF[lane] = cr.n0 == 0 && g.h0 ? g.h0[static_cast<int64_t>(b) * g.D + chc] : 0.0f;
   if (wave == 0) sC[lane] = decay_factor(dec, g.c);
   Window w{};
   if constexpr (PACKED) w = window_of(g.cuc, g.S, t0, TOK);
@@ -329,14 +334,11 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
     cH = join<PACKED>(p, cH, sH[u][lane]);
     cP = join_p<PACKED>(p, cP);
   }
-  const Carry cr(g, tile, chain, lane);
   const float tP = join_p<PACKED>(P, cP), tH = join<PACKED>(P, cH, h);
   if (wave == WAVES - 1) cr.give(tP, tH);   // the last wave's is the tile's
   cr.fetch(sM, wave, lane);
-  float first = 0.0f;
-  if (!PACKED && cr.n0 == 0 && g.h0) first = g.h0[static_cast<int64_t>(b) * g.D + chc];
   __syncthreads();
-  const float before = cr.take<PACKED>(sM, lane, first);
+  const float before = cr.take<PACKED>(sM, lane, PACKED ? 0.0f : sF[lane]);
   if (wave == WAVES - 1) cr.pass_on(join<PACKED>(tP, before, tH));
   const float carry = join<PACKED>(cP, before, cH);
   if (!on) return;

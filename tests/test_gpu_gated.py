@@ -271,6 +271,41 @@ def test_equal_calls_give_equal_bits_and_hT_may_be_h0():
     assert torch.equal(h, hT) and torch.equal(y2, y)
 
 
+def _in_place(x, r, i, decay, h0, cu):
+    """The scan with hT written over h0."""
+    import ctypes
+    D, dt = x.shape[-1], m3.M3_BF16 if x.dtype == BF16 else m3.M3_F32
+    dims = ctypes.byref(m3.m3_gated_dims(h0.shape[0], x.shape[-2], D, dt, 8.0, 0, 0, 0, 0))
+    lib, h, y = m3.library(), h0.clone(), torch.empty_like(x)
+    ws = torch.empty(lib.m3_gated_scan_workspace_size(dims, cu is not None), dtype=torch.uint8, device="cuda")
+    p = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())
+    assert lib.m3_gated_scan(dims, p(cu), p(x), p(r), p(i), p(decay), p(h), p(y), p(h), None, p(ws),
+                             ws.numel(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+    return y, h
+
+
+@pytest.mark.parametrize("B,T", [(1, 600), (3, 1900), (2, 5000)])
+def test_hT_over_h0_in_every_tile_count(B, T):
+    """Every tile of the first group has read h0 before the last one writes
+    hT: with fewer tiles than a group, within the second, and beyond."""
+    x, r, i, decay, h0 = _inputs((B, T), 1000, BF16, 21, B)
+    h0 = h0 * 100   # a tile that took the new state for the old one would show
+    y, hT, _ = m3.gated_scan(x, r, i, decay, h0=h0)
+    for _ in range(5):
+        y2, h = _in_place(x, r, i, decay, h0, None)
+        assert torch.equal(h, hT) and torch.equal(y2, y)
+
+
+def test_hT_over_h0_packed():
+    lengths = [700, 0, 1, 255, 1044]
+    x, r, i, decay, h0 = _inputs((sum(lengths),), 1000, BF16, 22, len(lengths))
+    cu = torch.tensor([0] + lengths).cumsum(0).to(torch.int32).cuda()
+    y, hT, _ = m3.gated_scan(x, r, i, decay, h0=h0, cu_seqlens=cu)
+    for _ in range(5):
+        y2, h = _in_place(x, r, i, decay, h0, cu)
+        assert torch.equal(h, hT) and torch.equal(y2, y)
+
+
 def test_graphs_and_streams():
     """Two captured graphs, replayed in turn with eager work between, and a
     call on another stream, all equal the eager result."""

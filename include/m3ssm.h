@@ -413,7 +413,7 @@ typedef struct {
   int32_t nheads_k; /* Hk >= 1                                             */
   int32_t headdim;  /* D: 64 or 128                                        */
   int32_t dtype;    /* m3_dtype of q, k, v, o and gradients                */
-  float scale;      /* of the scores; finite                               */
+  float scale;      /* of the scores; finite, >= 2^-126                    */
   int64_t ld_q, ld_k, ld_v, ld_o, ld_do; /* >= H D, < 2^24, multiples of 8,
                                             or 0                           */
   int64_t stride_k, stride_v; /* decode: elements from one sequence's cache

@@ -279,7 +279,9 @@ m3_status check_attn(const m3_attn_dims* d, bool decode) {
   if (d->nseq <= 0 || d->tokens_k <= 0 || (!decode && d->tokens_q <= 0)) return M3_ERR_SHAPE;
   if (d->nheads_q <= 0 || d->nheads_k <= 0 || d->headdim <= 0) return M3_ERR_SHAPE;
   if (d->nheads_q % d->nheads_k) return M3_ERR_SHAPE;
-  if (!isfinite(d->scale)) return M3_ERR_SHAPE;
+  // the maximum of the scores is that of the products, and a masked one's
+  // scale * -inf has to stay -inf
+  if (!isfinite(d->scale) || d->scale < 1.1754944e-38f) return M3_ERR_SHAPE;
   if (bad_dtype(d->dtype)) return M3_ERR_DTYPE;
   if (!m3::attn_supported(d->headdim)) return M3_ERR_UNSUPPORTED;
   const int64_t wq = static_cast<int64_t>(d->nheads_q) * d->headdim;

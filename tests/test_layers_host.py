@@ -200,6 +200,14 @@ def test_attn_refusals():
     assert lib.m3_attn_decode_workspace_size(ctypes.byref(_adims(headdim=96))) == 0
 
 
+def test_attn_refuses_scales_that_are_not_positive():
+    """A masked score is -inf before its scale, and the maximum is taken of
+    the products: neither holds for a scale of zero or below."""
+    for s in (0.0, -0.125, 1e-39):
+        d = _adims(scale=s)
+        assert _attn(d) == SHAPE and _attn_bwd(d) == SHAPE and _decode(d) == SHAPE, s
+
+
 def test_helpers_refuse_host_tensors():
     z = torch.zeros
     with pytest.raises(ValueError):

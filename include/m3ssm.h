@@ -376,7 +376,8 @@ typedef struct {
   int32_t rotary_dim; /* even, 0 .. D                                      */
   int32_t dtype;      /* m3_dtype of q, k, their outputs and gradients     */
   uint32_t flags;     /* M3_ROPE_HALF                                      */
-  float eps;          /* finite, >= 0 (a row of zeros with eps = 0: NaN)   */
+  float eps;          /* finite, >= 0 (a row whose mean square and eps are
+                         together below 2^-126 has no finite norm)         */
   double base;        /* finite, > 0                                       */
   int64_t ld_q, ld_k; /* >= H D, multiples of 8, or 0                      */
   int64_t ld_dq, ld_dk;

@@ -643,6 +643,9 @@ def _dims(kind, *fields):
     """The dims of a call, read only, with the reference that ctypes passes:
     equal calls share them."""
     d = kind(*fields)
+    for (name, _), v in zip(kind._fields_, fields):   # ctypes cuts silently
+        if isinstance(v, int) and getattr(d, name) != v:
+            raise ValueError(f"{name}: {v} is out of range")
     return d, ctypes.byref(d)
 
 
@@ -925,6 +928,8 @@ def attn_decode(q, k_cache, v_cache, lengths, scale=None, o=None, ws=None, strea
     if q.dim() != 3 or k_cache.dim() != 4:
         raise ValueError("q must be [S, Hq, D], the caches [S, cap, Hk, D]")
     S, Hq, D = q.shape
+    if S == 0:
+        raise ValueError("q holds no sequence")
     cap, Hk = k_cache.shape[1:3]
     code = dtype_code(q.dtype)
     strides = []

@@ -208,6 +208,17 @@ def test_attn_refuses_scales_that_are_not_positive():
         assert _attn(d) == SHAPE and _attn_bwd(d) == SHAPE and _decode(d) == SHAPE, s
 
 
+def test_sizes_beyond_the_struct_are_refused():
+    """More rows than an int32 holds must not wrap round to fewer."""
+    for v in (2 ** 31, 2 ** 32 + 5, -2 ** 33):
+        with pytest.raises(ValueError, match="seqlen"):
+            m3._dims(m3.m3_gated_dims, 1, v, 64, m3.M3_BF16, 8.0, 0, 0, 0, 0)
+    with pytest.raises(ValueError, match="flags"):
+        m3._dims(m3.m3_qk_dims, 1, 4, 2, 64, 64, m3.M3_BF16, -1, 1e-6, 1e4, 0, 0, 0, 0)
+    d, _ = m3._dims(m3.m3_gated_dims, 1, 2 ** 31 - 1, 64, m3.M3_BF16, 8, 0, 0, 0, 0)
+    assert d.seqlen == 2 ** 31 - 1 and d.c == 8.0
+
+
 def test_helpers_refuse_host_tensors():
     z = torch.zeros
     with pytest.raises(ValueError):

@@ -193,6 +193,8 @@ m3_status scan_prefill(const m3_dims* d, const void* x, const void* dt, const fl
 // ---------------------------------------------------------------------------
 // the other layers of a hybrid stack
 bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+// rows and tiles are counted in int, beyond the last one as well
+constexpr int kMostRows = 0x7fff0000;
 bool bad_dtype(int t) { return t != M3_F32 && t != M3_BF16; }
 // a kernel's threads are counted in 32 bits
 bool grid_fits(int64_t blocks, int threads) { return blocks <= int64_t{0xffffffff} / threads; }
@@ -207,6 +209,7 @@ bool any_misaligned(const void* const (&p)[N]) {
 m3_status check_gated(const m3_gated_dims* d, bool scan, bool packed) {
   if (!d) return M3_ERR_NULL;
   if (d->batch <= 0 || d->width <= 0 || (scan && d->seqlen <= 0)) return M3_ERR_SHAPE;
+  if (d->batch > kMostRows || d->width > kMostRows || (scan && d->seqlen > kMostRows)) return M3_ERR_SHAPE;
   if (!isfinite(d->c) || d->c <= 0.0f) return M3_ERR_SHAPE;
   const int64_t lds[] = {d->ld_x, d->ld_r, d->ld_i, d->ld_g};
   for (int64_t ld : lds)
@@ -237,6 +240,7 @@ m3::GatedArgs gated_args(const m3_gated_dims* d) {
 m3_status check_qk(const m3_qk_dims* d) {
   if (!d) return M3_ERR_NULL;
   if (d->tokens <= 0 || d->nheads_q <= 0 || d->nheads_k <= 0 || d->headdim <= 0) return M3_ERR_SHAPE;
+  if (d->tokens > kMostRows) return M3_ERR_SHAPE;
   if (d->rotary_dim < 0 || d->rotary_dim > d->headdim || d->rotary_dim % 2) return M3_ERR_SHAPE;
   if (d->flags & ~M3_ROPE_HALF) return M3_ERR_SHAPE;
   if (!isfinite(d->eps) || d->eps < 0.0f) return M3_ERR_SHAPE;
@@ -277,6 +281,7 @@ m3::QkNormArgs qk_args(const m3_qk_dims* d) {
 m3_status check_attn(const m3_attn_dims* d, bool decode) {
   if (!d) return M3_ERR_NULL;
   if (d->nseq <= 0 || d->tokens_k <= 0 || (!decode && d->tokens_q <= 0)) return M3_ERR_SHAPE;
+  if (d->tokens_k > kMostRows || (!decode && d->tokens_q > kMostRows)) return M3_ERR_SHAPE;
   if (d->nheads_q <= 0 || d->nheads_k <= 0 || d->headdim <= 0) return M3_ERR_SHAPE;
   if (d->nheads_q % d->nheads_k) return M3_ERR_SHAPE;
   // the maximum of the scores is that of the products, and a masked one's

@@ -219,6 +219,18 @@ def test_sizes_beyond_the_struct_are_refused():
     assert d.seqlen == 2 ** 31 - 1 and d.c == 8.0
 
 
+def test_counts_near_the_end_of_an_int_are_refused():
+    """A loop or a tile count past the last row must not overflow."""
+    n = 2 ** 31 - 5
+    assert _qk(_qdims(tokens=n)) == SHAPE and _qk_bwd(_qdims(tokens=n)) == SHAPE
+    assert m3.library().m3_qk_norm_rope_backward_workspace_size(ctypes.byref(_qdims(tokens=n))) == 0
+    assert _attn(_adims(tokens_q=n)) == SHAPE and _attn(_adims(tokens_k=n)) == SHAPE
+    assert _decode(_adims(tokens_k=n)) == SHAPE
+    for k in (dict(seqlen=n, width=1), dict(width=n), dict(batch=n, width=1)):
+        assert _scan(_gdims(**k)) == SHAPE and _scan_bwd(_gdims(**k)) == SHAPE, k
+    assert _step(_gdims(batch=n, width=1)) == SHAPE
+
+
 def test_helpers_refuse_host_tensors():
     z = torch.zeros
     with pytest.raises(ValueError):

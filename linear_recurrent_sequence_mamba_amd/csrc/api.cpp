@@ -308,7 +308,7 @@ m3_status check_attn(const m3_attn_dims* d, bool decode) {
         !grid_fits((static_cast<int64_t>(d->tokens_q) * d->nheads_q + 1) / 2, 32) ||
         !grid_fits(static_cast<int64_t>(d->tokens_k) * wk / 1024 + 1, 256))
       return M3_ERR_SHAPE;
-  } else if (!grid_fits(static_cast<int64_t>(d->nseq) * d->nheads_q * 512, 256)) {
+  } else if (!grid_fits(static_cast<int64_t>(d->nseq) * d->nheads_q + 512, 256)) {   // 512: parts
     return M3_ERR_SHAPE;
   }
   return M3_OK;

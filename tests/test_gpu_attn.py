@@ -230,6 +230,23 @@ def test_decode(case, dtype):
     _check("lse", lse, wl, torch.tensor(2.0 ** -24 * (D + 8) * scale * D * 16 + 2.0 ** -19 * 8))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_decode_of_many_sequences(dtype):
+    """More sequences and heads than 2^15 together; some of them checked."""
+    S, cap, Hq, Hk, D = 600, 70, 64, 8, 64
+    g = torch.Generator().manual_seed(S)
+    q = torch.randn(S, Hq, D, generator=g).to(dtype).cuda()
+    k, v = (torch.randn(S, cap, Hk, D, generator=g).to(dtype).cuda() for _ in range(2))
+    lengths = torch.randint(0, cap + 1, (S,), generator=g).tolist()
+    o, lse = m3.attn_decode(q, k, v, torch.tensor(lengths, dtype=torch.int32).cuda())
+    torch.cuda.synchronize()
+    for s in (0, 1, 299, 511, 512, 513, 598, 599):
+        one = slice(s, s + 1)
+        wo, bo, wl = _decode_ref(q[one], k[one], v[one], lengths[one], D ** -0.5, dtype)
+        _check("o", o[one], wo, bo)
+        _check("lse", lse[one], wl, torch.tensor(2.0 ** -24 * (D + 8) * D ** 0.5 * 16 + 2.0 ** -19 * 8))
+
+
 def test_decode_lengths_are_clamped():
     q = torch.randn(2, 2, 64, device="cuda")
     k, v = torch.randn(2, 50, 1, 64, device="cuda"), torch.randn(2, 50, 1, 64, device="cuda")

@@ -231,6 +231,13 @@ def test_counts_near_the_end_of_an_int_are_refused():
     assert _step(_gdims(batch=n, width=1)) == SHAPE
 
 
+def test_decode_takes_large_batches():
+    lib = m3.library()
+    size = lambda **k: lib.m3_attn_decode_workspace_size(ctypes.byref(_adims(tokens_k=4096, nheads_q=64, nheads_k=8, **k)))
+    assert size(nseq=512) > 0 and size(nseq=4096) > 0 and size(nseq=200000) > 0
+    assert size(nseq=1 << 20) == 0   # 2^26 workgroups
+
+
 def test_helpers_refuse_host_tensors():
     z = torch.zeros
     with pytest.raises(ValueError):

@@ -6,8 +6,8 @@
 //   dv_j = sum_i p_ij do_i,  dk_j = scale sum_i ds_ij q_i,
 //   dq_i = scale sum_j ds_ij k_j
 //
-// k_attn_stat turns (o, do, lse) into one pair per row and head; k_attn_dq
-// takes queries as lanes and walks over keys, k_attn_dkv takes keys as lanes
+// k_attn_dq takes queries as lanes and walks over keys; it also turns (o, do,
+// lse) into one pair per row and head for k_attn_dkv, which takes keys as lanes
 // and walks over queries.  Both recompute s from q and k, so no sum is shared
 // between workgroups: there are no atomics, and equal calls give equal bits.
 // The heads of a group add up in one workgroup, or, where that would leave
@@ -16,32 +16,6 @@
 
 namespace m3 {
 namespace {
-
-// D / 8 lanes to a row and head; behind all rows' numbers infinity and 0
-template <typename T, int D>
-__global__ __launch_bounds__(256) void k_attn_stat(AttnArgs a) {
-  constexpr int G = D / 8;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * (256 / G) + threadIdx.x / G;
-  const int64_t all = static_cast<int64_t>(a.Tq) * a.Hq;
-  const int64_t m = n < all ? n : all - 1;
-  const int64_t t = m / a.Hq;
-  const int h = static_cast<int>(m % a.Hq), e = 8 * (threadIdx.x % G);
-  float o[8], g[8], s = 0.0f;
-  ld8(static_cast<const T*>(a.co), t * a.ldo + h * D + e, o);
-  ld8(static_cast<const T*>(a.dout), t * a.lddo + h * D + e, g);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) s = fmaf(o[j], g[j], s);
-  s = group_sum<G>(s);
-  if (n == 0 && e == 0) {
-    a.stat[2 * all] = INFINITY;
-    a.stat[2 * all + 1] = 0.0f;
-  }
-  if (n < all && e == 0) {
-    float* st = a.stat + static_cast<int64_t>(h) * a.Tq + t;
-    st[0] = a.clse[m] * kLog2eA;
-    st[static_cast<int64_t>(a.Hq) * a.Tq] = s;
-  }
-}
 
 // ---------------------------------------------------------------------------
 // One step of a sum over tiles of 32 rows, the same for the three gradients:
@@ -147,6 +121,11 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nslot = gridDim.x / a.Hq;
   const int h = blockIdx.x % a.Hq;
+  const int64_t all = static_cast<int64_t>(a.Tq) * a.Hq;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {   // behind all rows' numbers
+    a.stat[2 * all] = INFINITY;
+    a.stat[2 * all + 1] = 0.0f;
+  }
   const Slot sl = slot_of<BM>(a.cuq, a.S, a.Tq, nslot - 1 - static_cast<int>(blockIdx.x / a.Hq), lane);
   if (sl.s < 0) return;
   const int q0 = clamp_row(a.cuq[sl.s], a.Tq), q1 = clamp_row(a.cuq[sl.s + 1], a.Tq);
@@ -167,9 +146,23 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
       frag_load(g[kk], d + 16 * kk);
     }
   }
-  const float* st = a.stat + static_cast<int64_t>(h) * a.Tq + row;
-  const float lse = st[0] == -INFINITY ? INFINITY : st[0];   // no key: every weight 0
-  float dd = st[static_cast<int64_t>(a.Hq) * a.Tq];
+  float lse = a.clse[row * a.Hq + h] * kLog2eA, dd = 0.0f;
+  {
+    // D = <o, do>; the other half of the row is in lane ^ 32
+    const T* p = static_cast<const T*>(a.co) + row * a.ldo + h * D + 8 * half;
+    Frag<T> o[D / 16];
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) frag_load(o[kk], p + 16 * kk);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) dd = frag_dot(o[kk], g[kk], dd);
+    dd = half_sum(dd);
+  }
+  float* st = a.stat + static_cast<int64_t>(h) * a.Tq + row;
+  if (half == 0 && i < Lq) {
+    st[0] = lse;
+    st[all] = dd;
+  }
+  if (lse == -INFINITY) lse = INFINITY;   // no key: every weight 0
   f16v dq[D / 32];
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) dq[d] = f16v{};
@@ -202,7 +195,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
       __syncthreads();
     }
     dd = half_sum(r);
-    if (half == 0 && i < Lq) a.stat[(static_cast<int64_t>(a.Hq) + h) * a.Tq + row] = dd;
+    if (half == 0 && i < Lq) st[all] = dd;
   }
   if (ntile > 0) {
     L::template load2<WAVES>(sKV[0], kp, a.ldk, vp, a.ldv, 0, Lk - 1, wave, lane);
@@ -378,15 +371,12 @@ int group_parts(int Tk, int S, int Hq, int Hk) {
 template <typename T, int D>
 hipError_t run(const AttnArgs& a, hipStream_t s) {
   constexpr int W = 4, B = 32 * W;
-  const int64_t rows = static_cast<int64_t>(a.Tq) * a.Hq, per = 256 / (D / 8);
-  k_attn_stat<T, D><<<static_cast<unsigned>((rows + per - 1) / per), 256, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
   const int64_t nk = (static_cast<int64_t>(a.Tk) / B + a.S) * a.Hk * a.gsplit;
   const int64_t nq = (static_cast<int64_t>(a.Tq) / B + a.S) * a.Hq;
   k_attn_dq<T, D, W><<<static_cast<unsigned>(nq), 64 * W, 0, s>>>(a);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  // dk after dq, which may have left it a better D
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  // after dq, which leaves them lse and D
   if constexpr (D == 64) {
     k_attn_dkv<T, D, W, kDkv><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
   } else {

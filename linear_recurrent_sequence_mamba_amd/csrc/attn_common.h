@@ -53,6 +53,17 @@ __device__ __forceinline__ void frag_load(Frag<float>& f, const float* p) {
   f.a = *reinterpret_cast<const f4*>(p);
   f.b = *reinterpret_cast<const f4*>(p + 4);
 }
+// sum + <a, b> over a lane's eight elements
+__device__ __forceinline__ float frag_dot(const Frag<bf16_t>& a, const Frag<bf16_t>& b, float sum) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum = fmaf(static_cast<float>(a.v[j]), static_cast<float>(b.v[j]), sum);
+  return sum;
+}
+__device__ __forceinline__ float frag_dot(const Frag<float>& a, const Frag<float>& b, float sum) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sum = fmaf(a.a[j], b.a[j], fmaf(a.b[j], b.b[j], sum));
+  return sum;
+}
 // elements 8 s .. 8 s + 7 of a result (bf16: rounded to nearest, off by at
 // most 2^-8 of each weight before products that are summed in fp32)
 __device__ __forceinline__ void frag_from(Frag<bf16_t>& f, const float* v) {

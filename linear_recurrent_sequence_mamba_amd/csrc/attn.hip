@@ -232,7 +232,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   const int nslot = gridDim.x / a.Hq;
   const int h = blockIdx.x % a.Hq;
   // late tiles of a sequence see most keys: they start first
-  const Slot sl = slot_of<BM>(a.cuq, a.S, a.Tq, nslot - 1 - static_cast<int>(blockIdx.x / a.Hq), lane);
+  const Slot sl = query_slot<BM>(a, static_cast<int>(blockIdx.x / a.Hq), nslot, lane);
   if (sl.s < 0) return;
   const int q0 = clamp_row(a.cuq[sl.s], a.Tq), q1 = clamp_row(a.cuq[sl.s + 1], a.Tq);
   const int k0 = clamp_row(a.cuk[sl.s], a.Tk), k1 = clamp_row(a.cuk[sl.s + 1], a.Tk);

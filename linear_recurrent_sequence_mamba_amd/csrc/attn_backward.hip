@@ -126,7 +126,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
     a.stat[2 * all] = INFINITY;
     a.stat[2 * all + 1] = 0.0f;
   }
-  const Slot sl = slot_of<BM>(a.cuq, a.S, a.Tq, nslot - 1 - static_cast<int>(blockIdx.x / a.Hq), lane);
+  const Slot sl = query_slot<BM>(a, static_cast<int>(blockIdx.x / a.Hq), nslot, lane);
   if (sl.s < 0) return;
   const int q0 = clamp_row(a.cuq[sl.s], a.Tq), q1 = clamp_row(a.cuq[sl.s + 1], a.Tq);
   const int k0 = clamp_row(a.cuk[sl.s], a.Tk), k1 = clamp_row(a.cuk[sl.s + 1], a.Tk);
@@ -249,7 +249,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   const int per = a.Hk * a.gsplit;
   const int part = blockIdx.x % a.gsplit, hk = blockIdx.x % per / a.gsplit;
   // early keys are seen by most queries: they start first
-  const Slot sl = slot_of<BK>(a.cuk, a.S, a.Tk, static_cast<int>(blockIdx.x / per), lane);
+  const Slot sl = key_slot<BK>(a, static_cast<int>(blockIdx.x / per), lane);
   if (sl.s < 0) return;
   const int q0 = clamp_row(a.cuq[sl.s], a.Tq), q1 = clamp_row(a.cuq[sl.s + 1], a.Tq);
   const int k0 = clamp_row(a.cuk[sl.s], a.Tk), k1 = clamp_row(a.cuk[sl.s + 1], a.Tk);

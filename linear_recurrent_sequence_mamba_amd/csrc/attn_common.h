@@ -244,6 +244,70 @@ __device__ __forceinline__ Slot slot_of(const int32_t* cu, int S, int T, int slo
   return tile < 0 ? Slot{-1, 0} : Slot{lo, tile};
 }
 
+// The same for up to 64 sequences, in the order of the tiles' work, the largest
+// first: a batch of few, uneven sequences then ends at once on all CUs.  A lane
+// has a sequence of n tiles whose work grows by one from `a` on; the level at
+// which the rank lies is found by bisection between 0 and `top`.  (Counts are
+// below 2^24, so sums of floats are exact.)  `tile` is counted from the least
+// work.
+struct Ranked {
+  int n, a;
+  __device__ __forceinline__ Ranked(const int32_t* cu, int S, int T, int B, int lane) : n(0), a(0) {
+    if (lane < S) n = (max(0, clamp_row(cu[lane + 1], T) - clamp_row(cu[lane], T)) + B - 1) / B;
+  }
+  __device__ __forceinline__ int count(int x) const {   // tiles of level x and more
+    return __builtin_amdgcn_readfirstlane(
+        static_cast<int>(group_sum<64>(static_cast<float>(max(0, min(a + n - x, n))))));
+  }
+  __device__ __forceinline__ Slot at(int rank, int top, int lane) const {
+    if (rank >= count(0)) return Slot{-1, 0};
+    int lo = 0, hi = top;   // count(lo) > rank >= count(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (count(mid) > rank) lo = mid; else hi = mid;
+    }
+    const int nth = rank - count(hi);   // by all lanes: not behind a condition
+    const bool has = lo >= a && lo < a + n;
+    const uint64_t mask = __ballot(has);
+    const int before = __popcll(mask & ((uint64_t{1} << lane) - 1));
+    const uint64_t one = __ballot(has && before == nth);
+    if (one == 0) return Slot{-1, 0};
+    const int s = __builtin_ctzll(one);
+    return Slot{s, lo - __builtin_amdgcn_readlane(a, s)};
+  }
+};
+
+// Whether workgroups are taken in the order of their work: where a wave has a
+// lane for each sequence.  dk and dv always gain (8 sequences of 2048, 16 heads
+// of 128 on 2: all gradients 802 -> 702 us).  The queries' tiles gain where the
+// last workgroups weigh most, up to about four a CU (8192 rows in 3 uneven
+// sequences, 16 heads of 128: 131 -> 122 us; 4 of 2048: 97 -> 85; but 32 of 256:
+// 39 -> 43); with more of them several sequences' keys share the caches for
+// nothing (8 of 2048, 32 heads of 64: 200 us, ranked 215).
+__device__ __forceinline__ bool by_work(const AttnArgs& a) { return a.S > 1 && a.S <= 64; }
+
+// the n-th tile of B queries to start, of nslot
+template <int B>
+__device__ __forceinline__ Slot query_slot(const AttnArgs& a, int n, int nslot, int lane) {
+  if (!by_work(a) || gridDim.x > 2048) return slot_of<B>(a.cuq, a.S, a.Tq, nslot - 1 - n, lane);
+  Ranked r(a.cuq, a.S, a.Tq, B, lane);
+  if (lane < a.S) {   // tiles of keys before the first query's own
+    const int lk = clamp_row(a.cuk[lane + 1], a.Tk) - clamp_row(a.cuk[lane], a.Tk);
+    const int lq = clamp_row(a.cuq[lane + 1], a.Tq) - clamp_row(a.cuq[lane], a.Tq);
+    r.a = max(0, lk - lq) / B;
+  }
+  return r.at(n, max(a.Tq, a.Tk) / B + 3, lane);
+}
+// the n-th tile of B keys to start: the first keys are seen by most queries
+template <int B>
+__device__ __forceinline__ Slot key_slot(const AttnArgs& a, int n, int lane) {
+  if (!by_work(a)) return slot_of<B>(a.cuk, a.S, a.Tk, n, lane);
+  const Ranked r(a.cuk, a.S, a.Tk, B, lane);
+  Slot s = r.at(n, a.Tk / B + 3, lane);
+  if (s.s >= 0) s.tile = __builtin_amdgcn_readlane(r.n, s.s) - 1 - s.tile;
+  return s;
+}
+
 // maximum and sum of lanes l and l ^ 32, in both.  The swap exchanges the
 // upper half of its first operand with the lower half of its second.
 __device__ __forceinline__ float half_max(float v) {

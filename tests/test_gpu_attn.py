@@ -63,6 +63,20 @@ CASES = [  # queries and keys of each sequence, Hq, Hk, D
     ([257], [321], 5, 1, 64), ([0, 0, 2], [0, 4, 2], 2, 2, 128)]
 
 
+def _many(n, seed):
+    """n sequences of up to 40 queries; some are empty, some go on from more keys."""
+    g = torch.Generator().manual_seed(seed)
+    nq = torch.randint(0, 41, (n,), generator=g).tolist()
+    more = torch.randint(-5, 60, (n,), generator=g).clamp(min=0).tolist()
+    return nq, [a + b for a, b in zip(nq, more)]
+
+
+# more sequences than a wave has lanes; more workgroups than are taken in the
+# order of their work; sequences of several tiles whose order that changes
+CASES += [(*_many(70, 1), 4, 2, 64), (*_many(64, 2), 40, 4, 64), (*_many(64, 3), 3, 1, 128),
+          ([130, 400, 0, 257], [600, 400, 9, 300], 4, 2, 64), ([129, 300, 20], [129, 300, 700], 2, 2, 128)]
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("case", CASES)
 def test_prompt_and_gradients(case, dtype):

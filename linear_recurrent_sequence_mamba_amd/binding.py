@@ -723,10 +723,10 @@ def _nst(T):
     return (T + M3_GATED_CHUNK - 1) // M3_GATED_CHUNK
 
 
-def _ws(n, what, device):
+def _ws(n, what, like):
     if n == 0:
         raise M3Error(2, what)
-    return torch.empty((n + 15) // 16 * 16, dtype=torch.uint8, device=device)
+    return like.new_empty(((n + 15) // 16 * 16,), dtype=torch.uint8)
 
 
 def gated_scan(x, r, i, decay, h0=None, c=8.0, cu_seqlens=None, want_hT=True, want_states=False,
@@ -740,13 +740,12 @@ def gated_scan(x, r, i, decay, h0=None, c=8.0, cu_seqlens=None, want_hT=True, wa
     _dense("h0", h0, (B, D), torch.float32, optional=True)
     lib = _lib()
     with _on(dev, stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        hT = torch.empty((B, D), dtype=torch.float32, device=x.device) if want_hT else None
+        y = x.new_empty(x.shape)
+        hT = decay.new_empty((B, D)) if want_hT else None
         st = None
         if want_states:
-            st = torch.empty(((_nst(T),) if packed else (B, _nst(T))) + (D,), dtype=torch.float32,
-                             device=x.device)
-        ws = _ws(lib.m3_gated_scan_workspace_size(ref, packed), "m3_gated_scan", x.device)
+            st = decay.new_empty(((_nst(T),) if packed else (B, _nst(T))) + (D,))
+        ws = _ws(lib.m3_gated_scan_workspace_size(ref, packed), "m3_gated_scan", x)
         e = lib.m3_gated_scan(ref, _addr(cu_seqlens), _addr(x), _addr(r), _addr(i),
                               _addr(decay), _addr(h0), _addr(y), _addr(hT), _addr(st), _addr(ws),
                               ws.numel(), _raw(dev))
@@ -770,11 +769,11 @@ def gated_scan_backward(x, r, i, decay, dy, states, h0=None, dhT=None, c=8.0, cu
     _dense("states", states, ((_nst(T),) if packed else (B, _nst(T))) + (D,), torch.float32)
     lib = _lib()
     with _on(dev, stream):
-        g = {k: torch.empty(x.shape, dtype=x.dtype, device=x.device) for k in ("x", "r", "i")}
-        g["decay"] = torch.empty(D, dtype=torch.float32, device=x.device)
-        g["h0"] = torch.empty((B, D), dtype=torch.float32, device=x.device) if h0 is not None else None
+        g = {k: x.new_empty(x.shape) for k in ("x", "r", "i")}
+        g["decay"] = decay.new_empty((D,))
+        g["h0"] = decay.new_empty((B, D)) if h0 is not None else None
         ws = _ws(lib.m3_gated_scan_backward_workspace_size(ref, packed),
-                 "m3_gated_scan_backward", x.device)
+                 "m3_gated_scan_backward", x)
         e = lib.m3_gated_scan_backward(
             ref, _addr(cu_seqlens), _addr(x), _addr(r), _addr(i), _addr(decay), _addr(h0),
             _addr(states), _addr(dy), _addr(dhT), _addr(g["x"]), _addr(g["r"]), _addr(g["i"]),
@@ -848,14 +847,13 @@ def qk_norm_rope_backward(q, k, positions, dq_out, dk_out, q_weight=None, k_weig
     ref = _qk_setup(q, k, positions, q_weight, k_weight, eps, base, rotary_dim, flags)
     _dense("dq_out", dq_out, q.shape, q.dtype)
     _dense("dk_out", dk_out, k.shape, q.dtype)
-    lib, f32 = _lib(), torch.float32
+    lib = _lib()
     with _on(dev, stream):
-        g = dict(q=torch.empty(q.shape, dtype=q.dtype, device=q.device),
-                 k=torch.empty(k.shape, dtype=q.dtype, device=q.device))
+        g = dict(q=q.new_empty(q.shape), k=q.new_empty(k.shape))
         for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            g[n] = None if w is None else torch.empty(w.shape, dtype=f32, device=q.device)
+            g[n] = None if w is None else w.new_empty(w.shape)
         ws = _ws(lib.m3_qk_norm_rope_backward_workspace_size(ref),
-                 "m3_qk_norm_rope_backward", q.device)
+                 "m3_qk_norm_rope_backward", q)
         e = lib.m3_qk_norm_rope_backward(
             ref, _addr(q), _addr(k), _addr(q_weight), _addr(k_weight), _addr(positions),
             _addr(dq_out), _addr(dk_out), _addr(g["q"]), _addr(g["k"]), _addr(g["q_weight"]),
@@ -889,8 +887,8 @@ def attn_prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, scale=None, stream=
     dev = _same_device("q k v cu_seqlens_q cu_seqlens_k", q, k, v, cu_seqlens_q, cu_seqlens_k)
     ref = _attn_setup(q, k, v, cu_seqlens_q, cu_seqlens_k, scale)
     with _on(dev, stream):
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        o = q.new_empty(q.shape)
+        lse = q.new_empty(q.shape[:2], dtype=torch.float32)
         e = _lib().m3_attn_prefill_varlen(ref, _addr(cu_seqlens_q), _addr(cu_seqlens_k),
                                           _addr(q), _addr(k), _addr(v), _addr(o), _addr(lse),
                                           _raw(dev))
@@ -909,9 +907,9 @@ def attn_prefill_varlen_backward(q, k, v, o, lse, d_o, cu_seqlens_q, cu_seqlens_
     _dense("lse", lse, q.shape[:2], torch.float32)
     lib = _lib()
     with _on(dev, stream):
-        dq, dk, dv = (torch.empty(t.shape, dtype=q.dtype, device=q.device) for t in (q, k, v))
+        dq, dk, dv = (q.new_empty(t.shape) for t in (q, k, v))
         ws = _ws(lib.m3_attn_prefill_varlen_backward_workspace_size(ref),
-                 "m3_attn_prefill_varlen_backward", q.device)
+                 "m3_attn_prefill_varlen_backward", q)
         e = lib.m3_attn_prefill_varlen_backward(
             ref, _addr(cu_seqlens_q), _addr(cu_seqlens_k), _addr(q), _addr(k), _addr(v),
             _addr(o), _addr(lse), _addr(d_o), _addr(dq), _addr(dk), _addr(dv), _addr(ws), ws.numel(),
@@ -947,10 +945,10 @@ def attn_decode(q, k_cache, v_cache, lengths, scale=None, o=None, ws=None, strea
     lib = _lib()
     with _on(dev, stream):
         if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty((S, Hq), dtype=torch.float32, device=q.device)
+            o = q.new_empty(q.shape)
+        lse = q.new_empty((S, Hq), dtype=torch.float32)
         if ws is None:
-            ws = _ws(lib.m3_attn_decode_workspace_size(ref), "m3_attn_decode", q.device)
+            ws = _ws(lib.m3_attn_decode_workspace_size(ref), "m3_attn_decode", q)
         e = lib.m3_attn_decode(ref, _addr(lengths), _addr(q), _addr(k_cache),
                                _addr(v_cache), _addr(o), _addr(lse), _addr(ws),
                                ws.numel() * ws.element_size(), _raw(dev))

@@ -29,14 +29,12 @@ namespace {
 // products into the sum, and s of the tile `nxt`.  It is laid out product by
 // product, each with its share of the softmax and the operand of the product
 // two steps on: dp's products beside the exponentials, those of the next s
-// beside the rest of ds.  Rows count from `edge` on (kDq: up to it), the lane's
-// own offset 4 (lane / 32) taken off.
+// beside the rest of ds.  Scores that do not count are -inf (hide_*).
 enum { kDv = 0, kDk = 1, kDq = 2, kDkv = 3 };
 template <typename T, int D, int KIND>
 __device__ __forceinline__ void grad_step(f16v* sum, f16v* sum2, f16v& s, f16v& s2, const Frag<T>* x,
                                           const Frag<T>* y, const char* cur, const char* nxt,
-                                          const float* stat, float lse, float dd, float c, int edge,
-                                          int lane) {
+                                          const float* stat, float lse, float dd, float c, int lane) {
   using L = Tile<T, D>;
   constexpr bool DS = KIND != kDv;
   constexpr int N1 = D / 16;                  // products of each kind
@@ -84,8 +82,7 @@ __device__ __forceinline__ void grad_step(f16v* sum, f16v* sum2, f16v& s, f16v& 
     for (int e = 0; e < 16; ++e) {
       if (e * SW / 16 == n) {
         if (e % 4 == 0 && e < 12) l4[(e / 4 + 1) & 1] = stats(0, e / 4 + 1);
-        float w = __builtin_amdgcn_exp2f(fmaf(s[e], c, -l4[(e / 4) & 1][e % 4]));
-        w = (KIND == kDq ? row_of(e, 0) < edge : row_of(e, 0) >= edge) ? w : 0.0f;
+        const float w = __builtin_amdgcn_exp2f(fmaf(s[e], c, -l4[(e / 4) & 1][e % 4]));
         s[e] = w;
         if (KIND == kDv || KIND == kDkv) {
           v8[e % 8] = w;
@@ -100,6 +97,19 @@ __device__ __forceinline__ void grad_step(f16v* sum, f16v* sum2, f16v& s, f16v& 
     }
     __builtin_amdgcn_sched_barrier(0);
   }
+}
+
+// Only the rows before `edge`, or from it on, count.  (Called for the few tiles
+// on the diagonal: in every step it would be a fifth of the vector instructions.)
+__device__ __forceinline__ void hide_after(f16v& s, int edge, int lane) {
+  edge -= 4 * (opaque(lane) >> 5);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) s[e] = row_of(e, 0) < edge ? s[e] : -INFINITY;
+}
+__device__ __forceinline__ void hide_before(f16v& s, int edge, int lane) {
+  edge -= 4 * (opaque(lane) >> 5);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) s[e] = row_of(e, 0) >= edge ? s[e] : -INFINITY;
 }
 
 // D_i = <o_i, do_i> takes o as it was rounded, from weights that were.  Over n
@@ -157,12 +167,12 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
     for (int kk = 0; kk < D / 16; ++kk) dd = frag_dot(o[kk], g[kk], dd);
     dd = half_sum(dd);
   }
+  if (lse == -INFINITY) lse = INFINITY;   // no key: every weight 0
   float* st = a.stat + static_cast<int64_t>(h) * a.Tq + row;
   if (half == 0 && i < Lq) {
     st[0] = lse;
     st[all] = dd;
   }
-  if (lse == -INFINITY) lse = INFINITY;   // no key: every weight 0
   f16v dq[D / 32];
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) dq[d] = f16v{};
@@ -197,11 +207,16 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
     dd = half_sum(r);
     if (half == 0 && i < Lq) st[all] = dd;
   }
+  const auto pr = L::pair(kp, a.ldk, vp, a.ldv, wave, lane);
+  auto fetch = [&](int buf, int t) __attribute__((always_inline)) {
+    L::template load2<WAVES>(sKV[buf], pr, kp, a.ldk, vp, a.ldv, 0, t * BN, Lk - 1, wave, lane);
+  };
+  const int all_see = min(iw, Lq - 1) + off + 1;   // keys that every query of the wave sees
   if (ntile > 0) {
-    L::template load2<WAVES>(sKV[0], kp, a.ldk, vp, a.ldv, 0, Lk - 1, wave, lane);
+    fetch(0, 0);
     lds_loads_done();
     __syncthreads();
-    if (ntile > 1) L::template load2<WAVES>(sKV[1], kp, a.ldk, vp, a.ldv, BN, Lk - 1, wave, lane);
+    if (ntile > 1) fetch(1, 1);
     s = f16v{};
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) s = mma(L::frag(sKV[0], 0, kk, lane), q[kk], s);
@@ -211,8 +226,9 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
     lds_loads_done();
     __syncthreads();   // tile t + 1 is there; every wave is done with t - 1
     const int nxt = cur == 2 ? 0 : cur + 1, aft = nxt == 2 ? 0 : nxt + 1;
-    if (t + 2 < ntile) L::template load2<WAVES>(sKV[aft], kp, a.ldk, vp, a.ldv, (t + 2) * BN, Lk - 1, wave, lane);
-    grad_step<T, D, kDq>(dq, nullptr, s, s2, q, g, sKV[cur], sKV[nxt], nullptr, lse, dd, c, sees - t * BN - 4 * half, lane);
+    if (t + 2 < ntile) fetch(aft, t + 2);
+    if ((t + 1) * BN > all_see) hide_after(s, sees - t * BN, lane);
+    grad_step<T, D, kDq>(dq, nullptr, s, s2, q, g, sKV[cur], sKV[nxt], nullptr, lse, dd, c, lane);
     cur = nxt;
   };
   for (int t = 0; t < ntile; t += 2) {   // by two: the scores change places
@@ -278,10 +294,11 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   const int nt = max(0, (Lq + BQ - 1) / BQ - first), all = nt * gper;
   // the tiles run over the queries of one head after the other
   int fh = hk * grp + part * gper, fi = first;   // of the next fetch
+  const T* qp = static_cast<const T*>(a.q) + static_cast<int64_t>(q0) * a.ldq;
+  const T* gp = static_cast<const T*>(a.dout) + static_cast<int64_t>(q0) * a.lddo;
+  const auto pr = L::pair(qp, a.ldq, gp, a.lddo, wave, lane);
   auto fetch = [&](int buf) __attribute__((always_inline)) {
-    const T* qp = static_cast<const T*>(a.q) + static_cast<int64_t>(q0) * a.ldq + fh * D;
-    const T* gp = static_cast<const T*>(a.dout) + static_cast<int64_t>(q0) * a.lddo + fh * D;
-    L::template load2<WAVES>(sQG[buf], qp, a.ldq, gp, a.lddo, fi * BQ, Lq - 1, wave, lane);
+    L::template load2<WAVES>(sQG[buf], pr, qp, a.ldq, gp, a.lddo, fh * D, fi * BQ, Lq - 1, wave, lane);
     if (wave == 0) {   // lse of 32 rows, then D of them; past the last row infinity and 0
       const int i = fi * BQ + (lane & 31);
       const float* src = a.stat + (i < Lq ? (static_cast<int64_t>(half) * a.Hq + fh) * a.Tq + q0 + i
@@ -311,8 +328,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
     if (n + 2 < all) fetch(aft);
     const int i0 = ci * BQ;
     // rows i >= j - off count
-    grad_step<T, D, KIND>(sum, sum2, s, s2, k, v, sQG[cur], sQG[nxt], sS[cur], 0.0f, 0.0f, c,
-                          j - off - i0 - 4 * half, lane);
+    if (i0 < jw + 31 - off) hide_before(s, j - off - i0, lane);
+    grad_step<T, D, KIND>(sum, sum2, s, s2, k, v, sQG[cur], sQG[nxt], sS[cur], 0.0f, 0.0f, c, lane);
     cur = nxt;
     if (++ci == first + nt) ci = first;
   };

@@ -166,6 +166,39 @@ struct Tile {
     }
   }
 
+  // The same for a loop over tiles: a lane's first row in a or b, and the bytes
+  // to the next one.  A tile that is whole then takes one product and a few
+  // additions instead of a clamp and two products for each load.
+  struct Pair {
+    const char* at;
+    uint32_t ld;
+  };
+  static __device__ __forceinline__ Pair pair(const T* a, int64_t lda, const T* b, int64_t ldb, int w,
+                                              int lane) {
+    const int r = group_row(w) + lane_row(lane);
+    const bool second = r >= 32;
+    const int64_t ld = second ? ldb : lda;
+    return Pair{reinterpret_cast<const char*>((second ? b : a) + (r & 31) * ld + EPC * (lane % CPR)),
+                static_cast<uint32_t>(ld) * static_cast<uint32_t>(sizeof(T))};
+  }
+  // `by` elements beyond a and b
+  template <int NW>
+  static __device__ __forceinline__ void load2(char* lds, const Pair& p, const T* a, int64_t lda,
+                                               const T* b, int64_t ldb, int64_t by, int row0, int last,
+                                               int w, int lane) {
+    if (RB == 512 || row0 + 31 > last) {   // (512: a and b are in loads of their own)
+      load2<NW>(lds, a + by, lda, b + by, ldb, row0, last, w, opaque(lane));
+      return;
+    }
+    const char* src = p.at + by * static_cast<int64_t>(sizeof(T)) +
+                      static_cast<uint64_t>(static_cast<uint32_t>(row0)) * p.ld;
+#pragma unroll
+    for (int n = 0; n < NG / NW; ++n)
+      __builtin_amdgcn_global_load_lds(
+          (const M3_GLB void*)(src + static_cast<uint64_t>(p.ld) * group_row(n * NW)),
+          (M3_LDS void*)(lds + place(n * NW + w)), 16, 0, 0);
+  }
+
   // fragment kk (elements 16 kk ..) of rows row0 + lane % 32 (row0 0 or 32)
   static __device__ __forceinline__ Frag<T> frag(const char* lds, int row0, int kk, int lane) {
     const int r = lane & 31, h = lane >> 5;

@@ -17,7 +17,7 @@ struct AttnArgs {
   const void *co, *dout;        // o and its gradient, rows ldo / lddo apart
   const float* clse;
   void *dq, *dk, *dv;           // dense rows
-  float* stat;                  // workspace [2, Hq, Tq]: lse log2(e), then <o, do>; infinity and 0
+  float* stat;                  // workspace [2, Hq, Tq]: lse log2(e), then -<o, do>; infinity and 0
   float *pk, *pv;               // workspace [gsplit, Tk, Hk, D]: parts of dk, dv
   // decode
   const int32_t* len;           // [S] rows of each sequence's cache

@@ -178,8 +178,9 @@ __device__ __forceinline__ float weigh_ahead(Rows<D>& st, f16v* s, f16v* next, c
       st.o[d] = mma(op[n % 3], p[m / (D / 32)], st.o[d]);
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      if (e * S / E != n) continue;
+    for (int j = 0; j < (E + S - 1) / S; ++j) {
+      const int e = (n * E + S - 1) / S + j;
+      if (e >= E || e * S / E != n) continue;
       const float v = __builtin_amdgcn_exp2f(fmaf(s[e / 16][e % 16], c, -m0));
       s[e / 16][e % 16] = v;
       st.l += v;
@@ -187,16 +188,19 @@ __device__ __forceinline__ float weigh_ahead(Rows<D>& st, f16v* s, f16v* next, c
       if (e % 8 == 7) {
         float e8[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) e8[j] = s[e / 16][e % 16 - 7 + j];
+        for (int x = 0; x < 8; ++x) e8[x] = s[e / 16][e % 16 - 7 + x];
         frag_from(p[e / 8], e8);
       }
     }
     // the last quarter of the next scores is still on its way at step NM
     constexpr int M0 = NM + 3, MS = 2 * NM - M0;
-    if (n == M0) mx = next[0][0];
+    // two at a time: one instruction takes the maximum of three
 #pragma unroll
-    for (int e = 1; e < E; ++e)
-      if (M0 + e * MS / E == n) mx = fmaxf(mx, next[e / 16][e % 16]);
+    for (int j = 0; j < (E / 2 + MS - 1) / MS; ++j) {
+      const int e = 2 * (((n - M0) * (E / 2) + MS - 1) / MS + j);
+      if (n >= M0 && e < E && M0 + e / 2 * MS / (E / 2) == n)
+        mx = fmaxf(fmaxf(mx, next[e / 16][e % 16]), next[e / 16][e % 16 + 1]);
+    }
     if (n >= M0) asm volatile("" : "+v"(mx));
     __builtin_amdgcn_sched_barrier(0);
   }

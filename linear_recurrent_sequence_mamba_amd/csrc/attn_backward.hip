@@ -34,7 +34,7 @@ enum { kDv = 0, kDk = 1, kDq = 2, kDkv = 3 };
 template <typename T, int D, int KIND>
 __device__ __forceinline__ void grad_step(f16v* sum, f16v* sum2, f16v& s, f16v& s2, const Frag<T>* x,
                                           const Frag<T>* y, const char* cur, const char* nxt,
-                                          const float* stat, float lse, float dd, float c, int lane) {
+                                          const float* stat, float lse, const f16v& nd, float c, int lane) {
   using L = Tile<T, D>;
   constexpr bool DS = KIND != kDv;
   constexpr int N1 = D / 16;                  // products of each kind
@@ -50,17 +50,34 @@ __device__ __forceinline__ void grad_step(f16v* sum, f16v* sum2, f16v& s, f16v& 
     const int m = (n - B) % N1;
     return L::frag_t(cur, (DS && n >= C ? 0 : 32) + 16 * (m / (N1 / 2)), 32 * (m % (N1 / 2)), lane);
   };
-  // lse (which = 0) or D (1) of the rows 8 b + 4 half + 0 .. 3; of queries as
+  // lse (which = 0) or -D (1) of the rows 8 b + 4 half + 0 .. 3; of queries as
   // lanes they are the lane's own
   auto stats = [&](int which, int b) __attribute__((always_inline)) -> f4 {
-    if (KIND == kDq) return which ? f4{dd, dd, dd, dd} : f4{lse, lse, lse, lse};
+    if (KIND == kDq) return f4{lse, lse, lse, lse};
     return *reinterpret_cast<const f4*>(stat + 32 * which + 8 * b + 4 * half);
   };
-  f16v dp;
-  if (DS) dp = f16v{};
+  f16v dp;   // - D from the start: the products are added to it
+  if (KIND == kDq) {
+    if constexpr (D == 128) {
+      dp = nd;
+    } else {   // 16 registers more would leave two waves a SIMD instead of three
+      float x = nd[0];
+      asm volatile("" : "+v"(x));
+#pragma unroll
+      for (int e = 0; e < 16; ++e) dp[e] = x;
+    }
+  }
+  if (KIND == kDk || KIND == kDkv) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const f4 d = stats(1, b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dp[4 * b + j] = d[j];
+    }
+  }
   s2 = f16v{};
   Frag<T> op[3], f[2], f2_[2];
-  f4 l4[2], d4[2];
+  f4 l4[2];
   l4[0] = stats(0, 0);
   op[0] = operand(0);
   op[1] = operand(1);
@@ -77,7 +94,6 @@ __device__ __forceinline__ void grad_step(f16v* sum, f16v* sum2, f16v& s, f16v& 
       if (n < C) sum2[d] = mma(op[n % 3], f2_[w], sum2[d]);
       else sum[d] = mma(op[n % 3], f[w], sum[d]);
     }
-    if (DS && n == A - 1) d4[0] = stats(1, 0);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       if (e * SW / 16 == n) {
@@ -90,8 +106,7 @@ __device__ __forceinline__ void grad_step(f16v* sum, f16v* sum2, f16v& s, f16v& 
         }
       }
       if (DS && A + 1 + e * SD / 16 == n) {
-        if (e % 4 == 0 && e < 12) d4[(e / 4 + 1) & 1] = stats(1, e / 4 + 1);
-        w8[e % 8] = s[e] * (dp[e] - d4[(e / 4) & 1][e % 4]);
+        w8[e % 8] = s[e] * dp[e];
         if (e % 8 == 7) frag_from(f[e / 8], w8);
       }
     }
@@ -171,7 +186,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   float* st = a.stat + static_cast<int64_t>(h) * a.Tq + row;
   if (half == 0 && i < Lq) {
     st[0] = lse;
-    st[all] = dd;
+    st[all] = -dd;
   }
   f16v dq[D / 32];
 #pragma unroll
@@ -205,7 +220,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
       __syncthreads();
     }
     dd = half_sum(r);
-    if (half == 0 && i < Lq) st[all] = dd;
+    if (half == 0 && i < Lq) st[all] = -dd;
   }
   const auto pr = L::pair(kp, a.ldk, vp, a.ldv, wave, lane);
   auto fetch = [&](int buf, int t) __attribute__((always_inline)) {
@@ -221,6 +236,9 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) s = mma(L::frag(sKV[0], 0, kk, lane), q[kk], s);
   }
+  f16v nd;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) nd[e] = -dd;
   int cur = 0;
   auto step = [&](int t, f16v& s, f16v& s2) __attribute__((always_inline)) {
     lds_loads_done();
@@ -228,7 +246,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
     const int nxt = cur == 2 ? 0 : cur + 1, aft = nxt == 2 ? 0 : nxt + 1;
     if (t + 2 < ntile) fetch(aft, t + 2);
     if ((t + 1) * BN > all_see) hide_after(s, sees - t * BN, lane);
-    grad_step<T, D, kDq>(dq, nullptr, s, s2, q, g, sKV[cur], sKV[nxt], nullptr, lse, dd, c, lane);
+    grad_step<T, D, kDq>(dq, nullptr, s, s2, q, g, sKV[cur], sKV[nxt], nullptr, lse, nd, c, lane);
     cur = nxt;
   };
   for (int t = 0; t < ntile; t += 2) {   // by two: the scores change places
@@ -299,7 +317,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   const auto pr = L::pair(qp, a.ldq, gp, a.lddo, wave, lane);
   auto fetch = [&](int buf) __attribute__((always_inline)) {
     L::template load2<WAVES>(sQG[buf], pr, qp, a.ldq, gp, a.lddo, fh * D, fi * BQ, Lq - 1, wave, lane);
-    if (wave == 0) {   // lse of 32 rows, then D of them; past the last row infinity and 0
+    if (wave == 0) {   // lse of 32 rows, then -D of them; past the last row infinity and 0
       const int i = fi * BQ + (lane & 31);
       const float* src = a.stat + (i < Lq ? (static_cast<int64_t>(half) * a.Hq + fh) * a.Tq + q0 + i
                                           : 2 * static_cast<int64_t>(a.Hq) * a.Tq + half);
@@ -329,7 +347,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
     const int i0 = ci * BQ;
     // rows i >= j - off count
     if (i0 < jw + 31 - off) hide_before(s, j - off - i0, lane);
-    grad_step<T, D, KIND>(sum, sum2, s, s2, k, v, sQG[cur], sQG[nxt], sS[cur], 0.0f, 0.0f, c, lane);
+    grad_step<T, D, KIND>(sum, sum2, s, s2, k, v, sQG[cur], sQG[nxt], sS[cur], 0.0f, f16v{}, c, lane);
     cur = nxt;
     if (++ci == first + nt) ci = first;
   };

@@ -229,7 +229,9 @@ template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn(AttnArgs a) {
   using L = Tile<T, D>;
   constexpr int BM = 32 * WAVES, BN = 64, NB = 2;
-  __shared__ __align__(16) char sK[2][L::BYTES], sV[2][L::BYTES];
+  // (variables of their own, used by name: of one array the compiler takes every
+  // read to follow the loads that are on their way, and waits for them)
+  __shared__ __align__(16) char sK0[L::BYTES], sK1[L::BYTES], sV0[L::BYTES], sV1[L::BYTES];
   __shared__ int sSpecial;
   if (threadIdx.x == 0) sSpecial = 0;   // read after the tiles' barriers
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -273,41 +275,46 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   f16v s[NB], next[NB];
   const int nw = (max(wmost, 0) + BN - 1) / BN;   // tiles that the wave sees
   const int npipe = max(0, min(tmask, ntile - 1)) & ~1;   // (no tile: none)
-  auto arrive = [&](int t) __attribute__((always_inline)) {
+  auto arrive = [&](int t, char* K, char* V) __attribute__((always_inline)) {
     lds_loads_done();
     __syncthreads();   // V of t and K of t + 1 are there; every wave is done with t - 1
-    if (t + 2 < ntile) L::template load<WAVES>(sK[t & 1], kp, a.ldk, (t + 2) * BN, Lk - 1, wave, lane);
-    if (t + 1 < ntile) L::template load<WAVES>(sV[(t + 1) & 1], vp, a.ldv, (t + 1) * BN, Lk - 1, wave, lane);
+    if (t + 2 < ntile) L::template load<WAVES>(K, kp, a.ldk, (t + 2) * BN, Lk - 1, wave, lane);
+    if (t + 1 < ntile) L::template load<WAVES>(V, vp, a.ldv, (t + 1) * BN, Lk - 1, wave, lane);
+    // At D = 128 it is faster to let the loads end before the tiles at hand are
+    // read (16384 tokens, 16 heads: 1042 us, not waiting 1061), at D = 64 not to
+    // (packed rows of 32 heads: 264 and 255 us).
+    if (D == 128) lds_loads_done();
   };
   if (ntile > 0) {
-    L::template load<WAVES>(sK[0], kp, a.ldk, 0, Lk - 1, wave, lane);
+    L::template load<WAVES>(sK0, kp, a.ldk, 0, Lk - 1, wave, lane);
     lds_loads_done();
     __syncthreads();
-    L::template load<WAVES>(sV[0], vp, a.ldv, 0, Lk - 1, wave, lane);
-    if (ntile > 1) L::template load<WAVES>(sK[1], kp, a.ldk, BN, Lk - 1, wave, lane);
-    score<T, D, NB>(s, q, sK[0], lane);
+    L::template load<WAVES>(sV0, vp, a.ldv, 0, Lk - 1, wave, lane);
+    if (ntile > 1) L::template load<WAVES>(sK1, kp, a.ldk, BN, Lk - 1, wave, lane);
+    score<T, D, NB>(s, q, sK0, lane);
   }
   float mx = npipe > 0 ? max_of<NB>(s) : 0.0f;
   for (int t = 0; t < npipe; t += 2) {
-    arrive(t);
+    arrive(t, sK0, sV1);
     raise_max<D>(st, mx, c);
-    mx = weigh_ahead<T, D, NB>(st, s, next, q, sK[1], sV[0], c, lane);
-    arrive(t + 1);
+    mx = weigh_ahead<T, D, NB>(st, s, next, q, sK1, sV0, c, lane);
+    arrive(t + 1, sK1, sV0);
     raise_max<D>(st, mx, c);
-    mx = weigh_ahead<T, D, NB>(st, next, s, q, sK[0], sV[1], c, lane);
+    mx = weigh_ahead<T, D, NB>(st, next, s, q, sK0, sV1, c, lane);
   }
 #pragma unroll 1
   for (int t = npipe; t < ntile; ++t) {
-    arrive(t);
+    char* const V = t & 1 ? sV1 : sV0;
+    arrive(t, t & 1 ? sK1 : sK0, t & 1 ? sV0 : sV1);
     if (t >= tmask) {
-      if (drop_special<T, D, 64 * WAVES>(sV[t & 1])) sSpecial = 1;
+      if (drop_special<T, D, 64 * WAVES>(V)) sSpecial = 1;
       __syncthreads();
     }
     if (t >= nw) continue;
     hide<NB>(s, sees - t * BN, lane);
     raise_max<D>(st, max_of<NB>(s), c);
-    weigh<T, D, NB>(st, s, sV[t & 1], c, lane);
-    if (t + 1 < nw) score<T, D, NB>(s, q, sK[(t + 1) & 1], lane);
+    weigh<T, D, NB>(st, s, V, c, lane);
+    if (t + 1 < nw) score<T, D, NB>(s, q, t & 1 ? sK0 : sK1, lane);
   }
   if (ntile > 0 && sSpecial) {
     for (int key = tmask * BN; key < most; ++key) {

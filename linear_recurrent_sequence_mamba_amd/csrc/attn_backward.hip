@@ -16,103 +16,107 @@
 
 namespace m3 {
 namespace {
+typedef int i4 __attribute__((ext_vector_type(4)));
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
 
 // ---------------------------------------------------------------------------
-// One step of a sum over tiles of 32 rows, the same for the three gradients:
-//   kDv  lanes are keys, rows queries: sum += p^T do
-//   kDk  lanes are keys, rows queries: sum += ds^T q
-//   kDkv both, sum for dk and sum2 for dv
-//   kDq  lanes are queries, rows keys: sum += ds k
-// A tile holds the rows that s is formed of (q, q, k) and, from row 32 on, the
-// others (do, do, v); x and y are the lanes' own (k v, k v, q do).  From s of
-// the tile `cur` the step forms the weights, then (kDk, kDq) ds, then the
-// products into the sum, and s of the tile `nxt`.  It is laid out product by
-// product, each with its share of the softmax and the operand of the product
-// two steps on: dp's products beside the exponentials, those of the next s
-// beside the rest of ds.  Scores that do not count are -inf (hide_*).
-enum { kDv = 0, kDk = 1, kDq = 2, kDkv = 3 };
+// One step of the sums over tiles of 32 rows:
+//   kDq   lanes are queries, rows keys: sum += ds k
+//   kDkv  lanes are keys, rows queries: sum (dk) += ds^T q, sum2 (dv) += p^T do
+// A tile holds the rows that s is formed of (k; q) and, from row 32 on, the
+// others (v; do); x and y are the lanes' own (q do; k v).  From s of the tile
+// `cur` the step forms the weights, dp and ds, the products into the sums, and
+// s of the tile `nxt`.  It is laid out product by product, each with its share
+// of the softmax and the operand of a product some steps on: dp's products
+// beside the exponentials, those of the next s beside the rest of ds.  Scores
+// that do not count are -inf (hide_*).
+enum { kDq = 0, kDkv = 1 };
+
 template <typename T, int D, int KIND>
-__device__ __forceinline__ void grad_step(f16v* sum, f16v* sum2, f16v& s, f16v& s2, const Frag<T>* x,
-                                          const Frag<T>* y, const char* cur, const char* nxt,
-                                          const float* stat, float lse, const f16v& nd, float c, int lane) {
+struct Grad {
   using L = Tile<T, D>;
-  constexpr bool DS = KIND != kDv;
-  constexpr int N1 = D / 16;                  // products of each kind
-  constexpr int A = DS ? N1 : 0, B = A + N1;  // first product of s2, of the first sum
-  constexpr int C = KIND == kDkv ? B + N1 : B;        // ... of dk's
+  static constexpr int N1 = D / 16;                  // products of each kind
+  static constexpr int A = N1, B = A + N1;           // first product of s2, of the first sum
+  static constexpr int C = KIND == kDkv ? B + N1 : B;        // ... of dk's
+  static constexpr int N = C + N1;
+  // operands are read so many products before they are used (dk and dv of 128
+  // channels have a SIMD to themselves; two everywhere: 2% slower)
+  static constexpr int AHEAD = D == 128 && KIND == kDkv ? 4 : 3, R = AHEAD + 1;
   // steps over which the weights are spread: beside dp's products, or until
   // dv's sum needs them; and those of ds, which follows dp
-  constexpr int SW = KIND == kDv || KIND == kDkv ? B + N1 / 2 : A, SD = C + N1 / 2 - A - 1;
-  const int half = lane >> 5;
-  auto operand = [&](int n) __attribute__((always_inline)) -> Frag<T> {
+  static constexpr int SW = KIND == kDkv ? B + N1 / 2 : A, SD = C + N1 / 2 - A - 1;
+
+  static __device__ __forceinline__ Frag<T> operand(const char* cur, const char* nxt, int n, int lane) {
     if (n < A) return L::frag(cur, 32, n, lane);
     if (n < B) return L::frag(nxt, 0, n - A, lane);
     const int m = (n - B) % N1;
-    return L::frag_t(cur, (DS && n >= C ? 0 : 32) + 16 * (m / (N1 / 2)), 32 * (m % (N1 / 2)), lane);
-  };
+    return L::frag_t(cur, (n >= C ? 0 : 32) + 16 * (m / (N1 / 2)), 32 * (m % (N1 / 2)), lane);
+  }
   // lse (which = 0) or -D (1) of the rows 8 b + 4 half + 0 .. 3; of queries as
   // lanes they are the lane's own
-  auto stats = [&](int which, int b) __attribute__((always_inline)) -> f4 {
+  static __device__ __forceinline__ f4 stats(const float* stat, float lse, int which, int b, int lane) {
     if (KIND == kDq) return f4{lse, lse, lse, lse};
-    return *reinterpret_cast<const f4*>(stat + 32 * which + 8 * b + 4 * half);
-  };
-  f16v dp;   // - D from the start: the products are added to it
-  if (KIND == kDq) {
-    if constexpr (D == 128) {
-      dp = nd;
-    } else {   // 16 registers more would leave two waves a SIMD instead of three
-      float x = nd[0];
-      asm volatile("" : "+v"(x));
-#pragma unroll
-      for (int e = 0; e < 16; ++e) dp[e] = x;
-    }
+    const int at = 32 * which + 8 * b + 4 * (lane >> 5);
+    return *reinterpret_cast<const f4*>(stat + at);
   }
-  if (KIND == kDk || KIND == kDkv) {
+  static __device__ __forceinline__ void step(f16v* sum, f16v* sum2, f16v& s, f16v& s2, const Frag<T>* x,
+                                              const Frag<T>* y, const char* cur, const char* nxt,
+                                              const float* stat, float lse, float nd, float c,
+                                              int lane) {
+    f16v dp;   // - D from the start: the products are added to it
+    if (KIND == kDq) {
+      float z = nd;   // (a vector of it would be kept in 16 registers)
+      asm volatile("" : "+v"(z));
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const f4 d = stats(1, b);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) dp[4 * b + j] = d[j];
-    }
-  }
-  s2 = f16v{};
-  Frag<T> op[3], f[2], f2_[2];
-  f4 l4[2];
-  l4[0] = stats(0, 0);
-  op[0] = operand(0);
-  op[1] = operand(1);
-  float w8[8], v8[8];
-#pragma unroll
-  for (int n = 0; n < C + N1; ++n) {
-    if (n + 2 < C + N1) op[(n + 2) % 3] = operand(n + 2);
-    if (n < A) {
-      dp = mma(op[n % 3], y[n], dp);
-    } else if (n < B) {
-      s2 = mma(op[n % 3], x[n - A], s2);
+      for (int e = 0; e < 16; ++e) dp[e] = z;
     } else {
-      const int m = (n - B) % N1, w = m / (N1 / 2), d = m % (N1 / 2);
-      if (n < C) sum2[d] = mma(op[n % 3], f2_[w], sum2[d]);
-      else sum[d] = mma(op[n % 3], f[w], sum[d]);
-    }
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if (e * SW / 16 == n) {
-        if (e % 4 == 0 && e < 12) l4[(e / 4 + 1) & 1] = stats(0, e / 4 + 1);
-        const float w = __builtin_amdgcn_exp2f(fmaf(s[e], c, -l4[(e / 4) & 1][e % 4]));
-        s[e] = w;
-        if (KIND == kDv || KIND == kDkv) {
-          v8[e % 8] = w;
-          if (e % 8 == 7) frag_from(KIND == kDv ? f[e / 8] : f2_[e / 8], v8);
+      for (int b = 0; b < 4; ++b) {
+        const f4 d = stats(stat, 0.0f, 1, b, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dp[4 * b + j] = d[j];
+      }
+    }
+    s2 = f16v{};
+    Frag<T> op[R], f[2], fw[2];
+    f4 l4[2];
+    l4[0] = stats(stat, lse, 0, 0, lane);
+#pragma unroll
+    for (int n = 0; n < AHEAD; ++n) op[n] = operand(cur, nxt, n, lane);
+    float w8[8], v8[8];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      if (n + AHEAD < N) op[(n + AHEAD) % R] = operand(cur, nxt, n + AHEAD, lane);
+      if (n < A) {
+        dp = mma(op[n % R], y[n], dp);
+      } else if (n < B) {
+        s2 = mma(op[n % R], x[n - A], s2);
+      } else {
+        const int m = (n - B) % N1, w = m / (N1 / 2), d = m % (N1 / 2);
+        if (n < C) sum2[d] = mma(op[n % R], fw[w], sum2[d]);
+        else sum[d] = mma(op[n % R], f[w], sum[d]);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        if (e * SW / 16 == n) {
+          if (e % 4 == 0 && e < 12) l4[(e / 4 + 1) & 1] = stats(stat, lse, 0, e / 4 + 1, lane);
+          const float w = __builtin_amdgcn_exp2f(fmaf(s[e], c, -l4[(e / 4) & 1][e % 4]));
+          s[e] = w;
+          if (KIND == kDkv) {
+            v8[e % 8] = w;
+            if (e % 8 == 7) frag_from(fw[e / 8], v8);
+          }
+        }
+        if (A + 1 + e * SD / 16 == n) {
+          w8[e % 8] = s[e] * dp[e];
+          if (e % 8 == 7) frag_from(f[e / 8], w8);
         }
       }
-      if (DS && A + 1 + e * SD / 16 == n) {
-        w8[e % 8] = s[e] * dp[e];
-        if (e % 8 == 7) frag_from(f[e / 8], w8);
-      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_barrier(0);
   }
-}
+};
 
 // Only the rows before `edge`, or from it on, count.  (Called for the few tiles
 // on the diagonal: in every step it would be a fifth of the vector instructions.)
@@ -142,7 +146,10 @@ template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn_dq(AttnArgs a) {
   using L = Tile<T, D>;
   constexpr int BM = 32 * WAVES, BN = 32;
-  __shared__ __align__(16) char sKV[3][L::BYTES];   // tiles t, t + 1 (its s), t + 2 (arriving)
+  // Tiles t, t + 1 (its s), t + 2 and t + 3 (arriving).  Variables of their own,
+  // used by name: of one array the compiler takes every read to follow the loads
+  // that are on their way, and waits for them.
+  __shared__ __align__(16) char sT0[L::BYTES], sT1[L::BYTES], sT2[L::BYTES], sT3[L::BYTES];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nslot = gridDim.x / a.Hq;
   const int h = blockIdx.x % a.Hq;
@@ -203,15 +210,15 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
     float r = 0.0f;
 #pragma unroll 1
     for (int t = 0; t < ntile; ++t) {
-      L::template load2<WAVES>(sKV[0], kp, a.ldk, vp, a.ldv, t * BN, Lk - 1, wave, lane);
+      L::template load2<WAVES>(sT0, kp, a.ldk, vp, a.ldv, t * BN, Lk - 1, wave, lane);
       lds_loads_done();
       __syncthreads();
       s = f16v{};
       s2 = f16v{};
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        s = mma(L::frag(sKV[0], 0, kk, lane), q[kk], s);
-        s2 = mma(L::frag(sKV[0], 32, kk, lane), g[kk], s2);
+        s = mma(L::frag(sT0, 0, kk, lane), q[kk], s);
+        s2 = mma(L::frag(sT0, 32, kk, lane), g[kk], s2);
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e)
@@ -223,35 +230,42 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
     if (half == 0 && i < Lq) st[all] = -dd;
   }
   const auto pr = L::pair(kp, a.ldk, vp, a.ldv, wave, lane);
-  auto fetch = [&](int buf, int t) __attribute__((always_inline)) {
-    L::template load2<WAVES>(sKV[buf], pr, kp, a.ldk, vp, a.ldv, 0, t * BN, Lk - 1, wave, lane);
+  auto fetch = [&](char* to, int t) __attribute__((always_inline)) {
+    L::template load2<WAVES>(to, pr, kp, a.ldk, vp, a.ldv, 0, t * BN, Lk - 1, wave, lane);
   };
   const int all_see = min(iw, Lq - 1) + off + 1;   // keys that every query of the wave sees
   if (ntile > 0) {
-    fetch(0, 0);
+    fetch(sT0, 0);
     lds_loads_done();
     __syncthreads();
-    if (ntile > 1) fetch(1, 1);
+    if (ntile > 1) fetch(sT1, 1);
+    if (ntile > 2) fetch(sT2, 2);
     s = f16v{};
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) s = mma(L::frag(sKV[0], 0, kk, lane), q[kk], s);
+    for (int kk = 0; kk < D / 16; ++kk) s = mma(L::frag(sT0, 0, kk, lane), q[kk], s);
   }
-  f16v nd;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) nd[e] = -dd;
-  int cur = 0;
-  auto step = [&](int t, f16v& s, f16v& s2) __attribute__((always_inline)) {
-    lds_loads_done();
-    __syncthreads();   // tile t + 1 is there; every wave is done with t - 1
-    const int nxt = cur == 2 ? 0 : cur + 1, aft = nxt == 2 ? 0 : nxt + 1;
-    if (t + 2 < ntile) fetch(aft, t + 2);
+  // (in the loop's body all loads are made, so that the compiler, too, knows
+  // which are still on their way)
+  auto step = [&](auto in, int t, char* cur, char* nxt, char* aft, f16v& s, f16v& s2)
+                  __attribute__((always_inline)) {
+    if (in.value || t + 2 < ntile) lds_loads_but<L::NG / WAVES>(); else lds_loads_done();
+    tiles_barrier();   // tile t + 1 is there; every wave is done with t - 1
+    if (in.value || t + 3 < ntile) fetch(aft, t + 3);
     if ((t + 1) * BN > all_see) hide_after(s, sees - t * BN, lane);
-    grad_step<T, D, kDq>(dq, nullptr, s, s2, q, g, sKV[cur], sKV[nxt], nullptr, lse, nd, c, lane);
-    cur = nxt;
+    Grad<T, D, kDq>::step(dq, nullptr, s, s2, q, g, cur, nxt, nullptr, lse, -dd, c, lane);
   };
-  for (int t = 0; t < ntile; t += 2) {   // by two: the scores change places
-    step(t, s, s2);
-    if (t + 1 < ntile) step(t + 1, s2, s);
+  int t = 0;
+  for (; t + 6 < ntile; t += 4) {   // the scores change places, the buffers go round
+    step(Yes{}, t, sT0, sT1, sT3, s, s2);
+    step(Yes{}, t + 1, sT1, sT2, sT0, s2, s);
+    step(Yes{}, t + 2, sT2, sT3, sT1, s, s2);
+    step(Yes{}, t + 3, sT3, sT0, sT2, s2, s);
+  }
+  for (; t < ntile; t += 4) {
+    step(No{}, t, sT0, sT1, sT3, s, s2);
+    if (t + 1 < ntile) step(No{}, t + 1, sT1, sT2, sT0, s2, s);
+    if (t + 2 < ntile) step(No{}, t + 2, sT2, sT3, sT1, s, s2);
+    if (t + 3 < ntile) step(No{}, t + 3, sT3, sT0, sT2, s2, s);
   }
   if (i >= Lq) return;
   T* o = static_cast<T*>(a.dq) + (row * a.Hq + h) * D + 4 * half;
@@ -264,21 +278,19 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
 }
 
 // ---------------------------------------------------------------------------
-// dv and dk: 32 keys a wave, tiles of 32 queries of the group's heads in LDS.
-// They are two kernels: one for both needs a fifth fewer products, but keys,
-// values, both sums and a tile's scores are more than 256 registers, which
-// leaves one wave a SIMD and copies between the halves of its register file
-// (8192 packed rows, 16 heads of 128 on 2: 600 us, against 162 + 204 us).  At
-// head dimension 64 both fit (16384 packed rows, 32 heads on 8, all gradients:
-// 0.97 ms, in two kernels 1.45 ms).
-
-template <typename T, int D, int WAVES, int KIND>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn_dkv(AttnArgs a) {
+// dk and dv: 32 keys a wave, tiles of 32 queries of the group's heads in LDS.
+// At head dimension 128 keys, values, both sums and a tile's scores are more
+// than 256 registers, which leaves one wave a SIMD; two kernels of two waves
+// each need a quarter more products (one row of 8192, 16 heads of 128 on 2, all
+// gradients: 1.06 ms, one kernel 0.95; in fp32 a quarter more as well).  8192
+// packed rows: 285 us, 0.73 PFLOP/s.
+template <typename T, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, D == 128 ? 1 : 2) void k_attn_dkv(AttnArgs a) {
   using L = Tile<T, D>;
   constexpr int BK = 32 * WAVES, BQ = 32;
-  // tiles t, t + 1 (its s), t + 2 (arriving)
-  __shared__ __align__(16) char sQG[3][L::BYTES];
-  __shared__ __align__(16) float sS[3][2 * BQ];
+  // tiles t, t + 1 (its s), t + 2 and t + 3 (arriving), as in k_attn_dq
+  __shared__ __align__(16) char sT0[L::BYTES], sT1[L::BYTES], sT2[L::BYTES], sT3[L::BYTES];
+  __shared__ __align__(16) float sS0[2 * BQ], sS1[2 * BQ], sS2[2 * BQ], sS3[2 * BQ];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int per = a.Hk * a.gsplit;
   const int part = blockIdx.x % a.gsplit, hk = blockIdx.x % per / a.gsplit;
@@ -300,7 +312,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       frag_load(k[kk], p + 16 * kk);
-      if (KIND != kDv) frag_load(v[kk], r + 16 * kk);
+      frag_load(v[kk], r + 16 * kk);
     }
   }
   f16v sum[D / 32], sum2[D / 32];
@@ -315,14 +327,15 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   const T* qp = static_cast<const T*>(a.q) + static_cast<int64_t>(q0) * a.ldq;
   const T* gp = static_cast<const T*>(a.dout) + static_cast<int64_t>(q0) * a.lddo;
   const auto pr = L::pair(qp, a.ldq, gp, a.lddo, wave, lane);
-  auto fetch = [&](int buf) __attribute__((always_inline)) {
-    L::template load2<WAVES>(sQG[buf], pr, qp, a.ldq, gp, a.lddo, fh * D, fi * BQ, Lq - 1, wave, lane);
-    if (wave == 0) {   // lse of 32 rows, then -D of them; past the last row infinity and 0
-      const int i = fi * BQ + (lane & 31);
-      const float* src = a.stat + (i < Lq ? (static_cast<int64_t>(half) * a.Hq + fh) * a.Tq + q0 + i
-                                          : 2 * static_cast<int64_t>(a.Hq) * a.Tq + half);
-      __builtin_amdgcn_global_load_lds((const M3_GLB void*)src, (M3_LDS void*)sS[buf], 4, 0, 0);
-    }
+  constexpr int kLoads = L::NG / WAVES + 1;   // of a wave for one tile
+  auto fetch = [&](char* to, float* st) __attribute__((always_inline)) {
+    L::template load2<WAVES>(to, pr, qp, a.ldq, gp, a.lddo, fh * D, fi * BQ, Lq - 1, wave, lane);
+    // lse of 32 rows, then -D of them; past the last row infinity and 0.  (Every
+    // wave loads the same, so that all count the same number of loads.)
+    const int i = fi * BQ + (lane & 31);
+    const float* src = a.stat + (i < Lq ? (static_cast<int64_t>(half) * a.Hq + fh) * a.Tq + q0 + i
+                                        : 2 * static_cast<int64_t>(a.Hq) * a.Tq + half);
+    __builtin_amdgcn_global_load_lds((const M3_GLB void*)src, (M3_LDS void*)st, 4, 0, 0);
     if (++fi == first + nt) {
       fi = first;
       ++fh;
@@ -330,30 +343,50 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   };
   f16v s, s2;
   if (all > 0) {
-    fetch(0);
+    fetch(sT0, sS0);
     lds_loads_done();
     __syncthreads();
-    if (all > 1) fetch(1);
+    if (all > 1) fetch(sT1, sS1);
+    if (all > 2) fetch(sT2, sS2);
     s = f16v{};
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) s = mma(L::frag(sQG[0], 0, kk, lane), k[kk], s);
+    for (int kk = 0; kk < D / 16; ++kk) s = mma(L::frag(sT0, 0, kk, lane), k[kk], s);
   }
-  int ci = first, cur = 0;   // the tile at hand and its buffer
-  auto step = [&](int n, f16v& s, f16v& s2) __attribute__((always_inline)) {
-    lds_loads_done();
-    __syncthreads();   // tile n + 1 is there; every wave is done with n - 1
-    const int nxt = cur == 2 ? 0 : cur + 1, aft = nxt == 2 ? 0 : nxt + 1;
-    if (n + 2 < all) fetch(aft);
+  int ci = first;   // the tile at hand
+  auto step = [&](auto in, int n, char* cur, char* nxt, char* aft, float* st, float* sa, f16v& s,
+                  f16v& s2) __attribute__((always_inline)) {
+    if (in.value || n + 2 < all) lds_loads_but<kLoads>(); else lds_loads_done();
+    tiles_barrier();   // tile n + 1 is there; every wave is done with n - 1
+    if (in.value || n + 3 < all) fetch(aft, sa);
     const int i0 = ci * BQ;
+    if constexpr (D == 128 && sizeof(T) == 2) {
+      // k and v in the other half of the registers, from where products take
+      // them as well, so that the sums and scores do not have to be moved there
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        i4 kx = __builtin_bit_cast(i4, k[kk]), vx = __builtin_bit_cast(i4, v[kk]);
+        asm volatile("" : "+a"(kx), "+a"(vx));
+        k[kk] = __builtin_bit_cast(Frag<T>, kx);
+        v[kk] = __builtin_bit_cast(Frag<T>, vx);
+      }
+    }
     // rows i >= j - off count
     if (i0 < jw + 31 - off) hide_before(s, j - off - i0, lane);
-    grad_step<T, D, KIND>(sum, sum2, s, s2, k, v, sQG[cur], sQG[nxt], sS[cur], 0.0f, f16v{}, c, lane);
-    cur = nxt;
+    Grad<T, D, kDkv>::step(sum, sum2, s, s2, k, v, cur, nxt, st, 0.0f, 0.0f, c, lane);
     if (++ci == first + nt) ci = first;
   };
-  for (int n = 0; n < all; n += 2) {   // by two: the scores change places
-    step(n, s, s2);
-    if (n + 1 < all) step(n + 1, s2, s);
+  int n = 0;
+  for (; n + 6 < all; n += 4) {
+    step(Yes{}, n, sT0, sT1, sT3, sS0, sS3, s, s2);
+    step(Yes{}, n + 1, sT1, sT2, sT0, sS1, sS0, s2, s);
+    step(Yes{}, n + 2, sT2, sT3, sT1, sS2, sS1, s, s2);
+    step(Yes{}, n + 3, sT3, sT0, sT2, sS3, sS2, s2, s);
+  }
+  for (; n < all; n += 4) {
+    step(No{}, n, sT0, sT1, sT3, sS0, sS3, s, s2);
+    if (n + 1 < all) step(No{}, n + 1, sT1, sT2, sT0, sS1, sS0, s2, s);
+    if (n + 2 < all) step(No{}, n + 2, sT2, sT3, sT1, sS2, sS1, s, s2);
+    if (n + 3 < all) step(No{}, n + 3, sT3, sT0, sT2, sS3, sS2, s2, s);
   }
   if (j >= Lk) return;
   const int64_t at = (row * a.Hk + hk) * D + 4 * half;
@@ -371,8 +404,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
           put4(parts + to + 32 * d + 8 * e, x0, x1, x2, x3);
       }
   };
-  if (KIND != kDv) store(sum, a.dk, a.pk, a.scale);
-  if (KIND != kDk) store(KIND == kDv ? sum : sum2, a.dv, a.pv, 1.0f);
+  store(sum, a.dk, a.pk, a.scale);
+  store(sum2, a.dv, a.pv, 1.0f);
 }
 
 // adds the parts of a group in order, for the rows that belong to a sequence
@@ -391,15 +424,17 @@ __global__ __launch_bounds__(256) void k_attn_sum(AttnArgs a) {
   put4(static_cast<T*>(a.dv) + n, v.x, v.y, v.z, v.w);
 }
 
-// Parts of a group of heads: at least 1024 workgroups of 128 keys where the
-// group has the heads for it, in equal parts: their work is uneven, and a third
-// and fourth of them a CU even it out (8192 packed rows, 16 heads of 128 on 2:
-// aiming at 512, dv 245 and dk 330 us; at 1024, 168 and 226).
-int group_parts(int Tk, int S, int Hq, int Hk) {
+// Parts of a group of heads: workgroups of 128 keys for twice the chip where the
+// group has the heads for it, in equal parts.  Resident are one a CU (D = 128)
+// or two; with half as many the uneven ends of a batch show, with twice as many
+// the sums of the parts (all gradients of 4 sequences of 2048, 16 heads of 128
+// on 2: from 256 workgroups on 381 us, 512 305, 1024 335; of 3 uneven ones of
+// 8192 rows together, 16 heads of 64 on 2: 512 278, 1024 244).
+int group_parts(int Tk, int Hq, int Hk, int D) {
   const int g = Hq / Hk;
   const int64_t blocks = (static_cast<int64_t>(Tk) / 128 + 1) * Hk;
   for (int n = 1; n < g; ++n)
-    if (g % n == 0 && blocks * n >= 1024) return n;
+    if (g % n == 0 && blocks * n >= (D == 128 ? 512 : 1024)) return n;
   return g;
 }
 
@@ -412,13 +447,7 @@ hipError_t run(const AttnArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // after dq, which leaves them lse and D
-  if constexpr (D == 64) {
-    k_attn_dkv<T, D, W, kDkv><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
-  } else {
-    k_attn_dkv<T, D, W, kDv><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    k_attn_dkv<T, D, W, kDk><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
-  }
+  k_attn_dkv<T, D, W><<<static_cast<unsigned>(nk), 64 * W, 0, s>>>(a);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   if (a.gsplit > 1) {
     const int64_t n = static_cast<int64_t>(a.Tk) * a.Hk * D / 4;
@@ -433,14 +462,14 @@ constexpr size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 size_t attn_backward_workspace_bytes(int Tq, int Tk, int S, int Hq, int Hk, int D) {
-  const int g = group_parts(Tk, S, Hq, Hk);
+  const int g = group_parts(Tk, Hq, Hk, D);
   size_t n = up256(2 * sizeof(float) * (Tq * static_cast<size_t>(Hq) + 1));
   if (g > 1) n += 2 * up256(sizeof(float) * g * static_cast<size_t>(Tk) * Hk * D);
   return n;
 }
 
 hipError_t launch_attn_backward(AttnArgs& a, int bf16, void* ws, hipStream_t s) {
-  a.gsplit = group_parts(a.Tk, a.S, a.Hq, a.Hk);
+  a.gsplit = group_parts(a.Tk, a.Hq, a.Hk, a.D);
   char* c = static_cast<char*>(ws);
   a.stat = reinterpret_cast<float*>(c);
   c += up256(2 * sizeof(float) * (a.Tq * static_cast<size_t>(a.Hq) + 1));

@@ -190,8 +190,9 @@ struct Tile {
       load2<NW>(lds, a + by, lda, b + by, ldb, row0, last, w, opaque(lane));
       return;
     }
+    // (opaque: one address now, not one for each load kept over the loop)
     const char* src = p.at + by * static_cast<int64_t>(sizeof(T)) +
-                      static_cast<uint64_t>(static_cast<uint32_t>(row0)) * p.ld;
+                      static_cast<uint64_t>(static_cast<uint32_t>(opaque(row0))) * p.ld;
 #pragma unroll
     for (int n = 0; n < NG / NW; ++n)
       __builtin_amdgcn_global_load_lds(
@@ -202,12 +203,12 @@ struct Tile {
   // fragment kk (elements 16 kk ..) of rows row0 + lane % 32 (row0 0 or 32)
   static __device__ __forceinline__ Frag<T> frag(const char* lds, int row0, int kk, int lane) {
     const int r = lane & 31, h = lane >> 5;
-    const char* a;
+    int at = static_cast<int>(sizeof(T)) * (8 * h + 16 * kk);
     if constexpr (RB == 128)
-      a = lds + ((r >> 2) & 3) * G4 + ((r >> 1) & 1) * G1 + ((r & 1) + 2 * (r >> 4)) * RB + 4 * RB * (row0 / 32);
+      at += ((r >> 2) & 3) * G4 + ((r >> 1) & 1) * G1 + ((r & 1) + 2 * (r >> 4)) * RB + 4 * RB * (row0 / 32);
     else
-      a = lds + ((r >> 2) & 3) * G4 + (r & 3) * G1 + (r >> 4) * RB + (RB == 256 ? 2 * RB : HALF) * (row0 / 32);
-    a += 8 * sizeof(T) * h + 16 * sizeof(T) * kk;
+      at += ((r >> 2) & 3) * G4 + (r & 3) * G1 + (r >> 4) * RB + (RB == 256 ? 2 * RB : HALF) * (row0 / 32);
+    const char* a = lds + at;
     Frag<T> f;
     if constexpr (sizeof(T) == 2) {
       f.v = *reinterpret_cast<const bh8*>(a);
@@ -227,13 +228,15 @@ struct Tile {
       // a transposing read: sixteen lanes point at four rows of sixteen
       // elements, each lane at four; lane i receives column i of the four
       const int i = lane & 15, c = i >> 2;
-      const char* a = lds + h * G4 + (RB == 128 ? (c >> 1) * G1 + (c & 1) * RB : c * G1) +
-                      32 * ((lane >> 4) & 1) + 8 * (i & 3) + far + 2 * d0;
+      const int at = h * G4 + (RB == 128 ? (c >> 1) * G1 + (c & 1) * RB : c * G1) +
+                     32 * ((lane >> 4) & 1) + 8 * (i & 3) + far + 2 * d0;
+      const char* a = lds + at;
       const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((M3_LDS s4v*)a);
       const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((M3_LDS s4v*)(a + 2 * G4));
       f.v = __builtin_bit_cast(bh8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      const char* a = lds + h * G4 + far + 4 * (d0 + (lane & 31));
+      const int at = h * G4 + far + 4 * (d0 + (lane & 31));
+      const char* a = lds + at;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         f.a[j] = *reinterpret_cast<const float*>(a + j * G1);
@@ -247,6 +250,23 @@ struct Tile {
 // the loads to LDS that this wave has issued are there
 __device__ __forceinline__ void lds_loads_done() {
   __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
+}
+// ... but for the last N of them
+template <int N>
+__device__ __forceinline__ void lds_loads_but() {
+  static_assert(N < 16, "the low bits of the count");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | N);
+}
+
+// A barrier behind which the tiles are read that every wave has waited for by
+// lds_loads_but, while later ones are still on their way (__syncthreads would
+// wait for those, too): this wave's reads of LDS are done, and nothing moves
+// over it.
+__device__ __forceinline__ void tiles_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 // Sequence and tile of a slot.  A sequence's tiles of B rows take the slots

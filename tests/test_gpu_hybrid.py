@@ -130,3 +130,40 @@ def test_gradients_through_the_layers():
     _near("y", y.cpu(), yd.detach(), 1e-5)
     for name, u, w in zip(("q", "k", "v", "wq", "wk", "r", "i", "decay"), got, want):
         _near("d" + name, u.cpu(), w, 1e-5)
+
+
+def test_layers_on_two_streams_at_once():
+    """Calls of two streams share the chip, tiles of two scans in flight
+    together among them; each has the bits that it has alone."""
+    def work(seed):
+        g = torch.Generator().manual_seed(seed)
+        n = lambda *s: torch.randn(*s, generator=g).to(BF16).cuda()
+        T, Hq, Hk, D = 2600, 8, 2, 64
+        cu = torch.tensor([0, 700, 703, 2600], dtype=torch.int32).cuda()
+        q, k, v, do = n(T, Hq, D), n(T, Hk, D), n(T, Hk, D), n(T, Hq, D)
+        x, r, i, dy = (n(T, Hq * D) for _ in range(4))
+        decay, pos = torch.linspace(-6, -2, Hq * D).cuda(), torch.arange(T, dtype=torch.int32).cuda()
+        cache, lens = n(3, 1500, Hk, D), torch.tensor([1500, 0, 77], dtype=torch.int32).cuda()
+
+        def run():
+            y, hT, st = m3.gated_scan(x, r, i, decay, cu_seqlens=cu, want_states=True)
+            d = m3.gated_scan_backward(x, r, i, decay, dy, st, cu_seqlens=cu)
+            qr, kr = m3.qk_norm_rope(q, k, pos)
+            o, lse = m3.attn_prefill_varlen(qr, kr, v, cu, cu)
+            return [y, hT, d["x"], d["decay"], o, lse,
+                    *m3.attn_prefill_varlen_backward(qr, kr, v, o, lse, do, cu, cu),
+                    *m3.attn_decode(q[:3], cache, cache, lens)]
+        return run
+
+    runs = [work(41), work(42)]
+    want = [[t.clone() for t in f()] for f in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for n in range(4):
+        got = []
+        for s, f in zip(streams, runs):
+            with torch.cuda.stream(s):
+                got.append(f())
+        torch.cuda.synchronize()
+        for w, o in zip(want, got):
+            assert all(torch.equal(a, b) for a, b in zip(w, o)), n

@@ -352,9 +352,12 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
   using L = Tile<T, D>;
+  // A wave's tile (32 rows of K, 32 of V); afterwards its o [32][D] in fp32.  One
+  // buffer, as the other waves' loads fill the time (32 caches of 4096, 8 heads,
+  // in fp32: 244 us at D = 128, 110 at 64; with two buffers half as many waves
+  // fit, 402 and 145 us; in bf16 the same within 3%).
   constexpr int BN = 32;
-  // a wave's two tiles (32 rows of K, 32 of V); afterwards its o [32][D] in fp32
-  __shared__ __align__(16) char sKV[WAVES][2][L::BYTES];
+  __shared__ __align__(16) char sKV[WAVES][L::BYTES];
   __shared__ float sM[WAVES][32], sL[WAVES][32];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, g = a.Hq / a.Hk, ng = (g + 31) / 32;
@@ -382,21 +385,22 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
   const float c = a.scale * kLog2eA;
   const T* kp = static_cast<const T*>(a.k) + s * a.bk + hk * D;
   const T* vp = static_cast<const T*>(a.v) + s * a.bv + hk * D;
+  auto fetch = [&](int t) __attribute__((always_inline)) {
+    L::template load2<1>(sKV[wave], kp, a.ldk, vp, a.ldv, t * BN, len - 1, 0, lane);
+  };
   int t = t0 + wave;
-  if (t < t1) {
-    L::template load2<1>(sKV[wave][0], kp, a.ldk, vp, a.ldv, t * BN, len - 1, 0, lane);
-  }
-  for (int u = 0; t < t1; t += WAVES, ++u) {
+  if (t < t1) fetch(t);
+  for (; t < t1; t += WAVES) {
     lds_loads_done();
-    if (t + WAVES < t1) {
-      L::template load2<1>(sKV[wave][(u + 1) & 1], kp, a.ldk, vp, a.ldv, (t + WAVES) * BN, len - 1, 0, lane);
-    }
-    const char* KV = sKV[wave][u & 1];
     // rows past the end repeat the last one, which every query sees
     if ((t + 1) * BN <= len)
-      attend<T, D, false>(st, q, KV, c, BN, lane);
+      attend<T, D, false>(st, q, sKV[wave], c, BN, lane);
     else
-      attend<T, D, true>(st, q, KV, c, len - t * BN, lane);
+      attend<T, D, true>(st, q, sKV[wave], c, len - t * BN, lane);
+    if (t + WAVES < t1) {
+      lds_reads_done();
+      fetch(t + WAVES);
+    }
   }
   const float l = half_sum(st.l);
   if (half == 0) {
@@ -404,8 +408,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
     sL[wave][lane] = l;
   }
   // o of this wave, over its own tiles (of which it is done reading)
-  static_assert(2 * L::BYTES >= static_cast<int>(sizeof(float)) * 32 * D, "room for o");
-  float* so = reinterpret_cast<float*>(&sKV[wave][0][0]);
+  static_assert(L::BYTES >= static_cast<int>(sizeof(float)) * 32 * D, "room for o");
+  float* so = reinterpret_cast<float*>(sKV[wave]);
 #pragma unroll
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll
@@ -426,7 +430,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
       // a wave that saw no key has l = 0 and o = 0
       if (lw != 0.0f) {
         ls = fmaf(f, lw, ls);
-        const f4 ow = *reinterpret_cast<const f4*>(reinterpret_cast<const float*>(&sKV[w][0][0]) + r * D + d);
+        const f4 ow = *reinterpret_cast<const f4*>(reinterpret_cast<const float*>(sKV[w]) + r * D + d);
         v.x = fmaf(f, ow.x, v.x);
         v.y = fmaf(f, ow.y, v.y);
         v.z = fmaf(f, ow.z, v.z);
@@ -543,7 +547,7 @@ hipError_t launch_attn_decode(AttnArgs& a, int bf16, void* ws, hipStream_t s) {
   a.po = static_cast<float*>(ws);
   a.pm = a.po + static_cast<size_t>(a.D) * a.S * a.Hq * a.nsplit;
   if (bf16) return a.D == 64 ? run_decode<bf16_t, 64, 4>(a, s) : run_decode<bf16_t, 128, 4>(a, s);
-  return a.D == 64 ? run_decode<float, 64, 4>(a, s) : run_decode<float, 128, 2>(a, s);
+  return a.D == 64 ? run_decode<float, 64, 4>(a, s) : run_decode<float, 128, 4>(a, s);
 }
 
 }  // namespace m3

@@ -268,6 +268,12 @@ __device__ __forceinline__ void tiles_barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
+// this wave's reads of LDS are done
+__device__ __forceinline__ void lds_reads_done() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);
+  asm volatile("" ::: "memory");
+}
 
 // Sequence and tile of a slot.  A sequence's tiles of B rows take the slots
 // from cu[s] / B + s on: the next sequence's first slot is never before the

@@ -27,12 +27,22 @@ struct GatedArgs {
   // workspace
   unsigned* ticket;
   int32_t* cuc;               // clean offsets
+  struct GatedWindow* win;    // what every 32 rows of a packed call hold
   unsigned long long* slots;  // carries [ntile, nchain, channels of a chain]
   float* part;                // parts of ddecay [chunks, D]
   int64_t ldx, ldr, ldi, ldg;
   int B, T, D, S;             // B sequences (packed: of T rows together)
   int ncb, nchain, ntile;
   float c;
+};
+
+// The rows t0 .. t0 + 31 of a packed batch as bit masks: bit j of `start` /
+// `end`: row t0 + j is the first / last of its sequence; `live`: it belongs to
+// one.  s0 is at or before the sequence of the first live row, s1 at or behind
+// that of the last.
+struct alignas(32) GatedWindow {
+  uint32_t start, end, live;
+  int32_t s0, s1;
 };
 
 struct GatedPlan {

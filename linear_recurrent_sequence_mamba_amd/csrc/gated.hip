@@ -175,37 +175,8 @@ struct Carry {
   }
 };
 
-// Clears the ticket counter and the carry slots; for packed calls also writes
-// the clean offsets (clamped into [0, T] and raised to the largest one before)
-// and gives the state rows of empty sequences their value (src row or 0).
-__global__ void k_gated_init(GatedArgs a, const float* src, float* dst, int64_t nslot) {
-  const int tid = threadIdx.x;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + tid; i < nslot / 2; i += step)
-    reinterpret_cast<ulonglong2*>(a.slots)[i] = ulonglong2{kNotYet, kNotYet};   // 64 slots to a chain
-  if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;
-  if (!a.cu) return;
-  __shared__ int part[256];
-  for (int k = blockIdx.x; k <= a.S; k += gridDim.x) {
-    int v = 0;
-    for (int j = tid; j <= k; j += blockDim.x) v = max(v, min(a.cu[j], a.T));
-    part[tid] = v;
-    __syncthreads();
-    for (int o = blockDim.x / 2; o > 0; o >>= 1) {
-      if (tid < o) part[tid] = max(part[tid], part[tid + o]);
-      __syncthreads();
-    }
-    const int start = part[0];
-    __syncthreads();
-    if (tid == 0) a.cuc[k] = start;
-    if (k < a.S && dst && min(a.cu[k + 1], a.T) <= start)
-      for (int j = tid; j < a.D; j += blockDim.x)
-        dst[static_cast<int64_t>(k) * a.D + j] = src ? src[static_cast<int64_t>(k) * a.D + j] : 0.0f;
-  }
-}
-
 // The last sequence that starts at or before row t (-1: none), by a search
-// over the clean offsets that every lane of the wave does alike.
+// over the clean offsets.
 __device__ __forceinline__ int seq_of(const int32_t* cu, int S, int t) {
   int lo = 0, hi = S + 1;   // first index with cu > t
   while (lo < hi) {
@@ -215,37 +186,93 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int S, int t) {
   return lo - 1;
 }
 
-// The rows t0 .. t0 + n of a packed batch as bit masks, with the sequences of
-// the window in order: bit j of `start` / `end`: row t0 + j is the first /
-// last of its sequence; `live`: it belongs to one.
-struct Window {
-  uint32_t start, end, live;
-  int s0;   // the sequence of the first live row (or the first that starts)
-};
-__device__ __forceinline__ Window window_of(const int32_t* cu, int S, int t0, int n) {
-  Window w{0u, 0u, 0u, 0};
-  int s = seq_of(cu, S, t0);
-  if (s < 0) s = 0;
-  w.s0 = s;
-  while (s < S) {
-    const int b = cu[s] - t0, e = cu[s + 1] - t0;
-    if (b >= n) break;
-    if (e > b && e > 0) {
-      if (b >= 0) w.start |= 1u << b;
-      if (e <= n) w.end |= 1u << (e - 1);
-      const uint32_t upto = e >= 32 ? 0xffffffffu : (1u << e) - 1u;
-      w.live |= upto & ~(b > 0 ? (1u << b) - 1u : 0u);
-    }
-    ++s;
+// Offsets clamped into [0, T] and raised to the largest one before, by one
+// workgroup: a thread takes `per` of them, and the threads' maxima are joined.
+template <int THREADS>
+__device__ __forceinline__ void clean_offsets(const int32_t* cu, int S, int T, int32_t* c) {
+  __shared__ int top[THREADS];
+  const int tid = threadIdx.x, per = S / THREADS + 1, k0 = tid * per, k1 = min(k0 + per, S + 1);
+  int v = 0;
+  for (int k = k0; k < k1; ++k) {
+    v = max(v, min(cu[k], T));
+    c[k] = v;
   }
-  const uint32_t all = n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-  w.live &= all;
-  return w;
+  top[tid] = v;
+  __syncthreads();
+  for (int o = 1; o < THREADS; o <<= 1) {
+    const int w = tid >= o ? top[tid - o] : 0;
+    __syncthreads();
+    top[tid] = max(top[tid], w);
+    __syncthreads();
+  }
+  const int before = tid > 0 ? top[tid - 1] : 0;
+  for (int k = k0; k < k1; ++k) c[k] = max(c[k], before);
+  __syncthreads();
 }
-// the sequence before s that has rows
-__device__ __forceinline__ int prev_seq(const int32_t* cu, int s) {
-  do --s; while (s > 0 && cu[s + 1] <= cu[s]);
-  return s;
+
+// Clears the ticket counter and the carry slots; for packed calls also writes
+// the clean offsets and the windows, and gives the state rows of empty sequences
+// their value (src row or 0).  Up to kInitSeqs offsets are cleaned by every
+// workgroup for itself, more by k_gated_clean before.
+constexpr int kInitSeqs = 8192;
+__global__ __launch_bounds__(256) void k_gated_init(GatedArgs a, const float* src, float* dst,
+                                                    int64_t nslot) {
+  const int tid = threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * blockDim.x + tid;
+  for (int64_t i = at; i < nslot / 2; i += step)
+    reinterpret_cast<ulonglong2*>(a.slots)[i] = ulonglong2{kNotYet, kNotYet};   // 64 slots to a chain
+  if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;
+  if (!a.cu) return;
+  __shared__ int32_t own[kInitSeqs + 1];
+  const int32_t* c = a.cuc;
+  if (a.S <= kInitSeqs) {
+    clean_offsets<256>(a.cu, a.S, a.T, own);
+    if (blockIdx.x == 0)
+      for (int k = tid; k <= a.S; k += 256) a.cuc[k] = own[k];
+    c = own;
+  }
+  for (int64_t n = at; n * 32 < a.T; n += step) {
+    const int t0 = static_cast<int>(n * 32);
+    GatedWindow w{0u, 0u, 0u, 0, 0};
+    w.s0 = max(0, seq_of(c, a.S, t0));
+    w.s1 = min(max(0, seq_of(c, a.S, min(t0 + 32, a.T) - 1)), a.S - 1);
+    for (int s = w.s0; s < a.S; ++s) {
+      const int b = c[s] - t0, e = c[s + 1] - t0;
+      if (b >= 32) break;
+      if (e > b && e > 0) {
+        if (b >= 0) w.start |= 1u << b;
+        if (e <= 32) w.end |= 1u << (e - 1);
+        const uint32_t upto = e >= 32 ? 0xffffffffu : (1u << e) - 1u;
+        w.live |= upto & ~(b > 0 ? (1u << b) - 1u : 0u);
+      }
+    }
+    a.win[n] = w;
+  }
+  if (dst)
+    for (int k = blockIdx.x; k < a.S; k += gridDim.x)
+      if (c[k + 1] <= c[k])
+        for (int j = tid; j < a.D; j += blockDim.x)
+          dst[static_cast<int64_t>(k) * a.D + j] = src ? src[static_cast<int64_t>(k) * a.D + j] : 0.0f;
+}
+__global__ __launch_bounds__(1024) void k_gated_clean(GatedArgs a) {
+  clean_offsets<1024>(a.cu, a.S, a.T, a.cuc);
+}
+
+// A wave's TOK rows of a window: one 32-byte load where a search over the offsets
+// would be a chain of them (16384 x 2048 in 64 sequences: fp32 124 us, with the
+// search 145, bf16 86 and 98).
+template <int TOK>
+__device__ __forceinline__ GatedWindow window_of(const GatedArgs& g, int t0) {
+  GatedWindow w{0u, 0u, 0u, 0, 0};
+  if (t0 >= g.T) return w;
+  w = g.win[t0 / 32];
+  const uint32_t some = TOK == 32 ? 0xffffffffu : (1u << (TOK & 31)) - 1u;
+  const int sh = TOK == 32 ? 0 : t0 % 32;
+  w.start = w.start >> sh & some;
+  w.end = w.end >> sh & some;
+  w.live = w.live >> sh & some;
+  return w;
 }
 
 __device__ __forceinline__ unsigned take_ticket(const GatedArgs& a) {
@@ -270,7 +297,7 @@ __device__ __forceinline__ unsigned take_ticket(const GatedArgs& a) {
 template <typename T, int TOK, int WAVES, bool PACKED>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
   constexpr int TILE = TOK * WAVES;
-  static_assert(TOK <= 32 && kGatedChunk % TOK == 0, "rows of a window in 32 bits");
+  static_assert(TOK <= 32 && 32 % TOK == 0 && kGatedChunk % TOK == 0, "rows in one window");
   static_assert(WAVES >= kGroup, "a wave for each slot before a tile");
   __shared__ float sH[WAVES][64], sP[WAVES][64], sC[64], sF[64];
   __shared__ u64 sM[kGroup][64];
@@ -299,8 +326,8 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
   if (!PACKED && wave == 0)
     sF[lane] = cr.n0 == 0 && g.h0 ? g.h0[static_cast<int64_t>(b) * g.D + chc] : 0.0f;
   if (wave == 0) sC[lane] = decay_factor(dec, g.c);
-  Window w{};
-  if constexpr (PACKED) w = window_of(g.cuc, g.S, t0, TOK);
+  GatedWindow w{};
+  if constexpr (PACKED) w = window_of<TOK>(g, t0);
   __syncthreads();
   const float k = sC[lane];
 
@@ -379,7 +406,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_scan(GatedArgs g) {
 template <typename T, int TOK, int WAVES, bool PACKED>
 __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_backward(GatedArgs g) {
   constexpr int TILE = TOK * WAVES;
-  static_assert(TILE == kGatedChunk && TOK <= 32, "one saved state per tile; rows of a window in 32 bits");
+  static_assert(TILE == kGatedChunk && 32 % TOK == 0, "one saved state per tile; rows in one window");
   static_assert(WAVES >= kGroup, "a wave for each slot before a tile");
   __shared__ float sH[WAVES][64], sP[WAVES][64], sC[64];
   __shared__ u64 sM[kGroup][64];
@@ -403,8 +430,8 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_backward(GatedArgs g) {
   load_rows<T, TOK>(ri, static_cast<const T*>(g.i) + row0 * g.ldi, g.ldi, chc, t0, g.T);
   load_rows<T, TOK>(rd, static_cast<const T*>(g.dy) + row0 * g.D, g.D, chc, t0, g.T);
   if (wave == 0) sC[lane] = decay_factor(dec, g.c);
-  Window w{};
-  if constexpr (PACKED) w = window_of(g.cuc, g.S, t0, TOK);
+  GatedWindow w{};
+  if constexpr (PACKED) w = window_of<TOK>(g, t0);
   __syncthreads();
   const float k = sC[lane];
 
@@ -467,12 +494,9 @@ __global__ __launch_bounds__(64 * WAVES, 4) void k_gated_backward(GatedArgs g) {
   // backward: q from zero and the product of a
   float q = 0.0f;
   P = 1.0f;
-  int se = 0;   // the sequence of the last row
-  if constexpr (PACKED) {
-    se = seq_of(g.cuc, g.S, min(t0 + TOK, g.T) - 1);
-    if (se < 0) se = 0;
-    if (se >= g.S) se = prev_seq(g.cuc, g.S);
-  }
+  int se = w.s1;   // the sequence of the wave's last row
+  if constexpr (PACKED)
+    while (se > 0 && g.cuc[se] >= min(t0 + TOK, g.T)) --se;
   int sb = se;
 #pragma unroll
   for (int j = TOK - 1; j >= 0; --j) {
@@ -642,7 +666,12 @@ hipError_t run_backward(GatedArgs& g, hipStream_t s) {
 hipError_t run_init(const GatedArgs& g, const float* src, float* dst, int64_t nslot, hipStream_t s) {
   if (g.ntile == 1 && !g.cu) return hipSuccess;
   int64_t blocks = (nslot + 1023) / 1024;
-  if (g.cu && blocks < g.S + 1) blocks = g.S + 1;
+  if (g.cu) {
+    const int64_t windows = (static_cast<int64_t>(g.T) + 8191) / 8192, rows = g.S < 256 ? g.S : 256;
+    if (blocks < windows) blocks = windows;
+    if (blocks < rows) blocks = rows;
+    if (g.S > kInitSeqs) k_gated_clean<<<1, 1024, 0, s>>>(g);
+  }
   if (blocks > 4096) blocks = 4096;
   if (blocks < 1) blocks = 1;
   k_gated_init<<<static_cast<unsigned>(blocks), 256, 0, s>>>(g, src, dst, nslot);
@@ -676,6 +705,7 @@ static int64_t gated_slots(const GatedPlan& p) {
 size_t gated_workspace_bytes(int B, int T, int D, bool packed, bool backward) {
   const GatedPlan p = gated_plan(B, T, D, packed, backward);
   size_t n = 256 + up256(sizeof(int32_t) * (static_cast<size_t>(B) + 1));
+  if (packed) n += up256(sizeof(GatedWindow) * ((static_cast<size_t>(T) + 31) / 32));
   n += up256(sizeof(u64) * gated_slots(p));
   if (backward) n += up256(sizeof(float) * D * (packed ? 1 : B) * p.ntile);
   return n;
@@ -691,6 +721,8 @@ void gated_carve(GatedArgs& g, bool backward, void* ws) {
   c += 256;
   g.cuc = reinterpret_cast<int32_t*>(c);
   c += up256(sizeof(int32_t) * (static_cast<size_t>(g.B) + 1));
+  g.win = reinterpret_cast<GatedWindow*>(c);
+  if (g.cu) c += up256(sizeof(GatedWindow) * ((static_cast<size_t>(g.T) + 31) / 32));
   g.slots = reinterpret_cast<u64*>(c);
   c += up256(sizeof(u64) * gated_slots(p));
   g.part = reinterpret_cast<float*>(c);

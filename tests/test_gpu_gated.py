@@ -160,6 +160,35 @@ def _raw_scan(x, r, i, decay, h0, cu, y):
     return y, hT, st
 
 
+def test_packed_with_thousands_of_sequences():
+    """More offsets than one workgroup's memory holds, most windows with many."""
+    g = torch.Generator().manual_seed(31)
+    test_packed(torch.randint(0, 4, (9000,), generator=g).tolist(), BF16)
+
+
+@pytest.mark.parametrize("S", [3, 700, 8192, 8193, 20000])
+def test_any_offsets_are_cleaned(S):
+    """Offsets in any order give the bits of the cleaned ones, gradients too."""
+    T, D = 3000, 33
+    x, r, i, decay, h0 = _inputs((T,), D, F32, 9, S)
+    g = torch.Generator().manual_seed(S)
+    rise = torch.sort(torch.randint(0, T, (S + 1,), generator=g))[0]
+    bad = rise + torch.randint(-300, 30, (S + 1,), generator=g) * (torch.rand(S + 1, generator=g) < 0.2)
+    good = bad.clamp(0, T).cummax(0)[0]
+    bad, good = bad.to(torch.int32).cuda(), good.to(torch.int32).cuda()
+    dhT = torch.randn(S, D, generator=g).cuda()
+    body = slice(int(good[0]), int(good[-1]))
+    res = []
+    for cu in (bad, good):
+        y, hT, st = m3.gated_scan(x, r, i, decay, h0=h0, cu_seqlens=cu, want_states=True)
+        d = m3.gated_scan_backward(x, r, i, decay, x, st, h0=h0, dhT=dhT, cu_seqlens=cu)
+        res.append([y[body], hT, d["x"][body], d["r"][body], d["i"][body], d["decay"], d["h0"]])
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(*res))
+    empty = (good[1:] == good[:-1])
+    assert torch.equal(res[0][1][empty], h0[empty]) and torch.equal(res[0][6][empty], dhT[empty])
+
+
 def test_offsets_that_do_not_rise_are_cleaned():
     T, D = 300, 64
     x, r, i, decay, h0 = _inputs((T,), D, F32, 9, 4)

@@ -303,7 +303,7 @@ m3_status check_attn(const m3_attn_dims* d, bool decode) {
     return M3_ERR_ALIGN;
   if (!decode) {
     const int64_t tiles = (static_cast<int64_t>(d->tokens_q > d->tokens_k ? d->tokens_q
-                                                                          : d->tokens_k) >> 7) + d->nseq;
+                                                                          : d->tokens_k) >> 7) + d->nseq + 1;
     if (tiles > 0x7fffffff || !grid_fits(tiles * d->nheads_q, 256) ||
         !grid_fits((static_cast<int64_t>(d->tokens_q) * d->nheads_q + 1) / 2, 32) ||
         !grid_fits(static_cast<int64_t>(d->tokens_k) * wk / 1024 + 1, 256))

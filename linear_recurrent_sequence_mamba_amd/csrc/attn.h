@@ -27,10 +27,18 @@ struct AttnArgs {
   int Tq, Tk, S, Hq, Hk, D;
   int cap;                      // decode: rows a cache has room for
   int gsplit;                   // parts of a group of heads (backward of k, v)
+  int lp;                       // log2 of the heads of a group that a tile of queries takes
   int nsplit;                   // parts of a cache (decode)
   float scale;
 };
 
+// Heads that share k and v and lie in one tile of 128 (query, head) pairs: the
+// largest power of two that divides the group, up to 32.
+inline int attn_log_pack(int Hq, int Hk) {
+  int lp = 0;
+  while (lp < 5 && (Hq / Hk) % (2 << lp) == 0) ++lp;
+  return lp;
+}
 bool attn_supported(int D);
 size_t attn_backward_workspace_bytes(int Tq, int Tk, int S, int Hq, int Hk, int D);
 size_t attn_decode_workspace_bytes(int S, int cap, int Hq, int Hk, int D);

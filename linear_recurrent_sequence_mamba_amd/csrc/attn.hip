@@ -219,8 +219,8 @@ __device__ __forceinline__ void attend(Rows<D>& st, const Frag<T>* q, const char
 }
 
 // ---------------------------------------------------------------------------
-// The prompt: a workgroup takes 32 WAVES queries of one head; K and V tiles
-// of BN keys are double-buffered in LDS.  Two waves a SIMD (D = 64: three), so
+// The prompt: a workgroup takes 128 (query, head) columns; K and V tiles of BN
+// keys are double-buffered in LDS.  Two waves a SIMD (D = 64: three), so
 // that one's softmax runs beside another's products as well.  16384 tokens, 16
 // heads of 128: 1.03 ms, 1.06 PFLOP/s, matrix cores busy 56% and vector units
 // 49% of the cycles; packed rows of 32 heads of 64: 257 us, 0.77 PFLOP/s, 41%
@@ -228,29 +228,28 @@ __device__ __forceinline__ void attend(Rows<D>& st, const Frag<T>* q, const char
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn(AttnArgs a) {
   using L = Tile<T, D>;
-  constexpr int BM = 32 * WAVES, BN = 64, NB = 2;
+  static_assert(WAVES == 4, "128 columns");
+  constexpr int BN = 64, NB = 2;
   // (variables of their own, used by name: of one array the compiler takes every
   // read to follow the loads that are on their way, and waits for them)
   __shared__ __align__(16) char sK0[L::BYTES], sK1[L::BYTES], sV0[L::BYTES], sV1[L::BYTES];
   __shared__ int sSpecial;
   if (threadIdx.x == 0) sSpecial = 0;   // read after the tiles' barriers
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nslot = gridDim.x / a.Hq;
-  const int h = blockIdx.x % a.Hq;
+  const Columns col(a);
   // late tiles of a sequence see most keys: they start first
-  const Slot sl = query_slot<BM>(a, static_cast<int>(blockIdx.x / a.Hq), nslot, lane);
+  const Slot sl = col.slot(a, lane);
   if (sl.s < 0) return;
   const int q0 = clamp_row(a.cuq[sl.s], a.Tq), q1 = clamp_row(a.cuq[sl.s + 1], a.Tq);
   const int k0 = clamp_row(a.cuk[sl.s], a.Tk), k1 = clamp_row(a.cuk[sl.s + 1], a.Tk);
   const int Lq = q1 - q0, Lk = max(0, k1 - k0);
-  const int i0 = sl.tile * BM;
+  const int i0 = sl.tile * col.queries;
   if (i0 >= Lq) return;
-  const int off = Lk - Lq;
-  const int hk = h / (a.Hq / a.Hk);
+  const int off = Lk - Lq, hk = col.hk, h = col.head(lane);
 
   const int half = lane >> 5;
-  const int iw = i0 + 32 * wave;               // the wave's first query
-  const int i = iw + (lane & 31);              // the lane's
+  const int iw = i0 + col.first(wave);         // the wave's first query
+  const int i = iw + col.query(lane);          // the lane's
   const int64_t row = q0 + min(i, Lq - 1);
   Frag<T> q[D / 16];
   {
@@ -262,11 +261,11 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   st.init();
   const float c = a.scale * kLog2eA;
   const int sees = min(i, Lq - 1) + off + 1;   // keys that the lane's query sees
-  const int most = min(min(i0 + BM, Lq) + off, Lk);   // that any query of the block sees
+  const int most = min(min(i0 + col.queries, Lq) + off, Lk);   // that any query of the block sees
   const int ntile = most <= 0 ? 0 : (most + BN - 1) / BN;
   // from here on some query of the block does not see the whole tile
   const int tmask = max(0, min(i0, Lq - 1) + off + 1) / BN;
-  const int wmost = min(min(iw + 32, Lq) + off, Lk);
+  const int wmost = min(min(iw + col.per_wave(), Lq) + off, Lk);
   const T* kp = static_cast<const T*>(a.k) + static_cast<int64_t>(k0) * a.ldk + hk * D;
   const T* vp = static_cast<const T*>(a.v) + static_cast<int64_t>(k0) * a.ldv + hk * D;
   // K runs one tile ahead of V.  Tiles that every query of the block sees
@@ -501,9 +500,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 
 template <typename T, int D>
 hipError_t run_attn(const AttnArgs& a, hipStream_t s) {
-  constexpr int BM = 128;
-  const int64_t slots = a.Tq / BM + a.S;
-  k_attn<T, D, BM / 32><<<static_cast<unsigned>(slots * a.Hq), 2 * BM, 0, s>>>(a);
+  const int64_t slots = (a.Tq >> (7 - a.lp)) + a.S;
+  k_attn<T, D, 4><<<static_cast<unsigned>(slots * (a.Hq >> a.lp)), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -533,6 +531,7 @@ int decode_parts(int S, int cap, int Hq, int Hk) {
 bool attn_supported(int D) { return D == 64 || D == 128; }
 
 hipError_t launch_attn(AttnArgs& a, int bf16, hipStream_t s) {
+  a.lp = attn_log_pack(a.Hq, a.Hk);
   if (bf16) return a.D == 64 ? run_attn<bf16_t, 64>(a, s) : run_attn<bf16_t, 128>(a, s);
   return a.D == 64 ? run_attn<float, 64>(a, s) : run_attn<float, 128>(a, s);
 }

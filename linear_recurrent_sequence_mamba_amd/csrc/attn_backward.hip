@@ -145,28 +145,28 @@ constexpr int kExactD = 512;
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn_dq(AttnArgs a) {
   using L = Tile<T, D>;
-  constexpr int BM = 32 * WAVES, BN = 32;
+  static_assert(WAVES == 4, "128 columns");
+  constexpr int BN = 32;
   // Tiles t, t + 1 (its s), t + 2 and t + 3 (arriving).  Variables of their own,
   // used by name: of one array the compiler takes every read to follow the loads
   // that are on their way, and waits for them.
   __shared__ __align__(16) char sT0[L::BYTES], sT1[L::BYTES], sT2[L::BYTES], sT3[L::BYTES];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nslot = gridDim.x / a.Hq;
-  const int h = blockIdx.x % a.Hq;
+  const Columns col(a);
   const int64_t all = static_cast<int64_t>(a.Tq) * a.Hq;
   if (blockIdx.x == 0 && threadIdx.x == 0) {   // behind all rows' numbers
     a.stat[2 * all] = INFINITY;
     a.stat[2 * all + 1] = 0.0f;
   }
-  const Slot sl = query_slot<BM>(a, static_cast<int>(blockIdx.x / a.Hq), nslot, lane);
+  const Slot sl = col.slot(a, lane);
   if (sl.s < 0) return;
   const int q0 = clamp_row(a.cuq[sl.s], a.Tq), q1 = clamp_row(a.cuq[sl.s + 1], a.Tq);
   const int k0 = clamp_row(a.cuk[sl.s], a.Tk), k1 = clamp_row(a.cuk[sl.s + 1], a.Tk);
   const int Lq = q1 - q0, Lk = max(0, k1 - k0);
-  const int i0 = sl.tile * BM;
+  const int i0 = sl.tile * col.queries;
   if (i0 >= Lq) return;
-  const int off = Lk - Lq, hk = h / (a.Hq / a.Hk), half = lane >> 5;
-  const int iw = i0 + 32 * wave, i = iw + (lane & 31);
+  const int off = Lk - Lq, hk = col.hk, h = col.head(lane), half = lane >> 5;
+  const int iw = i0 + col.first(wave), i = iw + col.query(lane);
   const int64_t row = q0 + min(i, Lq - 1);
   Frag<T> q[D / 16], g[D / 16];
   {
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   for (int d = 0; d < D / 32; ++d) dq[d] = f16v{};
   const float c = a.scale * kLog2eA;
   const int sees = min(i, Lq - 1) + off + 1;
-  const int most = min(min(i0 + BM, Lq) + off, Lk);
+  const int most = min(min(i0 + col.queries, Lq) + off, Lk);
   const int ntile = most <= 0 ? 0 : (most + BN - 1) / BN;
   const T* kp = static_cast<const T*>(a.k) + static_cast<int64_t>(k0) * a.ldk + hk * D;
   const T* vp = static_cast<const T*>(a.v) + static_cast<int64_t>(k0) * a.ldv + hk * D;
@@ -288,6 +288,7 @@ template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, D == 128 ? 1 : 2) void k_attn_dkv(AttnArgs a) {
   using L = Tile<T, D>;
   constexpr int BK = 32 * WAVES, BQ = 32;
+  static_assert(BK == 128, "1 << 7 keys");
   // tiles t, t + 1 (its s), t + 2 and t + 3 (arriving), as in k_attn_dq
   __shared__ __align__(16) char sT0[L::BYTES], sT1[L::BYTES], sT2[L::BYTES], sT3[L::BYTES];
   __shared__ __align__(16) float sS0[2 * BQ], sS1[2 * BQ], sS2[2 * BQ], sS3[2 * BQ];
@@ -295,7 +296,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 128 ? 1 : 2) void k_attn_dkv(AttnA
   const int per = a.Hk * a.gsplit;
   const int part = blockIdx.x % a.gsplit, hk = blockIdx.x % per / a.gsplit;
   // early keys are seen by most queries: they start first
-  const Slot sl = key_slot<BK>(a, static_cast<int>(blockIdx.x / per), lane);
+  const Slot sl = key_slot(a, 7, static_cast<int>(blockIdx.x / per), lane);
   if (sl.s < 0) return;
   const int q0 = clamp_row(a.cuq[sl.s], a.Tq), q1 = clamp_row(a.cuq[sl.s + 1], a.Tq);
   const int k0 = clamp_row(a.cuk[sl.s], a.Tk), k1 = clamp_row(a.cuk[sl.s + 1], a.Tk);
@@ -430,9 +431,9 @@ __global__ __launch_bounds__(256) void k_attn_sum(AttnArgs a) {
 // the sums of the parts (all gradients of 4 sequences of 2048, 16 heads of 128
 // on 2: from 256 workgroups on 381 us, 512 305, 1024 335; of 3 uneven ones of
 // 8192 rows together, 16 heads of 64 on 2: 512 278, 1024 244).
-int group_parts(int Tk, int Hq, int Hk, int D) {
+int group_parts(int Tk, int S, int Hq, int Hk, int D) {
   const int g = Hq / Hk;
-  const int64_t blocks = (static_cast<int64_t>(Tk) / 128 + 1) * Hk;
+  const int64_t blocks = (static_cast<int64_t>(Tk) / 128 + S / 2 + 1) * Hk;   // a sequence ends inside a tile
   for (int n = 1; n < g; ++n)
     if (g % n == 0 && blocks * n >= (D == 128 ? 512 : 1024)) return n;
   return g;
@@ -442,7 +443,7 @@ template <typename T, int D>
 hipError_t run(const AttnArgs& a, hipStream_t s) {
   constexpr int W = 4, B = 32 * W;
   const int64_t nk = (static_cast<int64_t>(a.Tk) / B + a.S) * a.Hk * a.gsplit;
-  const int64_t nq = (static_cast<int64_t>(a.Tq) / B + a.S) * a.Hq;
+  const int64_t nq = (static_cast<int64_t>(a.Tq >> (7 - a.lp)) + a.S) * (a.Hq >> a.lp);
   k_attn_dq<T, D, W><<<static_cast<unsigned>(nq), 64 * W, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -462,14 +463,15 @@ constexpr size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 size_t attn_backward_workspace_bytes(int Tq, int Tk, int S, int Hq, int Hk, int D) {
-  const int g = group_parts(Tk, Hq, Hk, D);
+  const int g = group_parts(Tk, S, Hq, Hk, D);
   size_t n = up256(2 * sizeof(float) * (Tq * static_cast<size_t>(Hq) + 1));
   if (g > 1) n += 2 * up256(sizeof(float) * g * static_cast<size_t>(Tk) * Hk * D);
   return n;
 }
 
 hipError_t launch_attn_backward(AttnArgs& a, int bf16, void* ws, hipStream_t s) {
-  a.gsplit = group_parts(a.Tk, a.Hq, a.Hk, a.D);
+  a.lp = attn_log_pack(a.Hq, a.Hk);
+  a.gsplit = group_parts(a.Tk, a.S, a.Hq, a.Hk, a.D);
   char* c = static_cast<char*>(ws);
   a.stat = reinterpret_cast<float*>(c);
   c += up256(2 * sizeof(float) * (a.Tq * static_cast<size_t>(a.Hq) + 1));

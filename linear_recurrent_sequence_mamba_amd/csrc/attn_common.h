@@ -284,13 +284,13 @@ struct Slot {
   int s, tile;   // s = -1: none
 };
 __device__ __forceinline__ int clamp_row(int v, int T) { return max(0, min(v, T)); }
-template <int B>
-__device__ __forceinline__ Slot slot_of(const int32_t* cu, int S, int T, int slot, int lane) {
+// (B = 1 << lb)
+__device__ __forceinline__ Slot slot_of(const int32_t* cu, int S, int T, int lb, int slot, int lane) {
   int lo = 0, n = S;
   for (;;) {
     const int step = (n + 63) / 64;
     const int s = lo + lane * step;
-    const bool le = s < lo + n && clamp_row(cu[s < S ? s : S - 1], T) / B + s <= slot;
+    const bool le = s < lo + n && (clamp_row(cu[s < S ? s : S - 1], T) >> lb) + s <= slot;
     const int cnt = __popcll(__ballot(le));
     if (cnt == 0) return Slot{-1, 0};
     const int at = lo + (cnt - 1) * step;
@@ -299,7 +299,7 @@ __device__ __forceinline__ Slot slot_of(const int32_t* cu, int S, int T, int slo
     if (step == 1) break;
   }
   lo = __builtin_amdgcn_readfirstlane(lo);
-  const int tile = slot - (clamp_row(cu[lo], T) / B + lo);
+  const int tile = slot - ((clamp_row(cu[lo], T) >> lb) + lo);
   return tile < 0 ? Slot{-1, 0} : Slot{lo, tile};
 }
 
@@ -311,8 +311,9 @@ __device__ __forceinline__ Slot slot_of(const int32_t* cu, int S, int T, int slo
 // work.
 struct Ranked {
   int n, a;
-  __device__ __forceinline__ Ranked(const int32_t* cu, int S, int T, int B, int lane) : n(0), a(0) {
-    if (lane < S) n = (max(0, clamp_row(cu[lane + 1], T) - clamp_row(cu[lane], T)) + B - 1) / B;
+  __device__ __forceinline__ Ranked(const int32_t* cu, int S, int T, int lb, int lane) : n(0), a(0) {
+    if (lane < S)
+      n = (max(0, clamp_row(cu[lane + 1], T) - clamp_row(cu[lane], T)) + (1 << lb) - 1) >> lb;
   }
   __device__ __forceinline__ int count(int x) const {   // tiles of level x and more
     return __builtin_amdgcn_readfirstlane(
@@ -345,27 +346,49 @@ struct Ranked {
 // nothing (8 of 2048, 32 heads of 64: 200 us, ranked 215).
 __device__ __forceinline__ bool by_work(const AttnArgs& a) { return a.S > 1 && a.S <= 64; }
 
-// the n-th tile of B queries to start, of nslot
-template <int B>
-__device__ __forceinline__ Slot query_slot(const AttnArgs& a, int n, int nslot, int lane) {
-  if (!by_work(a) || gridDim.x > 2048) return slot_of<B>(a.cuq, a.S, a.Tq, nslot - 1 - n, lane);
-  Ranked r(a.cuq, a.S, a.Tq, B, lane);
+// the n-th tile of 1 << lb queries to start, of nslot
+__device__ __forceinline__ Slot query_slot(const AttnArgs& a, int lb, int n, int nslot, int lane) {
+  if (!by_work(a) || gridDim.x > 2048) return slot_of(a.cuq, a.S, a.Tq, lb, nslot - 1 - n, lane);
+  Ranked r(a.cuq, a.S, a.Tq, lb, lane);
   if (lane < a.S) {   // tiles of keys before the first query's own
     const int lk = clamp_row(a.cuk[lane + 1], a.Tk) - clamp_row(a.cuk[lane], a.Tk);
     const int lq = clamp_row(a.cuq[lane + 1], a.Tq) - clamp_row(a.cuq[lane], a.Tq);
-    r.a = max(0, lk - lq) / B;
+    r.a = max(0, lk - lq) >> lb;
   }
-  return r.at(n, max(a.Tq, a.Tk) / B + 3, lane);
+  return r.at(n, (max(a.Tq, a.Tk) >> lb) + 3, lane);
 }
-// the n-th tile of B keys to start: the first keys are seen by most queries
-template <int B>
-__device__ __forceinline__ Slot key_slot(const AttnArgs& a, int n, int lane) {
-  if (!by_work(a)) return slot_of<B>(a.cuk, a.S, a.Tk, n, lane);
-  const Ranked r(a.cuk, a.S, a.Tk, B, lane);
-  Slot s = r.at(n, a.Tk / B + 3, lane);
+// the n-th tile of 1 << lb keys to start: the first keys are seen by most queries
+__device__ __forceinline__ Slot key_slot(const AttnArgs& a, int lb, int n, int lane) {
+  if (!by_work(a)) return slot_of(a.cuk, a.S, a.Tk, lb, n, lane);
+  const Ranked r(a.cuk, a.S, a.Tk, lb, lane);
+  Slot s = r.at(n, (a.Tk >> lb) + 3, lane);
   if (s.s >= 0) s.tile = __builtin_amdgcn_readlane(r.n, s.s) - 1 - s.tile;
   return s;
 }
+
+// The (query, head) pairs of a workgroup's 128 columns: 128 >> lp queries of
+// 1 << lp heads that share k and v.  So fewer keys are loaded for queries that do
+// not see them, and short sequences fill a tile (packed rows of 32 heads of 64 on
+// 8: 240 us, one head a tile 249; 1000 sequences of 16, 16 heads of 128 on 4: 71
+// and 194).
+struct Columns {
+  int lp, queries, nslot, group, hk;   // queries of a workgroup; groups of heads, the own k and v
+  __device__ __forceinline__ explicit Columns(const AttnArgs& a) : lp(a.lp), queries(128 >> a.lp) {
+    const int ngroup = a.Hq >> lp;
+    nslot = gridDim.x / ngroup;
+    group = blockIdx.x % ngroup;
+    hk = (group << lp) / (a.Hq / a.Hk);
+  }
+  __device__ __forceinline__ Slot slot(const AttnArgs& a, int lane) const {
+    return query_slot(a, 7 - lp, static_cast<int>(blockIdx.x / (a.Hq >> lp)), nslot, lane);
+  }
+  __device__ __forceinline__ int first(int wave) const { return wave * (32 >> lp); }   // query of a wave
+  __device__ __forceinline__ int per_wave() const { return 32 >> lp; }
+  __device__ __forceinline__ int query(int lane) const { return (lane & 31) >> lp; }
+  __device__ __forceinline__ int head(int lane) const {
+    return (group << lp) + (lane & ((1 << lp) - 1));
+  }
+};
 
 // maximum and sum of lanes l and l ^ 32, in both.  The swap exchanges the
 // upper half of its first operand with the lower half of its second.

@@ -71,9 +71,10 @@ def _many(n, seed):
     return nq, [a + b for a, b in zip(nq, more)]
 
 
-# more sequences than a wave has lanes; more workgroups than are taken in the
+# groups of 32 and 12 heads; more sequences than a wave has lanes; more workgroups than are taken in the
 # order of their work; sequences of several tiles whose order that changes
-CASES += [(*_many(70, 1), 4, 2, 64), (*_many(64, 2), 40, 4, 64), (*_many(64, 3), 3, 1, 128),
+CASES += [([5, 40, 3], [9, 40, 70], 32, 1, 64), ([9, 70], [9, 200], 24, 2, 128),
+          (*_many(70, 1), 4, 2, 64), (*_many(64, 2), 40, 4, 64), (*_many(64, 3), 3, 1, 128),
           ([130, 400, 0, 257], [600, 400, 9, 300], 4, 2, 64), ([129, 300, 20], [129, 300, 700], 2, 2, 128)]
 
 

@@ -222,9 +222,9 @@ __device__ __forceinline__ void attend(Rows<D>& st, const Frag<T>* q, const char
 // The prompt: a workgroup takes 128 (query, head) columns; K and V tiles of BN
 // keys are double-buffered in LDS.  Two waves a SIMD (D = 64: three), so
 // that one's softmax runs beside another's products as well.  16384 tokens, 16
-// heads of 128: 1.03 ms, 1.06 PFLOP/s, matrix cores busy 56% and vector units
-// 49% of the cycles; packed rows of 32 heads of 64: 257 us, 0.77 PFLOP/s, 41%
-// and 71%.
+// heads of 128: 1.02 ms, 1.08 PFLOP/s, matrix cores busy 56% and vector units
+// 49% of the cycles; packed rows of 32 heads of 64: 242 us, 0.81 PFLOP/s, 40%
+// and 70%.
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn(AttnArgs a) {
   using L = Tile<T, D>;

@@ -141,7 +141,7 @@ constexpr int kExactD = 512;
 
 // ---------------------------------------------------------------------------
 // dq: 32 queries a wave, tiles of 32 keys in LDS (8192 packed rows, 16 heads of
-// 128 on 2: 176 us, 0.89 PFLOP/s, matrix cores busy 48%, vector units 35%)
+// 128 on 2: 166 us, 0.95 PFLOP/s, matrix cores busy 48%, vector units 35%)
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn_dq(AttnArgs a) {
   using L = Tile<T, D>;
@@ -283,7 +283,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
 // than 256 registers, which leaves one wave a SIMD; two kernels of two waves
 // each need a quarter more products (one row of 8192, 16 heads of 128 on 2, all
 // gradients: 1.06 ms, one kernel 0.95; fp32, two rows of 2048: 1.29 and 1.10).
-// 8192 packed rows: 273 us, 0.77 PFLOP/s, matrix cores busy 37%, vector units 30%.
+// 8192 packed rows: 268 us, 0.78 PFLOP/s, matrix cores busy 37%, vector units 30%.
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, D == 128 ? 1 : 2) void k_attn_dkv(AttnArgs a) {
   using L = Tile<T, D>;

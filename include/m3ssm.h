@@ -421,6 +421,10 @@ typedef struct {
                                  to the next, multiples of 8; 0: Tk rows   */
 } m3_attn_dims;
 
+/* (0 if dims is invalid; a call that is not split over keys, as those with many
+ * queries are not, needs no more than the 16 bytes returned for it) */
+size_t m3_attn_prefill_varlen_workspace_size(const m3_attn_dims* dims);
+
 /* q [Tq, Hq, D], k and v [Tk, Hk, D] packed by cu_seqlens_q and cu_seqlens_k
  * to o [Tq, Hq, D] and lse [Tq, Hq] fp32 (natural logarithm; NULL: not
  * written).  Offsets are clamped into their rows, so no access leaves the
@@ -430,7 +434,8 @@ typedef struct {
  * that see it and no others. */
 m3_status m3_attn_prefill_varlen(const m3_attn_dims* dims, const int32_t* cu_seqlens_q,
                                  const int32_t* cu_seqlens_k, const void* q, const void* k,
-                                 const void* v, void* o, float* lse, void* stream);
+                                 const void* v, void* o, float* lse, void* ws, size_t ws_bytes,
+                                 void* stream);
 
 size_t m3_attn_prefill_varlen_backward_workspace_size(const m3_attn_dims* dims);
 

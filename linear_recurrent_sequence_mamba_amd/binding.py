@@ -160,6 +160,7 @@ def _lib():
                 ("m3_gated_scan_workspace_size", [gp, i32]),
                 ("m3_gated_scan_backward_workspace_size", [gp, i32]),
                 ("m3_qk_norm_rope_backward_workspace_size", [qp]),
+                ("m3_attn_prefill_varlen_workspace_size", [ap]),
                 ("m3_attn_prefill_varlen_backward_workspace_size", [ap]),
                 ("m3_attn_decode_workspace_size", [ap])):
             getattr(lib, name).restype = sz
@@ -170,7 +171,7 @@ def _lib():
                 ("m3_gated_step", [gp] + [vp] * 7),
                 ("m3_qk_norm_rope", [qp] + [vp] * 8),
                 ("m3_qk_norm_rope_backward", [qp] + [vp] * 12 + [sz, vp]),
-                ("m3_attn_prefill_varlen", [ap] + [vp] * 8),
+                ("m3_attn_prefill_varlen", [ap] + [vp] * 8 + [sz, vp]),
                 ("m3_attn_prefill_varlen_backward", [ap] + [vp] * 12 + [sz, vp]),
                 ("m3_attn_decode", [ap] + [vp] * 7 + [sz, vp])):
             getattr(lib, name).restype = ctypes.c_int
@@ -886,12 +887,14 @@ def attn_prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, scale=None, stream=
     (o, lse).  Rows behind the last sequence are not written."""
     dev = _same_device("q k v cu_seqlens_q cu_seqlens_k", q, k, v, cu_seqlens_q, cu_seqlens_k)
     ref = _attn_setup(q, k, v, cu_seqlens_q, cu_seqlens_k, scale)
+    lib = _lib()
     with _on(dev, stream):
         o = q.new_empty(q.shape)
         lse = q.new_empty(q.shape[:2], dtype=torch.float32)
-        e = _lib().m3_attn_prefill_varlen(ref, _addr(cu_seqlens_q), _addr(cu_seqlens_k),
-                                          _addr(q), _addr(k), _addr(v), _addr(o), _addr(lse),
-                                          _raw(dev))
+        ws = _ws(lib.m3_attn_prefill_varlen_workspace_size(ref), "m3_attn_prefill_varlen", q)
+        e = lib.m3_attn_prefill_varlen(ref, _addr(cu_seqlens_q), _addr(cu_seqlens_k), _addr(q),
+                                       _addr(k), _addr(v), _addr(o), _addr(lse), _addr(ws),
+                                       ws.numel(), _raw(dev))
     if e != 0:
         raise M3Error(e, "m3_attn_prefill_varlen")
     return o, lse

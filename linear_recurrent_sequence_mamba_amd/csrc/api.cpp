@@ -761,15 +761,26 @@ m3_status m3_qk_norm_rope_backward(const m3_qk_dims* d, const void* q, const voi
       m3::launch_qk_norm_backward(a, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
 }
 
+size_t m3_attn_prefill_varlen_workspace_size(const m3_attn_dims* d) {
+  if (check_attn(d, false) != M3_OK) return 0;
+  const size_t n = m3::attn_workspace_bytes(d->tokens_q, d->tokens_k, d->nseq, d->nheads_q,
+                                            d->nheads_k, d->headdim, d->dtype == M3_BF16);
+  return n ? n : 16;
+}
+
 m3_status m3_attn_prefill_varlen(const m3_attn_dims* d, const int32_t* cu_seqlens_q,
                                  const int32_t* cu_seqlens_k, const void* q, const void* k,
-                                 const void* v, void* o, float* lse, void* stream) {
+                                 const void* v, void* o, float* lse, void* ws, size_t ws_bytes,
+                                 void* stream) {
   m3_status st = check_attn(d, false);
   if (st != M3_OK) return st;
   if (!cu_seqlens_q || !cu_seqlens_k || !q || !k || !v || !o) return M3_ERR_NULL;
-  const void* const ptrs[] = {q, k, v, o, lse};
+  const void* const ptrs[] = {q, k, v, o, lse, ws};
   if (any_misaligned(ptrs) || misaligned4(cu_seqlens_q) || misaligned4(cu_seqlens_k))
     return M3_ERR_ALIGN;
+  const size_t need = m3::attn_workspace_bytes(d->tokens_q, d->tokens_k, d->nseq, d->nheads_q,
+                                               d->nheads_k, d->headdim, d->dtype == M3_BF16);
+  if (need && (!ws || ws_bytes < need)) return M3_ERR_WORKSPACE;
   m3::AttnArgs a = attn_args(d);
   a.cuq = cu_seqlens_q;
   a.cuk = cu_seqlens_k;
@@ -778,7 +789,7 @@ m3_status m3_attn_prefill_varlen(const m3_attn_dims* d, const int32_t* cu_seqlen
   a.v = v;
   a.o = o;
   a.lse = lse;
-  return hip_status(m3::launch_attn(a, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
+  return hip_status(m3::launch_attn(a, d->dtype == M3_BF16, ws, static_cast<hipStream_t>(stream)));
 }
 
 size_t m3_attn_prefill_varlen_backward_workspace_size(const m3_attn_dims* d) {

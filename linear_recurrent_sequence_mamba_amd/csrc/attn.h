@@ -19,16 +19,16 @@ struct AttnArgs {
   void *dq, *dk, *dv;           // dense rows
   float* stat;                  // workspace [2, Hq, Tq]: lse log2(e), then -<o, do>; infinity and 0
   float *pk, *pv;               // workspace [gsplit, Tk, Hk, D]: parts of dk, dv
+  float *po, *pm;               // workspace: parts of o and their (max, sum)
   // decode
   const int32_t* len;           // [S] rows of each sequence's cache
-  float *po, *pm;               // workspace: parts of o and their (max, sum)
   int64_t ldq, ldk, ldv, ldo, lddo;
   int64_t bk, bv;               // decode: elements from one sequence's cache to the next
   int Tq, Tk, S, Hq, Hk, D;
   int cap;                      // decode: rows a cache has room for
   int gsplit;                   // parts of a group of heads (backward of k, v)
   int lp;                       // log2 of the heads of a group that a tile of queries takes
-  int nsplit;                   // parts of a cache (decode)
+  int nsplit;                   // parts of the keys (prompt) or of a cache (decode)
   float scale;
 };
 
@@ -42,7 +42,8 @@ inline int attn_log_pack(int Hq, int Hk) {
 bool attn_supported(int D);
 size_t attn_backward_workspace_bytes(int Tq, int Tk, int S, int Hq, int Hk, int D);
 size_t attn_decode_workspace_bytes(int S, int cap, int Hq, int Hk, int D);
-hipError_t launch_attn(AttnArgs& a, int bf16, hipStream_t s);
+size_t attn_workspace_bytes(int Tq, int Tk, int S, int Hq, int Hk, int D, int bf16);
+hipError_t launch_attn(AttnArgs& a, int bf16, void* ws, hipStream_t s);
 hipError_t launch_attn_backward(AttnArgs& a, int bf16, void* ws, hipStream_t s);
 hipError_t launch_attn_decode(AttnArgs& a, int bf16, void* ws, hipStream_t s);
 

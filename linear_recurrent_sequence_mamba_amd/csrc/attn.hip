@@ -225,7 +225,7 @@ __device__ __forceinline__ void attend(Rows<D>& st, const Frag<T>* q, const char
 // heads of 128: 1.02 ms, 1.08 PFLOP/s, matrix cores busy 56% and vector units
 // 49% of the cycles; packed rows of 32 heads of 64: 242 us, 0.81 PFLOP/s, 40%
 // and 70%.
-template <typename T, int D, int WAVES>
+template <typename T, int D, int WAVES, bool SPLIT>
 __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_attn(AttnArgs a) {
   using L = Tile<T, D>;
   static_assert(WAVES == 4, "128 columns");
@@ -260,36 +260,48 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   Rows<D> st;
   st.init();
   const float c = a.scale * kLog2eA;
-  const int sees = min(i, Lq - 1) + off + 1;   // keys that the lane's query sees
-  const int most = min(min(i0 + col.queries, Lq) + off, Lk);   // that any query of the block sees
-  const int ntile = most <= 0 ? 0 : (most + BN - 1) / BN;
+  int sees = min(i, Lq - 1) + off + 1;   // keys that the lane's query sees
+  int most = min(min(i0 + col.queries, Lq) + off, Lk);   // that any query of the block sees
+  int ntile = most <= 0 ? 0 : (most + BN - 1) / BN;
   // from here on some query of the block does not see the whole tile
-  const int tmask = max(0, min(i0, Lq - 1) + off + 1) / BN;
+  int tmask = max(0, min(i0, Lq - 1) + off + 1) / BN;
   const int wmost = min(min(iw + col.per_wave(), Lq) + off, Lk);
+  int nw = (max(wmost, 0) + BN - 1) / BN;   // tiles that the wave sees
+  int last = Lk - 1;
   const T* kp = static_cast<const T*>(a.k) + static_cast<int64_t>(k0) * a.ldk + hk * D;
   const T* vp = static_cast<const T*>(a.v) + static_cast<int64_t>(k0) * a.ldv + hk * D;
+  if (SPLIT) {   // this workgroup's tiles, counted from its first key
+    const int per = (ntile + a.nsplit - 1) / a.nsplit, t0 = min(static_cast<int>(blockIdx.y) * per, ntile);
+    ntile = min(per, ntile - t0);
+    kp += static_cast<int64_t>(t0 * BN) * a.ldk;
+    vp += static_cast<int64_t>(t0 * BN) * a.ldv;
+    sees -= t0 * BN;
+    last -= t0 * BN;
+    most = min(most - t0 * BN, ntile * BN);
+    tmask = max(0, tmask - t0);
+    nw = min(max(0, nw - t0), ntile);
+  }
   // K runs one tile ahead of V.  Tiles that every query of the block sees
   // whole come first, in pairs (the two sets of scores change places): while
   // a tile's weights are formed the next tile's scores are.
   f16v s[NB], next[NB];
-  const int nw = (max(wmost, 0) + BN - 1) / BN;   // tiles that the wave sees
   const int npipe = max(0, min(tmask, ntile - 1)) & ~1;   // (no tile: none)
   auto arrive = [&](int t, char* K, char* V) __attribute__((always_inline)) {
     lds_loads_done();
     __syncthreads();   // V of t and K of t + 1 are there; every wave is done with t - 1
-    if (t + 2 < ntile) L::template load<WAVES>(K, kp, a.ldk, (t + 2) * BN, Lk - 1, wave, lane);
-    if (t + 1 < ntile) L::template load<WAVES>(V, vp, a.ldv, (t + 1) * BN, Lk - 1, wave, lane);
+    if (t + 2 < ntile) L::template load<WAVES>(K, kp, a.ldk, (t + 2) * BN, last, wave, lane);
+    if (t + 1 < ntile) L::template load<WAVES>(V, vp, a.ldv, (t + 1) * BN, last, wave, lane);
     // At D = 128 it is faster to let the loads end before the tiles at hand are
     // read (16384 tokens, 16 heads: 1042 us, not waiting 1061), at D = 64 not to
     // (packed rows of 32 heads: 264 and 255 us).
     if (D == 128) lds_loads_done();
   };
   if (ntile > 0) {
-    L::template load<WAVES>(sK0, kp, a.ldk, 0, Lk - 1, wave, lane);
+    L::template load<WAVES>(sK0, kp, a.ldk, 0, last, wave, lane);
     lds_loads_done();
     __syncthreads();
-    L::template load<WAVES>(sV0, vp, a.ldv, 0, Lk - 1, wave, lane);
-    if (ntile > 1) L::template load<WAVES>(sK1, kp, a.ldk, BN, Lk - 1, wave, lane);
+    L::template load<WAVES>(sV0, vp, a.ldv, 0, last, wave, lane);
+    if (ntile > 1) L::template load<WAVES>(sK1, kp, a.ldk, BN, last, wave, lane);
     score<T, D, NB>(s, q, sK0, lane);
   }
   float mx = npipe > 0 ? max_of<NB>(s) : 0.0f;
@@ -329,6 +341,17 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
   }
   const float l = half_sum(st.l);
   if (i >= Lq) return;
+  if constexpr (SPLIT) {
+    const int64_t at = (row * a.Hq + h) * a.nsplit + blockIdx.y;
+    float* o = a.po + at * D + 4 * half;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        put4(o + 32 * d + 8 * e, st.o[d][4 * e], st.o[d][4 * e + 1], st.o[d][4 * e + 2], st.o[d][4 * e + 3]);
+    if (half == 0) *reinterpret_cast<f2*>(a.pm + 2 * at) = f2{st.m, l};
+    return;
+  }
   const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);   // a NaN stays
   T* o = static_cast<T*>(a.o) + row * a.ldo + h * D + 4 * half;
 #pragma unroll
@@ -452,7 +475,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
   }
 }
 
-// Joins the parts of one (sequence, head) per workgroup: 256 / (D / 4) groups
+// Joins the parts of one (sequence or query, head) per workgroup: 256 / (D / 4) groups
 // of threads take every so manieth part each, four channels a thread.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
@@ -460,6 +483,10 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   __shared__ f4 sv[NG][D / 4];
   __shared__ float sl[NG];
   const int64_t n = blockIdx.x;
+  if (a.cuq) {   // of queries: those that belong to a sequence
+    const int64_t row = n / a.Hq;
+    if (row < clamp_row(a.cuq[0], a.Tq) || row >= clamp_row(a.cuq[a.S], a.Tq)) return;
+  }
   const int dl = threadIdx.x % (D / 4), g = threadIdx.x / (D / 4), lane = threadIdx.x & 63;
   const f2* pm = reinterpret_cast<const f2*>(a.pm) + n * a.nsplit;
   float m = -INFINITY;
@@ -501,8 +528,31 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 template <typename T, int D>
 hipError_t run_attn(const AttnArgs& a, hipStream_t s) {
   const int64_t slots = (a.Tq >> (7 - a.lp)) + a.S;
-  k_attn<T, D, 4><<<static_cast<unsigned>(slots * (a.Hq >> a.lp)), 256, 0, s>>>(a);
+  const dim3 grid(static_cast<unsigned>(slots * (a.Hq >> a.lp)), static_cast<unsigned>(a.nsplit));
+  if (a.nsplit == 1) {
+    k_attn<T, D, 4, false><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  k_attn<T, D, 4, true><<<grid, 256, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_attn_join<T, D><<<static_cast<unsigned>(static_cast<int64_t>(a.Tq) * a.Hq), 256, 0, s>>>(a);
   return hipGetLastError();
+}
+
+// Parts of the keys where queries are so few that four would still not fill the
+// chip (two workgroups a CU), each with 512 keys at the least of a sequence of
+// mean length, in fp32, whose products take longer, 256.  16 queries of 16384
+// keys, 16 heads of 128 on 2: 340 us whole, 26 split; 256 of 8192: 170 and 42; 2048
+// of 2048, 4 heads of 128: 43 and 32; but 1024 of 1024, 16 heads on 2, in two: 27
+// and 41, as the parts of so many rows have to be joined.  fp32, 2 of 1400, 64
+// heads of 64 on 8: 98, 55 with 512 keys, 30 with 256.
+int prompt_parts(int Tq, int Tk, int S, int Hq, int Hk, int bf16) {
+  const int lp = attn_log_pack(Hq, Hk);
+  const int64_t blocks = ((static_cast<int64_t>(Tq) >> (7 - lp)) + S) * (Hq >> lp);
+  const int n = static_cast<int>(512 / blocks), most = Tk / S / (bf16 ? 512 : 256);
+  if (n < 4 || most < 2) return 1;
+  return n < most ? n : most;
 }
 
 template <typename T, int D, int WAVES>
@@ -530,8 +580,16 @@ int decode_parts(int S, int cap, int Hq, int Hk) {
 
 bool attn_supported(int D) { return D == 64 || D == 128; }
 
-hipError_t launch_attn(AttnArgs& a, int bf16, hipStream_t s) {
+size_t attn_workspace_bytes(int Tq, int Tk, int S, int Hq, int Hk, int D, int bf16) {
+  const int n = prompt_parts(Tq, Tk, S, Hq, Hk, bf16);
+  return n == 1 ? 0 : sizeof(float) * (static_cast<size_t>(D) + 2) * Tq * Hq * n;
+}
+
+hipError_t launch_attn(AttnArgs& a, int bf16, void* ws, hipStream_t s) {
   a.lp = attn_log_pack(a.Hq, a.Hk);
+  a.nsplit = prompt_parts(a.Tq, a.Tk, a.S, a.Hq, a.Hk, bf16);
+  a.po = static_cast<float*>(ws);
+  a.pm = a.po + static_cast<size_t>(a.D) * a.Tq * a.Hq * a.nsplit;
   if (bf16) return a.D == 64 ? run_attn<bf16_t, 64>(a, s) : run_attn<bf16_t, 128>(a, s);
   return a.D == 64 ? run_attn<float, 64>(a, s) : run_attn<float, 128>(a, s);
 }

@@ -73,6 +73,9 @@ def _many(n, seed):
 
 # groups of 32 and 12 heads; more sequences than a wave has lanes; more workgroups than are taken in the
 # order of their work; sequences of several tiles whose order that changes
+# few queries of many keys, whose keys are split over workgroups
+CASES += [([2], [3000], 16, 2, 64), ([1, 5, 0, 9], [2600, 1500, 0, 700], 4, 2, 128),
+          ([90, 70], [1100, 1300], 3, 3, 64)]
 CASES += [([5, 40, 3], [9, 40, 70], 32, 1, 64), ([9, 70], [9, 200], 24, 2, 128),
           (*_many(70, 1), 4, 2, 64), (*_many(64, 2), 40, 4, 64), (*_many(64, 3), 3, 1, 128),
           ([130, 400, 0, 257], [600, 400, 9, 300], 4, 2, 64), ([129, 300, 20], [129, 300, 700], 2, 2, 128)]
@@ -114,7 +117,7 @@ def test_rows_behind_the_last_sequence_stay():
     p = lambda t: ctypes.c_void_p(t.data_ptr())
     s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     lib = m3.library()
-    assert lib.m3_attn_prefill_varlen(ctypes.byref(d), p(cu), p(cu), p(q), p(k), p(v), p(o), p(lse), s) == 0
+    assert lib.m3_attn_prefill_varlen(ctypes.byref(d), p(cu), p(cu), p(q), p(k), p(v), p(o), p(lse), None, 0, s) == 0
     g = [torch.full_like(t, 7.0) for t in (q, k, v)]
     ws = torch.empty(lib.m3_attn_prefill_varlen_backward_workspace_size(ctypes.byref(d)), dtype=torch.uint8,
                      device="cuda")
@@ -124,6 +127,44 @@ def test_rows_behind_the_last_sequence_stay():
     torch.cuda.synchronize()
     for t in (o, lse, *g):
         assert (t[150:] == 7).all() and not (t[:150] == 7).all(-1).any()
+
+
+def test_few_queries_of_many_keys():
+    """The keys split over workgroups: rows that no sequence covers stay, NaN of
+    what a query does not see as well, and replays of a graph keep the bits."""
+    Hq, Hk, D, nk = 4, 2, 64, [3000, 2500]
+    q, k, v, _ = _inputs(12, 5510, Hq, Hk, D, BF16, 31)
+    cq, ck = _dev([2, 5, 9]), _dev([5, 3005, 5505])
+    k[:5] = v[:5] = float("nan")
+    v[3004, 0] = float("inf")   # the last key of the first sequence: its last query alone sees it
+    o, lse = torch.full_like(q, 7.0), torch.full((12, Hq), 7.0, device="cuda")
+    d = m3.m3_attn_dims(2, 12, 5510, Hq, Hk, D, m3.M3_BF16, 0.125, *[0] * 7)
+    lib = m3.library()
+    n = lib.m3_attn_prefill_varlen_workspace_size(ctypes.byref(d))
+    assert n > 16
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")   # NaN
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+
+    def run():
+        assert lib.m3_attn_prefill_varlen(ctypes.byref(d), p(cq), p(ck), p(q), p(k), p(v), p(o), p(lse), p(ws), n,
+                                          ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+    run()
+    torch.cuda.synchronize()
+    for t in (o, lse):
+        assert (t[:2] == 7).all() and (t[9:] == 7).all()
+    assert torch.isinf(o[4, :2]).all() and torch.isfinite(o[2:4]).all() and torch.isfinite(o[5:9]).all()
+    assert torch.isfinite(o[4, 2:]).all() and torch.isfinite(lse[2:9]).all()
+    want = [o.clone(), lse.clone()]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for _ in range(3):
+        o.fill_(7.0)
+        lse.fill_(7.0)
+        ws.fill_(255)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
 
 
 def test_offsets_outside_the_rows_touch_nothing_else():
@@ -143,7 +184,7 @@ def test_offsets_outside_the_rows_touch_nothing_else():
         d = m3.m3_attn_dims(2, T, T, H, H, D, m3.M3_BF16, 0.125, 0, 0, 0, 0, 0, 0, 0)
         ws = torch.empty(lib.m3_attn_prefill_varlen_backward_workspace_size(ctypes.byref(d)),
                          dtype=torch.uint8, device="cuda")
-        assert lib.m3_attn_prefill_varlen(ctypes.byref(d), p(c), p(c), p(q), p(k), p(v), p(o), p(lse), s) == 0
+        assert lib.m3_attn_prefill_varlen(ctypes.byref(d), p(c), p(c), p(q), p(k), p(v), p(o), p(lse), None, 0, s) == 0
         assert lib.m3_attn_prefill_varlen_backward(
             ctypes.byref(d), p(c), p(c), p(q), p(k), p(v), p(o), p(lse), p(do), p(dq), p(dk), p(dv), p(ws),
             ws.numel(), s) == 0

@@ -78,7 +78,7 @@ def _qk_bwd(d, **o):
 
 def _attn(d, **o):
     return _call("m3_attn_prefill_varlen", d, ("cuq", "cuk", "q", "k", "v", "o", "lse"),
-                 ("cuq", "cuk", "q", "k", "v", "o"), o, ws=False)
+                 ("cuq", "cuk", "q", "k", "v", "o"), o)
 
 
 def _attn_bwd(d, **o):
@@ -94,7 +94,7 @@ def test_header_declares_and_the_library_exports():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     src = re.sub(r"/\*.*?\*/", "", open(os.path.join(root, "include", "m3ssm.h")).read(), flags=re.S)
     for n in ("m3_gated_scan", "m3_gated_scan_backward", "m3_gated_step", "m3_qk_norm_rope",
-              "m3_qk_norm_rope_backward", "m3_attn_prefill_varlen", "m3_attn_prefill_varlen_backward",
+              "m3_qk_norm_rope_backward", "m3_attn_prefill_varlen", "m3_attn_prefill_varlen_workspace_size", "m3_attn_prefill_varlen_backward",
               "m3_attn_decode", "m3_gated_scan_workspace_size", "m3_gated_scan_backward_workspace_size",
               "m3_qk_norm_rope_backward_workspace_size", "m3_attn_prefill_varlen_backward_workspace_size",
               "m3_attn_decode_workspace_size"):
@@ -198,6 +198,11 @@ def test_attn_refusals():
     n = lib.m3_attn_decode_workspace_size(ctypes.byref(long))
     assert n > 16 and _decode(long, ws_bytes=n - 1) == WS and _decode(long, ws=None) == WS
     assert lib.m3_attn_decode_workspace_size(ctypes.byref(_adims(headdim=96))) == 0
+    few = _adims(tokens_q=8, tokens_k=100000)
+    n = lib.m3_attn_prefill_varlen_workspace_size(ctypes.byref(few))
+    assert n > 16 and _attn(few, ws_bytes=n - 1) == WS and _attn(few, ws=None) == WS
+    assert lib.m3_attn_prefill_varlen_workspace_size(ctypes.byref(_adims())) == 16
+    assert lib.m3_attn_prefill_varlen_workspace_size(ctypes.byref(_adims(headdim=96))) == 0
 
 
 def test_attn_refuses_scales_that_are_not_positive():

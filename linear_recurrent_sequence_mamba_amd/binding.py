@@ -881,6 +881,14 @@ def _attn_setup(q, k, v, cu_q, cu_k, scale, ld_o=0, ld_do=0):
                  *ld, ld_o, ld_do, 0, 0)[1]
 
 
+def _split_ws(n, like):
+    """The workspace of a call that may be split, and its bytes; none for the
+    16 bytes that stand for a call that is not."""
+    if n <= 16:
+        return None, 0
+    return like.new_empty(((n + 15) // 16 * 16,), dtype=torch.uint8), n
+
+
 def attn_prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, scale=None, stream=None):
     """Causal attention of packed sequences: q [Tq, Hq, D], k and v
     [Tk, Hk, D] (m3_attn_prefill_varlen; scale D^-1/2 by default).  Returns
@@ -891,10 +899,10 @@ def attn_prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, scale=None, stream=
     with _on(dev, stream):
         o = q.new_empty(q.shape)
         lse = q.new_empty(q.shape[:2], dtype=torch.float32)
-        ws = _ws(lib.m3_attn_prefill_varlen_workspace_size(ref), "m3_attn_prefill_varlen", q)
+        ws, n = _split_ws(lib.m3_attn_prefill_varlen_workspace_size(ref), q)
         e = lib.m3_attn_prefill_varlen(ref, _addr(cu_seqlens_q), _addr(cu_seqlens_k), _addr(q),
-                                       _addr(k), _addr(v), _addr(o), _addr(lse), _addr(ws),
-                                       ws.numel(), _raw(dev))
+                                       _addr(k), _addr(v), _addr(o), _addr(lse), _addr(ws), n,
+                                       _raw(dev))
     if e != 0:
         raise M3Error(e, "m3_attn_prefill_varlen")
     return o, lse
@@ -951,10 +959,11 @@ def attn_decode(q, k_cache, v_cache, lengths, scale=None, o=None, ws=None, strea
             o = q.new_empty(q.shape)
         lse = q.new_empty((S, Hq), dtype=torch.float32)
         if ws is None:
-            ws = _ws(lib.m3_attn_decode_workspace_size(ref), "m3_attn_decode", q)
+            ws, n = _split_ws(lib.m3_attn_decode_workspace_size(ref), q)
+        else:
+            n = ws.numel() * ws.element_size()
         e = lib.m3_attn_decode(ref, _addr(lengths), _addr(q), _addr(k_cache),
-                               _addr(v_cache), _addr(o), _addr(lse), _addr(ws),
-                               ws.numel() * ws.element_size(), _raw(dev))
+                               _addr(v_cache), _addr(o), _addr(lse), _addr(ws), n, _raw(dev))
     if e != 0:
         raise M3Error(e, "m3_attn_decode")
     return o, lse

@@ -67,6 +67,21 @@ __device__ __forceinline__ bool drop_special(char* V) {
   return found;
 }
 
+// Rows 32 + n .. 63 of a wave's own tile become 0.  What was loaded there behind
+// the end of a cache repeats its last row, and the weights there are 0: a zero
+// times a value that is infinite would be NaN.
+template <typename T, int D>
+__device__ __forceinline__ void clear_rows(char* KV, int n, int lane) {
+  using L = Tile<T, D>;
+  lane = opaque(lane);
+  char* const at = KV + 16 * lane;
+  n += 32 - L::lane_row(lane);
+#pragma unroll
+  for (int g = 0; g < L::NG; ++g)
+    if (L::group_row(g) >= n) *reinterpret_cast<uint4*>(at + L::place(g)) = uint4{0u, 0u, 0u, 0u};
+  lds_reads_done();   // (and writes)
+}
+
 // Scores of 32 queries against NB x 32 keys
 template <typename T, int D, int NB>
 __device__ __forceinline__ void score(f16v* s, const Frag<T>* q, const char* K, int lane) {
@@ -414,11 +429,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
   if (t < t1) fetch(t);
   for (; t < t1; t += WAVES) {
     lds_loads_done();
-    // rows past the end repeat the last one, which every query sees
-    if ((t + 1) * BN <= len)
+    if ((t + 1) * BN <= len) {
       attend<T, D, false>(st, q, sKV[wave], c, BN, lane);
-    else
+    } else {   // keys past the end are hidden, their values cleared
+      clear_rows<T, D>(sKV[wave], len - t * BN, lane);
       attend<T, D, true>(st, q, sKV[wave], c, len - t * BN, lane);
+    }
     if (t + WAVES < t1) {
       lds_reads_done();
       fetch(t + WAVES);

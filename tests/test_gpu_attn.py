@@ -379,3 +379,33 @@ def test_equal_bits_graphs_and_streams():
     o, lse = m3.attn_prefill_varlen(q, k, v, cu, cu, stream=s)
     s.synchronize()
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def _tail_specials(v, s, n, D):
+    """Infinities of both signs and NaN in the last rows of a cache's values."""
+    v[s, n - 1, 0, 3] = float("inf")
+    v[s, n - 1, -1, D - 1] = -float("inf")
+    if n > 1:
+        v[s, n - 2, 0, 9] = float("nan")
+        v[s, n - 2, 0, 40] = float("inf")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_of_infinite_values_in_a_cache_that_ends_inside_a_tile(D, dtype):
+    """The last row is there once: what is loaded for the rest of its tile must
+    not turn an infinity into NaN.  Whole tiles, one row, and caches that are
+    split over workgroups among them."""
+    Hq, Hk = 6, 2
+    for lengths, cap in (([1, 33, 64, 95, 2, 31], 96), ([1500, 513, 1026], 1500)):
+        S = len(lengths)
+        g = torch.Generator().manual_seed(cap + D)
+        q = torch.randn(S, Hq, D, generator=g).to(dtype).cuda()
+        k, v = (torch.randn(S, cap, Hk, D, generator=g).to(dtype).cuda() for _ in range(2))
+        for s, n in enumerate(lengths):
+            _tail_specials(v, s, n, D)
+        o, lse = m3.attn_decode(q, k, v, torch.tensor(lengths, dtype=torch.int32).cuda())
+        torch.cuda.synchronize()
+        wo, bo, wl = _decode_ref(q, k, v, lengths, D ** -0.5, dtype)
+        _check("o", o, wo, bo)
+        _check("lse", lse, wl, torch.tensor(2.0 ** -24 * (D + 8) * D ** 0.5 * 16 + 2.0 ** -19 * 8))

@@ -607,9 +607,13 @@ _HERE = contextlib.nullcontext()
 
 def _on(index, stream):
     """A context for the launch.  Nothing is switched where nothing has to be:
-    a small call is bound by the host."""
-    if stream is None and index == torch.cuda.current_device():
-        return _HERE
+    a small call is bound by the host.  The launch goes to the tensors' device,
+    so a stream of another one is refused."""
+    if stream is None:
+        if index == torch.cuda.current_device():
+            return _HERE
+    elif stream.device.index != index:
+        raise ValueError(f"stream is of {stream.device}, the tensors are on cuda:{index}")
     return _Switch(index, stream)
 
 

@@ -307,3 +307,19 @@ def test_reference_gradients_against_differentiation():
     want = torch.autograd.grad((ref.attn(*w, 0.3)[0] * do).sum(), w)
     for a, b in zip((dq, dk, dv), want):
         assert float((a - b).abs().max()) <= 1e-12
+
+
+class _StreamOf:
+    """What the helpers look at in a stream."""
+
+    def __init__(self, device):
+        self.device = torch.device(device)
+        self.cuda_stream = 0
+
+
+def test_a_stream_of_another_device_is_refused():
+    """The call would go to the tensors' device, on a stream that the caller did
+    not name."""
+    with pytest.raises(ValueError, match="cuda:1.*cuda:0"):
+        m3._on(0, _StreamOf("cuda:1"))
+    assert isinstance(m3._on(1, _StreamOf("cuda:1")), m3._Switch)

@@ -409,3 +409,52 @@ def test_decode_of_infinite_values_in_a_cache_that_ends_inside_a_tile(D, dtype):
         wo, bo, wl = _decode_ref(q, k, v, lengths, D ** -0.5, dtype)
         _check("o", o, wo, bo)
         _check("lse", lse, wl, torch.tensor(2.0 ** -24 * (D + 8) * D ** 0.5 * 16 + 2.0 ** -19 * 8))
+
+
+def _of_sequence(q, k, v, do, o, lse, grads, a, c, dtype):
+    """Rows a of queries and c of keys against the definition."""
+    scale = q.shape[-1] ** -0.5
+    x, y, z, w = ref.f64(q[a]), ref.f64(k[c]), ref.f64(v[c]), ref.f64(do[a])
+    wo, wl, p = ref.attn(x, y, z, scale)
+    (wq, wk, wv), (bq, bk, bv) = ref.attn_grads(x, y, z, w, scale, dtype)
+    _check("o", o[a], wo, ref.attn_bound(x, y, z, wo, p, scale, dtype))
+    _check("lse", lse[a], wl, torch.tensor(2.0 ** -24 * (q.shape[-1] + 8) * q.shape[-1] ** 0.5 * 16 + 2.0 ** -19 * 8))
+    for n, got, want, b in (("dq", grads[0][a], wq, bq), ("dk", grads[1][c], wk, bk), ("dv", grads[2][c], wv, bv)):
+        _check(n, got, want, b)
+
+
+def test_rows_times_heads_beyond_2_to_28():
+    """2^34 and more elements of q: sequences at both ends and in the middle."""
+    torch.cuda.empty_cache()   # 110 GB
+    n, Hq, D, L = (1 << 23) + 1000, 32, 64, 200
+    q = torch.empty(n, Hq, D, dtype=BF16, device="cuda")
+    for r in range(0, n, 1 << 18):
+        q[r:r + (1 << 18)].normal_()
+    k, v = torch.randn(n, 1, D, device="cuda").to(BF16), torch.randn(n, 1, D, device="cuda").to(BF16)
+    cut = list(range(0, n, L)) + [n]
+    cu = _dev(cut)
+    o, lse = m3.attn_prefill_varlen(q, k, v, cu, cu)
+    g = m3.attn_prefill_varlen_backward(q, k, v, o, lse, q, cu, cu)
+    torch.cuda.synchronize()
+    for s in (0, 1, len(cut) // 2, len(cut) - 3, len(cut) - 2):
+        rows = slice(cut[s], cut[s + 1])
+        say(f"sequence {s}: rows {rows.start}..{rows.stop}")
+        _of_sequence(q, k, v, q, o, lse, g, rows, rows, BF16)
+
+
+def test_keys_of_more_than_2_to_34_elements():
+    """The last sequence's keys lie behind 2^34 elements of a sequence that has
+    no query, whose gradients are 0."""
+    torch.cuda.empty_cache()   # 140 GB
+    n0, L, H, D = (1 << 24) - 100, 201, 16, 64
+    k, v = (torch.empty(n0 + L, H, D, dtype=BF16, device="cuda") for _ in range(2))
+    k[n0:].normal_()
+    v[n0:].normal_()
+    q, do = torch.randn(70, H, D, device="cuda").to(BF16), torch.randn(70, H, D, device="cuda").to(BF16)
+    cq, ck = _dev([0, 0, 70]), _dev([0, n0, n0 + L])
+    o, lse = m3.attn_prefill_varlen(q, k, v, cq, ck)
+    g = m3.attn_prefill_varlen_backward(q, k, v, o, lse, do, cq, ck)
+    torch.cuda.synchronize()
+    for t in g[1:]:
+        assert not t[:5000].any() and not t[n0 - 5000:n0].any()
+    _of_sequence(q, k, v, do, o, lse, g, slice(0, 70), slice(n0, n0 + L), BF16)

@@ -323,3 +323,19 @@ def test_a_stream_of_another_device_is_refused():
     with pytest.raises(ValueError, match="cuda:1.*cuda:0"):
         m3._on(0, _StreamOf("cuda:1"))
     assert isinstance(m3._on(1, _StreamOf("cuda:1")), m3._Switch)
+
+
+def test_attention_takes_what_its_launches_hold():
+    """Rows times heads beyond 2^28 and keys of more than 2^34 elements: a grid
+    has a workgroup for 128 rows and a head, and fewer where heads share one."""
+    lib = m3.library()
+    size = lambda **k: lib.m3_attn_prefill_varlen_workspace_size(ctypes.byref(_adims(**k)))
+    back = lambda **k: lib.m3_attn_prefill_varlen_backward_workspace_size(ctypes.byref(_adims(**k)))
+    for k in (dict(tokens_q=(1 << 23) + 1, nheads_q=32, nheads_k=1), dict(tokens_q=1 << 26, nheads_q=8),
+              dict(tokens_q=9000000, tokens_k=9000000, nheads_q=32, nheads_k=8),
+              dict(tokens_k=(1 << 24) + 64, nheads_q=16, nheads_k=16, headdim=128)):
+        assert size(**k) > 0, k
+        rows = k.get("tokens_q", 100) * k["nheads_q"]
+        assert back(**k) >= 8 * rows, k
+    # 2^24 workgroups of 256 threads are more than a launch counts
+    assert size(tokens_q=1 << 27, nheads_q=16) == 0 and back(tokens_k=1 << 27, nheads_q=16) == 0

@@ -366,7 +366,7 @@ m3_status m3_gated_step(const m3_gated_dims* dims, float* h, const void* x, cons
  *     pairs (u_2j, u_2j+1), j < rotary_dim / 2, turned by
  *     position * base^(-2j / rotary_dim); the other channels stay as they are.
  * flags: M3_ROPE_HALF pairs (u_j, u_j+rotary_dim/2) instead.  Angles are
- * reduced in fp64, so any int32 position keeps its phase. */
+ * reduced in fp64, so any int32 position keeps its phase (to about 1e-6 rad). */
 #define M3_ROPE_HALF (1u << 0)
 typedef struct {
   int32_t tokens;     /* T >= 1 rows, of any number of sequences           */

@@ -13,6 +13,7 @@
 #include "gated.h"
 #include "m3_launch.h"
 #include "qk_norm.h"
+#include "rope_freq.h"
 
 namespace {
 
@@ -271,10 +272,7 @@ m3::QkNormArgs qk_args(const m3_qk_dims* d) {
   a.ldk = d->ld_k ? d->ld_k : wk;
   a.ld_dq = d->ld_dq ? d->ld_dq : wq;
   a.ld_dk = d->ld_dk ? d->ld_dk : wk;
-  // by products: 128 of them are off by 2^-46, far below the phase's fp32
-  const double next = a.rot ? pow(d->base, -2.0 / a.rot) : 0.0;
-  double f = 0.15915494309189533577;   // 1 / (2 pi)
-  for (int j = 0; j < a.rot / 2; ++j, f *= next) a.freq[j] = f;
+  m3::rope_freq(d->base, a.rot, a.freq);
   return a;
 }
 

@@ -128,3 +128,10 @@ def test_gradient_against_differences():
         up.view(-1)[e] += h
         dn.view(-1)[e] -= h
         assert abs((loss(up) - loss(dn)) / (2 * h) - float(d["q"].view(-1)[e])) <= 4e-3
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("half", [False, True])
+def test_far_positions_of_many_pairs(half, dtype):
+    """All 128 pairs of the widest head, at positions up to the ends of an int."""
+    test_norm_rotation_and_gradients((65, 2, 1, 256, 256, half, 2147483647, False), dtype)

@@ -339,3 +339,36 @@ def test_attention_takes_what_its_launches_hold():
         assert back(**k) >= 8 * rows, k
     # 2^24 workgroups of 256 threads are more than a launch counts
     assert size(tokens_q=1 << 27, nheads_q=16) == 0 and back(tokens_k=1 << 27, nheads_q=16) == 0
+
+
+FREQ_CPP = """
+#include "rope_freq.h"
+extern "C" void table(double base, int rot, double* f) { m3::rope_freq(base, rot, f); }
+"""
+
+
+@pytest.mark.parametrize("rot", [2, 18, 32, 64, 128, 256])
+def test_rotary_frequencies(rot, tmp_path):
+    """Turns a position, base^(-2 j / rot) / (2 pi), against 50 digits.  In half
+    steps of fp64: 1 / (2 pi) one, two powers two each (one step of the math
+    library), two products one each, and an exponent off by one turns the power
+    by its logarithm, y = (2 j / rot) |ln base|."""
+    import subprocess
+    from decimal import Decimal, localcontext
+    src, out = tmp_path / "t.cpp", tmp_path / "t.so"
+    src.write_text(FREQ_CPP)
+    csrc = os.path.join(os.path.dirname(m3.LIB_PATH), "csrc")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-I", csrc, str(src), "-o", str(out)], check=True)
+    lib = ctypes.CDLL(str(out))
+    lib.table.argtypes = [ctypes.c_double, ctypes.c_int, ctypes.c_void_p]
+    for base in (0.5, 1.0, 100.0, 1e4, 5e5, 1e6):
+        f = (ctypes.c_double * 128)()
+        lib.table(base, rot, f)
+        with localcontext() as c:
+            c.prec = 60
+            two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+            for j in range(rot // 2):
+                y = Decimal(2 * j) / Decimal(rot) * Decimal(base).ln()
+                want = (-y).exp() / two_pi
+                err = abs(Decimal(f[j]) - want) / want * 2 ** 53
+                assert err <= 7 + abs(y), (base, rot, j, float(err))

@@ -39,6 +39,15 @@ inline int attn_log_pack(int Hq, int Hk) {
   while (lp < 5 && (Hq / Hk) % (2 << lp) == 0) ++lp;
   return lp;
 }
+// Workgroups of a launch over queries: 128 pairs each, in as many slots as hold any
+// split of Tq rows into S sequences.
+inline int64_t attn_query_workgroups(int Tq, int S, int Hq, int Hk) {
+  const int lp = attn_log_pack(Hq, Hk);
+  return ((static_cast<int64_t>(Tq) >> (7 - lp)) + S) * (Hq >> lp);
+}
+// Up to so many of them are taken in the order of their work, by up to so many
+// sequences.
+constexpr int kRankedWorkgroups = 2048, kRankedSeqs = 64;
 bool attn_supported(int D);
 size_t attn_backward_workspace_bytes(int Tq, int Tk, int S, int Hq, int Hk, int D);
 size_t attn_decode_workspace_bytes(int S, int cap, int Hq, int Hk, int D);

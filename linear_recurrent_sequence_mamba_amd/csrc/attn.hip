@@ -543,8 +543,8 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 
 template <typename T, int D>
 hipError_t run_attn(const AttnArgs& a, hipStream_t s) {
-  const int64_t slots = (a.Tq >> (7 - a.lp)) + a.S;
-  const dim3 grid(static_cast<unsigned>(slots * (a.Hq >> a.lp)), static_cast<unsigned>(a.nsplit));
+  const dim3 grid(static_cast<unsigned>(attn_query_workgroups(a.Tq, a.S, a.Hq, a.Hk)),
+                  static_cast<unsigned>(a.nsplit));
   if (a.nsplit == 1) {
     k_attn<T, D, 4, false><<<grid, 256, 0, s>>>(a);
     return hipGetLastError();
@@ -564,8 +564,7 @@ hipError_t run_attn(const AttnArgs& a, hipStream_t s) {
 // and 41, as the parts of so many rows have to be joined.  fp32, 2 of 1400, 64
 // heads of 64 on 8: 98, 55 with 512 keys, 30 with 256.
 int prompt_parts(int Tq, int Tk, int S, int Hq, int Hk, int bf16) {
-  const int lp = attn_log_pack(Hq, Hk);
-  const int64_t blocks = ((static_cast<int64_t>(Tq) >> (7 - lp)) + S) * (Hq >> lp);
+  const int64_t blocks = attn_query_workgroups(Tq, S, Hq, Hk);
   const int n = static_cast<int>(512 / blocks), most = Tk / S / (bf16 ? 512 : 256);
   if (n < 4 || most < 2) return 1;
   return n < most ? n : most;

@@ -443,7 +443,7 @@ template <typename T, int D>
 hipError_t run(const AttnArgs& a, hipStream_t s) {
   constexpr int W = 4, B = 32 * W;
   const int64_t nk = (static_cast<int64_t>(a.Tk) / B + a.S) * a.Hk * a.gsplit;
-  const int64_t nq = (static_cast<int64_t>(a.Tq >> (7 - a.lp)) + a.S) * (a.Hq >> a.lp);
+  const int64_t nq = attn_query_workgroups(a.Tq, a.S, a.Hq, a.Hk);
   k_attn_dq<T, D, W><<<static_cast<unsigned>(nq), 64 * W, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

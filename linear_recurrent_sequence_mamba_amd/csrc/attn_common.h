@@ -344,11 +344,11 @@ struct Ranked {
 // sequences, 16 heads of 128: 131 -> 122 us; 4 of 2048: 97 -> 85; but 32 of 256:
 // 39 -> 43); with more of them several sequences' keys share the caches for
 // nothing (8 of 2048, 32 heads of 64: 200 us, ranked 215).
-__device__ __forceinline__ bool by_work(const AttnArgs& a) { return a.S > 1 && a.S <= 64; }
+__device__ __forceinline__ bool by_work(const AttnArgs& a) { return a.S > 1 && a.S <= kRankedSeqs; }
 
 // the n-th tile of 1 << lb queries to start, of nslot
 __device__ __forceinline__ Slot query_slot(const AttnArgs& a, int lb, int n, int nslot, int lane) {
-  if (!by_work(a) || gridDim.x > 2048) return slot_of(a.cuq, a.S, a.Tq, lb, nslot - 1 - n, lane);
+  if (!by_work(a) || gridDim.x > kRankedWorkgroups) return slot_of(a.cuq, a.S, a.Tq, lb, nslot - 1 - n, lane);
   Ranked r(a.cuq, a.S, a.Tq, lb, lane);
   if (lane < a.S) {   // tiles of keys before the first query's own
     const int lk = clamp_row(a.cuk[lane + 1], a.Tk) - clamp_row(a.cuk[lane], a.Tk);

@@ -71,11 +71,11 @@ def _many(n, seed):
     return nq, [a + b for a, b in zip(nq, more)]
 
 
-# groups of 32 and 12 heads; more sequences than a wave has lanes; more workgroups than are taken in the
-# order of their work; sequences of several tiles whose order that changes
 # few queries of many keys, whose keys are split over workgroups
 CASES += [([2], [3000], 16, 2, 64), ([1, 5, 0, 9], [2600, 1500, 0, 700], 4, 2, 128),
           ([90, 70], [1100, 1300], 3, 3, 64)]
+# groups of 32 and 12 heads; more sequences than a wave has lanes; as many; sequences of several tiles that are
+# taken in the order of their work
 CASES += [([5, 40, 3], [9, 40, 70], 32, 1, 64), ([9, 70], [9, 200], 24, 2, 128),
           (*_many(70, 1), 4, 2, 64), (*_many(64, 2), 40, 4, 64), (*_many(64, 3), 3, 1, 128),
           ([130, 400, 0, 257], [600, 400, 9, 300], 4, 2, 64), ([129, 300, 20], [129, 300, 700], 2, 2, 128)]
@@ -458,3 +458,16 @@ def test_keys_of_more_than_2_to_34_elements():
     for t in g[1:]:
         assert not t[:5000].any() and not t[n0 - 5000:n0].any()
     _of_sequence(q, k, v, do, o, lse, g, slice(0, 70), slice(n0, n0 + L), BF16)
+
+
+# 64 sequences of 40 heads: more workgroups than are taken in the order of their
+# work (counted in test_layers_host.py)
+MANY_Q, MANY_K = _many(60, 2)
+MANY_Q, MANY_K = [300, 0, 257, 130] + MANY_Q, [400, 3, 257, 100] + MANY_K
+MANY_HEADS = 40, [40, 8]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("Hk", MANY_HEADS[1])
+def test_few_sequences_in_more_workgroups_than_are_ranked(Hk, dtype):
+    test_prompt_and_gradients((MANY_Q, MANY_K, MANY_HEADS[0], Hk, 64), dtype)

@@ -372,3 +372,32 @@ def test_rotary_frequencies(rot, tmp_path):
                 want = (-y).exp() / two_pi
                 err = abs(Decimal(f[j]) - want) / want * 2 ** 53
                 assert err <= 7 + abs(y), (base, rot, j, float(err))
+
+
+GRID_CPP = """
+#include "attn.h"
+extern "C" long long workgroups(int Tq, int S, int Hq, int Hk) { return m3::attn_query_workgroups(Tq, S, Hq, Hk); }
+extern "C" int ranked(int seqs) { return seqs ? m3::kRankedSeqs : m3::kRankedWorkgroups; }
+"""
+
+
+def test_attention_cases_reach_both_orders_of_work(tmp_path):
+    """Tiles of queries are taken by work up to a number of workgroups and by a
+    search beyond: the GPU tests have several sequences on both sides."""
+    import subprocess
+    from tests import test_gpu_attn as t
+    src, out = tmp_path / "t.cpp", tmp_path / "t.so"
+    src.write_text(GRID_CPP)
+    csrc = os.path.join(os.path.dirname(m3.LIB_PATH), "csrc")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-D__HIP_PLATFORM_AMD__", "-I", csrc, "-I",
+                    "/opt/rocm/include", str(src), "-o", str(out)], check=True)
+    lib = ctypes.CDLL(str(out))
+    lib.workgroups.restype = ctypes.c_longlong
+    assert lib.workgroups(16384, 5, 32, 8) == (16384 // 32 + 5) * 8 and lib.workgroups(1, 1, 3, 1) == 3
+    seqs, most = lib.ranked(1), lib.ranked(0)
+    for Hk in t.MANY_HEADS[1]:
+        assert 1 < len(t.MANY_Q) <= seqs
+        assert lib.workgroups(sum(t.MANY_Q) + 3, len(t.MANY_Q), t.MANY_HEADS[0], Hk) > most
+    by_work = [c for c in t.CASES if 1 < len(c[0]) <= seqs and max(c[0]) > 128 and
+               lib.workgroups(sum(c[0]) + 3, len(c[0]), c[2], c[3]) <= most]
+    assert len(by_work) >= 3

@@ -7,9 +7,10 @@
   catch what it is for.
 * The C ABI layer (api.cpp: argument checks, workspace sizing) is rebuilt
   with clang's ASan + UBSan for the host side only, linked with the kernel
-  objects of the normal build, and tests/test_abi.py (every error path of
-  every entry point; none of them launches a kernel) runs against it in a
-  child process that preloads clang's ASan runtime.
+  objects of the normal build, and tests/test_abi.py and
+  tests/test_layers_host.py (the error paths of the core's and of the other
+  layers' entry points; none of them launches a kernel) run against it in
+  child processes that preload clang's ASan runtime.
 
 Leak checking is off: the HIP runtime keeps allocations until exit."""
 import glob
@@ -126,3 +127,40 @@ sys.exit(pytest.main([{os.path.join(ROOT, 'tests', 'test_abi.py')!r}, "-q", "-s"
 """
     r = _run(code, _clang_asan(hipcc))
     assert r.returncode == 0, (r.stdout[-2000:], r.stderr[-3000:])
+
+
+def _sanitized_abi(folder):
+    """(library with an instrumented api.cpp, clang's ASan runtime)"""
+    from linear_recurrent_sequence_mamba_amd import build as libbuild
+    hipcc = _hipcc()
+    kernels = [os.path.join(libbuild.OUT_DIR, s + ".o") for s in libbuild.SOURCES if s.endswith(".hip")]
+    if not all(os.path.exists(k) for k in kernels):
+        libbuild.build()
+    host = [f for x in ("-fsanitize=address", "-fsanitize=undefined", "-fno-sanitize-recover=undefined",
+                        "-fno-omit-frame-pointer") for f in ("-Xarch_host", x)]
+    obj, lib = str(folder / "api_san.o"), str(folder / "libm3ssm_san.so")
+    arch = f"--offload-arch={libbuild.ARCH}"
+    for cmd in ([hipcc, "-x", "hip", arch, "-O1", "-g", "-fPIC", "-std=c++17", *host, "-c",
+                 os.path.join(libbuild.CSRC, "api.cpp"), "-o", obj],
+                [hipcc, arch, "-shared", "-fPIC", "-shared-libsan", *host, obj, *kernels, "-o", lib]):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr[-3000:]
+    return lib, _clang_asan(hipcc)
+
+
+def test_layer_refusals_under_asan_ubsan(tmp_path):
+    """The refusals, sizes and counts near the end of an int of the gated
+    recurrence, the q/k norms and attention (the tests that use the library)."""
+    lib, runtime = _sanitized_abi(tmp_path)
+    code = f"""
+import sys
+sys.path.insert(0, {ROOT!r})
+from linear_recurrent_sequence_mamba_amd import binding as m3
+m3.LIB_PATH = {lib!r}
+import pytest
+sys.exit(pytest.main([{os.path.join(ROOT, 'tests', 'test_layers_host.py')!r}, "-q", "-s", "-p", "no:cacheprovider",
+                      "-k", "refus or struct or counts or large_batches or takes_what or exports"]))
+"""
+    r = _run(code, runtime)
+    assert r.returncode == 0, (r.stdout[-2000:], r.stderr[-3000:])
+    assert " passed" in r.stdout and int(r.stdout.split(" passed")[0].split()[-1]) >= 10, r.stdout[-500:]

@@ -384,15 +384,18 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) * D == 512 ? 1 : 2) void k_at
 // tile's columns.  A workgroup takes a part of one sequence's cache, its
 // waves every WAVES-th tile of 32 keys each, without barriers; the waves'
 // sums are joined in LDS and the parts by k_attn_join.  Bound by reading the
-// cache: 65536 keys of 16 heads of 64 in 50 us when called again and again (5.4
-// TB/s: the last-level cache holds part of it), the join 4.5 us.
+// cache: 65536 keys of 16 heads of 64 in 49 us when called again and again (5.5
+// TB/s: the last-level cache holds part of it), the join 4.6 us; 32 caches of 4096,
+// 8 heads of 128, in a graph over 16 different ones 112 us (4.8 TB/s), in fp32
+// 244 us (4.4), of 64 65 us (4.2) and 113 us (4.8).
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_attn_decode(AttnArgs a) {
   using L = Tile<T, D>;
   // A wave's tile (32 rows of K, 32 of V); afterwards its o [32][D] in fp32.  One
   // buffer, as the other waves' loads fill the time (32 caches of 4096, 8 heads,
   // in fp32: 244 us at D = 128, 110 at 64; with two buffers half as many waves
-  // fit, 402 and 145 us; in bf16 the same within 3%).
+  // fit, 402 and 145 us; in bf16 the same within 3%).  Resident are two workgroups
+  // a CU at D = 64 and, with 348 registers and more, one at D = 128.
   constexpr int BN = 32;
   __shared__ __align__(16) char sKV[WAVES][L::BYTES];
   __shared__ float sM[WAVES][32], sL[WAVES][32];
@@ -581,8 +584,8 @@ hipError_t run_decode(const AttnArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Parts of a cache: enough workgroups for the chip (two a CU), each with 512
-// keys at the least, four tiles of 32 for each of four waves.
+// Parts of a cache: two workgroups for every CU (at D = 128 they follow each other),
+// each with 512 keys at the least, four tiles of 32 for each of four waves.
 int decode_parts(int S, int cap, int Hq, int Hk) {
   const int64_t blocks = static_cast<int64_t>(S) * Hk * ((Hq / Hk + 31) / 32);
   int64_t n = (512 + blocks - 1) / blocks;

@@ -466,6 +466,46 @@ m3_status m3_attn_decode(const m3_attn_dims* dims, const int32_t* lengths, const
                          const void* k, const void* v, void* o, float* lse, void* ws,
                          size_t ws_bytes, void* stream);
 
+/* The norms before and after a block, fused with its gate and residual scale:
+ *     z = y / sqrt(mean(y^2) + eps) * y_weight   (M3_BLOCK_RAW: y * y_weight),
+ *     h = x + scale * act(gate) * z,
+ *     n = h / sqrt(mean(h^2) + eps) * n_weight,
+ * with x the residual stream, y what the block gave, h the stream after it and
+ * n what the next block reads, from h before its rounding.  flags:
+ * M3_GATE_SIGMOID or M3_GATE_SILU, the gate's activation (neither: the gate as
+ * it is), and M3_BLOCK_RAW. */
+#define M3_GATE_SIGMOID (1u << 0)
+#define M3_GATE_SILU (1u << 1)
+#define M3_BLOCK_RAW (1u << 2)
+typedef struct {
+  int32_t tokens; /* T >= 1 rows                                           */
+  int32_t width;  /* W, 1 .. 16384, any                                    */
+  int32_t dtype;  /* m3_dtype of rows and their gradients                  */
+  uint32_t flags;
+  float eps;      /* finite, >= 0 (a row whose mean square and eps are
+                     together below 2^-126 has no finite norm)             */
+  int64_t ld_x, ld_y, ld_gate; /* >= W or 0                                */
+} m3_block_dims;
+
+/* x, y, gate (NULL: 1) [T, W] to h and n (NULL: not written) [T, W], dense.
+ * y_weight, scale, n_weight [W] fp32 or NULL (1).  With dense rows h may be x
+ * or y.  Widths and distances that are multiples of 8 are read 8 elements at a
+ * time. */
+m3_status m3_block_norm(const m3_block_dims* dims, const void* x, const void* y, const void* gate,
+                        const float* y_weight, const float* scale, const float* n_weight, void* h,
+                        void* n, void* stream);
+
+size_t m3_block_norm_backward_workspace_size(const m3_block_dims* dims);
+
+/* Gradients from dh and dn (dense; one of them may be NULL, which is 0): dx, dy
+ * and, if gate is given, dgate in dtype, dense; dy_weight, dscale, dn_weight [W]
+ * fp32 (NULL: not written), summed in a fixed order. */
+m3_status m3_block_norm_backward(const m3_block_dims* dims, const void* x, const void* y,
+                                 const void* gate, const float* y_weight, const float* scale,
+                                 const float* n_weight, const void* dh, const void* dn, void* dx,
+                                 void* dy, void* dgate, float* dy_weight, float* dscale,
+                                 float* dn_weight, void* ws, size_t ws_bytes, void* stream);
+
 /* Static, human-readable name of a status. */
 const char* m3_status_str(m3_status status);
 

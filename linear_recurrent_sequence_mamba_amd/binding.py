@@ -24,6 +24,7 @@ M3_THETA_IS_ANGLE = 1 << 0
 M3_A_PER_TOKEN = 1 << 1
 M3_ROPE_HALF = 1 << 0
 M3_GATED_CHUNK = 128
+M3_GATE_SIGMOID, M3_GATE_SILU, M3_BLOCK_RAW = 1 << 0, 1 << 1, 1 << 2
 
 STATUS = {0: "M3_OK", 1: "M3_ERR_NULL", 2: "M3_ERR_SHAPE", 3: "M3_ERR_DTYPE",
           4: "M3_ERR_UNSUPPORTED", 5: "M3_ERR_ALIGN", 6: "M3_ERR_WORKSPACE", 7: "M3_ERR_HIP",
@@ -65,6 +66,12 @@ class m3_qk_dims(ctypes.Structure):
                 ("flags", ctypes.c_uint32), ("eps", ctypes.c_float), ("base", ctypes.c_double),
                 ("ld_q", ctypes.c_int64), ("ld_k", ctypes.c_int64), ("ld_dq", ctypes.c_int64),
                 ("ld_dk", ctypes.c_int64)]
+
+
+class m3_block_dims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("eps", ctypes.c_float),
+                ("ld_x", ctypes.c_int64), ("ld_y", ctypes.c_int64), ("ld_gate", ctypes.c_int64)]
 
 
 class m3_attn_dims(ctypes.Structure):
@@ -156,10 +163,12 @@ def _lib():
         lib.m3_decode_tokens.argtypes = [dp] + [vp] * 11 + [vp]
         gp, qp, ap, i32 = (ctypes.POINTER(m3_gated_dims), ctypes.POINTER(m3_qk_dims),
                            ctypes.POINTER(m3_attn_dims), ctypes.c_int)
+        bp = ctypes.POINTER(m3_block_dims)
         for name, args in (
                 ("m3_gated_scan_workspace_size", [gp, i32]),
                 ("m3_gated_scan_backward_workspace_size", [gp, i32]),
                 ("m3_qk_norm_rope_backward_workspace_size", [qp]),
+                ("m3_block_norm_backward_workspace_size", [bp]),
                 ("m3_attn_prefill_varlen_workspace_size", [ap]),
                 ("m3_attn_prefill_varlen_backward_workspace_size", [ap]),
                 ("m3_attn_decode_workspace_size", [ap])):
@@ -171,6 +180,8 @@ def _lib():
                 ("m3_gated_step", [gp] + [vp] * 7),
                 ("m3_qk_norm_rope", [qp] + [vp] * 8),
                 ("m3_qk_norm_rope_backward", [qp] + [vp] * 12 + [sz, vp]),
+                ("m3_block_norm", [bp] + [vp] * 9),
+                ("m3_block_norm_backward", [bp] + [vp] * 15 + [sz, vp]),
                 ("m3_attn_prefill_varlen", [ap] + [vp] * 8 + [sz, vp]),
                 ("m3_attn_prefill_varlen_backward", [ap] + [vp] * 12 + [sz, vp]),
                 ("m3_attn_decode", [ap] + [vp] * 7 + [sz, vp])):
@@ -971,3 +982,58 @@ def attn_decode(q, k_cache, v_cache, lengths, scale=None, o=None, ws=None, strea
     if e != 0:
         raise M3Error(e, "m3_attn_decode")
     return o, lse
+
+
+def _block_setup(x, y, gate, y_weight, scale, n_weight, eps, flags):
+    if x.dim() != 2:
+        raise ValueError("x must be [T, W]")
+    T, W = x.shape
+    code = dtype_code(x.dtype)
+    lds = [_rows("x", x, x.shape, x.dtype), _rows("y", y, x.shape, x.dtype),
+           0 if gate is None else _rows("gate", gate, x.shape, x.dtype)]
+    for n, t in (("y_weight", y_weight), ("scale", scale), ("n_weight", n_weight)):
+        _dense(n, t, (W,), torch.float32, optional=True)
+    return _dims(m3_block_dims, T, W, code, flags, eps, *lds)[1]
+
+
+def block_norm(x, y, gate=None, y_weight=None, scale=None, n_weight=None, eps=1e-6, flags=0,
+               want_n=True, stream=None):
+    """A block's output y [T, W] normed, gated, scaled and added to the
+    residual stream x, and the stream normed for the next block
+    (m3_block_norm).  Returns (h, n)."""
+    dev = _same_device("x y gate y_weight scale n_weight", x, y, gate, y_weight, scale, n_weight)
+    ref = _block_setup(x, y, gate, y_weight, scale, n_weight, eps, flags)
+    with _on(dev, stream):
+        h = x.new_empty(x.shape)
+        n = x.new_empty(x.shape) if want_n else None
+        e = _lib().m3_block_norm(ref, _addr(x), _addr(y), _addr(gate), _addr(y_weight),
+                                 _addr(scale), _addr(n_weight), _addr(h), _addr(n), _raw(dev))
+    if e != 0:
+        raise M3Error(e, "m3_block_norm")
+    return h, n
+
+
+def block_norm_backward(x, y, dh, dn, gate=None, y_weight=None, scale=None, n_weight=None,
+                        eps=1e-6, flags=0, stream=None) -> dict:
+    """Gradients of block_norm for dh and dn (one of them may be None): a dict
+    with x, y and gate in their dtype and, for those that are given, y_weight,
+    scale and n_weight in fp32."""
+    dev = _same_device("x y dh dn gate y_weight scale n_weight", x, y, dh, dn, gate, y_weight,
+                       scale, n_weight)
+    ref = _block_setup(x, y, gate, y_weight, scale, n_weight, eps, flags)
+    _dense("dh", dh, x.shape, x.dtype, optional=True)
+    _dense("dn", dn, x.shape, x.dtype, optional=True)
+    lib = _lib()
+    with _on(dev, stream):
+        g = {n: None if t is None else t.new_empty(t.shape) for n, t in
+             (("x", x), ("y", y), ("gate", gate), ("y_weight", y_weight), ("scale", scale),
+              ("n_weight", n_weight))}
+        ws = _ws(lib.m3_block_norm_backward_workspace_size(ref), "m3_block_norm_backward", x)
+        e = lib.m3_block_norm_backward(
+            ref, _addr(x), _addr(y), _addr(gate), _addr(y_weight), _addr(scale), _addr(n_weight),
+            _addr(dh), _addr(dn), _addr(g["x"]), _addr(g["y"]), _addr(g["gate"]),
+            _addr(g["y_weight"]), _addr(g["scale"]), _addr(g["n_weight"]), _addr(ws), ws.numel(),
+            _raw(dev))
+    if e != 0:
+        raise M3Error(e, "m3_block_norm_backward")
+    return g

@@ -10,6 +10,7 @@
 
 #include "../../include/m3ssm.h"
 #include "attn.h"
+#include "block_norm.h"
 #include "gated.h"
 #include "m3_launch.h"
 #include "qk_norm.h"
@@ -273,6 +274,35 @@ m3::QkNormArgs qk_args(const m3_qk_dims* d) {
   a.ld_dq = d->ld_dq ? d->ld_dq : wq;
   a.ld_dk = d->ld_dk ? d->ld_dk : wk;
   m3::rope_freq(d->base, a.rot, a.freq);
+  return a;
+}
+
+m3_status check_block(const m3_block_dims* d) {
+  if (!d) return M3_ERR_NULL;
+  if (d->tokens <= 0 || d->width <= 0 || d->tokens > kMostRows) return M3_ERR_SHAPE;
+  if (d->flags & ~(M3_GATE_SIGMOID | M3_GATE_SILU | M3_BLOCK_RAW)) return M3_ERR_SHAPE;
+  if ((d->flags & M3_GATE_SIGMOID) && (d->flags & M3_GATE_SILU)) return M3_ERR_SHAPE;
+  if (!isfinite(d->eps) || d->eps < 0.0f) return M3_ERR_SHAPE;
+  const int64_t lds[] = {d->ld_x, d->ld_y, d->ld_gate};
+  for (int64_t ld : lds)
+    if (ld != 0 && ld < d->width) return M3_ERR_SHAPE;
+  if (bad_dtype(d->dtype)) return M3_ERR_DTYPE;
+  if (d->width > m3::kBlockNormMaxWidth) return M3_ERR_UNSUPPORTED;
+  return M3_OK;
+}
+
+m3::BlockNormArgs block_args(const m3_block_dims* d) {
+  m3::BlockNormArgs a{};
+  a.T = d->tokens;
+  a.W = d->width;
+  a.act = d->flags & M3_GATE_SILU      ? m3::kGateSilu
+          : d->flags & M3_GATE_SIGMOID ? m3::kGateSigmoid
+                                       : m3::kGateLinear;
+  a.raw = (d->flags & M3_BLOCK_RAW) != 0;
+  a.eps = d->eps;
+  a.ldx = d->ld_x ? d->ld_x : d->width;
+  a.ldy = d->ld_y ? d->ld_y : d->width;
+  a.ldg = d->ld_gate ? d->ld_gate : d->width;
   return a;
 }
 
@@ -852,6 +882,63 @@ m3_status m3_attn_decode(const m3_attn_dims* d, const int32_t* lengths, const vo
   a.o = o;
   a.lse = lse;
   return hip_status(m3::launch_attn_decode(a, d->dtype == M3_BF16, ws, static_cast<hipStream_t>(stream)));
+}
+
+m3_status m3_block_norm(const m3_block_dims* d, const void* x, const void* y, const void* gate,
+                        const float* y_weight, const float* scale, const float* n_weight, void* h,
+                        void* n, void* stream) {
+  m3_status st = check_block(d);
+  if (st != M3_OK) return st;
+  if (!x || !y || !h) return M3_ERR_NULL;
+  const void* const ptrs[] = {x, y, gate, y_weight, scale, n_weight, h, n};
+  if (any_misaligned(ptrs)) return M3_ERR_ALIGN;
+  m3::BlockNormArgs a = block_args(d);
+  a.x = x;
+  a.y = y;
+  a.gate = gate;
+  a.wy = y_weight;
+  a.scale = scale;
+  a.wn = n_weight;
+  a.h = h;
+  a.n = n;
+  return hip_status(m3::launch_block_norm(a, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
+}
+
+size_t m3_block_norm_backward_workspace_size(const m3_block_dims* d) {
+  if (check_block(d) != M3_OK) return 0;
+  return m3::block_norm_workspace_bytes(d->tokens, d->width);
+}
+
+m3_status m3_block_norm_backward(const m3_block_dims* d, const void* x, const void* y,
+                                 const void* gate, const float* y_weight, const float* scale,
+                                 const float* n_weight, const void* dh, const void* dn, void* dx,
+                                 void* dy, void* dgate, float* dy_weight, float* dscale,
+                                 float* dn_weight, void* ws, size_t ws_bytes, void* stream) {
+  m3_status st = check_block(d);
+  if (st != M3_OK) return st;
+  if (!x || !y || (!dh && !dn) || !dx || !dy || (gate && !dgate)) return M3_ERR_NULL;
+  const void* const ptrs[] = {x,  y,  gate,  y_weight,  scale,  n_weight,  dh, dn,
+                              dx, dy, dgate, dy_weight, dscale, dn_weight, ws};
+  if (any_misaligned(ptrs)) return M3_ERR_ALIGN;
+  if (!ws || ws_bytes < m3::block_norm_workspace_bytes(d->tokens, d->width)) return M3_ERR_WORKSPACE;
+  m3::BlockNormArgs a = block_args(d);
+  a.x = x;
+  a.y = y;
+  a.gate = gate;
+  a.wy = y_weight;
+  a.scale = scale;
+  a.wn = n_weight;
+  a.dh = dh;
+  a.dn = dn;
+  a.dx = dx;
+  a.dy = dy;
+  a.dgate = dgate;
+  a.dwy = dy_weight;
+  a.dscale = dscale;
+  a.dwn = dn_weight;
+  a.part = static_cast<float*>(ws);
+  return hip_status(
+      m3::launch_block_norm_backward(a, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

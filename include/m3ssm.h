@@ -466,6 +466,66 @@ m3_status m3_attn_decode(const m3_attn_dims* dims, const int32_t* lengths, const
                          const void* k, const void* v, void* o, float* lse, void* ws,
                          size_t ws_bytes, void* stream);
 
+/* The gated delta rule, one state S [Dk, Dv] per value head:
+ *     S' = exp(g_t) S_{t-1},   u_t = beta_t (v_t - S'^T k_t),
+ *     S_t = S' + k_t u_t^T,    o_t = scale S_t^T q_t.
+ * Value head h reads head h / (Hv / Hk) of q and k.  g is the logarithm of the
+ * decay (meant to be <= 0, not checked; below -128 it counts as -128, a decay
+ * that is 0 in fp32) and beta the strength of the write, both activated.  Keys
+ * are used as they are: of length 1 (m3_qk_norm_rope without rotation and with
+ * weights Dk^-1/2 makes them so) they keep the recurrence stable for beta up
+ * to 2.  States are fp32 and kept to fp32's accuracy: bf16 inputs enter the
+ * matrix cores exactly, computed operands and fp32 inputs as sums of up to
+ * three bf16 parts (so an infinity may come out as NaN). */
+typedef struct {
+  int32_t batch;     /* Bsz, or S sequences of a packed call, >= 1         */
+  int32_t seqlen;    /* T, or all rows of a packed call (ignored by the step) */
+  int32_t nheads_k;  /* Hk >= 1                                            */
+  int32_t nheads_v;  /* Hv, a multiple of Hk                               */
+  int32_t headdim_k; /* Dk: 64 or 128                                      */
+  int32_t headdim_v; /* Dv: 64 or 128                                      */
+  int32_t dtype;     /* m3_dtype of q, k, v, g, beta, o and gradients      */
+  float scale;       /* of the outputs; finite                             */
+  int64_t ld_q, ld_k, ld_v;  /* >= H D, < 2^24, multiples of 8, or 0; a dense
+                                call's sequences follow each other T rows apart */
+  int64_t ld_g, ld_beta;     /* >= Hv, < 2^24, or 0                        */
+} m3_delta_dims;
+
+/* tokens between the states that m3_delta_scan saves for the backward pass */
+#define M3_DELTA_CHUNK 64
+
+/* Bytes of device workspace (packed: nonzero for calls with cu_seqlens); 0 if
+ * dims is invalid. */
+size_t m3_delta_scan_workspace_size(const m3_delta_dims* dims, int packed);
+
+/* The scan over q, k [Bsz, T, Hk, Dk], v [Bsz, T, Hv, Dv], g, beta
+ * [Bsz, T, Hv] (cu_seqlens NULL) or, packed, the same without Bsz:
+ *   o       as v, dense
+ *   hT      [Bsz, Hv, Dk, Dv] fp32, the state after the last token (NULL: not
+ *           written)
+ *   states  the state before every chunk of M3_DELTA_CHUNK tokens, for the
+ *           backward pass (NULL: not written): [slots, Hv, Dk, Dv] fp32 with
+ *           slots = Bsz ceil(T / M3_DELTA_CHUNK), of a packed call
+ *           floor(T / M3_DELTA_CHUNK) + S, of which those that no chunk takes
+ *           are left as they are
+ * h0 [Bsz, Hv, Dk, Dv] fp32 or NULL (zero), may alias hT.  An empty sequence's
+ * hT is its h0.  Packed offsets are clamped into [0, T], so no access leaves
+ * the buffers whatever they hold; they are meant to rise, and the rows of a
+ * batch whose offsets do not are unspecified.  Rows that no sequence covers
+ * are left as they are.  A NaN or Inf stays in its sequence and heads, and may
+ * reach all outputs from its chunk on.  g and beta need only their elements'
+ * alignment. */
+m3_status m3_delta_scan(const m3_delta_dims* dims, const int32_t* cu_seqlens, const void* q,
+                        const void* k, const void* v, const void* g, const void* beta,
+                        const float* h0, void* o, float* hT, float* states, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* One token per sequence: h [Bsz, Hv, Dk, Dv] fp32 advances in place by q, k
+ * [Bsz, Hk, Dk], v [Bsz, Hv, Dv], g, beta [Bsz, Hv]; o [Bsz, Hv, Dv].
+ * dims->seqlen is ignored. */
+m3_status m3_delta_step(const m3_delta_dims* dims, float* h, const void* q, const void* k,
+                        const void* v, const void* g, const void* beta, void* o, void* stream);
+
 /* The norms before and after a block, fused with its gate and residual scale:
  *     z = y / sqrt(mean(y^2) + eps) * y_weight   (M3_BLOCK_RAW: y * y_weight),
  *     h = x + scale * act(gate) * z,

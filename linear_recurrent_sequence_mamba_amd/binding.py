@@ -24,6 +24,7 @@ M3_THETA_IS_ANGLE = 1 << 0
 M3_A_PER_TOKEN = 1 << 1
 M3_ROPE_HALF = 1 << 0
 M3_GATED_CHUNK = 128
+M3_DELTA_CHUNK = 64
 M3_GATE_SIGMOID, M3_GATE_SILU, M3_BLOCK_RAW = 1 << 0, 1 << 1, 1 << 2
 
 STATUS = {0: "M3_OK", 1: "M3_ERR_NULL", 2: "M3_ERR_SHAPE", 3: "M3_ERR_DTYPE",
@@ -66,6 +67,15 @@ class m3_qk_dims(ctypes.Structure):
                 ("flags", ctypes.c_uint32), ("eps", ctypes.c_float), ("base", ctypes.c_double),
                 ("ld_q", ctypes.c_int64), ("ld_k", ctypes.c_int64), ("ld_dq", ctypes.c_int64),
                 ("ld_dk", ctypes.c_int64)]
+
+
+class m3_delta_dims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("seqlen", ctypes.c_int32),
+                ("nheads_k", ctypes.c_int32), ("nheads_v", ctypes.c_int32),
+                ("headdim_k", ctypes.c_int32), ("headdim_v", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("ld_q", ctypes.c_int64),
+                ("ld_k", ctypes.c_int64), ("ld_v", ctypes.c_int64), ("ld_g", ctypes.c_int64),
+                ("ld_beta", ctypes.c_int64)]
 
 
 class m3_block_dims(ctypes.Structure):
@@ -163,11 +173,12 @@ def _lib():
         lib.m3_decode_tokens.argtypes = [dp] + [vp] * 11 + [vp]
         gp, qp, ap, i32 = (ctypes.POINTER(m3_gated_dims), ctypes.POINTER(m3_qk_dims),
                            ctypes.POINTER(m3_attn_dims), ctypes.c_int)
-        bp = ctypes.POINTER(m3_block_dims)
+        bp, ep = ctypes.POINTER(m3_block_dims), ctypes.POINTER(m3_delta_dims)
         for name, args in (
                 ("m3_gated_scan_workspace_size", [gp, i32]),
                 ("m3_gated_scan_backward_workspace_size", [gp, i32]),
                 ("m3_qk_norm_rope_backward_workspace_size", [qp]),
+                ("m3_delta_scan_workspace_size", [ep, i32]),
                 ("m3_block_norm_backward_workspace_size", [bp]),
                 ("m3_attn_prefill_varlen_workspace_size", [ap]),
                 ("m3_attn_prefill_varlen_backward_workspace_size", [ap]),
@@ -180,6 +191,8 @@ def _lib():
                 ("m3_gated_step", [gp] + [vp] * 7),
                 ("m3_qk_norm_rope", [qp] + [vp] * 8),
                 ("m3_qk_norm_rope_backward", [qp] + [vp] * 12 + [sz, vp]),
+                ("m3_delta_scan", [ep] + [vp] * 11 + [sz, vp]),
+                ("m3_delta_step", [ep] + [vp] * 8),
                 ("m3_block_norm", [bp] + [vp] * 9),
                 ("m3_block_norm_backward", [bp] + [vp] * 15 + [sz, vp]),
                 ("m3_attn_prefill_varlen", [ap] + [vp] * 8 + [sz, vp]),
@@ -982,6 +995,94 @@ def attn_decode(q, k_cache, v_cache, lengths, scale=None, o=None, ws=None, strea
     if e != 0:
         raise M3Error(e, "m3_attn_decode")
     return o, lse
+
+
+def _flat(name, t, dims):
+    """A dense call's [Bsz, T, ...] as token rows."""
+    if t is None or t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} axes")
+    try:
+        return t.view(t.shape[0] * t.shape[1], *t.shape[2:])
+    except RuntimeError:
+        raise ValueError(f"{name}: sequences must follow each other without a gap") from None
+
+
+def _delta_setup(q, k, v, g, beta, scale, cu_seqlens):
+    """(dims, reference, packed, slots of chunks)"""
+    packed = cu_seqlens is not None
+    if packed:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must hold S + 1 offsets")
+        if q.dim() != 3 or v.dim() != 3:
+            raise ValueError("q, k and v must be [T, heads, headdim] with cu_seqlens")
+        B, T = cu_seqlens.numel() - 1, q.shape[0]
+        _dense("cu_seqlens", cu_seqlens, (B + 1,), torch.int32)
+        rows, slots = T, T // M3_DELTA_CHUNK + B
+    else:
+        if q.dim() != 4:
+            raise ValueError("q, k and v must be [Bsz, T, heads, headdim] without cu_seqlens")
+        B, T = q.shape[:2]
+        q, k, v = (_flat(n, t, 4) for n, t in (("q", q), ("k", k), ("v", v)))
+        g, beta = (_flat(n, t, 3) for n, t in (("g", g), ("beta", beta)))
+        rows, slots = B * T, B * ((T + M3_DELTA_CHUNK - 1) // M3_DELTA_CHUNK)
+    Hk, Dk = q.shape[1:]
+    Hv, Dv = v.shape[1:]
+    dt = q.dtype
+    d, ref = _dims(m3_delta_dims, B, T, Hk, Hv, Dk, Dv, dtype_code(dt),
+                   Dk ** -0.5 if scale is None else scale, _rows("q", q, (rows, Hk, Dk), dt),
+                   _rows("k", k, (rows, Hk, Dk), dt), _rows("v", v, (rows, Hv, Dv), dt),
+                   _rows("g", g, (rows, Hv), dt), _rows("beta", beta, (rows, Hv), dt))
+    return d, ref, packed, slots
+
+
+def delta_scan(q, k, v, g, beta, h0=None, scale=None, cu_seqlens=None, want_hT=True,
+               want_states=False, stream=None):
+    """The gated delta rule over q, k [Bsz, T, Hk, Dk], v [Bsz, T, Hv, Dv], g
+    and beta [Bsz, T, Hv], or packed without Bsz and with cu_seqlens
+    (m3_delta_scan; scale Dk^-1/2 by default).  Returns (o, hT, states);
+    states are for delta_scan_backward."""
+    dev = _same_device("q k v g beta h0 cu_seqlens", q, k, v, g, beta, h0, cu_seqlens)
+    d, ref, packed, slots = _delta_setup(q, k, v, g, beta, scale, cu_seqlens)
+    state = (d.batch, d.nheads_v, d.headdim_k, d.headdim_v)
+    _dense("h0", h0, state, torch.float32, optional=True)
+    lib = _lib()
+    with _on(dev, stream):
+        o = v.new_empty(v.shape)
+        hT = v.new_empty(state, dtype=torch.float32) if want_hT else None
+        st = v.new_empty((slots,) + state[1:], dtype=torch.float32) if want_states else None
+        ws = _ws(lib.m3_delta_scan_workspace_size(ref, packed), "m3_delta_scan", q)
+        e = lib.m3_delta_scan(ref, _addr(cu_seqlens), _addr(q), _addr(k), _addr(v), _addr(g),
+                              _addr(beta), _addr(h0), _addr(o), _addr(hT), _addr(st), _addr(ws),
+                              ws.numel(), _raw(dev))
+    if e != 0:
+        raise M3Error(e, "m3_delta_scan")
+    return o, hT, st
+
+
+def delta_step(h, q, k, v, g, beta, scale=None, o=None, stream=None):
+    """Advances h [Bsz, Hv, Dk, Dv] (fp32, in place) by one token of q, k
+    [Bsz, Hk, Dk], v [Bsz, Hv, Dv], g and beta [Bsz, Hv]; returns o (allocated
+    unless given)."""
+    dev = _same_device("h q k v g beta o", h, q, k, v, g, beta, o)
+    if h.dim() != 4 or q.dim() != 3:
+        raise ValueError("h must be [Bsz, Hv, Dk, Dv], q and k [Bsz, Hk, Dk]")
+    B, Hv, Dk, Dv = h.shape
+    Hk, dt = q.shape[1], q.dtype
+    _dense("h", h, h.shape, torch.float32)
+    _, ref = _dims(m3_delta_dims, B, 1, Hk, Hv, Dk, Dv, dtype_code(dt),
+                   Dk ** -0.5 if scale is None else scale, _rows("q", q, (B, Hk, Dk), dt),
+                   _rows("k", k, (B, Hk, Dk), dt), _rows("v", v, (B, Hv, Dv), dt),
+                   _rows("g", g, (B, Hv), dt), _rows("beta", beta, (B, Hv), dt))
+    with _on(dev, stream):
+        if o is None:
+            o = v.new_empty(v.shape)
+        else:
+            _dense("o", o, v.shape, dt)
+        e = _lib().m3_delta_step(ref, _addr(h), _addr(q), _addr(k), _addr(v), _addr(g),
+                                 _addr(beta), _addr(o), _raw(dev))
+    if e != 0:
+        raise M3Error(e, "m3_delta_step")
+    return o
 
 
 def _block_setup(x, y, gate, y_weight, scale, n_weight, eps, flags):

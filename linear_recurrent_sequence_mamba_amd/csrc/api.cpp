@@ -11,6 +11,7 @@
 #include "../../include/m3ssm.h"
 #include "attn.h"
 #include "block_norm.h"
+#include "delta.h"
 #include "gated.h"
 #include "m3_launch.h"
 #include "qk_norm.h"
@@ -274,6 +275,57 @@ m3::QkNormArgs qk_args(const m3_qk_dims* d) {
   a.ld_dq = d->ld_dq ? d->ld_dq : wq;
   a.ld_dk = d->ld_dk ? d->ld_dk : wk;
   m3::rope_freq(d->base, a.rot, a.freq);
+  return a;
+}
+
+m3_status check_delta(const m3_delta_dims* d, bool scan, bool packed) {
+  if (!d) return M3_ERR_NULL;
+  if (d->batch <= 0 || (scan && d->seqlen <= 0)) return M3_ERR_SHAPE;
+  if (d->batch > kMostRows || (scan && d->seqlen > kMostRows)) return M3_ERR_SHAPE;
+  if (d->nheads_k <= 0 || d->nheads_v <= 0 || d->headdim_k <= 0 || d->headdim_v <= 0)
+    return M3_ERR_SHAPE;
+  if (d->nheads_v % d->nheads_k) return M3_ERR_SHAPE;
+  if (!isfinite(d->scale)) return M3_ERR_SHAPE;
+  if (bad_dtype(d->dtype)) return M3_ERR_DTYPE;
+  if (!m3::delta_supported(d->headdim_k, d->headdim_v)) return M3_ERR_UNSUPPORTED;
+  const int64_t wk = static_cast<int64_t>(d->nheads_k) * d->headdim_k;
+  const int64_t wv = static_cast<int64_t>(d->nheads_v) * d->headdim_v;
+  const int64_t most = int64_t{1} << 24;   // a chunk's rows are 32-bit offsets apart
+  if (wk >= most || wv >= most) return M3_ERR_SHAPE;
+  const int64_t lds[][2] = {{d->ld_q, wk}, {d->ld_k, wk}, {d->ld_v, wv}, {d->ld_g, d->nheads_v}, {d->ld_beta, d->nheads_v}};
+  for (const auto& l : lds)
+    if (l[0] != 0 && (l[0] < l[1] || l[0] >= most)) return M3_ERR_SHAPE;
+  if ((d->ld_q | d->ld_k | d->ld_v) % 8) return M3_ERR_ALIGN;
+  // a workgroup for each chunk and head, for each sequence, head and 16 columns
+  if (!grid_fits(static_cast<int64_t>(d->batch) * d->nheads_v * (d->headdim_v / 16), 256)) return M3_ERR_SHAPE;
+  if (scan) {
+    const int64_t slots = m3::delta_slots(d->batch, d->seqlen, packed);
+    if (slots > 0x7fffffff || !grid_fits(slots * d->nheads_v, 256)) return M3_ERR_SHAPE;
+  }
+  return M3_OK;
+}
+
+// g and beta may be columns of any row
+bool misaligned_gates(const m3_delta_dims* d, const void* g, const void* beta) {
+  const uintptr_t m = d->dtype == M3_BF16 ? 1u : 3u;
+  return ((reinterpret_cast<uintptr_t>(g) | reinterpret_cast<uintptr_t>(beta)) & m) != 0;
+}
+
+m3::DeltaArgs delta_args(const m3_delta_dims* d) {
+  m3::DeltaArgs a{};
+  a.B = d->batch;
+  a.T = d->seqlen;
+  a.Hk = d->nheads_k;
+  a.Hv = d->nheads_v;
+  a.Dk = d->headdim_k;
+  a.Dv = d->headdim_v;
+  a.scale = d->scale;
+  const int64_t wk = static_cast<int64_t>(a.Hk) * a.Dk, wv = static_cast<int64_t>(a.Hv) * a.Dv;
+  a.ldq = d->ld_q ? d->ld_q : wk;
+  a.ldk = d->ld_k ? d->ld_k : wk;
+  a.ldv = d->ld_v ? d->ld_v : wv;
+  a.ldg = d->ld_g ? d->ld_g : a.Hv;
+  a.ldb = d->ld_beta ? d->ld_beta : a.Hv;
   return a;
 }
 
@@ -882,6 +934,57 @@ m3_status m3_attn_decode(const m3_attn_dims* d, const int32_t* lengths, const vo
   a.o = o;
   a.lse = lse;
   return hip_status(m3::launch_attn_decode(a, d->dtype == M3_BF16, ws, static_cast<hipStream_t>(stream)));
+}
+
+size_t m3_delta_scan_workspace_size(const m3_delta_dims* d, int packed) {
+  if (check_delta(d, true, packed != 0) != M3_OK) return 0;
+  return m3::delta_workspace_bytes(d->batch, d->seqlen, d->nheads_v, d->headdim_k, d->headdim_v,
+                                   packed != 0);
+}
+
+m3_status m3_delta_scan(const m3_delta_dims* d, const int32_t* cu_seqlens, const void* q,
+                        const void* k, const void* v, const void* g, const void* beta,
+                        const float* h0, void* o, float* hT, float* states, void* ws,
+                        size_t ws_bytes, void* stream) {
+  const bool packed = cu_seqlens != nullptr;
+  m3_status st = check_delta(d, true, packed);
+  if (st != M3_OK) return st;
+  if (!q || !k || !v || !g || !beta || !o) return M3_ERR_NULL;
+  const void* const ptrs[] = {q, k, v, h0, o, hT, states, ws};
+  if (any_misaligned(ptrs) || misaligned4(cu_seqlens) || misaligned_gates(d, g, beta)) return M3_ERR_ALIGN;
+  if (!ws || ws_bytes < m3::delta_workspace_bytes(d->batch, d->seqlen, d->nheads_v, d->headdim_k,
+                                                  d->headdim_v, packed))
+    return M3_ERR_WORKSPACE;
+  m3::DeltaArgs a = delta_args(d);
+  a.cu = cu_seqlens;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.beta = beta;
+  a.h0 = h0;
+  a.o = o;
+  a.hT = hT;
+  a.states = states;
+  m3::delta_carve(a, ws);
+  return hip_status(m3::launch_delta_scan(a, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
+}
+
+m3_status m3_delta_step(const m3_delta_dims* d, float* h, const void* q, const void* k,
+                        const void* v, const void* g, const void* beta, void* o, void* stream) {
+  m3_status st = check_delta(d, false, false);
+  if (st != M3_OK) return st;
+  if (!h || !q || !k || !v || !g || !beta || !o) return M3_ERR_NULL;
+  const void* const ptrs[] = {h, q, k, v, o};
+  if (any_misaligned(ptrs) || misaligned_gates(d, g, beta)) return M3_ERR_ALIGN;
+  m3::DeltaArgs a = delta_args(d);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.beta = beta;
+  a.o = o;
+  return hip_status(m3::launch_delta_step(a, h, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
 }
 
 m3_status m3_block_norm(const m3_block_dims* d, const void* x, const void* y, const void* gate,

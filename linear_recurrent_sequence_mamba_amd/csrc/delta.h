@@ -1,0 +1,36 @@
+// delta.h -- host-side launch interface of the gated delta rule.  Not part of
+// the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace m3 {
+
+constexpr int kDeltaChunk = 64;   // tokens of a chunk
+
+struct DeltaArgs {
+  const void *q, *k, *v, *g, *beta;   // token rows, ld* elements apart
+  const float* h0;                    // [B, Hv, Dk, Dv] or null
+  const int32_t* cu;                  // packed: [B + 1] row offsets, else null
+  void* o;                            // dense rows
+  float* hT;                          // [B, Hv, Dk, Dv] or null
+  float* states;                      // [slots, Hv, Dk, Dv] or null
+  // workspace
+  float* pm;                          // [slots, Hv, 64, 64]
+  float* gates;                       // [slots, Hv, 3, 64]
+  int64_t ldq, ldk, ldv, ldg, ldb;
+  int B, T, Hk, Hv, Dk, Dv;           // B sequences of T rows (packed: of T rows together)
+  int nslot;
+  float scale;
+};
+
+bool delta_supported(int Dk, int Dv);
+int64_t delta_slots(int B, int T, bool packed);
+size_t delta_workspace_bytes(int B, int T, int Hv, int Dk, int Dv, bool packed);
+void delta_carve(DeltaArgs& a, void* ws);
+hipError_t launch_delta_scan(DeltaArgs& a, int bf16, hipStream_t s);
+hipError_t launch_delta_step(const DeltaArgs& a, float* h, int bf16, hipStream_t s);
+
+}  // namespace m3

@@ -20,11 +20,27 @@ struct DeltaArgs {
   // workspace
   float* pm;                          // [slots, Hv, 64, 64]
   float* gates;                       // [slots, Hv, 3, 64]
+  float* ends;                        // segments' ends from a zero state, then the states before
+                                      // them, in the order of results [segment slots, Hv, Dv / 16,
+                                      // Dk / 16, 64, 4]
+  uint16_t* maps;                     // segments' maps of a state less their decay, in parts and in
+                                      // the order of operands [segment slots, Hv, parts, Dk / 16,
+                                      // Dk / 32, 64, 8]
+  float* decays;                      // segments' decays [segment slots, Hv]
   int64_t ldq, ldk, ldv, ldg, ldb;
   int B, T, Hk, Hv, Dk, Dv;           // B sequences of T rows (packed: of T rows together)
   int nslot;
+  int lseg, nseg;                     // log2 of a segment's chunks, segment slots
   float scale;
 };
+
+// Segments of the chain: how many chunks (log2) each has.
+struct DeltaPlan {
+  int lseg;
+  int64_t nseg;   // slots of segments
+  bool split;     // some sequence may have more than one
+};
+DeltaPlan delta_plan(int B, int T, int Hv, int Dv, bool packed);
 
 bool delta_supported(int Dk, int Dv);
 int64_t delta_slots(int B, int T, bool packed);

@@ -27,7 +27,7 @@ namespace {
 // are small.
 template <typename T, int DK>
 __global__ __launch_bounds__(256) void k_delta_chunk(DeltaArgs a) {
-  using X = Rows64<DK>;
+  using X = Rows64<DK, true>;
   constexpr int NI = DeltaParts<T>::IN, LM = 68;
   // K and Q, then the matrices A and [T \ P^T]
   constexpr int TILES = 2 * NI * X::PLANE, MATS = 2 * 64 * LM * static_cast<int>(sizeof(float));
@@ -42,9 +42,10 @@ __global__ __launch_bounds__(256) void k_delta_chunk(DeltaArgs a) {
   const int h = blockIdx.x % a.Hv, slot = blockIdx.x / a.Hv, hk = h / (a.Hv / a.Hk);
   const DeltaSlot sl(a, slot, lane);
   if (sl.n <= 0) return;
-  Stage<T, DK, 256> stage;
+  const typename X::Lane xl(lane);
+  Stage<T, DK, 256, true> stage;
   stage.load(static_cast<const T*>(a.k) + sl.row0 * a.ldk + hk * DK, a.ldk, sl.n);
-  Stage<T, DK, 256> stage_q;
+  Stage<T, DK, 256, true> stage_q;
   stage_q.load(static_cast<const T*>(a.q) + sl.row0 * a.ldq + hk * DK, a.ldq, sl.n);
   if (w == 0) {
     const int64_t row = sl.row0 + min(lane, sl.n - 1);
@@ -52,7 +53,7 @@ __global__ __launch_bounds__(256) void k_delta_chunk(DeltaArgs a) {
     float bt = ld1(static_cast<const T*>(a.beta), row * a.ldb + h);
     if (lane >= sl.n) gt = bt = 0.0f;
     gt = gt < -128.0f ? -128.0f : gt;   // exp is 0 there, and -inf has no differences
-    double G = gt;
+    double G = gt * 1.4426950408889634;   // powers of 2 from here on
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const double o = __shfl_up(G, d, 64);
@@ -62,25 +63,25 @@ __global__ __launch_bounds__(256) void k_delta_chunk(DeltaArgs a) {
     sB[lane] = bt;
     const double end = __shfl(G, 63, 64);
     float* p = a.gates + (static_cast<int64_t>(slot) * a.Hv + h) * 192 + lane;
-    p[0] = expf(static_cast<float>(G));
-    p[64] = expf(static_cast<float>(end - G));
+    p[0] = __builtin_amdgcn_exp2f(static_cast<float>(G));
+    p[64] = __builtin_amdgcn_exp2f(static_cast<float>(end - G));
     p[128] = bt;
   }
-  stage.store(sK, sl.n);
-  stage_q.store(sQ, sl.n);
+  stage.store(sK);
+  stage_q.store(sQ);
   __syncthreads();
 
   f4 kk[4], qk[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f4{0, 0, 0, 0};
 #pragma unroll
-  for (int c = 0; c < DK; c += 32) {
-    const Parts<NI> ka = X::template by_row<NI>(sK, 16 * w, c, lane);
-    const Parts<NI> qa = X::template by_row<NI>(sQ, 16 * w, c, lane);
+  for (int x = 0; x < DK / 32; ++x) {
+    const Parts<NI> ka = X::template by_row<NI>(sK, xl, w, x);
+    const Parts<NI> qa = X::template by_row<NI>(sQ, xl, w, x);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (j <= w) {
-        const Parts<NI> kb = X::template by_row<NI>(sK, 16 * j, c, lane);
+        const Parts<NI> kb = X::template by_row<NI>(sK, xl, j, x);
         kk[j] = mmp<3>(ka, kb, kk[j]);
         qk[j] = mmp<3>(qa, kb, qk[j]);
       }
@@ -95,7 +96,7 @@ __global__ __launch_bounds__(256) void k_delta_chunk(DeltaArgs a) {
       for (int e = 0; e < 4; ++e) {
         const int i = 16 * w + 4 * g + e;
         const bool in = j < w || r <= 4 * g + e, strict = j < w || r < 4 * g + e;
-        const float d = in ? expf(static_cast<float>(sG[i] - Gj)) : 0.0f;
+        const float d = in ? __builtin_amdgcn_exp2f(static_cast<float>(sG[i] - Gj)) : 0.0f;
         sA[i][16 * j + r] = strict ? sB[i] * d * kk[j][e] : 0.0f;
         p[e] = in ? a.scale * d * qk[j][e] : 0.0f;
       }
@@ -160,150 +161,381 @@ __global__ __launch_bounds__(256) void k_delta_chunk(DeltaArgs a) {
 // The chain.  A wave holds 16 columns of a head's state, so that nothing of it
 // is ever exchanged; the NW waves of a workgroup share K, Q and the chunk's
 // matrix in LDS.  The next chunk is on its way in registers meanwhile.
-template <typename T, int DK, int NW>
-__global__ __launch_bounds__(64 * NW) void k_delta_chain(DeltaArgs a) {
+//
+// Where sequences and heads are too few to fill the chip, a sequence's chunks
+// are cut into segments.  A segment maps the state before it as S -> E + F S.
+// kEnds gives E (a state that starts from zero), kMaps F (the columns of the
+// identity as a state, without values), k_delta_join passes the states through
+// the segments, and the segments then run at once.
+//
+// Parts (bf16): what reaches the state has three, so that it keeps fp32's
+// accuracy; P and U, which only reach outputs in bf16, two; a map, whose decay
+// is kept apart in fp32, two (2^-17 of what the segment's keys take out).
+//
+// With room for two of a chunk's tiles (NBUF = 2) the next chunk's are written
+// while waves still read this one's, and one barrier a chunk is enough.
+enum { kFull = 0, kEnds = 1, kMaps = 2 };
+
+template <typename T, int DK, int NT, bool FULL>
+struct ChainTiles {
   using X = Rows64<DK>;
   using M = Rows64<64>;
-  constexpr int NI = DeltaParts<T>::IN, NO = DeltaParts<T>::OUT, NT = 64 * NW, KS = DK / 32, DT = DK / 16;
-  __shared__ __align__(16) char sK[NI * X::PLANE], sQ[NI * X::PLANE], sM[3 * M::PLANE];
-  __shared__ __align__(16) float sGate[192];
+  static constexpr int NI = DeltaParts<T>::IN, NO = DeltaParts<T>::OUT;
+  static constexpr int BK = NI * X::PLANE, BQ = FULL ? BK : 0, BM = 3 * M::PLANE, BUF = BK + BQ + BM + 768;
+  static constexpr int NG = (192 + NT - 1) / NT;
+  Stage<T, DK, NT> k, q;
+  Stage<float, 64, NT> m;
+  float g[NG];
+  __device__ __forceinline__ void store(char* b) const {
+    k.store(b);
+    if constexpr (FULL) q.store(b + BK);
+    m.store(b + BK + BQ);
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+      if (threadIdx.x + i * NT < 192) reinterpret_cast<float*>(b + BK + BQ + BM)[threadIdx.x + i * NT] = g[i];
+  }
+};
+
+template <typename T, int DK, int NW, int NBUF, int MODE>
+__device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, int slot, int h, int slice, char* smem) {
+  using X = Rows64<DK>;
+  constexpr bool FULL = MODE == kFull;
+  constexpr int NT = 64 * NW, KS = DK / 32, DT = DK / 16;
+  using Tiles = ChainTiles<T, DK, NT, FULL>;
+  constexpr int NI = Tiles::NI, NO = Tiles::NO, NS = MODE == kMaps ? NO : 3;
+  constexpr int BK = Tiles::BK, BQ = Tiles::BQ, BM = Tiles::BM, BUF = Tiles::BUF;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  const int nsl = a.Dv / (16 * NW);
-  int n = blockIdx.x;
-  const int slice = n % nsl;
-  n /= nsl;
-  const int h = n % a.Hv, s = n / a.Hv, hk = h / (a.Hv / a.Hk);
-  const int col = (slice * NW + w) * 16 + r;
-  const DeltaSeq seq(a, s);
+  const int r = lane & 15, g = lane >> 4, hk = h / (a.Hv / a.Hk);
+  const int cs = slice * NW + w, col = 16 * cs + r;   // of the values, or of the map
   const Triangle tri(lane);
-  const int64_t state = (static_cast<int64_t>(s) * a.Hv + h) * DK * a.Dv + col;
+  const typename X::Lane xl(lane);
+  const Rows64<64>::Lane ml(lane);
+  const int64_t head = static_cast<int64_t>(seg.s) * a.Hv + h, shead = static_cast<int64_t>(slot) * a.Hv + h;
+  const int64_t dd = static_cast<int64_t>(DK) * a.Dv;
+  const uint32_t at = static_cast<uint32_t>(8 * g * a.Dv + col);   // of a state
+  const uint32_t end_at = (cs * DT * 64 + lane) * 4;               // of a segment's
 
   f4 S[DT];
 #pragma unroll
-  for (int t = 0; t < DT; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) S[t][e] = a.h0 ? a.h0[state + static_cast<int64_t>(16 * t + 4 * g + e) * a.Dv] : 0.0f;
-
-  const int nch = (seq.len + kDeltaChunk - 1) / kDeltaChunk;
-  Stage<T, DK, NT> stK, stQ;
-  Stage<float, 64, NT> stM;
-  float stG[(192 + NT - 1) / NT];
-  Raw1<T> stV[16];
-  auto fetch = [&](int c) __attribute__((always_inline)) {
-    const int64_t row0 = seq.row0 + static_cast<int64_t>(c) * kDeltaChunk;
-    const int cnt = min(kDeltaChunk, seq.len - c * kDeltaChunk);
-    const int64_t at = static_cast<int64_t>(seq.slot0 + c) * a.Hv + h;
-    stK.load(static_cast<const T*>(a.k) + row0 * a.ldk + hk * DK, a.ldk, cnt);
-    stM.load(a.pm + at * 4096, 64, 64);
-#pragma unroll
-    for (int i = 0; i < (192 + NT - 1) / NT; ++i)
-      stG[i] = a.gates[at * 192 + min(static_cast<int>(threadIdx.x) + i * NT, 191)];
-    const T* v = static_cast<const T*>(a.v) + row0 * a.ldv + h * a.Dv + col;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) stV[i].load(v, min(16 * (i / 4) + 4 * g + i % 4, cnt - 1) * a.ldv);
-    stQ.load(static_cast<const T*>(a.q) + row0 * a.ldq + hk * DK, a.ldq, cnt);
-  };
-  if (nch > 0) fetch(0);
-  for (int c = 0; c < nch; ++c) {
-    const int cnt = min(kDeltaChunk, seq.len - c * kDeltaChunk);
-    stK.store(sK, cnt);
-    stQ.store(sQ, cnt);
-#pragma unroll
-    for (int i = 0; i < Stage<float, 64, NT>::N; ++i) {
-      const int x = threadIdx.x + i * NT;
-      float f[8];
-      stM.v[i].get(f);
-      M::template put<3>(sM, x / 8, x % 8 * 8, f);
-    }
-#pragma unroll
-    for (int i = 0; i < (192 + NT - 1) / NT; ++i)
-      if (threadIdx.x + i * NT < 192) sGate[threadIdx.x + i * NT] = stG[i];
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 16 * (i / 4) + 4 * g + i % 4 < cnt ? stV[i].f() : 0.0f;
-    __syncthreads();
-    if (c + 1 < nch) fetch(c + 1);
-    const int64_t slot = static_cast<int64_t>(seq.slot0 + c) * a.Hv + h;
-    if (a.states) {
-      float* p = a.states + slot * DK * a.Dv + col;
-#pragma unroll
-      for (int t = 0; t < DT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[static_cast<int64_t>(16 * t + 4 * g + e) * a.Dv] = S[t][e];
-    }
-    // K S0 and Q S0
-    f4 ks[4], qs[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ks[i] = qs[i] = f4{0, 0, 0, 0};
-#pragma unroll
-    for (int x = 0; x < KS; ++x) {
-      Parts<3> sp;
-      split_d<3>(sp, S[2 * x], S[2 * x + 1]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) ks[i] = mmp<3>(X::template by_row<NI>(sK, 16 * i, 32 * x, lane), sp, ks[i]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) qs[i] = mmp<NO>(X::template by_row<NI>(sQ, 16 * i, 32 * x, lane), sp, qs[i]);
-    }
-    // R = beta (V - exp(G) K S0) in place of K S0
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f4 st = *reinterpret_cast<const f4*>(&sGate[16 * i + 4 * g]);
-      const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + 16 * i + 4 * g]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) ks[i][e] = bt[e] * fmaf(-st[e], ks[i][e], v[4 * i + e]);
-    }
-    // U = T R: R itself for the diagonal
-    Parts<3> rp[2];
-    split_d<3>(rp[0], ks[0], ks[1]);
-    split_d<3>(rp[1], ks[2], ks[3]);
-    f4 u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      u[i] = ks[i];
-#pragma unroll
-      for (int x = 0; x <= i / 2; ++x) u[i] = mmp<3>(tri.t<3>(sM, i, x, lane), rp[x], u[i]);
-    }
-    // O = scale exp(G) Q S0 + P U
-    {
-      Parts<NO> up[2];
-      split_d<NO>(up[0], u[0], u[1]);
-      split_d<NO>(up[1], u[2], u[3]);
-      T* o = static_cast<T*>(a.o) + (seq.row0 + static_cast<int64_t>(c) * kDeltaChunk) * a.Hv * a.Dv + h * a.Dv + col;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f4 st = *reinterpret_cast<const f4*>(&sGate[16 * i + 4 * g]);
-        f4 y;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = a.scale * st[e] * qs[i][e];
-#pragma unroll
-        for (int x = 0; x <= i / 2; ++x) y = mmp<NO>(tri.p<NO>(sM, i, x, lane), up[x], y);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = 16 * i + 4 * g + e;
-          if (row < cnt) o[static_cast<int64_t>(row) * a.Hv * a.Dv] = from_f32<T>(y[e]);
-        }
-      }
-    }
-    // S1 = exp(G_end) S0 + K^T (exp(G_end - G) U)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] *= *reinterpret_cast<const f4*>(&sGate[64 + 16 * i + 4 * g]);
-    split_d<3>(rp[0], u[0], u[1]);
-    split_d<3>(rp[1], u[2], u[3]);
-    const float last = sGate[63];
-#pragma unroll
-    for (int t = 0; t < DT; ++t) {
-      S[t] *= last;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) S[t] = mmp<3>(X::template by_col<NI>(sK, 32 * x, 16 * t, lane), rp[x], S[t]);
-    }
-    __syncthreads();
-  }
-  if (a.hT)
+  for (int t = 0; t < DT; ++t) S[t] = f4{0, 0, 0, 0};
+  if constexpr (MODE == kMaps) {
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) a.hT[state + static_cast<int64_t>(16 * t + 4 * g + e) * a.Dv] = S[t][e];
+      for (int e = 0; e < 4; ++e) S[t][e] = tile_row(t, e) + 8 * g == col ? 1.0f : 0.0f;
+  } else if (FULL && seg.j > 0) {
+#pragma unroll
+    for (int t = 0; t < DT; ++t) S[t] = *reinterpret_cast<const f4*>(a.ends + shead * dd + end_at + t * 256);
+  } else if (a.h0 && seg.j == 0) {
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[t][e] = (a.h0 + head * dd + tile_row(t, e) * a.Dv)[at];
+  }
+
+  Tiles st;
+  Cols<T> stV;
+  const int c1 = seg.c0 + seg.nch;
+  auto rows = [&](int c) __attribute__((always_inline)) { return min(kDeltaChunk, seg.len - c * kDeltaChunk); };
+  auto first = [&](int c) __attribute__((always_inline)) { return seg.row0 + static_cast<int64_t>(c) * kDeltaChunk; };
+  // (behind the last chunk the last one again, unused)
+  auto fetch = [&](int c) __attribute__((always_inline)) {
+    c = min(c, c1 - 1);
+    const int64_t m = static_cast<int64_t>(seg.slot0 + c) * a.Hv + h;
+    st.k.load(static_cast<const T*>(a.k) + first(c) * a.ldk + hk * DK, a.ldk, rows(c));
+    st.m.load(a.pm + m * 4096, 64, 64);
+#pragma unroll
+    for (int i = 0; i < Tiles::NG; ++i) st.g[i] = (a.gates + m * 192)[min(threadIdx.x + i * NT, 191u)];
+    if constexpr (FULL) st.q.load(static_cast<const T*>(a.q) + first(c) * a.ldq + hk * DK, a.ldq, rows(c));
+  };
+  auto fetch_v = [&](int c) __attribute__((always_inline)) {
+    c = min(c, c1 - 1);
+    if constexpr (MODE != kMaps) stV.load(static_cast<const T*>(a.v) + first(c) * a.ldv + h * a.Dv, a.ldv, rows(c), col, g);
+  };
+  if (seg.nch > 0) {
+    fetch(seg.c0);
+    fetch_v(seg.c0);
+    st.store(smem);
+    fetch(seg.c0 + 1);
+  }
+  char* buf = smem;
+  float decay = 1.0f;   // of the segment
+  for (int c = seg.c0; c < c1; ++c) {
+    const char *sK = buf, *sQ = buf + BK, *sM = buf + BK + BQ;
+    const float* sGate = reinterpret_cast<const float*>(buf + BK + BQ + BM);
+    tiles_barrier();
+    if (FULL && a.states) {
+      float* p = a.states + (static_cast<int64_t>(seg.slot0 + c) * a.Hv + h) * dd;
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) (p + tile_row(t, e) * a.Dv)[at] = S[t][e];
+    }
+    // K S0 and Q S0, the next operands read ahead of their products
+    f4 ks[4], qs[4];
+    Parts<NI> ka[2][4], qa[2][4];
+    Parts<NS> sp[2];
+    auto read = [&](int x) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ka[x & 1][i] = X::template by_row<NI>(sK, xl, i, x);
+      if constexpr (FULL)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qa[x & 1][i] = X::template by_row<NI>(sQ, xl, i, x);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ks[i] = qs[i] = f4{0, 0, 0, 0};
+    read(0);
+    split_d<NS>(sp[0], S[0], S[1]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+      if (x + 1 < KS) {
+        read(x + 1);
+        split_d<NS>(sp[(x + 1) & 1], S[2 * x + 2], S[2 * x + 3]);
+      }
+      mmp<NS>(ks, ka[x & 1], sp[x & 1]);
+      if constexpr (FULL) mmp<NO>(qs, qa[x & 1], sp[x & 1]);
+      if constexpr (NI == 1) interleave<FULL ? 8 : 4, FULL ? 20 : 4 * NS, FULL ? 3 : 4>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // R = beta (V - exp(G) K S0) in place of K S0
+    Parts<1> ta[2][6];
+    tri.t6(ta[0], sM, ml, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f4 st = *reinterpret_cast<const f4*>(&sGate[tile_row(i, 0) + 8 * g]);
+      const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + tile_row(i, 0) + 8 * g]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ks[i][e] = bt[e] * fmaf(-st[e], ks[i][e], MODE == kMaps ? 0.0f : stV.v[4 * i + e].f());
+    }
+    Parts<NS> rp[2];
+    split_d<NS>(rp[0], ks[0], ks[1]);
+    split_d<NS>(rp[1], ks[2], ks[3]);
+    __builtin_amdgcn_sched_barrier(0);
+    // U = T R: R itself for the diagonal
+    f4 u[6] = {ks[0], ks[1], ks[2], ks[3], f4{0, 0, 0, 0}, f4{0, 0, 0, 0}};
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      if (n + 1 < NS) tri.t6(ta[(n + 1) & 1], sM, ml, n + 1);
+      mm6<NS>(u, ta[n & 1], rp, n);
+      if (n == 0 && NBUF == 2) {
+        buf = buf == smem ? smem + BUF : smem;
+        st.store(buf);   // (the last time unread)
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    u[2] += u[4];
+    u[3] += u[5];
+    // O = scale exp(G) Q S0 + P U
+    if constexpr (FULL) {
+      Parts<1> pa[2][6];
+      tri.p6(pa[0], sM, ml, 0);
+      f4 y[6];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f4 st = *reinterpret_cast<const f4*>(&sGate[tile_row(i, 0) + 8 * g]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[i][e] = a.scale * st[e] * qs[i][e];
+      }
+      y[4] = y[5] = f4{0, 0, 0, 0};
+      Parts<NO> up[2];
+      split_d<NO>(up[0], u[0], u[1]);
+      split_d<NO>(up[1], u[2], u[3]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < NO; ++n) {
+        if (n + 1 < NO) tri.p6(pa[(n + 1) & 1], sM, ml, n + 1);
+        mm6<NO>(y, pa[n & 1], up, n);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      y[2] += y[4];
+      y[3] += y[5];
+      const int ldo = a.Hv * a.Dv;
+      const ChunkRows o(static_cast<T*>(a.o) + first(c) * ldo + h * a.Dv, ldo, rows(c));
+      const uint32_t orow = static_cast<uint32_t>(ldo) * static_cast<uint32_t>(sizeof(T));
+      const uint32_t oat = 8 * g * orow + col * static_cast<uint32_t>(sizeof(T));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o.store1(T{}, oat + tile_row(i, e) * orow, y[i][e]);
+    }
+    fetch_v(c + 1);
+    // S1 = exp(G_end) S0 + K^T (exp(G_end - G) U)
+    Parts<NI> kc[2][4];
+    auto read_t = [&](int n) __attribute__((always_inline)) {   // four tiles of S, 32 rows
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        kc[n & 1][t] = X::template by_col<NI>(sK, xl, 4 * (n % (DT / 4)) + t, n / (DT / 4));
+    };
+    Parts<NS> ep[2];
+    read_t(0);
+    const float last = sGate[63];
+    decay *= last;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) u[i] *= *reinterpret_cast<const f4*>(&sGate[64 + tile_row(i, 0) + 8 * g]);
+    split_d<NS>(ep[0], u[0], u[1]);
+#pragma unroll
+    for (int t = 0; t < DT; ++t) S[t] *= last;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < DT / 2; ++n) {
+      if (n + 1 < DT / 2) read_t(n + 1);
+      if (n == 0) {
+#pragma unroll
+        for (int i = 2; i < 4; ++i) u[i] *= *reinterpret_cast<const f4*>(&sGate[64 + tile_row(i, 0) + 8 * g]);
+        split_d<NS>(ep[1], u[2], u[3]);
+      }
+      mmp<NS>(*reinterpret_cast<f4(*)[4]>(&S[4 * (n % (DT / 4))]), kc[n & 1], ep[n / (DT / 4)]);
+      if constexpr (NI == 1)
+        if (n == 0) interleave<10, 4 * NS, 4>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (NBUF == 1) {
+      tiles_barrier();
+      st.store(buf);
+    }
+    fetch(c + 2);
+  }
+  if constexpr (MODE == kMaps) {   // less its decay, as the A operand of a product over its columns
+    uint16_t* p = a.maps + shead * NS * DK * DK;
+    const uint32_t to = col / 32 * 512 + (col % 32 / 8 * 16 + 4 * g) * 8 + col % 8;
+#pragma unroll
+    for (int t = 0; t < DT; ++t) {
+      Parts<NS> f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[t][e] -= tile_row(t, e) + 8 * g == col ? decay : 0.0f;
+      split_d<NS>(f, S[t], S[t]);
+#pragma unroll
+      for (int n = 0; n < NS; ++n) {
+        const uint4 u = __builtin_bit_cast(uint4, f.p[n]);
+        const uint32_t i = to + (n * DT + t) * KS * 512;
+        p[i] = static_cast<uint16_t>(u.x);
+        p[i + 8] = static_cast<uint16_t>(u.x >> 16);
+        p[i + 16] = static_cast<uint16_t>(u.y);
+        p[i + 24] = static_cast<uint16_t>(u.y >> 16);
+      }
+    }
+    if (cs == 0 && lane == 0) a.decays[shead] = decay;
+  } else if constexpr (MODE == kEnds) {   // to where the next segment starts
+#pragma unroll
+    for (int t = 0; t < DT; ++t) *reinterpret_cast<f4*>(a.ends + (shead + a.Hv) * dd + end_at + t * 256) = S[t];
+  } else if (seg.last && a.hT) {
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) (a.hT + head * dd + tile_row(t, e) * a.Dv)[at] = S[t][e];
+  }
+}
+
+template <typename T, int DK, int NW, int NBUF>
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_chain(DeltaArgs a) {
+  __shared__ __align__(16) char smem[NBUF * ChainTiles<T, DK, 64 * NW, true>::BUF];
+  const int nsl = a.Dv / (16 * NW), n = blockIdx.x / nsl;
+  const DeltaSeg seg(a, n / a.Hv, threadIdx.x & 63);
+  if (seg.s >= 0) chain<T, DK, NW, NBUF, kFull>(a, seg, n / a.Hv, n % a.Hv, blockIdx.x % nsl, smem);
+}
+
+// E and F of all segments but the last, F of none before the second
+template <typename T, int DK, int NW, int NBUF>
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_segments(DeltaArgs a) {
+  __shared__ __align__(16) char smem[NBUF * ChainTiles<T, DK, 64 * NW, false>::BUF];
+  const int nv = a.Dv / (16 * NW), nsl = nv + DK / (16 * NW);
+  const int n = blockIdx.x / nsl, slice = blockIdx.x % nsl;
+  const DeltaSeg seg(a, n / a.Hv, threadIdx.x & 63);
+  if (seg.s < 0 || seg.last) return;
+  if (slice < nv) chain<T, DK, NW, NBUF, kEnds>(a, seg, n / a.Hv, n % a.Hv, slice, smem);
+  else if (seg.j > 0) chain<T, DK, NW, NBUF, kMaps>(a, seg, n / a.Hv, n % a.Hv, slice - nv, smem);
+}
+
+// The states before the segments: S_{j+1} = E_j + d_j S_j + F_j S_j, with the
+// decay d_j apart from the map.  E_j lies where S_{j+1} goes; S_1 is there
+// already.  A wave has 16 columns of a sequence's head.  F arrives in blocks of
+// 32 columns which lie as the operands do, through a ring of blocks in LDS.
+template <int DK, int NP>
+__global__ __launch_bounds__(64) void k_delta_join(DeltaArgs a) {
+  constexpr int KS = DK / 32, DT = DK / 16, NF = NP * DT;   // NF: operands of a block
+  // each by its name, so that reads of one do not wait for the others' loads
+  __shared__ __align__(16) char r0[NF * 1024], r1[NF * 1024], r2[KS > 2 ? NF * 1024 : 16], r3[KS > 2 ? NF * 1024 : 16];
+  auto ring = [&](int x) __attribute__((always_inline)) { return x == 0 ? r0 : x == 1 ? r1 : x == 2 ? r2 : r3; };
+  const int lane = threadIdx.x;
+  const int nsl = a.Dv / 16;
+  int b = blockIdx.x;
+  const int slice = b % nsl;
+  b /= nsl;
+  const int h = b % a.Hv, s = b / a.Hv;
+  int len, slot0;
+  if (a.cu) {
+    const int c = clamp_row(a.cu[s], a.T);
+    len = max(0, clamp_row(a.cu[s + 1], a.T) - c);
+    slot0 = (c >> (6 + a.lseg)) + s;
+  } else {
+    len = a.T;
+    slot0 = s * (a.nseg / a.B);
+  }
+  const int nseg = (((len + kDeltaChunk - 1) / kDeltaChunk) + (1 << a.lseg) - 1) >> a.lseg;
+  if (nseg <= 2) return;
+  const int64_t shead = static_cast<int64_t>(slot0 + 1) * a.Hv + h, step = static_cast<int64_t>(a.Hv) * DK * a.Dv;
+  float* p = a.ends + shead * DK * a.Dv + (slice * DT * 64 + lane) * 4;
+  const uint16_t* f = a.maps + shead * NP * DK * DK + lane * 8;
+  const float* d = a.decays + shead;
+  // block x of segment j's map
+  auto fetch = [&](int j, int x) __attribute__((always_inline)) {
+    const uint16_t* from = f + static_cast<int64_t>(j - 1) * a.Hv * NP * DK * DK + x * 512;
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+      __builtin_amdgcn_global_load_lds((const M3_GLB void*)(from + i * KS * 512), (M3_LDS void*)(ring(x) + i * 1024), 16, 0, 0);
+  };
+  f4 S[DT], E[DT], next[DT];
+  float dec = d[0], dnext = 0.0f;
+#pragma unroll
+  for (int t = 0; t < DT; ++t) {
+    S[t] = *reinterpret_cast<const f4*>(p + t * 256);
+    E[t] = *reinterpret_cast<const f4*>(p + step + t * 256);
+    next[t] = f4{0, 0, 0, 0};
+  }
+#pragma unroll
+  for (int x = 0; x < KS - 1; ++x) fetch(1, x);
+  for (int j = 1; j + 1 < nseg; ++j) {
+    p += step;
+    const bool more = j + 2 < nseg;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) E[t][e] = fmaf(dec, S[t][e], E[t][e]);
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+      // this block is there; the KS - 2 behind it may be on their way
+      if (x == 0 || more) __builtin_amdgcn_s_waitcnt(0x0f70 | ((KS - 2) * NF & 15) | ((KS - 2) * NF >> 4 << 14));
+      else lds_loads_done();
+      lds_reads_done();
+      if (x == 0) fetch(j, KS - 1);
+      else if (more) fetch(j + 1, x - 1);
+      if (x == 1 && more) {   // the next E_j
+        dnext = d[static_cast<int64_t>(j) * a.Hv];
+#pragma unroll
+        for (int t = 0; t < DT; ++t) next[t] = *reinterpret_cast<const f4*>(p + step + t * 256);
+      }
+      Parts<NP> sp;
+      split_d<NP>(sp, S[2 * x], S[2 * x + 1]);
+      const char* blk = ring(x) + lane * 16;
+#pragma unroll
+      for (int t = 0; t < DT; t += 4) {
+        Parts<NP> fp[4];
+#pragma unroll
+        for (int m = 0; m < NP; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) fp[i].p[m] = *reinterpret_cast<const bh8*>(blk + (m * DT + t + i) * 1024);
+        mmp<NP>(*reinterpret_cast<f4(*)[4]>(&E[t]), fp, sp);
+      }
+    }
+    dec = dnext;
+#pragma unroll
+    for (int t = 0; t < DT; ++t) {
+      S[t] = E[t];
+      E[t] = next[t];
+      *reinterpret_cast<f4*>(p + t * 256) = S[t];
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -392,14 +624,32 @@ __global__ __launch_bounds__(256) void k_delta_step(DeltaArgs a, float* hp) {
   }
 }
 
+template <typename T, int DK, int NW>
+hipError_t run_chain(const DeltaArgs& a, bool split, hipStream_t s) {
+  constexpr int NBUF = sizeof(T) == 2 ? 2 : 1;
+  const int64_t heads = static_cast<int64_t>(a.nseg) * a.Hv;
+  if (split) {
+    k_delta_segments<T, DK, NW, NBUF>
+        <<<static_cast<unsigned>(heads * ((a.Dv + DK) / (16 * NW))), 64 * NW, 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    k_delta_join<DK, DeltaParts<T>::OUT>
+        <<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hv * (a.Dv / 16)), 64, 0, s>>>(a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  k_delta_chain<T, DK, NW, NBUF><<<static_cast<unsigned>(heads * (a.Dv / (16 * NW))), 64 * NW, 0, s>>>(a);
+  return hipGetLastError();
+}
+
 template <typename T, int DK>
-hipError_t run_scan(const DeltaArgs& a, hipStream_t s) {
+hipError_t run_scan(const DeltaArgs& a, bool split, hipStream_t s) {
   k_delta_chunk<T, DK><<<static_cast<unsigned>(static_cast<int64_t>(a.nslot) * a.Hv), 256, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t heads = static_cast<int64_t>(a.B) * a.Hv;
-  k_delta_chain<T, DK, 4><<<static_cast<unsigned>(heads * (a.Dv / 64)), 256, 0, s>>>(a);
-  return hipGetLastError();
+  if constexpr (DK == 128 && sizeof(T) == 2)
+    if (a.Dv == 128 && split) return run_chain<T, DK, 8>(a, split, s);
+  return run_chain<T, DK, 4>(a, split, s);
 }
 
 template <typename T>
@@ -419,19 +669,45 @@ int64_t delta_slots(int B, int T, bool packed) {
   return static_cast<int64_t>(B) * ((T + kDeltaChunk - 1) / kDeltaChunk);
 }
 
-size_t delta_workspace_bytes(int B, int T, int Hv, int, int, bool packed) {
-  return sizeof(float) * (4096 + 192) * static_cast<size_t>(delta_slots(B, T, packed)) * Hv;
+DeltaPlan delta_plan(int B, int T, int Hv, int Dv, bool packed) {
+  const int64_t waves = static_cast<int64_t>(B) * Hv * (Dv / 16);
+  const int64_t chunks = ((packed ? T / B : T) + kDeltaChunk - 1) / kDeltaChunk;   // of a sequence, on average
+  DeltaPlan p{30, B, false};
+  for (int l = 3; l < 10; ++l)
+    if (waves * (chunks >> l) <= 2048) {
+      if ((chunks >> l) >= 4) p.lseg = l, p.split = true;
+      break;
+    }
+  if (p.split)
+    p.nseg = packed ? (static_cast<int64_t>(T) >> (6 + p.lseg)) + B
+                    : B * ((chunks + (int64_t{1} << p.lseg) - 1) >> p.lseg);
+  return p;
+}
+
+size_t delta_workspace_bytes(int B, int T, int Hv, int Dk, int Dv, bool packed) {
+  const DeltaPlan p = delta_plan(B, T, Hv, Dv, packed);
+  const size_t chunks = static_cast<size_t>(4096 + 192) * delta_slots(B, T, packed) * Hv;
+  // (maps of two parts take no less than their room for three)
+  const size_t segs = p.split ? (static_cast<size_t>(Dk) * (sizeof(float) * Dv + 3 * sizeof(uint16_t) * Dk) + sizeof(float) * 4) * p.nseg * Hv : 0;
+  return sizeof(float) * chunks + segs;
 }
 
 void delta_carve(DeltaArgs& a, void* ws) {
+  const DeltaPlan p = delta_plan(a.B, a.T, a.Hv, a.Dv, a.cu != nullptr);
+  a.lseg = p.lseg;
+  a.nseg = static_cast<int>(p.nseg);
   a.nslot = static_cast<int>(delta_slots(a.B, a.T, a.cu != nullptr));
   a.pm = static_cast<float*>(ws);
   a.gates = a.pm + static_cast<size_t>(4096) * a.nslot * a.Hv;
+  a.ends = a.gates + static_cast<size_t>(192) * a.nslot * a.Hv;
+  a.maps = reinterpret_cast<uint16_t*>(a.ends + static_cast<size_t>(a.Dk) * a.Dv * a.nseg * a.Hv);
+  a.decays = reinterpret_cast<float*>(a.maps + static_cast<size_t>(3) * a.Dk * a.Dk * a.nseg * a.Hv);
 }
 
 hipError_t launch_delta_scan(DeltaArgs& a, int bf16, hipStream_t s) {
-  if (bf16) return a.Dk == 64 ? run_scan<bf16_t, 64>(a, s) : run_scan<bf16_t, 128>(a, s);
-  return a.Dk == 64 ? run_scan<float, 64>(a, s) : run_scan<float, 128>(a, s);
+  const bool split = a.lseg < 30;
+  if (bf16) return a.Dk == 64 ? run_scan<bf16_t, 64>(a, split, s) : run_scan<bf16_t, 128>(a, split, s);
+  return a.Dk == 64 ? run_scan<float, 64>(a, split, s) : run_scan<float, 128>(a, split, s);
 }
 
 hipError_t launch_delta_step(const DeltaArgs& a, float* h, int bf16, hipStream_t s) {

@@ -7,12 +7,13 @@
 // with a + b below the number of parts that are asked for.  Inputs in bf16 are
 // one exact part.
 //
-// A result holds column lane % 16 and rows 4 (lane / 16) + {0..3} of a 16x16
-// tile.  Two tiles below each other are the B operand of a product over their
-// 32 rows if the A operand takes its k slots 8 g + j in the order
-// 16 (j / 4) + 4 g + j % 4 (g = lane / 16): results go on to the next product
-// without leaving their lanes, and a wave that holds some columns of the state
-// never needs another wave's.
+// A result holds column lane % 16 and in element e row 4 g + e (g = lane / 16)
+// of a 16x16 tile.  Which rows of a matrix those are is free: tile i takes rows
+// tile_row(i, g, e) = 32 (i / 2) + 8 g + 4 (i % 2) + e, of tokens and of the
+// state alike, so that two tiles' elements are k slots 8 g .. 8 g + 7 of 32
+// rows: the B operand of the next product, whose A operand has its k in order.
+// Results go on without leaving their lanes, and a wave that holds some columns
+// of the state never needs another wave's.
 #pragma once
 
 #include "delta.h"
@@ -21,29 +22,33 @@
 namespace m3 {
 namespace {
 
+__device__ __forceinline__ constexpr int tile_row(int i, int e) { return 32 * (i >> 1) + 4 * (i & 1) + e; }   // (+ 8 g)
+
 template <int NP>
 struct Parts {
   bh8 p[NP];
 };
 
-// eight floats as NP parts
+// Eight floats as NP parts.  (What a part leaves could be had by one product of
+// pairs each, (part, part') . (-1, 0) + x, exactly and with 28 instead of 44
+// instructions, but those run at a lower rate: the maps of 16384 tokens of 16
+// heads 205 us instead of 182.)  An infinity leaves NaN.
 template <int NP>
 __device__ __forceinline__ void split8(Parts<NP>& f, const float* v) {
-  float r[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) r[j] = v[j];
+  for (int j = 0; j < 4; ++j) {
+    float x = v[2 * j], y = v[2 * j + 1];
 #pragma unroll
-  for (int n = 0; n < NP; ++n)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bh2 h = __builtin_convertvector(f2{r[2 * j], r[2 * j + 1]}, bh2);
+    for (int n = 0; n < NP; ++n) {
+      const bh2 h = __builtin_convertvector(f2{x, y}, bh2);
       f.p[n][2 * j] = h[0];
       f.p[n][2 * j + 1] = h[1];
       if (n + 1 < NP) {
-        r[2 * j] -= static_cast<float>(h[0]);
-        r[2 * j + 1] -= static_cast<float>(h[1]);
+        x -= static_cast<float>(h[0]);
+        y -= static_cast<float>(h[1]);
       }
     }
+  }
 }
 // two tiles of a result below each other
 template <int NP>
@@ -63,16 +68,34 @@ __device__ __forceinline__ f4 mmp(const Parts<NA>& a, const Parts<NB>& b, f4 c) 
   return c;
 }
 
-// 64 rows of C bf16 in LDS, one plane for each part.  Row r starts at
-// r (2 C + 32) + 16 (r / 8) bytes, which is 32 (r % 8) + 16 (r / 8 % 2) modulo
-// the 256 bytes of all banks: sixteen rows' reads of 8 bytes and eight rows'
-// transposing reads of 32 bytes both fall on different banks.
-template <int C>
-struct Rows64 {
-  static constexpr int ST = 2 * C + 32;
-  static constexpr int PLANE = 64 * ST + 128;
-  static __device__ __forceinline__ int at(int r, int c) { return r * ST + 16 * (r >> 3) + 2 * c; }
+// c[n] += a[n] b for C independent sums, so that no product waits for the one
+// before it
+template <int N, int NA, int NB, int C>
+__device__ __forceinline__ void mmp(f4 (&c)[C], const Parts<NA> (&a)[C], const Parts<NB>& b) {
+#pragma unroll
+  for (int i = 0; i < NA; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      if (i + j < N)
+#pragma unroll
+        for (int n = 0; n < C; ++n) c[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[n].p[i], b.p[j], c[n], 0, 0, 0);
+}
 
+// 64 rows of C (64 or 128) bf16 in LDS, one plane for each part, without room
+// between them: of a row's 16-byte pieces, four follow each other and are
+// exchanged with the others as the row says, and the order of the four as well.
+// So sixteen rows' reads of a piece (4 cycles; the hardware takes lanes 0 .. 3,
+// 12 .. 15 and 20 .. 27 together, and so on) fall on different banks, and eight
+// rows' transposing reads of halves of four pieces on each twice (4 cycles).
+// Natural: tiles are read by rows 16 i + lane % 16, else as tile_row() says.
+template <int C, bool NATURAL = false>
+struct Rows64 {
+  static constexpr int RB = 2 * C, PLANE = 64 * RB, X = C / 32;
+  static __device__ __forceinline__ int turn(int r) { return C == 128 ? r & 3 : (r >> 1) & 1; }
+  static __device__ __forceinline__ int at(int r, int c) {   // c a multiple of 8
+    const int t = (r >> (NATURAL ? 3 : 4)) & 1 ? 3 : 0;
+    return r * RB + (((c >> 3) ^ (4 * turn(r)) ^ t) << 4);
+  }
   // rows r, columns c .. c + 7 (c a multiple of 8)
   template <int NP>
   static __device__ __forceinline__ void put(char* lds, int r, int c, const float* v) {
@@ -81,32 +104,38 @@ struct Rows64 {
 #pragma unroll
     for (int n = 0; n < NP; ++n) *reinterpret_cast<bh8*>(lds + n * PLANE + at(r, c)) = f.p[n];
   }
-  // operand with row (column) r0 + lane % 16 and k = columns c0 .. c0 + 31
+  // a lane's addresses of operands by row and by column, for each 32 columns
+  struct Lane {
+    int row[X], col[X];
+    __device__ __forceinline__ explicit Lane(int lane) {
+      const int u = (lane & 15) >> 2, v = lane & 3, g = lane >> 4;
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        row[x] = (NATURAL ? lane & 15 : 8 * u + v) * RB + ((x ^ turn(v)) << 6) + ((g ^ (u & 2 ? 3 : 0)) << 4);
+        col[x] = (8 * g + u) * RB + ((x ^ turn(u)) << 6) + ((v ^ (g & 2 ? 3 : 0)) << 4);
+      }
+    }
+  };
+  // rows of tile i, k = columns 32 x ..
   template <int NP>
-  static __device__ __forceinline__ Parts<NP> by_row(const char* lds, int r0, int c0, int lane) {
-    const char* a = lds + at(lane & 15, 4 * (lane >> 4)) + r0 * ST + 16 * (r0 >> 3) + 2 * c0;
+  static __device__ __forceinline__ Parts<NP> by_row(const char* lds, const Lane& l, int i, int x) {
+    const char* a = lds + l.row[x] + (NATURAL ? 16 * i : 32 * (i >> 1) + 4 * (i & 1)) * RB;
     Parts<NP> f;
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      const uint2 x = *reinterpret_cast<const uint2*>(a + n * PLANE);
-      const uint2 y = *reinterpret_cast<const uint2*>(a + n * PLANE + 32);
-      f.p[n] = __builtin_bit_cast(bh8, uint4{x.x, x.y, y.x, y.y});
-    }
+    for (int n = 0; n < NP; ++n) f.p[n] = *reinterpret_cast<const bh8*>(a + n * PLANE);
     return f;
   }
-  // operand with row (column) c0 + lane % 16 and k = rows r0 .. r0 + 31
-  // (transposing reads: sixteen lanes point at four rows of sixteen elements,
-  // four each, and lane i receives column i)
+  // columns of tile i, k = rows 32 x .. (transposing reads: sixteen lanes point
+  // at four rows of sixteen elements, four each, and lane i receives column i)
   template <int NP>
-  static __device__ __forceinline__ Parts<NP> by_col(const char* lds, int r0, int c0, int lane) {
-    const int i = lane & 15;
-    const char* a = lds + at(4 * (lane >> 4) + (i >> 2), 4 * (i & 3)) + r0 * ST + 16 * (r0 >> 3) + 2 * c0;
+  static __device__ __forceinline__ Parts<NP> by_col(const char* lds, const Lane& l, int i, int x) {
+    const char* a = lds + l.col[i >> 1] + 32 * x * RB + 8 * (i & 1);
     Parts<NP> f;
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
-      const s4v x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((M3_LDS s4v*)(a + n * PLANE));
-      const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((M3_LDS s4v*)(a + n * PLANE + 16 * ST + 32));
-      f.p[n] = __builtin_bit_cast(bh8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+      const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((M3_LDS s4v*)(a + n * PLANE));
+      const s4v z = __builtin_amdgcn_ds_read_tr16_b64_v4i16((M3_LDS s4v*)(a + n * PLANE + 4 * RB));
+      f.p[n] = __builtin_bit_cast(bh8, __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7));
     }
     return f;
   }
@@ -114,58 +143,70 @@ struct Rows64 {
 
 // A 64x64 matrix that holds two triangles: T strictly below the diagonal (its
 // diagonal is 1) and P, transposed, on and above it.  An operand of one of them
-// keeps its own side of the diagonal's tiles: masks for the lane's elements of
-// such a tile.
+// on the diagonal keeps its own side, by masks: of its row 8 u + 4 a + v (tile
+// a of two) and columns 8 g + j those with j < 4 a + v (P: <=) where g is u,
+// all before, none behind.
 struct Triangle {
-  uint32_t low[2];    // by_row: columns before the lane's row
-  uint32_t upto[2];   // by_col: rows up to the lane's column
+  uint32_t before, upto, below[2], on[2];
   __device__ __forceinline__ explicit Triangle(int lane) {
-    const int r = lane & 15, g = lane >> 4;
+    const int u = (lane & 15) >> 2, v = lane & 3, g = lane >> 4;
+    before = g < u ? ~0u : 0u;
+    upto = g <= u ? ~0u : 0u;
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      low[p] = (4 * g + 2 * p < r ? 0xffffu : 0u) | (4 * g + 2 * p + 1 < r ? 0xffff0000u : 0u);
-      upto[p] = (4 * g + 2 * p <= r ? 0xffffu : 0u) | (4 * g + 2 * p + 1 <= r ? 0xffff0000u : 0u);
+      below[p] = before | (g == u ? (2 * p < v ? 0xffffu : 0u) | (2 * p + 1 < v ? 0xffff0000u : 0u) : 0u);
+      on[p] = before | (g == u ? (2 * p <= v ? 0xffffu : 0u) | (2 * p + 1 <= v ? 0xffff0000u : 0u) : 0u);
     }
   }
-  // the tile of the diagonal is the first (FIRST) or the second of the operand's
-  // two; behind a first one nothing is left
-  template <bool FIRST, int NP>
-  static __device__ __forceinline__ void keep(Parts<NP>& f, const uint32_t* m) {
+  __device__ __forceinline__ void keep(Parts<1>& f, int a, const uint32_t* m) const {
+    uint4 u = __builtin_bit_cast(uint4, f.p[0]);
+    u.x &= a ? upto : m[0];
+    u.y &= a ? upto : m[1];
+    u.z &= a ? m[0] : before;
+    u.w &= a ? m[1] : before;
+    f.p[0] = __builtin_bit_cast(bh8, u);
+  }
+  // part n of the six operands of T or P below or on the diagonal: tiles of rows
+  // and blocks of 32 columns (0, 0), (1, 0), (2, 0), (3, 0), (2, 1), (3, 1)
+  using M = Rows64<64>;
+  __device__ __forceinline__ void t6(Parts<1> (&f)[6], const char* lds, const M::Lane& l, int n) const {
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-      uint4 u = __builtin_bit_cast(uint4, f.p[n]);
-      if (FIRST) {
-        u.x &= m[0];
-        u.y &= m[1];
-        u.z = u.w = 0u;
-      } else {
-        u.z &= m[0];
-        u.w &= m[1];
-      }
-      f.p[n] = __builtin_bit_cast(bh8, u);
+    for (int k = 0; k < 6; ++k) {
+      f[k] = M::by_row<1>(lds + n * M::PLANE, l, k < 4 ? k : k - 2, k < 4 ? 0 : 1);
+      if (k < 2 || k >= 4) keep(f[k], k & 1, below);
     }
   }
-  // rows 16 it .. of T, columns 32 s .. (s <= it / 2)
-  template <int NP>
-  __device__ __forceinline__ Parts<NP> t(const char* lds, int it, int s, int lane) const {
-    Parts<NP> f = Rows64<64>::by_row<NP>(lds, 16 * it, 32 * s, lane);
-    if (s == it / 2) {
-      if (it & 1) keep<false, NP>(f, low);
-      else keep<true, NP>(f, low);
+  __device__ __forceinline__ void p6(Parts<1> (&f)[6], const char* lds, const M::Lane& l, int n) const {
+#pragma unroll
+    for (int k = 0; k < 6; ++k) {
+      f[k] = M::by_col<1>(lds + n * M::PLANE, l, k < 4 ? k : k - 2, k < 4 ? 0 : 1);
+      if (k < 2 || k >= 4) keep(f[k], k & 1, on);
     }
-    return f;
-  }
-  // rows 16 it .. of P, columns 32 s ..
-  template <int NP>
-  __device__ __forceinline__ Parts<NP> p(const char* lds, int it, int s, int lane) const {
-    Parts<NP> f = Rows64<64>::by_col<NP>(lds, 32 * s, 16 * it, lane);
-    if (s == it / 2) {
-      if (it & 1) keep<false, NP>(f, upto);
-      else keep<true, NP>(f, upto);
-    }
-    return f;
   }
 };
+
+// c += (a triangle's part n) b over the six operands, c[4], c[5] for the second
+// half of the columns; the parts j of b with n + j < N
+template <int N, int NB>
+__device__ __forceinline__ void mm6(f4 (&c)[6], const Parts<1> (&a)[6], const Parts<NB> (&b)[2], int n) {
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+    if (n + j < N)
+#pragma unroll
+      for (int k = 0; k < 6; ++k) c[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[k].p[0], b[k < 4 ? 0 : 1].p[j], c[k], 0, 0, 0);
+}
+
+// The order of a region's instructions: RD reads of LDS, then products with V
+// others behind each, in whose time they run.
+template <int RD, int MM, int V>
+__device__ __forceinline__ void interleave() {
+  if constexpr (RD > 0) __builtin_amdgcn_sched_group_barrier(0x100, RD, 0);
+#pragma unroll
+  for (int i = 0; i < MM; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+  }
+}
 
 // parts of an input in T, and of a computed operand that only reaches outputs in T
 template <typename T>
@@ -174,21 +215,37 @@ struct DeltaParts {
   static constexpr int OUT = sizeof(T) == 2 ? 2 : 3;
 };
 
-// the rows of a sequence and its first slot
-struct DeltaSeq {
-  int64_t row0;
-  int len, slot0;
-  __device__ __forceinline__ DeltaSeq(const DeltaArgs& a, int s) {
+// A segment of a sequence's chunks, by its slot; s = -1: the slot has none.  An
+// empty sequence has one segment without chunks.
+struct DeltaSeg {
+  int s, j;         // sequence, segment of it
+  int c0, nch;      // its first chunk, its chunks
+  int len, slot0;   // the sequence's rows and first chunk slot
+  bool last;        // the sequence's last segment
+  int64_t row0;     // the sequence's first row
+  __device__ __forceinline__ DeltaSeg(const DeltaArgs& a, int slot, int lane) {
     if (a.cu) {
+      const Slot x = slot_of(a.cu, a.B, a.T, min(31, 6 + a.lseg), slot, lane);
+      s = x.s;
+      j = x.tile;
+      if (s < 0) return;
       const int b = clamp_row(a.cu[s], a.T), e = clamp_row(a.cu[s + 1], a.T);
       row0 = b;
       len = max(0, e - b);
       slot0 = b / kDeltaChunk + s;
     } else {
+      const int per = a.nseg / a.B;
+      s = slot / per;
+      j = slot - s * per;
       row0 = static_cast<int64_t>(s) * a.T;
       len = a.T;
       slot0 = s * ((a.T + kDeltaChunk - 1) / kDeltaChunk);
     }
+    const int all = (len + kDeltaChunk - 1) / kDeltaChunk;
+    c0 = a.lseg > 24 ? 0 : j << a.lseg;
+    nch = a.lseg > 24 ? all : min(1 << a.lseg, all - c0);
+    last = c0 + nch >= all;
+    if (j > 0 && nch <= 0) s = -1;
   }
 };
 // the rows of a chunk; n = 0: the slot has none
@@ -211,27 +268,81 @@ struct DeltaSlot {
   }
 };
 
+// The rows of a chunk in memory, as a buffer that ends behind the last one:
+// loads behind it give zeros and stores are dropped, so a chunk that is not
+// whole needs no other code.  Offsets are in bytes, below 2^32 (64 rows of less
+// than 2^24 elements).
+struct ChunkRows {
+  __amdgpu_buffer_rsrc_t rsrc;
+  template <typename T>
+  __device__ __forceinline__ ChunkRows(const T* p, int64_t ld, int n)
+      : rsrc(__builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(p), 0, static_cast<int>(static_cast<uint32_t>(n) * static_cast<uint32_t>(ld) * static_cast<uint32_t>(sizeof(T))), 0x00020000)) {}
+  __device__ __forceinline__ void load8(Vec8<bf16_t>& v, uint32_t off) const {
+    v.u = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
+  }
+  __device__ __forceinline__ void load8(Vec8<float>& v, uint32_t off) const {
+    v.a = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0));
+    v.b = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, off + 16, 0, 0));
+  }
+  __device__ __forceinline__ void load1(Raw1<bf16_t>& v, uint32_t off) const {
+    v.u = __builtin_amdgcn_raw_buffer_load_b16(rsrc, off, 0, 0);
+  }
+  __device__ __forceinline__ void load1(Raw1<float>& v, uint32_t off) const {
+    v.v = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rsrc, off, 0, 0));
+  }
+  __device__ __forceinline__ void store1(bf16_t, uint32_t off, float v) const {
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v)), rsrc, off, 0, 0);
+  }
+  __device__ __forceinline__ void store1(float, uint32_t off, float v) const {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rsrc, off, 0, 0);
+  }
+};
+
+// eight elements of an input as they are stored: bf16 as loaded, fp32 in parts
+template <class R>
+__device__ __forceinline__ void put_raw(char* lds, int r, int c, const Vec8<bf16_t>& v) {
+  *reinterpret_cast<uint4*>(lds + R::at(r, c)) = v.u;
+}
+template <class R>
+__device__ __forceinline__ void put_raw(char* lds, int r, int c, const Vec8<float>& v) {
+  float f[8];
+  v.get(f);
+  R::template put<3>(lds, r, c, f);
+}
+
 // 64 rows of C elements on their way to LDS through the registers of NT
 // threads; rows from n on are zeros
-template <typename T, int C, int NT>
+template <typename T, int C, int NT, bool NATURAL = false>
 struct Stage {
-  static constexpr int N = 64 * C / 8 / NT;
+  using R = Rows64<C, NATURAL>;
+  static constexpr int N = 64 * C / 8 / NT, RPI = NT * 8 / C;   // rows of one load
   Vec8<T> v[N];
   __device__ __forceinline__ void load(const T* p, int64_t ld, int n) {
+    const ChunkRows rows(p, ld, n);
+    const uint32_t r = threadIdx.x / (C / 8), c = threadIdx.x % (C / 8) * 8;
+    const uint32_t row = static_cast<uint32_t>(ld) * static_cast<uint32_t>(sizeof(T));
+    const uint32_t off = r * row + c * static_cast<uint32_t>(sizeof(T));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int x = threadIdx.x + i * NT, r = x / (C / 8), c = x % (C / 8) * 8;
-      v[i].load(p + min(r, n - 1) * ld + c);
-    }
+    for (int i = 0; i < N; ++i) rows.load8(v[i], off + i * RPI * row);
   }
-  __device__ __forceinline__ void store(char* lds, int n) const {
+  __device__ __forceinline__ void store(char* lds) const {
+    const int r = threadIdx.x / (C / 8), c = threadIdx.x % (C / 8) * 8;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int x = threadIdx.x + i * NT, r = x / (C / 8), c = x % (C / 8) * 8;
-      float f[8];
-      v[i].get(f, r < n);
-      Rows64<C>::template put<DeltaParts<T>::IN>(lds, r, c, f);
-    }
+    for (int i = 0; i < N; ++i) put_raw<R>(lds, r + i * RPI, c, v[i]);
+  }
+};
+
+// A wave's 16 columns of 64 rows, in the layout of results (element 4 i + e of
+// tile i).  p is the first row's first column.
+template <typename T>
+struct Cols {
+  Raw1<T> v[16];
+  __device__ __forceinline__ void load(const T* p, int64_t ld, int n, int col, int g) {
+    const ChunkRows rows(p, ld, n);
+    const uint32_t row = static_cast<uint32_t>(ld) * static_cast<uint32_t>(sizeof(T));
+    const uint32_t off = 8 * g * row + col * static_cast<uint32_t>(sizeof(T));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) rows.load1(v[i], off + tile_row(i / 4, i % 4) * row);
   }
 };
 

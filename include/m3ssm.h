@@ -503,9 +503,10 @@ size_t m3_delta_scan_workspace_size(const m3_delta_dims* dims, int packed);
  *   o       as v, dense
  *   hT      [Bsz, Hv, Dk, Dv] fp32, the state after the last token (NULL: not
  *           written)
- *   states  the state before every chunk of M3_DELTA_CHUNK tokens, for the
- *           backward pass (NULL: not written): [slots, Hv, Dk, Dv] fp32 with
- *           slots = Bsz ceil(T / M3_DELTA_CHUNK), of a packed call
+ *   states  for the backward pass (NULL: not written): of every chunk of
+ *           M3_DELTA_CHUNK tokens the state before it [Dk, Dv] and the u of its
+ *           tokens [M3_DELTA_CHUNK, Dv], [slots, Hv, Dk + M3_DELTA_CHUNK, Dv]
+ *           fp32 with slots = Bsz ceil(T / M3_DELTA_CHUNK), of a packed call
  *           floor(T / M3_DELTA_CHUNK) + S, of which those that no chunk takes
  *           are left as they are
  * h0 [Bsz, Hv, Dk, Dv] fp32 or NULL (zero), may alias hT.  An empty sequence's
@@ -519,6 +520,19 @@ m3_status m3_delta_scan(const m3_delta_dims* dims, const int32_t* cu_seqlens, co
                         const void* k, const void* v, const void* g, const void* beta,
                         const float* h0, void* o, float* hT, float* states, void* ws,
                         size_t ws_bytes, void* stream);
+
+size_t m3_delta_scan_backward_workspace_size(const m3_delta_dims* dims, int packed);
+
+/* Gradients for L = <o, d_o> + <hT, dhT> (dhT NULL = 0), with `states` as
+ * m3_delta_scan wrote them for the same inputs and d_o dense: dq, dk, dv, dg,
+ * dbeta in dtype, dense, and dh0 fp32 (NULL: not written).  The value heads of
+ * a head of q and k are summed in order (no atomics): equal calls return equal
+ * bits. */
+m3_status m3_delta_scan_backward(const m3_delta_dims* dims, const int32_t* cu_seqlens,
+                                 const void* q, const void* k, const void* v, const void* g,
+                                 const void* beta, const float* states, const void* d_o,
+                                 const float* dhT, void* dq, void* dk, void* dv, void* dg,
+                                 void* dbeta, float* dh0, void* ws, size_t ws_bytes, void* stream);
 
 /* One token per sequence: h [Bsz, Hv, Dk, Dv] fp32 advances in place by q, k
  * [Bsz, Hk, Dk], v [Bsz, Hv, Dv], g, beta [Bsz, Hv]; o [Bsz, Hv, Dv].

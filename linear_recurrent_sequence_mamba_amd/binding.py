@@ -179,6 +179,7 @@ def _lib():
                 ("m3_gated_scan_backward_workspace_size", [gp, i32]),
                 ("m3_qk_norm_rope_backward_workspace_size", [qp]),
                 ("m3_delta_scan_workspace_size", [ep, i32]),
+                ("m3_delta_scan_backward_workspace_size", [ep, i32]),
                 ("m3_block_norm_backward_workspace_size", [bp]),
                 ("m3_attn_prefill_varlen_workspace_size", [ap]),
                 ("m3_attn_prefill_varlen_backward_workspace_size", [ap]),
@@ -192,6 +193,7 @@ def _lib():
                 ("m3_qk_norm_rope", [qp] + [vp] * 8),
                 ("m3_qk_norm_rope_backward", [qp] + [vp] * 12 + [sz, vp]),
                 ("m3_delta_scan", [ep] + [vp] * 11 + [sz, vp]),
+                ("m3_delta_scan_backward", [ep] + [vp] * 16 + [sz, vp]),
                 ("m3_delta_step", [ep] + [vp] * 8),
                 ("m3_block_norm", [bp] + [vp] * 9),
                 ("m3_block_norm_backward", [bp] + [vp] * 15 + [sz, vp]),
@@ -1035,6 +1037,10 @@ def _delta_setup(q, k, v, g, beta, scale, cu_seqlens):
     return d, ref, packed, slots
 
 
+def _delta_states(d, slots):
+    return (slots, d.nheads_v, d.headdim_k + M3_DELTA_CHUNK, d.headdim_v)
+
+
 def delta_scan(q, k, v, g, beta, h0=None, scale=None, cu_seqlens=None, want_hT=True,
                want_states=False, stream=None):
     """The gated delta rule over q, k [Bsz, T, Hk, Dk], v [Bsz, T, Hv, Dv], g
@@ -1049,7 +1055,9 @@ def delta_scan(q, k, v, g, beta, h0=None, scale=None, cu_seqlens=None, want_hT=T
     with _on(dev, stream):
         o = v.new_empty(v.shape)
         hT = v.new_empty(state, dtype=torch.float32) if want_hT else None
-        st = v.new_empty((slots,) + state[1:], dtype=torch.float32) if want_states else None
+        st = None
+        if want_states:
+            st = v.new_empty(_delta_states(d, slots), dtype=torch.float32)
         ws = _ws(lib.m3_delta_scan_workspace_size(ref, packed), "m3_delta_scan", q)
         e = lib.m3_delta_scan(ref, _addr(cu_seqlens), _addr(q), _addr(k), _addr(v), _addr(g),
                               _addr(beta), _addr(h0), _addr(o), _addr(hT), _addr(st), _addr(ws),
@@ -1057,6 +1065,35 @@ def delta_scan(q, k, v, g, beta, h0=None, scale=None, cu_seqlens=None, want_hT=T
     if e != 0:
         raise M3Error(e, "m3_delta_scan")
     return o, hT, st
+
+
+def delta_scan_backward(q, k, v, g, beta, d_o, states, h0=None, dhT=None, scale=None,
+                        cu_seqlens=None, stream=None) -> dict:
+    """Gradients of delta_scan (m3_delta_scan_backward): a dict with q, k, v,
+    g, beta in their dtype and (if h0 is given) h0 in fp32.  Rows that no
+    sequence covers are not written."""
+    dev = _same_device("q k v g beta d_o states h0 dhT cu_seqlens", q, k, v, g, beta, d_o, states,
+                       h0, dhT, cu_seqlens)
+    d, ref, packed, slots = _delta_setup(q, k, v, g, beta, scale, cu_seqlens)
+    state = (d.batch, d.nheads_v, d.headdim_k, d.headdim_v)
+    _dense("h0", h0, state, torch.float32, optional=True)
+    _dense("dhT", dhT, state, torch.float32, optional=True)
+    _dense("d_o", d_o, v.shape, v.dtype)
+    _dense("states", states, _delta_states(d, slots), torch.float32)
+    lib = _lib()
+    with _on(dev, stream):
+        r = {n: t.new_empty(t.shape) for n, t in (("q", q), ("k", k), ("v", v), ("g", g),
+                                                  ("beta", beta))}
+        r["h0"] = None if h0 is None else h0.new_empty(state)
+        ws = _ws(lib.m3_delta_scan_backward_workspace_size(ref, packed),
+                 "m3_delta_scan_backward", q)
+        e = lib.m3_delta_scan_backward(
+            ref, _addr(cu_seqlens), _addr(q), _addr(k), _addr(v), _addr(g), _addr(beta),
+            _addr(states), _addr(d_o), _addr(dhT), _addr(r["q"]), _addr(r["k"]), _addr(r["v"]),
+            _addr(r["g"]), _addr(r["beta"]), _addr(r["h0"]), _addr(ws), ws.numel(), _raw(dev))
+    if e != 0:
+        raise M3Error(e, "m3_delta_scan_backward")
+    return r
 
 
 def delta_step(h, q, k, v, g, beta, scale=None, o=None, stream=None):

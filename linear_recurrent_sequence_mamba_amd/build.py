@@ -18,8 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libm3ssm.so")
 SOURCES = ["api.cpp", "attn.hip", "attn_backward.hip", "backward.hip", "backward_mma.hip",
-           "block_norm.hip", "decode.hip", "decode_tokens.hip", "delta.hip", "gated.hip", "prefill.hip",
-           "qk_norm.hip"]
+           "block_norm.hip", "decode.hip", "decode_tokens.hip", "delta.hip", "delta_backward.hip",
+           "gated.hip", "prefill.hip", "qk_norm.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

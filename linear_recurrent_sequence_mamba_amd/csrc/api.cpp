@@ -970,6 +970,48 @@ m3_status m3_delta_scan(const m3_delta_dims* d, const int32_t* cu_seqlens, const
   return hip_status(m3::launch_delta_scan(a, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
 }
 
+size_t m3_delta_scan_backward_workspace_size(const m3_delta_dims* d, int packed) {
+  if (check_delta(d, true, packed != 0) != M3_OK) return 0;
+  return m3::delta_backward_workspace_bytes(d->batch, d->seqlen, d->nheads_v, d->headdim_k,
+                                            d->headdim_v, packed != 0);
+}
+
+m3_status m3_delta_scan_backward(const m3_delta_dims* d, const int32_t* cu_seqlens, const void* q,
+                                 const void* k, const void* v, const void* g, const void* beta,
+                                 const float* states, const void* d_o, const float* dhT, void* dq,
+                                 void* dk, void* dv, void* dg, void* dbeta, float* dh0, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  const bool packed = cu_seqlens != nullptr;
+  m3_status st = check_delta(d, true, packed);
+  if (st != M3_OK) return st;
+  if (!q || !k || !v || !g || !beta || !states || !d_o || !dq || !dk || !dv || !dg || !dbeta)
+    return M3_ERR_NULL;
+  const void* const ptrs[] = {q, k, v, states, d_o, dhT, dq, dk, dv, dg, dbeta, dh0, ws};
+  if (any_misaligned(ptrs) || misaligned4(cu_seqlens) || misaligned_gates(d, g, beta)) return M3_ERR_ALIGN;
+  if (!ws || ws_bytes < m3::delta_backward_workspace_bytes(d->batch, d->seqlen, d->nheads_v,
+                                                           d->headdim_k, d->headdim_v, packed))
+    return M3_ERR_WORKSPACE;
+  m3::DeltaArgs a = delta_args(d);
+  a.cu = cu_seqlens;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.g = g;
+  a.beta = beta;
+  a.cstates = states;
+  a.dout = d_o;
+  a.dhT = dhT;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dg = dg;
+  a.dbeta = dbeta;
+  a.dh0 = dh0;
+  m3::delta_backward_carve(a, ws);
+  return hip_status(
+      m3::launch_delta_backward(a, d->dtype == M3_BF16, static_cast<hipStream_t>(stream)));
+}
+
 m3_status m3_delta_step(const m3_delta_dims* d, float* h, const void* q, const void* k,
                         const void* v, const void* g, const void* beta, void* o, void* stream) {
   m3_status st = check_delta(d, false, false);

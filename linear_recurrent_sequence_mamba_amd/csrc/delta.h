@@ -9,6 +9,7 @@
 namespace m3 {
 
 constexpr int kDeltaChunk = 64;   // tokens of a chunk
+constexpr int kDeltaGates = 5 * 64;   // floats of a chunk's gates: exp(G), exp(G_end - G), beta, G in two parts
 
 struct DeltaArgs {
   const void *q, *k, *v, *g, *beta;   // token rows, ld* elements apart
@@ -16,10 +17,18 @@ struct DeltaArgs {
   const int32_t* cu;                  // packed: [B + 1] row offsets, else null
   void* o;                            // dense rows
   float* hT;                          // [B, Hv, Dk, Dv] or null
-  float* states;                      // [slots, Hv, Dk, Dv] or null
+  float* states;                      // [slots, Hv, Dk + 64, Dv] or null: the state before a chunk, then
+                                      // its u
+  // backward
+  const float *cstates, *dhT;
+  const void* dout;                   // dense rows
+  void *dq, *dk, *dv, *dg, *dbeta;    // dense rows
+  float* dh0;                         // [B, Hv, Dk, Dv] or null
   // workspace
   float* pm;                          // [slots, Hv, 64, 64]
-  float* gates;                       // [slots, Hv, 3, 64]
+  float* gates;                       // [slots, Hv, 5, 64]
+  float* after;                       // backward: gradients of the state behind a chunk [slots, Hv, Dk, Dv]
+  float* dr;                          // backward: those of R [slots, Hv, 64, Dv]
   float* ends;                        // segments' ends from a zero state, then the states before
                                       // them, in the order of results [segment slots, Hv, Dv / 16,
                                       // Dk / 16, 64, 4]
@@ -45,7 +54,11 @@ DeltaPlan delta_plan(int B, int T, int Hv, int Dv, bool packed);
 bool delta_supported(int Dk, int Dv);
 int64_t delta_slots(int B, int T, bool packed);
 size_t delta_workspace_bytes(int B, int T, int Hv, int Dk, int Dv, bool packed);
+size_t delta_backward_workspace_bytes(int B, int T, int Hv, int Dk, int Dv, bool packed);
 void delta_carve(DeltaArgs& a, void* ws);
+void delta_backward_carve(DeltaArgs& a, void* ws);
+hipError_t launch_delta_chunks(const DeltaArgs& a, int bf16, hipStream_t s);
+hipError_t launch_delta_backward(DeltaArgs& a, int bf16, hipStream_t s);
 hipError_t launch_delta_scan(DeltaArgs& a, int bf16, hipStream_t s);
 hipError_t launch_delta_step(const DeltaArgs& a, float* h, int bf16, hipStream_t s);
 

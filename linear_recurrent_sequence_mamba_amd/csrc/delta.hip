@@ -62,10 +62,13 @@ __global__ __launch_bounds__(256) void k_delta_chunk(DeltaArgs a) {
     sG[lane] = G;
     sB[lane] = bt;
     const double end = __shfl(G, 63, 64);
-    float* p = a.gates + (static_cast<int64_t>(slot) * a.Hv + h) * 192 + lane;
+    float* p = a.gates + (static_cast<int64_t>(slot) * a.Hv + h) * kDeltaGates + lane;
     p[0] = __builtin_amdgcn_exp2f(static_cast<float>(G));
     p[64] = __builtin_amdgcn_exp2f(static_cast<float>(end - G));
     p[128] = bt;
+    const float hi = static_cast<float>(G);
+    p[192] = hi;
+    p[256] = static_cast<float>(G - hi);
   }
   stage.store(sK);
   stage_q.store(sQ);
@@ -245,7 +248,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
     st.k.load(static_cast<const T*>(a.k) + first(c) * a.ldk + hk * DK, a.ldk, rows(c));
     st.m.load(a.pm + m * 4096, 64, 64);
 #pragma unroll
-    for (int i = 0; i < Tiles::NG; ++i) st.g[i] = (a.gates + m * 192)[min(threadIdx.x + i * NT, 191u)];
+    for (int i = 0; i < Tiles::NG; ++i) st.g[i] = (a.gates + m * kDeltaGates)[min(threadIdx.x + i * NT, 191u)];
     if constexpr (FULL) st.q.load(static_cast<const T*>(a.q) + first(c) * a.ldq + hk * DK, a.ldq, rows(c));
   };
   auto fetch_v = [&](int c) __attribute__((always_inline)) {
@@ -265,7 +268,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
     const float* sGate = reinterpret_cast<const float*>(buf + BK + BQ + BM);
     tiles_barrier();
     if (FULL && a.states) {
-      float* p = a.states + (static_cast<int64_t>(seg.slot0 + c) * a.Hv + h) * dd;
+      float* p = a.states + (static_cast<int64_t>(seg.slot0 + c) * a.Hv + h) * (dd + 64 * a.Dv);
 #pragma unroll
       for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -328,6 +331,13 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
     u[3] += u[5];
     // O = scale exp(G) Q S0 + P U
     if constexpr (FULL) {
+      if (a.states) {
+        float* p = a.states + (static_cast<int64_t>(seg.slot0 + c) * a.Hv + h) * (dd + 64 * a.Dv) + dd;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) (p + tile_row(i, e) * a.Dv)[at] = u[i][e];
+      }
       Parts<1> pa[2][6];
       tri.p6(pa[0], sM, ml, 0);
       f4 y[6];
@@ -643,9 +653,14 @@ hipError_t run_chain(const DeltaArgs& a, bool split, hipStream_t s) {
 }
 
 template <typename T, int DK>
-hipError_t run_scan(const DeltaArgs& a, bool split, hipStream_t s) {
+hipError_t run_chunks(const DeltaArgs& a, hipStream_t s) {
   k_delta_chunk<T, DK><<<static_cast<unsigned>(static_cast<int64_t>(a.nslot) * a.Hv), 256, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
+  return hipGetLastError();
+}
+
+template <typename T, int DK>
+hipError_t run_scan(const DeltaArgs& a, bool split, hipStream_t s) {
+  const hipError_t e = run_chunks<T, DK>(a, s);
   if (e != hipSuccess) return e;
   if constexpr (DK == 128 && sizeof(T) == 2)
     if (a.Dv == 128 && split) return run_chain<T, DK, 8>(a, split, s);
@@ -686,7 +701,7 @@ DeltaPlan delta_plan(int B, int T, int Hv, int Dv, bool packed) {
 
 size_t delta_workspace_bytes(int B, int T, int Hv, int Dk, int Dv, bool packed) {
   const DeltaPlan p = delta_plan(B, T, Hv, Dv, packed);
-  const size_t chunks = static_cast<size_t>(4096 + 192) * delta_slots(B, T, packed) * Hv;
+  const size_t chunks = static_cast<size_t>(4096 + kDeltaGates) * delta_slots(B, T, packed) * Hv;
   // (maps of two parts take no less than their room for three)
   const size_t segs = p.split ? (static_cast<size_t>(Dk) * (sizeof(float) * Dv + 3 * sizeof(uint16_t) * Dk) + sizeof(float) * 4) * p.nseg * Hv : 0;
   return sizeof(float) * chunks + segs;
@@ -699,9 +714,14 @@ void delta_carve(DeltaArgs& a, void* ws) {
   a.nslot = static_cast<int>(delta_slots(a.B, a.T, a.cu != nullptr));
   a.pm = static_cast<float*>(ws);
   a.gates = a.pm + static_cast<size_t>(4096) * a.nslot * a.Hv;
-  a.ends = a.gates + static_cast<size_t>(192) * a.nslot * a.Hv;
+  a.ends = a.gates + static_cast<size_t>(kDeltaGates) * a.nslot * a.Hv;
   a.maps = reinterpret_cast<uint16_t*>(a.ends + static_cast<size_t>(a.Dk) * a.Dv * a.nseg * a.Hv);
   a.decays = reinterpret_cast<float*>(a.maps + static_cast<size_t>(3) * a.Dk * a.Dk * a.nseg * a.Hv);
+}
+
+hipError_t launch_delta_chunks(const DeltaArgs& a, int bf16, hipStream_t s) {
+  if (bf16) return a.Dk == 64 ? run_chunks<bf16_t, 64>(a, s) : run_chunks<bf16_t, 128>(a, s);
+  return a.Dk == 64 ? run_chunks<float, 64>(a, s) : run_chunks<float, 128>(a, s);
 }
 
 hipError_t launch_delta_scan(DeltaArgs& a, int bf16, hipStream_t s) {

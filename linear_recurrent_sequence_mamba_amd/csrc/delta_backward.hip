@@ -1,0 +1,541 @@
+// delta_backward.hip -- the gradients of the gated delta rule (gfx950).
+//
+// With dO the gradient of the outputs, dS1 that of the state behind a chunk,
+// and the chunk's T, P and U as in the scan (P with the scale in it):
+//   dU = P^T dO + exp(G_end - G) K dS1,   dR = T^T dU,   dV = beta dR,
+//   dS0 = exp(G_end) dS1 + Q^T (scale exp(G) dO) - K^T (exp(G) dV)
+// is a chain over the chunks from the last to the first; and with
+//   dP = scale dO U^T (j <= i),  dA = -dR U^T (j < i),  Gamma_ij = exp(G_i - G_j),
+//   F = dP Gamma,  M = beta_i dA Gamma,  X1 = dO S0^T,  X2 = dR S0^T,  X3 = U dS1^T:
+//   dQ = scale exp(G) X1 + F K
+//   dK = F^T Q + (M + M^T) K - exp(G) beta X2 + exp(G_end - G) X3
+//   dbeta_i = dR_i.Y_i + sum_j dA_ij Gamma_ij k_i.k_j,   Y = V - exp(G) K S0
+// for each chunk by itself.  dR_i.Y_i is dR_i.v_i - exp(G_i) k_i.X2_i.  The
+// gradient through every exp(G) of a row adds up to
+//   dG_i = q_i.dq_i - k_i.dk_i + 2 (dR_i.U_i - dV_i.v_i),
+// to which the chunk's last row adds <S1, dS1> = sum_j exp(G_end - G_j) k_j.X3_j
+// + exp(G_end) <S0, dS1>; and dg_t = sum_{i >= t} dG_i.
+#include "delta_common.h"
+
+namespace m3 {
+namespace {
+
+// ---------------------------------------------------------------------------
+// The chain, as the scan's: a wave holds 16 columns of dS.
+template <typename T, int DK, int NW, int NBUF>
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_chain(DeltaArgs a) {
+  using X = Rows64<DK>;
+  using M = Rows64<64>;
+  constexpr int NT = 64 * NW, KS = DK / 32, DT = DK / 16, NI = DeltaParts<T>::IN;
+  constexpr int BK = NI * X::PLANE, BM = 3 * M::PLANE, BUF = 2 * BK + BM + 768, NG = (192 + NT - 1) / NT;
+  __shared__ __align__(16) char smem[NBUF * BUF];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int nsl = a.Dv / (16 * NW), n0 = blockIdx.x / nsl;
+  const int h = n0 % a.Hv, s = n0 / a.Hv, hk = h / (a.Hv / a.Hk);
+  const int col = 16 * ((blockIdx.x % nsl) * NW + w) + r;
+  const DeltaSeg seg(a, s, lane);   // (the whole sequence)
+  if (seg.s < 0) return;
+  const Triangle tri(lane);
+  const typename X::Lane xl(lane);
+  const M::Lane ml(lane);
+  const int64_t head = static_cast<int64_t>(seg.s) * a.Hv + h, dd = static_cast<int64_t>(DK) * a.Dv;
+  const uint32_t at = static_cast<uint32_t>(8 * g * a.Dv + col);
+  const int ldo = a.Hv * a.Dv;
+
+  f4 S[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[t][e] = a.dhT ? (a.dhT + head * dd + tile_row(t, e) * a.Dv)[at] : 0.0f;
+
+  Stage<T, DK, NT> stK, stQ;
+  Stage<float, 64, NT> stM;
+  float stG[NG];
+  Cols<T> stO;
+  auto rows = [&](int c) __attribute__((always_inline)) { return min(kDeltaChunk, seg.len - c * kDeltaChunk); };
+  auto first = [&](int c) __attribute__((always_inline)) { return seg.row0 + static_cast<int64_t>(c) * kDeltaChunk; };
+  auto fetch = [&](int c) __attribute__((always_inline)) {
+    c = max(c, 0);
+    const int64_t m = static_cast<int64_t>(seg.slot0 + c) * a.Hv + h;
+    stK.load(static_cast<const T*>(a.k) + first(c) * a.ldk + hk * DK, a.ldk, rows(c));
+    stM.load(a.pm + m * 4096, 64, 64);
+#pragma unroll
+    for (int i = 0; i < NG; ++i) stG[i] = (a.gates + m * kDeltaGates)[min(threadIdx.x + i * NT, 191u)];
+    stQ.load(static_cast<const T*>(a.q) + first(c) * a.ldq + hk * DK, a.ldq, rows(c));
+  };
+  auto fetch_o = [&](int c) __attribute__((always_inline)) {
+    c = max(c, 0);
+    stO.load(static_cast<const T*>(a.dout) + first(c) * ldo + h * a.Dv, ldo, rows(c), col, g);
+  };
+  auto store = [&](char* b) __attribute__((always_inline)) {
+    stK.store(b);
+    stQ.store(b + BK);
+    stM.store(b + 2 * BK);
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+      if (threadIdx.x + i * NT < 192) reinterpret_cast<float*>(b + 2 * BK + BM)[threadIdx.x + i * NT] = stG[i];
+  };
+  if (seg.nch > 0) {
+    fetch(seg.nch - 1);
+    fetch_o(seg.nch - 1);
+    store(smem);
+    fetch(seg.nch - 2);
+  }
+  char* buf = smem;
+  for (int c = seg.nch - 1; c >= 0; --c) {
+    const char *sK = buf, *sQ = buf + BK, *sM = buf + 2 * BK;
+    const float* sGate = reinterpret_cast<const float*>(buf + 2 * BK + BM);
+    const int64_t m = static_cast<int64_t>(seg.slot0 + c) * a.Hv + h;
+    tiles_barrier();
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) (a.after + m * dd + tile_row(t, e) * a.Dv)[at] = S[t][e];
+    // K dS1
+    f4 ks[4];
+    Parts<NI> ka[2][4];
+    Parts<3> sp[2];
+    auto read = [&](int x) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ka[x & 1][i] = X::template by_row<NI>(sK, xl, i, x);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ks[i] = f4{0, 0, 0, 0};
+    read(0);
+    split_d<3>(sp[0], S[0], S[1]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+      if (x + 1 < KS) {
+        read(x + 1);
+        split_d<3>(sp[(x + 1) & 1], S[2 * x + 2], S[2 * x + 3]);
+      }
+      mmp<3>(ks, ka[x & 1], sp[x & 1]);
+      if constexpr (NI == 1) interleave<4, 12, 4>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // dU = P^T dO + exp(G_end - G) K dS1
+    Parts<1> ta[2][6];
+    tri.pt6(ta[0], sM, ml, 0);
+    f4 u[6], o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f4 en = *reinterpret_cast<const f4*>(&sGate[64 + tile_row(i, 0) + 8 * g]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        o[i][e] = stO.v[4 * i + e].f();
+        u[i][e] = en[e] * ks[i][e];
+      }
+    }
+    u[4] = u[5] = f4{0, 0, 0, 0};
+    Parts<NI> op[2];
+    split_d<NI>(op[0], o[0], o[1]);
+    split_d<NI>(op[1], o[2], o[3]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      if (n < 2) tri.pt6(ta[(n + 1) & 1], sM, ml, n + 1);
+      else tri.tt6(ta[(n + 1) & 1], sM, ml, 0);
+      mmt6<3>(u, ta[n & 1], op, n);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    u[0] += u[4];
+    u[1] += u[5];
+    // dR = T^T dU: dU itself for the diagonal
+    Parts<3> up[2];
+    split_d<3>(up[0], u[0], u[1]);
+    split_d<3>(up[1], u[2], u[3]);
+    u[4] = u[5] = f4{0, 0, 0, 0};
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      if (n < 2) tri.tt6(ta[n & 1], sM, ml, n + 1);
+      mmt6<3>(u, ta[(n + 1) & 1], up, n);
+      if (n == 0 && NBUF == 2) {
+        buf = buf == smem ? smem + BUF : smem;
+        store(buf);   // (the last time unread)
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    u[0] += u[4];
+    u[1] += u[5];
+    // dV = beta dR, and what adds to dS0
+    {
+      const ChunkRows dv(static_cast<T*>(a.dv) + first(c) * ldo + h * a.Dv, ldo, rows(c));
+      const uint32_t orow = static_cast<uint32_t>(ldo) * static_cast<uint32_t>(sizeof(T));
+      const uint32_t oat = 8 * g * orow + col * static_cast<uint32_t>(sizeof(T));
+      float* dr = a.dr + m * 64 * a.Dv;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f4 st = *reinterpret_cast<const f4*>(&sGate[tile_row(i, 0) + 8 * g]);
+        const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + tile_row(i, 0) + 8 * g]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          (dr + tile_row(i, e) * a.Dv)[at] = u[i][e];
+          u[i][e] *= bt[e];
+          dv.store1(T{}, oat + tile_row(i, e) * orow, u[i][e]);
+          u[i][e] *= -st[e];
+          o[i][e] *= a.scale * st[e];
+        }
+      }
+    }
+    fetch_o(c - 1);
+    // dS0
+    Parts<NI> kc[2][4];
+    auto read_t = [&](int n) __attribute__((always_inline)) {   // four tiles of dS, 32 rows of K, then of Q
+      const char* tile = n < DT / 2 ? sK : sQ;
+      const int k = n % (DT / 2);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        kc[n & 1][t] = X::template by_col<NI>(tile, xl, 4 * (k % (DT / 4)) + t, k / (DT / 4));
+    };
+    Parts<3> ep[2];
+    read_t(0);
+    const float last = sGate[63];
+    split_d<3>(ep[0], u[0], u[1]);
+    split_d<3>(ep[1], u[2], u[3]);
+#pragma unroll
+    for (int t = 0; t < DT; ++t) S[t] *= last;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < DT; ++n) {
+      if (n + 1 < DT) read_t(n + 1);
+      const int k = n % (DT / 2);
+      if (n == DT / 2) {
+        split_d<3>(ep[0], o[0], o[1]);
+        split_d<3>(ep[1], o[2], o[3]);
+      }
+      mmp<3>(*reinterpret_cast<f4(*)[4]>(&S[4 * (k % (DT / 4))]), kc[n & 1], ep[k / (DT / 4)]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (NBUF == 1) {
+      tiles_barrier();
+      store(buf);
+    }
+    fetch(c - 2);
+  }
+  if (a.dh0)
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) (a.dh0 + head * dd + tile_row(t, e) * a.Dv)[at] = S[t][e];
+}
+
+// ---------------------------------------------------------------------------
+// The gradients of q, k, g and beta of a chunk and a head of k, its value heads
+// one after another.  Wave w has the 16 channels tile_row(w, ..) of q and k, so
+// it reads 16 rows of S0 and dS1 straight from memory; the products over value
+// channels (X1, X2, X3, dP, dA) go by 64 of them with dO, dR and U in LDS, where
+// K, Q, F and M + M^T follow.  dP and dA have twelve tiles (two rows of two
+// blocks of 32 by 32, lower), which the waves share.
+template <typename T, int DK>
+struct GradTiles {
+  using M = Rows64<64>;
+  static constexpr int NI = DeltaParts<T>::IN, NO = DeltaParts<T>::OUT;
+  static constexpr int ONE = (NI + 2 * NO) * M::PLANE;
+  static constexpr int TWO = 2 * NI * Rows64<DK>::PLANE + 2 * NO * M::PLANE;
+  static constexpr int BYTES = ONE > TWO ? ONE : TWO;
+};
+
+// tiles (i, j) of the lower half, n = 0 .. 11
+__device__ __forceinline__ constexpr int tile_i(int n) { return n < 4 ? n >> 1 : 2 + ((n - 4) >> 2); }
+__device__ __forceinline__ constexpr int tile_j(int n) { return n < 4 ? n & 1 : (n - 4) & 3; }
+
+template <typename T, int DK>
+__global__ __launch_bounds__(4 * DK, 2) void k_delta_grads(DeltaArgs a) {
+  using X = Rows64<DK>;
+  using M = Rows64<64>;
+  using G = GradTiles<T, DK>;
+  constexpr int NI = G::NI, NO = G::NO, NW = DK / 16, NT = 64 * NW, NTILE = (12 + NW - 1) / NW;
+  __shared__ __align__(16) char smem[G::BYTES];
+  __shared__ float sGate[kDeltaGates], sRow[3][NW][64], sE[4][64], sU[64], sV[64], sEnd[NW];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int hk = blockIdx.x % a.Hk, slot = blockIdx.x / a.Hk, group = a.Hv / a.Hk;
+  const DeltaSlot sl(a, slot, lane);
+  if (sl.n <= 0) return;
+  const typename X::Lane xl(lane);
+  const M::Lane ml(lane);
+  const int ldo = a.Hv * a.Dv;
+  char *sO = smem, *sR = smem + NI * M::PLANE, *sUt = sR + NO * M::PLANE;
+  char *sK = smem, *sQ = smem + NI * X::PLANE, *sF = smem + 2 * NI * X::PLANE, *sN = sF + NO * M::PLANE;
+  const int dkr = 32 * (w >> 1) + 8 * (r >> 2) + 4 * (w & 1) + (r & 3);   // the lane's channel of q and k
+  f4 dq[4], dk[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dq[i] = dk[i] = f4{0, 0, 0, 0};
+
+  for (int h = hk * group; h < (hk + 1) * group; ++h) {
+    const int64_t m = static_cast<int64_t>(slot) * a.Hv + h, dd = static_cast<int64_t>(DK) * a.Dv;
+    const float* S0 = a.cstates + m * (dd + 64 * a.Dv) + static_cast<int64_t>(dkr) * a.Dv + 8 * g;
+    const float* dS = a.after + m * dd + static_cast<int64_t>(dkr) * a.Dv + 8 * g;
+    f4 x1[4], x2[4], x3[4], dp[NTILE], da[NTILE];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x1[i] = x2[i] = x3[i] = f4{0, 0, 0, 0};
+#pragma unroll
+    for (int n = 0; n < NTILE; ++n) dp[n] = da[n] = f4{0, 0, 0, 0};
+    float both = 0.0f;   // of <S0, dS1>
+    constexpr int VN = 512 / NT;
+    float vdot[VN];
+#pragma unroll
+    for (int n = 0; n < VN; ++n) vdot[n] = 0.0f;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kDeltaGates; i += NT) sGate[i] = (a.gates + m * kDeltaGates)[i];
+    for (int c0 = 0; c0 < a.Dv; c0 += 64) {
+      Stage<T, 64, NT> so, sv;
+      Stage<float, 64, NT> sr, su;
+      so.load(static_cast<const T*>(a.dout) + sl.row0 * ldo + h * a.Dv + c0, ldo, sl.n);
+      sv.load(static_cast<const T*>(a.v) + sl.row0 * a.ldv + h * a.Dv + c0, a.ldv, sl.n);
+      sr.load(a.dr + m * 64 * a.Dv + c0, a.Dv, 64);
+      su.load(a.cstates + m * (dd + 64 * a.Dv) + dd + c0, a.Dv, 64);
+      Vec8<float> vs[2], vd[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        vs[x].load(S0 + c0 + 32 * x);
+        vd[x].load(dS + c0 + 32 * x);
+      }
+      if (c0 > 0) __syncthreads();
+      so.store(sO);
+#pragma unroll
+      for (int n = 0; n < VN; ++n) {
+        const int row = threadIdx.x / 8 + n * (NT / 8), c = threadIdx.x % 8 * 8;
+        float f[8], v[8];
+        sr.v[n].get(f);
+        sv.v[n].get(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) vdot[n] = fmaf(f[j], v[j], vdot[n]);
+        M::put<NO>(sR, row, c, f);
+        su.v[n].get(f);
+        M::put<NO>(sUt, row, c, f);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        Parts<NO> ps, pd;
+        {
+          float f[8], d[8];
+          vs[x].get(f);
+          vd[x].get(d);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) both = fmaf(f[j], d[j], both);
+          split8<NO>(ps, f);
+          split8<NO>(pd, d);
+        }
+        Parts<NI> oa[4];
+        Parts<NO> ra[4], ua[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          oa[i] = M::by_row<NI>(sO, ml, i, x);
+          ra[i] = M::by_row<NO>(sR, ml, i, x);
+          ua[i] = M::by_row<NO>(sUt, ml, i, x);
+        }
+        mmp<NO>(x1, oa, ps);
+        mmp<NO>(x2, ra, ps);
+        mmp<NO>(x3, ua, pd);
+        // the wave's own tiles of dP and dA
+#pragma unroll
+        for (int n = 0; n < NTILE; ++n) {
+          const int t = w + n * NW;
+          if (t < 12) {
+            const Parts<NO> ub = M::by_row<NO>(sUt, ml, tile_j(t), x);
+            dp[n] = mmp<NO>(M::by_row<NI>(sO, ml, tile_i(t), x), ub, dp[n]);
+            da[n] = mmp<NO>(M::by_row<NO>(sR, ml, tile_i(t), x), ub, da[n]);
+          }
+        }
+      }
+    }
+    Stage<T, DK, NT> stK, stQ;
+    stK.load(static_cast<const T*>(a.k) + sl.row0 * a.ldk + hk * DK, a.ldk, sl.n);
+    stQ.load(static_cast<const T*>(a.q) + sl.row0 * a.ldq + hk * DK, a.ldq, sl.n);
+#pragma unroll
+    for (int n = 0; n < VN; ++n) {
+      const float d = group_sum<8>(vdot[n]);
+      if (threadIdx.x % 8 == 0) sV[threadIdx.x / 8 + n * (NT / 8)] = d;
+    }
+    both = group_sum<64>(both);
+    __syncthreads();
+    stK.store(sK);
+    stQ.store(sQ);
+    for (int i = threadIdx.x; i < 256; i += NT) sE[i / 64][i % 64] = 0.0f;
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NTILE; ++n) {
+      const int t = w + n * NW;
+      if (t < 12) {
+        const int ti = tile_i(t), tj = tile_j(t), j = tile_row(tj, 0) + 8 * (r >> 2) + (r & 3);
+        f4 kk = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int x = 0; x < DK / 32; ++x)
+          kk = mmp<3>(X::template by_row<NI>(sK, xl, ti, x), X::template by_row<NI>(sK, xl, tj, x), kk);
+        const float gh = sGate[192 + j], gl = sGate[256 + j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = tile_row(ti, e) + 8 * g;
+          const float gam = i >= j ? __builtin_amdgcn_exp2f((sGate[192 + i] - gh) + (sGate[256 + i] - gl)) : 0.0f;
+          const float ag = i > j ? -da[n][e] * gam : 0.0f;
+          if (i == j) sU[i] = da[n][e];
+          const float es = group_sum<16>(ag * kk[e]);
+          if (r == 0) sE[tj][i] = es;
+          dp[n][e] = i >= j ? a.scale * dp[n][e] * gam : 0.0f;
+          da[n][e] = sGate[128 + i] * ag;
+        }
+        // F[i][j], and M + M^T at both places (on the diagonal's block of 32
+        // the other half comes from the tile that mirrors this one)
+        Parts<NO> pf, pn;
+        split_d<NO>(pf, dp[n], dp[n]);
+        split_d<NO>(pn, da[n], da[n]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = tile_row(ti, e) + 8 * g;
+#pragma unroll
+          for (int q = 0; q < NO; ++q) {
+            const uint16_t vf = __builtin_bit_cast(uint16_t, static_cast<__bf16>(pf.p[q][e]));
+            const uint16_t vn = __builtin_bit_cast(uint16_t, static_cast<__bf16>(pn.p[q][e]));
+            if (i >= j) *reinterpret_cast<uint16_t*>(sF + q * M::PLANE + M::at(i, j & ~7) + 2 * (j & 7)) = vf;
+            else *reinterpret_cast<uint16_t*>(sF + q * M::PLANE + M::at(i, j & ~7) + 2 * (j & 7)) = 0;
+            if (i >= j) {
+              *reinterpret_cast<uint16_t*>(sN + q * M::PLANE + M::at(i, j & ~7) + 2 * (j & 7)) = vn;
+              *reinterpret_cast<uint16_t*>(sN + q * M::PLANE + M::at(j, i & ~7) + 2 * (i & 7)) = vn;
+            }
+          }
+        }
+      }
+    }
+    __syncthreads();
+    // dQ = scale exp(G) X1 + F K,  dK = F^T Q + (M + M^T) K - exp(G) beta X2 + exp(G_end - G) X3
+    f4 hq[4], hkk[4];
+    float rx[16], re = 0.0f;
+    const T* kp = static_cast<const T*>(a.k) + sl.row0 * a.ldk + hk * DK + dkr;
+    const T* qp = static_cast<const T*>(a.q) + sl.row0 * a.ldq + hk * DK + dkr;
+    float kv[16], qv[16];
+#pragma unroll
+    for (int n = 0; n < 16; ++n) {
+      const int row = tile_row(n / 4, n % 4) + 8 * g, rc = min(row, sl.n - 1);
+      kv[n] = row < sl.n ? to_f32(kp[rc * a.ldk]) : 0.0f;
+      qv[n] = row < sl.n ? to_f32(qp[rc * a.ldq]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f4 st = *reinterpret_cast<const f4*>(&sGate[tile_row(i, 0) + 8 * g]);
+      const f4 en = *reinterpret_cast<const f4*>(&sGate[64 + tile_row(i, 0) + 8 * g]);
+      const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + tile_row(i, 0) + 8 * g]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float k = kv[4 * i + e], x = x3[i][e] * en[e];
+        hq[i][e] = a.scale * st[e] * x1[i][e];
+        rx[4 * i + e] = k * x2[i][e];
+        re = fmaf(k, x, re);
+        hkk[i][e] = fmaf(-st[e] * bt[e], x2[i][e], x);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const Parts<NI> kb = X::template by_col<NI>(sK, xl, w, x), qb = X::template by_col<NI>(sQ, xl, w, x);
+      Parts<NO> fa[4], ft[4], na[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= 2 * x) fa[i] = M::by_row<NO>(sF, ml, i, x);
+        if (i < 2 * x + 2) ft[i] = M::by_col<NO>(sF, ml, i, x);
+        na[i] = M::by_row<NO>(sN, ml, i, x);
+      }
+      mmp<NO>(hkk, na, kb);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i >= 2 * x) hq[i] = mmp<NO>(fa[i], kb, hq[i]);
+        if (i < 2 * x + 2) hkk[i] = mmp<NO>(ft[i], qb, hkk[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dq[i] += hq[i];
+      dk[i] += hkk[i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = tile_row(i, e) + 8 * g;
+        const float d = group_sum<16>(fmaf(qv[4 * i + e], hq[i][e], -kv[4 * i + e] * hkk[i][e]));
+        const float x = group_sum<16>(rx[4 * i + e]);
+        if (r == 0) {
+          sRow[0][w][row] = d;
+          sRow[1][w][row] = x;
+        }
+      }
+    }
+    re = group_sum<64>(re);
+    if (lane == 0) sEnd[w] = fmaf(sGate[63], both, re);
+    __syncthreads();
+    if (w == 0) {
+      float d = 0.0f, x = 0.0f, end = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NW; ++n) {
+        d += sRow[0][n][lane];
+        x += sRow[1][n][lane];
+        end += sEnd[n];
+      }
+      const float bt = sGate[128 + lane], rv = sV[lane];
+      const float db = rv - sGate[lane] * x + (sE[0][lane] + sE[1][lane]) + (sE[2][lane] + sE[3][lane]);
+      float dG = d + 2.0f * (sU[lane] - bt * rv);
+      if (lane == 63) dG += end;
+      // sums of the rows from here on
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const float y = __shfl_down(dG, o, 64);
+        if (lane + o < 64) dG += y;
+      }
+      if (lane < sl.n) {
+        const int64_t at = (sl.row0 + lane) * a.Hv + h;
+        static_cast<T*>(a.dg)[at] = from_f32<T>(dG);
+        static_cast<T*>(a.dbeta)[at] = from_f32<T>(db);
+      }
+    }
+  }
+  const int ldq = a.Hk * DK;
+  const ChunkRows oq(static_cast<T*>(a.dq) + sl.row0 * ldq + hk * DK, ldq, sl.n);
+  const ChunkRows ok(static_cast<T*>(a.dk) + sl.row0 * ldq + hk * DK, ldq, sl.n);
+  const uint32_t orow = static_cast<uint32_t>(ldq) * static_cast<uint32_t>(sizeof(T));
+  const uint32_t oat = 8 * g * orow + dkr * static_cast<uint32_t>(sizeof(T));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      oq.store1(T{}, oat + tile_row(i, e) * orow, dq[i][e]);
+      ok.store1(T{}, oat + tile_row(i, e) * orow, dk[i][e]);
+    }
+}
+
+template <typename T, int DK>
+hipError_t run_backward(const DeltaArgs& a, hipStream_t s) {
+  constexpr int NBUF = sizeof(T) == 2 ? 2 : 1;
+  const int64_t heads = static_cast<int64_t>(a.B) * a.Hv;
+  k_delta_back_chain<T, DK, 4, NBUF><<<static_cast<unsigned>(heads * (a.Dv / 64)), 256, 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_delta_grads<T, DK><<<static_cast<unsigned>(static_cast<int64_t>(a.nslot) * a.Hk), 4 * DK, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t delta_backward_workspace_bytes(int B, int T, int Hv, int Dk, int Dv, bool packed) {
+  const size_t chunks = static_cast<size_t>(delta_slots(B, T, packed)) * Hv;
+  return sizeof(float) * chunks * (4096 + kDeltaGates + static_cast<size_t>(Dk + 64) * Dv);
+}
+
+void delta_backward_carve(DeltaArgs& a, void* ws) {
+  a.lseg = 30;   // whole sequences
+  a.nseg = a.B;
+  a.nslot = static_cast<int>(delta_slots(a.B, a.T, a.cu != nullptr));
+  const size_t chunks = static_cast<size_t>(a.nslot) * a.Hv;
+  a.pm = static_cast<float*>(ws);
+  a.gates = a.pm + 4096 * chunks;
+  a.after = a.gates + kDeltaGates * chunks;
+  a.dr = a.after + static_cast<size_t>(a.Dk) * a.Dv * chunks;
+}
+
+hipError_t launch_delta_backward(DeltaArgs& a, int bf16, hipStream_t s) {
+  const hipError_t e = launch_delta_chunks(a, bf16, s);
+  if (e != hipSuccess) return e;
+  if (bf16) return a.Dk == 64 ? run_backward<bf16_t, 64>(a, s) : run_backward<bf16_t, 128>(a, s);
+  return a.Dk == 64 ? run_backward<float, 64>(a, s) : run_backward<float, 128>(a, s);
+}
+
+}  // namespace m3

@@ -166,6 +166,15 @@ struct Triangle {
     u.w &= a ? m[1] : before;
     f.p[0] = __builtin_bit_cast(bh8, u);
   }
+  // the other side: columns 8 g + j with j >= 4 a + v (or >)
+  __device__ __forceinline__ void keep_not(Parts<1>& f, int a, const uint32_t* m) const {
+    uint4 u = __builtin_bit_cast(uint4, f.p[0]);
+    u.x &= ~(a ? upto : m[0]);
+    u.y &= ~(a ? upto : m[1]);
+    u.z &= ~(a ? m[0] : before);
+    u.w &= ~(a ? m[1] : before);
+    f.p[0] = __builtin_bit_cast(bh8, u);
+  }
   // part n of the six operands of T or P below or on the diagonal: tiles of rows
   // and blocks of 32 columns (0, 0), (1, 0), (2, 0), (3, 0), (2, 1), (3, 1)
   using M = Rows64<64>;
@@ -183,6 +192,21 @@ struct Triangle {
       if (k < 2 || k >= 4) keep(f[k], k & 1, on);
     }
   }
+  // the same of their transposes: (0, 1), (1, 1), (2, 1), (3, 1), (0, 0), (1, 0)
+  __device__ __forceinline__ void tt6(Parts<1> (&f)[6], const char* lds, const M::Lane& l, int n) const {
+#pragma unroll
+    for (int k = 0; k < 6; ++k) {
+      f[k] = M::by_col<1>(lds + n * M::PLANE, l, k < 4 ? k : k - 4, k < 4 ? 1 : 0);
+      if (k >= 2) keep_not(f[k], k & 1, on);
+    }
+  }
+  __device__ __forceinline__ void pt6(Parts<1> (&f)[6], const char* lds, const M::Lane& l, int n) const {
+#pragma unroll
+    for (int k = 0; k < 6; ++k) {
+      f[k] = M::by_row<1>(lds + n * M::PLANE, l, k < 4 ? k : k - 4, k < 4 ? 1 : 0);
+      if (k >= 2) keep_not(f[k], k & 1, below);
+    }
+  }
 };
 
 // c += (a triangle's part n) b over the six operands, c[4], c[5] for the second
@@ -194,6 +218,16 @@ __device__ __forceinline__ void mm6(f4 (&c)[6], const Parts<1> (&a)[6], const Pa
     if (n + j < N)
 #pragma unroll
       for (int k = 0; k < 6; ++k) c[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[k].p[0], b[k < 4 ? 0 : 1].p[j], c[k], 0, 0, 0);
+}
+
+// the same for transposes, c[4], c[5] for the first half
+template <int N, int NB>
+__device__ __forceinline__ void mmt6(f4 (&c)[6], const Parts<1> (&a)[6], const Parts<NB> (&b)[2], int n) {
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+    if (n + j < N)
+#pragma unroll
+      for (int k = 0; k < 6; ++k) c[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[k].p[0], b[k < 4 ? 1 : 0].p[j], c[k], 0, 0, 0);
 }
 
 // The order of a region's instructions: RD reads of LDS, then products with V

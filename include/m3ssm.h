@@ -493,6 +493,8 @@ typedef struct {
 
 /* tokens between the states that m3_delta_scan saves for the backward pass */
 #define M3_DELTA_CHUNK 64
+/* what it saves of each, for each value head */
+#define M3_DELTA_STATE_FLOATS(dk, dv) (((dk) + 64) * (dv) + 64 * 64 + 5 * 64)
 
 /* Bytes of device workspace (packed: nonzero for calls with cu_seqlens); 0 if
  * dims is invalid. */
@@ -503,10 +505,11 @@ size_t m3_delta_scan_workspace_size(const m3_delta_dims* dims, int packed);
  *   o       as v, dense
  *   hT      [Bsz, Hv, Dk, Dv] fp32, the state after the last token (NULL: not
  *           written)
- *   states  for the backward pass (NULL: not written): of every chunk of
- *           M3_DELTA_CHUNK tokens the state before it [Dk, Dv] and the u of its
- *           tokens [M3_DELTA_CHUNK, Dv], [slots, Hv, Dk + M3_DELTA_CHUNK, Dv]
- *           fp32 with slots = Bsz ceil(T / M3_DELTA_CHUNK), of a packed call
+ *   states  for the backward pass (NULL: not written): [slots, Hv,
+ *           M3_DELTA_STATE_FLOATS(Dk, Dv)] fp32, for every chunk of
+ *           M3_DELTA_CHUNK tokens and head the state before it [Dk, Dv], the u
+ *           of its tokens and what else the backward pass reads, with slots =
+ *           Bsz ceil(T / M3_DELTA_CHUNK), of a packed call
  *           floor(T / M3_DELTA_CHUNK) + S, of which those that no chunk takes
  *           are left as they are
  * h0 [Bsz, Hv, Dk, Dv] fp32 or NULL (zero), may alias hT.  An empty sequence's

@@ -1037,8 +1037,13 @@ def _delta_setup(q, k, v, g, beta, scale, cu_seqlens):
     return d, ref, packed, slots
 
 
+def m3_delta_state_floats(dk, dv):
+    """M3_DELTA_STATE_FLOATS: what delta_scan saves of a chunk and head."""
+    return (dk + 64) * dv + 64 * 64 + 5 * 64
+
+
 def _delta_states(d, slots):
-    return (slots, d.nheads_v, d.headdim_k + M3_DELTA_CHUNK, d.headdim_v)
+    return (slots, d.nheads_v, m3_delta_state_floats(d.headdim_k, d.headdim_v))
 
 
 def delta_scan(q, k, v, g, beta, h0=None, scale=None, cu_seqlens=None, want_hT=True,

@@ -305,6 +305,9 @@ m3_status check_delta(const m3_delta_dims* d, bool scan, bool packed) {
   return M3_OK;
 }
 
+static_assert(M3_DELTA_CHUNK == m3::kDeltaChunk &&
+                  M3_DELTA_STATE_FLOATS(128, 64) == 192 * 64 + m3::kDeltaMatrix + m3::kDeltaGates,
+              "the header's sizes");
 // g and beta may be columns of any row
 bool misaligned_gates(const m3_delta_dims* d, const void* g, const void* beta) {
   const uintptr_t m = d->dtype == M3_BF16 ? 1u : 3u;

@@ -9,6 +9,7 @@
 namespace m3 {
 
 constexpr int kDeltaChunk = 64;   // tokens of a chunk
+constexpr int kDeltaMatrix = 64 * 64;
 constexpr int kDeltaGates = 5 * 64;   // floats of a chunk's gates: exp(G), exp(G_end - G), beta, G in two parts
 
 struct DeltaArgs {
@@ -17,16 +18,16 @@ struct DeltaArgs {
   const int32_t* cu;                  // packed: [B + 1] row offsets, else null
   void* o;                            // dense rows
   float* hT;                          // [B, Hv, Dk, Dv] or null
-  float* states;                      // [slots, Hv, Dk + 64, Dv] or null: the state before a chunk, then
-                                      // its u
+  float* states;                      // [slots, Hv, delta_state_floats] or null: the state before a chunk
+                                      // [Dk, Dv], its u [64, Dv], its matrix and its gates
   // backward
   const float *cstates, *dhT;
   const void* dout;                   // dense rows
   void *dq, *dk, *dv, *dg, *dbeta;    // dense rows
   float* dh0;                         // [B, Hv, Dk, Dv] or null
   // workspace
-  float* pm;                          // [slots, Hv, 64, 64]
-  float* gates;                       // [slots, Hv, 5, 64]
+  float* pm;                          // T \ P^T [64, 64] and the gates of chunk and head n: from pm + n
+  int64_t ldpm;                       // ldpm on (in `states` where those are saved)
   float* after;                       // backward: gradients of the state behind a chunk [slots, Hv, Dk, Dv]
   float* dr;                          // backward: those of R [slots, Hv, 64, Dv]
   float* ends;                        // segments' ends from a zero state, then the states before
@@ -49,15 +50,17 @@ struct DeltaPlan {
   int64_t nseg;   // slots of segments
   bool split;     // some sequence may have more than one
 };
-DeltaPlan delta_plan(int B, int T, int Hv, int Dv, bool packed);
+DeltaPlan delta_plan(int B, int T, int Hv, int Dk, int Dv, bool packed);
 
+inline int64_t delta_state_floats(int Dk, int Dv) {
+  return static_cast<int64_t>(Dk + kDeltaChunk) * Dv + kDeltaMatrix + kDeltaGates;
+}
 bool delta_supported(int Dk, int Dv);
 int64_t delta_slots(int B, int T, bool packed);
 size_t delta_workspace_bytes(int B, int T, int Hv, int Dk, int Dv, bool packed);
 size_t delta_backward_workspace_bytes(int B, int T, int Hv, int Dk, int Dv, bool packed);
 void delta_carve(DeltaArgs& a, void* ws);
 void delta_backward_carve(DeltaArgs& a, void* ws);
-hipError_t launch_delta_chunks(const DeltaArgs& a, int bf16, hipStream_t s);
 hipError_t launch_delta_backward(DeltaArgs& a, int bf16, hipStream_t s);
 hipError_t launch_delta_scan(DeltaArgs& a, int bf16, hipStream_t s);
 hipError_t launch_delta_step(const DeltaArgs& a, float* h, int bf16, hipStream_t s);

@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256) void k_delta_chunk(DeltaArgs a) {
     sG[lane] = G;
     sB[lane] = bt;
     const double end = __shfl(G, 63, 64);
-    float* p = a.gates + (static_cast<int64_t>(slot) * a.Hv + h) * kDeltaGates + lane;
+    float* p = a.pm + (static_cast<int64_t>(slot) * a.Hv + h) * a.ldpm + kDeltaMatrix + lane;
     p[0] = __builtin_amdgcn_exp2f(static_cast<float>(G));
     p[64] = __builtin_amdgcn_exp2f(static_cast<float>(end - G));
     p[128] = bt;
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(256) void k_delta_chunk(DeltaArgs a) {
     }
   }
   __syncthreads();
-  float* out = a.pm + (static_cast<int64_t>(slot) * a.Hv + h) * 4096;
+  float* out = a.pm + (static_cast<int64_t>(slot) * a.Hv + h) * a.ldpm;
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
     const int x = threadIdx.x + 256 * n;
@@ -246,9 +246,9 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
     c = min(c, c1 - 1);
     const int64_t m = static_cast<int64_t>(seg.slot0 + c) * a.Hv + h;
     st.k.load(static_cast<const T*>(a.k) + first(c) * a.ldk + hk * DK, a.ldk, rows(c));
-    st.m.load(a.pm + m * 4096, 64, 64);
+    st.m.load(a.pm + m * a.ldpm, 64, 64);
 #pragma unroll
-    for (int i = 0; i < Tiles::NG; ++i) st.g[i] = (a.gates + m * kDeltaGates)[min(threadIdx.x + i * NT, 191u)];
+    for (int i = 0; i < Tiles::NG; ++i) st.g[i] = (a.pm + m * a.ldpm + kDeltaMatrix)[min(threadIdx.x + i * NT, 191u)];
     if constexpr (FULL) st.q.load(static_cast<const T*>(a.q) + first(c) * a.ldq + hk * DK, a.ldq, rows(c));
   };
   auto fetch_v = [&](int c) __attribute__((always_inline)) {
@@ -259,7 +259,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
     fetch(seg.c0);
     fetch_v(seg.c0);
     st.store(smem);
-    fetch(seg.c0 + 1);
+    if constexpr (NBUF == 2) fetch(seg.c0 + 1);
   }
   char* buf = smem;
   float decay = 1.0f;   // of the segment
@@ -268,7 +268,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
     const float* sGate = reinterpret_cast<const float*>(buf + BK + BQ + BM);
     tiles_barrier();
     if (FULL && a.states) {
-      float* p = a.states + (static_cast<int64_t>(seg.slot0 + c) * a.Hv + h) * (dd + 64 * a.Dv);
+      float* p = a.states + (static_cast<int64_t>(seg.slot0 + c) * a.Hv + h) * a.ldpm;
 #pragma unroll
       for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -329,10 +329,11 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
     }
     u[2] += u[4];
     u[3] += u[5];
+    if constexpr (NBUF == 1) fetch(c + 1);   // (in few registers until then)
     // O = scale exp(G) Q S0 + P U
     if constexpr (FULL) {
       if (a.states) {
-        float* p = a.states + (static_cast<int64_t>(seg.slot0 + c) * a.Hv + h) * (dd + 64 * a.Dv) + dd;
+        float* p = a.states + (static_cast<int64_t>(seg.slot0 + c) * a.Hv + h) * a.ldpm + dd;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -403,8 +404,9 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
     if constexpr (NBUF == 1) {
       tiles_barrier();
       st.store(buf);
+    } else {
+      fetch(c + 2);
     }
-    fetch(c + 2);
   }
   if constexpr (MODE == kMaps) {   // less its decay, as the A operand of a product over its columns
     uint16_t* p = a.maps + shead * NS * DK * DK;
@@ -636,7 +638,7 @@ __global__ __launch_bounds__(256) void k_delta_step(DeltaArgs a, float* hp) {
 
 template <typename T, int DK, int NW>
 hipError_t run_chain(const DeltaArgs& a, bool split, hipStream_t s) {
-  constexpr int NBUF = sizeof(T) == 2 ? 2 : 1;
+  constexpr int NBUF = sizeof(T) == 2 && NW == 8 ? 2 : 1;
   const int64_t heads = static_cast<int64_t>(a.nseg) * a.Hv;
   if (split) {
     k_delta_segments<T, DK, NW, NBUF>
@@ -663,7 +665,7 @@ hipError_t run_scan(const DeltaArgs& a, bool split, hipStream_t s) {
   const hipError_t e = run_chunks<T, DK>(a, s);
   if (e != hipSuccess) return e;
   if constexpr (DK == 128 && sizeof(T) == 2)
-    if (a.Dv == 128 && split) return run_chain<T, DK, 8>(a, split, s);
+    if (a.Dv == 128) return run_chain<T, DK, 8>(a, split, s);
   return run_chain<T, DK, 4>(a, split, s);
 }
 
@@ -684,44 +686,59 @@ int64_t delta_slots(int B, int T, bool packed) {
   return static_cast<int64_t>(B) * ((T + kDeltaChunk - 1) / kDeltaChunk);
 }
 
-DeltaPlan delta_plan(int B, int T, int Hv, int Dv, bool packed) {
-  const int64_t waves = static_cast<int64_t>(B) * Hv * (Dv / 16);
-  const int64_t chunks = ((packed ? T / B : T) + kDeltaChunk - 1) / kDeltaChunk;   // of a sequence, on average
+// The chain takes about the same time for a chunk whether a SIMD has one wave or
+// two (6 us; half the waves' instructions wait for another's), so in such units
+// it costs a sequence's chunks, times the waves beyond 2048.  The length of the
+// longest of a packed batch is not known here; twice the mean is what uniform
+// lengths give.  Segments cost their chunks twice, without outputs 3/4, for as
+// many columns as the values and a state have together, and what joins them
+// 0.45 for each.  They are taken where that is less than 3/4 (in a training step
+// both are held by memory before that).  16384 tokens of 16 heads of 128: 2.3 ms
+// whole, in 32 segments of 8 chunks 330 us with the rest, 16 of 16 270, 8 of 32
+// 310.
+DeltaPlan delta_plan(int B, int T, int Hv, int Dk, int Dv, bool packed) {
+  const double rows = packed ? T : static_cast<double>(B) * T;
+  const double longest = (packed && B > 1 ? 2.0 * T / B : T) / kDeltaChunk, cols = Hv * (Dv / 16.0);
+  auto rounds = [](double waves) { return waves > 2048 ? waves / 2048 : 1.0; };
   DeltaPlan p{30, B, false};
-  for (int l = 3; l < 10; ++l)
-    if (waves * (chunks >> l) <= 2048) {
-      if ((chunks >> l) >= 4) p.lseg = l, p.split = true;
-      break;
+  double best = 0.75 * longest * rounds(B * cols);
+  for (int l = 3; l < 10 && longest / (1 << l) >= 3; ++l) {
+    const double n = rows / (kDeltaChunk << l) + (packed ? B : 0);
+    const double cost = (1 << l) * (0.75 * rounds(n * cols * (1.0 + static_cast<double>(Dk) / Dv)) + rounds(n * cols)) +
+                        0.45 * longest / (1 << l);
+    if (cost < best) {
+      best = cost;
+      p = DeltaPlan{l, 0, true};
     }
+  }
   if (p.split)
     p.nseg = packed ? (static_cast<int64_t>(T) >> (6 + p.lseg)) + B
-                    : B * ((chunks + (int64_t{1} << p.lseg) - 1) >> p.lseg);
+                    : B * ((static_cast<int64_t>(T) + (kDeltaChunk << p.lseg) - 1) / (kDeltaChunk << p.lseg));
   return p;
 }
 
 size_t delta_workspace_bytes(int B, int T, int Hv, int Dk, int Dv, bool packed) {
-  const DeltaPlan p = delta_plan(B, T, Hv, Dv, packed);
-  const size_t chunks = static_cast<size_t>(4096 + kDeltaGates) * delta_slots(B, T, packed) * Hv;
+  const DeltaPlan p = delta_plan(B, T, Hv, Dk, Dv, packed);
+  const size_t chunks = static_cast<size_t>(kDeltaMatrix + kDeltaGates) * delta_slots(B, T, packed) * Hv;
   // (maps of two parts take no less than their room for three)
   const size_t segs = p.split ? (static_cast<size_t>(Dk) * (sizeof(float) * Dv + 3 * sizeof(uint16_t) * Dk) + sizeof(float) * 4) * p.nseg * Hv : 0;
   return sizeof(float) * chunks + segs;
 }
 
 void delta_carve(DeltaArgs& a, void* ws) {
-  const DeltaPlan p = delta_plan(a.B, a.T, a.Hv, a.Dv, a.cu != nullptr);
+  const DeltaPlan p = delta_plan(a.B, a.T, a.Hv, a.Dk, a.Dv, a.cu != nullptr);
   a.lseg = p.lseg;
   a.nseg = static_cast<int>(p.nseg);
   a.nslot = static_cast<int>(delta_slots(a.B, a.T, a.cu != nullptr));
   a.pm = static_cast<float*>(ws);
-  a.gates = a.pm + static_cast<size_t>(4096) * a.nslot * a.Hv;
-  a.ends = a.gates + static_cast<size_t>(kDeltaGates) * a.nslot * a.Hv;
+  a.ldpm = kDeltaMatrix + kDeltaGates;
+  a.ends = a.pm + static_cast<size_t>(kDeltaMatrix + kDeltaGates) * a.nslot * a.Hv;
   a.maps = reinterpret_cast<uint16_t*>(a.ends + static_cast<size_t>(a.Dk) * a.Dv * a.nseg * a.Hv);
   a.decays = reinterpret_cast<float*>(a.maps + static_cast<size_t>(3) * a.Dk * a.Dk * a.nseg * a.Hv);
-}
-
-hipError_t launch_delta_chunks(const DeltaArgs& a, int bf16, hipStream_t s) {
-  if (bf16) return a.Dk == 64 ? run_chunks<bf16_t, 64>(a, s) : run_chunks<bf16_t, 128>(a, s);
-  return a.Dk == 64 ? run_chunks<float, 64>(a, s) : run_chunks<float, 128>(a, s);
+  if (a.states) {
+    a.ldpm = delta_state_floats(a.Dk, a.Dv);
+    a.pm = a.states + static_cast<size_t>(a.Dk + kDeltaChunk) * a.Dv;
+  }
 }
 
 hipError_t launch_delta_scan(DeltaArgs& a, int bf16, hipStream_t s) {

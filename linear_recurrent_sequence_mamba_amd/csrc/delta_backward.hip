@@ -59,9 +59,9 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
     c = max(c, 0);
     const int64_t m = static_cast<int64_t>(seg.slot0 + c) * a.Hv + h;
     stK.load(static_cast<const T*>(a.k) + first(c) * a.ldk + hk * DK, a.ldk, rows(c));
-    stM.load(a.pm + m * 4096, 64, 64);
+    stM.load(a.pm + m * a.ldpm, 64, 64);
 #pragma unroll
-    for (int i = 0; i < NG; ++i) stG[i] = (a.gates + m * kDeltaGates)[min(threadIdx.x + i * NT, 191u)];
+    for (int i = 0; i < NG; ++i) stG[i] = (a.pm + m * a.ldpm + kDeltaMatrix)[min(threadIdx.x + i * NT, 191u)];
     stQ.load(static_cast<const T*>(a.q) + first(c) * a.ldq + hk * DK, a.ldq, rows(c));
   };
   auto fetch_o = [&](int c) __attribute__((always_inline)) {
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
     fetch(seg.nch - 1);
     fetch_o(seg.nch - 1);
     store(smem);
-    fetch(seg.nch - 2);
+    if constexpr (NBUF == 2) fetch(seg.nch - 2);
   }
   char* buf = smem;
   for (int c = seg.nch - 1; c >= 0; --c) {
@@ -132,26 +132,53 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
     Parts<NI> op[2];
     split_d<NI>(op[0], o[0], o[1]);
     split_d<NI>(op[1], o[2], o[3]);
+    fetch_o(c - 1);
     __builtin_amdgcn_sched_barrier(0);
+    Parts<3> ep[2];
 #pragma unroll
     for (int n = 0; n < 3; ++n) {
       if (n < 2) tri.pt6(ta[(n + 1) & 1], sM, ml, n + 1);
-      else tri.tt6(ta[(n + 1) & 1], sM, ml, 0);
       mmt6<3>(u, ta[n & 1], op, n);
+      // (in the products' time) scale exp(G) dO, for dS0
+      if (n < 2) {
+#pragma unroll
+        for (int i = 2 * n; i < 2 * n + 2; ++i) o[i] *= a.scale * *reinterpret_cast<const f4*>(&sGate[tile_row(i, 0) + 8 * g]);
+        split_d<3>(ep[n], o[2 * n], o[2 * n + 1]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     u[0] += u[4];
     u[1] += u[5];
+    // dS0 = exp(G_end) dS1 + Q^T (scale exp(G) dO) ...
+    const float last = sGate[63];
+#pragma unroll
+    for (int t = 0; t < DT; ++t) S[t] *= last;
+    Parts<NI> kc[2][4];
+    auto read_t = [&](const char* tile, int n) __attribute__((always_inline)) {   // four tiles of dS, 32 rows
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        kc[n & 1][t] = X::template by_col<NI>(tile, xl, 4 * (n % (DT / 4)) + t, n / (DT / 4));
+    };
+    auto add = [&](const char* tile) __attribute__((always_inline)) {
+#pragma unroll
+      for (int n = 0; n < DT / 2; ++n) {
+        if (n + 1 < DT / 2) read_t(tile, n + 1);
+        mmp<3>(*reinterpret_cast<f4(*)[4]>(&S[4 * (n % (DT / 4))]), kc[n & 1], ep[n / (DT / 4)]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    read_t(sQ, 0);
     // dR = T^T dU: dU itself for the diagonal
     Parts<3> up[2];
     split_d<3>(up[0], u[0], u[1]);
     split_d<3>(up[1], u[2], u[3]);
+    add(sQ);
+    tri.tt6(ta[0], sM, ml, 0);
     u[4] = u[5] = f4{0, 0, 0, 0};
-    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int n = 0; n < 3; ++n) {
-      if (n < 2) tri.tt6(ta[n & 1], sM, ml, n + 1);
-      mmt6<3>(u, ta[(n + 1) & 1], up, n);
+      if (n < 2) tri.tt6(ta[(n + 1) & 1], sM, ml, n + 1);
+      mmt6<3>(u, ta[n & 1], up, n);
       if (n == 0 && NBUF == 2) {
         buf = buf == smem ? smem + BUF : smem;
         store(buf);   // (the last time unread)
@@ -160,7 +187,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
     }
     u[0] += u[4];
     u[1] += u[5];
-    // dV = beta dR, and what adds to dS0
+    read_t(sK, 0);
+    // dV = beta dR
     {
       const ChunkRows dv(static_cast<T*>(a.dv) + first(c) * ldo + h * a.Dv, ldo, rows(c));
       const uint32_t orow = static_cast<uint32_t>(ldo) * static_cast<uint32_t>(sizeof(T));
@@ -176,44 +204,21 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
           u[i][e] *= bt[e];
           dv.store1(T{}, oat + tile_row(i, e) * orow, u[i][e]);
           u[i][e] *= -st[e];
-          o[i][e] *= a.scale * st[e];
         }
       }
     }
-    fetch_o(c - 1);
-    // dS0
-    Parts<NI> kc[2][4];
-    auto read_t = [&](int n) __attribute__((always_inline)) {   // four tiles of dS, 32 rows of K, then of Q
-      const char* tile = n < DT / 2 ? sK : sQ;
-      const int k = n % (DT / 2);
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        kc[n & 1][t] = X::template by_col<NI>(tile, xl, 4 * (k % (DT / 4)) + t, k / (DT / 4));
-    };
-    Parts<3> ep[2];
-    read_t(0);
-    const float last = sGate[63];
+    // ... - K^T (exp(G) dV)
     split_d<3>(ep[0], u[0], u[1]);
     split_d<3>(ep[1], u[2], u[3]);
-#pragma unroll
-    for (int t = 0; t < DT; ++t) S[t] *= last;
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int n = 0; n < DT; ++n) {
-      if (n + 1 < DT) read_t(n + 1);
-      const int k = n % (DT / 2);
-      if (n == DT / 2) {
-        split_d<3>(ep[0], o[0], o[1]);
-        split_d<3>(ep[1], o[2], o[3]);
-      }
-      mmp<3>(*reinterpret_cast<f4(*)[4]>(&S[4 * (k % (DT / 4))]), kc[n & 1], ep[k / (DT / 4)]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    if constexpr (NBUF == 1) fetch(c - 1);   // (in few registers until then)
+    add(sK);
     if constexpr (NBUF == 1) {
       tiles_barrier();
       store(buf);
+    } else {
+      fetch(c - 2);
     }
-    fetch(c - 2);
   }
   if (a.dh0)
 #pragma unroll
@@ -224,11 +229,13 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
 
 // ---------------------------------------------------------------------------
 // The gradients of q, k, g and beta of a chunk and a head of k, its value heads
-// one after another.  Wave w has the 16 channels tile_row(w, ..) of q and k, so
-// it reads 16 rows of S0 and dS1 straight from memory; the products over value
-// channels (X1, X2, X3, dP, dA) go by 64 of them with dO, dR and U in LDS, where
-// K, Q, F and M + M^T follow.  dP and dA have twelve tiles (two rows of two
-// blocks of 32 by 32, lower), which the waves share.
+// one after another (MULTI: more than one).  Wave w has the 16 channels
+// tile_row(w, ..) of q and k, so it reads 16 rows of S0 and dS1 straight from
+// memory; the products over value channels (X1, X2, X3, dP, dA) go by 64 of them
+// with dO, dR and U in LDS, where K, Q, F^T and M^T follow: the transposes, as a
+// lane has four consecutive rows of a tile's column.  dP and dA have twelve
+// tiles (of two blocks of 32 by 32 on and one below the diagonal), which the
+// waves share.
 template <typename T, int DK>
 struct GradTiles {
   using M = Rows64<64>;
@@ -242,17 +249,18 @@ struct GradTiles {
 __device__ __forceinline__ constexpr int tile_i(int n) { return n < 4 ? n >> 1 : 2 + ((n - 4) >> 2); }
 __device__ __forceinline__ constexpr int tile_j(int n) { return n < 4 ? n & 1 : (n - 4) & 3; }
 
-template <typename T, int DK>
-__global__ __launch_bounds__(4 * DK, 2) void k_delta_grads(DeltaArgs a) {
+template <typename T, int DK, bool MULTI>
+__global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(DeltaArgs a) {
   using X = Rows64<DK>;
   using M = Rows64<64>;
   using G = GradTiles<T, DK>;
-  constexpr int NI = G::NI, NO = G::NO, NW = DK / 16, NT = 64 * NW, NTILE = (12 + NW - 1) / NW;
+  constexpr int NI = G::NI, NO = G::NO, NW = DK / 16, NT = 64 * NW, NTILE = (12 + NW - 1) / NW, VN = 512 / NT;
   __shared__ __align__(16) char smem[G::BYTES];
-  __shared__ float sGate[kDeltaGates], sRow[3][NW][64], sE[4][64], sU[64], sV[64], sEnd[NW];
+  __shared__ __align__(16) float sGate[kDeltaGates];
+  __shared__ float sRow[2][NW][64], sE[4][64], sU[64], sV[64], sEnd[NW];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  const int hk = blockIdx.x % a.Hk, slot = blockIdx.x / a.Hk, group = a.Hv / a.Hk;
+  const int r = lane & 15, g0 = lane >> 4;
+  const int hk = blockIdx.x % a.Hk, slot = blockIdx.x / a.Hk, group = MULTI ? a.Hv / a.Hk : 1;
   const DeltaSlot sl(a, slot, lane);
   if (sl.n <= 0) return;
   const typename X::Lane xl(lane);
@@ -261,44 +269,55 @@ __global__ __launch_bounds__(4 * DK, 2) void k_delta_grads(DeltaArgs a) {
   char *sO = smem, *sR = smem + NI * M::PLANE, *sUt = sR + NO * M::PLANE;
   char *sK = smem, *sQ = smem + NI * X::PLANE, *sF = smem + 2 * NI * X::PLANE, *sN = sF + NO * M::PLANE;
   const int dkr = 32 * (w >> 1) + 8 * (r >> 2) + 4 * (w & 1) + (r & 3);   // the lane's channel of q and k
+  const int64_t dd = static_cast<int64_t>(DK) * a.Dv;
   f4 dq[4], dk[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dq[i] = dk[i] = f4{0, 0, 0, 0};
 
   for (int h = hk * group; h < (hk + 1) * group; ++h) {
-    const int64_t m = static_cast<int64_t>(slot) * a.Hv + h, dd = static_cast<int64_t>(DK) * a.Dv;
-    const float* S0 = a.cstates + m * (dd + 64 * a.Dv) + static_cast<int64_t>(dkr) * a.Dv + 8 * g;
-    const float* dS = a.after + m * dd + static_cast<int64_t>(dkr) * a.Dv + 8 * g;
+    // (opaque: addresses are made again for each head, not kept over the loop)
+    const int tid = MULTI ? opaque(threadIdx.x) : threadIdx.x, g = MULTI ? opaque(g0) : g0;
+    const int64_t m = static_cast<int64_t>(slot) * a.Hv + h;
+    const float* S0 = a.cstates + m * a.ldpm;
+    const float* dS = a.after + m * dd;
+    const uint32_t sat = static_cast<uint32_t>(dkr * a.Dv + 8 * g);
     f4 x1[4], x2[4], x3[4], dp[NTILE], da[NTILE];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x1[i] = x2[i] = x3[i] = f4{0, 0, 0, 0};
 #pragma unroll
     for (int n = 0; n < NTILE; ++n) dp[n] = da[n] = f4{0, 0, 0, 0};
     float both = 0.0f;   // of <S0, dS1>
-    constexpr int VN = 512 / NT;
     float vdot[VN];
 #pragma unroll
     for (int n = 0; n < VN; ++n) vdot[n] = 0.0f;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kDeltaGates; i += NT) sGate[i] = (a.gates + m * kDeltaGates)[i];
-    for (int c0 = 0; c0 < a.Dv; c0 += 64) {
-      Stage<T, 64, NT> so, sv;
-      Stage<float, 64, NT> sr, su;
-      so.load(static_cast<const T*>(a.dout) + sl.row0 * ldo + h * a.Dv + c0, ldo, sl.n);
-      sv.load(static_cast<const T*>(a.v) + sl.row0 * a.ldv + h * a.Dv + c0, a.ldv, sl.n);
-      sr.load(a.dr + m * 64 * a.Dv + c0, a.Dv, 64);
-      su.load(a.cstates + m * (dd + 64 * a.Dv) + dd + c0, a.Dv, 64);
-      Vec8<float> vs[2], vd[2];
+    Stage<T, 64, NT> so, sv;
+    Stage<float, 64, NT> sr, su;
+    Vec8<float> vs[2], vd[2];
+    auto fetch = [&](int c0) __attribute__((always_inline)) {
+      so.load(static_cast<const T*>(a.dout) + sl.row0 * ldo + h * a.Dv + c0, ldo, sl.n, tid);
+      sv.load(static_cast<const T*>(a.v) + sl.row0 * a.ldv + h * a.Dv + c0, a.ldv, sl.n, tid);
+      sr.load(a.dr + m * 64 * a.Dv + c0, a.Dv, 64, tid);
+      su.load(S0 + dd + c0, a.Dv, 64, tid);
+    };
+    auto fetch_s = [&](int c0) __attribute__((always_inline)) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        vs[x].load(S0 + c0 + 32 * x);
-        vd[x].load(dS + c0 + 32 * x);
+        vs[x].load(S0 + c0 + 32 * x + sat);
+        vd[x].load(dS + c0 + 32 * x + sat);
       }
-      if (c0 > 0) __syncthreads();
-      so.store(sO);
+    };
+    fetch(0);
+    fetch_s(0);
+    Stage<T, DK, NT> stK, stQ;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kDeltaGates; i += NT) sGate[i] = (a.pm + m * a.ldpm + kDeltaMatrix)[i];
+    if (threadIdx.x < 256) sE[threadIdx.x / 64][threadIdx.x % 64] = 0.0f;
+    for (int c0 = 0; c0 < a.Dv; c0 += 64) {
+      if (c0 > 0) tiles_barrier();
+      so.store(sO, tid);
 #pragma unroll
       for (int n = 0; n < VN; ++n) {
-        const int row = threadIdx.x / 8 + n * (NT / 8), c = threadIdx.x % 8 * 8;
+        const int row = tid / 8 + n * (NT / 8), c = tid % 8 * 8;
         float f[8], v[8];
         sr.v[n].get(f);
         sv.v[n].get(v);
@@ -308,7 +327,13 @@ __global__ __launch_bounds__(4 * DK, 2) void k_delta_grads(DeltaArgs a) {
         su.v[n].get(f);
         M::put<NO>(sUt, row, c, f);
       }
-      __syncthreads();
+      if (c0 + 64 < a.Dv) {
+        fetch(c0 + 64);
+      } else {
+        stK.load(static_cast<const T*>(a.k) + sl.row0 * a.ldk + hk * DK, a.ldk, sl.n, tid);
+        stQ.load(static_cast<const T*>(a.q) + sl.row0 * a.ldq + hk * DK, a.ldq, sl.n, tid);
+      }
+      tiles_barrier();
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         Parts<NO> ps, pd;
@@ -321,17 +346,27 @@ __global__ __launch_bounds__(4 * DK, 2) void k_delta_grads(DeltaArgs a) {
           split8<NO>(ps, f);
           split8<NO>(pd, d);
         }
-        Parts<NI> oa[4];
-        Parts<NO> ra[4], ua[4];
+        {
+          Parts<NI> oa[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          oa[i] = M::by_row<NI>(sO, ml, i, x);
-          ra[i] = M::by_row<NO>(sR, ml, i, x);
-          ua[i] = M::by_row<NO>(sUt, ml, i, x);
+          for (int i = 0; i < 4; ++i) oa[i] = M::by_row<NI>(sO, ml, i, x);
+          mmp<NO>(x1, oa, ps);
         }
-        mmp<NO>(x1, oa, ps);
-        mmp<NO>(x2, ra, ps);
-        mmp<NO>(x3, ua, pd);
+        __builtin_amdgcn_sched_barrier(0);
+        {
+          Parts<NO> ra[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ra[i] = M::by_row<NO>(sR, ml, i, x);
+          mmp<NO>(x2, ra, ps);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        {
+          Parts<NO> ua[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ua[i] = M::by_row<NO>(sUt, ml, i, x);
+          mmp<NO>(x3, ua, pd);
+        }
+        __builtin_amdgcn_sched_barrier(0);
         // the wave's own tiles of dP and dA
 #pragma unroll
         for (int n = 0; n < NTILE; ++n) {
@@ -342,78 +377,58 @@ __global__ __launch_bounds__(4 * DK, 2) void k_delta_grads(DeltaArgs a) {
             da[n] = mmp<NO>(M::by_row<NO>(sR, ml, tile_i(t), x), ub, da[n]);
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
+      if (c0 + 64 < a.Dv) fetch_s(c0 + 64);
     }
-    Stage<T, DK, NT> stK, stQ;
-    stK.load(static_cast<const T*>(a.k) + sl.row0 * a.ldk + hk * DK, a.ldk, sl.n);
-    stQ.load(static_cast<const T*>(a.q) + sl.row0 * a.ldq + hk * DK, a.ldq, sl.n);
 #pragma unroll
     for (int n = 0; n < VN; ++n) {
       const float d = group_sum<8>(vdot[n]);
-      if (threadIdx.x % 8 == 0) sV[threadIdx.x / 8 + n * (NT / 8)] = d;
+      if (tid % 8 == 0) sV[tid / 8 + n * (NT / 8)] = d;
     }
     both = group_sum<64>(both);
-    __syncthreads();
-    stK.store(sK);
-    stQ.store(sQ);
-    for (int i = threadIdx.x; i < 256; i += NT) sE[i / 64][i % 64] = 0.0f;
-    __syncthreads();
+    tiles_barrier();
+    stK.store(sK, tid);
+    stQ.store(sQ, tid);
+    tiles_barrier();
 #pragma unroll
     for (int n = 0; n < NTILE; ++n) {
       const int t = w + n * NW;
       if (t < 12) {
         const int ti = tile_i(t), tj = tile_j(t), j = tile_row(tj, 0) + 8 * (r >> 2) + (r & 3);
+        const int i0 = tile_row(ti, 0) + 8 * g;
         f4 kk = f4{0, 0, 0, 0};
 #pragma unroll
         for (int x = 0; x < DK / 32; ++x)
           kk = mmp<3>(X::template by_row<NI>(sK, xl, ti, x), X::template by_row<NI>(sK, xl, tj, x), kk);
         const float gh = sGate[192 + j], gl = sGate[256 + j];
+        const f4 hi = *reinterpret_cast<const f4*>(&sGate[192 + i0]), lo = *reinterpret_cast<const f4*>(&sGate[256 + i0]);
+        const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + i0]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int i = tile_row(ti, e) + 8 * g;
-          const float gam = i >= j ? __builtin_amdgcn_exp2f((sGate[192 + i] - gh) + (sGate[256 + i] - gl)) : 0.0f;
-          const float ag = i > j ? -da[n][e] * gam : 0.0f;
-          if (i == j) sU[i] = da[n][e];
-          const float es = group_sum<16>(ag * kk[e]);
-          if (r == 0) sE[tj][i] = es;
-          dp[n][e] = i >= j ? a.scale * dp[n][e] * gam : 0.0f;
-          da[n][e] = sGate[128 + i] * ag;
+          const float gam = i0 + e >= j ? __builtin_amdgcn_exp2f((hi[e] - gh) + (lo[e] - gl)) : 0.0f;
+          if (i0 + e == j) sU[j] = da[n][e];
+          // (a product that is not finite stays out of the half that is not there)
+          const float ag = i0 + e > j ? -da[n][e] * gam : 0.0f;
+          const float es = group_sum<16>(ag == 0.0f ? 0.0f : ag * kk[e]);
+          if (r == 0) sE[tj][i0 + e] = es;
+          dp[n][e] = i0 + e >= j ? a.scale * dp[n][e] * gam : 0.0f;
+          da[n][e] = bt[e] * ag;
         }
-        // F[i][j], and M + M^T at both places (on the diagonal's block of 32
-        // the other half comes from the tile that mirrors this one)
-        Parts<NO> pf, pn;
-        split_d<NO>(pf, dp[n], dp[n]);
-        split_d<NO>(pn, da[n], da[n]);
+        Parts<NO> pf;
+        split_d<NO>(pf, dp[n], da[n]);
+        char* to = smem + 2 * NI * X::PLANE + M::at(j, i0 & ~7) + 2 * (i0 & 7);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = tile_row(ti, e) + 8 * g;
-#pragma unroll
-          for (int q = 0; q < NO; ++q) {
-            const uint16_t vf = __builtin_bit_cast(uint16_t, static_cast<__bf16>(pf.p[q][e]));
-            const uint16_t vn = __builtin_bit_cast(uint16_t, static_cast<__bf16>(pn.p[q][e]));
-            if (i >= j) *reinterpret_cast<uint16_t*>(sF + q * M::PLANE + M::at(i, j & ~7) + 2 * (j & 7)) = vf;
-            else *reinterpret_cast<uint16_t*>(sF + q * M::PLANE + M::at(i, j & ~7) + 2 * (j & 7)) = 0;
-            if (i >= j) {
-              *reinterpret_cast<uint16_t*>(sN + q * M::PLANE + M::at(i, j & ~7) + 2 * (j & 7)) = vn;
-              *reinterpret_cast<uint16_t*>(sN + q * M::PLANE + M::at(j, i & ~7) + 2 * (i & 7)) = vn;
-            }
-          }
+        for (int q = 0; q < NO; ++q) {
+          const uint4 u = __builtin_bit_cast(uint4, pf.p[q]);
+          *reinterpret_cast<uint2*>(to + q * M::PLANE) = uint2{u.x, u.y};
+          *reinterpret_cast<uint2*>(to + (NO + q) * M::PLANE) = uint2{u.z, u.w};
         }
       }
     }
-    __syncthreads();
+    tiles_barrier();
     // dQ = scale exp(G) X1 + F K,  dK = F^T Q + (M + M^T) K - exp(G) beta X2 + exp(G_end - G) X3
-    f4 hq[4], hkk[4];
     float rx[16], re = 0.0f;
-    const T* kp = static_cast<const T*>(a.k) + sl.row0 * a.ldk + hk * DK + dkr;
-    const T* qp = static_cast<const T*>(a.q) + sl.row0 * a.ldq + hk * DK + dkr;
-    float kv[16], qv[16];
-#pragma unroll
-    for (int n = 0; n < 16; ++n) {
-      const int row = tile_row(n / 4, n % 4) + 8 * g, rc = min(row, sl.n - 1);
-      kv[n] = row < sl.n ? to_f32(kp[rc * a.ldk]) : 0.0f;
-      qv[n] = row < sl.n ? to_f32(qp[rc * a.ldq]) : 0.0f;
-    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f4 st = *reinterpret_cast<const f4*>(&sGate[tile_row(i, 0) + 8 * g]);
@@ -421,38 +436,50 @@ __global__ __launch_bounds__(4 * DK, 2) void k_delta_grads(DeltaArgs a) {
       const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + tile_row(i, 0) + 8 * g]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float k = kv[4 * i + e], x = x3[i][e] * en[e];
-        hq[i][e] = a.scale * st[e] * x1[i][e];
+        const float k = X::template get<NI>(sK, tile_row(i, e) + 8 * g, dkr), x = x3[i][e] * en[e];
+        x1[i][e] *= a.scale * st[e];
         rx[4 * i + e] = k * x2[i][e];
         re = fmaf(k, x, re);
-        hkk[i][e] = fmaf(-st[e] * bt[e], x2[i][e], x);
+        x2[i][e] = fmaf(-st[e] * bt[e], x2[i][e], x);
       }
     }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const Parts<NI> kb = X::template by_col<NI>(sK, xl, w, x), qb = X::template by_col<NI>(sQ, xl, w, x);
-      Parts<NO> fa[4], ft[4], na[4];
+      Parts<NO> f[4];
+      // columns of block x and rows of its and later blocks; by_col: of the
+      // transpose's rows, which are its columns
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i >= 2 * x) fa[i] = M::by_row<NO>(sF, ml, i, x);
-        if (i < 2 * x + 2) ft[i] = M::by_col<NO>(sF, ml, i, x);
-        na[i] = M::by_row<NO>(sN, ml, i, x);
-      }
-      mmp<NO>(hkk, na, kb);
+      for (int i = 2 * x; i < 4; ++i) f[i] = M::by_col<NO>(sF, ml, i, x);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i >= 2 * x) hq[i] = mmp<NO>(fa[i], kb, hq[i]);
-        if (i < 2 * x + 2) hkk[i] = mmp<NO>(ft[i], qb, hkk[i]);
-      }
+      for (int i = 2 * x; i < 4; ++i) x1[i] = mmp<NO>(f[i], kb, x1[i]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 2 * x; i < 4; ++i) f[i] = M::by_col<NO>(sN, ml, i, x);
+#pragma unroll
+      for (int i = 2 * x; i < 4; ++i) x2[i] = mmp<NO>(f[i], kb, x2[i]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 2 * x + 2; ++i) f[i] = M::by_row<NO>(sF, ml, i, x);
+#pragma unroll
+      for (int i = 0; i < 2 * x + 2; ++i) x2[i] = mmp<NO>(f[i], qb, x2[i]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 2 * x + 2; ++i) f[i] = M::by_row<NO>(sN, ml, i, x);
+#pragma unroll
+      for (int i = 0; i < 2 * x + 2; ++i) x2[i] = mmp<NO>(f[i], kb, x2[i]);
+      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      dq[i] += hq[i];
-      dk[i] += hkk[i];
+      if constexpr (MULTI) {
+        dq[i] += x1[i];
+        dk[i] += x2[i];
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int row = tile_row(i, e) + 8 * g;
-        const float d = group_sum<16>(fmaf(qv[4 * i + e], hq[i][e], -kv[4 * i + e] * hkk[i][e]));
+        const float d = group_sum<16>(fmaf(X::template get<NI>(sQ, row, dkr), x1[i][e], -X::template get<NI>(sK, row, dkr) * x2[i][e]));
         const float x = group_sum<16>(rx[4 * i + e]);
         if (r == 0) {
           sRow[0][w][row] = d;
@@ -462,7 +489,7 @@ __global__ __launch_bounds__(4 * DK, 2) void k_delta_grads(DeltaArgs a) {
     }
     re = group_sum<64>(re);
     if (lane == 0) sEnd[w] = fmaf(sGate[63], both, re);
-    __syncthreads();
+    tiles_barrier();
     if (w == 0) {
       float d = 0.0f, x = 0.0f, end = 0.0f;
 #pragma unroll
@@ -487,12 +514,19 @@ __global__ __launch_bounds__(4 * DK, 2) void k_delta_grads(DeltaArgs a) {
         static_cast<T*>(a.dbeta)[at] = from_f32<T>(db);
       }
     }
+    if constexpr (!MULTI) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dq[i] = x1[i];
+        dk[i] = x2[i];
+      }
+    }
   }
   const int ldq = a.Hk * DK;
   const ChunkRows oq(static_cast<T*>(a.dq) + sl.row0 * ldq + hk * DK, ldq, sl.n);
   const ChunkRows ok(static_cast<T*>(a.dk) + sl.row0 * ldq + hk * DK, ldq, sl.n);
   const uint32_t orow = static_cast<uint32_t>(ldq) * static_cast<uint32_t>(sizeof(T));
-  const uint32_t oat = 8 * g * orow + dkr * static_cast<uint32_t>(sizeof(T));
+  const uint32_t oat = 8 * g0 * orow + dkr * static_cast<uint32_t>(sizeof(T));
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -504,36 +538,34 @@ __global__ __launch_bounds__(4 * DK, 2) void k_delta_grads(DeltaArgs a) {
 
 template <typename T, int DK>
 hipError_t run_backward(const DeltaArgs& a, hipStream_t s) {
-  constexpr int NBUF = sizeof(T) == 2 ? 2 : 1;
+  constexpr int NBUF = 1;
   const int64_t heads = static_cast<int64_t>(a.B) * a.Hv;
   k_delta_back_chain<T, DK, 4, NBUF><<<static_cast<unsigned>(heads * (a.Dv / 64)), 256, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_delta_grads<T, DK><<<static_cast<unsigned>(static_cast<int64_t>(a.nslot) * a.Hk), 4 * DK, 0, s>>>(a);
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.nslot) * a.Hk);
+  if (a.Hv == a.Hk) k_delta_grads<T, DK, false><<<grid, 4 * DK, 0, s>>>(a);
+  else k_delta_grads<T, DK, true><<<grid, 4 * DK, 0, s>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 size_t delta_backward_workspace_bytes(int B, int T, int Hv, int Dk, int Dv, bool packed) {
-  const size_t chunks = static_cast<size_t>(delta_slots(B, T, packed)) * Hv;
-  return sizeof(float) * chunks * (4096 + kDeltaGates + static_cast<size_t>(Dk + 64) * Dv);
+  return sizeof(float) * static_cast<size_t>(delta_slots(B, T, packed)) * Hv * (Dk + kDeltaChunk) * Dv;
 }
 
 void delta_backward_carve(DeltaArgs& a, void* ws) {
   a.lseg = 30;   // whole sequences
   a.nseg = a.B;
   a.nslot = static_cast<int>(delta_slots(a.B, a.T, a.cu != nullptr));
-  const size_t chunks = static_cast<size_t>(a.nslot) * a.Hv;
-  a.pm = static_cast<float*>(ws);
-  a.gates = a.pm + 4096 * chunks;
-  a.after = a.gates + kDeltaGates * chunks;
-  a.dr = a.after + static_cast<size_t>(a.Dk) * a.Dv * chunks;
+  a.ldpm = delta_state_floats(a.Dk, a.Dv);
+  a.pm = const_cast<float*>(a.cstates) + static_cast<size_t>(a.Dk + kDeltaChunk) * a.Dv;   // (only read)
+  a.after = static_cast<float*>(ws);
+  a.dr = a.after + static_cast<size_t>(a.Dk) * a.Dv * a.nslot * a.Hv;
 }
 
 hipError_t launch_delta_backward(DeltaArgs& a, int bf16, hipStream_t s) {
-  const hipError_t e = launch_delta_chunks(a, bf16, s);
-  if (e != hipSuccess) return e;
   if (bf16) return a.Dk == 64 ? run_backward<bf16_t, 64>(a, s) : run_backward<bf16_t, 128>(a, s);
   return a.Dk == 64 ? run_backward<float, 64>(a, s) : run_backward<float, 128>(a, s);
 }

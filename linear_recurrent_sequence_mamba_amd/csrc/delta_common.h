@@ -104,6 +104,16 @@ struct Rows64 {
 #pragma unroll
     for (int n = 0; n < NP; ++n) *reinterpret_cast<bh8*>(lds + n * PLANE + at(r, c)) = f.p[n];
   }
+  // one element
+  template <int NP>
+  static __device__ __forceinline__ float get(const char* lds, int r, int c) {
+    const char* a = lds + at(r, c & ~7) + 2 * (c & 7);
+    float v = 0.0f;
+#pragma unroll
+    for (int n = NP - 1; n >= 0; --n)
+      v += __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(a + n * PLANE)) << 16);
+    return v;
+  }
   // a lane's addresses of operands by row and by column, for each 32 columns
   struct Lane {
     int row[X], col[X];
@@ -351,16 +361,16 @@ struct Stage {
   using R = Rows64<C, NATURAL>;
   static constexpr int N = 64 * C / 8 / NT, RPI = NT * 8 / C;   // rows of one load
   Vec8<T> v[N];
-  __device__ __forceinline__ void load(const T* p, int64_t ld, int n) {
+  __device__ __forceinline__ void load(const T* p, int64_t ld, int n, uint32_t tid = threadIdx.x) {
     const ChunkRows rows(p, ld, n);
-    const uint32_t r = threadIdx.x / (C / 8), c = threadIdx.x % (C / 8) * 8;
+    const uint32_t r = tid / (C / 8), c = tid % (C / 8) * 8;
     const uint32_t row = static_cast<uint32_t>(ld) * static_cast<uint32_t>(sizeof(T));
     const uint32_t off = r * row + c * static_cast<uint32_t>(sizeof(T));
 #pragma unroll
     for (int i = 0; i < N; ++i) rows.load8(v[i], off + i * RPI * row);
   }
-  __device__ __forceinline__ void store(char* lds) const {
-    const int r = threadIdx.x / (C / 8), c = threadIdx.x % (C / 8) * 8;
+  __device__ __forceinline__ void store(char* lds, uint32_t tid = threadIdx.x) const {
+    const int r = tid / (C / 8), c = tid % (C / 8) * 8;
 #pragma unroll
     for (int i = 0; i < N; ++i) put_raw<R>(lds, r + i * RPI, c, v[i]);
   }

@@ -169,7 +169,7 @@ def test_rows_behind_and_between_are_left():
     p = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())
     ws = torch.empty(lib.m3_delta_scan_workspace_size(ctypes.byref(dims), 1), dtype=torch.uint8, device="cuda")
     o, hT = torch.full_like(v, 7.0), torch.empty_like(h0)
-    st = torch.empty((100 // 64 + 2, 1, 128, 64), device="cuda")
+    st = torch.empty((100 // 64 + 2, 1, m3.m3_delta_state_floats(64, 64)), device="cuda")
     s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     assert lib.m3_delta_scan(ctypes.byref(dims), p(cu), p(q), p(k), p(v), p(g), p(b), p(h0), p(o), p(hT), p(st), p(ws),
                              ws.numel(), s) == 0

@@ -6,7 +6,7 @@
 //
 // One pass: each row is read and written once and everything between stays in
 // registers, so the call is bound by HBM.  A workgroup takes a row at a time,
-// eight elements a thread, and keeps the weights in registers over its rows
+// 16 bytes a thread, and keeps the weights in registers over its rows
 // (from L2 they would be more bytes than the row); the next row is on its way
 // meanwhile.  The sums meet in LDS, one barrier each.
 //
@@ -25,83 +25,71 @@
 namespace m3 {
 namespace {
 
-constexpr int kElems = 8;   // of a thread at a time
-
-// A thread's elements of a row as loaded.  V = 8: NV times eight consecutive
-// ones; V = 1 (a width or a row distance that no vector divides): elements a
-// workgroup's threads apart.  Behind the row's end the first (last) are
-// repeated and their values are 0.
-template <typename T, int V, int NV>
-struct RowPart;
-template <typename T, int NV>
-struct RowPart<T, 8, NV> {
-  RawVec<T, 8> r[NV];
+// A thread's E elements of a row as loaded: whole vectors of V, or (V = 1: a
+// width or a row distance that no vector divides) single elements, both a
+// workgroup's threads apart.  Behind the row's end the first (last) are repeated
+// and their values are 0.
+template <typename T, int V, int E>
+struct RowPart {
+  RawVec<T, V> r[E / V];
   static __device__ __forceinline__ int index(int j) {
-    return ((j / kElems) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * kElems + j % kElems;
+    return ((j / V) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * V + j % V;
   }
   __device__ __forceinline__ void load(const T* row, int W) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = index(i * kElems);
-      r[i].load(row + (e < W ? e : 0));
+    for (int i = 0; i < E / V; ++i) {
+      const int e = index(i * V);
+      r[i].load(row + (V == 1 ? min(e, W - 1) : e < W ? e : 0));
     }
   }
   __device__ __forceinline__ void get(float* v, int W) const {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      r[i].get(v + i * kElems);
-      const bool on = index(i * kElems) < W;
+    for (int i = 0; i < E / V; ++i) {
+      r[i].get(v + i * V);
+      const bool on = index(i * V) < W;
 #pragma unroll
-      for (int j = 0; j < kElems; ++j) v[i * kElems + j] = on ? v[i * kElems + j] : 0.0f;
+      for (int j = 0; j < V; ++j) v[i * V + j] = on ? v[i * V + j] : 0.0f;
     }
   }
-  static __device__ __forceinline__ void put8(float* p, const float* v) {
-    *reinterpret_cast<f4*>(p) = f4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f4*>(p + 4) = f4{v[4], v[5], v[6], v[7]};
-  }
-  static __device__ __forceinline__ void put8(bf16_t* p, const float* v) {
-    uint32_t w[4];
+  static __device__ __forceinline__ void put(float* p, const float* v) {
+    if constexpr (V == 1) {
+      p[0] = v[0];
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[2 * k], v[2 * k + 1]}, bh2));
-    *reinterpret_cast<uint4*>(p) = uint4{w[0], w[1], w[2], w[3]};
-  }
-  static __device__ __forceinline__ void store(T* row, const float* v, int W) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = index(i * kElems);
-      if (e < W) put8(row + e, v + i * kElems);
+      for (int k = 0; k < V / 4; ++k) reinterpret_cast<f4*>(p)[k] = f4{v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]};
     }
   }
-};
-template <typename T, int NV>
-struct RowPart<T, 1, NV> {
-  Raw1<T> r[NV * kElems];
-  static __device__ __forceinline__ int index(int j) {
-    return j * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
-  }
-  __device__ __forceinline__ void load(const T* row, int W) {
+  static __device__ __forceinline__ void put(bf16_t* p, const float* v) {
+    if constexpr (V == 1) {
+      *reinterpret_cast<__bf16*>(p) = static_cast<__bf16>(v[0]);
+    } else {
+      uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < NV * kElems; ++j) r[j].load(row, min(index(j), W - 1));
+      for (int k = 0; k < 4; ++k)
+        w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[2 * k], v[2 * k + 1]}, bh2));
+      *reinterpret_cast<uint4*>(p) = uint4{w[0], w[1], w[2], w[3]};
+    }
   }
-  __device__ __forceinline__ void get(float* v, int W) const {
+  template <typename O>
+  static __device__ __forceinline__ void store(O* row, const float* v, int W) {
 #pragma unroll
-    for (int j = 0; j < NV * kElems; ++j) v[j] = index(j) < W ? r[j].f() : 0.0f;
-  }
-  static __device__ __forceinline__ void store(T* row, const float* v, int W) {
-#pragma unroll
-    for (int j = 0; j < NV * kElems; ++j)
-      if (index(j) < W) row[index(j)] = from_f32<T>(v[j]);
+    for (int i = 0; i < E / V; ++i) {
+      const int e = index(i * V);
+      if (e < W) put(row + e, v + i * V);
+    }
   }
 };
 
 // weights of a thread's elements (1 without any, 0 behind the end)
-template <typename R, int E>
+template <typename T, int V, int E>
 __device__ __forceinline__ void weights(float* w, const float* p, int W) {
+  if (p) {
+    RowPart<float, V, E> r;
+    r.load(p, W);
+    r.get(w, W);
+  } else {
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    const int e = R::index(j);
-    w[j] = e < W ? ld_or(p, e, 1.0f) : 0.0f;
+    for (int j = 0; j < E; ++j) w[j] = RowPart<T, V, E>::index(j) < W ? 1.0f : 0.0f;
   }
 }
 
@@ -144,20 +132,13 @@ __device__ __forceinline__ float gate_act(int act, float g, float& d) {
   return g * s;
 }
 
-template <typename T, int V, int NV>
+template <typename T, int V, int E>
 __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a) {
-  using R = RowPart<T, V, NV>;
-  constexpr int E = NV * kElems;
+  using R = RowPart<T, V, E>;
   __shared__ f2 sh[2][16];
   Sums sums{sh, 0};
   const int W = a.W;
   const float invW = 1.0f / static_cast<float>(W);
-  float wz[E], wn[E];   // of y (with the scale) and of n
-  weights<R, E>(wz, a.wy, W);
-  weights<R, E>(wn, a.scale, W);
-#pragma unroll
-  for (int j = 0; j < E; ++j) wz[j] *= wn[j];
-  weights<R, E>(wn, a.wn, W);
   const T* xp = static_cast<const T*>(a.x);
   const T* yp = static_cast<const T*>(a.y);
   const T* gp = static_cast<const T*>(a.gate);
@@ -168,6 +149,12 @@ __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a) {
     if (gp) rg.load(gp + t * a.ldg, W);
   };
   fetch(blockIdx.x);
+  float wz[E], wn[E];   // of y (with the scale) and of n
+  weights<T, V, E>(wz, a.wy, W);
+  weights<T, V, E>(wn, a.scale, W);
+#pragma unroll
+  for (int j = 0; j < E; ++j) wz[j] *= wn[j];
+  weights<T, V, E>(wn, a.wn, W);
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     float h[E], y[E], g[E];
     ry.get(y, W);
@@ -205,23 +192,13 @@ __global__ __launch_bounds__(1024) void k_block_norm(BlockNormArgs a) {
   }
 }
 
-template <typename T, int V, int NV>
+template <typename T, int V, int E>
 __global__ __launch_bounds__(1024) void k_block_norm_bwd(BlockNormArgs a) {
-  using R = RowPart<T, V, NV>;
-  constexpr int E = NV * kElems;
+  using R = RowPart<T, V, E>;
   __shared__ f2 sh[2][16];
   Sums sums{sh, 0};
   const int W = a.W;
   const float invW = 1.0f / static_cast<float>(W);
-  float wz[E], wn[E], pz[E], pn[E];
-  weights<R, E>(wz, a.wy, W);
-  weights<R, E>(wn, a.scale, W);
-#pragma unroll
-  for (int j = 0; j < E; ++j) {
-    wz[j] *= wn[j];
-    pz[j] = pn[j] = 0.0f;
-  }
-  weights<R, E>(wn, a.wn, W);
   const T* xp = static_cast<const T*>(a.x);
   const T* yp = static_cast<const T*>(a.y);
   const T* gp = static_cast<const T*>(a.gate);
@@ -236,6 +213,15 @@ __global__ __launch_bounds__(1024) void k_block_norm_bwd(BlockNormArgs a) {
     if (hp) rh.load(hp + t * W, W);
   };
   fetch(blockIdx.x);
+  float wz[E], wn[E], pz[E], pn[E];
+  weights<T, V, E>(wz, a.wy, W);
+  weights<T, V, E>(wn, a.scale, W);
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    wz[j] *= wn[j];
+    pz[j] = pn[j] = 0.0f;
+  }
+  weights<T, V, E>(wn, a.wn, W);
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     float h[E], u[E], act[E], da[E], dh[E], gm[E];
     ry.get(u, W);
@@ -305,8 +291,8 @@ __global__ __launch_bounds__(1024) void k_block_norm_bwd(BlockNormArgs a) {
     }
     R::store(static_cast<T*>(a.dy) + t * W, act, W);
   }
-  RowPart<float, V, NV>::store(a.part + static_cast<int64_t>(blockIdx.x) * 2 * W, pz, W);
-  RowPart<float, V, NV>::store(a.part + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * W, pn, W);
+  R::store(a.part + static_cast<int64_t>(blockIdx.x) * 2 * W, pz, W);
+  R::store(a.part + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * W, pn, W);
 }
 
 // The parts of P and dwn of `nblk` workgroups, joined: 64 columns a workgroup,
@@ -335,47 +321,62 @@ __global__ __launch_bounds__(1024) void k_block_norm_join(BlockNormArgs a, int n
   }
 }
 
-// Threads of a workgroup: one for every eight elements, up to 1024.
-int threads_of(int W) {
-  const int n = ((W + kElems - 1) / kElems + 63) / 64 * 64;
-  return n > 1024 ? 1024 : n;
+// Elements of a thread: a vector of 16 bytes, or four single ones, twice or four
+// times where 1024 threads are not enough for the row.  (Eight in fp32 spill the
+// gradients: 5003 rows of 1021 with them 162 us, with four 78.)
+int elems_of(int W, bool wide) {
+  const int e = wide ? 8 : 4;
+  return W <= 1024 * e ? e : W <= 2048 * e ? 2 * e : 4 * e;
+}
+int threads_of(int W, bool wide) {
+  const int e = elems_of(W, wide);
+  return ((W + e - 1) / e + 63) / 64 * 64;
 }
 // Workgroups: as many as are resident, each with several rows.
-int groups_of(int T, int W, int threads_per_cu) {
-  const int most = 256 * (threads_per_cu / threads_of(W));
+int groups_of(int T, int W, bool wide, int threads_per_cu) {
+  const int most = 256 * (threads_per_cu / threads_of(W, wide));
   return T < most ? T : most;
 }
 constexpr int kFwdThreads = 2048, kBwdThreads = 1024;
 
-// eight elements at a time: rows and their distances whole vectors
-bool vectors(const BlockNormArgs& a) { return a.W % 8 == 0 && (a.ldx | a.ldy | a.ldg) % 8 == 0; }
+// rows and their distances whole vectors of 16 bytes
+template <typename T>
+bool vectors(const BlockNormArgs& a) {
+  return (a.W | a.ldx | a.ldy | a.ldg) % (16 / static_cast<int>(sizeof(T))) == 0;
+}
+
+template <typename T, bool BWD, int V, int E>
+hipError_t run(const BlockNormArgs& a, int grid, int nt, hipStream_t s) {
+  if constexpr (BWD) k_block_norm_bwd<T, V, E><<<grid, nt, 0, s>>>(a);
+  else k_block_norm<T, V, E><<<grid, nt, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, bool BWD>
+hipError_t run_rows(const BlockNormArgs& a, int* grid, hipStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  const bool vec = vectors<T>(a), wide = vec && V == 8;
+  const int nt = threads_of(a.W, wide), e = elems_of(a.W, wide);
+  *grid = groups_of(a.T, a.W, wide, BWD ? kBwdThreads : kFwdThreads);
+  if (vec) {
+    if (e == V) return run<T, BWD, V, V>(a, *grid, nt, s);
+    if (e == 2 * V) return run<T, BWD, V, 2 * V>(a, *grid, nt, s);
+    if constexpr (V == 4) return run<T, BWD, V, 4 * V>(a, *grid, nt, s);
+  }
+  if (e == 4) return run<T, BWD, 1, 4>(a, *grid, nt, s);
+  return e == 8 ? run<T, BWD, 1, 8>(a, *grid, nt, s) : run<T, BWD, 1, 16>(a, *grid, nt, s);
+}
 
 template <typename T>
 hipError_t run_fwd(const BlockNormArgs& a, hipStream_t s) {
-  const int nt = threads_of(a.W), grid = groups_of(a.T, a.W, kFwdThreads);
-  const bool two = a.W > 1024 * kElems;
-  if (vectors(a)) {
-    if (two) k_block_norm<T, 8, 2><<<grid, nt, 0, s>>>(a);
-    else k_block_norm<T, 8, 1><<<grid, nt, 0, s>>>(a);
-  } else {
-    if (two) k_block_norm<T, 1, 2><<<grid, nt, 0, s>>>(a);
-    else k_block_norm<T, 1, 1><<<grid, nt, 0, s>>>(a);
-  }
-  return hipGetLastError();
+  int grid;
+  return run_rows<T, false>(a, &grid, s);
 }
 
 template <typename T>
 hipError_t run_bwd(const BlockNormArgs& a, hipStream_t s) {
-  const int nt = threads_of(a.W), grid = groups_of(a.T, a.W, kBwdThreads);
-  const bool two = a.W > 1024 * kElems;
-  if (vectors(a)) {
-    if (two) k_block_norm_bwd<T, 8, 2><<<grid, nt, 0, s>>>(a);
-    else k_block_norm_bwd<T, 8, 1><<<grid, nt, 0, s>>>(a);
-  } else {
-    if (two) k_block_norm_bwd<T, 1, 2><<<grid, nt, 0, s>>>(a);
-    else k_block_norm_bwd<T, 1, 1><<<grid, nt, 0, s>>>(a);
-  }
-  hipError_t e = hipGetLastError();
+  int grid;
+  const hipError_t e = run_rows<T, true>(a, &grid, s);
   if (e != hipSuccess || (!a.dwy && !a.dscale && !a.dwn)) return e;
   k_block_norm_join<<<2 * ((a.W + 63) / 64), 1024, 0, s>>>(a, grid);
   return hipGetLastError();
@@ -384,7 +385,9 @@ hipError_t run_bwd(const BlockNormArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t block_norm_workspace_bytes(int T, int W) {
-  return sizeof(float) * 2 * static_cast<size_t>(groups_of(T, W, kBwdThreads)) * W;
+  // (the more workgroups of the two kinds)
+  const int n = groups_of(T, W, false, kBwdThreads), m = groups_of(T, W, true, kBwdThreads);
+  return sizeof(float) * 2 * static_cast<size_t>(n > m ? n : m) * W;
 }
 
 hipError_t launch_block_norm(const BlockNormArgs& a, int bf16, hipStream_t s) {

@@ -50,7 +50,9 @@ struct DeltaPlan {
   int64_t nseg;   // slots of segments
   bool split;     // some sequence may have more than one
 };
-DeltaPlan delta_plan(int B, int T, int Hv, int Dk, int Dv, bool packed);
+DeltaPlan delta_plan(int B, int T, int Hv, int Dk, int Dv, bool packed, bool back);
+size_t delta_segment_bytes(const DeltaPlan& p, int Hv, int Dk, int Dv);
+void delta_carve_segments(DeltaArgs& a, const DeltaPlan& p, void* ws);
 
 inline int64_t delta_state_floats(int Dk, int Dv) {
   return static_cast<int64_t>(Dk + kDeltaChunk) * Dv + kDeltaMatrix + kDeltaGates;

@@ -15,83 +15,82 @@
 //   dG_i = q_i.dq_i - k_i.dk_i + 2 (dR_i.U_i - dV_i.v_i),
 // to which the chunk's last row adds <S1, dS1> = sum_j exp(G_end - G_j) k_j.X3_j
 // + exp(G_end) <S0, dS1>; and dg_t = sum_{i >= t} dG_i.
-#include "delta_common.h"
+#include "delta_chain.h"
 
 namespace m3 {
 namespace {
 
 // ---------------------------------------------------------------------------
-// The chain, as the scan's: a wave holds 16 columns of dS.
-template <typename T, int DK, int NW, int NBUF>
-__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_chain(DeltaArgs a) {
+// The chain, as the scan's and with its segments: a wave holds 16 columns of dS.
+// FULL false: only the gradient of the state before the segment, from none
+// behind it (the last segment: from dhT).
+template <typename T, int DK, int NW, int NBUF, bool FULL>
+__device__ __forceinline__ void back_chain(const DeltaArgs& a, const DeltaSeg& seg, int slot, int h, int slice, char* smem) {
   using X = Rows64<DK>;
   using M = Rows64<64>;
   constexpr int NT = 64 * NW, KS = DK / 32, DT = DK / 16, NI = DeltaParts<T>::IN;
-  constexpr int BK = NI * X::PLANE, BM = 3 * M::PLANE, BUF = 2 * BK + BM + 768, NG = (192 + NT - 1) / NT;
-  __shared__ __align__(16) char smem[NBUF * BUF];
+  using Tiles = ChainTiles<T, DK, NT, true>;
+  constexpr int BK = Tiles::BK, BM = Tiles::BM, BUF = Tiles::BUF;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  const int nsl = a.Dv / (16 * NW), n0 = blockIdx.x / nsl;
-  const int h = n0 % a.Hv, s = n0 / a.Hv, hk = h / (a.Hv / a.Hk);
-  const int col = 16 * ((blockIdx.x % nsl) * NW + w) + r;
-  const DeltaSeg seg(a, s, lane);   // (the whole sequence)
-  if (seg.s < 0) return;
+  const int r = lane & 15, g = lane >> 4, hk = h / (a.Hv / a.Hk);
+  const int cs = slice * NW + w, col = 16 * cs + r;
   const Triangle tri(lane);
   const typename X::Lane xl(lane);
   const M::Lane ml(lane);
-  const int64_t head = static_cast<int64_t>(seg.s) * a.Hv + h, dd = static_cast<int64_t>(DK) * a.Dv;
-  const uint32_t at = static_cast<uint32_t>(8 * g * a.Dv + col);
+  const int64_t head = static_cast<int64_t>(seg.s) * a.Hv + h, shead = static_cast<int64_t>(slot) * a.Hv + h;
+  const int64_t dd = static_cast<int64_t>(DK) * a.Dv;
+  const uint32_t at = static_cast<uint32_t>(8 * g * a.Dv + col), end_at = (cs * DT * 64 + lane) * 4;
   const int ldo = a.Hv * a.Dv;
 
   f4 S[DT];
 #pragma unroll
-  for (int t = 0; t < DT; ++t)
+  for (int t = 0; t < DT; ++t) S[t] = f4{0, 0, 0, 0};
+  if (!seg.last) {
+    if constexpr (FULL)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) S[t][e] = a.dhT ? (a.dhT + head * dd + tile_row(t, e) * a.Dv)[at] : 0.0f;
+      for (int t = 0; t < DT; ++t) S[t] = *reinterpret_cast<const f4*>(a.ends + shead * dd + end_at + t * 256);
+  } else if (a.dhT) {
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[t][e] = (a.dhT + head * dd + tile_row(t, e) * a.Dv)[at];
+  }
 
-  Stage<T, DK, NT> stK, stQ;
-  Stage<float, 64, NT> stM;
-  float stG[NG];
+  Tiles st;
   Cols<T> stO;
+  const int c0 = seg.c0, c1 = seg.c0 + seg.nch;
   auto rows = [&](int c) __attribute__((always_inline)) { return min(kDeltaChunk, seg.len - c * kDeltaChunk); };
   auto first = [&](int c) __attribute__((always_inline)) { return seg.row0 + static_cast<int64_t>(c) * kDeltaChunk; };
   auto fetch = [&](int c) __attribute__((always_inline)) {
-    c = max(c, 0);
+    c = max(c, c0);
     const int64_t m = static_cast<int64_t>(seg.slot0 + c) * a.Hv + h;
-    stK.load(static_cast<const T*>(a.k) + first(c) * a.ldk + hk * DK, a.ldk, rows(c));
-    stM.load(a.pm + m * a.ldpm, 64, 64);
+    st.k.load(static_cast<const T*>(a.k) + first(c) * a.ldk + hk * DK, a.ldk, rows(c));
+    st.m.load(a.pm + m * a.ldpm, 64, 64);
 #pragma unroll
-    for (int i = 0; i < NG; ++i) stG[i] = (a.pm + m * a.ldpm + kDeltaMatrix)[min(threadIdx.x + i * NT, 191u)];
-    stQ.load(static_cast<const T*>(a.q) + first(c) * a.ldq + hk * DK, a.ldq, rows(c));
+    for (int i = 0; i < Tiles::NG; ++i) st.g[i] = (a.pm + m * a.ldpm + kDeltaMatrix)[min(threadIdx.x + i * NT, 191u)];
+    st.q.load(static_cast<const T*>(a.q) + first(c) * a.ldq + hk * DK, a.ldq, rows(c));
   };
   auto fetch_o = [&](int c) __attribute__((always_inline)) {
-    c = max(c, 0);
+    c = max(c, c0);
     stO.load(static_cast<const T*>(a.dout) + first(c) * ldo + h * a.Dv, ldo, rows(c), col, g);
   };
-  auto store = [&](char* b) __attribute__((always_inline)) {
-    stK.store(b);
-    stQ.store(b + BK);
-    stM.store(b + 2 * BK);
-#pragma unroll
-    for (int i = 0; i < NG; ++i)
-      if (threadIdx.x + i * NT < 192) reinterpret_cast<float*>(b + 2 * BK + BM)[threadIdx.x + i * NT] = stG[i];
-  };
   if (seg.nch > 0) {
-    fetch(seg.nch - 1);
-    fetch_o(seg.nch - 1);
-    store(smem);
-    if constexpr (NBUF == 2) fetch(seg.nch - 2);
+    fetch(c1 - 1);
+    fetch_o(c1 - 1);
+    st.store(smem);
+    if constexpr (NBUF == 2) fetch(c1 - 2);
   }
   char* buf = smem;
-  for (int c = seg.nch - 1; c >= 0; --c) {
+  for (int c = c1 - 1; c >= c0; --c) {
     const char *sK = buf, *sQ = buf + BK, *sM = buf + 2 * BK;
     const float* sGate = reinterpret_cast<const float*>(buf + 2 * BK + BM);
     const int64_t m = static_cast<int64_t>(seg.slot0 + c) * a.Hv + h;
     tiles_barrier();
+    if constexpr (FULL)
 #pragma unroll
-    for (int t = 0; t < DT; ++t)
+      for (int t = 0; t < DT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) (a.after + m * dd + tile_row(t, e) * a.Dv)[at] = S[t][e];
+        for (int e = 0; e < 4; ++e) (a.after + m * dd + tile_row(t, e) * a.Dv)[at] = S[t][e];
     // K dS1
     f4 ks[4];
     Parts<NI> ka[2][4];
@@ -181,7 +180,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
       mmt6<3>(u, ta[n & 1], up, n);
       if (n == 0 && NBUF == 2) {
         buf = buf == smem ? smem + BUF : smem;
-        store(buf);   // (the last time unread)
+        st.store(buf);   // (the last time unread)
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -200,9 +199,9 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
         const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + tile_row(i, 0) + 8 * g]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          (dr + tile_row(i, e) * a.Dv)[at] = u[i][e];
+          if constexpr (FULL) (dr + tile_row(i, e) * a.Dv)[at] = u[i][e];
           u[i][e] *= bt[e];
-          dv.store1(T{}, oat + tile_row(i, e) * orow, u[i][e]);
+          if constexpr (FULL) dv.store1(T{}, oat + tile_row(i, e) * orow, u[i][e]);
           u[i][e] *= -st[e];
         }
       }
@@ -215,16 +214,40 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
     add(sK);
     if constexpr (NBUF == 1) {
       tiles_barrier();
-      store(buf);
+      st.store(buf);
     } else {
       fetch(c - 2);
     }
   }
-  if (a.dh0)
+  if constexpr (!FULL) {   // to where the segment before ends
+#pragma unroll
+    for (int t = 0; t < DT; ++t) *reinterpret_cast<f4*>(a.ends + (shead - a.Hv) * dd + end_at + t * 256) = S[t];
+  } else if (seg.j == 0 && a.dh0) {
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) (a.dh0 + head * dd + tile_row(t, e) * a.Dv)[at] = S[t][e];
+  }
+}
+
+template <typename T, int DK, int NW, int NBUF>
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_chain(DeltaArgs a) {
+  __shared__ __align__(16) char smem[NBUF * ChainTiles<T, DK, 64 * NW, true>::BUF];
+  const int nsl = a.Dv / (16 * NW), n = blockIdx.x / nsl;
+  const DeltaSeg seg(a, n / a.Hv, threadIdx.x & 63);
+  if (seg.s >= 0) back_chain<T, DK, NW, NBUF, true>(a, seg, n / a.Hv, n % a.Hv, blockIdx.x % nsl, smem);
+}
+
+// the gradients before all segments but the first, and the maps of those between
+template <typename T, int DK, int NW, int NBUF>
+__global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_segments(DeltaArgs a) {
+  __shared__ __align__(16) char smem[NBUF * ChainTiles<T, DK, 64 * NW, true>::BUF];
+  const int nv = a.Dv / (16 * NW), nsl = nv + DK / (16 * NW);
+  const int n = blockIdx.x / nsl, slice = blockIdx.x % nsl;
+  const DeltaSeg seg(a, n / a.Hv, threadIdx.x & 63);
+  if (seg.s < 0 || seg.j == 0) return;
+  if (slice < nv) back_chain<T, DK, NW, NBUF, false>(a, seg, n / a.Hv, n % a.Hv, slice, smem);
+  else if (!seg.last) chain<T, DK, NW, NBUF, kMapsT>(a, seg, n / a.Hv, n % a.Hv, slice - nv, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -255,6 +278,9 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
   using M = Rows64<64>;
   using G = GradTiles<T, DK>;
   constexpr int NI = G::NI, NO = G::NO, NW = DK / 16, NT = 64 * NW, NTILE = (12 + NW - 1) / NW, VN = 512 / NT;
+  // where there is room, the sums over heads wait in LDS (in registers they spill)
+  constexpr bool PARK = MULTI && sizeof(T) == 2;
+  __shared__ float sAcc[PARK ? 32 : 1][PARK ? NT : 1];
   __shared__ __align__(16) char smem[G::BYTES];
   __shared__ __align__(16) float sGate[kDeltaGates];
   __shared__ float sRow[2][NW][64], sE[4][64], sU[64], sV[64], sEnd[NW];
@@ -472,7 +498,14 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if constexpr (MULTI) {
+      if constexpr (PARK) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float *q = &sAcc[4 * i + e][tid], *k = &sAcc[16 + 4 * i + e][tid];
+          *q = h > hk * group ? *q + x1[i][e] : x1[i][e];
+          *k = h > hk * group ? *k + x2[i][e] : x2[i][e];
+        }
+      } else if constexpr (MULTI) {
         dq[i] += x1[i];
         dk[i] += x2[i];
       }
@@ -531,17 +564,36 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      oq.store1(T{}, oat + tile_row(i, e) * orow, dq[i][e]);
-      ok.store1(T{}, oat + tile_row(i, e) * orow, dk[i][e]);
+      oq.store1(T{}, oat + tile_row(i, e) * orow, PARK ? sAcc[4 * i + e][threadIdx.x] : dq[i][e]);
+      ok.store1(T{}, oat + tile_row(i, e) * orow, PARK ? sAcc[16 + 4 * i + e][threadIdx.x] : dk[i][e]);
     }
+}
+
+template <typename T, int DK, int NW>
+hipError_t run_back_chain(const DeltaArgs& a, hipStream_t s) {
+  constexpr int NBUF = sizeof(T) == 2 && NW == 8 ? 2 : 1;
+  const int64_t heads = static_cast<int64_t>(a.nseg) * a.Hv;
+  if (a.lseg < 30) {
+    k_delta_back_segments<T, DK, NW, NBUF>
+        <<<static_cast<unsigned>(heads * ((a.Dv + DK) / (16 * NW))), 64 * NW, 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    k_delta_join<DK, DeltaParts<T>::OUT, true>
+        <<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hv * (a.Dv / 16)), 64, 0, s>>>(a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  k_delta_back_chain<T, DK, NW, NBUF><<<static_cast<unsigned>(heads * (a.Dv / (16 * NW))), 64 * NW, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 template <typename T, int DK>
 hipError_t run_backward(const DeltaArgs& a, hipStream_t s) {
-  constexpr int NBUF = 1;
-  const int64_t heads = static_cast<int64_t>(a.B) * a.Hv;
-  k_delta_back_chain<T, DK, 4, NBUF><<<static_cast<unsigned>(heads * (a.Dv / 64)), 256, 0, s>>>(a);
-  hipError_t e = hipGetLastError();
+  hipError_t e;
+  if constexpr (DK == 128 && sizeof(T) == 2)
+    e = a.Dv == 128 ? run_back_chain<T, DK, 8>(a, s) : run_back_chain<T, DK, 4>(a, s);
+  else
+    e = run_back_chain<T, DK, 4>(a, s);
   if (e != hipSuccess) return e;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.nslot) * a.Hk);
   if (a.Hv == a.Hk) k_delta_grads<T, DK, false><<<grid, 4 * DK, 0, s>>>(a);
@@ -552,17 +604,18 @@ hipError_t run_backward(const DeltaArgs& a, hipStream_t s) {
 }  // namespace
 
 size_t delta_backward_workspace_bytes(int B, int T, int Hv, int Dk, int Dv, bool packed) {
-  return sizeof(float) * static_cast<size_t>(delta_slots(B, T, packed)) * Hv * (Dk + kDeltaChunk) * Dv;
+  return sizeof(float) * static_cast<size_t>(delta_slots(B, T, packed)) * Hv * (Dk + kDeltaChunk) * Dv +
+         delta_segment_bytes(delta_plan(B, T, Hv, Dk, Dv, packed, true), Hv, Dk, Dv);
 }
 
 void delta_backward_carve(DeltaArgs& a, void* ws) {
-  a.lseg = 30;   // whole sequences
-  a.nseg = a.B;
-  a.nslot = static_cast<int>(delta_slots(a.B, a.T, a.cu != nullptr));
+  const size_t chunks = static_cast<size_t>(delta_slots(a.B, a.T, a.cu != nullptr)) * a.Hv;
   a.ldpm = delta_state_floats(a.Dk, a.Dv);
   a.pm = const_cast<float*>(a.cstates) + static_cast<size_t>(a.Dk + kDeltaChunk) * a.Dv;   // (only read)
   a.after = static_cast<float*>(ws);
-  a.dr = a.after + static_cast<size_t>(a.Dk) * a.Dv * a.nslot * a.Hv;
+  a.dr = a.after + static_cast<size_t>(a.Dk) * a.Dv * chunks;
+  delta_carve_segments(a, delta_plan(a.B, a.T, a.Hv, a.Dk, a.Dv, a.cu != nullptr, true),
+                       a.dr + static_cast<size_t>(kDeltaChunk) * a.Dv * chunks);
 }
 
 hipError_t launch_delta_backward(DeltaArgs& a, int bf16, hipStream_t s) {

@@ -1,0 +1,395 @@
+// delta_chain.h -- the chain of the gated delta rule over a sequence's chunks, and
+// what passes states through its segments (gfx950).  Not part of the public ABI.
+#pragma once
+
+#include "delta_common.h"
+
+namespace m3 {
+namespace {
+
+// The chain.  A wave holds 16 columns of a head's state, so that nothing of it
+// is ever exchanged; the NW waves of a workgroup share K, Q and the chunk's
+// matrix in LDS.  The next chunk is on its way in registers meanwhile.
+//
+// Where sequences and heads are too few to fill the chip, a sequence's chunks
+// are cut into segments.  A segment maps the state before it as S -> E + F S.
+// kEnds gives E (a state that starts from zero), kMaps F (the columns of the
+// identity as a state, without values), k_delta_join passes the states through
+// the segments, and the segments then run at once.
+//
+// Parts (bf16): what reaches the state has three, so that it keeps fp32's
+// accuracy; P and U, which only reach outputs in bf16, two; a map, whose decay
+// is kept apart in fp32, two (2^-17 of what the segment's keys take out).
+//
+// With room for two of a chunk's tiles (NBUF = 2) the next chunk's are written
+// while waves still read this one's, and one barrier a chunk is enough.
+enum { kFull = 0, kEnds = 1, kMaps = 2, kMapsT = 3 };   // (kMapsT: the map's transpose, for the gradients)
+
+template <typename T, int DK, int NT, bool FULL>
+struct ChainTiles {
+  using X = Rows64<DK>;
+  using M = Rows64<64>;
+  static constexpr int NI = DeltaParts<T>::IN, NO = DeltaParts<T>::OUT;
+  static constexpr int BK = NI * X::PLANE, BQ = FULL ? BK : 0, BM = 3 * M::PLANE, BUF = BK + BQ + BM + 768;
+  static constexpr int NG = (192 + NT - 1) / NT;
+  Stage<T, DK, NT> k, q;
+  Stage<float, 64, NT> m;
+  float g[NG];
+  __device__ __forceinline__ void store(char* b) const {
+    k.store(b);
+    if constexpr (FULL) q.store(b + BK);
+    m.store(b + BK + BQ);
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+      if (threadIdx.x + i * NT < 192) reinterpret_cast<float*>(b + BK + BQ + BM)[threadIdx.x + i * NT] = g[i];
+  }
+};
+
+template <typename T, int DK, int NW, int NBUF, int MODE>
+__device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, int slot, int h, int slice, char* smem) {
+  using X = Rows64<DK>;
+  constexpr bool FULL = MODE == kFull, MAPS = MODE == kMaps || MODE == kMapsT;
+  constexpr int NT = 64 * NW, KS = DK / 32, DT = DK / 16;
+  using Tiles = ChainTiles<T, DK, NT, FULL>;
+  constexpr int NI = Tiles::NI, NO = Tiles::NO, NS = MAPS ? NO : 3;
+  constexpr int BK = Tiles::BK, BQ = Tiles::BQ, BM = Tiles::BM, BUF = Tiles::BUF;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4, hk = h / (a.Hv / a.Hk);
+  const int cs = slice * NW + w, col = 16 * cs + r;   // of the values, or of the map
+  const Triangle tri(lane);
+  const typename X::Lane xl(lane);
+  const Rows64<64>::Lane ml(lane);
+  const int64_t head = static_cast<int64_t>(seg.s) * a.Hv + h, shead = static_cast<int64_t>(slot) * a.Hv + h;
+  const int64_t dd = static_cast<int64_t>(DK) * a.Dv;
+  const uint32_t at = static_cast<uint32_t>(8 * g * a.Dv + col);   // of a state
+  const uint32_t end_at = (cs * DT * 64 + lane) * 4;               // of a segment's
+
+  f4 S[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) S[t] = f4{0, 0, 0, 0};
+  if constexpr (MAPS) {
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[t][e] = tile_row(t, e) + 8 * g == col ? 1.0f : 0.0f;
+  } else if (FULL && seg.j > 0) {
+#pragma unroll
+    for (int t = 0; t < DT; ++t) S[t] = *reinterpret_cast<const f4*>(a.ends + shead * dd + end_at + t * 256);
+  } else if (a.h0 && seg.j == 0) {
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[t][e] = (a.h0 + head * dd + tile_row(t, e) * a.Dv)[at];
+  }
+
+  Tiles st;
+  Cols<T> stV;
+  const int c1 = seg.c0 + seg.nch;
+  auto rows = [&](int c) __attribute__((always_inline)) { return min(kDeltaChunk, seg.len - c * kDeltaChunk); };
+  auto first = [&](int c) __attribute__((always_inline)) { return seg.row0 + static_cast<int64_t>(c) * kDeltaChunk; };
+  // (behind the last chunk the last one again, unused)
+  auto fetch = [&](int c) __attribute__((always_inline)) {
+    c = min(c, c1 - 1);
+    const int64_t m = static_cast<int64_t>(seg.slot0 + c) * a.Hv + h;
+    st.k.load(static_cast<const T*>(a.k) + first(c) * a.ldk + hk * DK, a.ldk, rows(c));
+    st.m.load(a.pm + m * a.ldpm, 64, 64);
+#pragma unroll
+    for (int i = 0; i < Tiles::NG; ++i) st.g[i] = (a.pm + m * a.ldpm + kDeltaMatrix)[min(threadIdx.x + i * NT, 191u)];
+    if constexpr (FULL) st.q.load(static_cast<const T*>(a.q) + first(c) * a.ldq + hk * DK, a.ldq, rows(c));
+  };
+  auto fetch_v = [&](int c) __attribute__((always_inline)) {
+    c = min(c, c1 - 1);
+    if constexpr (!MAPS) stV.load(static_cast<const T*>(a.v) + first(c) * a.ldv + h * a.Dv, a.ldv, rows(c), col, g);
+  };
+  if (seg.nch > 0) {
+    fetch(seg.c0);
+    fetch_v(seg.c0);
+    st.store(smem);
+    if constexpr (NBUF == 2) fetch(seg.c0 + 1);
+  }
+  char* buf = smem;
+  float decay = 1.0f;   // of the segment
+  for (int c = seg.c0; c < c1; ++c) {
+    const char *sK = buf, *sQ = buf + BK, *sM = buf + BK + BQ;
+    const float* sGate = reinterpret_cast<const float*>(buf + BK + BQ + BM);
+    tiles_barrier();
+    if (FULL && a.states) {
+      float* p = a.states + (static_cast<int64_t>(seg.slot0 + c) * a.Hv + h) * a.ldpm;
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) (p + tile_row(t, e) * a.Dv)[at] = S[t][e];
+    }
+    // K S0 and Q S0, the next operands read ahead of their products
+    f4 ks[4], qs[4];
+    Parts<NI> ka[2][4], qa[2][4];
+    Parts<NS> sp[2];
+    auto read = [&](int x) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ka[x & 1][i] = X::template by_row<NI>(sK, xl, i, x);
+      if constexpr (FULL)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qa[x & 1][i] = X::template by_row<NI>(sQ, xl, i, x);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ks[i] = qs[i] = f4{0, 0, 0, 0};
+    read(0);
+    split_d<NS>(sp[0], S[0], S[1]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+      if (x + 1 < KS) {
+        read(x + 1);
+        split_d<NS>(sp[(x + 1) & 1], S[2 * x + 2], S[2 * x + 3]);
+      }
+      mmp<NS>(ks, ka[x & 1], sp[x & 1]);
+      if constexpr (FULL) mmp<NO>(qs, qa[x & 1], sp[x & 1]);
+      if constexpr (NI == 1) interleave<FULL ? 8 : 4, FULL ? 20 : 4 * NS, FULL ? 3 : 4>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // R = beta (V - exp(G) K S0) in place of K S0
+    Parts<1> ta[2][6];
+    tri.t6(ta[0], sM, ml, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f4 st = *reinterpret_cast<const f4*>(&sGate[tile_row(i, 0) + 8 * g]);
+      const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + tile_row(i, 0) + 8 * g]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) ks[i][e] = bt[e] * fmaf(-st[e], ks[i][e], MAPS ? 0.0f : stV.v[4 * i + e].f());
+    }
+    Parts<NS> rp[2];
+    split_d<NS>(rp[0], ks[0], ks[1]);
+    split_d<NS>(rp[1], ks[2], ks[3]);
+    __builtin_amdgcn_sched_barrier(0);
+    // U = T R: R itself for the diagonal
+    f4 u[6] = {ks[0], ks[1], ks[2], ks[3], f4{0, 0, 0, 0}, f4{0, 0, 0, 0}};
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      if (n + 1 < NS) tri.t6(ta[(n + 1) & 1], sM, ml, n + 1);
+      mm6<NS>(u, ta[n & 1], rp, n);
+      if (n == 0 && NBUF == 2) {
+        buf = buf == smem ? smem + BUF : smem;
+        st.store(buf);   // (the last time unread)
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    u[2] += u[4];
+    u[3] += u[5];
+    if constexpr (NBUF == 1) fetch(c + 1);   // (in few registers until then)
+    // O = scale exp(G) Q S0 + P U
+    if constexpr (FULL) {
+      if (a.states) {
+        float* p = a.states + (static_cast<int64_t>(seg.slot0 + c) * a.Hv + h) * a.ldpm + dd;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) (p + tile_row(i, e) * a.Dv)[at] = u[i][e];
+      }
+      Parts<1> pa[2][6];
+      tri.p6(pa[0], sM, ml, 0);
+      f4 y[6];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f4 st = *reinterpret_cast<const f4*>(&sGate[tile_row(i, 0) + 8 * g]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[i][e] = a.scale * st[e] * qs[i][e];
+      }
+      y[4] = y[5] = f4{0, 0, 0, 0};
+      Parts<NO> up[2];
+      split_d<NO>(up[0], u[0], u[1]);
+      split_d<NO>(up[1], u[2], u[3]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int n = 0; n < NO; ++n) {
+        if (n + 1 < NO) tri.p6(pa[(n + 1) & 1], sM, ml, n + 1);
+        mm6<NO>(y, pa[n & 1], up, n);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      y[2] += y[4];
+      y[3] += y[5];
+      const int ldo = a.Hv * a.Dv;
+      const ChunkRows o(static_cast<T*>(a.o) + first(c) * ldo + h * a.Dv, ldo, rows(c));
+      const uint32_t orow = static_cast<uint32_t>(ldo) * static_cast<uint32_t>(sizeof(T));
+      const uint32_t oat = 8 * g * orow + col * static_cast<uint32_t>(sizeof(T));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o.store1(T{}, oat + tile_row(i, e) * orow, y[i][e]);
+    }
+    fetch_v(c + 1);
+    // S1 = exp(G_end) S0 + K^T (exp(G_end - G) U)
+    Parts<NI> kc[2][4];
+    auto read_t = [&](int n) __attribute__((always_inline)) {   // four tiles of S, 32 rows
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        kc[n & 1][t] = X::template by_col<NI>(sK, xl, 4 * (n % (DT / 4)) + t, n / (DT / 4));
+    };
+    Parts<NS> ep[2];
+    read_t(0);
+    const float last = sGate[63];
+    decay *= last;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) u[i] *= *reinterpret_cast<const f4*>(&sGate[64 + tile_row(i, 0) + 8 * g]);
+    split_d<NS>(ep[0], u[0], u[1]);
+#pragma unroll
+    for (int t = 0; t < DT; ++t) S[t] *= last;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < DT / 2; ++n) {
+      if (n + 1 < DT / 2) read_t(n + 1);
+      if (n == 0) {
+#pragma unroll
+        for (int i = 2; i < 4; ++i) u[i] *= *reinterpret_cast<const f4*>(&sGate[64 + tile_row(i, 0) + 8 * g]);
+        split_d<NS>(ep[1], u[2], u[3]);
+      }
+      mmp<NS>(*reinterpret_cast<f4(*)[4]>(&S[4 * (n % (DT / 4))]), kc[n & 1], ep[n / (DT / 4)]);
+      if constexpr (NI == 1)
+        if (n == 0) interleave<10, 4 * NS, 4>();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (NBUF == 1) {
+      tiles_barrier();
+      st.store(buf);
+    } else {
+      fetch(c + 2);
+    }
+  }
+  if constexpr (MAPS) {   // less its decay, as the A operand of a product over its columns (or rows)
+    uint16_t* p = a.maps + shead * NS * DK * DK;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[t][e] -= tile_row(t, e) + 8 * g == col ? decay : 0.0f;
+    if constexpr (MODE == kMaps) {
+      const uint32_t to = col / 32 * 512 + (col % 32 / 8 * 16 + 4 * g) * 8 + col % 8;
+#pragma unroll
+      for (int t = 0; t < DT; ++t) {
+        Parts<NS> f;
+        split_d<NS>(f, S[t], S[t]);
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+          const uint4 u = __builtin_bit_cast(uint4, f.p[n]);
+          const uint32_t i = to + (n * DT + t) * KS * 512;
+          p[i] = static_cast<uint16_t>(u.x);
+          p[i + 8] = static_cast<uint16_t>(u.x >> 16);
+          p[i + 16] = static_cast<uint16_t>(u.y);
+          p[i + 24] = static_cast<uint16_t>(u.y >> 16);
+        }
+      }
+    } else {   // row col of the transpose: row 4 (col / 8) + col % 4 of tile 2 (col / 32) + col / 4 % 2
+      const uint32_t to = (2 * (col >> 5) + ((col >> 2) & 1)) * KS * 512 + (16 * g + 4 * ((col >> 3) & 3) + (col & 3)) * 8;
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        Parts<NS> f;
+        split_d<NS>(f, S[2 * x], S[2 * x + 1]);
+#pragma unroll
+        for (int n = 0; n < NS; ++n) *reinterpret_cast<bh8*>(p + to + n * DT * KS * 512 + x * 512) = f.p[n];
+      }
+    }
+    if (cs == 0 && lane == 0) a.decays[shead] = decay;
+  } else if constexpr (MODE == kEnds) {   // to where the next segment starts
+#pragma unroll
+    for (int t = 0; t < DT; ++t) *reinterpret_cast<f4*>(a.ends + (shead + a.Hv) * dd + end_at + t * 256) = S[t];
+  } else if (seg.last && a.hT) {
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) (a.hT + head * dd + tile_row(t, e) * a.Dv)[at] = S[t][e];
+  }
+}
+
+// The states before the segments: S_{j+1} = E_j + d_j S_j + F_j S_j, with the
+// decay d_j apart from the map.  E_j lies where S_{j+1} goes; S_1 is there
+// already.  BACK: the gradients of the states behind them, from the last to the
+// first, with the maps' transposes.  A wave has 16 columns of a sequence's head.  F arrives in blocks of
+// 32 columns which lie as the operands do, through a ring of blocks in LDS.
+template <int DK, int NP, bool BACK>
+__global__ __launch_bounds__(64) void k_delta_join(DeltaArgs a) {
+  constexpr int KS = DK / 32, DT = DK / 16, NF = NP * DT;   // NF: operands of a block
+  // each by its name, so that reads of one do not wait for the others' loads
+  __shared__ __align__(16) char r0[NF * 1024], r1[NF * 1024], r2[KS > 2 ? NF * 1024 : 16], r3[KS > 2 ? NF * 1024 : 16];
+  auto ring = [&](int x) __attribute__((always_inline)) { return x == 0 ? r0 : x == 1 ? r1 : x == 2 ? r2 : r3; };
+  const int lane = threadIdx.x;
+  const int nsl = a.Dv / 16;
+  int b = blockIdx.x;
+  const int slice = b % nsl;
+  b /= nsl;
+  const int h = b % a.Hv, s = b / a.Hv;
+  int len, slot0;
+  if (a.cu) {
+    const int c = clamp_row(a.cu[s], a.T);
+    len = max(0, clamp_row(a.cu[s + 1], a.T) - c);
+    slot0 = (c >> (6 + a.lseg)) + s;
+  } else {
+    len = a.T;
+    slot0 = s * (a.nseg / a.B);
+  }
+  const int nseg = (((len + kDeltaChunk - 1) / kDeltaChunk) + (1 << a.lseg) - 1) >> a.lseg;
+  if (nseg <= 2) return;
+  const int64_t next_seg = BACK ? -a.Hv : a.Hv;
+  const int64_t shead = static_cast<int64_t>(slot0 + (BACK ? nseg - 2 : 1)) * a.Hv + h, step = next_seg * DK * a.Dv;
+  float* p = a.ends + shead * DK * a.Dv + (slice * DT * 64 + lane) * 4;
+  const uint16_t* f = a.maps + shead * NP * DK * DK + lane * 8;
+  const float* d = a.decays + shead;
+  // block x of segment j's map
+  auto fetch = [&](int j, int x) __attribute__((always_inline)) {
+    const uint16_t* from = f + (j - 1) * next_seg * NP * DK * DK + x * 512;
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+      __builtin_amdgcn_global_load_lds((const M3_GLB void*)(from + i * KS * 512), (M3_LDS void*)(ring(x) + i * 1024), 16, 0, 0);
+  };
+  f4 S[DT], E[DT], next[DT];
+  float dec = d[0], dnext = 0.0f;
+#pragma unroll
+  for (int t = 0; t < DT; ++t) {
+    S[t] = *reinterpret_cast<const f4*>(p + t * 256);
+    E[t] = *reinterpret_cast<const f4*>(p + step + t * 256);
+    next[t] = f4{0, 0, 0, 0};
+  }
+#pragma unroll
+  for (int x = 0; x < KS - 1; ++x) fetch(1, x);
+  for (int j = 1; j + 1 < nseg; ++j) {
+    p += step;
+    const bool more = j + 2 < nseg;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) E[t][e] = fmaf(dec, S[t][e], E[t][e]);
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+      // this block is there; the KS - 2 behind it may be on their way
+      if (x == 0 || more) __builtin_amdgcn_s_waitcnt(0x0f70 | ((KS - 2) * NF & 15) | ((KS - 2) * NF >> 4 << 14));
+      else lds_loads_done();
+      lds_reads_done();
+      if (x == 0) fetch(j, KS - 1);
+      else if (more) fetch(j + 1, x - 1);
+      if (x == 1 && more) {   // the next E_j
+        dnext = d[j * next_seg];
+#pragma unroll
+        for (int t = 0; t < DT; ++t) next[t] = *reinterpret_cast<const f4*>(p + step + t * 256);
+      }
+      Parts<NP> sp;
+      split_d<NP>(sp, S[2 * x], S[2 * x + 1]);
+      const char* blk = ring(x) + lane * 16;
+#pragma unroll
+      for (int t = 0; t < DT; t += 4) {
+        Parts<NP> fp[4];
+#pragma unroll
+        for (int m = 0; m < NP; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) fp[i].p[m] = *reinterpret_cast<const bh8*>(blk + (m * DT + t + i) * 1024);
+        mmp<NP>(*reinterpret_cast<f4(*)[4]>(&E[t]), fp, sp);
+      }
+    }
+    dec = dnext;
+#pragma unroll
+    for (int t = 0; t < DT; ++t) {
+      S[t] = E[t];
+      E[t] = next[t];
+      *reinterpret_cast<f4*>(p + t * 256) = S[t];
+    }
+  }
+}
+
+}  // namespace
+}  // namespace m3

@@ -272,7 +272,7 @@ struct GradTiles {
 __device__ __forceinline__ constexpr int tile_i(int n) { return n < 4 ? n >> 1 : 2 + ((n - 4) >> 2); }
 __device__ __forceinline__ constexpr int tile_j(int n) { return n < 4 ? n & 1 : (n - 4) & 3; }
 
-template <typename T, int DK, bool MULTI>
+template <typename T, int DK, int DV, bool MULTI>
 __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(DeltaArgs a) {
   using X = Rows64<DK>;
   using M = Rows64<64>;
@@ -291,11 +291,12 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
   if (sl.n <= 0) return;
   const typename X::Lane xl(lane);
   const M::Lane ml(lane);
-  const int ldo = a.Hv * a.Dv;
+  const int ldo = a.Hv * DV;
   char *sO = smem, *sR = smem + NI * M::PLANE, *sUt = sR + NO * M::PLANE;
   char *sK = smem, *sQ = smem + NI * X::PLANE, *sF = smem + 2 * NI * X::PLANE, *sN = sF + NO * M::PLANE;
+  const int wcol = X::tile_col(w, lane);   // the wave's channels in K and Q
   const int dkr = 32 * (w >> 1) + 8 * (r >> 2) + 4 * (w & 1) + (r & 3);   // the lane's channel of q and k
-  const int64_t dd = static_cast<int64_t>(DK) * a.Dv;
+  const int64_t dd = static_cast<int64_t>(DK) * DV;
   f4 dq[4], dk[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) dq[i] = dk[i] = f4{0, 0, 0, 0};
@@ -306,7 +307,7 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
     const int64_t m = static_cast<int64_t>(slot) * a.Hv + h;
     const float* S0 = a.cstates + m * a.ldpm;
     const float* dS = a.after + m * dd;
-    const uint32_t sat = static_cast<uint32_t>(dkr * a.Dv + 8 * g);
+    const uint32_t sat = static_cast<uint32_t>(dkr * DV + 8 * g);
     f4 x1[4], x2[4], x3[4], dp[NTILE], da[NTILE];
 #pragma unroll
     for (int i = 0; i < 4; ++i) x1[i] = x2[i] = x3[i] = f4{0, 0, 0, 0};
@@ -320,25 +321,24 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
     Stage<float, 64, NT> sr, su;
     Vec8<float> vs[2], vd[2];
     auto fetch = [&](int c0) __attribute__((always_inline)) {
-      so.load(static_cast<const T*>(a.dout) + sl.row0 * ldo + h * a.Dv + c0, ldo, sl.n, tid);
-      sv.load(static_cast<const T*>(a.v) + sl.row0 * a.ldv + h * a.Dv + c0, a.ldv, sl.n, tid);
-      sr.load(a.dr + m * 64 * a.Dv + c0, a.Dv, 64, tid);
-      su.load(S0 + dd + c0, a.Dv, 64, tid);
+      so.load(static_cast<const T*>(a.dout) + sl.row0 * ldo + h * DV + c0, ldo, sl.n, tid);
+      sv.load(static_cast<const T*>(a.v) + sl.row0 * a.ldv + h * DV + c0, a.ldv, sl.n, tid);
+      sr.load(a.dr + m * 64 * DV + c0, DV, 64, tid);
+      su.load(S0 + dd + c0, DV, 64, tid);
     };
-    auto fetch_s = [&](int c0) __attribute__((always_inline)) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        vs[x].load(S0 + c0 + 32 * x + sat);
-        vd[x].load(dS + c0 + 32 * x + sat);
-      }
+    auto fetch_s = [&](int c0, int x) __attribute__((always_inline)) {
+      vs[x].load(S0 + c0 + 32 * x + sat);
+      vd[x].load(dS + c0 + 32 * x + sat);
     };
     fetch(0);
-    fetch_s(0);
+    fetch_s(0, 0);
+    fetch_s(0, 1);
     Stage<T, DK, NT> stK, stQ;
     __syncthreads();
     for (int i = threadIdx.x; i < kDeltaGates; i += NT) sGate[i] = (a.pm + m * a.ldpm + kDeltaMatrix)[i];
     if (threadIdx.x < 256) sE[threadIdx.x / 64][threadIdx.x % 64] = 0.0f;
-    for (int c0 = 0; c0 < a.Dv; c0 += 64) {
+#pragma unroll
+    for (int c0 = 0; c0 < DV; c0 += 64) {
       if (c0 > 0) tiles_barrier();
       so.store(sO, tid);
 #pragma unroll
@@ -353,7 +353,7 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
         su.v[n].get(f);
         M::put<NO>(sUt, row, c, f);
       }
-      if (c0 + 64 < a.Dv) {
+      if (c0 + 64 < DV) {
         fetch(c0 + 64);
       } else {
         stK.load(static_cast<const T*>(a.k) + sl.row0 * a.ldk + hk * DK, a.ldk, sl.n, tid);
@@ -371,6 +371,7 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
           for (int j = 0; j < 8; ++j) both = fmaf(f[j], d[j], both);
           split8<NO>(ps, f);
           split8<NO>(pd, d);
+          if (c0 + 64 < DV) fetch_s(c0 + 64, x);
         }
         {
           Parts<NI> oa[4];
@@ -405,7 +406,6 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (c0 + 64 < a.Dv) fetch_s(c0 + 64);
     }
 #pragma unroll
     for (int n = 0; n < VN; ++n) {
@@ -471,7 +471,7 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
     }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const Parts<NI> kb = X::template by_col<NI>(sK, xl, w, x), qb = X::template by_col<NI>(sQ, xl, w, x);
+      const Parts<NI> kb = X::template by_col<NI>(sK, wcol, x), qb = X::template by_col<NI>(sQ, wcol, x);
       Parts<NO> f[4];
       // columns of block x and rows of its and later blocks; by_col: of the
       // transpose's rows, which are its columns
@@ -596,8 +596,13 @@ hipError_t run_backward(const DeltaArgs& a, hipStream_t s) {
     e = run_back_chain<T, DK, 4>(a, s);
   if (e != hipSuccess) return e;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.nslot) * a.Hk);
-  if (a.Hv == a.Hk) k_delta_grads<T, DK, false><<<grid, 4 * DK, 0, s>>>(a);
-  else k_delta_grads<T, DK, true><<<grid, 4 * DK, 0, s>>>(a);
+  if (a.Dv == 64) {
+    if (a.Hv == a.Hk) k_delta_grads<T, DK, 64, false><<<grid, 4 * DK, 0, s>>>(a);
+    else k_delta_grads<T, DK, 64, true><<<grid, 4 * DK, 0, s>>>(a);
+  } else {
+    if (a.Hv == a.Hk) k_delta_grads<T, DK, 128, false><<<grid, 4 * DK, 0, s>>>(a);
+    else k_delta_grads<T, DK, 128, true><<<grid, 4 * DK, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 

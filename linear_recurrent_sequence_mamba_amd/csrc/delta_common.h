@@ -135,6 +135,23 @@ struct Rows64 {
     for (int n = 0; n < NP; ++n) f.p[n] = *reinterpret_cast<const bh8*>(a + n * PLANE);
     return f;
   }
+  // a lane's address for one tile of columns whose number is not a constant
+  static __device__ __forceinline__ int tile_col(int i, int lane) {
+    const int u = (lane & 15) >> 2, v = lane & 3, g = lane >> 4;
+    return (8 * g + u) * RB + (((i >> 1) ^ turn(u)) << 6) + ((v ^ (g & 2 ? 3 : 0)) << 4) + 8 * (i & 1);
+  }
+  template <int NP>
+  static __device__ __forceinline__ Parts<NP> by_col(const char* lds, int tile_col, int x) {
+    const char* a = lds + tile_col + 32 * x * RB;
+    Parts<NP> f;
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+      const s4v y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((M3_LDS s4v*)(a + n * PLANE));
+      const s4v z = __builtin_amdgcn_ds_read_tr16_b64_v4i16((M3_LDS s4v*)(a + n * PLANE + 4 * RB));
+      f.p[n] = __builtin_bit_cast(bh8, __builtin_shufflevector(y, z, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    return f;
+  }
   // columns of tile i, k = rows 32 x .. (transposing reads: sixteen lanes point
   // at four rows of sixteen elements, four each, and lane i receives column i)
   template <int NP>

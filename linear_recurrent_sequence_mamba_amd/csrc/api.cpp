@@ -296,12 +296,10 @@ m3_status check_delta(const m3_delta_dims* d, bool scan, bool packed) {
   for (const auto& l : lds)
     if (l[0] != 0 && (l[0] < l[1] || l[0] >= most)) return M3_ERR_SHAPE;
   if ((d->ld_q | d->ld_k | d->ld_v) % 8) return M3_ERR_ALIGN;
-  // a workgroup for each chunk and head, for each sequence, head and 16 columns
-  if (!grid_fits(static_cast<int64_t>(d->batch) * d->nheads_v * (d->headdim_v / 16), 256)) return M3_ERR_SHAPE;
-  if (scan) {
-    const int64_t slots = m3::delta_slots(d->batch, d->seqlen, packed);
-    if (slots > 0x7fffffff || !grid_fits(slots * d->nheads_v, 256)) return M3_ERR_SHAPE;
-  }
+  // the step: 4 Dv threads for a sequence's head.  The scan: at most 4 (Dk + Dv)
+  // for each chunk and head
+  const int64_t slots = scan ? m3::delta_slots(d->batch, d->seqlen, packed) : d->batch;
+  if (slots > 0x7fffffff || !grid_fits(slots * d->nheads_v, scan ? 1024 : 512)) return M3_ERR_SHAPE;
   return M3_OK;
 }
 

@@ -72,7 +72,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
     for (int t = 0; t < DT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) S[t][e] = tile_row(t, e) + 8 * g == col ? 1.0f : 0.0f;
-  } else if (FULL && seg.j > 0) {
+  } else if (FULL && (seg.j > 0 || (a.h0 && !seg.last))) {
 #pragma unroll
     for (int t = 0; t < DT; ++t) S[t] = *reinterpret_cast<const f4*>(a.ends + shead * dd + end_at + t * 256);
   } else if (a.h0 && seg.j == 0) {
@@ -80,6 +80,9 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
     for (int t = 0; t < DT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) S[t][e] = (a.h0 + head * dd + tile_row(t, e) * a.Dv)[at];
+    if constexpr (MODE == kEnds)   // (hT may be h0, and is written while the first segment runs)
+#pragma unroll
+      for (int t = 0; t < DT; ++t) *reinterpret_cast<f4*>(a.ends + shead * dd + end_at + t * 256) = S[t];
   }
 
   Tiles st;
@@ -301,8 +304,9 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
 // The states before the segments: S_{j+1} = E_j + d_j S_j + F_j S_j, with the
 // decay d_j apart from the map.  E_j lies where S_{j+1} goes; S_1 is there
 // already.  BACK: the gradients of the states behind them, from the last to the
-// first, with the maps' transposes.  A wave has 16 columns of a sequence's head.  F arrives in blocks of
-// 32 columns which lie as the operands do, through a ring of blocks in LDS.
+// first, with the maps' transposes.  A wave has 16 columns of a sequence's head.
+// F arrives in blocks of 32 columns which lie as the operands do, through a ring
+// of blocks in LDS.
 template <int DK, int NP, bool BACK>
 __global__ __launch_bounds__(64) void k_delta_join(DeltaArgs a) {
   constexpr int KS = DK / 32, DT = DK / 16, NF = NP * DT;   // NF: operands of a block

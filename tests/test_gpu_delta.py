@@ -118,6 +118,93 @@ def test_dense_equals_packed(dtype):
         assert torch.equal(dd[n].reshape(d[n].shape), d[n]), n
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(1, 2, 64, 64, 300), (2, 2, 128, 128, 200), (1, 3, 128, 64, 700), (2, 4, 64, 128, 129),
+                                   (1, 1, 64, 64, 2100)])
+def test_as_near_as_the_recurrence_in_32_bits(shape, dtype):
+    """The error (a norm) against that of the recurrence token by token in fp32.
+
+    Of a product of sums of three parts the terms from 2^-24 on are left out, three of them, where a product in
+    fp32 is off by half of 2^-24 at most: 6 times as much.  With the chunk's inverse and 1.3 for its norm: 8.  In
+    bf16 a result is rounded once more, U, and P, U and what reaches the gradients of q and k have two parts,
+    2^-16 of a product each, of at most six products that they pass through.  dg is a sum over the rows behind it
+    in the chunk of differences of q.dq, k.dk and v.dv, which are each off as dq, dk and dv are before their
+    rounding."""
+    hk, hv, dk, dv, L = shape
+    q, k, v, g, b, h0, do, dhT = _inputs(L, hk, hv, dk, dv, dtype, 40 + L, False, 1)
+    scale = dk ** -0.5
+    cu = torch.tensor([0, L], dtype=torch.int32).cuda()
+    o, hT, st = m3.delta_scan(q, k, v, g, b, h0=h0, cu_seqlens=cu, want_states=True)
+    d = m3.delta_scan_backward(q, k, v, g, b, do, st, h0=h0, dhT=dhT, cu_seqlens=cu)
+    got = [o, hT[0]] + [d[n] for n in ("q", "k", "v", "g", "beta")] + [d["h0"][0]]
+
+    def plain(t):
+        ins = [x.cpu().to(t).requires_grad_(True) for x in (q, k, v, g, b, h0[0])]
+        y, hs, _ = delta_ref.scan(*ins, scale)
+        loss = (y * do.cpu().to(t)).sum() + (hs[-1] * dhT[0].cpu().to(t)).sum()
+        return [y.detach(), hs[-1].detach()] + list(torch.autograd.grad(loss, ins))
+
+    want, near = plain(torch.float64), plain(F32)
+    names = ("o", "hT", "dq", "dk", "dv", "dg", "dbeta", "dh0")
+    size = lambda t: ref.f64(t).flatten(1).norm(dim=1)
+    rows = size(q) * size(want[2]) + size(k) * size(want[3]) + 2 * size(v) * size(want[4])
+    behind = torch.stack([rows[t:t // 64 * 64 + 64].pow(2).sum() for t in range(L)]).sqrt().norm()
+    for n, x, w, p in zip(names, got, want, near):
+        whole = float(w.norm())
+        tol = 8 * float((p.double() - w).norm()) + (0 if n in ("hT", "dh0") else ref.U[dtype] * whole)
+        if dtype == BF16 and n not in ("hT", "dh0", "dv"):
+            tol += 6 * 2.0 ** -16 * (whole if n != "dg" else float(behind))
+        if n == "dg":
+            tol += 8 * 2.0 ** -24 * float(behind)
+        e = float((ref.f64(x) - w).norm())
+        say(f"  {n}: {e / whole:.1e}, in 32 bits {float((p.double() - w).norm()) / whole:.1e}, {e / tol:.2f} of its bound")
+        assert e <= tol, (n, e, tol)
+
+
+def test_the_state_goes_on_in_place():
+    """hT may be h0, also where a sequence is cut into segments, which run at once."""
+    import ctypes
+    lib = m3.library()
+    for B, T, hk, hv, dk, dv, lengths in ((2, 4096, 1, 1, 64, 64, None), (3, 4300, 1, 2, 128, 128, [4000, 0, 300])):
+        rows = T if lengths else B * T
+        q, k, v, g, b, h0, _, _ = _inputs(rows, hk, hv, dk, dv, BF16, 50, False, B)
+        g = (g.float() * 0.02).to(BF16)   # what is at the start is still there at the end
+        cu = torch.tensor([0, 4000, 4000, 4300], dtype=torch.int32).cuda() if lengths else None
+        f = (lambda t: t) if lengths else (lambda t: t.unflatten(0, (B, T)))
+        o, hT, _ = m3.delta_scan(*(f(t) for t in (q, k, v, g, b)), h0=h0, cu_seqlens=cu)
+        dims = m3.m3_delta_dims(B, T, hk, hv, dk, dv, m3.M3_BF16, dk ** -0.5, 0, 0, 0, 0, 0)
+        p = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())
+        ws = torch.empty(lib.m3_delta_scan_workspace_size(ctypes.byref(dims), int(cu is not None)), dtype=torch.uint8,
+                         device="cuda")
+        y, h = torch.empty_like(v), h0.clone()
+        s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        for n in range(3):
+            h.copy_(h0)
+            assert lib.m3_delta_scan(ctypes.byref(dims), p(cu), p(q), p(k), p(v), p(g), p(b), p(h), p(y), p(h), None,
+                                     p(ws), ws.numel(), s) == 0
+            torch.cuda.synchronize()
+            assert torch.equal(h, hT) and torch.equal(y, o.reshape(y.shape)), (B, n)
+        assert not torch.equal(hT, m3.delta_scan(*(f(t) for t in (q, k, v, g, b)), cu_seqlens=cu)[1])
+
+
+@pytest.mark.parametrize("shape", [(2, 2100, 1, 1, 64, 128), (1, 3000, 1, 2, 128, 128)])
+def test_dense_prompts_in_segments(shape):
+    B, T, hk, hv, dk, dv = shape
+    for dtype in (F32, BF16):
+        q, k, v, g, b, h0, do, dhT = _inputs(B * T, hk, hv, dk, dv, dtype, 60, True, B)
+        g = (g.float() * 0.05).to(dtype)
+        f = lambda t: t.unflatten(0, (B, T))
+        o, hT, st = m3.delta_scan(f(q), f(k), f(v), f(g), f(b), h0=h0, want_states=True)
+        d = m3.delta_scan_backward(f(q), f(k), f(v), f(g), f(b), f(do), st, h0=h0, dhT=dhT)
+        for s in range(B):
+            c = slice(s * T, (s + 1) * T)
+            want = delta_ref.check(q[c], k[c], v[c], g[c], b[c], h0[s], dk ** -0.5, dtype, do[c], dhT[s])
+            got = {"o": o[s], "hT": hT[s], "dq": d["q"][s], "dk": d["k"][s], "dv": d["v"][s], "dg": d["g"][s],
+                   "dbeta": d["beta"][s], "dh0": d["h0"][s]}
+            for n, (val, bound) in want.items():
+                _check(n, got[n], val, bound)
+
+
 def test_strong_gates():
     """Decays of 0 (-inf and far below), no decay, no write, and writes of twice the miss."""
     L, hk, hv, dk, dv = 140, 1, 2, 64, 64

@@ -10,11 +10,13 @@
 //   dQ = scale exp(G) X1 + F K
 //   dK = F^T Q + (M + M^T) K - exp(G) beta X2 + exp(G_end - G) X3
 //   dbeta_i = dR_i.Y_i + sum_j dA_ij Gamma_ij k_i.k_j,   Y = V - exp(G) K S0
-// for each chunk by itself.  dR_i.Y_i is dR_i.v_i - exp(G_i) k_i.X2_i.  The
-// gradient through every exp(G) of a row adds up to
-//   dG_i = q_i.dq_i - k_i.dk_i + 2 (dR_i.U_i - dV_i.v_i),
-// to which the chunk's last row adds <S1, dS1> = sum_j exp(G_end - G_j) k_j.X3_j
-// + exp(G_end) <S0, dS1>; and dg_t = sum_{i >= t} dG_i.
+// for each chunk by itself.  dR_i.Y_i is dR_i.v_i - exp(G_i) k_i.X2_i.  With
+// C_ij = F_ij q_i.k_j + M_ij k_i.k_j (j < i) and z_j = exp(G_end - G_j) k_j.X3_j
+//   dG_i = sum_j C_ij - sum_j C_ji + scale exp(G_i) q_i.X1_i - exp(G_i) beta_i k_i.X2_i - z_i,
+// to which the chunk's last row adds sum_j z_j + exp(G_end) <S0, dS1>; and dg_t =
+// sum_{i >= t} dG_i.  (dG_i is also q_i.dq_i - k_i.dk_i + 2 (dR_i.U_i - dV_i.v_i),
+// but there the pairs of rows behind t, which are in dg_t twice with opposite
+// signs, come from sums that are rounded apart: 2 to 5 times the error in fp32.)
 #include "delta_chain.h"
 
 namespace m3 {
@@ -283,7 +285,7 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
   __shared__ float sAcc[PARK ? 32 : 1][PARK ? NT : 1];
   __shared__ __align__(16) char smem[G::BYTES];
   __shared__ __align__(16) float sGate[kDeltaGates];
-  __shared__ float sRow[2][NW][64], sE[4][64], sU[64], sV[64], sEnd[NW];
+  __shared__ float sRow[2][NW][64], sE[4][64], sW[4][64], sC[4][64], sV[64], sEnd[NW];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g0 = lane >> 4;
   const int hk = blockIdx.x % a.Hk, slot = blockIdx.x / a.Hk, group = MULTI ? a.Hv / a.Hk : 1;
@@ -336,7 +338,10 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
     Stage<T, DK, NT> stK, stQ;
     __syncthreads();
     for (int i = threadIdx.x; i < kDeltaGates; i += NT) sGate[i] = (a.pm + m * a.ldpm + kDeltaMatrix)[i];
-    if (threadIdx.x < 256) sE[threadIdx.x / 64][threadIdx.x % 64] = 0.0f;
+    if (threadIdx.x < 256) {
+      const int n = threadIdx.x / 64, i = threadIdx.x % 64;
+      sE[n][i] = sW[n][i] = sC[n][i] = 0.0f;
+    }
 #pragma unroll
     for (int c0 = 0; c0 < DV; c0 += 64) {
       if (c0 > 0) tiles_barrier();
@@ -423,24 +428,36 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
       if (t < 12) {
         const int ti = tile_i(t), tj = tile_j(t), j = tile_row(tj, 0) + 8 * (r >> 2) + (r & 3);
         const int i0 = tile_row(ti, 0) + 8 * g;
-        f4 kk = f4{0, 0, 0, 0};
+        f4 kk = f4{0, 0, 0, 0}, qk = f4{0, 0, 0, 0};
 #pragma unroll
-        for (int x = 0; x < DK / 32; ++x)
-          kk = mmp<3>(X::template by_row<NI>(sK, xl, ti, x), X::template by_row<NI>(sK, xl, tj, x), kk);
+        for (int x = 0; x < DK / 32; ++x) {
+          const Parts<NI> kb = X::template by_row<NI>(sK, xl, tj, x);
+          kk = mmp<3>(X::template by_row<NI>(sK, xl, ti, x), kb, kk);
+          qk = mmp<3>(X::template by_row<NI>(sQ, xl, ti, x), kb, qk);
+        }
         const float gh = sGate[192 + j], gl = sGate[256 + j];
         const f4 hi = *reinterpret_cast<const f4*>(&sGate[192 + i0]), lo = *reinterpret_cast<const f4*>(&sGate[256 + i0]);
         const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + i0]);
+        float col = 0.0f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float gam = i0 + e >= j ? __builtin_amdgcn_exp2f((hi[e] - gh) + (lo[e] - gl)) : 0.0f;
-          if (i0 + e == j) sU[j] = da[n][e];
           // (a product that is not finite stays out of the half that is not there)
-          const float ag = i0 + e > j ? -da[n][e] * gam : 0.0f;
-          const float es = group_sum<16>(ag == 0.0f ? 0.0f : ag * kk[e]);
-          if (r == 0) sE[tj][i0 + e] = es;
+          const float ag = i0 + e > j ? -da[n][e] * gam : 0.0f, ak = ag == 0.0f ? 0.0f : ag * kk[e];
           dp[n][e] = i0 + e >= j ? a.scale * dp[n][e] * gam : 0.0f;
           da[n][e] = bt[e] * ag;
+          // (the diagonal does not depend on G)
+          const float c = fmaf(bt[e], ak, i0 + e == j || dp[n][e] == 0.0f ? 0.0f : dp[n][e] * qk[e]);
+          col += c;
+          const float es = group_sum<16>(ak), cs = group_sum<16>(c);
+          if (r == 0) {
+            sE[tj][i0 + e] = es;
+            sW[tj][i0 + e] = cs;
+          }
         }
+        col += __shfl_xor(col, 16, 64);
+        col += __shfl_xor(col, 32, 64);
+        if (g == 0) sC[ti][j] = col;
         Parts<NO> pf;
         split_d<NO>(pf, dp[n], da[n]);
         char* to = smem + 2 * NI * X::PLANE + M::at(j, i0 & ~7) + 2 * (i0 & 7);
@@ -454,7 +471,7 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
     }
     tiles_barrier();
     // dQ = scale exp(G) X1 + F K,  dK = F^T Q + (M + M^T) K - exp(G) beta X2 + exp(G_end - G) X3
-    float rx[16], re = 0.0f;
+    float re = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f4 st = *reinterpret_cast<const f4*>(&sGate[tile_row(i, 0) + 8 * g]);
@@ -462,11 +479,17 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
       const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + tile_row(i, 0) + 8 * g]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float k = X::template get<NI>(sK, tile_row(i, e) + 8 * g, dkr), x = x3[i][e] * en[e];
+        const int row = tile_row(i, e) + 8 * g;
+        const float k = X::template get<NI>(sK, row, dkr), q = X::template get<NI>(sQ, row, dkr);
+        const float x = x3[i][e] * en[e], y = st[e] * bt[e] * x2[i][e];
         x1[i][e] *= a.scale * st[e];
-        rx[4 * i + e] = k * x2[i][e];
+        const float d = group_sum<16>(fmaf(q, x1[i][e], -k * (x + y))), kx = group_sum<16>(k * x2[i][e]);
+        if (r == 0) {
+          sRow[0][w][row] = d;
+          sRow[1][w][row] = kx;
+        }
         re = fmaf(k, x, re);
-        x2[i][e] = fmaf(-st[e] * bt[e], x2[i][e], x);
+        x2[i][e] = x - y;
       }
     }
 #pragma unroll
@@ -509,16 +532,6 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
         dq[i] += x1[i];
         dk[i] += x2[i];
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = tile_row(i, e) + 8 * g;
-        const float d = group_sum<16>(fmaf(X::template get<NI>(sQ, row, dkr), x1[i][e], -X::template get<NI>(sK, row, dkr) * x2[i][e]));
-        const float x = group_sum<16>(rx[4 * i + e]);
-        if (r == 0) {
-          sRow[0][w][row] = d;
-          sRow[1][w][row] = x;
-        }
-      }
     }
     re = group_sum<64>(re);
     if (lane == 0) sEnd[w] = fmaf(sGate[63], both, re);
@@ -531,9 +544,10 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
         x += sRow[1][n][lane];
         end += sEnd[n];
       }
-      const float bt = sGate[128 + lane], rv = sV[lane];
-      const float db = rv - sGate[lane] * x + (sE[0][lane] + sE[1][lane]) + (sE[2][lane] + sE[3][lane]);
-      float dG = d + 2.0f * (sU[lane] - bt * rv);
+      const float db = sV[lane] - sGate[lane] * x + (sE[0][lane] + sE[1][lane]) + (sE[2][lane] + sE[3][lane]);
+      float dG = d;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) dG += sW[n][lane] - sC[n][lane];
       if (lane == 63) dG += end;
       // sums of the rows from here on
 #pragma unroll

@@ -278,7 +278,7 @@ hipError_t run_chain(const DeltaArgs& a, bool split, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_delta_join<DK, DeltaParts<T>::OUT, false>
-        <<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hv * (a.Dv / 16)), 64, 0, s>>>(a);
+        <<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hv * (a.Dv / 16)), 2 * DK, 0, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -324,7 +324,7 @@ int64_t delta_slots(int B, int T, bool packed) {
 // longest of a packed batch is not known here; twice the mean is what uniform
 // lengths give.  Segments cost their chunks twice, without outputs 3/4, for as
 // many columns as the values and a state have together, and what joins them
-// 0.45 for each.  They are taken where that is less than 3/4 (in a training step
+// 0.2 for each.  They are taken where that is less than 3/4 (in a training step
 // both are held by memory before that).  16384 tokens of 16 heads of 128: 2.3 ms
 // whole, in 32 segments of 8 chunks 330 us with the rest, 16 of 16 270, 8 of 32
 // 310.
@@ -337,7 +337,7 @@ DeltaPlan delta_plan(int B, int T, int Hv, int Dk, int Dv, bool packed, bool bac
   for (int l = 3; l < 10 && longest / (1 << l) >= 2; ++l) {
     const double n = rows / (kDeltaChunk << l) + (packed ? B : 0);
     const double cost = (1 << l) * ((back ? 1.0 : 0.75) * rounds(n * cols * (1.0 + static_cast<double>(Dk) / Dv)) + rounds(n * cols)) +
-                        0.45 * longest / (1 << l);
+                        0.2 * longest / (1 << l);
     if (cost < best) {
       best = cost;
       p = DeltaPlan{l, 0, true};

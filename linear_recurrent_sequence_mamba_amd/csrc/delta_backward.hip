@@ -593,7 +593,7 @@ hipError_t run_back_chain(const DeltaArgs& a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_delta_join<DK, DeltaParts<T>::OUT, true>
-        <<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hv * (a.Dv / 16)), 64, 0, s>>>(a);
+        <<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hv * (a.Dv / 16)), 2 * DK, 0, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

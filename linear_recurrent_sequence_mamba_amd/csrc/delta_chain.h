@@ -304,21 +304,18 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
 // The states before the segments: S_{j+1} = E_j + d_j S_j + F_j S_j, with the
 // decay d_j apart from the map.  E_j lies where S_{j+1} goes; S_1 is there
 // already.  BACK: the gradients of the states behind them, from the last to the
-// first, with the maps' transposes.  A wave has 16 columns of a sequence's head.
-// F arrives in blocks of 32 columns which lie as the operands do, through a ring
-// of blocks in LDS.
+// first, with the maps' transposes.  A workgroup has 16 columns of a sequence's
+// head, a wave 32 rows of them; the rows of the next two maps are on their way
+// in its registers, and the waves exchange the parts of the state in LDS.
 template <int DK, int NP, bool BACK>
-__global__ __launch_bounds__(64) void k_delta_join(DeltaArgs a) {
-  constexpr int KS = DK / 32, DT = DK / 16, NF = NP * DT;   // NF: operands of a block
-  // each by its name, so that reads of one do not wait for the others' loads
-  __shared__ __align__(16) char r0[NF * 1024], r1[NF * 1024], r2[KS > 2 ? NF * 1024 : 16], r3[KS > 2 ? NF * 1024 : 16];
-  auto ring = [&](int x) __attribute__((always_inline)) { return x == 0 ? r0 : x == 1 ? r1 : x == 2 ? r2 : r3; };
-  const int lane = threadIdx.x;
-  const int nsl = a.Dv / 16;
-  int b = blockIdx.x;
-  const int slice = b % nsl;
-  b /= nsl;
-  const int h = b % a.Hv, s = b / a.Hv;
+__global__ __launch_bounds__(2 * DK, 1) void k_delta_join(DeltaArgs a) {
+  constexpr int KS = DK / 32, DT = DK / 16;
+  __shared__ bh8 sS[2][KS][NP][64];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // (a head's workgroups on one XCD where the heads are a multiple of 8, as they
+  // read the same maps)
+  const uint32_t heads = static_cast<uint32_t>(a.B) * a.Hv, b = blockIdx.x % heads;
+  const int slice = blockIdx.x / heads, h = b % a.Hv, s = b / a.Hv;
   int len, slot0;
   if (a.cu) {
     const int c = clamp_row(a.cu[s], a.T);
@@ -328,71 +325,79 @@ __global__ __launch_bounds__(64) void k_delta_join(DeltaArgs a) {
     len = a.T;
     slot0 = s * (a.nseg / a.B);
   }
-  const int nseg = (((len + kDeltaChunk - 1) / kDeltaChunk) + (1 << a.lseg) - 1) >> a.lseg;
-  if (nseg <= 2) return;
+  const int nmap = ((((len + kDeltaChunk - 1) / kDeltaChunk) + (1 << a.lseg) - 1) >> a.lseg) - 2;
+  if (nmap <= 0) return;
   const int64_t next_seg = BACK ? -a.Hv : a.Hv;
-  const int64_t shead = static_cast<int64_t>(slot0 + (BACK ? nseg - 2 : 1)) * a.Hv + h, step = next_seg * DK * a.Dv;
-  float* p = a.ends + shead * DK * a.Dv + (slice * DT * 64 + lane) * 4;
-  const uint16_t* f = a.maps + shead * NP * DK * DK + lane * 8;
+  const int64_t shead = static_cast<int64_t>(slot0 + (BACK ? nmap : 1)) * a.Hv + h, step = next_seg * DK * a.Dv;
+  float* p = a.ends + shead * DK * a.Dv + ((slice * DT + 2 * w) * 64 + lane) * 4;
+  const uint16_t* f = a.maps + shead * NP * DK * DK + (2 * w * KS * 64 + lane) * 8;
   const float* d = a.decays + shead;
-  // block x of segment j's map
-  auto fetch = [&](int j, int x) __attribute__((always_inline)) {
-    const uint16_t* from = f + (j - 1) * next_seg * NP * DK * DK + x * 512;
+  struct Map {
+    Parts<NP> f[2][KS];
+    f4 e[2];
+    float d;
+  } map[2];
+  auto fetch = [&](Map& m, int j) __attribute__((always_inline)) {   // (behind the last one the last again, unused)
+    j = min(j, nmap - 1);
+    const uint16_t* from = f + j * next_seg * NP * DK * DK;
 #pragma unroll
-    for (int i = 0; i < NF; ++i)
-      __builtin_amdgcn_global_load_lds((const M3_GLB void*)(from + i * KS * 512), (M3_LDS void*)(ring(x) + i * 1024), 16, 0, 0);
+    for (int t = 0; t < 2; ++t) {
+      m.e[t] = *reinterpret_cast<const f4*>(p + (j + 1) * step + t * 256);
+#pragma unroll
+      for (int x = 0; x < KS; ++x)
+#pragma unroll
+        for (int n = 0; n < NP; ++n) m.f[t][x].p[n] = *reinterpret_cast<const bh8*>(from + ((n * DT + t) * KS + x) * 512);
+    }
+    m.d = d[j * next_seg];
   };
-  f4 S[DT], E[DT], next[DT];
-  float dec = d[0], dnext = 0.0f;
+  f4 S[2];
 #pragma unroll
-  for (int t = 0; t < DT; ++t) {
-    S[t] = *reinterpret_cast<const f4*>(p + t * 256);
-    E[t] = *reinterpret_cast<const f4*>(p + step + t * 256);
-    next[t] = f4{0, 0, 0, 0};
-  }
+  for (int t = 0; t < 2; ++t) S[t] = *reinterpret_cast<const f4*>(p + t * 256);
+  fetch(map[0], 0);
+  fetch(map[1], 1);
+  // (the state is waited for here: in the loop its wait would be one for all that
+  // is on its way, in every turn)
+  asm volatile("" : "+v"(S[0]), "+v"(S[1]));
+  for (int j0 = 0; j0 < nmap; j0 += 2)
 #pragma unroll
-  for (int x = 0; x < KS - 1; ++x) fetch(1, x);
-  for (int j = 1; j + 1 < nseg; ++j) {
-    p += step;
-    const bool more = j + 2 < nseg;
+    for (int q = 0; q < 2; ++q) {
+      const int j = j0 + q;
+      if (j >= nmap) break;
+      Map& m = map[q];
+      Parts<NP> sp[KS];
+      split_d<NP>(sp[0], S[0], S[1]);
 #pragma unroll
-    for (int t = 0; t < DT; ++t)
+      for (int n = 0; n < NP; ++n) sS[q][w][n][lane] = sp[0].p[n];
+      tiles_barrier();
 #pragma unroll
-      for (int e = 0; e < 4; ++e) E[t][e] = fmaf(dec, S[t][e], E[t][e]);
+      for (int x = 0; x < KS; ++x)
 #pragma unroll
-    for (int x = 0; x < KS; ++x) {
-      // this block is there; the KS - 2 behind it may be on their way
-      if (x == 0 || more) __builtin_amdgcn_s_waitcnt(0x0f70 | ((KS - 2) * NF & 15) | ((KS - 2) * NF >> 4 << 14));
-      else lds_loads_done();
-      lds_reads_done();
-      if (x == 0) fetch(j, KS - 1);
-      else if (more) fetch(j + 1, x - 1);
-      if (x == 1 && more) {   // the next E_j
-        dnext = d[j * next_seg];
+        for (int n = 0; n < NP; ++n) sp[x].p[n] = sS[q][x][n][lane];
+      f4 c[4];   // (four sums, not to wait for each product)
 #pragma unroll
-        for (int t = 0; t < DT; ++t) next[t] = *reinterpret_cast<const f4*>(p + step + t * 256);
+      for (int t = 0; t < 2; ++t) {
+        c[2 + t] = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[t][e] = fmaf(m.d, S[t][e], m.e[t][e]);
       }
-      Parts<NP> sp;
-      split_d<NP>(sp, S[2 * x], S[2 * x + 1]);
-      const char* blk = ring(x) + lane * 16;
 #pragma unroll
-      for (int t = 0; t < DT; t += 4) {
-        Parts<NP> fp[4];
+      for (int x = 0; x < KS; x += 2)
 #pragma unroll
-        for (int m = 0; m < NP; ++m)
+        for (int i = 0; i < NP; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) fp[i].p[m] = *reinterpret_cast<const bh8*>(blk + (m * DT + t + i) * 1024);
-        mmp<NP>(*reinterpret_cast<f4(*)[4]>(&E[t]), fp, sp);
+          for (int k = 0; i + k < NP; ++k)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+                c[2 * y + t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(m.f[t][x + y].p[i], sp[x + y].p[k], c[2 * y + t], 0, 0, 0);
+      fetch(m, j + 2);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        S[t] = c[t] + c[2 + t];
+        *reinterpret_cast<f4*>(p + (j + 1) * step + t * 256) = S[t];
       }
     }
-    dec = dnext;
-#pragma unroll
-    for (int t = 0; t < DT; ++t) {
-      S[t] = E[t];
-      E[t] = next[t];
-      *reinterpret_cast<f4*>(p + t * 256) = S[t];
-    }
-  }
 }
 
 }  // namespace

@@ -325,9 +325,9 @@ int64_t delta_slots(int B, int T, bool packed) {
 // lengths give.  Segments cost their chunks twice, without outputs 3/4, for as
 // many columns as the values and a state have together, and what joins them
 // 0.2 for each.  They are taken where that is less than 3/4 (in a training step
-// both are held by memory before that).  16384 tokens of 16 heads of 128: 2.3 ms
-// whole, in 32 segments of 8 chunks 330 us with the rest, 16 of 16 270, 8 of 32
-// 310.
+// both are held by memory before that).  16384 tokens of 16 heads of 128: 1.43 ms
+// whole, in 32 segments of 8 chunks 380 us with the rest, 16 of 16 346, 8 of 32
+// 412.
 DeltaPlan delta_plan(int B, int T, int Hv, int Dk, int Dv, bool packed, bool back) {
   const double rows = packed ? T : static_cast<double>(B) * T;
   const double longest = (packed && B > 1 ? 2.0 * T / B : T) / kDeltaChunk, cols = Hv * (Dv / 16.0);

@@ -12,7 +12,12 @@
 //   O = scale (exp(G) Q S0 + P U),          S1 = exp(G_end) S0 + K^T (exp(G_end - G) U)
 //
 // k_delta_chunk makes T and P of every chunk and head at once; k_delta_chain
-// walks each sequence's chunks with the state in registers.
+// walks each sequence's chunks with the state in registers, in segments where
+// sequences are few and long.
+//
+// 64 tokens a chunk: half of them would double the states that a training step
+// keeps and the steps of the chain, each with the same latency; twice as many, the
+// work of T and P, which is quadratic, and the LDS for it.
 #include "delta_chain.h"
 
 namespace m3 {
@@ -24,7 +29,9 @@ namespace {
 // the diagonal's by substitution, a column a lane, then, diagonal by diagonal,
 //   T_IJ = -T_II sum_{J <= K < I} A_IK T_KJ.
 // Differences of G are taken in fp64, as G may be large where its differences
-// are small.
+// are small.  256 chunks of 16 heads of 128, bf16: 56 us for 204 MB, 3.6 TB/s, of
+// the 4.9 that a copy reaches: four workgroups a CU, whose barriers wait for loads
+// and for the substitution.
 template <typename T, int DK>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 4 : 2) void k_delta_chunk(DeltaArgs a) {
   using X = Rows64<DK, true>;
@@ -186,7 +193,9 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_segme
 // One token.  A workgroup takes 64 columns of a head's state, a thread four of
 // them in every sixteenth row.  With o = scale (exp(g) S^T q + (k.q) u) one
 // round of sums, over S^T k, S^T q and k.q, is enough, and the state is read
-// and written once: bound by HBM.
+// and written once: bound by HBM.  128 sequences of 64 heads of 128 x 64: 90 us
+// for 546 MB, 6.1 TB/s (the state's writes do not wait for HBM); a single sequence
+// is bound by the launch.
 template <typename T, int DK>
 __global__ __launch_bounds__(256) void k_delta_step(DeltaArgs a, float* hp) {
   constexpr int N = DK / 16;

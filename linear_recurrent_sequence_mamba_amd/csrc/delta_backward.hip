@@ -25,7 +25,8 @@ namespace {
 // ---------------------------------------------------------------------------
 // The chain, as the scan's and with its segments: a wave holds 16 columns of dS.
 // FULL false: only the gradient of the state before the segment, from none
-// behind it (the last segment: from dhT).
+// behind it (the last segment: from dhT).  Bound as the scan's: 5.5 us a chunk
+// of 128 x 64.
 template <typename T, int DK, int NW, int NBUF, bool FULL>
 __device__ __forceinline__ void back_chain(const DeltaArgs& a, const DeltaSeg& seg, int slot, int h, int slice, char* smem) {
   using X = Rows64<DK>;
@@ -261,6 +262,14 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
 // lane has four consecutive rows of a tile's column.  dP and dA have twelve
 // tiles (of two blocks of 32 by 32 on and one below the diagonal), which the
 // waves share.
+//
+// 128 chunks of 32 heads of 128 x 64, bf16: 205 us for 780 MB, 3.8 TB/s.  Its
+// registers leave room for one workgroup a CU, so that what a workgroup asks for
+// first and its products do not overlap with another's; two (128 registers) spill:
+// 400 us.  The next slab's rows are asked for as soon as the last one's are split.
+// AHEAD: a workgroup goes on to another chunk and head, whose first rows it asks
+// for before the products over tokens (without it 230 us); with 128 value
+// channels, several value heads or fp32 the registers for it are not there.
 template <typename T, int DK>
 struct GradTiles {
   using M = Rows64<64>;
@@ -274,6 +283,9 @@ struct GradTiles {
 __device__ __forceinline__ constexpr int tile_i(int n) { return n < 4 ? n >> 1 : 2 + ((n - 4) >> 2); }
 __device__ __forceinline__ constexpr int tile_j(int n) { return n < 4 ? n & 1 : (n - 4) & 3; }
 
+template <typename T, int DV, bool MULTI>
+constexpr bool grads_ahead() { return !MULTI && DV == 64 && sizeof(T) == 2; }
+
 template <typename T, int DK, int DV, bool MULTI>
 __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(DeltaArgs a) {
   using X = Rows64<DK>;
@@ -281,16 +293,20 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
   using G = GradTiles<T, DK>;
   constexpr int NI = G::NI, NO = G::NO, NW = DK / 16, NT = 64 * NW, NTILE = (12 + NW - 1) / NW, VN = 512 / NT;
   // where there is room, the sums over heads wait in LDS (in registers they spill)
-  constexpr bool PARK = MULTI && sizeof(T) == 2;
+  constexpr bool PARK = MULTI && sizeof(T) == 2, AHEAD = grads_ahead<T, DV, MULTI>();
   __shared__ float sAcc[PARK ? 32 : 1][PARK ? NT : 1];
   __shared__ __align__(16) char smem[G::BYTES];
   __shared__ __align__(16) float sGate[kDeltaGates];
   __shared__ float sRow[2][NW][64], sE[4][64], sW[4][64], sC[4][64], sV[64], sEnd[NW];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g0 = lane >> 4;
-  const int hk = blockIdx.x % a.Hk, slot = blockIdx.x / a.Hk, group = MULTI ? a.Hv / a.Hk : 1;
-  const DeltaSlot sl(a, slot, lane);
-  if (sl.n <= 0) return;
+  const int group = MULTI ? a.Hv / a.Hk : 1, items = a.nslot * a.Hk;
+  auto seek = [&](int n) {   // the next chunk and head that there is
+    while (n < items && DeltaSlot(a, n / a.Hk, lane).n <= 0) n += AHEAD ? static_cast<int>(gridDim.x) : items;
+    return n;
+  };
+  int item = seek(blockIdx.x);
+  if (item >= items) return;
   const typename X::Lane xl(lane);
   const M::Lane ml(lane);
   const int ldo = a.Hv * DV;
@@ -299,288 +315,316 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
   const int wcol = X::tile_col(w, lane);   // the wave's channels in K and Q
   const int dkr = 32 * (w >> 1) + 8 * (r >> 2) + 4 * (w & 1) + (r & 3);   // the lane's channel of q and k
   const int64_t dd = static_cast<int64_t>(DK) * DV;
-  f4 dq[4], dk[4];
+  const uint32_t sat0 = static_cast<uint32_t>(dkr * DV + 8 * g0);
+  Stage<T, 64, NT> so, sv;
+  Stage<float, 64, NT> sr, su;
+  Vec8<float> vs[2], vd[2];
+  float gate = 0.0f, gate2 = 0.0f;
+  // 64 columns of a chunk's rows, and of its states
+  auto fetch = [&](const DeltaSlot& sl, int64_t m, int h, int c0, int tid) __attribute__((always_inline)) {
+    so.load(static_cast<const T*>(a.dout) + sl.row0 * ldo + h * DV + c0, ldo, sl.n, tid);
+    sv.load(static_cast<const T*>(a.v) + sl.row0 * a.ldv + h * DV + c0, a.ldv, sl.n, tid);
+    sr.load(a.dr + m * 64 * DV + c0, DV, 64, tid);
+    su.load(a.cstates + m * a.ldpm + dd + c0, DV, 64, tid);
+  };
+  auto fetch_s = [&](int64_t m, int c0, int x, uint32_t sat) __attribute__((always_inline)) {
+    vs[x].load(a.cstates + m * a.ldpm + c0 + 32 * x + sat);
+    vd[x].load(a.after + m * dd + c0 + 32 * x + sat);
+  };
+  auto fetch_first = [&](const DeltaSlot& sl, int64_t m, int h, int tid, uint32_t sat) __attribute__((always_inline)) {
+    const float* p = a.pm + m * a.ldpm + kDeltaMatrix;
+    gate = p[min(tid, kDeltaGates - 1)];
+    if (NT < kDeltaGates) gate2 = p[min(tid + NT, kDeltaGates - 1)];
+    fetch(sl, m, h, 0, tid);
+    fetch_s(m, 0, 0, sat);
+    fetch_s(m, 0, 1, sat);
+  };
+  auto head_of = [&](int n, int h) { return static_cast<int64_t>(n / a.Hk) * a.Hv + h; };
+  if constexpr (AHEAD) {
+    const DeltaSlot sl(a, item / a.Hk, lane);
+    fetch_first(sl, head_of(item, item % a.Hk), item % a.Hk, threadIdx.x, sat0);
+  }
+  for (;;) {
+    const int hk = item % a.Hk, slot = item / a.Hk;
+    const DeltaSlot sl(a, slot, lane);
+    // (behind the last one itself again, unused)
+    int next = AHEAD ? seek(item + gridDim.x) : items;
+    const bool more = next < items;
+    if (!more) next = item;
+    f4 dq[4], dk[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dq[i] = dk[i] = f4{0, 0, 0, 0};
+    for (int i = 0; i < 4; ++i) dq[i] = dk[i] = f4{0, 0, 0, 0};
 
-  for (int h = hk * group; h < (hk + 1) * group; ++h) {
-    // (opaque: addresses are made again for each head, not kept over the loop)
-    const int tid = MULTI ? opaque(threadIdx.x) : threadIdx.x, g = MULTI ? opaque(g0) : g0;
-    const int64_t m = static_cast<int64_t>(slot) * a.Hv + h;
-    const float* S0 = a.cstates + m * a.ldpm;
-    const float* dS = a.after + m * dd;
-    const uint32_t sat = static_cast<uint32_t>(dkr * DV + 8 * g);
-    f4 x1[4], x2[4], x3[4], dp[NTILE], da[NTILE];
+    for (int h = hk * group; h < (hk + 1) * group; ++h) {
+      // (opaque: addresses are made again for each head, not kept over the loop)
+      const int tid = MULTI || AHEAD ? opaque(threadIdx.x) : threadIdx.x, g = MULTI || AHEAD ? opaque(g0) : g0;
+      const int64_t m = static_cast<int64_t>(slot) * a.Hv + h;
+      const uint32_t sat = static_cast<uint32_t>(dkr * DV + 8 * g);
+      f4 x1[4], x2[4], x3[4], dp[NTILE], da[NTILE];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x1[i] = x2[i] = x3[i] = f4{0, 0, 0, 0};
+      for (int i = 0; i < 4; ++i) x1[i] = x2[i] = x3[i] = f4{0, 0, 0, 0};
 #pragma unroll
-    for (int n = 0; n < NTILE; ++n) dp[n] = da[n] = f4{0, 0, 0, 0};
-    float both = 0.0f;   // of <S0, dS1>
-    float vdot[VN];
+      for (int n = 0; n < NTILE; ++n) dp[n] = da[n] = f4{0, 0, 0, 0};
+      float both = 0.0f;   // of <S0, dS1>
+      float vdot[VN];
 #pragma unroll
-    for (int n = 0; n < VN; ++n) vdot[n] = 0.0f;
-    Stage<T, 64, NT> so, sv;
-    Stage<float, 64, NT> sr, su;
-    Vec8<float> vs[2], vd[2];
-    auto fetch = [&](int c0) __attribute__((always_inline)) {
-      so.load(static_cast<const T*>(a.dout) + sl.row0 * ldo + h * DV + c0, ldo, sl.n, tid);
-      sv.load(static_cast<const T*>(a.v) + sl.row0 * a.ldv + h * DV + c0, a.ldv, sl.n, tid);
-      sr.load(a.dr + m * 64 * DV + c0, DV, 64, tid);
-      su.load(S0 + dd + c0, DV, 64, tid);
-    };
-    auto fetch_s = [&](int c0, int x) __attribute__((always_inline)) {
-      vs[x].load(S0 + c0 + 32 * x + sat);
-      vd[x].load(dS + c0 + 32 * x + sat);
-    };
-    fetch(0);
-    fetch_s(0, 0);
-    fetch_s(0, 1);
-    Stage<T, DK, NT> stK, stQ;
-    __syncthreads();
-    for (int i = threadIdx.x; i < kDeltaGates; i += NT) sGate[i] = (a.pm + m * a.ldpm + kDeltaMatrix)[i];
-    if (threadIdx.x < 256) {
-      const int n = threadIdx.x / 64, i = threadIdx.x % 64;
-      sE[n][i] = sW[n][i] = sC[n][i] = 0.0f;
-    }
+      for (int n = 0; n < VN; ++n) vdot[n] = 0.0f;
+      if constexpr (!AHEAD) fetch_first(sl, m, h, tid, sat);
+      Stage<T, DK, NT> stK, stQ;
+      tiles_barrier();
+      if (tid < kDeltaGates) sGate[tid] = gate;
+      if (NT < kDeltaGates && tid + NT < kDeltaGates) sGate[tid + NT] = gate2;
+      if (threadIdx.x < 256) {
+        const int n = threadIdx.x / 64, i = threadIdx.x % 64;
+        sE[n][i] = sW[n][i] = sC[n][i] = 0.0f;
+      }
 #pragma unroll
-    for (int c0 = 0; c0 < DV; c0 += 64) {
-      if (c0 > 0) tiles_barrier();
-      so.store(sO, tid);
+      for (int c0 = 0; c0 < DV; c0 += 64) {
+        if (c0 > 0) tiles_barrier();
+        so.store(sO, tid);
+#pragma unroll
+        for (int n = 0; n < VN; ++n) {
+          const int row = tid / 8 + n * (NT / 8), c = tid % 8 * 8;
+          float f[8], v[8];
+          sr.v[n].get(f);
+          sv.v[n].get(v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) vdot[n] = fmaf(f[j], v[j], vdot[n]);
+          M::put<NO>(sR, row, c, f);
+          su.v[n].get(f);
+          M::put<NO>(sUt, row, c, f);
+        }
+        if (c0 + 64 < DV) {
+          fetch(sl, m, h, c0 + 64, tid);
+        } else {
+          stK.load(static_cast<const T*>(a.k) + sl.row0 * a.ldk + hk * DK, a.ldk, sl.n, tid);
+          stQ.load(static_cast<const T*>(a.q) + sl.row0 * a.ldq + hk * DK, a.ldq, sl.n, tid);
+        }
+        tiles_barrier();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          Parts<NO> ps, pd;
+          {
+            float f[8], d[8];
+            vs[x].get(f);
+            vd[x].get(d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) both = fmaf(f[j], d[j], both);
+            split8<NO>(ps, f);
+            split8<NO>(pd, d);
+            if (c0 + 64 < DV) fetch_s(m, c0 + 64, x, sat);
+          }
+          {
+            Parts<NI> oa[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) oa[i] = M::by_row<NI>(sO, ml, i, x);
+            mmp<NO>(x1, oa, ps);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          {
+            Parts<NO> ra[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ra[i] = M::by_row<NO>(sR, ml, i, x);
+            mmp<NO>(x2, ra, ps);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          {
+            Parts<NO> ua[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ua[i] = M::by_row<NO>(sUt, ml, i, x);
+            mmp<NO>(x3, ua, pd);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          // the wave's own tiles of dP and dA
+#pragma unroll
+          for (int n = 0; n < NTILE; ++n) {
+            const int t = w + n * NW;
+            if (t < 12) {
+              const Parts<NO> ub = M::by_row<NO>(sUt, ml, tile_j(t), x);
+              dp[n] = mmp<NO>(M::by_row<NI>(sO, ml, tile_i(t), x), ub, dp[n]);
+              da[n] = mmp<NO>(M::by_row<NO>(sR, ml, tile_i(t), x), ub, da[n]);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
 #pragma unroll
       for (int n = 0; n < VN; ++n) {
-        const int row = tid / 8 + n * (NT / 8), c = tid % 8 * 8;
-        float f[8], v[8];
-        sr.v[n].get(f);
-        sv.v[n].get(v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) vdot[n] = fmaf(f[j], v[j], vdot[n]);
-        M::put<NO>(sR, row, c, f);
-        su.v[n].get(f);
-        M::put<NO>(sUt, row, c, f);
+        const float d = group_sum<8>(vdot[n]);
+        if (tid % 8 == 0) sV[tid / 8 + n * (NT / 8)] = d;
       }
-      if (c0 + 64 < DV) {
-        fetch(c0 + 64);
-      } else {
-        stK.load(static_cast<const T*>(a.k) + sl.row0 * a.ldk + hk * DK, a.ldk, sl.n, tid);
-        stQ.load(static_cast<const T*>(a.q) + sl.row0 * a.ldq + hk * DK, a.ldq, sl.n, tid);
+      both = group_sum<64>(both);
+      tiles_barrier();
+      stK.store(sK, tid);
+      stQ.store(sQ, tid);
+      tiles_barrier();
+      if constexpr (AHEAD) {
+        const DeltaSlot nsl(a, next / a.Hk, lane);
+        fetch_first(nsl, head_of(next, next % a.Hk), next % a.Hk, tid, sat);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int n = 0; n < NTILE; ++n) {
+        const int t = w + n * NW;
+        if (t < 12) {
+          const int ti = tile_i(t), tj = tile_j(t), j = tile_row(tj, 0) + 8 * (r >> 2) + (r & 3);
+          const int i0 = tile_row(ti, 0) + 8 * g;
+          f4 kk = f4{0, 0, 0, 0}, qk = f4{0, 0, 0, 0};
+#pragma unroll
+          for (int x = 0; x < DK / 32; ++x) {
+            const Parts<NI> kb = X::template by_row<NI>(sK, xl, tj, x);
+            kk = mmp<3>(X::template by_row<NI>(sK, xl, ti, x), kb, kk);
+            qk = mmp<3>(X::template by_row<NI>(sQ, xl, ti, x), kb, qk);
+          }
+          const float gh = sGate[192 + j], gl = sGate[256 + j];
+          const f4 hi = *reinterpret_cast<const f4*>(&sGate[192 + i0]), lo = *reinterpret_cast<const f4*>(&sGate[256 + i0]);
+          const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + i0]);
+          float col = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float gam = i0 + e >= j ? __builtin_amdgcn_exp2f((hi[e] - gh) + (lo[e] - gl)) : 0.0f;
+            // (a product that is not finite stays out of the half that is not there)
+            const float ag = i0 + e > j ? -da[n][e] * gam : 0.0f, ak = ag == 0.0f ? 0.0f : ag * kk[e];
+            dp[n][e] = i0 + e >= j ? a.scale * dp[n][e] * gam : 0.0f;
+            da[n][e] = bt[e] * ag;
+            // (the diagonal does not depend on G)
+            const float c = fmaf(bt[e], ak, i0 + e == j || dp[n][e] == 0.0f ? 0.0f : dp[n][e] * qk[e]);
+            col += c;
+            const float es = group_sum<16>(ak), cs = group_sum<16>(c);
+            if (r == 0) {
+              sE[tj][i0 + e] = es;
+              sW[tj][i0 + e] = cs;
+            }
+          }
+          col += __shfl_xor(col, 16, 64);
+          col += __shfl_xor(col, 32, 64);
+          if (g == 0) sC[ti][j] = col;
+          Parts<NO> pf;
+          split_d<NO>(pf, dp[n], da[n]);
+          char* to = smem + 2 * NI * X::PLANE + M::at(j, i0 & ~7) + 2 * (i0 & 7);
+#pragma unroll
+          for (int q = 0; q < NO; ++q) {
+            const uint4 u = __builtin_bit_cast(uint4, pf.p[q]);
+            *reinterpret_cast<uint2*>(to + q * M::PLANE) = uint2{u.x, u.y};
+            *reinterpret_cast<uint2*>(to + (NO + q) * M::PLANE) = uint2{u.z, u.w};
+          }
+        }
       }
       tiles_barrier();
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        Parts<NO> ps, pd;
-        {
-          float f[8], d[8];
-          vs[x].get(f);
-          vd[x].get(d);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) both = fmaf(f[j], d[j], both);
-          split8<NO>(ps, f);
-          split8<NO>(pd, d);
-          if (c0 + 64 < DV) fetch_s(c0 + 64, x);
-        }
-        {
-          Parts<NI> oa[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) oa[i] = M::by_row<NI>(sO, ml, i, x);
-          mmp<NO>(x1, oa, ps);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        {
-          Parts<NO> ra[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ra[i] = M::by_row<NO>(sR, ml, i, x);
-          mmp<NO>(x2, ra, ps);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        {
-          Parts<NO> ua[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ua[i] = M::by_row<NO>(sUt, ml, i, x);
-          mmp<NO>(x3, ua, pd);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        // the wave's own tiles of dP and dA
-#pragma unroll
-        for (int n = 0; n < NTILE; ++n) {
-          const int t = w + n * NW;
-          if (t < 12) {
-            const Parts<NO> ub = M::by_row<NO>(sUt, ml, tile_j(t), x);
-            dp[n] = mmp<NO>(M::by_row<NI>(sO, ml, tile_i(t), x), ub, dp[n]);
-            da[n] = mmp<NO>(M::by_row<NO>(sR, ml, tile_i(t), x), ub, da[n]);
-          }
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < VN; ++n) {
-      const float d = group_sum<8>(vdot[n]);
-      if (tid % 8 == 0) sV[tid / 8 + n * (NT / 8)] = d;
-    }
-    both = group_sum<64>(both);
-    tiles_barrier();
-    stK.store(sK, tid);
-    stQ.store(sQ, tid);
-    tiles_barrier();
-#pragma unroll
-    for (int n = 0; n < NTILE; ++n) {
-      const int t = w + n * NW;
-      if (t < 12) {
-        const int ti = tile_i(t), tj = tile_j(t), j = tile_row(tj, 0) + 8 * (r >> 2) + (r & 3);
-        const int i0 = tile_row(ti, 0) + 8 * g;
-        f4 kk = f4{0, 0, 0, 0}, qk = f4{0, 0, 0, 0};
-#pragma unroll
-        for (int x = 0; x < DK / 32; ++x) {
-          const Parts<NI> kb = X::template by_row<NI>(sK, xl, tj, x);
-          kk = mmp<3>(X::template by_row<NI>(sK, xl, ti, x), kb, kk);
-          qk = mmp<3>(X::template by_row<NI>(sQ, xl, ti, x), kb, qk);
-        }
-        const float gh = sGate[192 + j], gl = sGate[256 + j];
-        const f4 hi = *reinterpret_cast<const f4*>(&sGate[192 + i0]), lo = *reinterpret_cast<const f4*>(&sGate[256 + i0]);
-        const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + i0]);
-        float col = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float gam = i0 + e >= j ? __builtin_amdgcn_exp2f((hi[e] - gh) + (lo[e] - gl)) : 0.0f;
-          // (a product that is not finite stays out of the half that is not there)
-          const float ag = i0 + e > j ? -da[n][e] * gam : 0.0f, ak = ag == 0.0f ? 0.0f : ag * kk[e];
-          dp[n][e] = i0 + e >= j ? a.scale * dp[n][e] * gam : 0.0f;
-          da[n][e] = bt[e] * ag;
-          // (the diagonal does not depend on G)
-          const float c = fmaf(bt[e], ak, i0 + e == j || dp[n][e] == 0.0f ? 0.0f : dp[n][e] * qk[e]);
-          col += c;
-          const float es = group_sum<16>(ak), cs = group_sum<16>(c);
-          if (r == 0) {
-            sE[tj][i0 + e] = es;
-            sW[tj][i0 + e] = cs;
-          }
-        }
-        col += __shfl_xor(col, 16, 64);
-        col += __shfl_xor(col, 32, 64);
-        if (g == 0) sC[ti][j] = col;
-        Parts<NO> pf;
-        split_d<NO>(pf, dp[n], da[n]);
-        char* to = smem + 2 * NI * X::PLANE + M::at(j, i0 & ~7) + 2 * (i0 & 7);
-#pragma unroll
-        for (int q = 0; q < NO; ++q) {
-          const uint4 u = __builtin_bit_cast(uint4, pf.p[q]);
-          *reinterpret_cast<uint2*>(to + q * M::PLANE) = uint2{u.x, u.y};
-          *reinterpret_cast<uint2*>(to + (NO + q) * M::PLANE) = uint2{u.z, u.w};
-        }
-      }
-    }
-    tiles_barrier();
-    // dQ = scale exp(G) X1 + F K,  dK = F^T Q + (M + M^T) K - exp(G) beta X2 + exp(G_end - G) X3
-    float re = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f4 st = *reinterpret_cast<const f4*>(&sGate[tile_row(i, 0) + 8 * g]);
-      const f4 en = *reinterpret_cast<const f4*>(&sGate[64 + tile_row(i, 0) + 8 * g]);
-      const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + tile_row(i, 0) + 8 * g]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = tile_row(i, e) + 8 * g;
-        const float k = X::template get<NI>(sK, row, dkr), q = X::template get<NI>(sQ, row, dkr);
-        const float x = x3[i][e] * en[e], y = st[e] * bt[e] * x2[i][e];
-        x1[i][e] *= a.scale * st[e];
-        const float d = group_sum<16>(fmaf(q, x1[i][e], -k * (x + y))), kx = group_sum<16>(k * x2[i][e]);
-        if (r == 0) {
-          sRow[0][w][row] = d;
-          sRow[1][w][row] = kx;
-        }
-        re = fmaf(k, x, re);
-        x2[i][e] = x - y;
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const Parts<NI> kb = X::template by_col<NI>(sK, wcol, x), qb = X::template by_col<NI>(sQ, wcol, x);
-      Parts<NO> f[4];
-      // columns of block x and rows of its and later blocks; by_col: of the
-      // transpose's rows, which are its columns
-#pragma unroll
-      for (int i = 2 * x; i < 4; ++i) f[i] = M::by_col<NO>(sF, ml, i, x);
-#pragma unroll
-      for (int i = 2 * x; i < 4; ++i) x1[i] = mmp<NO>(f[i], kb, x1[i]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 2 * x; i < 4; ++i) f[i] = M::by_col<NO>(sN, ml, i, x);
-#pragma unroll
-      for (int i = 2 * x; i < 4; ++i) x2[i] = mmp<NO>(f[i], kb, x2[i]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < 2 * x + 2; ++i) f[i] = M::by_row<NO>(sF, ml, i, x);
-#pragma unroll
-      for (int i = 0; i < 2 * x + 2; ++i) x2[i] = mmp<NO>(f[i], qb, x2[i]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < 2 * x + 2; ++i) f[i] = M::by_row<NO>(sN, ml, i, x);
-#pragma unroll
-      for (int i = 0; i < 2 * x + 2; ++i) x2[i] = mmp<NO>(f[i], kb, x2[i]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (PARK) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float *q = &sAcc[4 * i + e][tid], *k = &sAcc[16 + 4 * i + e][tid];
-          *q = h > hk * group ? *q + x1[i][e] : x1[i][e];
-          *k = h > hk * group ? *k + x2[i][e] : x2[i][e];
-        }
-      } else if constexpr (MULTI) {
-        dq[i] += x1[i];
-        dk[i] += x2[i];
-      }
-    }
-    re = group_sum<64>(re);
-    if (lane == 0) sEnd[w] = fmaf(sGate[63], both, re);
-    tiles_barrier();
-    if (w == 0) {
-      float d = 0.0f, x = 0.0f, end = 0.0f;
-#pragma unroll
-      for (int n = 0; n < NW; ++n) {
-        d += sRow[0][n][lane];
-        x += sRow[1][n][lane];
-        end += sEnd[n];
-      }
-      const float db = sV[lane] - sGate[lane] * x + (sE[0][lane] + sE[1][lane]) + (sE[2][lane] + sE[3][lane]);
-      float dG = d;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) dG += sW[n][lane] - sC[n][lane];
-      if (lane == 63) dG += end;
-      // sums of the rows from here on
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const float y = __shfl_down(dG, o, 64);
-        if (lane + o < 64) dG += y;
-      }
-      if (lane < sl.n) {
-        const int64_t at = (sl.row0 + lane) * a.Hv + h;
-        static_cast<T*>(a.dg)[at] = from_f32<T>(dG);
-        static_cast<T*>(a.dbeta)[at] = from_f32<T>(db);
-      }
-    }
-    if constexpr (!MULTI) {
+      // dQ = scale exp(G) X1 + F K,  dK = F^T Q + (M + M^T) K - exp(G) beta X2 + exp(G_end - G) X3
+      float re = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        dq[i] = x1[i];
-        dk[i] = x2[i];
+        const f4 st = *reinterpret_cast<const f4*>(&sGate[tile_row(i, 0) + 8 * g]);
+        const f4 en = *reinterpret_cast<const f4*>(&sGate[64 + tile_row(i, 0) + 8 * g]);
+        const f4 bt = *reinterpret_cast<const f4*>(&sGate[128 + tile_row(i, 0) + 8 * g]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = tile_row(i, e) + 8 * g;
+          const float k = X::template get<NI>(sK, row, dkr), q = X::template get<NI>(sQ, row, dkr);
+          const float x = x3[i][e] * en[e], y = st[e] * bt[e] * x2[i][e];
+          x1[i][e] *= a.scale * st[e];
+          const float d = group_sum<16>(fmaf(q, x1[i][e], -k * (x + y))), kx = group_sum<16>(k * x2[i][e]);
+          if (r == 0) {
+            sRow[0][w][row] = d;
+            sRow[1][w][row] = kx;
+          }
+          re = fmaf(k, x, re);
+          x2[i][e] = x - y;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const Parts<NI> kb = X::template by_col<NI>(sK, wcol, x), qb = X::template by_col<NI>(sQ, wcol, x);
+        Parts<NO> f[4];
+        // columns of block x and rows of its and later blocks; by_col: of the
+        // transpose's rows, which are its columns
+#pragma unroll
+        for (int i = 2 * x; i < 4; ++i) f[i] = M::by_col<NO>(sF, ml, i, x);
+#pragma unroll
+        for (int i = 2 * x; i < 4; ++i) x1[i] = mmp<NO>(f[i], kb, x1[i]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 2 * x; i < 4; ++i) f[i] = M::by_col<NO>(sN, ml, i, x);
+#pragma unroll
+        for (int i = 2 * x; i < 4; ++i) x2[i] = mmp<NO>(f[i], kb, x2[i]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 2 * x + 2; ++i) f[i] = M::by_row<NO>(sF, ml, i, x);
+#pragma unroll
+        for (int i = 0; i < 2 * x + 2; ++i) x2[i] = mmp<NO>(f[i], qb, x2[i]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 2 * x + 2; ++i) f[i] = M::by_row<NO>(sN, ml, i, x);
+#pragma unroll
+        for (int i = 0; i < 2 * x + 2; ++i) x2[i] = mmp<NO>(f[i], kb, x2[i]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (PARK) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float *q = &sAcc[4 * i + e][tid], *k = &sAcc[16 + 4 * i + e][tid];
+            *q = h > hk * group ? *q + x1[i][e] : x1[i][e];
+            *k = h > hk * group ? *k + x2[i][e] : x2[i][e];
+          }
+        } else if constexpr (MULTI) {
+          dq[i] += x1[i];
+          dk[i] += x2[i];
+        }
+      }
+      re = group_sum<64>(re);
+      if (lane == 0) sEnd[w] = fmaf(sGate[63], both, re);
+      tiles_barrier();
+      if (w == 0) {
+        float d = 0.0f, x = 0.0f, end = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NW; ++n) {
+          d += sRow[0][n][lane];
+          x += sRow[1][n][lane];
+          end += sEnd[n];
+        }
+        const float db = sV[lane] - sGate[lane] * x + (sE[0][lane] + sE[1][lane]) + (sE[2][lane] + sE[3][lane]);
+        float dG = d;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) dG += sW[n][lane] - sC[n][lane];
+        if (lane == 63) dG += end;
+        // sums of the rows from here on
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+          const float y = __shfl_down(dG, o, 64);
+          if (lane + o < 64) dG += y;
+        }
+        if (lane < sl.n) {
+          const int64_t at = (sl.row0 + lane) * a.Hv + h;
+          static_cast<T*>(a.dg)[at] = from_f32<T>(dG);
+          static_cast<T*>(a.dbeta)[at] = from_f32<T>(db);
+        }
+      }
+      if constexpr (!MULTI) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dq[i] = x1[i];
+          dk[i] = x2[i];
+        }
       }
     }
+    const int ldq = a.Hk * DK;
+    const ChunkRows oq(static_cast<T*>(a.dq) + sl.row0 * ldq + hk * DK, ldq, sl.n);
+    const ChunkRows ok(static_cast<T*>(a.dk) + sl.row0 * ldq + hk * DK, ldq, sl.n);
+    const uint32_t orow = static_cast<uint32_t>(ldq) * static_cast<uint32_t>(sizeof(T));
+    const uint32_t oat = 8 * g0 * orow + dkr * static_cast<uint32_t>(sizeof(T));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        oq.store1(T{}, oat + tile_row(i, e) * orow, PARK ? sAcc[4 * i + e][threadIdx.x] : dq[i][e]);
+        ok.store1(T{}, oat + tile_row(i, e) * orow, PARK ? sAcc[16 + 4 * i + e][threadIdx.x] : dk[i][e]);
+      }
+    if (!more) break;
+    item = next;
   }
-  const int ldq = a.Hk * DK;
-  const ChunkRows oq(static_cast<T*>(a.dq) + sl.row0 * ldq + hk * DK, ldq, sl.n);
-  const ChunkRows ok(static_cast<T*>(a.dk) + sl.row0 * ldq + hk * DK, ldq, sl.n);
-  const uint32_t orow = static_cast<uint32_t>(ldq) * static_cast<uint32_t>(sizeof(T));
-  const uint32_t oat = 8 * g0 * orow + dkr * static_cast<uint32_t>(sizeof(T));
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      oq.store1(T{}, oat + tile_row(i, e) * orow, PARK ? sAcc[4 * i + e][threadIdx.x] : dq[i][e]);
-      ok.store1(T{}, oat + tile_row(i, e) * orow, PARK ? sAcc[16 + 4 * i + e][threadIdx.x] : dk[i][e]);
-    }
 }
 
 template <typename T, int DK, int NW>
@@ -609,7 +653,10 @@ hipError_t run_backward(const DeltaArgs& a, hipStream_t s) {
   else
     e = run_back_chain<T, DK, 4>(a, s);
   if (e != hipSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(a.nslot) * a.Hk);
+  const int64_t items = static_cast<int64_t>(a.nslot) * a.Hk;
+  const bool ahead = a.Dv == 64 && a.Hv == a.Hk && grads_ahead<T, 64, false>();
+  constexpr int most = 256 * 128 / DK;   // as many as are resident, of 4 or 8 waves with 256 registers
+  const unsigned grid = static_cast<unsigned>(ahead && items > most ? most : items);
   if (a.Dv == 64) {
     if (a.Hv == a.Hk) k_delta_grads<T, DK, 64, false><<<grid, 4 * DK, 0, s>>>(a);
     else k_delta_grads<T, DK, 64, true><<<grid, 4 * DK, 0, s>>>(a);

@@ -205,6 +205,33 @@ def test_dense_prompts_in_segments(shape):
                 _check(n, got[n], val, bound)
 
 
+@pytest.mark.parametrize("dk", [64, 128])
+def test_more_chunks_and_heads_than_workgroups(dk):
+    """Gradients whose workgroups go on from one chunk and head to the next, past slots that no chunk takes."""
+    lengths, heads, dv = [700, 0, 0, 64, 1, 299], 40, 64
+    q, k, v, g, b, h0, do, dhT = _inputs(sum(lengths), heads, heads, dk, dv, BF16, 70 + dk, False, len(lengths))
+    off = [0]
+    for n in lengths:
+        off.append(off[-1] + n)
+    cu = torch.tensor(off, dtype=torch.int32).cuda()
+    o, hT, st = m3.delta_scan(q, k, v, g, b, h0=h0, cu_seqlens=cu, want_states=True)
+    d = m3.delta_scan_backward(q, k, v, g, b, do, st, h0=h0, dhT=dhT, cu_seqlens=cu)
+    for s, n in enumerate(lengths):
+        if n == 0:
+            assert torch.equal(d["h0"][s], dhT[s])
+            continue
+        c = slice(off[s], off[s + 1])
+        for h in (0, 7, 23, 39):
+            x = slice(h, h + 1)
+            want = delta_ref.check(q[c, x], k[c, x], v[c, x], g[c, x], b[c, x], h0[s, x], dk ** -0.5, BF16, do[c, x],
+                                   dhT[s, x])
+            got = {"o": o[c, x], "hT": hT[s, x], "dq": d["q"][c, x], "dk": d["k"][c, x], "dv": d["v"][c, x],
+                   "dg": d["g"][c, x], "dbeta": d["beta"][c, x], "dh0": d["h0"][s, x]}
+            for name, (val, bound) in want.items():
+                _check(f"{name} of sequence {s}, head {h}", got[name], val, bound)
+                assert name == "dg" or _rel(got[name], val) <= 2 * ref.U[BF16], (name, s, h)
+
+
 def test_strong_gates():
     """Decays of 0 (-inf and far below), no decay, no write, and writes of twice the miss."""
     L, hk, hv, dk, dv = 140, 1, 2, 64, 64

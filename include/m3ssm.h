@@ -517,7 +517,8 @@ size_t m3_delta_scan_workspace_size(const m3_delta_dims* dims, int packed);
  * the buffers whatever they hold; they are meant to rise, and the rows of a
  * batch whose offsets do not are unspecified.  Rows that no sequence covers
  * are left as they are.  A NaN or Inf stays in its sequence and heads, and may
- * reach all outputs from its chunk on.  g and beta need only their elements'
+ * reach all outputs from its chunk on.  A token with beta = 0 and g = 0 leaves
+ * the state as it is, bit for bit.  g and beta need only their elements'
  * alignment. */
 m3_status m3_delta_scan(const m3_delta_dims* dims, const int32_t* cu_seqlens, const void* q,
                         const void* k, const void* v, const void* g, const void* beta,
@@ -566,8 +567,8 @@ typedef struct {
 
 /* x, y, gate (NULL: 1) [T, W] to h and n (NULL: not written) [T, W], dense.
  * y_weight, scale, n_weight [W] fp32 or NULL (1).  With dense rows h may be x
- * or y.  Widths and distances that are multiples of 8 are read 8 elements at a
- * time. */
+ * or y.  Widths and distances that are multiples of 16 bytes are read 16 bytes
+ * at a time. */
 m3_status m3_block_norm(const m3_block_dims* dims, const void* x, const void* y, const void* gate,
                         const float* y_weight, const float* scale, const float* n_weight, void* h,
                         void* n, void* stream);

@@ -55,6 +55,21 @@ struct RowPart {
       for (int j = 0; j < V; ++j) v[i * V + j] = on ? v[i * V + j] : 0.0f;
     }
   }
+  // N of them from element i on, of one vector
+  template <int N>
+  __device__ __forceinline__ void some(float* v, int i, bool on) const {
+    float f[V];
+    r[i / V].get(f);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = on ? f[i % V + j] : 0.0f;
+  }
+  // what is formed from them is formed anew from here on, not kept in registers
+  __device__ __forceinline__ void renew() {
+    constexpr int N = static_cast<int>(sizeof(r) / sizeof(uint32_t));
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(u[i]));
+  }
   static __device__ __forceinline__ void put(float* p, const float* v) {
     if constexpr (V == 1) {
       p[0] = v[0];
@@ -72,6 +87,26 @@ struct RowPart {
       for (int k = 0; k < 4; ++k)
         w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[2 * k], v[2 * k + 1]}, bh2));
       *reinterpret_cast<uint4*>(p) = uint4{w[0], w[1], w[2], w[3]};
+    }
+  }
+  // N values, of one vector
+  template <int N>
+  static __device__ __forceinline__ void put_some(float* p, const float* v) {
+    if constexpr (N == 4) *reinterpret_cast<f4*>(p) = f4{v[0], v[1], v[2], v[3]};
+    else if constexpr (N == 2) *reinterpret_cast<f2*>(p) = f2{v[0], v[1]};
+    else p[0] = v[0];
+  }
+  template <int N>
+  static __device__ __forceinline__ void put_some(bf16_t* p, const float* v) {
+    if constexpr (N == 1) {
+      put(p, v);
+    } else {
+      uint32_t w[N / 2];
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k)
+        w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{v[2 * k], v[2 * k + 1]}, bh2));
+      if constexpr (N == 4) *reinterpret_cast<uint2*>(p) = uint2{w[0], w[1]};
+      else *reinterpret_cast<uint32_t*>(p) = w[0];
     }
   }
   template <typename O>
@@ -299,6 +334,142 @@ __global__ __launch_bounds__(1024) void k_block_norm_bwd(BlockNormArgs a) {
   R::store(a.part + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * W, pn, W);
 }
 
+// The gradients where a thread has more elements than registers for all that the
+// kernel above keeps of them: a row is not asked for ahead, what its passes need
+// is formed from the loaded values each time, a few elements after the other, and
+// P and dwn are summed in LDS.
+template <typename T, int V, int E>
+__global__ __launch_bounds__(1024) void k_block_norm_bwd_lean(BlockNormArgs a) {
+  using R = RowPart<T, V, E>;
+  constexpr int N = V == 1 ? 1 : 4;   // elements at a time
+  __shared__ f2 sh[2][16];
+  __shared__ __align__(16) float acc[2][1024 * E];
+  Sums sums{sh, 0};
+  const int W = a.W;
+  const float invW = 1.0f / static_cast<float>(W);
+  float wz[E], wn[E];
+  weights<T, V, E>(wz, a.wy, W);
+  weights<T, V, E>(wn, a.scale, W);
+#pragma unroll
+  for (int j = 0; j < E; ++j) {
+    wz[j] *= wn[j];
+    acc[0][R::index(j)] = acc[1][R::index(j)] = 0.0f;   // (only the thread's own elements, ever)
+  }
+  weights<T, V, E>(wn, a.wn, W);
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    R rx, ry, rg, rh, rn;
+    ry.load(static_cast<const T*>(a.y) + t * a.ldy, W);
+    rx.load(static_cast<const T*>(a.x) + t * a.ldx, W);
+    if (a.gate) rg.load(static_cast<const T*>(a.gate) + t * a.ldg, W);
+    if (a.dn) rn.load(static_cast<const T*>(a.dn) + t * W, W);
+    if (a.dh) rh.load(static_cast<const T*>(a.dh) + t * W, W);
+    float iy = 1.0f, ih = 0.0f, c = 0.0f;
+    if (!a.raw) {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < E; i += N) {
+        float y[N];
+        ry.template some<N>(y, i, R::index(i / V * V) < W);
+#pragma unroll
+        for (int j = 0; j < N; ++j) s = fmaf(y[j], y[j], s);
+      }
+      iy = __builtin_amdgcn_rsqf(fmaf(sums(s, 0.0f).x, invW, a.eps));
+    }
+    // of elements i ..: weights, act(gate) and its derivative, u and h
+    struct Some {
+      bool on;
+      float act[N], da[N], u[N], h[N];
+    };
+    auto form = [&](Some& f, int i) __attribute__((always_inline)) {
+      f.on = R::index(i / V * V) < W;
+      ry.template some<N>(f.u, i, f.on);
+      rx.template some<N>(f.h, i, f.on);
+      if (a.gate) rg.template some<N>(f.act, i, f.on);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        f.u[j] *= iy;
+        f.da[j] = 0.0f;
+        f.act[j] = a.gate ? gate_act(a.act, f.act[j], f.da[j]) : 1.0f;
+        f.h[j] = fmaf(f.act[j] * wz[i + j], f.u[j], f.h[j]);
+      }
+    };
+    if (a.dn) {
+      float s = 0.0f, d = 0.0f;
+      ry.renew();
+#pragma unroll
+      for (int i = 0; i < E; i += N) {
+        Some f;
+        float gm[N];
+        form(f, i);
+        rn.template some<N>(gm, i, f.on);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          s = fmaf(f.h[j], f.h[j], s);
+          d = fmaf(gm[j] * wn[i + j], f.h[j], d);
+        }
+        if (i % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+      }
+      const f2 sd = sums(s, d);
+      ih = __builtin_amdgcn_rsqf(fmaf(sd.x, invW, a.eps));
+      c = sd.y * invW * ih * ih;
+    }
+    ry.renew();
+    rx.renew();
+    if (a.gate) rg.renew();
+    if (a.dn) rn.renew();
+    float gu[E], s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; i += N) {
+      Some f;
+      float gm[N], dh[N];
+      form(f, i);
+#pragma unroll
+      for (int j = 0; j < N; ++j) dh[j] = gm[j] = 0.0f;
+      if (a.dh) rh.template some<N>(dh, i, f.on);
+      if (a.dn) {
+        rn.template some<N>(gm, i, f.on);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          dh[j] += ih * fmaf(gm[j], wn[i + j], -f.h[j] * c);
+          gm[j] *= f.h[j] * ih;
+        }
+      }
+      const int e = R::index(i);
+      if (f.on) R::template put_some<N>(static_cast<T*>(a.dx) + t * W + e, dh);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float du = dh[j] * f.u[j], p = du * f.act[j];
+        f.da[j] *= du * wz[i + j];
+        gu[i + j] = f.act[j] * dh[j] * wz[i + j];
+        s = fmaf(gu[i + j], f.u[j], s);
+        acc[0][e + j] += p;
+        acc[1][e + j] += gm[j];
+      }
+      if (a.gate && f.on) R::template put_some<N>(static_cast<T*>(a.dgate) + t * W + e, f.da);
+      if (i % 4 == 0) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (!a.raw) {
+      const float m = sums(s, 0.0f).x * invW;
+      ry.renew();
+#pragma unroll
+      for (int i = 0; i < E; i += N) {
+        float y[N];
+        ry.template some<N>(y, i, R::index(i / V * V) < W);
+#pragma unroll
+        for (int j = 0; j < N; ++j) gu[i + j] = iy * fmaf(-y[j] * iy, m, gu[i + j]);
+      }
+    }
+    R::store(static_cast<T*>(a.dy) + t * W, gu, W);
+  }
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * W;
+#pragma unroll
+  for (int j = 0; j < E; ++j)
+    if (R::index(j) < W) {
+      part[R::index(j)] = acc[0][R::index(j)];
+      part[W + R::index(j)] = acc[1][R::index(j)];
+    }
+}
+
 // The parts of P and dwn of `nblk` workgroups, joined: 64 columns a workgroup,
 // its sixteen waves every sixteenth part each.
 __global__ __launch_bounds__(1024) void k_block_norm_join(BlockNormArgs a, int nblk) {
@@ -351,7 +522,8 @@ bool vectors(const BlockNormArgs& a) {
 
 template <typename T, bool BWD, int V, int E>
 hipError_t run(const BlockNormArgs& a, int grid, int nt, hipStream_t s) {
-  if constexpr (BWD) k_block_norm_bwd<T, V, E><<<grid, nt, 0, s>>>(a);
+  if constexpr (BWD && V < 8 && E == 8) k_block_norm_bwd_lean<T, V, E><<<grid, nt, 0, s>>>(a);
+  else if constexpr (BWD) k_block_norm_bwd<T, V, E><<<grid, nt, 0, s>>>(a);
   else k_block_norm<T, V, E><<<grid, nt, 0, s>>>(a);
   return hipGetLastError();
 }

@@ -337,11 +337,12 @@ __global__ __launch_bounds__(1024) void k_block_norm_bwd(BlockNormArgs a) {
 // The gradients where a thread has more elements than registers for all that the
 // kernel above keeps of them: a row is not asked for ahead, what its passes need
 // is formed from the loaded values each time, a few elements after the other, and
-// P and dwn are summed in LDS.
+// P and dwn are summed in LDS.  4854 rows of 5473 bf16: 242 us with the forward
+// call, in the kernel above, spilled, 627.
 template <typename T, int V, int E>
 __global__ __launch_bounds__(1024) void k_block_norm_bwd_lean(BlockNormArgs a) {
   using R = RowPart<T, V, E>;
-  constexpr int N = V == 1 ? 1 : 4;   // elements at a time
+  constexpr int N = V == 1 ? 1 : E == 16 ? 2 : 4;   // elements at a time
   __shared__ f2 sh[2][16];
   __shared__ __align__(16) float acc[2][1024 * E];
   Sums sums{sh, 0};
@@ -470,6 +471,199 @@ __global__ __launch_bounds__(1024) void k_block_norm_bwd_lean(BlockNormArgs a) {
     }
 }
 
+// Rows of more than 8192 elements where a thread would have 16 single or fp32 ones,
+// for which there are no registers: nothing of a row is kept, each pass reads it
+// again, from the caches (the rows under way are at most 320 KB a workgroup).
+// 2000 rows of 16383 bf16: forward 148 us (in registers, spilled, 377), with
+// gradients 444 (1602); 2000 of 16000 fp32 with gradients 477 (879).  In vectors of
+// bf16 the kernels above are faster: 71 us forward, with gradients 344 (517 so).
+//
+// A thread's K elements of a turn: a vector, or four single ones; behind the
+// row's end 0.
+template <typename T, int V>
+struct Turn {
+  static constexpr int K = V == 1 ? 4 : V, STEP = 1024 * K;
+  static __device__ __forceinline__ int first() { return threadIdx.x * V; }
+  static __device__ __forceinline__ int at(int e, int j) { return V == 1 ? e + 1024 * j : e + j; }
+  template <typename P>
+  static __device__ __forceinline__ void take(float* v, const P* row, int e, int W) {
+    if constexpr (V == 1) {
+      RawVec<P, 1> r[K];
+#pragma unroll
+      for (int j = 0; j < K; ++j) r[j].load(row + min(at(e, j), W - 1));
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        r[j].get(v + j);
+        v[j] = at(e, j) < W ? v[j] : 0.0f;
+      }
+    } else {
+      RawVec<P, K> r;
+      r.load(row + e);
+      r.get(v);
+    }
+  }
+  // weights, 1 without any
+  static __device__ __forceinline__ void take_or(float* v, const float* p, int e, int W) {
+    if (p) {
+      take(v, p, e, W);
+    } else {
+#pragma unroll
+      for (int j = 0; j < K; ++j) v[j] = 1.0f;
+    }
+  }
+  template <typename P>
+  static __device__ __forceinline__ void put(P* row, const float* v, int e, int W) {
+    if constexpr (V == 1) {
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (at(e, j) < W) RowPart<T, 1, 1>::put(row + at(e, j), v + j);
+    } else {
+      RowPart<T, V, V>::put(row + e, v);
+    }
+  }
+  // act(gate), its derivative, u and h
+  float wz[K], act[K], da[K], u[K], h[K];
+  __device__ __forceinline__ Turn(const BlockNormArgs& a, int64_t t, int e, float iy) {
+    take(u, static_cast<const T*>(a.y) + t * a.ldy, e, a.W);
+    take(h, static_cast<const T*>(a.x) + t * a.ldx, e, a.W);
+    if (a.gate) take(act, static_cast<const T*>(a.gate) + t * a.ldg, e, a.W);
+    float sc[K];
+    take_or(wz, a.wy, e, a.W);
+    take_or(sc, a.scale, e, a.W);
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      wz[j] *= sc[j];
+      u[j] *= iy;
+      da[j] = 0.0f;
+      act[j] = a.gate ? gate_act(a.act, act[j], da[j]) : 1.0f;
+      h[j] = fmaf(act[j] * wz[j], u[j], h[j]);
+    }
+  }
+  static __device__ __forceinline__ float square(const BlockNormArgs& a, int64_t t) {
+    float s = 0.0f;
+#pragma unroll 2
+    for (int e = first(); e < a.W; e += STEP) {
+      float y[K];
+      take(y, static_cast<const T*>(a.y) + t * a.ldy, e, a.W);
+#pragma unroll
+      for (int j = 0; j < K; ++j) s = fmaf(y[j], y[j], s);
+    }
+    return s;
+  }
+};
+
+template <typename T, int V>
+__global__ __launch_bounds__(1024) void k_block_norm_long(BlockNormArgs a) {
+  using P = Turn<T, V>;
+  __shared__ f2 sh[2][16];
+  Sums sums{sh, 0};
+  const float invW = 1.0f / static_cast<float>(a.W);
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const float iy = a.raw ? 1.0f : __builtin_amdgcn_rsqf(fmaf(sums(P::square(a, t), 0.0f).x, invW, a.eps));
+    float ih = 0.0f;
+    if (a.n) {   // (before h is written, which may be x or y)
+      float s = 0.0f;
+#pragma unroll 2
+      for (int e = P::first(); e < a.W; e += P::STEP) {
+        const P f(a, t, e, iy);
+#pragma unroll
+        for (int j = 0; j < P::K; ++j) s = fmaf(f.h[j], f.h[j], s);
+      }
+      ih = __builtin_amdgcn_rsqf(fmaf(sums(s, 0.0f).x, invW, a.eps));
+    }
+#pragma unroll 1
+    for (int e = P::first(); e < a.W; e += P::STEP) {
+      P f(a, t, e, iy);
+      P::put(static_cast<T*>(a.h) + t * a.W, f.h, e, a.W);
+      if (!a.n) continue;
+      float wn[P::K];
+      P::take_or(wn, a.wn, e, a.W);
+#pragma unroll
+      for (int j = 0; j < P::K; ++j) f.h[j] *= ih * wn[j];
+      P::put(static_cast<T*>(a.n) + t * a.W, f.h, e, a.W);
+    }
+  }
+}
+
+// With q = act(gate) wy scale u, so that gu u = q dH:
+//   sum gu u = sum q dh + (sum q gm - mean(gm m) / rms(h) sum q h) / rms(h)
+// is there before dH is, and all outputs are formed in one pass.
+template <typename T, int V>
+__global__ __launch_bounds__(1024) void k_block_norm_bwd_long(BlockNormArgs a) {
+  using P = Turn<T, V>;
+  constexpr int K = P::K;
+  __shared__ f2 sh[2][16];
+  __shared__ __align__(16) float acc[2][kBlockNormMaxWidth];   // (a thread's own elements, never another's)
+  Sums sums{sh, 0};
+  const int W = a.W;
+  const float invW = 1.0f / static_cast<float>(W);
+  for (int e = P::first(); e < W; e += P::STEP)
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (P::at(e, j) < W) acc[0][P::at(e, j)] = acc[1][P::at(e, j)] = 0.0f;
+  const T* dhp = static_cast<const T*>(a.dh);
+  const T* dnp = static_cast<const T*>(a.dn);
+  auto grads = [&](float* d, float* g, float* wn, int64_t t, int e) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) d[j] = g[j] = 0.0f;
+    if (dhp) P::take(d, dhp + t * W, e, W);
+    if (dnp) P::take(g, dnp + t * W, e, W);
+    P::take_or(wn, a.wn, e, W);
+  };
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const float iy = a.raw ? 1.0f : __builtin_amdgcn_rsqf(fmaf(sums(P::square(a, t), 0.0f).x, invW, a.eps));
+    float hh = 0.0f, gh = 0.0f, qd = 0.0f, qg = 0.0f, qh = 0.0f;
+#pragma unroll 1
+    for (int e = P::first(); e < W; e += P::STEP) {
+      float d[K], g[K], wn[K];
+      grads(d, g, wn, t, e);
+      const P f(a, t, e, iy);
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        const float gm = g[j] * wn[j], q = f.act[j] * f.wz[j] * f.u[j];
+        hh = fmaf(f.h[j], f.h[j], hh);
+        gh = fmaf(gm, f.h[j], gh);
+        qd = fmaf(q, d[j], qd);
+        qg = fmaf(q, gm, qg);
+        qh = fmaf(q, f.h[j], qh);
+      }
+    }
+    const f2 s1 = sums(hh, gh), s2 = sums(qd, qg);
+    const float sqh = sums(qh, 0.0f).x;
+    const float ih = dnp ? __builtin_amdgcn_rsqf(fmaf(s1.x, invW, a.eps)) : 0.0f;
+    const float c = s1.y * invW * ih * ih;
+    const float m = a.raw ? 0.0f : fmaf(ih, fmaf(-c, sqh, s2.y), s2.x) * invW;
+#pragma unroll 1
+    for (int e = P::first(); e < W; e += P::STEP) {
+      float d[K], g[K], wn[K];
+      grads(d, g, wn, t, e);
+      P f(a, t, e, iy);
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        d[j] += ih * fmaf(g[j], wn[j], -f.h[j] * c);
+        const float du = d[j] * f.u[j];
+        if (V > 1 || P::at(e, j) < W) {
+          acc[0][P::at(e, j)] += du * f.act[j];
+          acc[1][P::at(e, j)] += g[j] * f.h[j] * ih;
+        }
+        f.da[j] *= du * f.wz[j];
+        f.h[j] = iy * fmaf(-f.u[j], m, f.act[j] * d[j] * f.wz[j]);
+      }
+      P::put(static_cast<T*>(a.dx) + t * W, d, e, W);
+      if (a.gate) P::put(static_cast<T*>(a.dgate) + t * W, f.da, e, W);
+      P::put(static_cast<T*>(a.dy) + t * W, f.h, e, W);
+    }
+  }
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * 2 * W;
+  for (int e = P::first(); e < W; e += P::STEP)
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (P::at(e, j) < W) {
+        part[P::at(e, j)] = acc[0][P::at(e, j)];
+        part[W + P::at(e, j)] = acc[1][P::at(e, j)];
+      }
+}
+
 // The parts of P and dwn of `nblk` workgroups, joined: 64 columns a workgroup,
 // its sixteen waves every sixteenth part each.
 __global__ __launch_bounds__(1024) void k_block_norm_join(BlockNormArgs a, int nblk) {
@@ -520,9 +714,13 @@ bool vectors(const BlockNormArgs& a) {
   return (a.W | a.ldx | a.ldy | a.ldg) % (16 / static_cast<int>(sizeof(T))) == 0;
 }
 
+// Elements of a thread decide: few stay in registers throughout, of more only the
+// loaded values (gradients), of most nothing (figures at the kernels).
 template <typename T, bool BWD, int V, int E>
 hipError_t run(const BlockNormArgs& a, int grid, int nt, hipStream_t s) {
-  if constexpr (BWD && V < 8 && E == 8) k_block_norm_bwd_lean<T, V, E><<<grid, nt, 0, s>>>(a);
+  if constexpr (BWD && E == 16 && V < 8) k_block_norm_bwd_long<T, V><<<grid, 1024, 0, s>>>(a);
+  else if constexpr (E == 16 && V == 1) k_block_norm_long<T, V><<<grid, 1024, 0, s>>>(a);
+  else if constexpr (BWD && (V == 8 ? E == 16 : E == 8)) k_block_norm_bwd_lean<T, V, E><<<grid, nt, 0, s>>>(a);
   else if constexpr (BWD) k_block_norm_bwd<T, V, E><<<grid, nt, 0, s>>>(a);
   else k_block_norm<T, V, E><<<grid, nt, 0, s>>>(a);
   return hipGetLastError();

@@ -145,6 +145,32 @@ def test_equal_bits_in_place_and_replayed():
         assert all(torch.equal(gd[n], ed[n]) for n in gd), k
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("case", [(600, 5473, "silu", False, 0, "hn"), (300, 6001, "sigmoid", True, 0, "n"),
+                                  (300, 8192, "silu", False, 0, "h"), (530, 9001, "silu", False, 0, "hn"),
+                                  (290, 12345, None, False, 21, "n"), (270, 8208, "linear", True, 0, "h"),
+                                  (270, 16000, "silu", False, 0, "hn"), (3, 16383, "silu", False, 0, "hn")])
+def test_wide_rows_several_to_a_workgroup(case, dtype):
+    T, W, act, raw, cut, given = case
+    test_block_norm_and_gradients((T, W, act, raw, True, cut, given), dtype)
+
+
+@pytest.mark.parametrize("W", [4097, 9001, 12352])
+def test_wide_rows_in_place(W):
+    for dtype in (F32, BF16):
+        x, y, gate, (wy, sc, wn), _, _ = _inputs(540, W, dtype, "silu", True, 0, W)
+        h, n = m3.block_norm(x, y, gate, wy, sc, wn, flags=m3.M3_GATE_SILU)
+        dims = m3.m3_block_dims(540, W, m3.dtype_code(dtype), m3.M3_GATE_SILU, 1e-6, 0, 0, 0)
+        p = lambda t: ctypes.c_void_p(t.data_ptr())
+        for over in (0, 1):
+            ins = [x.clone(), y.clone()]
+            n2 = torch.empty_like(n)
+            assert m3.library().m3_block_norm(ctypes.byref(dims), p(ins[0]), p(ins[1]), p(gate), p(wy), p(sc), p(wn),
+                                              p(ins[over]), p(n2), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+            torch.cuda.synchronize()
+            assert torch.equal(ins[over], h) and torch.equal(n2, n) and torch.equal(ins[1 - over], (y, x)[over])
+
+
 def test_two_streams_and_refused_tensors():
     runs = []
     for seed in (11, 12):

@@ -404,6 +404,29 @@ def test_offsets_that_pass_32_bits():
     assert all(torch.equal(da[n], dc[n]) for n in da)
 
 
+def test_states_that_pass_32_bits():
+    """What is saved, and the gradients of the states, past 2^31 elements: the last sequence of many against a
+    call of its own, whose sums are grouped by segments (so: near, not equal)."""
+    B, T, H, dk, dv = 65, 4096, 32, 128, 64
+    g = torch.Generator(device="cuda").manual_seed(90)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=BF16)
+    unit = lambda t: torch.nn.functional.normalize(t, dim=-1)
+    q, k, v, do = unit(n(B, T, H, dk)), unit(n(B, T, H, dk)), n(B, T, H, dv), n(B, T, H, dv)
+    gt, b = -torch.nn.functional.softplus(n(B, T, H) - 3), torch.sigmoid(n(B, T, H))
+    dhT = torch.randn(B, H, dk, dv, generator=g, device="cuda")
+    o, hT, st = m3.delta_scan(q, k, v, gt, b, want_states=True)
+    assert st.numel() > 2 ** 31
+    d = m3.delta_scan_backward(q, k, v, gt, b, do, st, h0=dhT, dhT=dhT)   # (h0: only that its gradient is wanted)
+    x = [t[-1:].contiguous() for t in (q, k, v, gt, b, do, dhT)]
+    o1, hT1, st1 = m3.delta_scan(*x[:5], want_states=True)
+    d1 = m3.delta_scan_backward(*x[:5], x[5], st1, h0=x[6], dhT=x[6])
+    pairs = dict(o=(o, o1), hT=(hT, hT1), **{i: (d[i], d1[i]) for i in ("q", "k", "v", "g", "beta", "h0")})
+    for name, (many, one) in pairs.items():
+        e = float((many[-1].double() - one[0].double()).norm() / one.double().norm())
+        say(f"  {name}: {e:.1e}")
+        assert e <= (1e-5 if one.dtype == F32 else 2 * ref.U[BF16]), name
+
+
 def test_refused_tensors():
     q, k, v, g, b, h0, do, dhT = _inputs(10, 1, 2, 64, 64, BF16, 3)
     cu = torch.tensor([0, 10], dtype=torch.int32).cuda()

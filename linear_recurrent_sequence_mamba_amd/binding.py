@@ -609,7 +609,7 @@ def decode_tokens(h, x, B, C, dt, A, lam, theta, x_prev=None, B_prev=None,
 
 # ---------------------------------------------------------------------------
 # the other layers of a hybrid stack: gated recurrence, q/k norms with rotary
-# positions, causal attention
+# positions, causal attention, gated delta rule, norms around a block
 class _Switch:
     """The device of a call's tensors as the current one and, if given, the
     stream as the current one, so that what a helper allocates belongs to the

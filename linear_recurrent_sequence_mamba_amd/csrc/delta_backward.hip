@@ -268,32 +268,31 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
 // first and its products do not overlap with another's; two (128 registers) spill:
 // 400 us.  The next slab's rows are asked for as soon as the last one's are split.
 // AHEAD: a workgroup goes on to another chunk and head, whose first rows it asks
-// for before the products over tokens (without it 230 us); with 128 value
-// channels, several value heads or fp32 the registers for it are not there.
-template <typename T, int DK>
+// for before the products over tokens (without it 230 us); with 128 value channels
+// or fp32 the registers for it are not there (a packed batch of 8192 tokens, 16
+// heads on 8 of 128 x 128: 235 us with it, 219 without).
+template <typename T, int DK, bool KEEP>   // KEEP: K and Q stay for all heads
 struct GradTiles {
   using M = Rows64<64>;
   static constexpr int NI = DeltaParts<T>::IN, NO = DeltaParts<T>::OUT;
   static constexpr int ONE = (NI + 2 * NO) * M::PLANE;
-  static constexpr int TWO = 2 * NI * Rows64<DK>::PLANE + 2 * NO * M::PLANE;
-  static constexpr int BYTES = ONE > TWO ? ONE : TWO;
+  static constexpr int KQ = 2 * NI * Rows64<DK>::PLANE, TWO = KQ + 2 * NO * M::PLANE;
+  static constexpr int BYTES = KEEP ? KQ + ONE : ONE > TWO ? ONE : TWO;
 };
 
 // tiles (i, j) of the lower half, n = 0 .. 11
 __device__ __forceinline__ constexpr int tile_i(int n) { return n < 4 ? n >> 1 : 2 + ((n - 4) >> 2); }
 __device__ __forceinline__ constexpr int tile_j(int n) { return n < 4 ? n & 1 : (n - 4) & 3; }
 
-template <typename T, int DV, bool MULTI>
-constexpr bool grads_ahead() { return !MULTI && DV == 64 && sizeof(T) == 2; }
-
 template <typename T, int DK, int DV, bool MULTI>
 __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(DeltaArgs a) {
   using X = Rows64<DK>;
   using M = Rows64<64>;
-  using G = GradTiles<T, DK>;
+  using G = GradTiles<T, DK, MULTI && sizeof(T) == 2>;
   constexpr int NI = G::NI, NO = G::NO, NW = DK / 16, NT = 64 * NW, NTILE = (12 + NW - 1) / NW, VN = 512 / NT;
-  // where there is room, the sums over heads wait in LDS (in registers they spill)
-  constexpr bool PARK = MULTI && sizeof(T) == 2, AHEAD = grads_ahead<T, DV, MULTI>();
+  // where there is room, the sums over heads wait in LDS (in registers they spill),
+  // and K and Q stay there
+  constexpr bool PARK = MULTI && sizeof(T) == 2, AHEAD = DV == 64 && sizeof(T) == 2;
   __shared__ float sAcc[PARK ? 32 : 1][PARK ? NT : 1];
   __shared__ __align__(16) char smem[G::BYTES];
   __shared__ __align__(16) float sGate[kDeltaGates];
@@ -310,8 +309,8 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
   const typename X::Lane xl(lane);
   const M::Lane ml(lane);
   const int ldo = a.Hv * DV;
-  char *sO = smem, *sR = smem + NI * M::PLANE, *sUt = sR + NO * M::PLANE;
-  char *sK = smem, *sQ = smem + NI * X::PLANE, *sF = smem + 2 * NI * X::PLANE, *sN = sF + NO * M::PLANE;
+  char *sO = smem + (PARK ? G::KQ : 0), *sR = sO + NI * M::PLANE, *sUt = sR + NO * M::PLANE;
+  char *sK = smem, *sQ = smem + NI * X::PLANE, *sF = smem + G::KQ, *sN = sF + NO * M::PLANE;
   const int wcol = X::tile_col(w, lane);   // the wave's channels in K and Q
   const int dkr = 32 * (w >> 1) + 8 * (r >> 2) + 4 * (w & 1) + (r & 3);   // the lane's channel of q and k
   const int64_t dd = static_cast<int64_t>(DK) * DV;
@@ -342,7 +341,8 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
   auto head_of = [&](int n, int h) { return static_cast<int64_t>(n / a.Hk) * a.Hv + h; };
   if constexpr (AHEAD) {
     const DeltaSlot sl(a, item / a.Hk, lane);
-    fetch_first(sl, head_of(item, item % a.Hk), item % a.Hk, threadIdx.x, sat0);
+    const int h = item % a.Hk * group;
+    fetch_first(sl, head_of(item, h), h, threadIdx.x, sat0);
   }
   for (;;) {
     const int hk = item % a.Hk, slot = item / a.Hk;
@@ -354,6 +354,17 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
     f4 dq[4], dk[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) dq[i] = dk[i] = f4{0, 0, 0, 0};
+
+    auto fetch_kq = [&](Stage<T, DK, NT>& k, Stage<T, DK, NT>& q, int tid) __attribute__((always_inline)) {
+      k.load(static_cast<const T*>(a.k) + sl.row0 * a.ldk + hk * DK, a.ldk, sl.n, tid);
+      q.load(static_cast<const T*>(a.q) + sl.row0 * a.ldq + hk * DK, a.ldq, sl.n, tid);
+    };
+    if constexpr (PARK) {
+      Stage<T, DK, NT> k, q;
+      fetch_kq(k, q, threadIdx.x);
+      k.store(sK);
+      q.store(sQ);
+    }
 
     for (int h = hk * group; h < (hk + 1) * group; ++h) {
       // (opaque: addresses are made again for each head, not kept over the loop)
@@ -397,8 +408,7 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
         if (c0 + 64 < DV) {
           fetch(sl, m, h, c0 + 64, tid);
         } else {
-          stK.load(static_cast<const T*>(a.k) + sl.row0 * a.ldk + hk * DK, a.ldk, sl.n, tid);
-          stQ.load(static_cast<const T*>(a.q) + sl.row0 * a.ldq + hk * DK, a.ldq, sl.n, tid);
+          if constexpr (!PARK) fetch_kq(stK, stQ, tid);
         }
         tiles_barrier();
 #pragma unroll
@@ -455,12 +465,16 @@ __global__ __launch_bounds__(4 * DK, sizeof(T) == 2 ? 2 : 1) void k_delta_grads(
       }
       both = group_sum<64>(both);
       tiles_barrier();
-      stK.store(sK, tid);
-      stQ.store(sQ, tid);
-      tiles_barrier();
+      if constexpr (!PARK) {
+        stK.store(sK, tid);
+        stQ.store(sQ, tid);
+        tiles_barrier();
+      }
       if constexpr (AHEAD) {
-        const DeltaSlot nsl(a, next / a.Hk, lane);
-        fetch_first(nsl, head_of(next, next % a.Hk), next % a.Hk, tid, sat);
+        const bool same = MULTI && h + 1 < (hk + 1) * group;
+        const int n = same ? item : next, nh = same ? h + 1 : next % a.Hk * group;
+        const DeltaSlot nsl(a, n / a.Hk, lane);
+        fetch_first(nsl, head_of(n, nh), nh, tid, sat);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -654,8 +668,8 @@ hipError_t run_backward(const DeltaArgs& a, hipStream_t s) {
     e = run_back_chain<T, DK, 4>(a, s);
   if (e != hipSuccess) return e;
   const int64_t items = static_cast<int64_t>(a.nslot) * a.Hk;
-  const bool ahead = a.Dv == 64 && a.Hv == a.Hk && grads_ahead<T, 64, false>();
-  constexpr int most = 256 * 128 / DK;   // as many as are resident, of 4 or 8 waves with 256 registers
+  const bool multi = a.Hv != a.Hk, ahead = a.Dv == 64 && sizeof(T) == 2;
+  const int most = 256 * (multi || DK == 128 ? 1 : 2);   // as many as are resident
   const unsigned grid = static_cast<unsigned>(ahead && items > most ? most : items);
   if (a.Dv == 64) {
     if (a.Hv == a.Hk) k_delta_grads<T, DK, 64, false><<<grid, 4 * DK, 0, s>>>(a);

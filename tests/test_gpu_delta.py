@@ -205,11 +205,12 @@ def test_dense_prompts_in_segments(shape):
                 _check(n, got[n], val, bound)
 
 
+@pytest.mark.parametrize("heads,each", [(40, 1), (35, 2)])
 @pytest.mark.parametrize("dk", [64, 128])
-def test_more_chunks_and_heads_than_workgroups(dk):
+def test_more_chunks_and_heads_than_workgroups(dk, heads, each):
     """Gradients whose workgroups go on from one chunk and head to the next, past slots that no chunk takes."""
-    lengths, heads, dv = [700, 0, 0, 64, 1, 299], 40, 64
-    q, k, v, g, b, h0, do, dhT = _inputs(sum(lengths), heads, heads, dk, dv, BF16, 70 + dk, False, len(lengths))
+    lengths, dv = [700, 0, 0, 64, 1, 299], 64
+    q, k, v, g, b, h0, do, dhT = _inputs(sum(lengths), heads, heads * each, dk, dv, BF16, 70 + dk, False, len(lengths))
     off = [0]
     for n in lengths:
         off.append(off[-1] + n)
@@ -221,11 +222,11 @@ def test_more_chunks_and_heads_than_workgroups(dk):
             assert torch.equal(d["h0"][s], dhT[s])
             continue
         c = slice(off[s], off[s + 1])
-        for h in (0, 7, 23, 39):
-            x = slice(h, h + 1)
-            want = delta_ref.check(q[c, x], k[c, x], v[c, x], g[c, x], b[c, x], h0[s, x], dk ** -0.5, BF16, do[c, x],
+        for h in (0, 7, 23, heads - 1):
+            y, x = slice(h, h + 1), slice(h * each, (h + 1) * each)
+            want = delta_ref.check(q[c, y], k[c, y], v[c, x], g[c, x], b[c, x], h0[s, x], dk ** -0.5, BF16, do[c, x],
                                    dhT[s, x])
-            got = {"o": o[c, x], "hT": hT[s, x], "dq": d["q"][c, x], "dk": d["k"][c, x], "dv": d["v"][c, x],
+            got = {"o": o[c, x], "hT": hT[s, x], "dq": d["q"][c, y], "dk": d["k"][c, y], "dv": d["v"][c, x],
                    "dg": d["g"][c, x], "dbeta": d["beta"][c, x], "dh0": d["h0"][s, x]}
             for name, (val, bound) in want.items():
                 _check(f"{name} of sequence {s}, head {h}", got[name], val, bound)

@@ -54,6 +54,8 @@ DeltaPlan delta_plan(int B, int T, int Hv, int Dk, int Dv, bool packed, bool bac
 size_t delta_segment_bytes(const DeltaPlan& p, int Hv, int Dk, int Dv);
 void delta_carve_segments(DeltaArgs& a, const DeltaPlan& p, void* ws);
 
+// segments that may not be their sequences' last, at most
+inline int64_t delta_inner(const DeltaArgs& a) { return a.cu ? a.T >> (6 + a.lseg) : a.nseg - a.B; }
 inline int64_t delta_state_floats(int Dk, int Dv) {
   return static_cast<int64_t>(Dk + kDeltaChunk) * Dv + kDeltaMatrix + kDeltaGates;
 }

@@ -247,10 +247,10 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
   __shared__ __align__(16) char smem[NBUF * ChainTiles<T, DK, 64 * NW, true>::BUF];
   const int nv = a.Dv / (16 * NW), nsl = nv + DK / (16 * NW);
   const int n = blockIdx.x / nsl, slice = blockIdx.x % nsl;
-  const DeltaSeg seg(a, n / a.Hv, threadIdx.x & 63);
-  if (seg.s < 0 || seg.j == 0) return;
-  if (slice < nv) back_chain<T, DK, NW, NBUF, false>(a, seg, n / a.Hv, n % a.Hv, slice, smem);
-  else if (!seg.last) chain<T, DK, NW, NBUF, kMapsT>(a, seg, n / a.Hv, n % a.Hv, slice - nv, smem);
+  const DeltaSeg seg(a, n / a.Hv, threadIdx.x & 63, true);
+  if (seg.s < 0) return;
+  if (slice < nv) back_chain<T, DK, NW, NBUF, false>(a, seg, seg.slot, n % a.Hv, slice, smem);
+  else if (!seg.last) chain<T, DK, NW, NBUF, kMapsT>(a, seg, seg.slot, n % a.Hv, slice - nv, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -647,7 +647,7 @@ hipError_t run_back_chain(const DeltaArgs& a, hipStream_t s) {
   const int64_t heads = static_cast<int64_t>(a.nseg) * a.Hv;
   if (a.lseg < 30) {
     k_delta_back_segments<T, DK, NW, NBUF>
-        <<<static_cast<unsigned>(heads * ((a.Dv + DK) / (16 * NW))), 64 * NW, 0, s>>>(a);
+        <<<static_cast<unsigned>(delta_inner(a) * a.Hv * ((a.Dv + DK) / (16 * NW))), 64 * NW, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_delta_join<DK, DeltaParts<T>::OUT, true>

@@ -276,28 +276,69 @@ struct DeltaParts {
   static constexpr int OUT = sizeof(T) == 2 ? 2 : 3;
 };
 
+// the last sequence that starts at row x or before it, -1: none
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int S, int T, int x, int lane) {
+  int lo = 0, n = S;
+  for (;;) {
+    const int step = (n + 63) / 64, s = lo + lane * step;
+    const int cnt = __popcll(__ballot(s < lo + n && clamp_row(cu[s < S ? s : S - 1], T) <= x));
+    if (cnt == 0) return -1;
+    const int at = lo + (cnt - 1) * step;
+    n = min(step, lo + n - at);
+    lo = at;
+    if (step == 1) return __builtin_amdgcn_readfirstlane(lo);
+  }
+}
+
 // A segment of a sequence's chunks, by its slot; s = -1: the slot has none.  An
 // empty sequence has one segment without chunks.
 struct DeltaSeg {
+  int slot;
   int s, j;         // sequence, segment of it
   int c0, nch;      // its first chunk, its chunks
   int len, slot0;   // the sequence's rows and first chunk slot
   bool last;        // the sequence's last segment
   int64_t row0;     // the sequence's first row
-  __device__ __forceinline__ DeltaSeg(const DeltaArgs& a, int slot, int lane) {
+  __device__ __forceinline__ DeltaSeg(const DeltaArgs& a, int n, int lane) : slot(n) {
     if (a.cu) {
       const Slot x = slot_of(a.cu, a.B, a.T, min(31, 6 + a.lseg), slot, lane);
       s = x.s;
       j = x.tile;
-      if (s < 0) return;
-      const int b = clamp_row(a.cu[s], a.T), e = clamp_row(a.cu[s + 1], a.T);
-      row0 = b;
-      len = max(0, e - b);
-      slot0 = b / kDeltaChunk + s;
+      if (s >= 0) fill(a, clamp_row(a.cu[s], a.T));
     } else {
       const int per = a.nseg / a.B;
       s = slot / per;
       j = slot - s * per;
+      fill(a, 0);
+    }
+  }
+  // The n-th segment that is not its sequence's last (next: the one behind it).
+  // Packed: the rows of such a segment, counted from one, have one multiple of its
+  // length among them, so no more than T / length of them are looked for.
+  __device__ __forceinline__ DeltaSeg(const DeltaArgs& a, int n, int lane, bool next) {
+    if (a.cu) {
+      const int lb = 6 + a.lseg, x = (n + 1) << lb;
+      s = sequence_of(a.cu, a.B, a.T, x - 1, lane);
+      if (s < 0) return;
+      const int b = clamp_row(a.cu[s], a.T);
+      j = ((x - 1 - b) >> lb) + next;
+      slot = (b >> lb) + s + j;
+      fill(a, b);
+      if (!next && last) s = -1;
+    } else {
+      const int per = a.nseg / a.B;
+      s = n / (per - 1);
+      j = n - s * (per - 1) + next;
+      slot = s * per + j;
+      fill(a, 0);
+    }
+  }
+  __device__ __forceinline__ void fill(const DeltaArgs& a, int b) {
+    if (a.cu) {
+      row0 = b;
+      len = max(0, clamp_row(a.cu[s + 1], a.T) - b);
+      slot0 = b / kDeltaChunk + s;
+    } else {
       row0 = static_cast<int64_t>(s) * a.T;
       len = a.T;
       slot0 = s * ((a.T + kDeltaChunk - 1) / kDeltaChunk);

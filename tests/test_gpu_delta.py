@@ -96,7 +96,8 @@ def test_packed_scan_and_gradients(case, dtype):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_long_sequences_in_segments(dtype):
     """Long enough for several segments of a sequence, a short one and an empty one beside it."""
-    for lengths, hk, hv, dk, dv in (([2500, 0, 70, 1200], 1, 2, 64, 64), ([2243], 1, 1, 128, 128)):
+    for lengths, hk, hv, dk, dv in (([2500, 0, 70, 1200], 1, 2, 64, 64), ([2243], 1, 1, 128, 128),
+                                    ([20] * 7 + [0, 3000, 1, 64] + [33] * 5, 1, 1, 64, 128)):
         rows = sum(lengths)
         q, k, v, g, b, h0, do, dhT = _inputs(rows, hk, hv, dk, dv, dtype, rows, False, len(lengths))
         g = (g.float() * 0.05).to(dtype)   # what is at the start is still there at the end

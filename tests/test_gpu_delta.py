@@ -300,6 +300,30 @@ def test_rows_behind_and_between_are_left():
     _check("o", o[10:40], *want["o"])
 
 
+def test_batches_without_rows_and_offsets_that_do_not_rise():
+    """Sequences that are all empty leave every row and pass their states on; offsets that fall, are negative or
+    behind the rows keep within the buffers (their results are unspecified), and the next call is right."""
+    T, H = 3000, 2
+    q, k, v, g, b, h0, do, dhT = _inputs(T, H, H, 64, 64, BF16, 17, False, 5)
+    cu = lambda *o: torch.tensor(o, dtype=torch.int32).cuda()
+
+    def run(c):
+        o, hT, st = m3.delta_scan(q, k, v, g, b, h0=h0, cu_seqlens=c, want_states=True)
+        return o, hT, m3.delta_scan_backward(q, k, v, g, b, do, st, h0=h0, dhT=dhT, cu_seqlens=c)
+
+    for at in (0, 64, T):
+        _, hT, d = run(cu(*[at] * 6))
+        assert torch.equal(hT, h0) and torch.equal(d["h0"], dhT)
+    good = cu(0, 1300, 1300, 2800, 2900, T)
+    want = run(good)
+    for bad in ((2000, 100, 2900, 50, 3000, 0), (-7, 5000, -1, 2 ** 31 - 1, -2 ** 31, 3000), (0, 3000, 0, 3000, 0, 3000)):
+        run(cu(*bad))
+        torch.cuda.synchronize()
+    got = run(good)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert all(torch.equal(got[2][n], want[2][n]) for n in want[2])
+
+
 def test_nan_stays_in_its_sequence_and_head():
     lengths = [70, 130, 64]
     q, k, v, g, b, h0, do, dhT = _inputs(264, 2, 4, 64, 64, BF16, 7, False, 3)

@@ -286,7 +286,7 @@ hipError_t run_chain(const DeltaArgs& a, bool split, hipStream_t s) {
         <<<static_cast<unsigned>(delta_inner(a) * a.Hv * ((a.Dv + DK) / (16 * NW))), 64 * NW, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    k_delta_join<DK, DeltaParts<T>::OUT, false>
+    k_delta_join<DK, false>
         <<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hv * (a.Dv / 16)), 2 * DK, 0, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -371,7 +371,6 @@ DeltaPlan delta_plan(int B, int T, int Hv, int Dk, int Dv, bool packed, bool bac
 }
 
 size_t delta_segment_bytes(const DeltaPlan& p, int Hv, int Dk, int Dv) {
-  // (maps of two parts take no less than their room for three)
   return p.split ? (static_cast<size_t>(Dk) * (sizeof(float) * Dv + 3 * sizeof(uint16_t) * Dk) + sizeof(float) * 4) * p.nseg * Hv : 0;
 }
 

@@ -650,7 +650,7 @@ hipError_t run_back_chain(const DeltaArgs& a, hipStream_t s) {
         <<<static_cast<unsigned>(delta_inner(a) * a.Hv * ((a.Dv + DK) / (16 * NW))), 64 * NW, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    k_delta_join<DK, DeltaParts<T>::OUT, true>
+    k_delta_join<DK, true>
         <<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hv * (a.Dv / 16)), 2 * DK, 0, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -18,8 +18,10 @@ namespace {
 // the segments, and the segments then run at once.
 //
 // Parts (bf16): what reaches the state has three, so that it keeps fp32's
-// accuracy; P and U, which only reach outputs in bf16, two; a map, whose decay
-// is kept apart in fp32, two (2^-17 of what the segment's keys take out).
+// accuracy, a map and the state that it is applied to among it: where a segment's
+// keys overwrite the state, d S + F S cancels (with two parts a state behind slow
+// decays is off by 2.7e-6 of itself, with three by 3e-7).  P and U, which only reach
+// outputs in bf16, have two.
 //
 // With room for two of a chunk's tiles (NBUF = 2) the next chunk's are written
 // while waves still read this one's, and one barrier a chunk is enough.
@@ -59,7 +61,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
   constexpr bool FULL = MODE == kFull, MAPS = MODE == kMaps || MODE == kMapsT;
   constexpr int NT = 64 * NW, KS = DK / 32, DT = DK / 16;
   using Tiles = ChainTiles<T, DK, NT, FULL>;
-  constexpr int NI = Tiles::NI, NO = Tiles::NO, NS = MAPS ? NO : 3;
+  constexpr int NI = Tiles::NI, NO = Tiles::NO, NS = 3;
   constexpr int BK = Tiles::BK, BQ = Tiles::BQ, BM = Tiles::BM, BUF = Tiles::BUF;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4, hk = h / (a.Hv / a.Hk);
@@ -317,9 +319,9 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
 // in its registers, and the waves exchange the parts of the state in LDS.  1.4 us
 // a map of 128 x 128, bf16 (a wave for all rows, with maps in LDS: 2.6; it reads
 // four times as many operands in a row).
-template <int DK, int NP, bool BACK>
+template <int DK, bool BACK>
 __global__ __launch_bounds__(2 * DK, 1) void k_delta_join(DeltaArgs a) {
-  constexpr int KS = DK / 32, DT = DK / 16;
+  constexpr int KS = DK / 32, DT = DK / 16, NP = 3;
   __shared__ bh8 sS[2][KS][NP][64];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // (a head's workgroups on one XCD where the heads are a multiple of 8, as they

@@ -30,17 +30,19 @@ struct DeltaArgs {
   int64_t ldpm;                       // ldpm on (in `states` where those are saved)
   float* after;                       // backward: gradients of the state behind a chunk [slots, Hv, Dk, Dv]
   float* dr;                          // backward: those of R [slots, Hv, 64, Dv]
-  float* ends;                        // segments' ends from a zero state, then the states before
-                                      // them, in the order of results [segment slots, Hv, Dv / 16,
-                                      // Dk / 16, 64, 4]
-  uint16_t* maps;                     // segments' maps of a state less their decay, in parts and in
-                                      // the order of operands [segment slots, Hv, parts, Dk / 16,
-                                      // Dk / 32, 64, 8]
-  float* decays;                      // segments' decays [segment slots, Hv]
+  // (of segments that are not their sequences' last, DeltaSeg's n-th at n)
+  float* ends;                        // their ends from a zero state, then the states behind them, in
+                                      // the order of results [inner, Hv, Dv / 16, Dk / 16, 64, 4]
+  uint16_t* maps;                     // their maps of a state less their decay, in parts and in the
+                                      // order of operands [inner, Hv, parts, Dk / 16, Dk / 32, 64, 8]
+  float* decays;                      // their decays [inner, Hv]
+  float* firsts;                      // scan: the states before sequences of several segments, as
+                                      // `ends`, DeltaSeg's place() [min(B, inner), Hv, ..]
   int64_t ldq, ldk, ldv, ldg, ldb;
   int B, T, Hk, Hv, Dk, Dv;           // B sequences of T rows (packed: of T rows together)
   int nslot;
   int lseg, nseg;                     // log2 of a segment's chunks, segment slots
+  int inner;                          // segments that may not be their sequences' last, at most
   float scale;
 };
 
@@ -49,13 +51,12 @@ struct DeltaPlan {
   int lseg;
   int64_t nseg;   // slots of segments
   bool split;     // some sequence may have more than one
+  int64_t inner;  // segments that may not be their sequences' last, at most
 };
 DeltaPlan delta_plan(int B, int T, int Hv, int Dk, int Dv, bool packed, bool back);
-size_t delta_segment_bytes(const DeltaPlan& p, int Hv, int Dk, int Dv);
-void delta_carve_segments(DeltaArgs& a, const DeltaPlan& p, void* ws);
+size_t delta_segment_bytes(const DeltaPlan& p, int B, int Hv, int Dk, int Dv, bool back);
+void delta_carve_segments(DeltaArgs& a, const DeltaPlan& p, void* ws, bool back);
 
-// segments that may not be their sequences' last, at most
-inline int64_t delta_inner(const DeltaArgs& a) { return a.cu ? a.T >> (6 + a.lseg) : a.nseg - a.B; }
 inline int64_t delta_state_floats(int Dk, int Dv) {
   return static_cast<int64_t>(Dk + kDeltaChunk) * Dv + kDeltaMatrix + kDeltaGates;
 }

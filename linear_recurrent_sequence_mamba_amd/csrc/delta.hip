@@ -174,7 +174,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_chain
   __shared__ __align__(16) char smem[NBUF * ChainTiles<T, DK, 64 * NW, true>::BUF];
   const int nsl = a.Dv / (16 * NW), n = blockIdx.x / nsl;
   const DeltaSeg seg(a, n / a.Hv, threadIdx.x & 63);
-  if (seg.s >= 0) chain<T, DK, NW, NBUF, kFull>(a, seg, n / a.Hv, n % a.Hv, blockIdx.x % nsl, smem);
+  if (seg.s >= 0) chain<T, DK, NW, NBUF, kFull>(a, seg, n % a.Hv, blockIdx.x % nsl, smem);
 }
 
 // E and F of all segments but the last, F of none before the second
@@ -185,8 +185,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_segme
   const int n = blockIdx.x / nsl, slice = blockIdx.x % nsl;
   const DeltaSeg seg(a, n / a.Hv, threadIdx.x & 63, false);
   if (seg.s < 0) return;
-  if (slice < nv) chain<T, DK, NW, NBUF, kEnds>(a, seg, seg.slot, n % a.Hv, slice, smem);
-  else if (seg.j > 0) chain<T, DK, NW, NBUF, kMaps>(a, seg, seg.slot, n % a.Hv, slice - nv, smem);
+  if (slice < nv) chain<T, DK, NW, NBUF, kEnds>(a, seg, n % a.Hv, slice, smem);
+  else if (seg.j > 0) chain<T, DK, NW, NBUF, kMaps>(a, seg, n % a.Hv, slice - nv, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -283,7 +283,7 @@ hipError_t run_chain(const DeltaArgs& a, bool split, hipStream_t s) {
   const int64_t heads = static_cast<int64_t>(a.nseg) * a.Hv;
   if (split) {
     k_delta_segments<T, DK, NW, NBUF>
-        <<<static_cast<unsigned>(delta_inner(a) * a.Hv * ((a.Dv + DK) / (16 * NW))), 64 * NW, 0, s>>>(a);
+        <<<static_cast<unsigned>(static_cast<int64_t>(a.inner) * a.Hv * ((a.Dv + DK) / (16 * NW))), 64 * NW, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_delta_join<DK, false>
@@ -347,7 +347,7 @@ DeltaPlan delta_plan(int B, int T, int Hv, int Dk, int Dv, bool packed, bool bac
   const double rows = packed ? T : static_cast<double>(B) * T;
   const double longest = (packed && B > 1 ? 2.0 * T / B : T) / kDeltaChunk, cols = Hv * (Dv / 16.0);
   auto rounds = [](double waves) { return waves > 2048 ? waves / 2048 : 1.0; };
-  DeltaPlan p{30, B, false};
+  DeltaPlan p{30, B, false, 0};
   double best = 0.75 * longest * rounds(B * cols);
   for (int l = 3; l < 10 && longest / (1 << l) >= 2; ++l) {
     const double n = rows / (kDeltaChunk << l) + (packed ? B : 0);
@@ -355,44 +355,52 @@ DeltaPlan delta_plan(int B, int T, int Hv, int Dk, int Dv, bool packed, bool bac
                         0.2 * longest / (1 << l);
     if (cost < best) {
       best = cost;
-      p = DeltaPlan{l, 0, true};
+      p = DeltaPlan{l, 0, true, 0};
     }
   }
   if (!p.split && packed && B > 1) {
     const DeltaPlan one = delta_plan(1, T, Hv, Dk, Dv, false, back);
     int l = one.lseg;
     while (one.split && l < 30 && static_cast<double>(1 << l) < longest) ++l;
-    if (one.split && (static_cast<int64_t>(T) >> (6 + l)) >= 4) p = DeltaPlan{l, 0, true};
+    if (one.split && (static_cast<int64_t>(T) >> (6 + l)) >= 4) p = DeltaPlan{l, 0, true, 0};
   }
-  if (p.split)
+  if (p.split) {
     p.nseg = packed ? (static_cast<int64_t>(T) >> (6 + p.lseg)) + B
                     : B * ((static_cast<int64_t>(T) + (kDeltaChunk << p.lseg) - 1) / (kDeltaChunk << p.lseg));
+    p.inner = p.nseg - B;
+  }
   return p;
 }
 
-size_t delta_segment_bytes(const DeltaPlan& p, int Hv, int Dk, int Dv) {
-  return p.split ? (static_cast<size_t>(Dk) * (sizeof(float) * Dv + 3 * sizeof(uint16_t) * Dk) + sizeof(float) * 4) * p.nseg * Hv : 0;
+// A state, a map and a decay of each segment that may not be its sequence's last,
+// and in the scan the states before sequences of several.
+size_t delta_segment_bytes(const DeltaPlan& p, int B, int Hv, int Dk, int Dv, bool back) {
+  const size_t inner = p.inner, firsts = back ? 0 : B < p.inner ? B : p.inner, state = static_cast<size_t>(Dk) * Dv;
+  return Hv * (sizeof(float) * (state * (inner + firsts) + inner) + 3 * sizeof(uint16_t) * Dk * Dk * inner);
 }
 
-void delta_carve_segments(DeltaArgs& a, const DeltaPlan& p, void* ws) {
+void delta_carve_segments(DeltaArgs& a, const DeltaPlan& p, void* ws, bool back) {
   a.lseg = p.lseg;
   a.nseg = static_cast<int>(p.nseg);
   a.nslot = static_cast<int>(delta_slots(a.B, a.T, a.cu != nullptr));
+  a.inner = static_cast<int>(p.inner);
+  const size_t heads = static_cast<size_t>(a.inner) * a.Hv;
   a.ends = static_cast<float*>(ws);
-  a.maps = reinterpret_cast<uint16_t*>(a.ends + static_cast<size_t>(a.Dk) * a.Dv * a.nseg * a.Hv);
-  a.decays = reinterpret_cast<float*>(a.maps + static_cast<size_t>(3) * a.Dk * a.Dk * a.nseg * a.Hv);
+  a.maps = reinterpret_cast<uint16_t*>(a.ends + a.Dk * a.Dv * heads);
+  a.firsts = reinterpret_cast<float*>(a.maps + 3 * a.Dk * a.Dk * heads);   // (backward: none)
+  a.decays = a.firsts + static_cast<size_t>(a.Dk) * a.Dv * (back ? 0 : a.B < a.inner ? a.B : a.inner) * a.Hv;
 }
 
 size_t delta_workspace_bytes(int B, int T, int Hv, int Dk, int Dv, bool packed) {
   const size_t chunks = static_cast<size_t>(kDeltaMatrix + kDeltaGates) * delta_slots(B, T, packed) * Hv;
-  return sizeof(float) * chunks + delta_segment_bytes(delta_plan(B, T, Hv, Dk, Dv, packed, false), Hv, Dk, Dv);
+  return sizeof(float) * chunks + delta_segment_bytes(delta_plan(B, T, Hv, Dk, Dv, packed, false), B, Hv, Dk, Dv, false);
 }
 
 void delta_carve(DeltaArgs& a, void* ws) {
   a.pm = static_cast<float*>(ws);
   a.ldpm = kDeltaMatrix + kDeltaGates;
   delta_carve_segments(a, delta_plan(a.B, a.T, a.Hv, a.Dk, a.Dv, a.cu != nullptr, false),
-                       a.pm + static_cast<size_t>(a.ldpm) * delta_slots(a.B, a.T, a.cu != nullptr) * a.Hv);
+                       a.pm + static_cast<size_t>(a.ldpm) * delta_slots(a.B, a.T, a.cu != nullptr) * a.Hv, false);
   if (a.states) {
     a.ldpm = delta_state_floats(a.Dk, a.Dv);
     a.pm = a.states + static_cast<size_t>(a.Dk + kDeltaChunk) * a.Dv;

@@ -28,7 +28,7 @@ namespace {
 // behind it (the last segment: from dhT).  Bound as the scan's: 5.5 us a chunk
 // of 128 x 64.
 template <typename T, int DK, int NW, int NBUF, bool FULL>
-__device__ __forceinline__ void back_chain(const DeltaArgs& a, const DeltaSeg& seg, int slot, int h, int slice, char* smem) {
+__device__ __forceinline__ void back_chain(const DeltaArgs& a, const DeltaSeg& seg, int h, int slice, char* smem) {
   using X = Rows64<DK>;
   using M = Rows64<64>;
   constexpr int NT = 64 * NW, KS = DK / 32, DT = DK / 16, NI = DeltaParts<T>::IN;
@@ -40,7 +40,7 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& a, const DeltaSeg& s
   const Triangle tri(lane);
   const typename X::Lane xl(lane);
   const M::Lane ml(lane);
-  const int64_t head = static_cast<int64_t>(seg.s) * a.Hv + h, shead = static_cast<int64_t>(slot) * a.Hv + h;
+  const int64_t head = static_cast<int64_t>(seg.s) * a.Hv + h, shead = static_cast<int64_t>(seg.n) * a.Hv + h;
   const int64_t dd = static_cast<int64_t>(DK) * a.Dv;
   const uint32_t at = static_cast<uint32_t>(8 * g * a.Dv + col), end_at = (cs * DT * 64 + lane) * 4;
   const int ldo = a.Hv * a.Dv;
@@ -238,7 +238,7 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
   __shared__ __align__(16) char smem[NBUF * ChainTiles<T, DK, 64 * NW, true>::BUF];
   const int nsl = a.Dv / (16 * NW), n = blockIdx.x / nsl;
   const DeltaSeg seg(a, n / a.Hv, threadIdx.x & 63);
-  if (seg.s >= 0) back_chain<T, DK, NW, NBUF, true>(a, seg, n / a.Hv, n % a.Hv, blockIdx.x % nsl, smem);
+  if (seg.s >= 0) back_chain<T, DK, NW, NBUF, true>(a, seg, n % a.Hv, blockIdx.x % nsl, smem);
 }
 
 // the gradients before all segments but the first, and the maps of those between
@@ -249,8 +249,8 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
   const int n = blockIdx.x / nsl, slice = blockIdx.x % nsl;
   const DeltaSeg seg(a, n / a.Hv, threadIdx.x & 63, true);
   if (seg.s < 0) return;
-  if (slice < nv) back_chain<T, DK, NW, NBUF, false>(a, seg, seg.slot, n % a.Hv, slice, smem);
-  else if (!seg.last) chain<T, DK, NW, NBUF, kMapsT>(a, seg, seg.slot, n % a.Hv, slice - nv, smem);
+  if (slice < nv) back_chain<T, DK, NW, NBUF, false>(a, seg, n % a.Hv, slice, smem);
+  else if (!seg.last) chain<T, DK, NW, NBUF, kMapsT>(a, seg, n % a.Hv, slice - nv, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -647,7 +647,7 @@ hipError_t run_back_chain(const DeltaArgs& a, hipStream_t s) {
   const int64_t heads = static_cast<int64_t>(a.nseg) * a.Hv;
   if (a.lseg < 30) {
     k_delta_back_segments<T, DK, NW, NBUF>
-        <<<static_cast<unsigned>(delta_inner(a) * a.Hv * ((a.Dv + DK) / (16 * NW))), 64 * NW, 0, s>>>(a);
+        <<<static_cast<unsigned>(static_cast<int64_t>(a.inner) * a.Hv * ((a.Dv + DK) / (16 * NW))), 64 * NW, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_delta_join<DK, true>
@@ -685,7 +685,7 @@ hipError_t run_backward(const DeltaArgs& a, hipStream_t s) {
 
 size_t delta_backward_workspace_bytes(int B, int T, int Hv, int Dk, int Dv, bool packed) {
   return sizeof(float) * static_cast<size_t>(delta_slots(B, T, packed)) * Hv * (Dk + kDeltaChunk) * Dv +
-         delta_segment_bytes(delta_plan(B, T, Hv, Dk, Dv, packed, true), Hv, Dk, Dv);
+         delta_segment_bytes(delta_plan(B, T, Hv, Dk, Dv, packed, true), B, Hv, Dk, Dv, true);
 }
 
 void delta_backward_carve(DeltaArgs& a, void* ws) {
@@ -695,7 +695,7 @@ void delta_backward_carve(DeltaArgs& a, void* ws) {
   a.after = static_cast<float*>(ws);
   a.dr = a.after + static_cast<size_t>(a.Dk) * a.Dv * chunks;
   delta_carve_segments(a, delta_plan(a.B, a.T, a.Hv, a.Dk, a.Dv, a.cu != nullptr, true),
-                       a.dr + static_cast<size_t>(kDeltaChunk) * a.Dv * chunks);
+                       a.dr + static_cast<size_t>(kDeltaChunk) * a.Dv * chunks, true);
 }
 
 hipError_t launch_delta_backward(DeltaArgs& a, int bf16, hipStream_t s) {

@@ -56,7 +56,7 @@ struct ChainTiles {
 };
 
 template <typename T, int DK, int NW, int NBUF, int MODE>
-__device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, int slot, int h, int slice, char* smem) {
+__device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, int h, int slice, char* smem) {
   using X = Rows64<DK>;
   constexpr bool FULL = MODE == kFull, MAPS = MODE == kMaps || MODE == kMapsT;
   constexpr int NT = 64 * NW, KS = DK / 32, DT = DK / 16;
@@ -69,7 +69,7 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
   const Triangle tri(lane);
   const typename X::Lane xl(lane);
   const Rows64<64>::Lane ml(lane);
-  const int64_t head = static_cast<int64_t>(seg.s) * a.Hv + h, shead = static_cast<int64_t>(slot) * a.Hv + h;
+  const int64_t head = static_cast<int64_t>(seg.s) * a.Hv + h, shead = static_cast<int64_t>(seg.n) * a.Hv + h;
   const int64_t dd = static_cast<int64_t>(DK) * a.Dv;
   const uint32_t at = static_cast<uint32_t>(8 * g * a.Dv + col);   // of a state
   const uint32_t end_at = (cs * DT * 64 + lane) * 4;               // of a segment's
@@ -83,16 +83,19 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
 #pragma unroll
       for (int e = 0; e < 4; ++e) S[t][e] = tile_row(t, e) + 8 * g == col ? 1.0f : 0.0f;
   } else if (FULL && (seg.j > 0 || (a.h0 && !seg.last))) {
+    const float* p = seg.j > 0 ? a.ends + (shead - a.Hv) * dd : a.firsts + (static_cast<int64_t>(seg.place(a)) * a.Hv + h) * dd;
 #pragma unroll
-    for (int t = 0; t < DT; ++t) S[t] = *reinterpret_cast<const f4*>(a.ends + shead * dd + end_at + t * 256);
+    for (int t = 0; t < DT; ++t) S[t] = *reinterpret_cast<const f4*>(p + end_at + t * 256);
   } else if (a.h0 && seg.j == 0) {
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) S[t][e] = (a.h0 + head * dd + tile_row(t, e) * a.Dv)[at];
-    if constexpr (MODE == kEnds)   // (hT may be h0, and is written while the first segment runs)
+    if constexpr (MODE == kEnds) {   // (hT may be h0, and is written while the first segment runs)
+      float* p = a.firsts + (static_cast<int64_t>(seg.place(a)) * a.Hv + h) * dd;
 #pragma unroll
-      for (int t = 0; t < DT; ++t) *reinterpret_cast<f4*>(a.ends + shead * dd + end_at + t * 256) = S[t];
+      for (int t = 0; t < DT; ++t) *reinterpret_cast<f4*>(p + end_at + t * 256) = S[t];
+    }
   }
 
   Tiles st;
@@ -300,9 +303,9 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
       }
     }
     if (cs == 0 && lane == 0) a.decays[shead] = decay;
-  } else if constexpr (MODE == kEnds) {   // to where the next segment starts
+  } else if constexpr (MODE == kEnds) {
 #pragma unroll
-    for (int t = 0; t < DT; ++t) *reinterpret_cast<f4*>(a.ends + (shead + a.Hv) * dd + end_at + t * 256) = S[t];
+    for (int t = 0; t < DT; ++t) *reinterpret_cast<f4*>(a.ends + shead * dd + end_at + t * 256) = S[t];
   } else if (seg.last && a.hT) {
 #pragma unroll
     for (int t = 0; t < DT; ++t)
@@ -312,9 +315,9 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
 }
 
 // The states before the segments: S_{j+1} = E_j + d_j S_j + F_j S_j, with the
-// decay d_j apart from the map.  E_j lies where S_{j+1} goes; S_1 is there
-// already.  BACK: the gradients of the states behind them, from the last to the
-// first, with the maps' transposes.  A workgroup has 16 columns of a sequence's
+// decay d_j apart from the map.  E_j lies where S_{j+1} goes, with segment j; S_1
+// is there already.  BACK: the gradients of the states behind them, from the last
+// to the first, with the maps' transposes.  A workgroup has 16 columns of a sequence's
 // head, a wave 32 rows of them; the rows of the next two maps are on their way
 // in its registers, and the waves exchange the parts of the state in LDS.  1.4 us
 // a map of 128 x 128, bf16 (a wave for all rows, with maps in LDS: 2.6; it reads
@@ -328,22 +331,23 @@ __global__ __launch_bounds__(2 * DK, 1) void k_delta_join(DeltaArgs a) {
   // read the same maps)
   const uint32_t heads = static_cast<uint32_t>(a.B) * a.Hv, b = blockIdx.x % heads;
   const int slice = blockIdx.x / heads, h = b % a.Hv, s = b / a.Hv;
-  int len, slot0;
+  int len, n0;   // the number of its first segment
   if (a.cu) {
     const int c = clamp_row(a.cu[s], a.T);
     len = max(0, clamp_row(a.cu[s + 1], a.T) - c);
-    slot0 = (c >> (6 + a.lseg)) + s;
+    n0 = c >> (6 + a.lseg);
   } else {
     len = a.T;
-    slot0 = s * (a.nseg / a.B);
+    n0 = s * (a.nseg / a.B - 1);
   }
   const int nmap = ((((len + kDeltaChunk - 1) / kDeltaChunk) + (1 << a.lseg) - 1) >> a.lseg) - 2;
   if (nmap <= 0) return;
   const int64_t next_seg = BACK ? -a.Hv : a.Hv;
-  const int64_t shead = static_cast<int64_t>(slot0 + (BACK ? nmap : 1)) * a.Hv + h, step = next_seg * DK * a.Dv;
-  float* p = a.ends + shead * DK * a.Dv + ((slice * DT + 2 * w) * 64 + lane) * 4;
-  const uint16_t* f = a.maps + shead * NP * DK * DK + (2 * w * KS * 64 + lane) * 8;
-  const float* d = a.decays + shead;
+  const int64_t from = static_cast<int64_t>(n0 + (BACK ? nmap : 0)) * a.Hv + h, step = next_seg * DK * a.Dv;
+  const int64_t by = static_cast<int64_t>(n0 + (BACK ? nmap : 1)) * a.Hv + h;
+  float* p = a.ends + from * DK * a.Dv + ((slice * DT + 2 * w) * 64 + lane) * 4;
+  const uint16_t* f = a.maps + by * NP * DK * DK + (2 * w * KS * 64 + lane) * 8;
+  const float* d = a.decays + by;
   struct Map {
     Parts<NP> f[2][KS];
     f4 e[2];
@@ -351,14 +355,14 @@ __global__ __launch_bounds__(2 * DK, 1) void k_delta_join(DeltaArgs a) {
   } map[2];
   auto fetch = [&](Map& m, int j) __attribute__((always_inline)) {   // (behind the last one the last again, unused)
     j = min(j, nmap - 1);
-    const uint16_t* from = f + j * next_seg * NP * DK * DK;
+    const uint16_t* m0 = f + j * next_seg * NP * DK * DK;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       m.e[t] = *reinterpret_cast<const f4*>(p + (j + 1) * step + t * 256);
 #pragma unroll
       for (int x = 0; x < KS; ++x)
 #pragma unroll
-        for (int n = 0; n < NP; ++n) m.f[t][x].p[n] = *reinterpret_cast<const bh8*>(from + ((n * DT + t) * KS + x) * 512);
+        for (int n = 0; n < NP; ++n) m.f[t][x].p[n] = *reinterpret_cast<const bh8*>(m0 + ((n * DT + t) * KS + x) * 512);
     }
     m.d = d[j * next_seg];
   };

@@ -293,13 +293,13 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int S, int T, int 
 // A segment of a sequence's chunks, by its slot; s = -1: the slot has none.  An
 // empty sequence has one segment without chunks.
 struct DeltaSeg {
-  int slot;
   int s, j;         // sequence, segment of it
+  int n;            // its number among those that are not their sequences' last (the last: behind those)
   int c0, nch;      // its first chunk, its chunks
   int len, slot0;   // the sequence's rows and first chunk slot
   bool last;        // the sequence's last segment
   int64_t row0;     // the sequence's first row
-  __device__ __forceinline__ DeltaSeg(const DeltaArgs& a, int n, int lane) : slot(n) {
+  __device__ __forceinline__ DeltaSeg(const DeltaArgs& a, int slot, int lane) {
     if (a.cu) {
       const Slot x = slot_of(a.cu, a.B, a.T, min(31, 6 + a.lseg), slot, lane);
       s = x.s;
@@ -312,36 +312,39 @@ struct DeltaSeg {
       fill(a, 0);
     }
   }
-  // The n-th segment that is not its sequence's last (next: the one behind it).
+  // The i-th segment that is not its sequence's last (next: the one behind it).
   // Packed: the rows of such a segment, counted from one, have one multiple of its
-  // length among them, so no more than T / length of them are looked for.
-  __device__ __forceinline__ DeltaSeg(const DeltaArgs& a, int n, int lane, bool next) {
+  // length among them, so no more than T / length of them are looked for, and
+  // what is kept of them needs no more room.
+  __device__ __forceinline__ DeltaSeg(const DeltaArgs& a, int i, int lane, bool next) {
     if (a.cu) {
-      const int lb = 6 + a.lseg, x = (n + 1) << lb;
+      const int lb = 6 + a.lseg, x = (i + 1) << lb;
       s = sequence_of(a.cu, a.B, a.T, x - 1, lane);
       if (s < 0) return;
       const int b = clamp_row(a.cu[s], a.T);
       j = ((x - 1 - b) >> lb) + next;
-      slot = (b >> lb) + s + j;
       fill(a, b);
       if (!next && last) s = -1;
     } else {
       const int per = a.nseg / a.B;
-      s = n / (per - 1);
-      j = n - s * (per - 1) + next;
-      slot = s * per + j;
+      s = i / (per - 1);
+      j = i - s * (per - 1) + next;
       fill(a, 0);
     }
   }
+  // of a sequence of several segments: where what is kept once for each lies
+  __device__ __forceinline__ int place(const DeltaArgs& a) const { return a.B <= a.inner ? s : n - j; }
   __device__ __forceinline__ void fill(const DeltaArgs& a, int b) {
     if (a.cu) {
       row0 = b;
       len = max(0, clamp_row(a.cu[s + 1], a.T) - b);
       slot0 = b / kDeltaChunk + s;
+      n = (b >> min(31, 6 + a.lseg)) + j;
     } else {
       row0 = static_cast<int64_t>(s) * a.T;
       len = a.T;
       slot0 = s * ((a.T + kDeltaChunk - 1) / kDeltaChunk);
+      n = s * (a.nseg / a.B - 1) + j;
     }
     const int all = (len + kDeltaChunk - 1) / kDeltaChunk;
     c0 = a.lseg > 24 ? 0 : j << a.lseg;

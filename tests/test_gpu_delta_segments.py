@@ -50,3 +50,61 @@ def test_states_through_maps_keep_32_bits(dk, dv, dtype):
         tol = 2 * (p.double() - w).flatten(1).norm(dim=1)
         say(f"  {name}: {[f'{a:.1e}' for a in (e / size).tolist()]}, in 32 bits {[f'{a:.1e}' for a in (tol / 2 / size).tolist()]}")
         assert (e <= tol).all(), (name, e, tol)
+
+
+def _packed(lengths, hk, hv, dk, dv, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g)
+    unit = lambda t: t / t.norm(dim=-1, keepdim=True)
+    T = sum(lengths)
+    off = [0]
+    for m in lengths:
+        off.append(off[-1] + m)
+    ins = [t.to(dtype) for t in (unit(n(T, hk, dk)), unit(n(T, hk, dk)), n(T, hv, dv), -torch.rand(T, hv, generator=g) * 4e-3,
+                                 torch.sigmoid(n(T, hv)))]
+    return ins, n(len(lengths), hv, dk, dv), off, n(T, hv, dv).to(dtype), n(len(lengths), hv, dk, dv)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(1, 2, 64, 128), (1, 1, 128, 128)])
+def test_few_long_sequences_among_many(shape, dtype):
+    """More sequences than segments: long ones among them, one next to the other and with empty ones between, have
+    the results that they have alone, also where hT is h0."""
+    hk, hv, dk, dv = shape
+    lengths = [1] * 200 + [2500] + [0] * 90 + [3] * 150 + [1800, 1300] + [2] * 60 + [0] * 5
+    ins, h0, off, do, dhT = _packed(lengths, hk, hv, dk, dv, dtype, dk + dv)
+    dev = [t.cuda() for t in ins]
+    start, end, cu = h0.cuda(), dhT.cuda(), torch.tensor(off, dtype=torch.int32).cuda()
+    o, hT, st = m3.delta_scan(*dev, h0=start, cu_seqlens=cu, want_states=True)
+    d = m3.delta_scan_backward(*dev, do.cuda(), st, h0=start, dhT=end, cu_seqlens=cu)
+    for s, L in enumerate(lengths):
+        if L == 0:
+            assert torch.equal(hT[s].cpu(), h0[s]) and torch.equal(d["h0"][s].cpu(), dhT[s])
+        if L == 0 or s % 61 and L < 1000:
+            continue
+
+        def plain(t):
+            x = [y[off[s]:off[s + 1]].to(t) for y in ins] + [h0[s].to(t).requires_grad_(True)]
+            y, hs, _ = delta_ref.scan(*x, dk ** -0.5)
+            loss = (y * do[off[s]:off[s + 1]].to(t)).sum() + (hs[-1] * dhT[s].to(t)).sum()
+            return y.detach(), hs[-1].detach(), torch.autograd.grad(loss, x[-1])[0]
+
+        want, near = plain(torch.float64), plain(F32)
+        for name, x, w, p in zip(("o", "hT", "dh0"), (o[off[s]:off[s + 1]], hT[s], d["h0"][s]), want, near):
+            # (the recurrence's error, of a short sequence at least half a step of each element; and o's rounding,
+            # in bf16 after operands of two parts)
+            tol = 2 * float((p.double() - w).norm()) + 2.0 ** -24 * float(w.norm())
+            tol += (ref.U[dtype] * (1 + 2.0 ** -6) if name == "o" else 0) * float(w.norm())
+            e = float((ref.f64(x) - w).norm())
+            assert e <= tol, (s, L, name, e, tol)
+    # in place
+    import ctypes
+    lib = m3.library()
+    dims = m3.m3_delta_dims(len(lengths), sum(lengths), hk, hv, dk, dv, m3.dtype_code(dtype), dk ** -0.5, 0, 0, 0, 0, 0)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    ws = torch.empty(lib.m3_delta_scan_workspace_size(ctypes.byref(dims), 1), dtype=torch.uint8, device="cuda")
+    y, h = torch.empty_like(dev[2]), start.clone()
+    assert lib.m3_delta_scan(ctypes.byref(dims), p(cu), *(p(t) for t in dev), p(h), p(y), p(h), None, p(ws), ws.numel(),
+                             ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(h, hT) and torch.equal(y, o)

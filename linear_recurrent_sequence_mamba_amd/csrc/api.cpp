@@ -297,7 +297,8 @@ m3_status check_delta(const m3_delta_dims* d, bool scan, bool packed) {
     if (l[0] != 0 && (l[0] < l[1] || l[0] >= most)) return M3_ERR_SHAPE;
   if ((d->ld_q | d->ld_k | d->ld_v) % 8) return M3_ERR_ALIGN;
   // the step: 4 Dv threads for a sequence's head.  The scan: at most 4 (Dk + Dv)
-  // for each chunk and head
+  // for each chunk and head (what joins segments 2 Dk Dv / 16, once for at least
+  // eight chunks)
   const int64_t slots = scan ? m3::delta_slots(d->batch, d->seqlen, packed) : d->batch;
   if (slots > 0x7fffffff || !grid_fits(slots * d->nheads_v, scan ? 1024 : 512)) return M3_ERR_SHAPE;
   return M3_OK;

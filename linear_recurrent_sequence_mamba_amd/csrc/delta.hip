@@ -287,7 +287,7 @@ hipError_t run_chain(const DeltaArgs& a, bool split, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_delta_join<DK, false>
-        <<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hv * (a.Dv / 16)), 2 * DK, 0, s>>>(a);
+        <<<static_cast<unsigned>(static_cast<int64_t>(a.B < a.inner ? a.B : a.inner) * a.Hv * (a.Dv / 16)), 2 * DK, 0, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -651,7 +651,7 @@ hipError_t run_back_chain(const DeltaArgs& a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_delta_join<DK, true>
-        <<<static_cast<unsigned>(static_cast<int64_t>(a.B) * a.Hv * (a.Dv / 16)), 2 * DK, 0, s>>>(a);
+        <<<static_cast<unsigned>(static_cast<int64_t>(a.B < a.inner ? a.B : a.inner) * a.Hv * (a.Dv / 16)), 2 * DK, 0, s>>>(a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

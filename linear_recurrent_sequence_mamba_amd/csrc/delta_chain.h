@@ -329,16 +329,21 @@ __global__ __launch_bounds__(2 * DK, 1) void k_delta_join(DeltaArgs a) {
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // (a head's workgroups on one XCD where the heads are a multiple of 8, as they
   // read the same maps)
-  const uint32_t heads = static_cast<uint32_t>(a.B) * a.Hv, b = blockIdx.x % heads;
-  const int slice = blockIdx.x / heads, h = b % a.Hv, s = b / a.Hv;
-  int len, n0;   // the number of its first segment
-  if (a.cu) {
-    const int c = clamp_row(a.cu[s], a.T);
-    len = max(0, clamp_row(a.cu[s + 1], a.T) - c);
-    n0 = c >> (6 + a.lseg);
+  const uint32_t heads = static_cast<uint32_t>(min(a.B, a.inner)) * a.Hv, b = blockIdx.x % heads;
+  const int slice = blockIdx.x / heads, h = b % a.Hv, c = b / a.Hv;
+  int len, n0;   // the sequence's rows, the number of its first segment
+  if (a.B > a.inner) {   // by segments, a sequence with its first
+    const DeltaSeg seg(a, c, lane, false);
+    if (seg.s < 0 || seg.j > 0) return;
+    len = seg.len;
+    n0 = c;
+  } else if (a.cu) {
+    const int row = clamp_row(a.cu[c], a.T);
+    len = max(0, clamp_row(a.cu[c + 1], a.T) - row);
+    n0 = row >> (6 + a.lseg);
   } else {
     len = a.T;
-    n0 = s * (a.nseg / a.B - 1);
+    n0 = c * (a.nseg / a.B - 1);
   }
   const int nmap = ((((len + kDeltaChunk - 1) / kDeltaChunk) + (1 << a.lseg) - 1) >> a.lseg) - 2;
   if (nmap <= 0) return;

@@ -108,3 +108,20 @@ def test_few_long_sequences_among_many(shape, dtype):
                              ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
     torch.cuda.synchronize()
     assert torch.equal(h, hT) and torch.equal(y, o)
+
+
+def test_more_heads_of_sequences_than_a_launch_for_each():
+    """So many empty sequences that a workgroup for each 16 columns of each of their heads would pass 2^32 threads,
+    and long ones at their ends."""
+    B, hv, dk, dv, L = 70000, 32, 128, 128, [4000, 2000]
+    q, k, v, g, b = (t.cuda() for t in _packed(L, 1, hv, dk, dv, BF16, 5)[0])
+    cu = torch.full((B + 1,), L[0], dtype=torch.int32)
+    cu[0], cu[-1] = 0, sum(L)
+    o = m3.delta_scan(q, k, v, g, b, cu_seqlens=cu.cuda(), want_hT=False)[0]
+    for s, c in ((0, slice(0, L[0])), (1, slice(L[0], sum(L)))):
+        one = torch.tensor([0, L[s]], dtype=torch.int32).cuda()
+        want = m3.delta_scan(q[c], k[c], v[c], g[c], b[c], cu_seqlens=one)[0]
+        # (sums are grouped by other segments)
+        e = float((o[c].double() - want.double()).norm() / want.double().norm())
+        say(f"  {s}: {e:.1e}")
+        assert e <= 2.0 ** -8

@@ -630,9 +630,10 @@ __global__ __launch_bounds__(1024) void k_block_norm_bwd_long(BlockNormArgs a) {
     }
     const f2 s1 = sums(hh, gh), s2 = sums(qd, qg);
     const float sqh = sums(qh, 0.0f).x;
+    // (without dn an h that is not finite reaches nothing)
     const float ih = dnp ? __builtin_amdgcn_rsqf(fmaf(s1.x, invW, a.eps)) : 0.0f;
     const float c = s1.y * invW * ih * ih;
-    const float m = a.raw ? 0.0f : fmaf(ih, fmaf(-c, sqh, s2.y), s2.x) * invW;
+    const float m = a.raw ? 0.0f : (dnp ? fmaf(ih, fmaf(-c, sqh, s2.y), s2.x) : s2.x) * invW;
 #pragma unroll 1
     for (int e = P::first(); e < W; e += P::STEP) {
       float d[K], g[K], wn[K];
@@ -640,11 +641,11 @@ __global__ __launch_bounds__(1024) void k_block_norm_bwd_long(BlockNormArgs a) {
       P f(a, t, e, iy);
 #pragma unroll
       for (int j = 0; j < K; ++j) {
-        d[j] += ih * fmaf(g[j], wn[j], -f.h[j] * c);
+        if (dnp) d[j] += ih * fmaf(g[j], wn[j], -f.h[j] * c);
         const float du = d[j] * f.u[j];
         if (V > 1 || P::at(e, j) < W) {
           acc[0][P::at(e, j)] += du * f.act[j];
-          acc[1][P::at(e, j)] += g[j] * f.h[j] * ih;
+          if (dnp) acc[1][P::at(e, j)] += g[j] * f.h[j] * ih;
         }
         f.da[j] *= du * f.wz[j];
         f.h[j] = iy * fmaf(-f.u[j], m, f.act[j] * d[j] * f.wz[j]);

@@ -518,8 +518,8 @@ size_t m3_delta_scan_workspace_size(const m3_delta_dims* dims, int packed);
  * batch whose offsets do not are unspecified.  Rows that no sequence covers
  * are left as they are.  A NaN or Inf stays in its sequence and heads, and may
  * reach all outputs from its chunk on.  A token with beta = 0 and g = 0 leaves
- * the state as it is, bit for bit.  g and beta need only their elements'
- * alignment. */
+ * the state as it is (a zero may change its sign).  g and beta need only their
+ * elements' alignment. */
 m3_status m3_delta_scan(const m3_delta_dims* dims, const int32_t* cu_seqlens, const void* q,
                         const void* k, const void* v, const void* g, const void* beta,
                         const float* h0, void* o, float* hT, float* states, void* ws,

@@ -335,14 +335,17 @@ int64_t delta_slots(int B, int T, bool packed) {
 // many columns as the values and a state have together, and what joins them
 // 0.2 for each.  They are taken where that is less than 3/4 (in a training step
 // both are held by memory before that).  16384 tokens of 16 heads of 128: 1.43 ms
-// whole, in 32 segments of 8 chunks 380 us with the rest, 16 of 16 346, 8 of 32
-// 412.
+// whole, in 32 segments of 8 chunks 381 us with the rest, 16 of 16 333, 8 of 32
+// 382.  What the estimate costs: 16 sequences of 1024 rows, 8 heads of 64 x 64 in
+// fp32, are cut and take 172 us, whole 125; 24, the longest of 14000 of 16300, 16
+// heads of 128, 401, whole 1257.
 //
 // A packed batch that would stay whole may still have one sequence that is much
 // longer than the others: then segments no shorter than what uniform lengths give,
 // so that those have one each and only such a sequence has more.  (60 sequences of
-// 64 tokens and one of 4000, 8 heads of 128 x 64: 118 us instead of 271, with
-// gradients 312 instead of 654.  64 of 128, 32 heads: 151 and 147, 526 and 503.)
+// 64 tokens and one of 4000, 8 heads of 128 x 64: 123 us instead of 272, with
+// gradients 322 instead of 655.  64 of 128, 32 heads: 149 and 145, 526 and 505;
+// 1000 of 16, 16 heads of 128: 803 and 791, 2721 and 2691.)
 DeltaPlan delta_plan(int B, int T, int Hv, int Dk, int Dv, bool packed, bool back) {
   const double rows = packed ? T : static_cast<double>(B) * T;
   const double longest = (packed && B > 1 ? 2.0 * T / B : T) / kDeltaChunk, cols = Hv * (Dv / 16.0);

@@ -263,14 +263,18 @@ __global__ __launch_bounds__(64 * NW, sizeof(T) == 2 ? 2 : 1) void k_delta_back_
 // tiles (of two blocks of 32 by 32 on and one below the diagonal), which the
 // waves share.
 //
-// 128 chunks of 32 heads of 128 x 64, bf16: 205 us for 780 MB, 3.8 TB/s.  Its
+// 128 chunks of 32 heads of 128 x 64, bf16: 203 us for 780 MB, 3.8 TB/s.  Its
 // registers leave room for one workgroup a CU, so that what a workgroup asks for
 // first and its products do not overlap with another's; two (128 registers) spill:
 // 400 us.  The next slab's rows are asked for as soon as the last one's are split.
 // AHEAD: a workgroup goes on to another chunk and head, whose first rows it asks
 // for before the products over tokens (without it 230 us); with 128 value channels
 // or fp32 the registers for it are not there (a packed batch of 8192 tokens, 16
-// heads on 8 of 128 x 128: 235 us with it, 219 without).
+// heads on 8 of 128 x 128: 246 us with it, 226 without).  Some spill without it: 15
+// registers of bf16 with shared heads of 128 x 128, 29 and 90 of fp32 with shared
+// heads of 128 x 64 and 128 x 128, at most 11 of the others (4 x 2048 tokens, 32
+// heads on 16 of 128 x 128, fp32: 652 us, 540 of the 672 MB that it writes are
+// scratch).
 template <typename T, int DK, bool KEEP>   // KEEP: K and Q stay for all heads
 struct GradTiles {
   using M = Rows64<64>;

@@ -27,12 +27,14 @@ namespace {
 // while waves still read this one's, and one barrier a chunk is enough.
 //
 // What bounds it: each product needs the one before it.  A chunk takes 5.3 us
-// (Dk = Dv = 128, bf16; 1.43 ms for 256 chunks) with a wave on each SIMD, 7.3 us
-// with two: 980 vector and 182 matrix instructions on one path, of whose cycles
-// 45% issue, 39% wait for the matrix unit or a slot and 16% for LDS and barriers.
-// A second wave fills some of that, which is why segments pay although they do
-// most of the work twice.  With the states saved for a training step (48 KB a
-// chunk of 128 x 64) two waves a SIMD reach HBM's rate instead.
+// (Dk = Dv = 128, bf16; 1.37 ms for 256 chunks) with a wave on each SIMD, 7.3 us
+// with two: 730 vector and 182 matrix instructions on one path, with the states
+// saved 800.  There (4 x 2048 tokens, 32 heads of 128 x 64, a wave on each SIMD)
+// 46% of a wave's cycles issue, 39% wait for the matrix unit or a slot and 15% for
+// LDS and barriers.  A second wave fills some of that, which is why segments pay
+// although they do most of the work twice; but saved states (48 KB a chunk of
+// 128 x 64) bring them to HBM's rate: in four segments each the chain alone
+// takes 95 us for 480 MB, whole 184.
 enum { kFull = 0, kEnds = 1, kMaps = 2, kMapsT = 3 };   // (kMapsT: the map's transpose, for the gradients)
 
 template <typename T, int DK, int NT, bool FULL>
@@ -319,9 +321,10 @@ __device__ __forceinline__ void chain(const DeltaArgs& a, const DeltaSeg& seg, i
 // is there already.  BACK: the gradients of the states behind them, from the last
 // to the first, with the maps' transposes.  A workgroup has 16 columns of a sequence's
 // head, a wave 32 rows of them; the rows of the next two maps are on their way
-// in its registers, and the waves exchange the parts of the state in LDS.  1.4 us
-// a map of 128 x 128, bf16 (a wave for all rows, with maps in LDS: 2.6; it reads
-// four times as many operands in a row).
+// in its registers, and the waves exchange the parts of the state in LDS.  1.8 us
+// a map of 128 x 128, whose six products of parts follow each other (with two
+// parts, three products: 1.4, and a wave for all rows, with maps in LDS, which
+// reads four times as many operands in a row, 2.6).
 template <int DK, bool BACK>
 __global__ __launch_bounds__(2 * DK, 1) void k_delta_join(DeltaArgs a) {
   constexpr int KS = DK / 32, DT = DK / 16, NP = 3;

@@ -561,7 +561,8 @@ typedef struct {
   int32_t dtype;  /* m3_dtype of rows and their gradients                  */
   uint32_t flags;
   float eps;      /* finite, >= 0 (a row whose mean square and eps are
-                     together below 2^-126 has no finite norm)             */
+                     together below 2^-126 has no finite norm, and one
+                     whose sum of squares passes fp32's range becomes 0)   */
   int64_t ld_x, ld_y, ld_gate; /* >= W or 0                                */
 } m3_block_dims;
 

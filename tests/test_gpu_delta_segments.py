@@ -125,3 +125,40 @@ def test_more_heads_of_sequences_than_a_launch_for_each():
         e = float((o[c].double() - want.double()).norm() / want.double().norm())
         say(f"  {s}: {e:.1e}")
         assert e <= 2.0 ** -8
+
+
+def test_a_captured_batch_takes_other_offsets():
+    """The launches depend on sizes alone: a step captured once runs any offsets within its rows and sequences."""
+    S, T, hk, hv, dk, dv = 40, 6000, 1, 2, 64, 64
+    ins, h0, _, do, dhT = _packed([T], hk, hv, dk, dv, BF16, 31)
+    dev = [t.cuda() for t in ins]
+    g = torch.Generator().manual_seed(32)
+    h0, dhT = (torch.randn(S, hv, dk, dv, generator=g).cuda() for _ in range(2))
+    do = do.cuda()
+    batches = [[150] * 40, [6000] + [0] * 39, [0] * 20 + [2000, 1, 3000] + [17] * 17, [5] * 39 + [3333], [0] * 40]
+    offsets = [torch.tensor([0] + torch.tensor(b).cumsum(0).tolist(), dtype=torch.int32).cuda() for b in batches]
+    cu = offsets[0].clone()
+
+    def run(c):
+        o, hT, st = m3.delta_scan(*dev, h0=h0, cu_seqlens=c, want_states=True)
+        d = m3.delta_scan_backward(*dev, do, st, h0=h0, dhT=dhT, cu_seqlens=c)
+        return dict(o=o, hT=hT, **{"d" + n: t for n, t in d.items()})
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run(cu)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            out = run(cu)
+    for b, c in list(zip(batches, offsets)) * 2:
+        cu.copy_(c)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run(c)
+        n = sum(b)
+        for name, w in want.items():
+            x = out[name]
+            assert torch.equal(x, w) if name in ("hT", "dh0") else torch.equal(x[:n], w[:n]), (b[:3], name)
